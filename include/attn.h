@@ -332,6 +332,76 @@ ATTN_API int attn_decode_noalloc(const void *q, const void *kcache, const void *
 ATTN_API int attn_decode_splits(int B, int H, int Skv, int D);
 
 /*
+ * attn_rope -- rotary positions: turns the pairs of each head row of q and k by
+ * an angle proportional to the row's position, before attention or caching.
+ *
+ * Row element pairs are (x[p], x[p + rotary_dim/2]) (interleaved = 0) or
+ * (x[2p], x[2p + 1]) (interleaved = 1), p < rotary_dim / 2; elements from
+ * rotary_dim on are copied.  With n the row's position,
+ *
+ *     (a, b) -> mscale * (a cos(n w_p) - b sin(n w_p), b cos(n w_p) + a sin(n w_p)),
+ *
+ * w_p = freqs[p]; inverse = 1 turns by -n w_p, which takes a turn back and is
+ * also its gradient (grad_x = mscale R(-n) grad_out).  Scaled frequencies for
+ * long contexts are a matter of freqs and mscale.  Angles are formed modulo
+ * one turn in 64-bit fixed point, so far positions lose nothing; the
+ * arithmetic is fp32, rounded once to the output type.
+ *
+ *   q, q_out  (T, H, D) rows; k, k_out  (T, H_kv, D) rows, H_kv = 0 (and NULL)
+ *             for q alone.  An output may be its own input (same pointer and
+ *             strides: in place); any other overlap returns ATTN_EINVAL.
+ *             Slices of one fused (T, columns) matrix do not overlap.
+ *   strides   NULL (contiguous), or HOST int64[8]: elements from token to
+ *             token and from head to head of q, k, q_out and k_out.  Rows of
+ *             one tensor must not overlap.  (B, H, S, D) tensors are B calls, or
+ *             one call when B = 1.
+ *   positions device int32[T]; any value, negative ones turn backwards.
+ *   freqs     HOST double[rotary_dim / 2], radians per position, finite; read
+ *             during the call (a captured call keeps the values).
+ *   rotary_dim  even, 0 .. D.
+ *   mscale    finite multiplier of the turned elements (1 for none).
+ *
+ * D must be 64 or 128.  Tensors need element alignment only; 16-byte aligned
+ * pointers, strides and pair offsets are the fast case.  No workspace.
+ */
+ATTN_API int attn_rope(const void *q, const void *k, void *q_out, void *k_out, int T, int H, int H_kv, int D,
+                       const long long *strides, const int32_t *positions, const double *freqs, int rotary_dim,
+                       int interleaved, int inverse, float mscale, int dtype, void *stream);
+
+/*
+ * attn_rope_append -- attn_rope of new tokens whose turned keys, and values,
+ * go to their rows of a KV cache: one pass instead of a turn, two transposes
+ * and two copies.  This is the append that attn_fwd_chunked, attn_decode and
+ * attn_decode_tree expect of their caller, for prompts, single tokens
+ * and drafts.
+ *
+ * Sequence b's new tokens are [cu_seqlens[b], cu_seqlens[b + 1]), n_b of them.
+ * cache_len[b] = L_b counts them already (as in attn_fwd_chunked), so token i of
+ * the sequence goes to cache row L_b - n_b + i, which is also its position
+ * unless `positions` says otherwise (the tokens of a tree sit at their depth).
+ * A token whose row is negative is turned but not cached.  Tokens outside
+ * every sequence (before cu_seqlens[0], from cu_seqlens[B] on) are neither
+ * read nor written anywhere.  Other cache rows stay as they were.
+ *
+ *   q, q_out  (T, H, D) rows; k, v  (T, H_kv, D) rows, H_kv >= 1
+ *   k_out     NULL, or (T, H_kv, D) rows: the turned keys once more, token by
+ *             token (attn_fwd_packed reads them); may be k itself
+ *   kcache, vcache  (B, H_kv, Skv, D), contiguous, written
+ *   strides   NULL or HOST int64[10]: q, k, v, q_out, k_out, as in attn_rope
+ *   cu_seqlens  device int32[B + 1], nondecreasing, or NULL: T / B tokens per
+ *             sequence (T a multiple of B)
+ *   cache_len device int32[B], each clamped to [0, Skv], or NULL: every L_b = Skv
+ *   positions device int32[T] or NULL
+ *
+ * The rest as in attn_rope.
+ */
+ATTN_API int attn_rope_append(const void *q, const void *k, const void *v, void *q_out, void *k_out, void *kcache,
+                              void *vcache, int T, int H, int H_kv, int D, const long long *strides, int B, int Skv,
+                              const int32_t *cu_seqlens, const int32_t *cache_len, const int32_t *positions,
+                              const double *freqs, int rotary_dim, int interleaved, float mscale, int dtype,
+                              void *stream);
+
+/*
  * attn_device_status -- synchronise `stream`, then report and clear the
  * device-side status word.  Returns ATTN_OK, ATTN_ETIMEOUT when a kernel gave
  * up on a device-side wait (its output is then undefined), ATTN_ECONFLICT

@@ -10,6 +10,7 @@ no CPU path: when the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -41,6 +42,9 @@ SIGNATURES = {
     "attn_decode_gqa": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
     "attn_decode_noalloc": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp]),
     "attn_decode_splits": (_i, [_i, _i, _i, _i]),
+    "attn_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp]),
+    "attn_rope_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
+                              _i, _i, _f, _i, _vp]),
     "attn_device_status": (_i, [_vp]),
     "attn_last_error": (ctypes.c_char_p, []),
     "attn_release": (None, []),
@@ -326,6 +330,168 @@ def attn_decode_splits(B: int, H: int, Skv: int, D: int) -> int:
     return lib().attn_decode_splits(B, H, Skv, D)
 
 
+def _check_rows(name, t, like=None):
+    """A (T, heads, D) CUDA tensor whose head rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be (T, heads, D) with contiguous rows of D elements")
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must share q's dtype")
+        if t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2] or t.device != like.device:
+            raise ValueError(f"{name} must match q's tokens, head depth and device")
+
+
+def _ints_arg(name, t, n, device):
+    torch = _torch()
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()
+            and t.device == device):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {n} values on q's device")
+    return t
+
+
+def _freqs_arg(freqs, D):
+    torch = _torch()
+    if not (isinstance(freqs, torch.Tensor) and freqs.dtype == torch.float64 and freqs.dim() == 1
+            and not freqs.is_cuda and freqs.is_contiguous()) or 2 * freqs.numel() > D:
+        raise ValueError("freqs must be a contiguous 1-D float64 CPU tensor of rotary_dim / 2 <= D / 2 values")
+    return freqs
+
+
+def _on_device(device):
+    """Context in which ``device`` is the current one (the library launches there)."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _strides(*tensors):
+    st = []
+    for t in tensors:
+        st += (t.stride(0), t.stride(1)) if t is not None else (0, 0)
+    return (ctypes.c_longlong * len(st))(*st)
+
+
+def attn_rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: Optional[str] = None,
+                          factor: float = 1.0, original_len: int = 8192, low: float = 1.0, high: float = 4.0):
+    """Rotary frequencies in radians per position, a CPU float64 tensor of
+    rotary_dim / 2 values w_p = theta^(-2p / rotary_dim), for attn_rope and
+    attn_rope_append.  ``scaling`` stretches them for contexts ``factor`` times
+    longer:
+
+    "linear"      every w_p / factor (positions interpolated)
+    "ntk"         theta grows by factor^(r / (r - 2)), r = rotary_dim: the highest
+                  frequency stays, the lowest is divided by ``factor``
+    "wavelength"  by the turns t_p = original_len * w_p / 2 pi that pair p makes
+                  over the original context: w_p / factor below ``low`` turns, w_p
+                  above ``high``, and a linear blend in t_p between them
+    """
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and >= 0 (got {rotary_dim})")
+    if not (theta > 0 and factor > 0):
+        raise ValueError("theta and factor must be positive")
+    torch = _torch()
+    if scaling == "ntk" and rotary_dim > 2:
+        theta = theta * factor ** (rotary_dim / (rotary_dim - 2))
+    w = [theta ** (-2.0 * p / rotary_dim) for p in range(rotary_dim // 2)]
+    if scaling == "linear":
+        w = [x / factor for x in w]
+    elif scaling == "wavelength":
+        if not (original_len > 0 and high > low):
+            raise ValueError("wavelength scaling needs original_len > 0 and high > low")
+        blend = [min(1.0, max(0.0, (original_len * x / (2 * math.pi) - low) / (high - low))) for x in w]
+        w = [x * ((1 - s) / factor + s) for x, s in zip(w, blend)]
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r} (linear, ntk, wavelength)")
+    return torch.tensor(w, dtype=torch.float64)
+
+
+def attn_rope(q, k, positions, freqs, q_out=None, k_out=None, interleaved: bool = False, inverse: bool = False,
+              mscale: float = 1.0, stream=None):
+    """Rotary positions: turn the first 2 * len(freqs) elements of every head row
+    of q (T, H, D) and k (T, H_kv, D) by position * frequency.  k may be None.
+    Returns ``(q_out, k_out)`` (``q_out`` alone without k); pass ``q_out=q`` to
+    turn in place.  ``positions`` is int32 (T,), ``freqs`` from
+    attn_rope_frequencies.  ``inverse`` turns back, which is also the gradient.
+    Rows may be strided (slices of a fused projection).  See include/attn.h.
+    """
+    _check_rows("q", q)
+    if k is not None:
+        _check_rows("k", k, q)
+    T, H, D = q.shape
+    freqs = _freqs_arg(freqs, D)
+    pos = _ints_arg("positions", positions, T, q.device)
+    if pos is None:
+        raise ValueError("positions must be given")
+    torch = _torch()
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    _check_rows("q_out", q_out, q)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    if k is not None:
+        _check_rows("k_out", k_out, q)
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    with _on_device(q.device):
+        rc = lib().attn_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), T, H,
+                             k.shape[1] if k is not None else 0, D, _strides(q, k, q_out, k_out), pos.data_ptr(),
+                             freqs.data_ptr(), 2 * freqs.numel(), int(bool(interleaved)), int(bool(inverse)),
+                             float(mscale), _dtype_code(q), _stream_handle(stream))
+    _check(rc)
+    return (q_out, k_out) if k is not None else q_out
+
+
+def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=None, positions=None, q_out=None,
+                     k_out=None, interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """attn_rope of new tokens, with the turned keys and the values written to
+    their rows of a (B, H_kv, Skv, D) cache: token i of sequence b (tokens
+    [cu_seqlens[b], cu_seqlens[b + 1]), n of them; T / B each without cu_seqlens)
+    goes to row cache_len[b] - n + i, which is also its position unless
+    ``positions`` is given.  Returns ``q_out``, or ``(q_out, k_out)`` when a
+    ``k_out`` (T, H_kv, D) is given for the turned keys.  See include/attn.h.
+    """
+    _check_rows("q", q)
+    _check_rows("k", k, q)
+    _check_rows("v", v, q)
+    _check_tensor("kcache", kcache, 4)
+    _check_tensor("vcache", vcache, 4)
+    T, H, D = q.shape
+    H_kv = k.shape[1]
+    B, Skv = kcache.shape[0], kcache.shape[2]
+    if v.shape != k.shape or tuple(kcache.shape) != (B, H_kv, Skv, D) or vcache.shape != kcache.shape:
+        raise ValueError("k and v must be (T, H_kv, D), kcache and vcache (B, H_kv, Skv, D)")
+    if not (q.dtype == kcache.dtype == vcache.dtype):
+        raise TypeError("q, k, v and the caches must share one dtype")
+    if kcache.device != q.device or vcache.device != q.device:
+        raise ValueError("the caches must be on q's device")
+    freqs = _freqs_arg(freqs, D)
+    cu = _ints_arg("cu_seqlens", cu_seqlens, B + 1, q.device)
+    cl = _kv_len_arg(cache_len, B, q.device)
+    pos = _ints_arg("positions", positions, T, q.device)
+    if q_out is None:
+        q_out = _torch().empty((T, H, D), dtype=q.dtype, device=q.device)
+    _check_rows("q_out", q_out, q)
+    if k_out is not None:
+        _check_rows("k_out", k_out, q)
+    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    with _on_device(q.device):
+        rc = lib().attn_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), _ptr(k_out),
+                                    kcache.data_ptr(), vcache.data_ptr(), T, H, H_kv, D,
+                                    _strides(q, k, v, q_out, k_out), B, Skv, _ptr(cu), _ptr(cl), _ptr(pos),
+                                    freqs.data_ptr(), 2 * freqs.numel(), int(bool(interleaved)), float(mscale),
+                                    _dtype_code(q), _stream_handle(stream))
+    _check(rc)
+    return (q_out, k_out) if k_out is not None else q_out
+
+
 def attn_device_status(stream=None) -> None:
     """Synchronise the stream and raise AttnError if a kernel reported a timed-out
     wait (ATTN_ETIMEOUT) or a shared prefill work counter (ATTN_ECONFLICT)."""
@@ -342,7 +508,8 @@ def attn_release() -> None:
 
 
 __all__ = [
-    "attn_fwd", "attn_fwd_chunked", "attn_fwd_debug", "attn_fwd_host", "attn_decode", "attn_decode_noalloc", "attn_decode_splits", "attn_device_status", "attn_release",
+    "attn_fwd", "attn_fwd_chunked", "attn_fwd_debug", "attn_fwd_host", "attn_decode", "attn_decode_noalloc", "attn_decode_splits", "attn_rope",
+    "attn_rope_append", "attn_rope_frequencies", "attn_device_status", "attn_release",
     "attn_last_error", "attn_selftest_wait_timeout", "lib", "AttnError", "SIGNATURES", "LIB_PATH",
     "ATTN_F32", "ATTN_BF16", "ATTN_OK", "ATTN_EINVAL", "ATTN_EUNSUPPORTED", "ATTN_ECUDA",
     "ATTN_ENOMEM", "ATTN_ETIMEOUT", "ATTN_ECONFLICT",

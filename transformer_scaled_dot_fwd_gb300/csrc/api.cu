@@ -41,6 +41,50 @@ bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// A strided (n_outer, n_inner) set of rows of D elements: row (i, j) starts at
+// element i * so + j * si.  Strides of a dimension of one entry are ignored.
+struct Rows {
+    const char *p;
+    long long n_outer, n_inner, so, si;  // strides in bytes after make_rows
+    long long row;                       // bytes of one row
+};
+
+Rows make_rows(const void *p, long long n_outer, long long n_inner, long long so, long long si, long long D,
+               long long esz) {
+    Rows r{static_cast<const char *>(p), n_outer, n_inner, so * esz, si * esz, D * esz};
+    if (n_inner == 1) r.si = r.row;
+    if (n_outer == 1) r.so = r.si * n_inner > r.row ? r.si * n_inner : r.row;
+    return r;
+}
+
+// No two rows share a byte: one dimension's rows fit inside the other's stride.
+bool rows_distinct(const Rows &r) {
+    if (r.n_outer <= 0 || r.n_inner <= 0) return true;
+    return (r.si >= r.row && r.so >= (r.n_inner - 1) * r.si + r.row) ||
+           (r.so >= r.row && r.si >= (r.n_outer - 1) * r.so + r.row);
+}
+
+// May rows of a and b share a byte?  Disjoint extents, or two runs of columns
+// of one matrix (slices of a fused projection) are the cases known not to.
+bool rows_overlap(const Rows &a, const Rows &b) {
+    if (!a.p || !b.p || a.n_outer <= 0 || b.n_outer <= 0 || a.n_inner <= 0 || b.n_inner <= 0) return false;
+    auto extent = [](const Rows &r) { return (r.n_outer - 1) * r.so + (r.n_inner - 1) * r.si + r.row; };
+    if (!overlaps(a.p, static_cast<size_t>(extent(a)), b.p, static_cast<size_t>(extent(b)))) return false;
+    // columns [0, wa) of a and [off, off + wb) of b in rows of `period` bytes
+    auto columns_apart = [](const Rows &x, const Rows &y, bool outer) {
+        const long long period = outer ? x.so : x.si;
+        if (period != (outer ? y.so : y.si) || period <= 0) return false;
+        const long long wx = outer ? (x.n_inner - 1) * x.si + x.row : (x.n_outer - 1) * x.so + x.row;
+        const long long wy = outer ? (y.n_inner - 1) * y.si + y.row : (y.n_outer - 1) * y.so + y.row;
+        const long long d = static_cast<long long>(y.p - x.p);
+        const long long off = ((d % period) + period) % period;
+        return off >= wx && off + wy <= period;
+    };
+    return !columns_apart(a, b, true) && !columns_apart(a, b, false);
+}
+
+bool same_rows(const Rows &a, const Rows &b) { return a.p == b.p && a.so == b.so && a.si == b.si; }
+
 // ------------------------------------------------------------ device status word
 
 __device__ int g_status_word;
@@ -611,6 +655,126 @@ ATTN_API int attn_decode_noalloc(const void *q, const void *kcache, const void *
                  chunk, n_split, nullptr, nullptr, status, static_cast<cudaStream_t>(stream), H};
     cudaError_t e = launch_decode_noalloc(a, dtype == ATTN_F32);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_decode_noalloc launch");
+}
+
+// Shared by attn_rope (no cache) and attn_rope_append.
+static int rope_impl(const char *who, RopeArgs a, const long long *strides, const double *freqs, int inverse,
+                     int dtype, void *stream) {
+    g_last_error[0] = '\0';
+    const bool append = a.kcache || a.vcache;
+    if (a.T < 0 || a.H < 1 || a.H_kv < 0 || (append && (a.H_kv < 1 || a.B < 1 || a.Skv < 0)))
+        return fail(ATTN_EINVAL, "%s: need T >= 0, H >= 1, H_kv >= %d%s", who, append ? 1 : 0,
+                    append ? ", B >= 1, Skv >= 0" : "");
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return fail(ATTN_EINVAL, "%s: unknown dtype %d", who, dtype);
+    if (a.D <= 0) return fail(ATTN_EINVAL, "%s: D must be positive (got %d)", who, a.D);
+    if (a.D != 64 && a.D != 128) return fail(ATTN_EUNSUPPORTED, "%s: D = %d not supported (64 or 128)", who, a.D);
+    if (a.rotary_dim < 0 || a.rotary_dim > a.D || a.rotary_dim % 2)
+        return fail(ATTN_EINVAL, "%s: rotary_dim must be even, in [0, D] (got %d)", who, a.rotary_dim);
+    if ((a.interleaved != 0 && a.interleaved != 1) || (inverse != 0 && inverse != 1))
+        return fail(ATTN_EINVAL, "%s: interleaved and inverse must be 0 or 1", who);
+    if (!(fabsf(a.mscale) <= 3.4e38f)) return fail(ATTN_EINVAL, "%s: mscale must be finite", who);
+    if (a.rotary_dim > 0 && !freqs) return fail(ATTN_EINVAL, "%s: freqs must not be NULL", who);
+    for (int p = 0; p < a.rotary_dim / 2; ++p)
+        if (!isfinite(freqs[p])) return fail(ATTN_EINVAL, "%s: freqs[%d] is not finite", who, p);
+    if (a.T == 0) return ATTN_OK;
+    if (!a.q || !a.q_out || (a.H_kv > 0 && !a.k) || (!append && a.H_kv > 0 && !a.k_out) ||
+        (append && (!a.v || (a.Skv > 0 && (!a.kcache || !a.vcache)))))
+        return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
+    if (!append && !a.positions) return fail(ATTN_EINVAL, "%s: positions must not be NULL", who);
+    if (append && !a.cu_seqlens && a.T % a.B)
+        return fail(ATTN_EINVAL, "%s: without cu_seqlens T must be a multiple of B (got %d, %d)", who, a.T, a.B);
+    const long long esz = dtype == ATTN_BF16 ? 2 : 4;
+    const uintptr_t amask = static_cast<uintptr_t>(esz - 1);
+    if ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+         reinterpret_cast<uintptr_t>(a.q_out) | reinterpret_cast<uintptr_t>(a.k_out)) & amask)
+        return fail(ATTN_EINVAL, "%s: tensors must be aligned to their element size", who);
+    if (!aligned16(a.kcache) || !aligned16(a.vcache))
+        return fail(ATTN_EINVAL, "%s: kcache and vcache must be 16-byte aligned", who);
+    if ((reinterpret_cast<uintptr_t>(a.cu_seqlens) | reinterpret_cast<uintptr_t>(a.cache_len) |
+         reinterpret_cast<uintptr_t>(a.positions)) & 3u)
+        return fail(ATTN_EINVAL, "%s: cu_seqlens, cache_len and positions must be 4-byte aligned", who);
+    // views: q, k, v, q_out, k_out
+    const void *ptrs[5] = {a.q, a.H_kv ? a.k : nullptr, append ? a.v : nullptr, a.q_out, a.H_kv ? a.k_out : nullptr};
+    const int heads[5] = {a.H, a.H_kv, a.H_kv, a.H, a.H_kv};
+    const char *names[5] = {"q", "k", "v", "q_out", "k_out"};
+    const long long vec = 16 / esz;
+    Rows rows[5];
+    long long st[5][2];
+    bool wide = (a.rotary_dim / 2) % vec == 0;
+    for (int i = 0; i < 5; ++i) {
+        st[i][0] = strides ? strides[2 * i] : static_cast<long long>(heads[i]) * a.D;
+        st[i][1] = strides ? strides[2 * i + 1] : a.D;
+        rows[i] = make_rows(ptrs[i], a.T, heads[i], st[i][0], st[i][1], a.D, esz);
+        if (!ptrs[i]) continue;
+        if (!rows_distinct(rows[i]))
+            return fail(ATTN_EINVAL, "%s: the rows of %s overlap (strides %lld, %lld)", who, names[i], st[i][0], st[i][1]);
+        st[i][0] = rows[i].so / esz;
+        st[i][1] = rows[i].si / esz;
+        wide = wide && aligned16(ptrs[i]) && st[i][0] % vec == 0 && st[i][1] % vec == 0;
+    }
+    // an output may be its own input (in place); any other overlap is an error
+    for (int o = 3; o < 5; ++o)
+        for (int i = 0; i < 5; ++i) {
+            if (i == o || (i < 3 && i == o - 3 && same_rows(rows[i], rows[o]))) continue;
+            if (rows_overlap(rows[o], rows[i])) return fail(ATTN_EINVAL, "%s: %s overlaps %s", who, names[o], names[i]);
+        }
+    if (append) {
+        const long long cache_rows = static_cast<long long>(a.B) * a.H_kv;
+        const long long head = static_cast<long long>(a.Skv) * a.D;
+        const Rows kc = make_rows(a.kcache, cache_rows, 1, head, head, head, esz);
+        const Rows vc = make_rows(a.vcache, cache_rows, 1, head, head, head, esz);
+        if (a.Skv > 0) {
+            if (rows_overlap(kc, vc)) return fail(ATTN_EINVAL, "%s: kcache overlaps vcache", who);
+            for (int i = 0; i < 5; ++i)
+                if (rows_overlap(kc, rows[i]) || rows_overlap(vc, rows[i]))
+                    return fail(ATTN_EINVAL, "%s: %s overlaps a cache", who, names[i]);
+        }
+    }
+    a.q_ts = st[0][0], a.q_hs = st[0][1], a.k_ts = st[1][0], a.k_hs = st[1][1], a.v_ts = st[2][0], a.v_hs = st[2][1];
+    a.qo_ts = st[3][0], a.qo_hs = st[3][1], a.ko_ts = st[4][0], a.ko_hs = st[4][1];
+    // frequencies as fractions of a turn per position, modulo 1 (positions are whole numbers)
+    for (int p = 0; p < a.rotary_dim / 2; ++p) {
+        double f = freqs[p] / 6.283185307179586476925286766559;
+        f -= floor(f);
+        a.turns[p] = f < 1.0 ? static_cast<uint64_t>(ldexp(f, 64)) : 0;
+    }
+    a.sin_scale = inverse ? -a.mscale : a.mscale;
+    a.n_sm = num_sms();
+    a.stream = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_rope(a, dtype == ATTN_F32, wide);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, who);
+}
+
+ATTN_API int attn_rope(const void *q, const void *k, void *q_out, void *k_out, int T, int H, int H_kv, int D,
+                       const long long *strides, const int32_t *positions, const double *freqs, int rotary_dim,
+                       int interleaved, int inverse, float mscale, int dtype, void *stream) {
+    RopeArgs a{};
+    a.q = q, a.k = k, a.q_out = q_out, a.k_out = k_out;
+    a.T = T, a.H = H, a.H_kv = H_kv, a.D = D;
+    a.positions = positions;
+    a.rotary_dim = rotary_dim, a.interleaved = interleaved, a.mscale = mscale;
+    // strides holds q, k, q_out, k_out; rope_impl takes q, k, v, q_out, k_out
+    long long st[10] = {};
+    if (strides) {
+        for (int i = 0; i < 4; ++i) st[i] = strides[i];
+        for (int i = 0; i < 4; ++i) st[6 + i] = strides[4 + i];
+    }
+    return rope_impl("attn_rope", a, strides ? st : nullptr, freqs, inverse, dtype, stream);
+}
+
+ATTN_API int attn_rope_append(const void *q, const void *k, const void *v, void *q_out, void *k_out, void *kcache,
+                              void *vcache, int T, int H, int H_kv, int D, const long long *strides, int B, int Skv,
+                              const int32_t *cu_seqlens, const int32_t *cache_len, const int32_t *positions,
+                              const double *freqs, int rotary_dim, int interleaved, float mscale, int dtype,
+                              void *stream) {
+    g_last_error[0] = '\0';
+    if (!kcache || !vcache) return fail(ATTN_EINVAL, "attn_rope_append: kcache and vcache must not be NULL");
+    RopeArgs a{};
+    a.q = q, a.k = k, a.v = v, a.q_out = q_out, a.k_out = k_out, a.kcache = kcache, a.vcache = vcache;
+    a.T = T, a.H = H, a.H_kv = H_kv, a.D = D, a.B = B, a.Skv = Skv;
+    a.cu_seqlens = cu_seqlens, a.cache_len = cache_len, a.positions = positions;
+    a.rotary_dim = rotary_dim, a.interleaved = interleaved, a.mscale = mscale;
+    return rope_impl("attn_rope_append", a, strides, freqs, 0, dtype, stream);
 }
 
 ATTN_API int attn_device_status(void *stream) {

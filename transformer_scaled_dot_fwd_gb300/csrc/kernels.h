@@ -123,6 +123,27 @@ int decode_tc_chunk(int B, int H_kv, int Skv, int n_sm);
 cudaError_t launch_decode_tc(const DecodeArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
                              const CUtensorMap &tv);
 
+// Rotary positions (attn_rope, attn_rope_append).  Rows are (token, head) with
+// element strides; kcache == nullptr: no append.
+constexpr int kRopeMaxTokens = 8;  // tokens a block takes at most
+struct RopeArgs {
+    const void *q, *k, *v;      // (T, H | H_kv, D); v only with a cache
+    void *q_out, *k_out;        // k_out may be nullptr with a cache
+    void *kcache, *vcache;      // (B, H_kv, Skv, D) or nullptr
+    const int32_t *cu_seqlens;  // device int32[B + 1] or nullptr (T / B tokens each)
+    const int32_t *cache_len;   // device int32[B] or nullptr (Skv)
+    const int32_t *positions;   // device int32[T] or nullptr (the cache row)
+    long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+    int T, H, H_kv, D, B, Skv;
+    int rotary_dim, interleaved;
+    float mscale, sin_scale;    // multipliers of cos and of sin (negative sin_scale: inverse)
+    int n_sm;
+    cudaStream_t stream;
+    uint64_t turns[64];         // w_p / 2 pi as a fraction of 2^64
+};
+// wide: every address, stride and rotary_dim / 2 allows 16-byte accesses
+cudaError_t launch_rope(const RopeArgs &a, bool f32, bool wide);
+
 // Size of the library-static decode scratch used by attn_decode_noalloc.
 constexpr size_t kDecodeNoAllocScratchBytes = 32u << 20;
 
