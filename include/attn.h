@@ -332,6 +332,83 @@ ATTN_API int attn_decode_noalloc(const void *q, const void *kcache, const void *
 ATTN_API int attn_decode_splits(int B, int H, int Skv, int D);
 
 /*
+ * attn_fwd_packed -- prefill attention of sequences of different lengths packed
+ * one behind the other, without padding.
+ *
+ * Sequence s is tokens [cu_seqlens[s], cu_seqlens[s + 1]) of token-major (T, H, D)
+ * tensors, as projections write them.  Each sequence attends to itself only:
+ * token i of it sees its tokens j (j <= i when causal).  Grouped heads as in
+ * attn_fwd_gqa.  Rows outside every sequence (before cu_seqlens[0], from
+ * cu_seqlens[n_seq] on) are left as they were in out and lse.  A key that a row
+ * does not see leaves no trace in it, whatever its K and V hold: another
+ * sequence's or a later token's infinities and NaNs stay theirs.  Sequences of
+ * length 0 are allowed.
+ *
+ *   q, out    (T, H, D) rows; k, v  (T, H_kv, D) rows; out must not overlap
+ *             the inputs (slices of one fused matrix do not)
+ *   lse       NULL, or device float (T, H), written: the natural log-sum-exp
+ *             of each row's scaled scores
+ *   strides   NULL (contiguous), or HOST int64[8]: elements from token to token
+ *             and from head to head of q, k, v and out, multiples of 16 bytes;
+ *             pointers 16-byte aligned; rows of one tensor must not overlap
+ *   cu_seqlens  device int32[n_seq + 1], nondecreasing, within [0, T].  Other
+ *             contents give undefined rows of out, never an access outside
+ *             the tensors.
+ *   workspace   device memory of attn_fwd_packed_workspace(...) bytes, 16-byte
+ *             aligned (bf16; fp32 needs none), used until the call's work on
+ *             `stream` is done.  Calls that may run at the same time need one
+ *             each, and a captured call keeps its address.
+ *
+ * Scores are held as base-2 exponents in fp32: scaled scores above 2.3e38 in
+ * magnitude count as infinite.  A row whose every score is -inf is a NaN.
+ *
+ * dtype, D, scale and errors as in attn_fwd; "Concurrency" there applies to the
+ * bf16 form.  Results do not depend on how the sequences are packed or scheduled.
+ */
+ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *out, float *lse, int T, int H, int H_kv,
+                             int D, const long long *strides, const int32_t *cu_seqlens, int n_seq, float scale,
+                             int causal, int dtype, void *workspace, long long workspace_bytes, void *stream);
+/* Bytes of workspace that call needs (0 for fp32); negative on bad sizes. */
+ATTN_API long long attn_fwd_packed_workspace(int T, int n_seq, int H, int H_kv, int dtype);
+
+/*
+ * attn_decode_tree -- attention of a tree of drafted tokens over a KV cache:
+ * all the drafts of a speculative step in one pass over the cache.
+ *
+ * Sequence b has L_b = cache_len[b] valid cache rows, the last n_b =
+ * draft_len[b] of them drafted tokens in tree order (attn_rope_append puts
+ * them there).  Drafted token t hangs under drafted token parents[b][t] < t, or
+ * under the committed cache when that is negative (or not below t).  It sees
+ * the committed rows [0, L_b - n_b), its ancestors and itself.  A chain
+ * (parents[t] = t - 1) is attn_fwd_chunked's causal chunk.  Rows t >= n_b, and
+ * tokens whose cache row L_b - n_b + t is negative, are written as zeros.  Rows
+ * that a token does not see leave no trace in it, whatever they hold.
+ *
+ *   q, out      (B, H, T, D) rows, T <= 128
+ *   kcache, vcache  (B, H_kv, Skv, D), contiguous; H_kv divides H
+ *   strides     NULL (contiguous), or HOST int64[6]: elements from sequence to
+ *               sequence, head to head and token to token of q and of out,
+ *               multiples of 16 bytes (a token-major (B, T, H, D) tensor is one
+ *               choice)
+ *   parents     device int32, T values per sequence, parents_stride apart; 0:
+ *               one tree for all
+ *   cache_len   device int32[B], clamped to [0, Skv], or NULL (Skv)
+ *   draft_len   device int32[B], clamped to [0, T], or NULL (T)
+ *   workspace   device memory of attn_decode_tree_workspace(...) bytes, 16-byte
+ *               aligned (may be NULL when that is 0); rules as in attn_fwd_packed
+ *
+ * The splits of a sequence are merged in order: a call gives the same bits
+ * every time.  Scores beyond fp32's range as in attn_fwd_packed.  dtype, D, scale and errors as in attn_fwd; T > 128 returns
+ * ATTN_EUNSUPPORTED.
+ */
+ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vcache, void *out, int B, int H, int H_kv,
+                              int T, int Skv, int D, const long long *strides, const int32_t *parents,
+                              int parents_stride, const int32_t *cache_len, const int32_t *draft_len, float scale,
+                              int dtype, void *workspace, long long workspace_bytes, void *stream);
+/* Bytes of workspace that call needs on the current device (may be 0); negative on bad sizes. */
+ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int Skv, int D, int dtype);
+
+/*
  * attn_rope -- rotary positions: turns the pairs of each head row of q and k by
  * an angle proportional to the row's position, before attention or caching.
  *

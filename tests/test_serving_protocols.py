@@ -1,0 +1,319 @@
+"""CPU models of the mbarrier protocols of the packed prefill and the tree decode
+kernels: the prefill and decode protocols (test_barrier_protocols.py) with the
+guard warps that pass over the V tiles at the edge of what rows see.
+
+The guard waits for a request that the producer files after issuing a V load,
+then for that load, and the MMA warp waits for the guard before it reads the
+tile.  Random interleavings must finish, no wait may see its barrier two phases
+ahead, a tile must be loaded when the guard passes over it and clean when the
+MMA reads it, and an open request's slot must not be filed again.
+"""
+from __future__ import annotations
+
+import random
+
+import pytest
+
+from test_barrier_protocols import RING, Bar, Hazard, Sched, wait
+
+GUARD_RING = 8
+
+
+def wait_parity(bar, phase):
+    """What the hardware tests: the phase in progress has the other parity.  It
+    also holds one phase too early, which the guard's request has to rule out."""
+    return lambda: (bar.phase - phase) % 2 == 1
+
+
+def packed_run(items, stages, seed, mistake=None):
+    """items: (n_kv0, n_kv1, N, first edge tile)."""
+    sc = Sched(seed)
+    item_full, item_empty = [Bar() for _ in range(RING)], [Bar(3) for _ in range(RING)]
+    q_full, q_empty = [Bar(), Bar()], [Bar(), Bar()]
+    kv_full, kv_empty = [Bar() for _ in range(stages)], [Bar() for _ in range(stages)]
+    s_full, p_ready, o_full = [Bar(), Bar()], [Bar(), Bar()], [Bar(), Bar()]
+    g_full, g_clean = [Bar() for _ in range(GUARD_RING)], [Bar(2) for _ in range(GUARD_RING)]
+    req, ring = [None] * GUARD_RING, [None] * RING
+    cleaned_uses = set()
+    stream = list(items) + [(0, 0, -1, 0)]
+
+    def producer():
+        q_uses, issued, requests = [0, 0], 0, 0
+        for k, it in enumerate(stream):
+            slot = k % RING
+            if k >= RING:
+                yield wait(item_empty[slot], k // RING - 1)
+            ring[slot] = it
+            item_full[slot].arrive()
+            if it[2] < 0:
+                break
+
+            def load_q(x):
+                if it[x] == 0:
+                    return
+                if q_uses[x] > 0:
+                    yield wait(q_empty[x], q_uses[x] - 1)
+                sc.tma.append(q_full[x])
+                q_uses[x] += 1
+
+            def load_kv(j, kv):
+                nonlocal issued, requests
+                s = issued % stages
+                if issued >= stages:
+                    yield wait(kv_empty[s], issued // stages - 1)
+                sc.tma.append(kv_full[s])
+                if kv and j >= it[3]:
+                    assert req[requests % GUARD_RING] is None, "request slot still open"
+                    req[requests % GUARD_RING] = (s, issued // stages, issued)
+                    g_full[requests % GUARD_RING].arrive()
+                    requests += 1
+                issued += 1
+
+            yield from load_q(0)
+            for j in range(it[2]):
+                yield from load_kv(j, 0)
+                if j == 0:
+                    yield from load_q(1)
+                yield from load_kv(j, 1)
+        assert req[requests % GUARD_RING] is None, "request slot still open"
+        req[requests % GUARD_RING] = (-1, 0, 0)
+        g_full[requests % GUARD_RING].arrive()
+
+    def guard(lane):
+        r = 0
+        while True:
+            yield wait(g_full[r % GUARD_RING], r // GUARD_RING)
+            s, phase, use = req[r % GUARD_RING]
+            if s < 0:
+                return
+            if mistake == "guard_off_by_a_phase":
+                phase += 1
+            yield wait_parity(kv_full[s], phase)
+            assert kv_full[s].phase == phase + 1, "guard passes over a tile that is not the one requested"
+            if lane == 1:
+                cleaned_uses.add(use)
+            if g_clean[r % GUARD_RING].pending == 1:  # the other warp is done too
+                req[r % GUARD_RING] = None
+            g_clean[r % GUARD_RING].arrive()
+            r += 1
+
+    def mma():
+        consumed, cleaned, q_uses, pr = 0, 0, [0, 0], [0, 0]
+        for k in range(len(stream)):
+            yield wait(item_full[k % RING], k // RING)
+            n0, n1, N, edge = ring[k % RING]
+            item_empty[k % RING].arrive()
+            if N < 0:
+                return
+            kslot, have_k = 0, False
+            for x, n in enumerate((n0, n1)):
+                if n == 0:
+                    continue
+                yield wait(q_full[x], q_uses[x])
+                q_uses[x] += 1
+                if not have_k:
+                    kslot = consumed % stages
+                    yield wait(kv_full[kslot], consumed // stages)
+                    consumed += 1
+                    have_k = True
+                sc.commit.append(s_full[x])
+                if n == 1:
+                    sc.commit.append(q_empty[x])
+            sc.commit.append(kv_empty[kslot])
+            for j in range(N):
+                vslot, use = consumed % stages, consumed
+                yield wait(kv_full[vslot], consumed // stages)
+                consumed += 1
+                if j >= edge:
+                    if mistake != "mma_skips_guard":
+                        yield wait(g_clean[cleaned % GUARD_RING], cleaned // GUARD_RING)
+                    cleaned += 1
+                    assert use in cleaned_uses, "edge tile read before it was clean"
+                if j < n0:
+                    yield wait(p_ready[0], pr[0])
+                    pr[0] += 1
+                    if j == n0 - 1:
+                        sc.commit.append(o_full[0])
+                nxt, nslot = j + 1 < N, 0
+                if nxt:
+                    nslot = consumed % stages
+                    yield wait(kv_full[nslot], consumed // stages)
+                    consumed += 1
+                    if j + 1 < n0:
+                        sc.commit.append(s_full[0])
+                        if j + 2 == n0:
+                            sc.commit.append(q_empty[0])
+                if j < n1:
+                    yield wait(p_ready[1], pr[1])
+                    pr[1] += 1
+                    if j == n1 - 1:
+                        sc.commit.append(o_full[1])
+                sc.commit.append(kv_empty[vslot])
+                if nxt:
+                    if j + 1 < n1:
+                        sc.commit.append(s_full[1])
+                        if j + 2 == n1:
+                            sc.commit.append(q_empty[1])
+                    sc.commit.append(kv_empty[nslot])
+
+    def softmax(x):
+        sp, o_uses = 0, 0
+        for k in range(len(stream)):
+            slot = k % RING
+            yield wait(item_full[slot], k // RING)
+            it = ring[slot]
+            if it[2] < 0:
+                item_empty[slot].arrive()
+                return
+            for _ in range(it[x]):
+                yield wait(s_full[x], sp)
+                sp += 1
+                p_ready[x].arrive()
+            if it[x] > 0:
+                yield wait(o_full[x], o_uses)
+                o_uses += 1
+            assert ring[slot] is it, "item ring slot overwritten before it was released"
+            item_empty[slot].arrive()
+
+    return sc.run({"producer": producer(), "mma": mma(), "softmax0": softmax(0), "softmax1": softmax(1),
+                   "guard0": guard(0), "guard1": guard(1)})
+
+
+def packed_items(rnd):
+    out = []
+    for _ in range(rnd.randint(1, 24)):
+        N = rnd.choice((1, 1, 1, 2, 3, rnd.randint(1, 9)))
+        kind = rnd.random()
+        if kind < 0.4:
+            out.append((N, N, N, N - 1))                             # two heads, diagonal tile last
+        elif kind < 0.7:
+            out.append((N - 1, N, N, N - 2) if N > 1 else (1, 0, 1, 0))  # causal pair of tiles
+        elif kind < 0.85:
+            out.append((N, N, N, rnd.choice((N - 1, N))))            # not causal: ragged end or none
+        else:
+            out.append((N, 0, N, N - 1))
+    return out
+
+
+def _trials(stages, mistake=None, trials=150):
+    rnd = random.Random(stages + 100 * (mistake is not None))
+    bad = []
+    for t in range(trials):
+        items = packed_items(rnd)
+        for seed in range(2):
+            try:
+                r = packed_run(items, stages, seed + 10 * t, mistake)
+            except (Hazard, AssertionError) as e:
+                r = f"{type(e).__name__}: {e}"
+            if r:
+                bad.append((t, seed, r, items))
+    return bad
+
+
+@pytest.mark.parametrize("stages", [4, 8])  # the K/V ring at D = 128 and D = 64
+def test_packed_protocol(stages):
+    bad = _trials(stages)
+    assert not bad, bad[:3]
+
+
+@pytest.mark.parametrize("mistake", ["mma_skips_guard", "guard_off_by_a_phase"])
+def test_packed_model_catches_planted_mistakes(mistake):
+    assert _trials(4, mistake, trials=60), f"the model missed '{mistake}'"
+
+
+# ----------------------------------------------------------------------------- tree
+
+def tree_run(n, edge, stages, seed, p_rescale, mistake=None):
+    """n tiles of 64 keys, those from `edge` on guarded."""
+    sc = Sched(seed)
+    q_full = Bar()
+    kv_full, kv_empty = [Bar() for _ in range(stages)], [Bar() for _ in range(stages)]
+    s_full, p_ready = [Bar(), Bar()], [Bar(), Bar()]
+    o_done, o_full = Bar(), Bar()
+    e_full, e_clean = [Bar() for _ in range(4)], [Bar(2) for _ in range(4)]
+    clean = set()
+
+    def producer():
+        for issued in range(2 * n):
+            j, kv, s = issued // 2, issued % 2, issued % stages
+            if issued >= stages:
+                yield wait(kv_empty[s], issued // stages - 1)
+            sc.tma.append(kv_full[s])
+            if kv and j >= edge:
+                e_full[j - edge].arrive()
+
+    def guard(lane):
+        for j in range(edge, n):
+            u = 2 * j + 1
+            if mistake != "no_request":
+                yield wait(e_full[j - edge], 0)
+            yield wait_parity(kv_full[u % stages], u // stages)
+            assert kv_full[u % stages].phase == u // stages + 1, "guard is on another use of the stage"
+            if lane == 1:
+                clean.add(j)
+            e_clean[j - edge].arrive()
+
+    def mma():
+        yield wait(q_full, 0)
+        pr = [0, 0]
+        for j in range(n + 1 if n else 0):
+            if j < n:
+                ks = (2 * j) % stages
+                yield wait(kv_full[ks], (2 * j) // stages)
+                sc.commit.append(s_full[j & 1])
+                sc.commit.append(kv_empty[ks])
+            if j >= 1:
+                t = j - 1
+                x, vs = t & 1, (2 * t + 1) % stages
+                yield wait(kv_full[vs], (2 * t + 1) // stages)
+                if t >= edge:
+                    if mistake != "mma_skips_guard":
+                        yield wait(e_clean[t - edge], 0)
+                    assert t in clean, "edge tile read before it was clean"
+                yield wait(p_ready[x], pr[x])
+                pr[x] += 1
+                sc.commit.append(o_done)
+                sc.commit.append(kv_empty[vs])
+                if t == n - 1:
+                    sc.commit.append(o_full)
+
+    def softmax():
+        rnd = random.Random(seed + 1)
+        q_full.arrive()
+        sp = [0, 0]
+        for j in range(n):
+            x = j & 1
+            yield wait(s_full[x], sp[x])
+            sp[x] += 1
+            if j > 0 and rnd.random() < p_rescale:
+                yield wait(o_done, j - 1)
+            p_ready[x].arrive()
+        if n:
+            yield wait(o_full, 0)
+
+    return sc.run({"producer": producer(), "mma": mma(), "softmax": softmax(), "guard0": guard(0), "guard1": guard(1)})
+
+
+def _tree_trials(mistake=None):
+    bad = []
+    for n in range(0, 20):
+        for edge in range(max(0, n - 4), n + 1):
+            for seed in range(5):
+                for p in (0.0, 0.4, 1.0):
+                    try:
+                        r = tree_run(n, edge, 4, seed * 31 + n, p, mistake)
+                    except (Hazard, AssertionError) as e:
+                        r = f"{type(e).__name__}: {e}"
+                    if r:
+                        bad.append((n, edge, seed, p, r))
+    return bad
+
+
+def test_tree_protocol():
+    bad = _tree_trials()
+    assert not bad, bad[:3]
+
+
+@pytest.mark.parametrize("mistake", ["mma_skips_guard", "no_request"])
+def test_tree_model_catches_planted_mistakes(mistake):
+    assert _tree_trials(mistake), f"the model missed '{mistake}'"

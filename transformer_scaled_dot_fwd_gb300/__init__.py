@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -31,7 +32,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libattn.so")
 
 # The exported functions, as declared in include/attn.h: name -> (restype, argtypes)
-_vp, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+_vp, _i, _f, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
 SIGNATURES = {
     "attn_fwd": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _i, _vp]),
     "attn_fwd_gqa": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _i, _vp]),
@@ -42,6 +43,10 @@ SIGNATURES = {
     "attn_decode_gqa": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
     "attn_decode_noalloc": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp]),
     "attn_decode_splits": (_i, [_i, _i, _i, _i]),
+    "attn_fwd_packed": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _i, _f, _i, _i, _vp, _ll, _vp]),
+    "attn_fwd_packed_workspace": (_ll, [_i, _i, _i, _i, _i]),
+    "attn_decode_tree": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _f, _i, _vp, _ll, _vp]),
+    "attn_decode_tree_workspace": (_ll, [_i, _i, _i, _i, _i, _i, _i]),
     "attn_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp]),
     "attn_rope_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
                               _i, _i, _f, _i, _vp]),
@@ -330,6 +335,116 @@ def attn_decode_splits(B: int, H: int, Skv: int, D: int) -> int:
     return lib().attn_decode_splits(B, H, Skv, D)
 
 
+def _alloc_scope(stream):
+    """Context in which allocations belong to the stream the call runs on, so
+    that the caching allocator orders their reuse with it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+@functools.lru_cache(maxsize=4096)
+def _packed_workspace(T, n_seq, H, H_kv, dtype):
+    return lib().attn_fwd_packed_workspace(T, n_seq, H, H_kv, dtype)
+
+
+@functools.lru_cache(maxsize=4096)
+def _tree_workspace(B, H, H_kv, T, Skv, D, dtype, device):
+    return lib().attn_decode_tree_workspace(B, H, H_kv, T, Skv, D, dtype)
+
+
+def attn_fwd_packed(q, k, v, cu_seqlens, out=None, lse=None, scale: Optional[float] = None, causal: bool = False,
+                    return_lse: bool = False, stream=None):
+    """Prefill attention of packed sequences: q (T, H, D), k and v (T, H_kv, D),
+    sequence s being tokens [cu_seqlens[s], cu_seqlens[s + 1]) (int32, on the
+    device).  Rows may be strided (slices of a fused projection).  Returns
+    ``out`` (T, H, D), or ``(out, lse)`` with the (T, H) fp32 log-sum-exp when
+    ``return_lse`` (or an ``lse`` tensor) is given.  Rows outside every sequence
+    are not written.  See include/attn.h.
+    """
+    _check_rows("q", q)
+    _check_rows("k", k, q)
+    _check_rows("v", v, q)
+    T, H, D = q.shape
+    H_kv = k.shape[1]
+    if v.shape != k.shape or H_kv < 1 or H % H_kv:
+        raise ValueError("k and v must be (T, H_kv, D) matching q, with H_kv dividing H")
+    n_seq = cu_seqlens.shape[0] - 1 if cu_seqlens is not None and cu_seqlens.dim() == 1 else -1
+    if n_seq < 0:
+        raise ValueError("cu_seqlens must be 1-D with at least one value")
+    cu = _ints_arg("cu_seqlens", cu_seqlens, n_seq + 1, q.device)
+    dtype = _dtype_code(q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    torch = _torch()
+    with _on_device(q.device), _alloc_scope(stream):
+        if out is None:
+            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        _check_rows("out", out, q)
+        if out.shape != q.shape:
+            raise ValueError("out must match q's shape")
+        if lse is None and return_lse:
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        if lse is not None and not (lse.dtype == torch.float32 and tuple(lse.shape) == (T, H) and lse.is_contiguous()
+                                    and lse.device == q.device):
+            raise ValueError("lse must be a contiguous float32 (T, H) tensor on q's device")
+        need = _packed_workspace(T, n_seq, H, H_kv, dtype)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        rc = lib().attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), T, H, H_kv, D,
+                                   _strides(q, k, v, out), cu.data_ptr(), n_seq, float(scale), int(bool(causal)), dtype,
+                                   _ptr(ws), need, _stream_handle(stream))
+    _check(rc)
+    return (out, lse) if lse is not None else out
+
+
+def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None, out=None,
+                     scale: Optional[float] = None, stream=None):
+    """Attention of a tree of T <= 128 drafted tokens per sequence over a KV cache:
+    q (B, H, T, D) (any strides, contiguous head rows), caches (B, H_kv, Skv, D).
+    Sequence b's last draft_len[b] (default T) of its cache_len[b] (default Skv)
+    cache rows are the drafted tokens; ``parents`` int32 (B, T), or (T,) for one
+    tree, holds each token's parent among them, -1 for none.  A token sees the
+    committed cache, its ancestors and itself.  Returns ``out`` like q; rows
+    without a token are zeros.  See include/attn.h.
+    """
+    if not q.is_cuda or q.dim() != 4 or q.stride(3) != 1:
+        raise ValueError("q must be a CUDA (B, H, T, D) tensor with contiguous rows of D elements")
+    _check_tensor("kcache", kcache, 4)
+    _check_tensor("vcache", vcache, 4)
+    B, H, T, D = q.shape
+    H_kv, Skv = kcache.shape[1], kcache.shape[2]
+    if (tuple(kcache.shape) != (B, H_kv, Skv, D) or vcache.shape != kcache.shape or H_kv < 1 or H % H_kv):
+        raise ValueError("kcache and vcache must be (B, H_kv, Skv, D) matching q, with H_kv dividing H")
+    if not (q.dtype == kcache.dtype == vcache.dtype):
+        raise TypeError("q, kcache, vcache must share one dtype")
+    if kcache.device != q.device or vcache.device != q.device:
+        raise ValueError("the caches must be on q's device")
+    torch = _torch()
+    if not (parents.is_cuda and parents.dtype == torch.int32 and parents.is_contiguous() and parents.device == q.device
+            and tuple(parents.shape) in ((T,), (B, T))):
+        raise ValueError("parents must be a contiguous int32 (B, T) or (T,) tensor on q's device")
+    cl = _kv_len_arg(cache_len, B, q.device)
+    dl = _kv_len_arg(draft_len, B, q.device)
+    dtype = _dtype_code(q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on_device(q.device), _alloc_scope(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if not out.is_cuda or out.device != q.device or out.shape != q.shape or out.dtype != q.dtype or out.stride(3) != 1:
+            raise ValueError("out must match q's shape, dtype and device, with contiguous rows")
+        need = _tree_workspace(B, H, H_kv, T, Skv, D, dtype, q.device.index) if B and T and T <= 128 else 0
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        sq, so = q.stride(), out.stride()
+        rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), out.data_ptr(), B, H, H_kv, T,
+                                    Skv, D, (ctypes.c_longlong * 6)(sq[0], sq[1], sq[2], so[0], so[1], so[2]),
+                                    parents.data_ptr(), 0 if parents.dim() == 1 else T, _ptr(cl), _ptr(dl),
+                                    float(scale), dtype, _ptr(ws), max(need, 0), _stream_handle(stream))
+    _check(rc)
+    return out
+
+
 def _check_rows(name, t, like=None):
     """A (T, heads, D) CUDA tensor whose head rows are contiguous."""
     if not t.is_cuda:
@@ -508,7 +623,8 @@ def attn_release() -> None:
 
 
 __all__ = [
-    "attn_fwd", "attn_fwd_chunked", "attn_fwd_debug", "attn_fwd_host", "attn_decode", "attn_decode_noalloc", "attn_decode_splits", "attn_rope",
+    "attn_fwd", "attn_fwd_chunked", "attn_fwd_debug", "attn_fwd_host", "attn_decode", "attn_decode_noalloc", "attn_decode_splits", "attn_fwd_packed", "attn_decode_tree",
+    "attn_rope",
     "attn_rope_append", "attn_rope_frequencies", "attn_device_status", "attn_release",
     "attn_last_error", "attn_selftest_wait_timeout", "lib", "AttnError", "SIGNATURES", "LIB_PATH",
     "ATTN_F32", "ATTN_BF16", "ATTN_OK", "ATTN_EINVAL", "ATTN_EUNSUPPORTED", "ATTN_ECUDA",

@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libattn.so")
 SOURCES = ["api.cu", "prefill_tc.cu", "prefill_f32.cu", "decode.cu", "decode_gqa.cu", "decode_tc.cu", "decode_f32.cu", "decode_noalloc.cu", "debug.cu",
-           "rope.cu"]
+           "rope.cu", "tile_f32.cu", "tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

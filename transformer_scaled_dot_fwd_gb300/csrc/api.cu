@@ -188,6 +188,24 @@ int make_map_rows(CUtensorMap *map, const void *base, int D, long long rows) {
     return ATTN_OK;
 }
 
+// (D, T, heads) bf16 view of (T, heads, D) rows with byte strides; boxes of
+// 64 x 128 x 1 with 128-byte swizzle, rows past the end read as zero.
+int make_map_packed(CUtensorMap *map, const Rows &r, int D) {
+    EncodeTiledFn encode;
+    int rc = get_encode(&encode);
+    if (rc) return rc;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(r.n_outer),
+                                static_cast<cuuint64_t>(r.n_inner)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(r.so), static_cast<cuuint64_t>(r.si)};
+    const cuuint32_t box[3] = {64, 128, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult e = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<char *>(r.p), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) return fail(ATTN_ECUDA, "cuTensorMapEncodeTiled (packed) failed (%d)", static_cast<int>(e));
+    return ATTN_OK;
+}
+
 // ------------------------------------------------------------ decode workspace
 
 // The decode partials.  A buffer the workspace outgrows is kept on the
@@ -655,6 +673,204 @@ ATTN_API int attn_decode_noalloc(const void *q, const void *kcache, const void *
                  chunk, n_split, nullptr, nullptr, status, static_cast<cudaStream_t>(stream), H};
     cudaError_t e = launch_decode_noalloc(a, dtype == ATTN_F32);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_decode_noalloc launch");
+}
+
+ATTN_API long long attn_fwd_packed_workspace(int T, int n_seq, int H, int H_kv, int dtype) {
+    if (T < 0 || n_seq < 0 || H < 1 || H_kv < 1 || H % H_kv || (dtype != ATTN_F32 && dtype != ATTN_BF16)) return ATTN_EINVAL;
+    if (dtype == ATTN_F32) return 0;
+    return 16 * (1 + packed_plan_tiles(T, n_seq, packed_unit_rows(H, H_kv)));
+}
+
+ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *out, float *lse, int T, int H, int H_kv,
+                             int D, const long long *strides, const int32_t *cu_seqlens, int n_seq, float scale,
+                             int causal, int dtype, void *workspace, long long workspace_bytes, void *stream) {
+    g_last_error[0] = '\0';
+    const char *who = "attn_fwd_packed";
+    if (T < 0 || n_seq < 0 || H < 1) return fail(ATTN_EINVAL, "%s: need T >= 0, n_seq >= 0, H >= 1", who);
+    if (H_kv < 1 || H % H_kv != 0)
+        return fail(ATTN_EINVAL, "%s: H_kv must divide H (got H = %d, H_kv = %d)", who, H, H_kv);
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return fail(ATTN_EINVAL, "%s: unknown dtype %d", who, dtype);
+    if (D <= 0) return fail(ATTN_EINVAL, "%s: D must be positive (got %d)", who, D);
+    if (D != 64 && D != 128) return fail(ATTN_EUNSUPPORTED, "%s: D = %d not supported (64 or 128)", who, D);
+    if (!(scale >= 0.f) || isinf(scale)) return fail(ATTN_EINVAL, "%s: scale must be finite and >= 0", who);
+    if (causal != 0 && causal != 1) return fail(ATTN_EINVAL, "%s: causal must be 0 or 1", who);
+    if (T == 0 || n_seq == 0) return ATTN_OK;
+    if (!q || !k || !v || !out || !cu_seqlens) return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+        return fail(ATTN_EINVAL, "%s: q, k, v and out must be 16-byte aligned", who);
+    if ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(lse)) & 3u)
+        return fail(ATTN_EINVAL, "%s: cu_seqlens and lse must be 4-byte aligned", who);
+    if (H > 65535) return fail(ATTN_EINVAL, "%s: H must be <= 65535", who);
+    const long long esz = dtype == ATTN_BF16 ? 2 : 4;
+    const void *ptrs[4] = {q, k, v, out};
+    const int heads[4] = {H, H_kv, H_kv, H};
+    const char *names[4] = {"q", "k", "v", "out"};
+    Rows rows[4];
+    for (int i = 0; i < 4; ++i) {
+        const long long ts = strides ? strides[2 * i] : static_cast<long long>(heads[i]) * D;
+        const long long hs = strides ? strides[2 * i + 1] : D;
+        rows[i] = make_rows(ptrs[i], T, heads[i], ts, hs, D, esz);
+        if (!rows_distinct(rows[i]) || rows[i].so >= (1LL << 40) || rows[i].si >= (1LL << 40))
+            return fail(ATTN_EINVAL, "%s: the rows of %s overlap or lie too far apart (strides %lld, %lld)", who, names[i],
+                        ts, hs);
+        if (rows[i].so % 16 || rows[i].si % 16)
+            return fail(ATTN_EINVAL, "%s: the strides of %s must be multiples of 16 bytes", who, names[i]);
+    }
+    for (int i = 0; i < 3; ++i)
+        if (rows_overlap(rows[3], rows[i])) return fail(ATTN_EINVAL, "%s: out overlaps %s", who, names[i]);
+    if (lse) {
+        const Rows lr = make_rows(lse, T, 1, H, H, H, 4);
+        for (int i = 0; i < 4; ++i)
+            if (rows_overlap(lr, rows[i])) return fail(ATTN_EINVAL, "%s: lse overlaps %s", who, names[i]);
+    }
+    const long long need = attn_fwd_packed_workspace(T, n_seq, H, H_kv, dtype);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need || !aligned16(workspace))
+            return fail(ATTN_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes (got %lld)", who, need,
+                        workspace ? workspace_bytes : 0LL);
+        const Rows wr = make_rows(workspace, 1, 1, need, need, need, 1);
+        for (int i = 0; i < 4; ++i)
+            if (rows_overlap(wr, rows[i])) return fail(ATTN_EINVAL, "%s: workspace overlaps %s", who, names[i]);
+        if (overlaps(workspace, static_cast<size_t>(need), cu_seqlens, (static_cast<size_t>(n_seq) + 1) * 4) ||
+            (lse && overlaps(workspace, static_cast<size_t>(need), lse, static_cast<size_t>(T) * H * 4)))
+            return fail(ATTN_EINVAL, "%s: workspace overlaps cu_seqlens or lse", who);
+    }
+    int *status = nullptr;
+    int rc = status_word(&status);
+    if (rc) return rc;
+    PackedArgs a{};
+    a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
+    a.B = n_seq, a.H = H, a.H_kv = H_kv, a.Sq = T, a.Skv = T, a.D = D;
+    a.scale = scale, a.causal = causal, a.status = status;
+    a.stream = static_cast<cudaStream_t>(stream), a.n_sm = num_sms();
+    a.cu_seqlens = cu_seqlens, a.plan = static_cast<const int4 *>(workspace);
+    a.q_ts = rows[0].so / esz, a.q_hs = rows[0].si / esz, a.k_ts = rows[1].so / esz, a.k_hs = rows[1].si / esz;
+    a.v_ts = rows[2].so / esz, a.v_hs = rows[2].si / esz, a.o_ts = rows[3].so / esz, a.o_hs = rows[3].si / esz;
+    cudaError_t e;
+    if (dtype == ATTN_F32) {
+        e = launch_packed_f32(a);
+    } else {
+        const int unit = packed_unit_rows(H, H_kv);
+        const long long tiles = packed_plan_tiles(T, n_seq, unit);
+        if (tiles * (unit == 128 ? H / 2 : H) > 0x7fffffffLL)
+            return fail(ATTN_EINVAL, "%s: %lld tiles of %d heads are too many", who, tiles, H);
+        CUtensorMap tq, tk, tv;
+        if ((rc = make_map_packed(&tq, rows[0], D)) || (rc = make_map_packed(&tk, rows[1], D)) ||
+            (rc = make_map_packed(&tv, rows[2], D)))
+            return rc;
+        e = launch_packed_tc(a, tiles, tq, tk, tv);
+    }
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_fwd_packed launch");
+}
+
+ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int Skv, int D, int dtype) {
+    if (B < 1 || H < 1 || H_kv < 1 || H % H_kv || T < 0 || T > kTreeMaxTokens || Skv < 0 || (D != 64 && D != 128) ||
+        (dtype != ATTN_F32 && dtype != ATTN_BF16))
+        return ATTN_EINVAL;
+    if (T == 0 || Skv == 0) return 0;
+    const long long chunk = tree_chunk(B, H, H_kv, T, Skv, dtype == ATTN_F32, num_sms());
+    const long long n_split = (Skv + chunk - 1) / chunk;
+    return n_split == 1 ? 0 : static_cast<long long>(B) * H * T * n_split * (D + 2) * 4;
+}
+
+ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vcache, void *out, int B, int H, int H_kv,
+                              int T, int Skv, int D, const long long *strides, const int32_t *parents,
+                              int parents_stride, const int32_t *cache_len, const int32_t *draft_len, float scale,
+                              int dtype, void *workspace, long long workspace_bytes, void *stream) {
+    g_last_error[0] = '\0';
+    const char *who = "attn_decode_tree";
+    if (B < 1 || H < 1 || T < 0 || Skv < 0)
+        return fail(ATTN_EINVAL, "%s: need B >= 1, H >= 1, T >= 0, Skv >= 0", who);
+    if (H_kv < 1 || H % H_kv != 0)
+        return fail(ATTN_EINVAL, "%s: H_kv must divide H (got H = %d, H_kv = %d)", who, H, H_kv);
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return fail(ATTN_EINVAL, "%s: unknown dtype %d", who, dtype);
+    if (D <= 0) return fail(ATTN_EINVAL, "%s: D must be positive (got %d)", who, D);
+    if (D != 64 && D != 128) return fail(ATTN_EUNSUPPORTED, "%s: D = %d not supported (64 or 128)", who, D);
+    if (T > kTreeMaxTokens)
+        return fail(ATTN_EUNSUPPORTED, "%s: T = %d drafted tokens, at most %d", who, T, kTreeMaxTokens);
+    if (!(scale >= 0.f) || isinf(scale)) return fail(ATTN_EINVAL, "%s: scale must be finite and >= 0", who);
+    if (parents_stride != 0 && parents_stride < T)
+        return fail(ATTN_EINVAL, "%s: parents_stride must be 0 (one tree for all) or >= T", who);
+    if (T == 0) return ATTN_OK;
+    if (!q || !out || !parents || (Skv > 0 && (!kcache || !vcache))) return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
+    if (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(out))
+        return fail(ATTN_EINVAL, "%s: q, kcache, vcache and out must be 16-byte aligned", who);
+    if ((reinterpret_cast<uintptr_t>(parents) | reinterpret_cast<uintptr_t>(cache_len) |
+         reinterpret_cast<uintptr_t>(draft_len)) & 3u)
+        return fail(ATTN_EINVAL, "%s: parents, cache_len and draft_len must be 4-byte aligned", who);
+    const long long esz = dtype == ATTN_BF16 ? 2 : 4;
+    // q and out: (B, H, T) rows with three strides each
+    long long st[2][3];
+    for (int i = 0; i < 2; ++i) {
+        st[i][0] = B == 1 ? 0 : strides ? strides[3 * i] : static_cast<long long>(H) * T * D;
+        st[i][1] = H == 1 ? 0 : strides ? strides[3 * i + 1] : static_cast<long long>(T) * D;
+        st[i][2] = T == 1 ? 0 : strides ? strides[3 * i + 2] : D;
+        if (st[i][0] < 0 || st[i][1] < 0 || st[i][2] < 0)
+            return fail(ATTN_EINVAL, "%s: strides must not be negative", who);
+        if (st[i][0] * esz % 16 || st[i][1] * esz % 16 || st[i][2] * esz % 16)
+            return fail(ATTN_EINVAL, "%s: strides must be multiples of 16 bytes", who);
+    }
+    // rows of out must be distinct: sorted by stride, each one clears the extent of the smaller ones
+    {
+        long long s[3] = {st[1][0], st[1][1], st[1][2]}, n[3] = {B, H, T}, extent = D;
+        for (int x = 0; x < 3; ++x)
+            for (int y = x + 1; y < 3; ++y)
+                if (s[y] < s[x]) {
+                    const long long a = s[x], c = n[x];
+                    s[x] = s[y], n[x] = n[y], s[y] = a, n[y] = c;
+                }
+        for (int x = 0; x < 3; ++x) {
+            if (n[x] == 1) continue;
+            if (s[x] < extent) return fail(ATTN_EINVAL, "%s: the rows of out overlap", who);
+            extent += (n[x] - 1) * s[x];
+        }
+    }
+    const size_t q_bytes = static_cast<size_t>(((B - 1) * st[0][0] + (H - 1) * st[0][1] + (T - 1) * st[0][2] + D) * esz);
+    const size_t o_bytes = static_cast<size_t>(((B - 1) * st[1][0] + (H - 1) * st[1][1] + (T - 1) * st[1][2] + D) * esz);
+    const long long bh_kv = static_cast<long long>(B) * H_kv;
+    const size_t kv_bytes = static_cast<size_t>(bh_kv) * Skv * D * esz;
+    if (overlaps(out, o_bytes, q, q_bytes) || overlaps(out, o_bytes, kcache, kv_bytes) ||
+        overlaps(out, o_bytes, vcache, kv_bytes))
+        return fail(ATTN_EINVAL, "%s: out overlaps an input", who);
+    const bool f32 = dtype == ATTN_F32;
+    const int chunk = Skv > 0 ? tree_chunk(B, H, H_kv, T, Skv, f32, num_sms()) : 64;
+    const int n_split = Skv > 0 ? (Skv + chunk - 1) / chunk : 1;
+    const long long rows = static_cast<long long>(B) * H * T;
+    const long long blocks = bh_kv * n_split * (((H / H_kv) * static_cast<long long>(T) + 31) / 32);
+    if (rows >= (1LL << 31) || blocks >= (1LL << 31) || bh_kv * Skv >= (1LL << 31))
+        return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    const long long need = n_split == 1 ? 0 : rows * n_split * (D + 2) * 4;
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need || !aligned16(workspace))
+            return fail(ATTN_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes (got %lld)", who, need,
+                        workspace ? workspace_bytes : 0LL);
+        const size_t nb = static_cast<size_t>(need);
+        if (overlaps(workspace, nb, q, q_bytes) || overlaps(workspace, nb, out, o_bytes) ||
+            overlaps(workspace, nb, kcache, kv_bytes) || overlaps(workspace, nb, vcache, kv_bytes))
+            return fail(ATTN_EINVAL, "%s: workspace overlaps a tensor", who);
+    }
+    int *status = nullptr;
+    int rc = status_word(&status);
+    if (rc) return rc;
+    TreeArgs a{};
+    a.q = q, a.k = kcache, a.v = vcache, a.out = out;
+    a.parents = parents, a.cache_len = cache_len, a.draft_len = draft_len, a.parents_bs = parents_stride;
+    a.q_bs = st[0][0], a.q_hs = st[0][1], a.q_ts = st[0][2], a.o_bs = st[1][0], a.o_hs = st[1][1], a.o_ts = st[1][2];
+    a.B = B, a.H = H, a.H_kv = H_kv, a.T = T, a.Skv = Skv, a.D = D, a.scale = scale;
+    a.chunk = chunk, a.n_split = n_split;
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = a.part_o ? a.part_o + rows * n_split * D : nullptr;
+    a.status = status, a.stream = static_cast<cudaStream_t>(stream), a.n_sm = num_sms();
+    cudaError_t e;
+    if (f32) {
+        e = launch_tree_f32(a);
+    } else {
+        CUtensorMap tk{}, tv{};
+        if (Skv > 0 && ((rc = make_map(&tk, kcache, D, Skv, bh_kv, 64)) || (rc = make_map(&tv, vcache, D, Skv, bh_kv, 64))))
+            return rc;
+        e = launch_tree_tc(a, tk, tv);
+    }
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_decode_tree launch");
 }
 
 // Shared by attn_rope (no cache) and attn_rope_append.

@@ -46,6 +46,59 @@ struct FwdArgs {
     float *lse;             // (B, H, Sq) natural-log log-sum-exp of each row, or nullptr
 };
 
+// Packed sequences (attn_fwd_packed): FwdArgs with B = number of sequences and
+// Sq = Skv = T rows of all sequences together; kv_len is nullptr.
+struct PackedArgs : FwdArgs {
+    const int32_t *cu_seqlens;  // device int32[B + 1]
+    const int4 *plan;           // device: PackedPlan header, then its tile list
+    long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;  // element strides of a token, of a head
+};
+
+// What the plan kernel of a bf16 packed call writes to the caller's workspace:
+// one header entry and one int4 {first token, length, tile, -} per query-tile
+// unit of any head, longest rows first.
+struct PackedPlan {
+    int n_tiles, group, front, n_items;
+};
+// Rows of a tile unit: query-tile pairs, or single tiles when heads are paired.
+inline int packed_unit_rows(int H, int H_kv) { return ((H / H_kv) & 1) == 0 ? 128 : 256; }
+inline long long packed_plan_tiles(long long T, long long n_seq, int unit_rows) { return T / unit_rows + n_seq; }
+
+// bf16 tcgen05 packed prefill: plan kernel, then the prefill kernel.  tq/tk/tv
+// view (D, T, heads) with 64 x 128 x 1 boxes; plan_tiles entries follow the header.
+cudaError_t launch_packed_tc(const PackedArgs &a, long long plan_tiles, const CUtensorMap &tq, const CUtensorMap &tk,
+                             const CUtensorMap &tv);
+// fp32 packed prefill on the CUDA cores (no workspace).
+cudaError_t launch_packed_f32(const PackedArgs &a);
+
+// A tree of T drafted tokens per sequence against a KV cache (attn_decode_tree).
+// Row r of key/value head g is query head g * G + r / T, token r % T.
+constexpr int kTreeMaxTokens = 128;
+struct TreeArgs {
+    const void *q;              // (B, H, T, D) rows, element strides below
+    const void *k, *v;          // (B, H_kv, Skv, D)
+    void *out;                  // (B, H, T, D) rows
+    const int32_t *parents;     // device int32, parents_bs apart per sequence (0: one tree for all)
+    const int32_t *cache_len;   // device int32[B] or nullptr (Skv)
+    const int32_t *draft_len;   // device int32[B] or nullptr (T)
+    long long parents_bs, q_bs, q_hs, q_ts, o_bs, o_hs, o_ts;
+    int B, H, H_kv, T, Skv, D;
+    float scale;
+    int chunk, n_split;         // keys per split; 1 split writes out, more write partials
+    float *part_o;              // [(b * H_kv + g) * G * T + r][split][D] unnormalised
+    float *part_ml;             // the same rows: running max (log2 units), sum
+    int *status;
+    cudaStream_t stream;
+    int n_sm;
+};
+// Keys per split for these sizes (bf16 or fp32 kernel).
+int tree_chunk(int B, int H, int H_kv, int T, int Skv, bool f32, int n_sm);
+// bf16 tcgen05 kernel; tk/tv view the caches as (D, Skv, B * H_kv) with 64 x 64 x 1 boxes.
+cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv);
+cudaError_t launch_tree_f32(const TreeArgs &a);
+// Merges the splits' partials into out (either type).
+cudaError_t launch_tree_combine(const TreeArgs &a, bool f32);
+
 struct DecodeArgs {
     const void *q;          // (B, H, D) bf16 (fp32 for launch_decode_f32)
     const void *k, *v;      // (B, H_kv, Skv, D), same dtype

@@ -42,6 +42,7 @@ struct Item {
     int off;            // causal: key j visible from query row i iff j <= i + off
     int n_kv[kQTiles];  // K/V tiles each query tile needs (0: tile empty or fully padded)
     int N;              // max of n_kv
+    int start;          // packed sequences: first token of the sequence (row_base counts from it)
 };
 
 __device__ __forceinline__ bool pairs_heads(const FwdArgs &a) { return ((a.H / a.H_kv) & 1) == 0; }
@@ -178,6 +179,49 @@ inline bool plan_items(const FwdArgs &a, long long units, ItemPlan *plan, bool *
     plan->front = static_cast<int>(front);
     plan->n_items = static_cast<int>(n_items);
     return true;
+}
+
+// Packed sequences: work item t of the plan.  The list holds the tile units of
+// one head unit, longest first; head units are the minor index, in the same
+// blocks as decode_item's.
+__device__ __forceinline__ Item decode_item(int t, const PackedArgs &a, const PackedPlan &plan) {
+    Item it;
+    const int G = a.H / a.H_kv;
+    const bool hp = pairs_heads(a);
+    const int M = hp ? a.H / 2 : a.H;
+    int base = plan.front, cg = M - plan.front;
+    if (t < plan.front * plan.n_tiles) {
+        base = (t / (plan.group * plan.n_tiles)) * plan.group;
+        cg = plan.group;
+    }
+    const int tt = t - base * plan.n_tiles;
+    const int4 e = a.plan[1 + tt / cg];
+    const int u = base + tt % cg;
+    it.start = e.x;
+    it.Lb = e.y;
+    it.off = 0;
+    it.bh_base = hp ? 2 * u : u;
+    it.bh_step = hp ? 1 : 0;
+    it.row_base = e.z * (hp ? kBM : kQTiles * kBM);
+    it.row_step = hp ? 0 : kBM;
+    it.bh_kv = it.bh_base / G;
+    it.N = 0;
+#pragma unroll
+    for (int x = 0; x < kQTiles; ++x) {
+        const int row0 = it.row_base + x * it.row_step;
+        int n = 0;
+        if (row0 < it.Lb) n = ((a.causal ? min(it.Lb, row0 + kBM) : it.Lb) + kBN - 1) / kBN;
+        it.n_kv[x] = n;
+        it.N = max(it.N, n);
+    }
+    return it;
+}
+
+// First K/V tile of a packed item that some row of it sees only a part of: the
+// causal diagonal, or the tile that runs past the end of the sequence.
+__device__ __forceinline__ int first_edge_tile(const Item &it, int causal) {
+    const int end = it.Lb / kBN;
+    return causal ? min(it.row_base / kBM, end) : end;
 }
 
 }  // namespace attn

@@ -43,12 +43,24 @@
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [256+D, 256+2D);
 // P_x aliases the first 64 columns of S_x.
 // KV tiles wholly above the causal diagonal or past kv_len are never loaded.
+//
+// Packed sequences (attn_fwd_packed) run the same kernel on token-major
+// (T, H, D) views: a plan kernel lists the query tiles of all sequences,
+// longest first, and an item's tiles start at its sequence's first token.  A
+// K/V tile may then run into the next sequence, whose keys the row limits
+// hide; its values are hidden by P = 0, which would not hold against an
+// infinity or a NaN (0 * inf).  So warps 2-3, idle otherwise, look over
+// every V tile that some row sees only a part of before its MMA (the edge
+// tiles: on the diagonal, or past the sequence's end): rows past the end become
+// zeros, and non-finite elements become zeros that the epilogue adds back, to the
+// rows that see them only.
 #include "kernels.h"
 #include "prefill_sched.cuh"
 #include "ptx.cuh"
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 namespace attn {
 namespace {
@@ -73,6 +85,8 @@ struct Layout {
     static constexpr int kStageOff = kRingOff + kStages * kTileBytes;
     static constexpr int kBarOff = kStageOff + 8 * kStageBytes;
     static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // + barriers + alignment slack
+    static constexpr int kGuardOff = kBarOff + 512;          // packed sequences only
+    static constexpr int kSmemBytesPacked = kGuardOff + 512 + 1024;
     // TMEM column of S_x (and of P_x, which aliases it) and of O_x
     static __device__ __forceinline__ uint32_t s_col(int x) { return static_cast<uint32_t>(x) * 128u; }
     static __device__ __forceinline__ uint32_t o_col(int x) { return 256u + static_cast<uint32_t>(x) * D; }
@@ -94,6 +108,25 @@ struct Bars {
     int abort;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// Edge-tile requests from the producer to the guard warps (packed sequences).
+// The producer files one after issuing the loads of an edge V tile; each holds
+// a K/V ring stage until the MMA has read the cleaned tile, so no more than
+// half the ring's stages are open at once and kGuardRing slots never wrap.
+constexpr int kGuardRing = 8;
+struct GuardReq {
+    int stage;   // K/V ring stage of the tile, -1: no more work
+    int parity;  // of that stage's kv_full
+    int rows;    // rows of the tile inside the sequence (may exceed kBN)
+    int item;    // item ring slot
+};
+struct Guard {
+    uint64_t full[kGuardRing];   // request filed
+    uint64_t clean[kGuardRing];  // tile ready for the MMA
+    GuardReq req[kGuardRing];
+    int spoiled[kItemRing];      // the item met a non-finite value in an edge tile
+};
+static_assert(sizeof(Guard) <= 512, "guard block");
 
 // Work counters, one slot per launch: [0] next item, [2] epoch of the launch
 // using the slot (0: free); [1] and [3] unused.  Every CTA's producer takes
@@ -130,6 +163,7 @@ __device__ __forceinline__ void publish_item(Bars &bars, int slot, const Item &i
     d.n_kv[0] = it.n_kv[0];
     d.n_kv[1] = it.n_kv[1];
     d.N = it.N;
+    d.start = it.start;
 }
 __device__ __forceinline__ Item read_item(Bars &bars, int k) {
     const volatile Item &sv = bars.item[k % kItemRing];
@@ -144,6 +178,7 @@ __device__ __forceinline__ Item read_item(Bars &bars, int k) {
     it.n_kv[0] = sv.n_kv[0];
     it.n_kv[1] = sv.n_kv[1];
     it.N = sv.N;
+    it.start = sv.start;
     return it;
 }
 // Wait (warp-wide) until the item in ring slot k % kItemRing is published and
@@ -159,18 +194,23 @@ __device__ __forceinline__ void release_item(Bars &bars, int k) {
     mbar_arrive(&bars.item_empty[k % kItemRing]);
 }
 
-template <int D>
+// Any bf16 of the pair w infinite or NaN (exponent bits all ones)?
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
+
+template <int D, typename Args>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_tc_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap tq,
+    prefill_tc_kernel(const Args a, const __grid_constant__ CUtensorMap tq,
                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const int n_major, const int group, const int front, const int n_items,
                       unsigned int *sched, const unsigned int epoch) {
     using L = Layout<D>;
+    constexpr bool kPacked = std::is_same<Args, PackedArgs>::value;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *ring = smem + L::kRingOff;
     Bars &bars = *reinterpret_cast<Bars *>(smem + L::kBarOff);
+    Guard &guard = *reinterpret_cast<Guard *>(smem + L::kGuardOff);  // inside the allocation when kPacked
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
@@ -198,6 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars.item_full[s], 1);
             mbar_init(&bars.item_empty[s], kItemReaders);
         }
+        if constexpr (kPacked) {
+            for (int s = 0; s < kGuardRing; ++s) {
+                mbar_init(&guard.full[s], 1);
+                mbar_init(&guard.clean[s], 64);
+            }
+        }
         mbar_init(&bars.mma_done, 1);
         bars.abort = 0;
         fence_mbar_init();
@@ -222,7 +268,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kRegsProducer>();
         if (lane == 0) {
             if (owner != 0u && owner != epoch) report_status(a.status, 0x12, kStatusSchedConflict);
-            const unsigned int last_draw = static_cast<unsigned int>(n_items) + gridDim.x - 1u;
+            int total = n_items;
+            PackedPlan plan{};
+            if constexpr (kPacked) {  // the plan kernel counted the items
+                const int4 h = a.plan[0];
+                plan = PackedPlan{h.x, h.y, h.z, h.w};
+                total = h.w;
+            }
+            int requests = 0;  // edge V tiles filed with the guard warps
+            const unsigned int last_draw = static_cast<unsigned int>(total) + gridDim.x - 1u;
             uint32_t q_uses[kQTiles] = {0, 0};  // Q_x loads issued so far
             int issued = 0;                     // K/V ring loads issued so far
             bool ok = true;
@@ -241,14 +295,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int t = static_cast<int>(drawn);
                 Item it;
-                if (t < n_items) {
-                    it = decode_item(t, a, n_major, group, front);
+                if (t < total) {
+                    if constexpr (kPacked)
+                        it = decode_item(t, a, plan);
+                    else
+                        it = decode_item(t, a, n_major, group, front);
                 } else {
-                    it = Item{0, 0, 0, 0, 0, 0, 0, {0, 0}, -1};
+                    it = Item{0, 0, 0, 0, 0, 0, 0, {0, 0}, -1, 0};
                 }
                 publish_item(bars, slot, it);
+                if constexpr (kPacked) *static_cast<volatile int *>(&guard.spoiled[slot]) = 0;
                 mbar_arrive(&bars.item_full[slot]);
                 if (it.N < 0) break;
+                int kv_row = 0, edge = 0x7fffffff;
+                if constexpr (kPacked) {
+                    kv_row = it.start;
+                    edge = first_edge_tile(it, a.causal);
+                }
                 // ---- loads in the order the MMA warp consumes them: Q_0, K_0,
                 // Q_1, V_0, K_1, V_1, ...  (Q_1 waits for the previous item's
                 // last S1 to free its buffer; K_0 need not wait for that).
@@ -261,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < L::kSub; ++c)
                         tma_load_3d(smem + x * L::kTileBytes + c * L::kBlockBytes, &tq, &bars.q_full[x], c * 64,
-                                    it.row_base + x * it.row_step, it.bh_base + x * it.bh_step);
+                                    kv_row + it.row_base + x * it.row_step, it.bh_base + x * it.bh_step);
                     ++q_uses[x];
                 };
                 // K_j (kv = 0) or V_j (kv = 1) into the next ring stage
@@ -275,7 +338,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < L::kSub; ++c)
                         tma_load_3d(ring + s * L::kTileBytes + c * L::kBlockBytes, kv ? &tv : &tk, &bars.kv_full[s],
-                                    c * 64, j * kBN, it.bh_kv);
+                                    c * 64, kv_row + j * kBN, it.bh_kv);
+                    if constexpr (kPacked) {
+                        if (kv && j >= edge) {
+                            volatile GuardReq &rq = guard.req[requests % kGuardRing];
+                            rq.stage = s;
+                            rq.parity = (issued / L::kStages) & 1;
+                            rq.rows = it.Lb - j * kBN;
+                            rq.item = slot;
+                            mbar_arrive(&guard.full[requests % kGuardRing]);
+                            ++requests;
+                        }
+                    }
                     ++issued;
                 };
                 load_q(0);
@@ -283,6 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load_kv(j, 0);
                     if (j == 0) load_q(1);
                     load_kv(j, 1);
+                }
+            }
+            if constexpr (kPacked) {
+                // a slot's earlier request, kGuardRing before, has long been answered
+                if (ok) {
+                    *static_cast<volatile int *>(&guard.req[requests % kGuardRing].stage) = -1;
+                    mbar_arrive(&guard.full[requests % kGuardRing]);
                 }
             }
             // never leave with copies still landing in shared memory
@@ -320,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             idesc_o, (acc || kk > 0) ? 1u : 0u);
         };
         int consumed = 0;  // K/V ring stages consumed so far
+        int cleaned = 0;   // edge V tiles taken from the guard warps (packed)
         uint32_t q_uses[kQTiles] = {0, 0}, pr[kQTiles] = {0, 0};
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -335,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int N = it.N;
             if (N < 0) break;
             if (N == 0) continue;
+            int edge = 0x7fffffff;
+            if constexpr (kPacked) edge = __shfl_sync(0xffffffffu, first_edge_tile(it, a.causal), 0);
             // S_x_0 per query tile as soon as Q_x and K_0 are in (Q_1 may land
             // after Q_0: the previous item's last S1 freed its buffer late)
             {
@@ -364,6 +448,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int vslot = consumed % L::kStages;
                 if (!(ok = mbar_wait_warp(&bars.kv_full[vslot], (consumed / L::kStages) & 1, &bars.abort))) break;
                 ++consumed;
+                if constexpr (kPacked) {
+                    if (j >= edge) {
+                        if (!(ok = mbar_wait_warp(&guard.clean[cleaned % kGuardRing], (cleaned / kGuardRing) & 1,
+                                                  &bars.abort)))
+                            break;
+                        ++cleaned;
+                    }
+                }
                 tc_fence_after();
                 if (j < it.n_kv[0]) {
                     if (!(ok = mbar_wait_warp(&bars.p_ready[0], pr[0], &bars.abort))) break;
@@ -408,7 +500,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int never = 0;
         mbar_wait_warp(&bars.mma_done, 0, &never);
     } else if (warp < 4) {
-        regs_dec<kRegsProducer>();  // warps 2-3: no role, registers go to the softmax warps
+        regs_dec<kRegsProducer>();  // warps 2-3: registers go to the softmax warps
+        if constexpr (kPacked) {
+            // ============================================================ guard of the edge V tiles
+            const int tid = (warp - 2) * 32 + lane;
+            for (int r = 0;; ++r) {
+                const int slot = r % kGuardRing;
+                if (!mbar_wait_warp<64>(&guard.full[slot], (r / kGuardRing) & 1, &bars.abort)) break;
+                const volatile GuardReq &rq = guard.req[slot];
+                const int stage = rq.stage, parity = rq.parity, rows = rq.rows, item = rq.item;
+                if (stage < 0) break;
+                if (!mbar_wait_warp(&bars.kv_full[stage], parity, &bars.abort)) break;
+                const uint32_t tile = smem_u32(ring + stage * L::kTileBytes);
+                bool bad = false;
+#pragma unroll 8
+                for (int c = tid; c < L::kTileBytes / 16; c += 64) {  // 8 chunks a row, 128 rows a block
+                    const uint4 v = ld_shared_v4(tile + c * 16);
+                    if ((c >> 3) % kBN >= rows) {
+                        st_shared_v4(tile + c * 16, 0u, 0u, 0u, 0u);
+                    } else {
+                        const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
+                        if (n0 | n1 | n2 | n3) {
+                            bad = true;
+                            st_shared_v4(tile + c * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
+                        }
+                    }
+                }
+                if (bad) *static_cast<volatile int *>(&guard.spoiled[item]) = 1;
+                fence_proxy_async_shared();
+                mbar_arrive(&guard.clean[slot]);
+            }
+        }
     } else {
         // ================================================================ softmax + epilogue
         regs_inc<kRegsSoftmax>();
@@ -579,18 +701,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0) ++o_uses;
             // the item again, from its ring slot (nothing of it stays live through the tile loop)
             const Item it = read_item(bars, k);
-            release_item(bars, k);
+            if constexpr (!kPacked) release_item(bars, k);
             const int row0 = it.row_base + x * it.row_step;
             const int i = row0 + r;
+            // a packed row always sees a key; with nothing but -inf or NaN scores it is a NaN, not a zero
             const bool zero_row =
-                !have_o || (a.kv_len && !a.chunked && a.Sq == a.Skv && i >= it.Lb) || !(l > 0.f);
+                !have_o || (!kPacked && ((a.kv_len && !a.chunked && a.Sq == a.Skv && i >= it.Lb) || !(l > 0.f)));
             const float inv = zero_row ? 0.f : 1.f / l;
+            const int n_rows = kPacked ? it.Lb : a.Sq;
+            const int head = it.bh_base + x * it.bh_step;
             // log(sum_j exp(scale * s_j)) = ln 2 * (m_run + log2 l): l is kept relative to
             // m_run whether or not the lazy rescale has moved it
-            if (a.lse && i < a.Sq)
-                a.lse[static_cast<size_t>(it.bh_base + x * it.bh_step) * a.Sq + i] =
+            if (a.lse && i < n_rows)
+                a.lse[kPacked ? static_cast<size_t>(it.start + i) * a.H + head : static_cast<size_t>(head) * a.Sq + i] =
                     zero_row ? -INFINITY : (m_run + log2f(l)) * 0.6931471805599453f;
-            __nv_bfloat16 *obh = static_cast<__nv_bfloat16 *>(a.out) + static_cast<size_t>(it.bh_base + x * it.bh_step) * a.Sq * D;
+            __nv_bfloat16 *obh = static_cast<__nv_bfloat16 *>(a.out);
+            size_t o_row = D;
+            bool spoiled = false;
+            if constexpr (kPacked) {
+                obh += static_cast<size_t>(it.start) * a.o_ts + static_cast<size_t>(head) * a.o_hs;
+                o_row = static_cast<size_t>(a.o_ts);
+                spoiled = *static_cast<volatile int *>(&guard.spoiled[k % kItemRing]) != 0 && i < n_rows && have_o;
+                release_item(bars, k);
+            } else {
+                obh += static_cast<size_t>(head) * a.Sq * D;
+            }
             const int wrow0 = row0 + quarter * 32;  // first row of this warp
 #pragma unroll
             for (int c = 0; c < L::kSub; ++c) {
@@ -603,6 +738,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait();
                     reg_fence32(o);
                     reg_fence32(o + 32);
+                }
+                if constexpr (kPacked) {
+                    if (spoiled) {  // add the non-finite values that this row does see
+                        const int lim = a.causal ? i + 1 : it.Lb;
+                        const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v) +
+                                                  static_cast<size_t>(it.bh_kv) * a.v_hs + c * 64;
+#pragma unroll 1
+                        for (int key = first_edge_tile(it, a.causal) * kBN; key < lim; ++key) {
+                            const uint32_t *vr = reinterpret_cast<const uint32_t *>(
+                                vp + static_cast<size_t>(it.start + key) * a.v_ts);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const uint32_t w = vr[e], nf = nonfinite2(w);
+                                if (nf & 0xffffu) o[2 * e] = f2u(u2f(o[2 * e]) + bf16lo_to_f32(w));
+                                if (nf & 0xffff0000u) o[2 * e + 1] = f2u(u2f(o[2 * e + 1]) + bf16hi_to_f32(w));
+                            }
+                        }
+                    }
                 }
                 __syncwarp();  // the previous pass has read the buffer back
 #pragma unroll
@@ -621,8 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int rr = 4 * s4 + (lane >> 3), ch = lane & 7;
                     const uint4 v = ld_shared_v4(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
                     const int row = wrow0 + rr;
-                    if (row < a.Sq)
-                        *reinterpret_cast<uint4 *>(obh + static_cast<size_t>(row) * D + c * 64 + ch * 8) = v;
+                    if (row < n_rows)
+                        *reinterpret_cast<uint4 *>(obh + static_cast<size_t>(row) * o_row + c * 64 + ch * 8) = v;
                 }
             }
         }
@@ -694,15 +847,147 @@ cudaError_t launch_t(const FwdArgs &a, const CUtensorMap &tq, const CUtensorMap 
     cudaError_t e = sched_slot(a.stream, &sched, &epoch);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(plan.n_items < sms ? plan.n_items : sms);
-    e = cudaFuncSetAttribute(prefill_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    e = cudaFuncSetAttribute(prefill_tc_kernel<D, FwdArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     // programmatic dependent launch: back to back with the previous kernel,
     // the launch and the prologue overlap its end (griddep_wait in the kernel)
-    return launch_pdl(prefill_tc_kernel<D>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, tq, tk, tv,
+    return launch_pdl(prefill_tc_kernel<D, FwdArgs>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, tq, tk, tv,
                       plan.n_major, plan.group, plan.front, plan.n_items, sched, epoch);
 }
 
+// ------------------------------------------------------------ packed sequences
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanLevels = 1024;
+
+// Exclusive sum over the block's kPlanThreads values, from the last thread down.
+__device__ __forceinline__ int sum_above(int v, int *warp_sum) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_down_sync(0xffffffffu, s, d);
+        if (lane + d < 32) s += y;
+    }
+    if (lane == 0) warp_sum[warp] = s;
+    __syncthreads();
+    int above = 0;
+    for (int w = warp + 1; w < kPlanThreads / 32; ++w) above += warp_sum[w];
+    __syncthreads();
+    return above + s - v;
+}
+
+// Lists the query-tile units of all sequences in descending order of their
+// index within the sequence (of their causal cost; units from kPlanLevels - 1
+// on share the first place): counting sort in one block, linear in the
+// number of sequences and of units.  The order within one index is that of the
+// atomics; it decides where an item runs, not what it computes.
+__global__ void __launch_bounds__(kPlanThreads)
+    packed_plan_kernel(const PackedArgs a, int4 *out, const int cap, const int unit_rows, const int heads, const int grid) {
+    __shared__ int level[kPlanLevels];  // tiles of each index, then the next list position
+    __shared__ int warp_sum[kPlanThreads / 32];
+    __shared__ unsigned long long steps;
+    __shared__ int longest, extra;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x;
+    auto sequence = [&](int s, int *start) {  // clamped into the tensor whatever cu_seqlens holds
+        const int c0 = min(max(a.cu_seqlens[s], 0), a.Sq), c1 = min(max(a.cu_seqlens[s + 1], c0), a.Sq);
+        *start = c0;
+        return c1 - c0;
+    };
+    level[tid] = 0;
+    if (tid == 0) {
+        steps = 0;
+        longest = 0;
+        extra = 0;
+    }
+    __syncthreads();
+    unsigned long long mine = 0;
+    int most = 0;
+    for (int s = tid; s < a.B; s += kPlanThreads) {
+        int start;
+        const int len = sequence(s, &start), n = (len + unit_rows - 1) / unit_rows;
+        // K/V steps of the sequence's units: their count rises by unit_rows / kBN a unit when causal
+        const int kv = (len + kBN - 1) / kBN, per = unit_rows / kBN;
+        mine += a.causal ? static_cast<unsigned long long>(per) * n * (n + 1) / 2 : static_cast<unsigned long long>(kv) * n;
+        most = max(most, kv);
+        if (n > 0) {
+            atomicAdd(&level[min(n, kPlanLevels) - 1], 1);  // units 0 .. n - 1
+            // units past the last index share it
+            if (n > kPlanLevels) atomicAdd(&extra, n - kPlanLevels);
+        }
+    }
+    atomicAdd(&steps, mine);
+    atomicMax(&longest, most);
+    __syncthreads();
+    // sequences whose last unit is at this index or above = units of this index
+    const int here = level[tid];
+    const int units = here + sum_above(here, warp_sum);
+    const int n_here = units + (tid == kPlanLevels - 1 ? extra : 0);
+    const int first = sum_above(n_here, warp_sum);
+    level[tid] = first;
+    __syncthreads();
+    const int warp = tid / 32, lane = tid % 32;
+    for (int s = warp; s < a.B; s += kPlanThreads / 32) {
+        int start;
+        const int len = sequence(s, &start), n = (len + unit_rows - 1) / unit_rows;
+        for (int u = lane; u < n; u += 32) {
+            const int at = atomicAdd(&level[min(u, kPlanLevels - 1)], 1);
+            if (at < cap) out[1 + at] = make_int4(start, len, u, 0);
+        }
+    }
+    if (tid == 0) {
+        const int total = min(first + n_here, cap);  // thread 0 holds the last places
+        // blocks of head units as plan_items makes them, on the sequences' lengths
+        const long long kv_head_bytes = 2LL * a.Sq * a.D * 2;
+        const long long per_kv = unit_rows == kBM ? (a.H / a.H_kv) / 2 : a.H / a.H_kv;
+        long long c_l2 = kL2GroupBytes * per_kv / (kv_head_bytes > 0 ? kv_head_bytes : 1);
+        c_l2 = c_l2 > 1 ? c_l2 : 1;
+        const long long unit_steps = static_cast<long long>(steps);
+        const long long c_tail = unit_steps > 0
+            ? (kTailFactorX10 * longest * grid + 10 * unit_steps - 1) / (10 * unit_steps) : heads;
+        long long group = heads, front = 0;
+        if (kL2GroupBytes > 0 && c_l2 < heads && c_tail < heads) {
+            const long long n_front = (heads - c_tail) / c_l2;
+            if (n_front > 0) {
+                group = c_l2;
+                front = n_front * c_l2;
+            }
+        }
+        out[0] = make_int4(total, static_cast<int>(group), static_cast<int>(front), total * heads);
+    }
+}
+
+template <int D>
+cudaError_t launch_packed_t(const PackedArgs &a, long long plan_tiles, const CUtensorMap &tq, const CUtensorMap &tk,
+                            const CUtensorMap &tv) {
+    using L = Layout<D>;
+    const long long sms = a.n_sm > 0 ? a.n_sm : 1;
+    const int unit_rows = packed_unit_rows(a.H, a.H_kv);
+    const int heads = unit_rows == kBM ? a.H / 2 : a.H;
+    const long long most = plan_tiles * heads;
+    if (most > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
+    unsigned int *sched = nullptr, epoch = 0;
+    cudaError_t e = sched_slot(a.stream, &sched, &epoch);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(prefill_tc_kernel<D, PackedArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L::kSmemBytesPacked);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a, const_cast<int4 *>(a.plan),
+                   static_cast<int>(plan_tiles), unit_rows, heads, static_cast<int>(grid));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(prefill_tc_kernel<D, PackedArgs>, dim3(grid), dim3(kThreads), L::kSmemBytesPacked, a.stream, a,
+                      tq, tk, tv, 0, 0, 0, 0, sched, epoch);
+}
+
 }  // namespace
+
+cudaError_t launch_packed_tc(const PackedArgs &a, long long plan_tiles, const CUtensorMap &tq, const CUtensorMap &tk,
+                             const CUtensorMap &tv) {
+    return a.D == 64 ? launch_packed_t<64>(a, plan_tiles, tq, tk, tv) : launch_packed_t<128>(a, plan_tiles, tq, tk, tv);
+}
 
 cudaError_t reset_prefill_counters() {
     void *p = nullptr;

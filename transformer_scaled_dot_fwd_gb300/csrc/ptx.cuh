@@ -105,6 +105,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity,
     }
 }
 
+// Makes this thread's earlier shared-memory writes visible to the asynchronous
+// proxy (TMA, tcgen05 operands read through descriptors).
+__device__ __forceinline__ void fence_proxy_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialization waits here until the previous kernel in the stream has
 // finished and its writes are visible (a no-op when launched without it).

@@ -22,6 +22,7 @@
 // depth do not allow 16-byte accesses take the same code with VEC = 1.
 #include "kernels.h"
 #include "ptx.cuh"
+#include "serving.cuh"
 
 namespace attn {
 namespace {
@@ -38,22 +39,6 @@ template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Vec {
     T x[VEC];
 };
-
-// Number of the n nondecreasing values v[0..n) that are <= t, found by the
-// whole warp with 32 probes a step.  Any contents of v end the search.
-__device__ __forceinline__ int count_le(const int32_t *v, int n, int t, int lane) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + lane * step;
-        const unsigned le = __ballot_sync(0xffffffffu, at < hi && v[at] <= t);
-        const int c = le == 0xffffffffu ? 32 : __ffs(~le) - 1;  // leading probes that hold
-        if (c == 0) break;
-        hi = min(hi, lo + c * step);
-        lo = lo + (c - 1) * step + 1;
-    }
-    return lo;
-}
 
 struct Token {
     long long cache_row;  // (b * H_kv) * Skv + row of head 0's cache row, or -1: not cached

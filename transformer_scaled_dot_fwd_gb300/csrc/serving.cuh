@@ -1,0 +1,96 @@
+// Device helpers shared by the packed, rotary and tree kernels: the sequence of
+// a token, and what a drafted token sees of its tree.
+#pragma once
+
+#include "kernels.h"
+
+namespace attn {
+
+// Number of the n nondecreasing values v[0..n) that are <= t, found by the
+// whole warp with 32 probes a step.  Any contents of v end the search.
+__device__ __forceinline__ int count_le(const int32_t *v, int n, int t, int lane) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, at < hi && v[at] <= t);
+        const int c = le == 0xffffffffu ? 32 : __ffs(~le) - 1;  // leading probes that hold
+        if (c == 0) break;
+        hi = min(hi, lo + c * step);
+        lo = lo + (c - 1) * step + 1;
+    }
+    return lo;
+}
+
+// What the draft of one sequence looks like: L cache rows, the last n of them
+// drafted, so draft token j's key sits at row past + j (none when negative).
+struct Draft {
+    int L, n, past;
+};
+
+__device__ __forceinline__ Draft draft_of(const TreeArgs &a, int b) {
+    Draft d;
+    d.L = a.cache_len ? min(max(a.cache_len[b], 0), a.Skv) : a.Skv;
+    d.n = a.draft_len ? min(max(a.draft_len[b], 0), a.T) : a.T;
+    d.past = d.L - d.n;
+    return d;
+}
+
+// Bit sets of each drafted token's visible draft keys: itself and its
+// ancestors, as far as they have a cache row.  At least kTreeMaxTokens threads
+// call it together, `sync` joins them.  The parent relation is closed by
+// doubling: after round i a set holds the 2^i nearest ancestors.
+struct Ancestors {
+    uint32_t bits[kTreeMaxTokens][4];
+    int jump[kTreeMaxTokens];
+};
+
+template <typename Sync>
+__device__ __forceinline__ void build_ancestors(const TreeArgs &a, int b, const Draft &d, Ancestors &anc, int tid,
+                                                Sync sync) {
+    const int t = tid;
+    int jump = -1;
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (t < kTreeMaxTokens) {
+        if (t < d.n) {
+            const int p = a.parents[b * a.parents_bs + t];
+            jump = p >= 0 && p < t ? p : -1;
+            if (d.past + t >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = t / 32 == i ? 1u << (t % 32) : 0u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) anc.bits[t][i] = w[i];
+        anc.jump[t] = jump;
+    }
+    sync();
+    for (int reach = 1; reach < d.n; reach *= 2) {
+        int next = -1;
+        if (t < kTreeMaxTokens && jump >= 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] |= anc.bits[jump][i];
+            next = anc.jump[jump];
+        }
+        sync();
+        if (t < kTreeMaxTokens && jump >= 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) anc.bits[t][i] = w[i];
+            anc.jump[t] = jump = next;
+        }
+        sync();
+    }
+}
+
+// Visibility of draft-relative keys [s, s + 32) for a token with ancestor
+// words w: keys before 0 are the committed cache, keys from 128 on nothing.
+__device__ __forceinline__ uint32_t visible32(const uint32_t *w, int s) {
+    if (s <= -32) return 0xffffffffu;
+    if (s >= kTreeMaxTokens) return 0u;
+    if (s < 0) return ((1u << -s) - 1u) | (w[0] << -s);
+    const int i = s / 32, r = s % 32;
+    const uint32_t lo = w[i], hi = i < 3 ? w[i + 1] : 0u;
+    return __funnelshift_r(lo, hi, r);
+}
+
+}  // namespace attn
