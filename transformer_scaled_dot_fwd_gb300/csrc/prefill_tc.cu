@@ -71,6 +71,7 @@ constexpr uint32_t kRegsSoftmax = 216;   // warps 4-11: 128*64 + 256*216 <= 384*
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;  // lazy-rescale threshold (log2 units)
+constexpr float kHugeLog2 = 16777216.0f;  // 2^24: exponents this large have no fraction left
 constexpr int kItemRing = 4;          // work items in flight between the roles
 constexpr int kItemReaders = 32 + 256;  // MMA warp + both softmax warpgroups
 
@@ -636,7 +637,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float negm = m_run == -INFINITY ? 0.f : -m_run;
-                const uint64_t sl2x2 = f2_pack(sl2, sl2), negmx2 = f2_pack(negm, negm);
+                float mul = sl2;
+                if constexpr (kPacked) {
+                    // s * mul - m in one rounding leaves the rounding of m behind, 2^-24 of it: a
+                    // common factor of the row's weights, until it overflows them.  For huge
+                    // scores round the product first, so that the maximum's exponent is 0.
+                    if (__any_sync(0xffffffffu, negm < -kHugeLog2 || negm > kHugeLog2)) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) s[c] = f2u(__fmul_rn(u2f(s[c]), sl2));
+                        mul = 1.f;
+                    }
+                }
+                const uint64_t sl2x2 = f2_pack(mul, mul), negmx2 = f2_pack(negm, negm);
                 uint64_t l4[4] = {0, 0, 0, 0};  // packed partial row sums
                 // p = 2^(s*scale*log2e - m), packed into bf16 pairs over the S
                 // columns.  A hidden column holds -inf and 2^-inf is an exact

@@ -104,7 +104,7 @@ __device__ __forceinline__ void walk(F32Smem<D> &sm, const float *kbase, long lo
             float mt = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] *= sl2;
+                s[i][j] = __fmul_rn(s[i][j], sl2);  // rounded before the difference below: huge scores
                 if (see >> j & 1u) mt = fmaxf(mt, s[i][j]);
             }
 #pragma unroll

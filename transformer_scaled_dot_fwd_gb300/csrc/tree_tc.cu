@@ -44,6 +44,7 @@ constexpr int kCols = 256;       // TMEM: S buffers at columns 0 and 64, O at 12
 constexpr int kEdge = 4;         // tiles of 64 that 128 drafted keys at any offset can touch, and one to spare
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kHugeLog2 = 16777216.0f;  // 2^24
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
@@ -314,7 +315,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             const float negm = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: every p below is zero
-            const uint64_t sl2x2 = f2_pack(sl2, sl2), negmx2 = f2_pack(negm, negm);
+            float mul = sl2;
+            // huge scores: round the product before the difference (as in prefill_tc.cu)
+            if (__any_sync(0xffffffffu, negm < -kHugeLog2 || negm > kHugeLog2)) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) s[e] = f2u(__fmul_rn(u2f(s[e]), sl2));
+                mul = 1.f;
+            }
+            const uint64_t sl2x2 = f2_pack(mul, mul), negmx2 = f2_pack(negm, negm);
             uint64_t l4[4] = {0, 0, 0, 0};
             uint32_t p[kN / 2];
 #pragma unroll
