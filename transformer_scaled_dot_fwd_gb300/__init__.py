@@ -10,7 +10,6 @@ no CPU path: when the library is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -335,13 +334,85 @@ def attn_decode_splits(B: int, H: int, Skv: int, D: int) -> int:
     return lib().attn_decode_splits(B, H, Skv, D)
 
 
-def _alloc_scope(stream):
-    """Context in which allocations belong to the stream the call runs on, so
-    that the caching allocator orders their reuse with it."""
-    if stream is None:
-        return contextlib.nullcontext()
+# The serving entry points below are called once per layer and token, so their
+# checks read each tensor's attributes once.  A call for another device or stream
+# than the current one re-enters with that one current: outputs and
+# workspaces then belong to the stream the work runs on, and the caching
+# allocator orders their reuse with it.
+
+def _elsewhere(device, stream):
+    """Context to re-enter a call in, or None when device and stream are current."""
     torch = _torch()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    if stream is not None:
+        return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                 else torch.cuda.ExternalStream(int(stream), device=device))
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
+
+
+def _raw_stream(device):
+    """cudaStream_t of the device's current stream."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # spares building a Stream object
+    return get(device.index) if get is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _rows(name, t, T, D, dtype, device):
+    """(heads, token stride, head stride) of a (T, heads, D) tensor whose head rows
+    are contiguous."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or st[2] != 1 or shape[0] != T or shape[2] != D:
+        raise ValueError(f"{name} must be ({T}, heads, {D}) with contiguous rows of {D} elements (got {tuple(shape)})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must share q's dtype {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on q's device {device}")
+    return shape[1], st[0], st[1]
+
+
+def _first(q, ndim):
+    """(shape, strides, dtype code, device) of a call's q."""
+    shape, st = q.shape, q.stride()
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    if len(shape) != ndim or st[-1] != 1:
+        raise ValueError(f"q must be {ndim}-D with contiguous rows of D elements")
+    return shape, st, _dtype_code(q), q.device
+
+
+def _ints(name, t, shape, device):
+    """data_ptr of an optional int32 tensor."""
+    if t is None:
+        return None
+    if not (t.dtype == _torch().int32 and t.device == device and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on q's device")
+    return t.data_ptr()
+
+
+def _caches(kcache, vcache, dtype, device, D):
+    """(B, H_kv, Skv) of a pair of contiguous caches."""
+    shape = kcache.shape
+    if len(shape) != 4 or vcache.shape != shape or shape[3] != D:
+        raise ValueError(f"kcache and vcache must be (B, H_kv, Skv, {D})")
+    if kcache.dtype != dtype or vcache.dtype != dtype:
+        raise TypeError("q, kcache, vcache must share one dtype")
+    if kcache.device != device or vcache.device != device:
+        raise ValueError("the caches must be on q's device")
+    if not (kcache.is_contiguous() and vcache.is_contiguous()):
+        raise ValueError("kcache and vcache must be contiguous")
+    return shape[0], shape[1], shape[2]
+
+
+def _freqs_arg(freqs, D):
+    torch = _torch()
+    if not (isinstance(freqs, torch.Tensor) and freqs.dtype == torch.float64 and freqs.dim() == 1
+            and not freqs.is_cuda and freqs.is_contiguous()) or 2 * freqs.shape[0] > D:
+        raise ValueError("freqs must be a contiguous 1-D float64 CPU tensor of rotary_dim / 2 <= D / 2 values")
+    return freqs.data_ptr(), 2 * freqs.shape[0]
+
+
+_LL6, _LL8, _LL10 = (ctypes.c_longlong * n for n in (6, 8, 10))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -363,39 +434,41 @@ def attn_fwd_packed(q, k, v, cu_seqlens, out=None, lse=None, scale: Optional[flo
     ``return_lse`` (or an ``lse`` tensor) is given.  Rows outside every sequence
     are not written.  See include/attn.h.
     """
-    _check_rows("q", q)
-    _check_rows("k", k, q)
-    _check_rows("v", v, q)
-    T, H, D = q.shape
-    H_kv = k.shape[1]
-    if v.shape != k.shape or H_kv < 1 or H % H_kv:
+    (T, H, D), sq, code, device = _first(q, 3)
+    away = _elsewhere(device, stream)
+    if away is not None:
+        with away:
+            return attn_fwd_packed(q, k, v, cu_seqlens, out, lse, scale, causal, return_lse)
+    dtype = q.dtype
+    H_kv, kt, kh = _rows("k", k, T, D, dtype, device)
+    Hv, vt, vh = _rows("v", v, T, D, dtype, device)
+    if Hv != H_kv or H_kv < 1 or H % H_kv:
         raise ValueError("k and v must be (T, H_kv, D) matching q, with H_kv dividing H")
-    n_seq = cu_seqlens.shape[0] - 1 if cu_seqlens is not None and cu_seqlens.dim() == 1 else -1
-    if n_seq < 0:
+    if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be 1-D with at least one value")
-    cu = _ints_arg("cu_seqlens", cu_seqlens, n_seq + 1, q.device)
-    dtype = _dtype_code(q)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    n_seq = cu_seqlens.shape[0] - 1
+    cu = _ints("cu_seqlens", cu_seqlens, (n_seq + 1,), device)
     torch = _torch()
-    with _on_device(q.device), _alloc_scope(stream):
-        if out is None:
-            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-        _check_rows("out", out, q)
-        if out.shape != q.shape:
-            raise ValueError("out must match q's shape")
-        if lse is None and return_lse:
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-        if lse is not None and not (lse.dtype == torch.float32 and tuple(lse.shape) == (T, H) and lse.is_contiguous()
-                                    and lse.device == q.device):
-            raise ValueError("lse must be a contiguous float32 (T, H) tensor on q's device")
-        need = _packed_workspace(T, n_seq, H, H_kv, dtype)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-        rc = lib().attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), T, H, H_kv, D,
-                                   _strides(q, k, v, out), cu.data_ptr(), n_seq, float(scale), int(bool(causal)), dtype,
-                                   _ptr(ws), need, _stream_handle(stream))
-    _check(rc)
-    return (out, lse) if lse is not None else out
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dtype, device=device)
+    Ho, ot, oh = _rows("out", out, T, D, dtype, device)
+    if Ho != H:
+        raise ValueError("out must match q's shape")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((T, H), dtype=torch.float32, device=device)
+    elif not (lse.dtype == torch.float32 and lse.shape == (T, H) and lse.is_contiguous() and lse.device == device):
+        raise ValueError("lse must be a contiguous float32 (T, H) tensor on q's device")
+    need = _packed_workspace(T, n_seq, H, H_kv, code)
+    ws = torch.empty(need, dtype=torch.uint8, device=device).data_ptr() if need > 0 else None
+    rc = lib().attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), T, H, H_kv, D,
+                               _LL8(sq[0], sq[1], kt, kh, vt, vh, ot, oh), cu, n_seq,
+                               1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, code, ws, need,
+                               _raw_stream(device))
+    if rc:
+        _check(rc)
+    return out if lse is None else (out, lse)
 
 
 def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None, out=None,
@@ -408,87 +481,33 @@ def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None,
     committed cache, its ancestors and itself.  Returns ``out`` like q; rows
     without a token are zeros.  See include/attn.h.
     """
-    if not q.is_cuda or q.dim() != 4 or q.stride(3) != 1:
-        raise ValueError("q must be a CUDA (B, H, T, D) tensor with contiguous rows of D elements")
-    _check_tensor("kcache", kcache, 4)
-    _check_tensor("vcache", vcache, 4)
-    B, H, T, D = q.shape
-    H_kv, Skv = kcache.shape[1], kcache.shape[2]
-    if (tuple(kcache.shape) != (B, H_kv, Skv, D) or vcache.shape != kcache.shape or H_kv < 1 or H % H_kv):
+    (B, H, T, D), sq, code, device = _first(q, 4)
+    away = _elsewhere(device, stream)
+    if away is not None:
+        with away:
+            return attn_decode_tree(q, kcache, vcache, parents, cache_len, draft_len, out, scale)
+    Bc, H_kv, Skv = _caches(kcache, vcache, q.dtype, device, D)
+    if Bc != B or H_kv < 1 or H % H_kv:
         raise ValueError("kcache and vcache must be (B, H_kv, Skv, D) matching q, with H_kv dividing H")
-    if not (q.dtype == kcache.dtype == vcache.dtype):
-        raise TypeError("q, kcache, vcache must share one dtype")
-    if kcache.device != q.device or vcache.device != q.device:
-        raise ValueError("the caches must be on q's device")
+    one = parents.dim() == 1
+    par = _ints("parents", parents, (T,) if one else (B, T), device)
+    cl = _ints("cache_len", cache_len, (B,), device)
+    dl = _ints("draft_len", draft_len, (B,), device)
     torch = _torch()
-    if not (parents.is_cuda and parents.dtype == torch.int32 and parents.is_contiguous() and parents.device == q.device
-            and tuple(parents.shape) in ((T,), (B, T))):
-        raise ValueError("parents must be a contiguous int32 (B, T) or (T,) tensor on q's device")
-    cl = _kv_len_arg(cache_len, B, q.device)
-    dl = _kv_len_arg(draft_len, B, q.device)
-    dtype = _dtype_code(q)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _on_device(q.device), _alloc_scope(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if not out.is_cuda or out.device != q.device or out.shape != q.shape or out.dtype != q.dtype or out.stride(3) != 1:
-            raise ValueError("out must match q's shape, dtype and device, with contiguous rows")
-        need = _tree_workspace(B, H, H_kv, T, Skv, D, dtype, q.device.index) if B and T and T <= 128 else 0
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-        sq, so = q.stride(), out.stride()
-        rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), out.data_ptr(), B, H, H_kv, T,
-                                    Skv, D, (ctypes.c_longlong * 6)(sq[0], sq[1], sq[2], so[0], so[1], so[2]),
-                                    parents.data_ptr(), 0 if parents.dim() == 1 else T, _ptr(cl), _ptr(dl),
-                                    float(scale), dtype, _ptr(ws), max(need, 0), _stream_handle(stream))
-    _check(rc)
+    if out is None:
+        out = torch.empty_like(q)
+    so = out.stride()
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != device or so[3] != 1:
+        raise ValueError("out must match q's shape, dtype and device, with contiguous rows")
+    need = _tree_workspace(B, H, H_kv, T, Skv, D, code, device.index) if B and 0 < T <= 128 else 0
+    ws = torch.empty(need, dtype=torch.uint8, device=device).data_ptr() if need > 0 else None
+    rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), out.data_ptr(), B, H, H_kv, T,
+                                Skv, D, _LL6(sq[0], sq[1], sq[2], so[0], so[1], so[2]), par, 0 if one else T, cl, dl,
+                                1.0 / math.sqrt(D) if scale is None else scale, code, ws, need if need > 0 else 0,
+                                _raw_stream(device))
+    if rc:
+        _check(rc)
     return out
-
-
-def _check_rows(name, t, like=None):
-    """A (T, heads, D) CUDA tensor whose head rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{name} must be (T, heads, D) with contiguous rows of D elements")
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must share q's dtype")
-        if t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2] or t.device != like.device:
-            raise ValueError(f"{name} must match q's tokens, head depth and device")
-
-
-def _ints_arg(name, t, n, device):
-    torch = _torch()
-    if t is None:
-        return None
-    if not (t.is_cuda and t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()
-            and t.device == device):
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {n} values on q's device")
-    return t
-
-
-def _freqs_arg(freqs, D):
-    torch = _torch()
-    if not (isinstance(freqs, torch.Tensor) and freqs.dtype == torch.float64 and freqs.dim() == 1
-            and not freqs.is_cuda and freqs.is_contiguous()) or 2 * freqs.numel() > D:
-        raise ValueError("freqs must be a contiguous 1-D float64 CPU tensor of rotary_dim / 2 <= D / 2 values")
-    return freqs
-
-
-def _on_device(device):
-    """Context in which ``device`` is the current one (the library launches there)."""
-    torch = _torch()
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _strides(*tensors):
-    st = []
-    for t in tensors:
-        st += (t.stride(0), t.stride(1)) if t is not None else (0, 0)
-    return (ctypes.c_longlong * len(st))(*st)
 
 
 def attn_rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: Optional[str] = None,
@@ -534,33 +553,37 @@ def attn_rope(q, k, positions, freqs, q_out=None, k_out=None, interleaved: bool 
     attn_rope_frequencies.  ``inverse`` turns back, which is also the gradient.
     Rows may be strided (slices of a fused projection).  See include/attn.h.
     """
-    _check_rows("q", q)
-    if k is not None:
-        _check_rows("k", k, q)
-    T, H, D = q.shape
-    freqs = _freqs_arg(freqs, D)
-    pos = _ints_arg("positions", positions, T, q.device)
-    if pos is None:
+    (T, H, D), sq, code, device = _first(q, 3)
+    away = _elsewhere(device, stream)
+    if away is not None:
+        with away:
+            return attn_rope(q, k, positions, freqs, q_out, k_out, interleaved, inverse, mscale)
+    dtype = q.dtype
+    fr, rd = _freqs_arg(freqs, D)
+    pos = _ints("positions", positions, (T,), device)
+    if positions is None:
         raise ValueError("positions must be given")
     torch = _torch()
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    _check_rows("q_out", q_out, q)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
+        q_out = torch.empty((T, H, D), dtype=dtype, device=device)
+    Ho, ot, oh = _rows("q_out", q_out, T, D, dtype, device)
+    H_kv = kt = kh = kot = koh = Hko = 0
     if k is not None:
-        _check_rows("k_out", k_out, q)
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        H_kv, kt, kh = _rows("k", k, T, D, dtype, device)
+        if k_out is None:
+            k_out = torch.empty((T, H_kv, D), dtype=dtype, device=device)
+        Hko, kot, koh = _rows("k_out", k_out, T, D, dtype, device)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if Ho != H or Hko != H_kv:
         raise ValueError("q_out and k_out must have the shapes of q and k")
-    with _on_device(q.device):
-        rc = lib().attn_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), T, H,
-                             k.shape[1] if k is not None else 0, D, _strides(q, k, q_out, k_out), pos.data_ptr(),
-                             freqs.data_ptr(), 2 * freqs.numel(), int(bool(interleaved)), int(bool(inverse)),
-                             float(mscale), _dtype_code(q), _stream_handle(stream))
-    _check(rc)
-    return (q_out, k_out) if k is not None else q_out
+    rc = lib().attn_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                         None if k is None else k_out.data_ptr(), T, H, H_kv, D,
+                         _LL8(sq[0], sq[1], kt, kh, ot, oh, kot, koh), pos, fr, rd, 1 if interleaved else 0,
+                         1 if inverse else 0, mscale, code, _raw_stream(device))
+    if rc:
+        _check(rc)
+    return q_out if k is None else (q_out, k_out)
 
 
 def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=None, positions=None, q_out=None,
@@ -572,39 +595,35 @@ def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=
     ``positions`` is given.  Returns ``q_out``, or ``(q_out, k_out)`` when a
     ``k_out`` (T, H_kv, D) is given for the turned keys.  See include/attn.h.
     """
-    _check_rows("q", q)
-    _check_rows("k", k, q)
-    _check_rows("v", v, q)
-    _check_tensor("kcache", kcache, 4)
-    _check_tensor("vcache", vcache, 4)
-    T, H, D = q.shape
-    H_kv = k.shape[1]
-    B, Skv = kcache.shape[0], kcache.shape[2]
-    if v.shape != k.shape or tuple(kcache.shape) != (B, H_kv, Skv, D) or vcache.shape != kcache.shape:
+    (T, H, D), sq, code, device = _first(q, 3)
+    away = _elsewhere(device, stream)
+    if away is not None:
+        with away:
+            return attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens, cache_len, positions, q_out, k_out,
+                                    interleaved, mscale)
+    dtype = q.dtype
+    H_kv, kt, kh = _rows("k", k, T, D, dtype, device)
+    Hv, vt, vh = _rows("v", v, T, D, dtype, device)
+    B, Hc, Skv = _caches(kcache, vcache, dtype, device, D)
+    if Hv != H_kv or Hc != H_kv:
         raise ValueError("k and v must be (T, H_kv, D), kcache and vcache (B, H_kv, Skv, D)")
-    if not (q.dtype == kcache.dtype == vcache.dtype):
-        raise TypeError("q, k, v and the caches must share one dtype")
-    if kcache.device != q.device or vcache.device != q.device:
-        raise ValueError("the caches must be on q's device")
-    freqs = _freqs_arg(freqs, D)
-    cu = _ints_arg("cu_seqlens", cu_seqlens, B + 1, q.device)
-    cl = _kv_len_arg(cache_len, B, q.device)
-    pos = _ints_arg("positions", positions, T, q.device)
+    fr, rd = _freqs_arg(freqs, D)
+    cu = _ints("cu_seqlens", cu_seqlens, (B + 1,), device)
+    cl = _ints("cache_len", cache_len, (B,), device)
+    pos = _ints("positions", positions, (T,), device)
     if q_out is None:
-        q_out = _torch().empty((T, H, D), dtype=q.dtype, device=q.device)
-    _check_rows("q_out", q_out, q)
-    if k_out is not None:
-        _check_rows("k_out", k_out, q)
-    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
+        q_out = _torch().empty((T, H, D), dtype=dtype, device=device)
+    Ho, ot, oh = _rows("q_out", q_out, T, D, dtype, device)
+    Hko, kot, koh = (H_kv, 0, 0) if k_out is None else _rows("k_out", k_out, T, D, dtype, device)
+    if Ho != H or Hko != H_kv:
         raise ValueError("q_out and k_out must have the shapes of q and k")
-    with _on_device(q.device):
-        rc = lib().attn_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), _ptr(k_out),
-                                    kcache.data_ptr(), vcache.data_ptr(), T, H, H_kv, D,
-                                    _strides(q, k, v, q_out, k_out), B, Skv, _ptr(cu), _ptr(cl), _ptr(pos),
-                                    freqs.data_ptr(), 2 * freqs.numel(), int(bool(interleaved)), float(mscale),
-                                    _dtype_code(q), _stream_handle(stream))
-    _check(rc)
-    return (q_out, k_out) if k_out is not None else q_out
+    rc = lib().attn_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+                                None if k_out is None else k_out.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
+                                T, H, H_kv, D, _LL10(sq[0], sq[1], kt, kh, vt, vh, ot, oh, kot, koh), B, Skv, cu, cl,
+                                pos, fr, rd, 1 if interleaved else 0, mscale, code, _raw_stream(device))
+    if rc:
+        _check(rc)
+    return q_out if k_out is None else (q_out, k_out)
 
 
 def attn_device_status(stream=None) -> None:
