@@ -223,97 +223,209 @@ def test_packed_model_catches_planted_mistakes(mistake):
 
 # ----------------------------------------------------------------------------- tree
 
-def tree_run(n, edge, stages, seed, p_rescale, mistake=None):
-    """n tiles of 64 keys, those from `edge` on guarded."""
+def tree_run(runs, stages, seed, mistake=None):
+    """runs: (n tiles, first edge tile, one row tile?) per unit run of a CTA."""
     sc = Sched(seed)
-    q_full = Bar()
+    run_full, run_empty = [Bar() for _ in range(RING)], [Bar(3) for _ in range(RING)]
+    q_full = Bar(2)
     kv_full, kv_empty = [Bar() for _ in range(stages)], [Bar() for _ in range(stages)]
-    s_full, p_ready = [Bar(), Bar()], [Bar(), Bar()]
-    o_done, o_full = Bar(), Bar()
-    e_full, e_clean = [Bar() for _ in range(4)], [Bar(2) for _ in range(4)]
-    clean = set()
+    s_full, p_ready, o_full = [Bar(), Bar()], [Bar(), Bar()], [Bar(), Bar()]
+    g_full, g_clean = [Bar() for _ in range(GUARD_RING)], [Bar(2) for _ in range(GUARD_RING)]
+    join = Bar(2)
+    req, ring = [None] * GUARD_RING, [None] * RING
+    cleaned_uses = set()
+    q_owner = [None]           # run whose Q is staged
+    o_owner = [None, None]     # run whose values O_x accumulates
+    stream = list(runs) + [(-1, 0, False)]
 
     def producer():
-        for issued in range(2 * n):
-            j, kv, s = issued // 2, issued % 2, issued % stages
-            if issued >= stages:
-                yield wait(kv_empty[s], issued // stages - 1)
-            sc.tma.append(kv_full[s])
-            if kv and j >= edge:
-                e_full[j - edge].arrive()
+        issued, requests = 0, 0
+        for k, r in enumerate(stream):
+            if k >= RING:
+                yield wait(run_empty[k % RING], k // RING - 1)
+            ring[k % RING] = r
+            run_full[k % RING].arrive()
+            n, edge, one = r
+            if n < 0:
+                break
+            order = [(0, 0), (1, 0)] + [x for j in range(n) for x in ((j, 1), (j + 2, 0))] if one else [
+                x for j in range(n) for x in ((j, 0), (j, 1))]
+            for j, kv in order:
+                if j >= n:
+                    continue
+                s = issued % stages
+                if issued >= stages:
+                    yield wait(kv_empty[s], issued // stages - 1)
+                sc.tma.append(kv_full[s])
+                if kv and j >= edge:
+                    assert req[requests % GUARD_RING] is None, "request slot still open"
+                    req[requests % GUARD_RING] = (s, issued // stages, issued)
+                    g_full[requests % GUARD_RING].arrive()
+                    requests += 1
+                issued += 1
+        assert req[requests % GUARD_RING] is None, "request slot still open"
+        req[requests % GUARD_RING] = (-1, 0, 0)
+        g_full[requests % GUARD_RING].arrive()
 
     def guard(lane):
-        for j in range(edge, n):
-            u = 2 * j + 1
-            if mistake != "no_request":
-                yield wait(e_full[j - edge], 0)
-            yield wait_parity(kv_full[u % stages], u // stages)
-            assert kv_full[u % stages].phase == u // stages + 1, "guard is on another use of the stage"
-            if lane == 1:
-                clean.add(j)
-            e_clean[j - edge].arrive()
+        r = 0
+        while True:
+            yield wait(g_full[r % GUARD_RING], r // GUARD_RING)
+            s, phase, use = req[r % GUARD_RING]
+            if s < 0:
+                return
+            yield wait_parity(kv_full[s], phase)
+            assert kv_full[s].phase == phase + 1, "guard passes over a tile that is not the one requested"
+            cleaned_uses.add((lane, use))
+            if g_clean[r % GUARD_RING].pending == 1:
+                req[r % GUARD_RING] = None
+            g_clean[r % GUARD_RING].arrive()
+            r += 1
 
     def mma():
-        yield wait(q_full, 0)
+        st = dict(consumed=0, cleaned=0)
         pr = [0, 0]
-        for j in range(n + 1 if n else 0):
-            if j < n:
-                ks = (2 * j) % stages
-                yield wait(kv_full[ks], (2 * j) // stages)
-                sc.commit.append(s_full[j & 1])
+
+        def stage():
+            s, use = st["consumed"] % stages, st["consumed"]
+            yield wait(kv_full[s], use // stages)
+            st["consumed"] += 1
+            st["slot"], st["use"] = s, use
+
+        def v_tile(j, edge):
+            yield from stage()
+            if j >= edge:
+                if mistake != "mma_skips_guard":
+                    yield wait(g_clean[st["cleaned"] % GUARD_RING], st["cleaned"] // GUARD_RING)
+                st["cleaned"] += 1
+                assert {(0, st["use"]), (1, st["use"])} <= cleaned_uses, "edge tile read before it was clean"
+            return st["slot"]
+
+        def scores(x, k):
+            assert q_owner[0] == k, "Q of another run"
+            sc.commit.append(s_full[x])
+
+        def mix(x, k):
+            assert o_owner[x] in (None, k), "O still belongs to another run"
+            o_owner[x] = k
+
+        for k in range(len(stream)):
+            yield wait(run_full[k % RING], k // RING)
+            n, edge, one = ring[k % RING]
+            run_empty[k % RING].arrive()
+            if n < 0:
+                return
+            yield wait(q_full, k)
+            if one:
+                for x in range(min(2, n)):
+                    yield from stage()
+                    scores(x, k)
+                    sc.commit.append(kv_empty[st["slot"]])
+                for j in range(n):
+                    x = j & 1
+                    vs = yield from v_tile(j, edge)
+                    yield wait(p_ready[x], pr[x])
+                    pr[x] += 1
+                    mix(x, k)
+                    if j + 2 >= n:
+                        sc.commit.append(o_full[x])
+                    sc.commit.append(kv_empty[vs])
+                    if j + 2 < n:
+                        yield from stage()
+                        scores(x, k)
+                        sc.commit.append(kv_empty[st["slot"]])
+            else:
+                yield from stage()
+                ks = st["slot"]
+                scores(0, k)
+                scores(1, k)
                 sc.commit.append(kv_empty[ks])
-            if j >= 1:
-                t = j - 1
-                x, vs = t & 1, (2 * t + 1) % stages
-                yield wait(kv_full[vs], (2 * t + 1) // stages)
-                if t >= edge:
-                    if mistake != "mma_skips_guard":
-                        yield wait(e_clean[t - edge], 0)
-                    assert t in clean, "edge tile read before it was clean"
-                yield wait(p_ready[x], pr[x])
-                pr[x] += 1
-                sc.commit.append(o_done)
-                sc.commit.append(kv_empty[vs])
-                if t == n - 1:
-                    sc.commit.append(o_full)
+                for j in range(n):
+                    vs = yield from v_tile(j, edge)
+                    yield wait(p_ready[0], pr[0])
+                    pr[0] += 1
+                    mix(0, k)
+                    if j + 1 == n:
+                        sc.commit.append(o_full[0])
+                    else:
+                        yield from stage()
+                        ks = st["slot"]
+                        scores(0, k)
+                    yield wait(p_ready[1], pr[1])
+                    pr[1] += 1
+                    mix(1, k)
+                    if j + 1 == n:
+                        sc.commit.append(o_full[1])
+                    sc.commit.append(kv_empty[vs])
+                    if j + 1 < n:
+                        scores(1, k)
+                        sc.commit.append(kv_empty[ks])
 
-    def softmax():
-        rnd = random.Random(seed + 1)
-        q_full.arrive()
-        sp = [0, 0]
-        for j in range(n):
-            x = j & 1
-            yield wait(s_full[x], sp[x])
-            sp[x] += 1
-            if j > 0 and rnd.random() < p_rescale:
-                yield wait(o_done, j - 1)
-            p_ready[x].arrive()
-        if n:
-            yield wait(o_full, 0)
+    staged = {}
 
-    return sc.run({"producer": producer(), "mma": mma(), "softmax": softmax(), "guard0": guard(0), "guard1": guard(1)})
+    def softmax(x):
+        sp, o_uses, joins = 0, [0, 0], 0
+        for k in range(len(stream)):
+            yield wait(run_full[k % RING], k // RING)
+            r = ring[k % RING]
+            n, edge, one = r
+            if n < 0:
+                return
+            staged[k] = staged.get(k, 0) + 1
+            q_owner[0] = k if staged[k] == 2 else None
+            q_full.arrive()
+            for _ in range((n - x + 1) // 2 if one else n):
+                yield wait(s_full[x], sp)
+                sp += 1
+                p_ready[x].arrive()
+            if one:
+                join.arrive()
+                yield wait(join, joins)
+                joins += 1
+            for y in range(2):
+                used = not one or y < n
+                if used and (one or y == x):
+                    yield wait(o_full[y], o_uses[y])
+                o_uses[y] += used
+            for y in range(2):
+                if (not one and y == x) or (one and y < n):
+                    assert o_owner[y] == k, "O overwritten before it was read"
+            assert ring[k % RING] is r, "run slot overwritten before it was released"
+            run_empty[k % RING].arrive()
+            if mistake != "no_join":
+                join.arrive()
+                yield wait(join, joins)
+                joins += 1
+            o_owner[x] = None
+
+    return sc.run({"producer": producer(), "mma": mma(), "softmax0": softmax(0), "softmax1": softmax(1),
+                   "guard0": guard(0), "guard1": guard(1)})
 
 
-def _tree_trials(mistake=None):
+def _tree_trials(stages, mistake=None, trials=200):
+    rnd = random.Random(stages + 17 * (mistake is not None))
     bad = []
-    for n in range(0, 20):
-        for edge in range(max(0, n - 4), n + 1):
-            for seed in range(5):
-                for p in (0.0, 0.4, 1.0):
-                    try:
-                        r = tree_run(n, edge, 4, seed * 31 + n, p, mistake)
-                    except (Hazard, AssertionError) as e:
-                        r = f"{type(e).__name__}: {e}"
-                    if r:
-                        bad.append((n, edge, seed, p, r))
+    for t in range(trials):
+        runs = []
+        for _ in range(rnd.randint(1, 10)):
+            n = rnd.choice((1, 1, 2, 3, rnd.randint(1, 12)))
+            runs.append((n, max(0, n - rnd.randint(0, 3)), stages == 5 or rnd.random() < 0.5))
+        for seed in range(2):
+            try:
+                r = tree_run(runs, stages, seed + 10 * t, mistake)
+            except (Hazard, AssertionError) as e:
+                r = f"{type(e).__name__}: {e}"
+            if r:
+                bad.append((t, seed, r, runs))
     return bad
 
 
-def test_tree_protocol():
-    bad = _tree_trials()
+@pytest.mark.parametrize("stages", [4, 5, 8])  # pairs and single row tiles at D = 128, both at D = 64
+def test_tree_protocol(stages):
+    bad = _tree_trials(stages)
     assert not bad, bad[:3]
 
 
-@pytest.mark.parametrize("mistake", ["mma_skips_guard", "no_request"])
+@pytest.mark.parametrize("mistake", ["mma_skips_guard", "no_join"])
 def test_tree_model_catches_planted_mistakes(mistake):
-    assert _tree_trials(mistake), f"the model missed '{mistake}'"
+    assert _tree_trials(4, mistake, trials=80), f"the model missed '{mistake}'"

@@ -768,9 +768,13 @@ ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int
         (dtype != ATTN_F32 && dtype != ATTN_BF16))
         return ATTN_EINVAL;
     if (T == 0 || Skv == 0) return 0;
-    const long long chunk = tree_chunk(B, H, H_kv, T, Skv, dtype == ATTN_F32, num_sms());
-    const long long n_split = (Skv + chunk - 1) / chunk;
-    return n_split == 1 ? 0 : static_cast<long long>(B) * H * T * n_split * (D + 2) * 4;
+    if (dtype == ATTN_F32) {
+        const long long chunk = tree_chunk_f32(B, H, H_kv, T, Skv, num_sms());
+        const long long n_split = (Skv + chunk - 1) / chunk;
+        return n_split == 1 ? 0 : static_cast<long long>(B) * H * T * n_split * (D + 2) * 4;
+    }
+    const long long grid = tree_tc_grid(B, H, H_kv, T, Skv, num_sms());
+    return grid * 32 + 2 * grid * tree_tc_slot_rows(H, H_kv, T) * (D + 2) * 4;
 }
 
 ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vcache, void *out, int B, int H, int H_kv,
@@ -833,13 +837,15 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
         overlaps(out, o_bytes, vcache, kv_bytes))
         return fail(ATTN_EINVAL, "%s: out overlaps an input", who);
     const bool f32 = dtype == ATTN_F32;
-    const int chunk = Skv > 0 ? tree_chunk(B, H, H_kv, T, Skv, f32, num_sms()) : 64;
-    const int n_split = Skv > 0 ? (Skv + chunk - 1) / chunk : 1;
     const long long rows = static_cast<long long>(B) * H * T;
-    const long long blocks = bh_kv * n_split * (((H / H_kv) * static_cast<long long>(T) + 31) / 32);
-    if (rows >= (1LL << 31) || blocks >= (1LL << 31) || bh_kv * Skv >= (1LL << 31))
+    if (rows >= (1LL << 31) || bh_kv * Skv >= (1LL << 31)) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    const int chunk = f32 && Skv > 0 ? tree_chunk_f32(B, H, H_kv, T, Skv, num_sms()) : 64;
+    const int n_split = !f32 ? tree_tc_grid(B, H, H_kv, T, Skv, num_sms()) : Skv > 0 ? (Skv + chunk - 1) / chunk : 1;
+    if (f32 && bh_kv * n_split * (((H / H_kv) * static_cast<long long>(T) + 31) / 32) >= (1LL << 31))
         return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
-    const long long need = n_split == 1 ? 0 : rows * n_split * (D + 2) * 4;
+    const long long need = attn_decode_tree_workspace(B, H, H_kv, T, Skv, D, dtype);
+    // rows of partial results
+    const long long parts = f32 ? rows * n_split : 2LL * n_split * tree_tc_slot_rows(H, H_kv, T);
     if (need > 0) {
         if (!workspace || workspace_bytes < need || !aligned16(workspace))
             return fail(ATTN_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes (got %lld)", who, need,
@@ -858,17 +864,20 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
     a.q_bs = st[0][0], a.q_hs = st[0][1], a.q_ts = st[0][2], a.o_bs = st[1][0], a.o_hs = st[1][1], a.o_ts = st[1][2];
     a.B = B, a.H = H, a.H_kv = H_kv, a.T = T, a.Skv = Skv, a.D = D, a.scale = scale;
     a.chunk = chunk, a.n_split = n_split;
-    a.part_o = static_cast<float *>(workspace);
-    a.part_ml = a.part_o ? a.part_o + rows * n_split * D : nullptr;
+    if (need > 0) {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = a.part_o + parts * D;
+        a.merge = reinterpret_cast<int *>(a.part_ml + parts * 2);
+    }
     a.status = status, a.stream = static_cast<cudaStream_t>(stream), a.n_sm = num_sms();
     cudaError_t e;
     if (f32) {
         e = launch_tree_f32(a);
     } else {
-        CUtensorMap tk{}, tv{};
-        if (Skv > 0 && ((rc = make_map(&tk, kcache, D, Skv, bh_kv, 64)) || (rc = make_map(&tv, vcache, D, Skv, bh_kv, 64))))
+        CUtensorMap tk, tv;
+        if (Skv > 0 && ((rc = make_map(&tk, kcache, D, Skv, bh_kv)) || (rc = make_map(&tv, vcache, D, Skv, bh_kv))))
             return rc;
-        e = launch_tree_tc(a, tk, tv);
+        e = Skv > 0 ? launch_tree_tc(a, tk, tv) : launch_tree_zero(a);
     }
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_decode_tree launch");
 }

@@ -84,20 +84,26 @@ struct TreeArgs {
     long long parents_bs, q_bs, q_hs, q_ts, o_bs, o_hs, o_ts;
     int B, H, H_kv, T, Skv, D;
     float scale;
-    int chunk, n_split;         // keys per split; 1 split writes out, more write partials
-    float *part_o;              // [(b * H_kv + g) * G * T + r][split][D] unnormalised
-    float *part_ml;             // the same rows: running max (log2 units), sum
+    int chunk, n_split;         // fp32: keys per split and splits; bf16: n_split CTAs
+    // Partial results: O unnormalised [D] and (running max in log2 units, sum) of
+    // fp32: row ((b * H_kv + g) * G * T + r) * n_split + split
+    // bf16: row slot * slot_rows + r, two slots per CTA (tree_tc.cu)
+    float *part_o, *part_ml;
+    int *merge;                 // bf16: 8 ints per CTA, the unit it shares with later CTAs
     int *status;
     cudaStream_t stream;
     int n_sm;
 };
-// Keys per split for these sizes (bf16 or fp32 kernel).
-int tree_chunk(int B, int H, int H_kv, int T, int Skv, bool f32, int n_sm);
-// bf16 tcgen05 kernel; tk/tv view the caches as (D, Skv, B * H_kv) with 64 x 64 x 1 boxes.
+// fp32: keys per split for these sizes.
+int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int n_sm);
+// bf16: CTAs for these sizes, and rows of a workspace slot.
+int tree_tc_grid(int B, int H, int H_kv, int T, int Skv, int n_sm);
+int tree_tc_slot_rows(int H, int H_kv, int T);
+// bf16 tcgen05 kernel and its merge; tk/tv view the caches as (D, Skv, B * H_kv) with 64 x 128 x 1 boxes.
 cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv);
+cudaError_t launch_tree_zero(const TreeArgs &a);  // bf16, Skv = 0
 cudaError_t launch_tree_f32(const TreeArgs &a);
-// Merges the splits' partials into out (either type).
-cudaError_t launch_tree_combine(const TreeArgs &a, bool f32);
+cudaError_t launch_tree_merge_f32(const TreeArgs &a);
 
 struct DecodeArgs {
     const void *q;          // (B, H, D) bf16 (fp32 for launch_decode_f32)

@@ -71,6 +71,7 @@ __device__ __forceinline__ void build_ancestors(const TreeArgs &a, int b, const 
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] |= anc.bits[jump][i];
             next = anc.jump[jump];
+            if (next >= jump) next = -1;  // never, unless a wait gave up: stay inside the set
         }
         sync();
         if (t < kTreeMaxTokens && jump >= 0) {

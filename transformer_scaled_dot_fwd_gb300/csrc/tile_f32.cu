@@ -333,7 +333,7 @@ cudaError_t launch_tree_f32_t(const TreeArgs &a) {
     const unsigned grid = static_cast<unsigned>(a.B * a.H_kv) * a.n_split * row_tiles;
     e = launch_pdl(tree_f32_kernel<D>, dim3(grid), dim3(kThreads), smem, a.stream, a, row_tiles);
     if (e != cudaSuccess || a.n_split == 1) return e;
-    return launch_tree_combine(a, true);
+    return launch_tree_merge_f32(a);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // Attention of a tree of drafted tokens over a KV cache on the sm_103a tensor
-// cores (attn_decode_tree, bf16), and the merge of its splits (either type).
+// cores (attn_decode_tree, bf16), and the merges of its partial results.
 //
 // Every sequence has T drafted tokens hanging under its committed cache.  Token
 // t sees the cache before the draft, itself and its ancestors:
@@ -8,27 +8,35 @@
 // of 128-row tiles (row r: head r / T, token r % T), so one read of the cache
 // serves G T rows; with up to 128 rows the pass over the cache is bound by HBM.
 //
-// One CTA per (sequence and cached head, split of the keys, row tile), two on
-// an SM.  Per tile of 64 keys, as in the grouped decode kernel:
-//     S = Q K_j^T  (M 128, N 64, K = D),   O += P V_j  (P from TMEM),
-// S double-buffered in TMEM so that the scores of the next tile are computed
-// under this tile's softmax.  Splits write their unnormalised O, running max and
-// sum in fp32; the merge is exact.  Row tiles of one split are neighbours in the
-// grid and read the same keys from L2.
+// Work split.  A unit is a cached head of a sequence with one or two of its row
+// tiles, its cost the number of its 128-key tiles.  One persistent CTA per SM
+// takes an equal run of the list of all units' tiles, whatever the lengths are:
+// no tail, and at most two units per CTA are shared with neighbours.  Those
+// leave their unnormalised O, running max and sum in fp32 in the CTA's slots of
+// the workspace, for a merge in the order of the keys; whole units are written
+// out directly.
+//
+// Two softmax warpgroups (streams) keep two S and two O accumulators in TMEM
+// busy.  A unit with two row tiles gives each stream one of them, and both read
+// the same K/V tiles.  A unit with one row tile gives the streams alternate K/V
+// tiles; they join their O, max and sum at the end of the unit's run.  Order:
+//     two tiles:  S0_0 S1_0 | PV0_j S0_{j+1} PV1_j S1_{j+1} | ...
+//     one tile:   S0_0 S1_1 | PV_j S_{j+2} (stream j & 1)   | ...
+// so that a stream always has the other's MMAs to hide behind.
 //
 // Masks.  Ancestor sets are 128-bit words per token, closed by doubling over the
-// parent links while the first tiles are on their way.  Tiles in front of the
-// draft carry no mask; the last ones (the edge tiles, at most four) take the
-// 64 bits of their keys out of the row's set.  A weight of zero does not hide an
-// infinite or NaN value from the second product (0 * inf), and rows past the
-// sequence's end hold whatever the cache was left with, so two guard warps pass
-// over the V of the edge tiles before their MMA: rows past the end become zeros,
-// non-finite elements of drafted rows become zeros which the epilogue adds back
-// to the rows that see them.
+// parent links.  Tiles in front of the draft carry no mask; the last ones (the
+// edge tiles, at most three) take the 128 bits of their keys out of the row's set.  A
+// weight of zero does not hide an infinite or NaN value from the second product
+// (0 * inf), and rows past the sequence's end hold whatever the cache was left
+// with, so two guard warps pass over the V of the edge tiles before their MMA:
+// rows past the end become zeros, non-finite elements of drafted rows become
+// zeros which the epilogue adds back to the rows that see them.
 //
-// Roles (8 warps): warp 0 TMA producer (K_j, V_j through a ring), warp 1 TMEM
-// allocation and MMA issue, warps 2-5 Q staging, ancestor sets, softmax and
-// epilogue (thread = row = TMEM lane), warps 6-7 guard.
+// Roles (12 warps): warp 0 walks the CTA's run and loads K_j, V_j through a ring
+// of 128-row TMA tiles, warp 1 allocates TMEM and issues the MMAs, warps 2-3
+// guard, warps 4-7 and 8-11 are the streams (Q staging, ancestor sets, softmax,
+// epilogue; thread = row = TMEM lane).
 #include "kernels.h"
 #include "ptx.cuh"
 #include "serving.cuh"
@@ -36,76 +44,111 @@
 namespace attn {
 namespace {
 
-constexpr int kN = 64;           // keys per K/V tile
+constexpr int kN = 128;          // keys per K/V tile
 constexpr int kM = 128;          // rows per tile
-constexpr int kThreads = 256;
-constexpr int kStages = 4;       // K/V ring: 97 KB of shared memory at D = 128, two CTAs an SM
-constexpr int kCols = 256;       // TMEM: S buffers at columns 0 and 64, O at 128
-constexpr int kEdge = 4;         // tiles of 64 that 128 drafted keys at any offset can touch, and one to spare
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsOther = 64;     // warps 0-3 after setmaxnreg
+constexpr uint32_t kRegsSoftmax = 216;  // warps 4-11: 128 * 64 + 256 * 216 <= 384 * 168
+constexpr int kTmemCols = 512;   // S0 0, S1 128, O0 256, O1 256 + D
+constexpr int kRing = 4;         // unit runs in flight between the roles
+constexpr int kRingReaders = 32 + 256;
+constexpr int kGuardRing = 8;    // edge-tile requests (see prefill_tc.cu); fewer are ever open
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kHugeLog2 = 16777216.0f;  // 2^24
+// Fewest K/V tiles a CTA takes: below it a run costs more to start and merge
+// than to compute.
+#ifndef ATTN_TREE_MIN_TILES
+#define ATTN_TREE_MIN_TILES 2
+#endif
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
 
-template <int D>
+// A run of K/V tiles [j0, j0 + n) of one unit.
+struct Run {
+    int b, bk;      // sequence, sequence and cached head
+    int tile;       // first row tile
+    int j0, n;      // n < 0: no more work
+    int slot;       // workspace slot, -1: the whole unit, written out
+    int L, nd, past;
+};
+
+struct GuardReq {
+    int stage, parity, rows, run;  // rows of the tile inside the sequence; run: ring slot
+};
+
+// Single: one row tile in all, its second Q buffer is one more K/V stage.
+template <int D, bool Single>
 struct Layout {
     static constexpr int kSub = D / 64;
-    static constexpr int kQBlock = kM * 128;
-    static constexpr int kKvBlock = kN * 128;
-    static constexpr int kKvBytes = kSub * kKvBlock;
-    static constexpr int kRingOff = kSub * kQBlock;
-    static constexpr int kAncOff = kRingOff + kStages * kKvBytes;
-    static constexpr int kBarOff = kAncOff + static_cast<int>(sizeof(Ancestors));
-    static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+    static constexpr int kBlock = 128 * 128;        // 128 rows x 128 bytes
+    static constexpr int kTile = kSub * kBlock;
+    static constexpr int kQTiles = Single ? 1 : 2;
+    static constexpr int kStages = D == 128 ? (Single ? 5 : 4) : 8;
+    static constexpr int kRingOff = kQTiles * kTile;
+    static constexpr int kAncOff = kRingOff + kStages * kTile;
+    static constexpr int kExOff = kAncOff + static_cast<int>(sizeof(Ancestors));
+    static constexpr int kBarOff = kExOff + 256 * 8;
+    static constexpr int kSmemBytes = kBarOff + 1024 + 1024;
 };
 
 struct Bars {
-    uint64_t q_full;            // Q staged by the softmax warps
-    uint64_t kv_full[kStages];
-    uint64_t kv_empty[kStages];
-    uint64_t s_full[2];
-    uint64_t p_ready[2];
-    uint64_t o_done;            // one phase per P V
-    uint64_t o_full;
-    uint64_t edge_full[kEdge];  // load of the edge tile's V issued
-    uint64_t edge_clean[kEdge];
+    uint64_t q_full;
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t s_full[2], p_ready[2], o_full[2];
+    uint64_t run_full[kRing], run_empty[kRing];
+    uint64_t guard_full[kGuardRing], guard_clean[kGuardRing];
+    uint64_t join;              // both streams (a barrier with a limit)
     uint64_t mma_done;
+    Run run[kRing];
+    GuardReq req[kGuardRing];
+    int spoiled[kRing];
     uint32_t tmem_base;
     int abort;
-    int spoiled;                // a non-finite value in an edge tile
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 1024, "barrier block");
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+// Every unit has at least one tile, so that the rows of empty sequences are
+// written (as zeros) like the others.
+__device__ __forceinline__ int tiles_of(const TreeArgs &a, int b) {
+    const int L = a.cache_len ? min(max(a.cache_len[b], 0), a.Skv) : a.Skv;
+    return max(1, (L + kN - 1) / kN);
+}
+
+__device__ __forceinline__ bool take_run(Bars &bars, int k, Run *r) {
+    if (!mbar_wait_warp(&bars.run_full[k % kRing], (k / kRing) & 1, &bars.abort)) return false;
+    const volatile Run &s = bars.run[k % kRing];
+    r->b = s.b, r->bk = s.bk, r->tile = s.tile, r->j0 = s.j0, r->n = s.n, r->slot = s.slot;
+    r->L = s.L, r->nd = s.nd, r->past = s.past;
+    return true;
+}
+
+// First edge tile of a run, relative to j0: a tile that some row sees only a
+// part of, or that runs past the end.
+__device__ __forceinline__ int edge_of(const Run &r) { return min(r.n, max(0, max(0, r.past) / kN - r.j0)); }
+
+template <int D, bool Single>
+__global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const TreeArgs a, const int row_tiles, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv) {
-    griddep_launch_dependents();
-    griddep_wait();
-    using L = Layout<D>;
-    const int m = blockIdx.x % row_tiles, c = (blockIdx.x / row_tiles) % a.n_split;
-    const int bk = blockIdx.x / row_tiles / a.n_split, b = bk / a.H_kv, g = bk % a.H_kv;
-    const int G = a.H / a.H_kv, rows = G * a.T, r0 = m * kM;
-    const Draft d = draft_of(a, b);
-    const int k0 = c * a.chunk;
-    const int nkeys = min(a.chunk, d.L - k0);  // <= 0: nothing here
-    if (nkeys <= 0 && a.n_split > 1) return;   // the merge never reads this split
-    const int n = nkeys > 0 ? (nkeys + kN - 1) / kN : 0;
-    // first tile that some row sees only a part of, or that runs past the end
-    const int edge = min(n, max(0, d.past - k0) / kN);
-
+    using L = Layout<D, Single>;
+    constexpr int kStages = L::kStages;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + L::kRingOff;
     Ancestors &anc = *reinterpret_cast<Ancestors *>(smem + L::kAncOff);
+    float2 *ex = reinterpret_cast<float2 *>(smem + L::kExOff);  // [stream][row] max, sum
     Bars &bars = *reinterpret_cast<Bars *>(smem + L::kBarOff);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int G = a.H / a.H_kv, rows = G * a.T;
+    const int pairs = (row_tiles + 1) / 2;
 
     if (threadIdx.x == 0) {
-        mbar_init(&bars.q_full, kM);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+        mbar_init(&bars.q_full, 256);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars.kv_full[s], 1);
             mbar_init(&bars.kv_empty[s], 1);
@@ -113,288 +156,531 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bars.s_full[x], 1);
             mbar_init(&bars.p_ready[x], kM);
+            mbar_init(&bars.o_full[x], 1);
         }
-        mbar_init(&bars.o_done, 1);
-        mbar_init(&bars.o_full, 1);
-        for (int x = 0; x < kEdge; ++x) {
-            mbar_init(&bars.edge_full[x], 1);
-            mbar_init(&bars.edge_clean[x], 64);
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&bars.run_full[s], 1);
+            mbar_init(&bars.run_empty[s], kRingReaders);
         }
+        for (int s = 0; s < kGuardRing; ++s) {
+            mbar_init(&bars.guard_full[s], 1);
+            mbar_init(&bars.guard_clean[s], 64);
+        }
+        mbar_init(&bars.join, 256);
         mbar_init(&bars.mma_done, 1);
         bars.abort = 0;
-        bars.spoiled = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(&bars.tmem_base, kCols);
+        tmem_alloc(&bars.tmem_base, kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem_base;
+    griddep_launch_dependents();
+    griddep_wait();
 
     if (warp == 0) {
-        // ================================================================ TMA producer
-        if (lane == 0) {
-            prefetch_tmap(&tk);
-            prefetch_tmap(&tv);
-            bool ok = true;
-            int issued = 0;
-            for (; issued < 2 * n && ok; ++issued) {
-                const int j = issued / 2, kv = issued % 2, s = issued % kStages;
-                if (issued >= kStages &&
-                    !(ok = mbar_wait(&bars.kv_empty[s], ((issued / kStages) - 1) & 1, &bars.abort)))
-                    break;
-                mbar_arrive_expect_tx(&bars.kv_full[s], L::kKvBytes);
+        // ================================================================ walk and TMA loads
+        regs_dec<kRegsOther>();
+        const int per = a.H_kv * pairs;  // units of a sequence
+        long long total = 0;             // tiles of all units
+        for (int b0 = lane; b0 < a.B; b0 += 32) total += tiles_of(a, b0);
 #pragma unroll
-                for (int cb = 0; cb < L::kSub; ++cb)
-                    tma_load_3d(ring + s * L::kKvBytes + cb * L::kKvBlock, kv ? &tv : &tk, &bars.kv_full[s], cb * 64,
-                                k0 + j * kN, bk);
-                if (kv && j >= edge) mbar_arrive(&bars.edge_full[j - edge]);
+        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        total *= per;
+        // CTA i of N takes tiles [total i / N, total (i + 1) / N)
+        const long long most = (total + ATTN_TREE_MIN_TILES - 1) / ATTN_TREE_MIN_TILES;
+        const int N = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+        const bool idle = static_cast<int>(blockIdx.x) >= N;
+        const long long lo = idle ? 0 : total * blockIdx.x / N, hi = idle ? 0 : total * (blockIdx.x + 1LL) / N;
+        // sequence that holds tile lo, and the first tile of that sequence's units
+        int b = 0;
+        long long base = 0;
+        for (int b0 = 0; !idle && b0 < a.B; b0 += 32) {
+            const long long t = b0 + lane < a.B ? static_cast<long long>(tiles_of(a, b0 + lane)) * per : 0;
+            long long sum = t;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += y;
             }
+            const unsigned past = __ballot_sync(0xffffffffu, base + sum > lo);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                b = b0 + f;
+                base += __shfl_sync(0xffffffffu, sum - t, f);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) {
+            int issued = 0, requests = 0, k = 0;
+            bool ok = true;
+            int4 rec = make_int4(-1, 0, 0, 0), rec2 = make_int4(0, 0, 0, 0);
+            long long pos = lo;
+            int nt = tiles_of(a, b);
+            int u = static_cast<int>((lo - base) / nt), j = static_cast<int>((lo - base) % nt);
+            while (ok) {
+                const int slot = k % kRing;
+                if (k >= kRing && !(ok = mbar_wait(&bars.run_empty[slot], ((k / kRing) - 1) & 1, &bars.abort))) break;
+                Run r{0, 0, 0, 0, -1, 0, 0, 0, 0};
+                if (pos < hi) {
+                    const Draft d = draft_of(a, b);
+                    r.b = b;
+                    r.bk = b * a.H_kv + u / pairs;
+                    r.tile = 2 * (u % pairs);
+                    r.j0 = j;
+                    r.n = static_cast<int>(min(static_cast<long long>(nt - j), hi - pos));
+                    r.slot = r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
+                    r.L = d.L, r.nd = d.n, r.past = d.past;
+                    if (j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w
+                        const long long last = pos + nt - 1;
+                        rec = make_int4(r.bk, r.tile, b, static_cast<int>(((last + 1) * N - 1) / total));
+                        rec2 = make_int4(d.n, d.past, 0, 0);
+                    }
+                }
+                volatile Run &w = bars.run[slot];
+                w.b = r.b, w.bk = r.bk, w.tile = r.tile, w.j0 = r.j0, w.n = r.n, w.slot = r.slot;
+                w.L = r.L, w.nd = r.nd, w.past = r.past;
+                *static_cast<volatile int *>(&bars.spoiled[slot]) = 0;
+                mbar_arrive(&bars.run_full[slot]);
+                if (r.n < 0) break;
+                const int edge = edge_of(r);
+                auto load = [&](int jj, int kv) {
+                    if (!ok || jj >= r.n) return;
+                    const int s = issued % kStages;
+                    if (issued >= kStages && !(ok = mbar_wait(&bars.kv_empty[s], ((issued / kStages) - 1) & 1, &bars.abort)))
+                        return;
+                    mbar_arrive_expect_tx(&bars.kv_full[s], L::kTile);
+#pragma unroll
+                    for (int c = 0; c < L::kSub; ++c)
+                        tma_load_3d(ring + s * L::kTile + c * L::kBlock, kv ? &tv : &tk, &bars.kv_full[s], c * 64,
+                                    (r.j0 + jj) * kN, r.bk);
+                    if (kv && jj >= edge) {
+                        volatile GuardReq &q = bars.req[requests % kGuardRing];
+                        q.stage = s, q.parity = (issued / kStages) & 1, q.rows = r.L - (r.j0 + jj) * kN, q.run = slot;
+                        mbar_arrive(&bars.guard_full[requests % kGuardRing]);
+                        ++requests;
+                    }
+                    ++issued;
+                };
+                if (Single || r.tile + 1 >= row_tiles) {  // one row tile: K0 K1 | V0 K2 | V1 K3 | ...
+                    load(0, 0);
+                    load(1, 0);
+                    for (int jj = 0; jj < r.n && ok; ++jj) {
+                        load(jj, 1);
+                        load(jj + 2, 0);
+                    }
+                } else {
+                    for (int jj = 0; jj < r.n && ok; ++jj) {
+                        load(jj, 0);
+                        load(jj, 1);
+                    }
+                }
+                pos += r.n;
+                ++k;
+                j = 0;
+                if (r.j0 + r.n == nt && ++u == per) {
+                    u = 0;
+                    if (++b < a.B) nt = tiles_of(a, b);
+                }
+            }
+            if (ok) {  // no more work for the guard
+                *static_cast<volatile int *>(&bars.req[requests % kGuardRing].stage) = -1;
+                mbar_arrive(&bars.guard_full[requests % kGuardRing]);
+            }
+            int4 *out = reinterpret_cast<int4 *>(a.merge) + 2 * blockIdx.x;
+            out[0] = rec;
+            out[1] = rec2;
             // never leave with copies still landing in shared memory
             volatile int never = 0;
-            for (int u = max(0, issued - kStages); u < issued; ++u)
-                mbar_wait(&bars.kv_full[u % kStages], (u / kStages) & 1, &never);
+            for (int x = max(0, issued - kStages); x < issued; ++x)
+                mbar_wait(&bars.kv_full[x % kStages], (x / kStages) & 1, &never);
         }
     } else if (warp == 1) {
         // ================================================================ MMA issuer
+        regs_dec<kRegsOther>();
         const uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0);
         const uint32_t idesc_o = idesc_bf16_f32(kM, D, 1);
-        const uint64_t dq = sdesc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t dq0 = sdesc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t dk0 = sdesc_sw128(smem_u32(ring), 16, 1024);
-        const uint64_t dv0 = sdesc_sw128(smem_u32(ring), L::kKvBlock, 1024);
-        auto issue_s = [&](int x, int slot) {
-            const uint64_t db = desc_add(dk0, (slot * L::kKvBytes) >> 4);
+        const uint64_t dv0 = sdesc_sw128(smem_u32(ring), L::kBlock, 1024);
+        auto issue_s = [&](int x, int qbuf, int slot) {  // S_x = Q_qbuf K^T
+            const uint64_t da = desc_add(dq0, (qbuf * L::kTile) >> 4), db = desc_add(dk0, (slot * L::kTile) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                mma_ss_warp(tmem + static_cast<uint32_t>(x) * kN,
-                            desc_add(dq, ((kk / 4) * L::kQBlock + (kk % 4) * 32) >> 4),
-                            desc_add(db, ((kk / 4) * L::kKvBlock + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk / 4) * L::kBlock + (kk % 4) * 32) >> 4;
+                mma_ss_warp(tmem + x * 128u, desc_add(da, off), desc_add(db, off), idesc_s, kk > 0);
+            }
         };
-        auto issue_pv = [&](int x, int slot, bool acc) {
-            const uint64_t db = desc_add(dv0, (slot * L::kKvBytes) >> 4);
+        auto issue_pv = [&](int x, int slot, bool acc) {  // O_x (+)= P_x V
+            const uint64_t db = desc_add(dv0, (slot * L::kTile) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kN / 16; ++kk)
-                mma_ts_warp(tmem + 128u, tmem + static_cast<uint32_t>(x) * kN + kk * 8,
+                mma_ts_warp(tmem + 256u + x * static_cast<uint32_t>(D), tmem + x * 128u + kk * 8,
                             desc_add(db, (kk * 16 * 128) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
         };
-        uint32_t pr0 = 0, pr1 = 0;
-        bool ok = mbar_wait_warp(&bars.q_full, 0, &bars.abort);
-        tc_fence_after();
-        // order: S_0 | S_1 PV_0 | S_2 PV_1 | ... | PV_{n-1}; S_j reuses the buffer whose P PV_{j-2} read
-        for (int j = 0; j <= n && ok && n > 0; ++j) {
-            if (j < n) {
-                const int ks = (2 * j) % kStages;
-                if (!(ok = mbar_wait_warp(&bars.kv_full[ks], ((2 * j) / kStages) & 1, &bars.abort))) break;
+        int consumed = 0, cleaned = 0;
+        uint32_t pr[2] = {0, 0}, qp = 0;
+        bool ok = true;
+        auto next_stage = [&](int *slot) {  // wait for the next ring stage
+            *slot = consumed % kStages;
+            if (!(ok = mbar_wait_warp(&bars.kv_full[*slot], (consumed / kStages) & 1, &bars.abort))) return;
+            ++consumed;
+        };
+        auto guarded = [&](bool edge) {
+            if (!edge) return;
+            if ((ok = mbar_wait_warp(&bars.guard_clean[cleaned % kGuardRing], (cleaned / kGuardRing) & 1, &bars.abort)))
+                ++cleaned;
+        };
+        for (int k = 0; ok; ++k) {
+            Run r;
+            if (!(ok = take_run(bars, k, &r))) break;
+            mbar_arrive(&bars.run_empty[k % kRing]);
+            const int n = __shfl_sync(0xffffffffu, r.n, 0);
+            if (n < 0) break;
+            const int edge = __shfl_sync(0xffffffffu, edge_of(r), 0);
+            const bool one = Single || __shfl_sync(0xffffffffu, r.tile, 0) + 1 >= row_tiles;
+            if (!(ok = mbar_wait_warp(&bars.q_full, qp, &bars.abort))) break;
+            qp ^= 1;
+            int ks = 0, vs = 0;
+            if (one) {
+                // stream x = tile & 1, both on Q buffer 0
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x >= n) break;
+                    next_stage(&ks);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(x, 0, ks);
+                    tc_commit_warp(&bars.s_full[x]);
+                    tc_commit_warp(&bars.kv_empty[ks]);
+                }
+                auto step = [&](int j, int x) {
+                    next_stage(&vs);
+                    if (ok) guarded(j >= edge);
+                    if (!ok || !(ok = mbar_wait_warp(&bars.p_ready[x], pr[x], &bars.abort))) return;
+                    pr[x] ^= 1;
+                    tc_fence_after();
+                    issue_pv(x, vs, j >= 2);
+                    if (j + 2 >= n) tc_commit_warp(&bars.o_full[x]);
+                    tc_commit_warp(&bars.kv_empty[vs]);
+                    if (j + 2 < n) {
+                        next_stage(&ks);
+                        if (!ok) return;
+                        tc_fence_after();
+                        issue_s(x, 0, ks);
+                        tc_commit_warp(&bars.s_full[x]);
+                        tc_commit_warp(&bars.kv_empty[ks]);
+                    }
+                };
+                for (int j = 0; j < n && ok; j += 2) {
+                    step(j, 0);
+                    if (ok && j + 1 < n) step(j + 1, 1);
+                }
+            } else {
+                next_stage(&ks);
+                if (!ok) break;
                 tc_fence_after();
-                issue_s(j & 1, ks);
-                tc_commit_warp(&bars.s_full[j & 1]);
+                issue_s(0, 0, ks);
+                tc_commit_warp(&bars.s_full[0]);
+                issue_s(1, L::kQTiles - 1, ks);
+                tc_commit_warp(&bars.s_full[1]);
                 tc_commit_warp(&bars.kv_empty[ks]);
-            }
-            if (j >= 1) {
-                const int t = j - 1, x = t & 1, vs = (2 * t + 1) % kStages;
-                if (!(ok = mbar_wait_warp(&bars.kv_full[vs], ((2 * t + 1) / kStages) & 1, &bars.abort))) break;
-                if (t >= edge && !(ok = mbar_wait_warp(&bars.edge_clean[t - edge], 0, &bars.abort))) break;
-                if (!(ok = mbar_wait_warp(&bars.p_ready[x], x ? pr1 : pr0, &bars.abort))) break;
-                if (x) pr1 ^= 1; else pr0 ^= 1;
-                tc_fence_after();
-                issue_pv(x, vs, t > 0);
-                tc_commit_warp(&bars.o_done);
-                tc_commit_warp(&bars.kv_empty[vs]);
-                if (t == n - 1) tc_commit_warp(&bars.o_full);
+                for (int j = 0; j < n && ok; ++j) {
+                    next_stage(&vs);
+                    if (ok) guarded(j >= edge);
+                    if (!ok || !(ok = mbar_wait_warp(&bars.p_ready[0], pr[0], &bars.abort))) break;
+                    pr[0] ^= 1;
+                    tc_fence_after();
+                    issue_pv(0, vs, j > 0);
+                    const bool next = j + 1 < n;
+                    if (!next) tc_commit_warp(&bars.o_full[0]);
+                    if (next) {
+                        next_stage(&ks);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(0, 0, ks);
+                        tc_commit_warp(&bars.s_full[0]);
+                    }
+                    if (!(ok = mbar_wait_warp(&bars.p_ready[1], pr[1], &bars.abort))) break;
+                    pr[1] ^= 1;
+                    tc_fence_after();
+                    issue_pv(1, vs, j > 0);
+                    if (!next) tc_commit_warp(&bars.o_full[1]);
+                    tc_commit_warp(&bars.kv_empty[vs]);
+                    if (next) {
+                        issue_s(1, L::kQTiles - 1, ks);
+                        tc_commit_warp(&bars.s_full[1]);
+                        tc_commit_warp(&bars.kv_empty[ks]);
+                    }
+                }
             }
         }
         // every MMA must have finished before TMEM is released
         tc_commit_warp(&bars.mma_done);
         volatile int never = 0;
         mbar_wait_warp(&bars.mma_done, 0, &never);
-    } else if (warp >= 6) {
+    } else if (warp < 4) {
         // ================================================================ guard of the edge V tiles
-        const int tid = threadIdx.x - 192;
-        for (int j = edge; j < n; ++j) {
-            const int u = 2 * j + 1, s = u % kStages;
-            // the request comes after this use's load was issued, and the stage is
-            // not reused before edge_clean: kv_full cannot be a phase off
-            if (!mbar_wait_warp<64>(&bars.edge_full[j - edge], 0, &bars.abort)) break;
-            if (!mbar_wait_warp(&bars.kv_full[s], (u / kStages) & 1, &bars.abort)) break;
-            const uint32_t tile = smem_u32(ring + s * L::kKvBytes);
-            const int end = d.L - k0 - j * kN;  // rows of the tile inside the sequence
+        regs_dec<kRegsOther>();
+        const int tid = threadIdx.x - 64;
+        for (int q = 0;; ++q) {
+            const int slot = q % kGuardRing;
+            // a request comes after its load was issued, and its stage is not reused
+            // before guard_clean: kv_full cannot be a phase off
+            if (!mbar_wait_warp<64>(&bars.guard_full[slot], (q / kGuardRing) & 1, &bars.abort)) break;
+            const volatile GuardReq &rq = bars.req[slot];
+            const int stage = rq.stage, parity = rq.parity, inside = rq.rows, run = rq.run;
+            if (stage < 0) break;
+            if (!mbar_wait_warp(&bars.kv_full[stage], parity, &bars.abort)) break;
+            const uint32_t tile = smem_u32(ring + stage * L::kTile);
             bool bad = false;
 #pragma unroll 8
-            for (int i = tid; i < L::kKvBytes / 16; i += 64) {  // 8 chunks a row, 64 rows a block
-                const uint4 v = ld_shared_v4(tile + i * 16);
-                if ((i >> 3) % kN >= end) {
-                    st_shared_v4(tile + i * 16, 0u, 0u, 0u, 0u);
+            for (int c = tid; c < L::kTile / 16; c += 64) {  // 8 chunks a row, 128 rows a block
+                const uint4 v = ld_shared_v4(tile + c * 16);
+                if ((c >> 3) % kN >= inside) {
+                    st_shared_v4(tile + c * 16, 0u, 0u, 0u, 0u);
                 } else {
                     const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
                     if (n0 | n1 | n2 | n3) {
                         bad = true;
-                        st_shared_v4(tile + i * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
+                        st_shared_v4(tile + c * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
                     }
                 }
             }
-            if (bad) *static_cast<volatile int *>(&bars.spoiled) = 1;
+            if (bad) *static_cast<volatile int *>(&bars.spoiled[run]) = 1;
             fence_proxy_async_shared();
-            mbar_arrive(&bars.edge_clean[j - edge]);
+            mbar_arrive(&bars.guard_clean[slot]);
         }
     } else {
-        // ================================================================ softmax + epilogue
-        const int quarter = warp % 4;       // TMEM lanes [32 * quarter, 32 * quarter + 32)
+        // ================================================================ softmax streams
+        regs_inc<kRegsSoftmax>();
+        const int x = (warp - 4) / 4;
+        const int quarter = warp % 4;  // TMEM lanes [32 * quarter, 32 * quarter + 32)
         const int row = quarter * 32 + lane;
-        const int tid = threadIdx.x - 64;   // 0 .. 127, for the staging loops
-        // Q rows, swizzled as a TMA load would leave them; rows without a token are zeros
-#pragma unroll 4
-        for (int i = tid; i < kM * D / 8; i += kM) {
-            const int rr = i / (D / 8), ch = i % (D / 8), r = r0 + rr;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows && r % a.T < d.n)
-                x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + b * a.q_bs +
-                                                     (g * G + r / a.T) * a.q_hs + (r % a.T) * a.q_ts + ch * 8);
-            st_shared_v4(smem_u32(smem) + (ch / 8) * L::kQBlock + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), x.x, x.y, x.z,
-                         x.w);
-        }
-        fence_proxy_async_shared();
-        mbar_arrive(&bars.q_full);
-        build_ancestors(a, b, d, anc, tid, [] { named_bar_sync(1, kM); });
-        const int r = r0 + row, t = r % a.T;
-        const bool live = r < rows && t < d.n && d.past + t >= 0;
-        const uint32_t *set = anc.bits[t];
+        const int tid = threadIdx.x - 128;  // 0 .. 255 over both streams
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t t_s = t_lane + x * 128u, t_o = t_lane + 256u + x * static_cast<uint32_t>(D);
         const float sl2 = a.scale * kLog2e;
-        float m_run = -INFINITY, l = 0.f;
+        uint32_t sp = 0, o_uses[2] = {0, 0};
+        int anc_of = -1;  // sequence whose ancestor sets are in shared memory
         bool ok = true;
-        for (int j = 0; j < n && ok; ++j) {
-            const int x = j & 1;
-            if (!(ok = mbar_wait_warp<32>(&bars.s_full[x], (j >> 1) & 1, &bars.abort))) break;
-            tc_fence_after();
-            uint32_t s[kN];
-            tmem_ld32(t_lane + x * kN, s);
-            tmem_ld32(t_lane + x * kN + 32, s + 32);
-            tmem_ld_wait();
-            reg_fence32(s);
-            reg_fence32(s + 32);
-            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            if (j >= edge) {
-                const int at = k0 + j * kN - d.past;
-                see[0] = live ? visible32(set, at) : 0u;
-                see[1] = live ? visible32(set, at + 32) : 0u;
-#pragma unroll
-                for (int e = 0; e < kN; ++e)
-                    if (!(see[e / 32] >> (e % 32) & 1u)) s[e] = f2u(-INFINITY);
-            }
-            float m4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(u2f(s[2 * e]), u2f(s[2 * e + 1]));
-#pragma unroll
-            for (int cc = 8; cc < kN; cc += 2) m4[(cc / 2) % 4] = fmax3(m4[(cc / 2) % 4], u2f(s[cc]), u2f(s[cc + 1]));
-            const float raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            const float m_new = fmaxf(m_run, raw == -INFINITY ? -INFINITY : raw * sl2);
-            const bool grow = m_new > m_run + kRescaleLog2;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float factor = grow ? ex2_approx(m_run - m_new) : 1.f;
-                if (grow) {
-                    l *= factor;
-                    m_run = m_new;
+        uint32_t joins = 0;
+        auto join = [&] {  // waits for all threads of both streams, or for the abort flag
+            mbar_arrive(&bars.join);
+            ok = mbar_wait_warp(&bars.join, joins & 1, &bars.abort) && ok;
+            ++joins;
+        };
+        for (int k = 0; ok; ++k) {
+            Run r;
+            if (!(ok = take_run(bars, k, &r))) break;
+            if (r.n < 0) break;
+            const bool one = Single || r.tile + 1 >= row_tiles;
+            const int edge = edge_of(r);
+            // Q rows, swizzled as a TMA load would leave them; rows without a token are
+            // zeros.  The last MMA that read the buffers is complete (end of the previous run).
+            {
+                const int n_chunk = (one ? 1 : 2) * kM * D / 8;
+                const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + r.b * a.q_bs;
+                const int h0 = (r.bk - r.b * a.H_kv) * G;
+#pragma unroll 4
+                for (int i = tid; i < n_chunk; i += 256) {
+                    const int rr = i / (D / 8), ch = i % (D / 8), q = r.tile * kM + rr;
+                    const int h = q / a.T, t = q - h * a.T;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (q < rows && t < r.nd) v = *reinterpret_cast<const uint4 *>(Q + (h0 + h) * a.q_hs + t * a.q_ts + ch * 8);
+                    const int rt = rr % kM;
+                    st_shared_v4(smem_u32(smem) + (rr / kM) * L::kTile + (ch / 8) * L::kBlock + rt * 128 +
+                                     (((ch & 7) ^ (rt & 7)) << 4), v.x, v.y, v.z, v.w);
                 }
-                if (j > 0) {
-                    // O holds PV_0 .. PV_{j-1}: wait for the last of them
-                    if (!(ok = mbar_wait_warp(&bars.o_done, (j - 1) & 1, &bars.abort))) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int cc = 0; cc < D / 32; ++cc) {
-                        uint32_t o[32];
-                        tmem_ld32(t_lane + 128 + cc * 32, o);
-                        tmem_ld_wait();
-                        reg_fence32(o);
+            }
+            fence_proxy_async_shared();
+            mbar_arrive(&bars.q_full);
+            if (edge < r.n && anc_of != r.b) {
+                build_ancestors(a, r.b, Draft{r.L, r.nd, r.past}, anc, tid, join);
+                anc_of = r.b;
+            }
+            const int q = (r.tile + (one ? 0 : x)) * kM + row;  // this thread's row of the unit
+            const int t = q % a.T;
+            const bool live = q < rows && t < r.nd && r.past + t >= 0;
+            const uint32_t *set = anc.bits[t];
+            const int n = one ? (r.n - x + 1) / 2 : r.n;  // tiles of this stream
+            float m_run = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i) {
+                const int j = one ? 2 * i + x : i;
+                if (!(ok = mbar_wait_warp<32>(&bars.s_full[x], sp, &bars.abort))) break;
+                sp ^= 1;
+                tc_fence_after();
+                uint32_t s[128];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = f2u(u2f(o[e]) * factor);
-                        tmem_st32(t_lane + 128 + cc * 32, o);
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) reg_fence32(s + c * 32);
+                const bool masked = j >= edge;
+                if (masked) {
+                    const int at = (r.j0 + j) * kN - r.past;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t see = live ? visible32(set, at + 32 * c) : 0u;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see >> e & 1u)) s[32 * c + e] = f2u(-INFINITY);
+                    }
+                }
+                float m8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m8[e] = fmaxf(u2f(s[2 * e]), u2f(s[2 * e + 1]));
+#pragma unroll
+                for (int c = 16; c < 128; c += 2) m8[(c / 2) % 8] = fmax3(m8[(c / 2) % 8], u2f(s[c]), u2f(s[c + 1]));
+                const float raw = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+                const float m_new = fmaxf(m_run, raw == -INFINITY ? -INFINITY : raw * sl2);
+                const bool grow = m_new > m_run + kRescaleLog2;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float factor = grow ? ex2_approx(m_run - m_new) : 1.f;
+                    if (grow) {
+                        l *= factor;
+                        m_run = m_new;
+                    }
+                    if (i > 0) {  // this stream's earlier P V are complete: S was issued after them
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + c * 32, o);
+                            tmem_ld_wait();
+                            reg_fence32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = f2u(u2f(o[e]) * factor);
+                            tmem_st32(t_o + c * 32, o);
+                        }
+                    }
+                }
+                const float negm = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: every p below is zero
+                float mul = sl2;
+                // huge scores: round the product before the difference (as in prefill_tc.cu); a
+                // scale of 0: a hidden key's -inf must not become NaN
+                if (__any_sync(0xffffffffu, negm < -kHugeLog2 || negm > kHugeLog2) || sl2 == 0.f) {
+                    const int at = (r.j0 + j) * kN - r.past;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t see = !masked ? 0xffffffffu : live ? visible32(set, at + 32 * c) : 0u;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            s[32 * c + e] = see >> e & 1u ? f2u(__fmul_rn(u2f(s[32 * c + e]), sl2)) : f2u(-INFINITY);
+                    }
+                    mul = 1.f;
+                }
+                const uint64_t mul2 = f2_pack(mul, mul), negm2 = f2_pack(negm, negm);
+                uint64_t l4[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int c = 64 * h + 2 * e;
+                        const uint64_t arg = ffma2(f2_pack(u2f(s[c]), u2f(s[c + 1])), mul2, negm2);
+                        const float p0 = ex2_approx(f2_lo(arg)), p1 = ex2_approx(f2_hi(arg));
+                        l4[e % 4] = fadd2(l4[e % 4], f2_pack(p0, p1));
+                        // P is rounded to bf16, the operand type of the second product: each
+                        // weight is off by at most 2^-8 of itself; the sum keeps fp32
+                        p[e] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32(t_s + h * 32, p);
+                }
+                const uint64_t l2 = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+                l += f2_lo(l2) + f2_hi(l2);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bars.p_ready[x]);
+            }
+            // ---- epilogue
+            const bool other = one && r.n > 1;  // the other stream has a part of the same rows
+            float w = 1.f, w_other = 0.f, m = m_run, sum = l;
+            if (one) {
+                ex[x * kM + row] = make_float2(m_run, l);
+                join();
+                const float2 y = ex[(x ^ 1) * kM + row];
+                m = fmaxf(m_run, y.x);
+                const float ref = m == -INFINITY ? 0.f : m;
+                w = ex2_approx(m_run - ref);
+                w_other = ex2_approx(y.x - ref);
+                sum = l * w + y.y * w_other;
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const bool used = one ? y < r.n : true;
+                if (used && (one || y == x) && ok) ok = mbar_wait_warp(&bars.o_full[y], o_uses[y] & 1, &bars.abort);
+                if (used) ++o_uses[y];
+            }
+            tc_fence_after();
+            const bool write = ok && q < rows;
+            const bool spoiled = *static_cast<volatile int *>(&bars.spoiled[k % kRing]) != 0 && live;
+            const float inv = 1.f / sum;
+            const size_t part = static_cast<size_t>(r.slot < 0 ? 0 : r.slot) * (L::kQTiles * kM) + (one ? 0 : x * kM) + row;
+            // a unit of one row tile: stream 0 writes the first half of the columns, stream 1 the second
+            const int c0 = one ? x * (D / 64) : 0, c1 = one ? c0 + D / 64 : D / 32;
+            const int h = (r.bk - r.b * a.H_kv) * G + q / a.T;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + r.b * a.o_bs + h * a.o_hs + t * a.o_ts;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                __syncwarp();
+                uint32_t o[32];  // TMEM of this CTA: loaded unconditionally, used only when valid
+                tmem_ld32((one ? t_lane + 256u : t_o) + c * 32, o);
+                tmem_ld_wait();
+                reg_fence32(o);
+                if (one) {
+                    const float wa = x ? w_other : w, wb = x ? w : w_other;  // of O0, of O1
+                    uint32_t o1[32];
+                    tmem_ld32(t_lane + 256u + D + c * 32, o1);
+                    tmem_ld_wait();
+                    reg_fence32(o1);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = f2u(other ? fmaf(wa, u2f(o[e]), wb * u2f(o1[e])) : wa * u2f(o[e]));
+                }
+                if (spoiled) {  // add the non-finite values of the edge tiles that this row sees
+                    const __nv_bfloat16 *V = static_cast<const __nv_bfloat16 *>(a.v) + static_cast<size_t>(r.bk) * a.Skv * D + c * 32;
+                    const int end = min(r.L, (r.j0 + r.n) * kN);
+#pragma unroll 1
+                    for (int key = (r.j0 + edge) * kN; key < end; ++key) {
+                        if (!(visible32(set, key - r.past) & 1u)) continue;
+                        const uint32_t *vr = reinterpret_cast<const uint32_t *>(V + static_cast<size_t>(key) * D);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint32_t v = vr[e], nf = nonfinite2(v);
+                            if (nf & 0xffffu) o[2 * e] = f2u(u2f(o[2 * e]) + bf16lo_to_f32(v));
+                            if (nf & 0xffff0000u) o[2 * e + 1] = f2u(u2f(o[2 * e + 1]) + bf16hi_to_f32(v));
+                        }
+                    }
+                }
+                if (write && r.slot >= 0) {
+                    float4 *dst = reinterpret_cast<float4 *>(a.part_o + part * D + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(u2f(o[4 * e]), u2f(o[4 * e + 1]), u2f(o[4 * e + 2]), u2f(o[4 * e + 3]));
+                } else if (write) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(out + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            pk[y] = live ? pack_bf16x2(u2f(o[8 * e + 2 * y]) * inv, u2f(o[8 * e + 2 * y + 1]) * inv) : 0u;
+                        dst[e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
                 }
             }
-            const float negm = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: every p below is zero
-            float mul = sl2;
-            // huge scores: round the product before the difference (as in prefill_tc.cu)
-            if (__any_sync(0xffffffffu, negm < -kHugeLog2 || negm > kHugeLog2)) {
-#pragma unroll
-                for (int e = 0; e < kN; ++e) s[e] = f2u(__fmul_rn(u2f(s[e]), sl2));
-                mul = 1.f;
-            }
-            const uint64_t sl2x2 = f2_pack(mul, mul), negmx2 = f2_pack(negm, negm);
-            uint64_t l4[4] = {0, 0, 0, 0};
-            uint32_t p[kN / 2];
-#pragma unroll
-            for (int e = 0; e < kN / 2; ++e) {
-                const uint64_t arg = ffma2(f2_pack(u2f(s[2 * e]), u2f(s[2 * e + 1])), sl2x2, negmx2);
-                float p0 = ex2_approx(f2_lo(arg)), p1 = ex2_approx(f2_hi(arg));
-                if (j >= edge) {  // with a scale of 0 a hidden -inf would become NaN
-                    p0 = see[e / 16] >> ((2 * e) % 32) & 1u ? p0 : 0.f;
-                    p1 = see[e / 16] >> ((2 * e + 1) % 32) & 1u ? p1 : 0.f;
-                }
-                l4[e % 4] = fadd2(l4[e % 4], f2_pack(p0, p1));
-                // P is rounded to bf16, the operand type of the second product: each
-                // weight is off by at most 2^-8 of itself; the sum keeps fp32
-                p[e] = pack_bf16x2(p0, p1);
-            }
-            const uint64_t l2 = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
-            l += f2_lo(l2) + f2_hi(l2);
-            tmem_st32(t_lane + x * kN, p);
-            tmem_st_wait();
+            if (write && r.slot >= 0 && (!one || x == 0)) *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(m, sum);
+            mbar_arrive(&bars.run_empty[k % kRing]);
             tc_fence_before();
-            mbar_arrive(&bars.p_ready[x]);
+            __syncwarp();
+            // both streams are done with Q, the O accumulators, the ancestor sets and ex
+            join();
         }
-        // ---- epilogue
-        if (ok && n > 0) {
-            ok = mbar_wait_warp(&bars.o_full, 0, &bars.abort);
-            tc_fence_after();
-        }
-        const bool write = ok && r < rows;
-        const bool have = live && n > 0;
-        const bool spoiled = n > 0 && *static_cast<volatile int *>(&bars.spoiled) != 0 && have;
-        const size_t part = (static_cast<size_t>(bk) * rows + r) * a.n_split + c;
-        const float inv = 1.f / l;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts;
-#pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];  // TMEM of this CTA: loaded unconditionally, used only when valid
-            tmem_ld32(t_lane + 128 + cc * 32, o);
-            tmem_ld_wait();
-            reg_fence32(o);
-            if (spoiled) {  // add the non-finite values of the edge tiles that this row sees
-                const __nv_bfloat16 *V = static_cast<const __nv_bfloat16 *>(a.v) + static_cast<size_t>(bk) * a.Skv * D + cc * 32;
-#pragma unroll 1
-                for (int key = k0 + edge * kN; key < k0 + nkeys; ++key) {
-                    if (!(visible32(set, key - d.past) & 1u)) continue;
-                    const uint32_t *vr = reinterpret_cast<const uint32_t *>(V + static_cast<size_t>(key) * D);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint32_t w = vr[e], nf = nonfinite2(w);
-                        if (nf & 0xffffu) o[2 * e] = f2u(u2f(o[2 * e]) + bf16lo_to_f32(w));
-                        if (nf & 0xffff0000u) o[2 * e + 1] = f2u(u2f(o[2 * e + 1]) + bf16hi_to_f32(w));
-                    }
-                }
-            }
-            if (!write) continue;
-            if (a.n_split > 1) {
-                float4 *dst = reinterpret_cast<float4 *>(a.part_o + part * D + cc * 32);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dst[e] = make_float4(u2f(o[4 * e]), u2f(o[4 * e + 1]), u2f(o[4 * e + 2]), u2f(o[4 * e + 3]));
-            } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(out + cc * 32);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        pk[y] = have ? pack_bf16x2(u2f(o[8 * e + 2 * y]) * inv, u2f(o[8 * e + 2 * y + 1]) * inv) : 0u;
-                    dst[e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
-            }
-        }
-        if (write && a.n_split > 1) *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(m_run, l);
     }
 
     tc_fence_before();
@@ -402,23 +688,73 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 1) {
         tc_fence_after();
         __syncwarp();
-        tmem_dealloc(tmem, kCols);
+        tmem_dealloc(tmem, kTmemCols);
     }
     if (threadIdx.x == 0 && bars.abort) report_timeout(a.status, 0x44);
 }
 
-// ------------------------------------------------------------ merge of the splits
+// ------------------------------------------------------------ merges of partial results
 
 __device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
 
-// One warp per row: out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, M the
-// largest m_c.  The splits are added in order, so the result does not depend on
-// how the CTAs ran.
-template <int D, typename T>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
+// One row from n parts, by a warp: out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,
+// M the largest m_c, the parts added in order.  part(c) is the row's index in O and ml.
+template <int D, typename T, typename Part>
+__device__ __forceinline__ void merge_row(const float *po, const float *pml, int n, bool live, T *out, int lane, Part part) {
+    const float2 *ml = reinterpret_cast<const float2 *>(pml);
+    float M = -INFINITY;
+    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[part(c)].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    const int col = D == 64 ? 4 * (lane % 16) : 4 * lane;
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+        const size_t at = part(c);
+        const float2 x = ml[at];
+        const float4 o = *reinterpret_cast<const float4 *>(po + at * D + col);
+        const float w = ex2_approx(x.x - ref);
+        sum = fmaf(w, x.y, sum);
+        // a part in which the row saw nothing holds zeros
+        acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
+    }
+    const float inv = live ? 1.f / sum : 0.f;
+    if (lane < D / 4)
+        store4(out + col, live ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv)
+                               : make_float4(0.f, 0.f, 0.f, 0.f));
+}
+
+// bf16: block (i, y) merges 32 rows of the unit that begins in CTA i of the main
+// kernel and ends in a later one: slot 2 i + 1, then slot 2 c of the CTAs after it.
+template <int D>
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const int slot_rows) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int i = blockIdx.x, lane = threadIdx.x % 32;
+    const int4 rec = reinterpret_cast<const int4 *>(a.merge)[2 * i];
+    if (rec.x < 0) return;
+    const int4 rec2 = reinterpret_cast<const int4 *>(a.merge)[2 * i + 1];
+    const int bk = rec.x, tile = rec.y, b = rec.z, last = rec.w, nd = rec2.x, past = rec2.y;
+    const int G = a.H / a.H_kv, rows = G * a.T;
+    for (int rr = blockIdx.y * 32 + threadIdx.x / 32; rr < blockIdx.y * 32 + 32; rr += 8) {
+        const int q = tile * kM + rr;
+        if (q >= rows || rr >= slot_rows) return;
+        const int h = (bk - b * a.H_kv) * G + q / a.T, t = q % a.T;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + b * a.o_bs + h * a.o_hs + t * a.o_ts;
+        merge_row<D>(a.part_o, a.part_ml, last - i + 1, t < nd && past + t >= 0, out, lane, [&](int c) {
+            return static_cast<size_t>(c == 0 ? 2 * i + 1 : 2 * (i + c)) * slot_rows + rr;
+        });
+    }
+}
+
+// fp32: one warp per row, n_split parts of `chunk` keys.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_f32_kernel(const TreeArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     const int G = a.H / a.H_kv, rows = G * a.T, lane = threadIdx.x % 32;
@@ -428,71 +764,81 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     const int t = r % a.T;
     const Draft d = draft_of(a, b);
     const bool live = t < d.n && d.past + t >= 0;
-    const int n = live ? (d.L + a.chunk - 1) / a.chunk : 0;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + R * a.n_split;
-    const float *po = a.part_o + R * a.n_split * D;
-    float M = -INFINITY;
-    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[c].x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    const int col = D == 64 ? 4 * (lane % 16) : 4 * lane;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-        const float2 x = ml[c];
-        const float4 o = *reinterpret_cast<const float4 *>(po + static_cast<size_t>(c) * D + col);
-        const float w = ex2_approx(x.x - ref);
-        sum = fmaf(w, x.y, sum);
-        // a split in which the row saw nothing holds zeros
-        acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
-    }
-    const float inv = live ? 1.f / sum : 0.f;
-    T *out = static_cast<T *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts;
-    if (lane < D / 4) store4(out + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    float *out = static_cast<float *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts;
+    merge_row<D>(a.part_o, a.part_ml, live ? (d.L + a.chunk - 1) / a.chunk : 0, live, out, lane,
+                 [&](int c) { return static_cast<size_t>(R) * a.n_split + c; });
 }
 
-template <int D>
-cudaError_t launch_tree_t(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv) {
-    using L = Layout<D>;
-    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+// No cache rows at all: zeros.
+__global__ void tree_zero_kernel(const TreeArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long n = static_cast<long long>(a.B) * a.H * a.T * (a.D / 8);
+    for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const long long r = i / (a.D / 8), c = i % (a.D / 8);
+        const long long t = r % a.T, h = r / a.T % a.H, b = r / a.T / a.H;
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + b * a.o_bs + h * a.o_hs + t * a.o_ts + c * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+template <int D, bool Single>
+cudaError_t launch_tree_t(const TreeArgs &a, int row_tiles, const CUtensorMap &tk, const CUtensorMap &tv) {
+    using L = Layout<D, Single>;
+    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, Single>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         L::kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int row_tiles = ((a.H / a.H_kv) * a.T + kM - 1) / kM;
-    const unsigned grid = static_cast<unsigned>(a.B * a.H_kv) * a.n_split * row_tiles;
-    e = launch_pdl(tree_tc_kernel<D>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, row_tiles, tk, tv);
-    if (e != cudaSuccess || a.n_split == 1) return e;
-    return launch_tree_combine(a, false);
+    const unsigned grid = static_cast<unsigned>(a.n_split);
+    e = launch_pdl(tree_tc_kernel<D, Single>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, row_tiles, tk, tv);
+    if (e != cudaSuccess || grid == 1) return e;
+    const int slot_rows = L::kQTiles * kM;
+    const int rows = (a.H / a.H_kv) * a.T;
+    const unsigned y = static_cast<unsigned>(((rows < slot_rows ? rows : slot_rows) + 31) / 32);
+    return launch_pdl(tree_join_kernel<D>, dim3(grid - 1, y), dim3(256), 0, a.stream, a, slot_rows);
 }
 
 }  // namespace
 
-int tree_chunk(int B, int H, int H_kv, int T, int Skv, bool f32, int n_sm) {
-    // several waves of the CTAs an SM holds, at least a few tiles each
-    const int rows = (H / H_kv) * T, per_tile = f32 ? 32 : kM;
-    const long long units = static_cast<long long>(B) * H_kv * ((rows + per_tile - 1) / per_tile);
-    const long long tiles = (static_cast<long long>(Skv) + kN - 1) / kN;
+int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int n_sm) {
+    // several waves of the blocks an SM holds, at least two tiles of 64 keys each
+    const int rows = (H / H_kv) * T;
+    const long long units = static_cast<long long>(B) * H_kv * ((rows + 31) / 32);
+    const long long tiles = (static_cast<long long>(Skv) + 63) / 64;
     const long long want = 6LL * 2 * (n_sm > 0 ? n_sm : 1);
     long long per = (units * tiles + want - 1) / want;
-    const long long least = f32 ? 2 : 8;
-    per = per < least ? least : per;
+    per = per < 2 ? 2 : per;
     per = per > tiles ? tiles : per;
     per = per < 1 ? 1 : per;
-    return static_cast<int>(per * kN);
+    return static_cast<int>(per * 64);
+}
+
+int tree_tc_grid(int B, int H, int H_kv, int T, int Skv, int n_sm) {
+    const int row_tiles = ((H / H_kv) * T + kM - 1) / kM;
+    const long long tiles = Skv > kN ? (static_cast<long long>(Skv) + kN - 1) / kN : 1;
+    const long long total = static_cast<long long>(B) * H_kv * ((row_tiles + 1) / 2) * tiles;
+    const long long most = (total + ATTN_TREE_MIN_TILES - 1) / ATTN_TREE_MIN_TILES;
+    return static_cast<int>(most < n_sm ? most : n_sm);
+}
+
+int tree_tc_slot_rows(int H, int H_kv, int T) { return (H / H_kv) * T <= kM ? kM : 2 * kM; }
+
+cudaError_t launch_tree_zero(const TreeArgs &a) {
+    return launch_pdl(tree_zero_kernel, dim3(static_cast<unsigned>(a.n_sm)), dim3(256), 0, a.stream, a);
 }
 
 cudaError_t launch_tree_tc(const TreeArgs &a, const CUtensorMap &tk, const CUtensorMap &tv) {
-    return a.D == 64 ? launch_tree_t<64>(a, tk, tv) : launch_tree_t<128>(a, tk, tv);
+    const int row_tiles = ((a.H / a.H_kv) * a.T + kM - 1) / kM;
+    if (a.D == 64)
+        return row_tiles == 1 ? launch_tree_t<64, true>(a, row_tiles, tk, tv) : launch_tree_t<64, false>(a, row_tiles, tk, tv);
+    return row_tiles == 1 ? launch_tree_t<128, true>(a, row_tiles, tk, tv) : launch_tree_t<128, false>(a, row_tiles, tk, tv);
 }
 
-cudaError_t launch_tree_combine(const TreeArgs &a, bool f32) {
+cudaError_t launch_tree_merge_f32(const TreeArgs &a) {
     const long long R = static_cast<long long>(a.B) * a.H * a.T;
     const dim3 grid(static_cast<unsigned>((R + 7) / 8));
-    if (a.D == 64)
-        return f32 ? launch_pdl(tree_merge_kernel<64, float>, grid, dim3(256), 0, a.stream, a)
-                   : launch_pdl(tree_merge_kernel<64, __nv_bfloat16>, grid, dim3(256), 0, a.stream, a);
-    return f32 ? launch_pdl(tree_merge_kernel<128, float>, grid, dim3(256), 0, a.stream, a)
-               : launch_pdl(tree_merge_kernel<128, __nv_bfloat16>, grid, dim3(256), 0, a.stream, a);
+    return a.D == 64 ? launch_pdl(tree_merge_f32_kernel<64>, grid, dim3(256), 0, a.stream, a)
+                     : launch_pdl(tree_merge_f32_kernel<128>, grid, dim3(256), 0, a.stream, a);
 }
 
 }  // namespace attn
