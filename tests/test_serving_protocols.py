@@ -17,6 +17,7 @@ import pytest
 from test_barrier_protocols import RING, Bar, Hazard, Sched, wait
 
 GUARD_RING = 8
+TREE_REQS = 16
 
 
 def wait_parity(bar, phase):
@@ -227,14 +228,17 @@ def tree_run(runs, stages, seed, mistake=None):
     """runs: (n tiles, first edge tile, one row tile?) per unit run of a CTA."""
     sc = Sched(seed)
     run_full, run_empty = [Bar() for _ in range(RING)], [Bar(3) for _ in range(RING)]
-    q_full = Bar(2)
+    q_full, q_free = [Bar(2), Bar(2)], Bar()
     kv_full, kv_empty = [Bar() for _ in range(stages)], [Bar() for _ in range(stages)]
     s_full, p_ready, o_full = [Bar(), Bar()], [Bar(), Bar()], [Bar(), Bar()]
-    g_full, g_clean = [Bar() for _ in range(GUARD_RING)], [Bar(2) for _ in range(GUARD_RING)]
+    g_full, g_clean = [Bar() for _ in range(TREE_REQS)], [Bar(2) for _ in range(TREE_REQS)]
     join = Bar(2)
-    req, ring = [None] * GUARD_RING, [None] * RING
+    req, ring = [None] * TREE_REQS, [None] * RING
+    open_reqs = [0]
     cleaned_uses = set()
+    staged = {}                # guard warps that have staged a run's Q and sets
     q_owner = [None]           # run whose Q is staged
+    set_owner = [None, None]   # run whose ancestor sets are in each buffer
     o_owner = [None, None]     # run whose values O_x accumulates
     stream = list(runs) + [(-1, 0, False)]
 
@@ -248,6 +252,15 @@ def tree_run(runs, stages, seed, mistake=None):
             n, edge, one = r
             if n < 0:
                 break
+
+            def request(what):
+                nonlocal requests
+                assert req[requests % TREE_REQS] is None, "request slot still open"
+                req[requests % TREE_REQS] = what
+                g_full[requests % TREE_REQS].arrive()
+                requests += 1
+
+            request((-2, 0, k))
             order = [(0, 0), (1, 0)] + [x for j in range(n) for x in ((j, 1), (j + 2, 0))] if one else [
                 x for j in range(n) for x in ((j, 0), (j, 1))]
             for j, kv in order:
@@ -258,28 +271,40 @@ def tree_run(runs, stages, seed, mistake=None):
                     yield wait(kv_empty[s], issued // stages - 1)
                 sc.tma.append(kv_full[s])
                 if kv and j >= edge:
-                    assert req[requests % GUARD_RING] is None, "request slot still open"
-                    req[requests % GUARD_RING] = (s, issued // stages, issued)
-                    g_full[requests % GUARD_RING].arrive()
-                    requests += 1
+                    request((s, issued // stages, issued))
                 issued += 1
-        assert req[requests % GUARD_RING] is None, "request slot still open"
-        req[requests % GUARD_RING] = (-1, 0, 0)
-        g_full[requests % GUARD_RING].arrive()
+        assert req[requests % TREE_REQS] is None, "request slot still open"
+        req[requests % TREE_REQS] = (-1, 0, 0)
+        g_full[requests % TREE_REQS].arrive()
+
+    done = {}
 
     def guard(lane):
-        r = 0
+        r, cleaned = 0, 0
         while True:
-            yield wait(g_full[r % GUARD_RING], r // GUARD_RING)
-            s, phase, use = req[r % GUARD_RING]
-            if s < 0:
+            yield wait(g_full[r % TREE_REQS], r // TREE_REQS)
+            s, phase, use = req[r % TREE_REQS]
+            if s == -1:
                 return
-            yield wait_parity(kv_full[s], phase)
-            assert kv_full[s].phase == phase + 1, "guard passes over a tile that is not the one requested"
-            cleaned_uses.add((lane, use))
-            if g_clean[r % GUARD_RING].pending == 1:
-                req[r % GUARD_RING] = None
-            g_clean[r % GUARD_RING].arrive()
+            if s == -2:
+                k = use
+                if k >= 2:
+                    yield wait(run_empty[(k - 2) % RING], (k - 2) // RING)
+                set_owner[k & 1] = k
+                if k >= 1 and mistake != "no_q_free":
+                    yield wait(q_free, k - 1)
+                staged[k] = staged.get(k, 0) + 1
+                q_owner[0] = k if staged[k] == 2 else None
+                q_full[k & 1].arrive()
+            else:
+                yield wait_parity(kv_full[s], phase)
+                assert kv_full[s].phase == phase + 1, "guard passes over a tile that is not the one requested"
+                cleaned_uses.add((lane, use))
+                g_clean[cleaned % TREE_REQS].arrive()
+                cleaned += 1
+            done[r] = done.get(r, 0) + 1
+            if done[r] == 2:
+                req[r % TREE_REQS] = None
             r += 1
 
     def mma():
@@ -296,14 +321,17 @@ def tree_run(runs, stages, seed, mistake=None):
             yield from stage()
             if j >= edge:
                 if mistake != "mma_skips_guard":
-                    yield wait(g_clean[st["cleaned"] % GUARD_RING], st["cleaned"] // GUARD_RING)
+                    yield wait(g_clean[st["cleaned"] % TREE_REQS], st["cleaned"] // TREE_REQS)
                 st["cleaned"] += 1
                 assert {(0, st["use"]), (1, st["use"])} <= cleaned_uses, "edge tile read before it was clean"
             return st["slot"]
 
-        def scores(x, k):
+        def scores(x, k, left):
             assert q_owner[0] == k, "Q of another run"
             sc.commit.append(s_full[x])
+            left[0] -= 1
+            if left[0] == 0:
+                sc.commit.append(q_free)
 
         def mix(x, k):
             assert o_owner[x] in (None, k), "O still belongs to another run"
@@ -315,11 +343,12 @@ def tree_run(runs, stages, seed, mistake=None):
             run_empty[k % RING].arrive()
             if n < 0:
                 return
-            yield wait(q_full, k)
+            yield wait(q_full[k & 1], k >> 1)
+            left = [(2 * n if not one else n)]  # S MMAs of the run still to issue
             if one:
                 for x in range(min(2, n)):
                     yield from stage()
-                    scores(x, k)
+                    scores(x, k, left)
                     sc.commit.append(kv_empty[st["slot"]])
                 for j in range(n):
                     x = j & 1
@@ -332,13 +361,13 @@ def tree_run(runs, stages, seed, mistake=None):
                     sc.commit.append(kv_empty[vs])
                     if j + 2 < n:
                         yield from stage()
-                        scores(x, k)
+                        scores(x, k, left)
                         sc.commit.append(kv_empty[st["slot"]])
             else:
                 yield from stage()
                 ks = st["slot"]
-                scores(0, k)
-                scores(1, k)
+                scores(0, k, left)
+                scores(1, k, left)
                 sc.commit.append(kv_empty[ks])
                 for j in range(n):
                     vs = yield from v_tile(j, edge)
@@ -350,7 +379,7 @@ def tree_run(runs, stages, seed, mistake=None):
                     else:
                         yield from stage()
                         ks = st["slot"]
-                        scores(0, k)
+                        scores(0, k, left)
                     yield wait(p_ready[1], pr[1])
                     pr[1] += 1
                     mix(1, k)
@@ -358,10 +387,8 @@ def tree_run(runs, stages, seed, mistake=None):
                         sc.commit.append(o_full[1])
                     sc.commit.append(kv_empty[vs])
                     if j + 1 < n:
-                        scores(1, k)
+                        scores(1, k, left)
                         sc.commit.append(kv_empty[ks])
-
-    staged = {}
 
     def softmax(x):
         sp, o_uses, joins = 0, [0, 0], 0
@@ -371,12 +398,11 @@ def tree_run(runs, stages, seed, mistake=None):
             n, edge, one = r
             if n < 0:
                 return
-            staged[k] = staged.get(k, 0) + 1
-            q_owner[0] = k if staged[k] == 2 else None
-            q_full.arrive()
+            yield wait(q_full[k & 1], k >> 1)
             for _ in range((n - x + 1) // 2 if one else n):
                 yield wait(s_full[x], sp)
                 sp += 1
+                assert set_owner[k & 1] == k, "ancestor sets of another run"
                 p_ready[x].arrive()
             if one:
                 join.arrive()
@@ -391,8 +417,10 @@ def tree_run(runs, stages, seed, mistake=None):
                 if (not one and y == x) or (one and y < n):
                     assert o_owner[y] == k, "O overwritten before it was read"
             assert ring[k % RING] is r, "run slot overwritten before it was released"
+            assert set_owner[k & 1] == k, "ancestor sets of another run"
             run_empty[k % RING].arrive()
-            if mistake != "no_join":
+            o_owner[x] = None if not one else o_owner[x]
+            if one and mistake != "no_join":
                 join.arrive()
                 yield wait(join, joins)
                 joins += 1
@@ -426,6 +454,6 @@ def test_tree_protocol(stages):
     assert not bad, bad[:3]
 
 
-@pytest.mark.parametrize("mistake", ["mma_skips_guard", "no_join"])
+@pytest.mark.parametrize("mistake", ["mma_skips_guard", "no_join", "no_q_free"])
 def test_tree_model_catches_planted_mistakes(mistake):
     assert _tree_trials(4, mistake, trials=80), f"the model missed '{mistake}'"

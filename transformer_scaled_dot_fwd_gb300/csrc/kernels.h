@@ -87,7 +87,7 @@ struct TreeArgs {
     int chunk, n_split;         // fp32: keys per split and splits; bf16: n_split CTAs
     // Partial results: O unnormalised [D] and (running max in log2 units, sum) of
     // fp32: row ((b * H_kv + g) * G * T + r) * n_split + split
-    // bf16: row slot * slot_rows + r, two slots per CTA (tree_tc.cu)
+    // bf16: two slots per CTA of slot_rows rows, O as [slot][D / 4][row][4] (tree_tc.cu)
     float *part_o, *part_ml;
     int *merge;                 // bf16: 8 ints per CTA, the unit it shares with later CTAs
     int *status;

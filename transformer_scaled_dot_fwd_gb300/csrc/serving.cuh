@@ -37,47 +37,57 @@ __device__ __forceinline__ Draft draft_of(const TreeArgs &a, int b) {
 }
 
 // Bit sets of each drafted token's visible draft keys: itself and its
-// ancestors, as far as they have a cache row.  At least kTreeMaxTokens threads
-// call it together, `sync` joins them.  The parent relation is closed by
-// doubling: after round i a set holds the 2^i nearest ancestors.
+// ancestors, as far as they have a cache row.  `Threads` threads call it
+// together, `sync` joins them.  The parent relation is closed by doubling: after
+// round i a set holds the 2^i nearest ancestors.
 struct Ancestors {
     uint32_t bits[kTreeMaxTokens][4];
     int jump[kTreeMaxTokens];
 };
 
-template <typename Sync>
+template <int Threads, typename Sync>
 __device__ __forceinline__ void build_ancestors(const TreeArgs &a, int b, const Draft &d, Ancestors &anc, int tid,
                                                 Sync sync) {
-    const int t = tid;
-    int jump = -1;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (t < kTreeMaxTokens) {
+    constexpr int kEach = kTreeMaxTokens / Threads;  // tokens tid, tid + Threads, ...
+    int jump[kEach];
+    uint32_t w[kEach][4];
+#pragma unroll
+    for (int y = 0; y < kEach; ++y) {
+        const int t = tid + y * Threads;
+        jump[y] = -1;
         if (t < d.n) {
             const int p = a.parents[b * a.parents_bs + t];
-            jump = p >= 0 && p < t ? p : -1;
-            if (d.past + t >= 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = t / 32 == i ? 1u << (t % 32) : 0u;
-            }
+            jump[y] = p >= 0 && p < t ? p : -1;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) anc.bits[t][i] = w[i];
-        anc.jump[t] = jump;
+        for (int i = 0; i < 4; ++i) {
+            w[y][i] = t < d.n && d.past + t >= 0 && t / 32 == i ? 1u << (t % 32) : 0u;
+            anc.bits[t][i] = w[y][i];
+        }
+        anc.jump[t] = jump[y];
     }
     sync();
     for (int reach = 1; reach < d.n; reach *= 2) {
-        int next = -1;
-        if (t < kTreeMaxTokens && jump >= 0) {
+        int next[kEach];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] |= anc.bits[jump][i];
-            next = anc.jump[jump];
-            if (next >= jump) next = -1;  // never, unless a wait gave up: stay inside the set
+        for (int y = 0; y < kEach; ++y) {
+            next[y] = -1;
+            if (jump[y] >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[y][i] |= anc.bits[jump[y]][i];
+                next[y] = anc.jump[jump[y]];
+                if (next[y] >= jump[y]) next[y] = -1;  // never, unless a wait gave up: stay inside the set
+            }
         }
         sync();
-        if (t < kTreeMaxTokens && jump >= 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) anc.bits[t][i] = w[i];
-            anc.jump[t] = jump = next;
+        for (int y = 0; y < kEach; ++y) {
+            const int t = tid + y * Threads;
+            if (jump[y] >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) anc.bits[t][i] = w[y][i];
+                anc.jump[t] = jump[y] = next[y];
+            }
         }
         sync();
     }

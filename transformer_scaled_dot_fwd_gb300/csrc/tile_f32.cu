@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
     const Draft d = draft_of(a, b);
     const int k0 = c * a.chunk, k1 = min(k0 + a.chunk, d.L);
     if (k0 >= k1 && a.n_split > 1) return;  // the merge never reads this split
-    build_ancestors(a, b, d, sm.anc, tid, [] { __syncthreads(); });
+    build_ancestors<kThreads>(a, b, d, sm.anc, tid, [] { __syncthreads(); });
     for (int i = tid; i < kRows * D / 4; i += kThreads) {
         const int r = r0 + i / (D / 4), col = 4 * (i % (D / 4));
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -35,8 +35,9 @@
 //
 // Roles (12 warps): warp 0 walks the CTA's run and loads K_j, V_j through a ring
 // of 128-row TMA tiles, warp 1 allocates TMEM and issues the MMAs, warps 2-3
-// guard, warps 4-7 and 8-11 are the streams (Q staging, ancestor sets, softmax,
-// epilogue; thread = row = TMEM lane).
+// stage the next unit's Q and ancestor sets while the streams finish the last
+// one, and guard, warps 4-7 and 8-11 are the streams (softmax, epilogue; thread =
+// row = TMEM lane).
 #include "kernels.h"
 #include "ptx.cuh"
 #include "serving.cuh"
@@ -52,7 +53,9 @@ constexpr uint32_t kRegsSoftmax = 216;  // warps 4-11: 128 * 64 + 256 * 216 <= 3
 constexpr int kTmemCols = 512;   // S0 0, S1 128, O0 256, O1 256 + D
 constexpr int kRing = 4;         // unit runs in flight between the roles
 constexpr int kRingReaders = 32 + 256;
-constexpr int kGuardRing = 8;    // edge-tile requests (see prefill_tc.cu); fewer are ever open
+// Requests to warps 2-3: one per run and one per edge tile.  No more than kRing
+// runs are open at once, and an edge tile holds a K/V stage: fewer than 16 in all.
+constexpr int kGuardRing = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kHugeLog2 = 16777216.0f;  // 2^24
@@ -76,8 +79,17 @@ struct Run {
 };
 
 struct GuardReq {
-    int stage, parity, rows, run;  // rows of the tile inside the sequence; run: ring slot
+    int stage;   // K/V stage of an edge tile, kStageRun: a new run, kEnd: no more work
+    int parity;  // of the stage's kv_full
+    int rows;    // rows of the tile inside the sequence
+    int run;     // ring slot
 };
+constexpr int kEnd = -1, kStageRun = -2;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Single: one row tile in all, its second Q buffer is one more K/V stage.
 template <int D, bool Single>
@@ -89,18 +101,19 @@ struct Layout {
     static constexpr int kStages = D == 128 ? (Single ? 5 : 4) : 8;
     static constexpr int kRingOff = kQTiles * kTile;
     static constexpr int kAncOff = kRingOff + kStages * kTile;
-    static constexpr int kExOff = kAncOff + static_cast<int>(sizeof(Ancestors));
+    static constexpr int kExOff = kAncOff + 2 * static_cast<int>(sizeof(Ancestors));
     static constexpr int kBarOff = kExOff + 256 * 8;
     static constexpr int kSmemBytes = kBarOff + 1024 + 1024;
 };
 
 struct Bars {
-    uint64_t q_full;
+    uint64_t q_full[2];         // Q and ancestor sets of run k staged: [k & 1]
+    uint64_t q_free;            // a run's last S MMA is complete
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2], p_ready[2], o_full[2];
     uint64_t run_full[kRing], run_empty[kRing];
     uint64_t guard_full[kGuardRing], guard_clean[kGuardRing];
-    uint64_t join;              // both streams (a barrier with a limit)
+    uint64_t join, guard_join;  // both streams, both guard warps (barriers with a limit)
     uint64_t mma_done;
     Run run[kRing];
     GuardReq req[kGuardRing];
@@ -112,16 +125,15 @@ static_assert(sizeof(Bars) <= 1024, "barrier block");
 
 // Every unit has at least one tile, so that the rows of empty sequences are
 // written (as zeros) like the others.
-__device__ __forceinline__ int tiles_of(const TreeArgs &a, int b) {
-    const int L = a.cache_len ? min(max(a.cache_len[b], 0), a.Skv) : a.Skv;
-    return max(1, (L + kN - 1) / kN);
-}
+__device__ __forceinline__ int tiles_of(const Draft &d) { return max(1, (d.L + kN - 1) / kN); }
 
+__device__ __forceinline__ Run read_run(Bars &bars, int slot) {
+    const volatile Run &s = bars.run[slot];
+    return Run{s.b, s.bk, s.tile, s.j0, s.n, s.slot, s.L, s.nd, s.past};
+}
 __device__ __forceinline__ bool take_run(Bars &bars, int k, Run *r) {
     if (!mbar_wait_warp(&bars.run_full[k % kRing], (k / kRing) & 1, &bars.abort)) return false;
-    const volatile Run &s = bars.run[k % kRing];
-    r->b = s.b, r->bk = s.bk, r->tile = s.tile, r->j0 = s.j0, r->n = s.n, r->slot = s.slot;
-    r->L = s.L, r->nd = s.nd, r->past = s.past;
+    *r = read_run(bars, k % kRing);
     return true;
 }
 
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t dsmem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + L::kRingOff;
-    Ancestors &anc = *reinterpret_cast<Ancestors *>(smem + L::kAncOff);
+    Ancestors *anc = reinterpret_cast<Ancestors *>(smem + L::kAncOff);  // [run & 1]
     float2 *ex = reinterpret_cast<float2 *>(smem + L::kExOff);  // [stream][row] max, sum
     Bars &bars = *reinterpret_cast<Bars *>(smem + L::kBarOff);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -148,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
-        mbar_init(&bars.q_full, 256);
+        for (int x = 0; x < 2; ++x) mbar_init(&bars.q_full[x], 64);
+        mbar_init(&bars.q_free, 1);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars.kv_full[s], 1);
             mbar_init(&bars.kv_empty[s], 1);
@@ -167,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars.guard_clean[s], 64);
         }
         mbar_init(&bars.join, 256);
+        mbar_init(&bars.guard_join, 64);
         mbar_init(&bars.mma_done, 1);
         bars.abort = 0;
         fence_mbar_init();
@@ -187,7 +201,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kRegsOther>();
         const int per = a.H_kv * pairs;  // units of a sequence
         long long total = 0;             // tiles of all units
-        for (int b0 = lane; b0 < a.B; b0 += 32) total += tiles_of(a, b0);
+        Draft mine{0, 0, 0};             // of sequence b0 + lane
+        for (int b0 = lane; b0 < a.B; b0 += 32) {
+            mine = draft_of(a, b0);
+            total += tiles_of(mine);
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
         total *= per;
@@ -200,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int b = 0;
         long long base = 0;
         for (int b0 = 0; !idle && b0 < a.B; b0 += 32) {
-            const long long t = b0 + lane < a.B ? static_cast<long long>(tiles_of(a, b0 + lane)) * per : 0;
+            if (a.B > 32) mine = draft_of(a, min(b0 + lane, a.B - 1));
+            const long long t = b0 + lane < a.B ? static_cast<long long>(tiles_of(mine)) * per : 0;
             long long sum = t;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -216,19 +235,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
+        Draft d{__shfl_sync(0xffffffffu, mine.L, b % 32), __shfl_sync(0xffffffffu, mine.n, b % 32), 0};
+        d.past = d.L - d.n;
         if (lane == 0) {
             int issued = 0, requests = 0, k = 0;
             bool ok = true;
             int4 rec = make_int4(-1, 0, 0, 0), rec2 = make_int4(0, 0, 0, 0);
             long long pos = lo;
-            int nt = tiles_of(a, b);
+            int nt = tiles_of(d);
             int u = static_cast<int>((lo - base) / nt), j = static_cast<int>((lo - base) % nt);
             while (ok) {
                 const int slot = k % kRing;
                 if (k >= kRing && !(ok = mbar_wait(&bars.run_empty[slot], ((k / kRing) - 1) & 1, &bars.abort))) break;
                 Run r{0, 0, 0, 0, -1, 0, 0, 0, 0};
                 if (pos < hi) {
-                    const Draft d = draft_of(a, b);
                     r.b = b;
                     r.bk = b * a.H_kv + u / pairs;
                     r.tile = 2 * (u % pairs);
@@ -248,6 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *static_cast<volatile int *>(&bars.spoiled[slot]) = 0;
                 mbar_arrive(&bars.run_full[slot]);
                 if (r.n < 0) break;
+                auto request = [&](int stage, int parity, int inside) {
+                    volatile GuardReq &q = bars.req[requests % kGuardRing];
+                    q.stage = stage, q.parity = parity, q.rows = inside, q.run = slot;
+                    mbar_arrive(&bars.guard_full[requests % kGuardRing]);
+                    ++requests;
+                };
+                request(kStageRun, 0, 0);
                 const int edge = edge_of(r);
                 auto load = [&](int jj, int kv) {
                     if (!ok || jj >= r.n) return;
@@ -259,12 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < L::kSub; ++c)
                         tma_load_3d(ring + s * L::kTile + c * L::kBlock, kv ? &tv : &tk, &bars.kv_full[s], c * 64,
                                     (r.j0 + jj) * kN, r.bk);
-                    if (kv && jj >= edge) {
-                        volatile GuardReq &q = bars.req[requests % kGuardRing];
-                        q.stage = s, q.parity = (issued / kStages) & 1, q.rows = r.L - (r.j0 + jj) * kN, q.run = slot;
-                        mbar_arrive(&bars.guard_full[requests % kGuardRing]);
-                        ++requests;
-                    }
+                    if (kv && jj >= edge) request(s, (issued / kStages) & 1, r.L - (r.j0 + jj) * kN);
                     ++issued;
                 };
                 if (Single || r.tile + 1 >= row_tiles) {  // one row tile: K0 K1 | V0 K2 | V1 K3 | ...
@@ -285,11 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 j = 0;
                 if (r.j0 + r.n == nt && ++u == per) {
                     u = 0;
-                    if (++b < a.B) nt = tiles_of(a, b);
+                    if (++b < a.B) {
+                        d = draft_of(a, b);
+                        nt = tiles_of(d);
+                    }
                 }
             }
             if (ok) {  // no more work for the guard
-                *static_cast<volatile int *>(&bars.req[requests % kGuardRing].stage) = -1;
+                *static_cast<volatile int *>(&bars.req[requests % kGuardRing].stage) = kEnd;
                 mbar_arrive(&bars.guard_full[requests % kGuardRing]);
             }
             int4 *out = reinterpret_cast<int4 *>(a.merge) + 2 * blockIdx.x;
@@ -324,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             desc_add(db, (kk * 16 * 128) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
         };
         int consumed = 0, cleaned = 0;
-        uint32_t pr[2] = {0, 0}, qp = 0;
+        uint32_t pr[2] = {0, 0};
         bool ok = true;
         auto next_stage = [&](int *slot) {  // wait for the next ring stage
             *slot = consumed % kStages;
@@ -344,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n < 0) break;
             const int edge = __shfl_sync(0xffffffffu, edge_of(r), 0);
             const bool one = Single || __shfl_sync(0xffffffffu, r.tile, 0) + 1 >= row_tiles;
-            if (!(ok = mbar_wait_warp(&bars.q_full, qp, &bars.abort))) break;
-            qp ^= 1;
+            if (!(ok = mbar_wait_warp(&bars.q_full[k & 1], (k >> 1) & 1, &bars.abort))) break;
             int ks = 0, vs = 0;
             if (one) {
                 // stream x = tile & 1, both on Q buffer 0
@@ -358,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issue_s(x, 0, ks);
                     tc_commit_warp(&bars.s_full[x]);
                     tc_commit_warp(&bars.kv_empty[ks]);
+                    if (x + 1 == n) tc_commit_warp(&bars.q_free);
                 }
                 auto step = [&](int j, int x) {
                     next_stage(&vs);
@@ -375,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         issue_s(x, 0, ks);
                         tc_commit_warp(&bars.s_full[x]);
                         tc_commit_warp(&bars.kv_empty[ks]);
+                        if (j + 3 == n) tc_commit_warp(&bars.q_free);  // the last S of the run
                     }
                 };
                 for (int j = 0; j < n && ok; j += 2) {
@@ -390,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_s(1, L::kQTiles - 1, ks);
                 tc_commit_warp(&bars.s_full[1]);
                 tc_commit_warp(&bars.kv_empty[ks]);
+                if (n == 1) tc_commit_warp(&bars.q_free);
                 for (int j = 0; j < n && ok; ++j) {
                     next_stage(&vs);
                     if (ok) guarded(j >= edge);
@@ -416,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         issue_s(1, L::kQTiles - 1, ks);
                         tc_commit_warp(&bars.s_full[1]);
                         tc_commit_warp(&bars.kv_empty[ks]);
+                        if (j + 2 == n) tc_commit_warp(&bars.q_free);
                     }
                 }
             }
@@ -425,16 +453,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int never = 0;
         mbar_wait_warp(&bars.mma_done, 0, &never);
     } else if (warp < 4) {
-        // ================================================================ guard of the edge V tiles
+        // ================================================================ Q, ancestor sets, guard of the edge V tiles
         regs_dec<kRegsOther>();
         const int tid = threadIdx.x - 64;
-        for (int q = 0;; ++q) {
+        bool ok = true;
+        uint32_t joins = 0;
+        auto join = [&] {  // both warps, or the abort flag
+            mbar_arrive(&bars.guard_join);
+            ok = mbar_wait_warp(&bars.guard_join, joins & 1, &bars.abort) && ok;
+            ++joins;
+        };
+        // Run k, in ring slot `slot`.  Its set buffer was last read by run k - 2, its Q
+        // buffers by the S MMAs of run k - 1.
+        auto stage_run = [&](int k, int slot) {
+            const Run r = read_run(bars, slot);
+            if (k >= 2 && !(ok = mbar_wait_warp<64>(&bars.run_empty[(k - 2) % kRing], ((k - 2) / kRing) & 1, &bars.abort)))
+                return;
+            if (edge_of(r) < r.n) build_ancestors<64>(a, r.b, Draft{r.L, r.nd, r.past}, anc[k & 1], tid, join);
+            if (!ok || (k >= 1 && !(ok = mbar_wait_warp<64>(&bars.q_free, (k - 1) & 1, &bars.abort)))) return;
+            // rows as a TMA load would leave them (128-byte swizzle); rows without a token are zeros
+            constexpr int kChunks = D / 8, kStep = 64 / kChunks;  // 16-byte chunks of a row; rows a pass
+            const int n_rows = (Single || r.tile + 1 >= row_tiles ? 1 : 2) * kM;
+            const int ch = tid % kChunks;
+            const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + r.b * a.q_bs +
+                                     static_cast<long long>(r.bk - r.b * a.H_kv) * G * a.q_hs + ch * 8;
+            int q = r.tile * kM + tid / kChunks, h = q / a.T, t = q - h * a.T;
+            const uint32_t base = smem_u32(smem) + (ch / 8) * L::kBlock;
+#pragma unroll 4
+            for (int rr = tid / kChunks; rr < n_rows; rr += kStep) {
+                const bool in = q < rows && t < r.nd;
+                const int rt = rr % kM;
+                cp_async16(base + (rr / kM) * L::kTile + rt * 128 + (((ch & 7) ^ (rt & 7)) << 4),
+                           in ? Q + h * a.q_hs + t * a.q_ts : static_cast<const __nv_bfloat16 *>(a.q), in ? 16u : 0u);
+                q += kStep;
+                t += kStep;
+                while (t >= a.T) t -= a.T, ++h;
+            }
+            cp_async_wait_all();
+            fence_proxy_async_shared();
+            mbar_arrive(&bars.q_full[k & 1]);
+        };
+        for (int q = 0, k = 0, edges = 0; ok; ++q) {
             const int slot = q % kGuardRing;
             // a request comes after its load was issued, and its stage is not reused
             // before guard_clean: kv_full cannot be a phase off
             if (!mbar_wait_warp<64>(&bars.guard_full[slot], (q / kGuardRing) & 1, &bars.abort)) break;
             const volatile GuardReq &rq = bars.req[slot];
             const int stage = rq.stage, parity = rq.parity, inside = rq.rows, run = rq.run;
+            if (stage == kStageRun) {
+                stage_run(k++, run);
+                continue;
+            }
             if (stage < 0) break;
             if (!mbar_wait_warp(&bars.kv_full[stage], parity, &bars.abort)) break;
             const uint32_t tile = smem_u32(ring + stage * L::kTile);
@@ -454,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (bad) *static_cast<volatile int *>(&bars.spoiled[run]) = 1;
             fence_proxy_async_shared();
-            mbar_arrive(&bars.guard_clean[slot]);
+            mbar_arrive(&bars.guard_clean[edges % kGuardRing]);  // edge tiles are counted by themselves
+            ++edges;
         }
     } else {
         // ================================================================ softmax streams
@@ -462,12 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = (warp - 4) / 4;
         const int quarter = warp % 4;  // TMEM lanes [32 * quarter, 32 * quarter + 32)
         const int row = quarter * 32 + lane;
-        const int tid = threadIdx.x - 128;  // 0 .. 255 over both streams
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t t_s = t_lane + x * 128u, t_o = t_lane + 256u + x * static_cast<uint32_t>(D);
         const float sl2 = a.scale * kLog2e;
         uint32_t sp = 0, o_uses[2] = {0, 0};
-        int anc_of = -1;  // sequence whose ancestor sets are in shared memory
         bool ok = true;
         uint32_t joins = 0;
         auto join = [&] {  // waits for all threads of both streams, or for the abort flag
@@ -476,39 +544,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++joins;
         };
         for (int k = 0; ok; ++k) {
-            Run r;
-            if (!(ok = take_run(bars, k, &r))) break;
-            if (r.n < 0) break;
-            const bool one = Single || r.tile + 1 >= row_tiles;
-            const int edge = edge_of(r);
-            // Q rows, swizzled as a TMA load would leave them; rows without a token are
-            // zeros.  The last MMA that read the buffers is complete (end of the previous run).
+            bool one, live;
+            int n, edge, at0;  // tiles of this stream, first edge tile, draft-relative first key of the run
+            const uint32_t *set;
             {
-                const int n_chunk = (one ? 1 : 2) * kM * D / 8;
-                const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + r.b * a.q_bs;
-                const int h0 = (r.bk - r.b * a.H_kv) * G;
-#pragma unroll 4
-                for (int i = tid; i < n_chunk; i += 256) {
-                    const int rr = i / (D / 8), ch = i % (D / 8), q = r.tile * kM + rr;
-                    const int h = q / a.T, t = q - h * a.T;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (q < rows && t < r.nd) v = *reinterpret_cast<const uint4 *>(Q + (h0 + h) * a.q_hs + t * a.q_ts + ch * 8);
-                    const int rt = rr % kM;
-                    st_shared_v4(smem_u32(smem) + (rr / kM) * L::kTile + (ch / 8) * L::kBlock + rt * 128 +
-                                     (((ch & 7) ^ (rt & 7)) << 4), v.x, v.y, v.z, v.w);
-                }
+                Run r;
+                if (!(ok = take_run(bars, k, &r))) break;
+                if (r.n < 0) break;
+                one = Single || r.tile + 1 >= row_tiles;
+                edge = edge_of(r);
+                const int q = (r.tile + (one ? 0 : x)) * kM + row;  // this thread's row of the unit
+                const int t = q % a.T;
+                live = q < rows && t < r.nd && r.past + t >= 0;
+                set = anc[k & 1].bits[t];
+                n = one ? (r.n - x + 1) / 2 : r.n;
+                at0 = r.j0 * kN - r.past;
             }
-            fence_proxy_async_shared();
-            mbar_arrive(&bars.q_full);
-            if (edge < r.n && anc_of != r.b) {
-                build_ancestors(a, r.b, Draft{r.L, r.nd, r.past}, anc, tid, join);
-                anc_of = r.b;
-            }
-            const int q = (r.tile + (one ? 0 : x)) * kM + row;  // this thread's row of the unit
-            const int t = q % a.T;
-            const bool live = q < rows && t < r.nd && r.past + t >= 0;
-            const uint32_t *set = anc.bits[t];
-            const int n = one ? (r.n - x + 1) / 2 : r.n;  // tiles of this stream
+            // the ancestor sets (and Q) of this run
+            if (!(ok = mbar_wait_warp<32>(&bars.q_full[k & 1], (k >> 1) & 1, &bars.abort))) break;
             float m_run = -INFINITY, l = 0.f;
             for (int i = 0; i < n; ++i) {
                 const int j = one ? 2 * i + x : i;
@@ -523,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 4; ++c) reg_fence32(s + c * 32);
                 const bool masked = j >= edge;
                 if (masked) {
-                    const int at = (r.j0 + j) * kN - r.past;
+                    const int at = at0 + j * kN;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t see = live ? visible32(set, at + 32 * c) : 0u;
@@ -564,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // huge scores: round the product before the difference (as in prefill_tc.cu); a
                 // scale of 0: a hidden key's -inf must not become NaN
                 if (__any_sync(0xffffffffu, negm < -kHugeLog2 || negm > kHugeLog2) || sl2 == 0.f) {
-                    const int at = (r.j0 + j) * kN - r.past;
+                    const int at = at0 + j * kN;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t see = !masked ? 0xffffffffu : live ? visible32(set, at + 32 * c) : 0u;
@@ -597,7 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&bars.p_ready[x]);
             }
-            // ---- epilogue
+            // ---- epilogue (the run again, from its ring slot: nothing of it stays live above)
+            const Run r = read_run(bars, k % kRing);
+            const int q = (r.tile + (one ? 0 : x)) * kM + row, t = q % a.T;
             const bool other = one && r.n > 1;  // the other stream has a part of the same rows
             float w = 1.f, w_other = 0.f, m = m_run, sum = l;
             if (one) {
@@ -620,7 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool write = ok && q < rows;
             const bool spoiled = *static_cast<volatile int *>(&bars.spoiled[k % kRing]) != 0 && live;
             const float inv = 1.f / sum;
-            const size_t part = static_cast<size_t>(r.slot < 0 ? 0 : r.slot) * (L::kQTiles * kM) + (one ? 0 : x * kM) + row;
+            constexpr int slot_rows = L::kQTiles * kM;
+            const int slot_row = (one ? 0 : x * kM) + row;
             // a unit of one row tile: stream 0 writes the first half of the columns, stream 1 the second
             const int c0 = one ? x * (D / 64) : 0, c1 = one ? c0 + D / 64 : D / 32;
             const int h = (r.bk - r.b * a.H_kv) * G + q / a.T;
@@ -658,10 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (write && r.slot >= 0) {
-                    float4 *dst = reinterpret_cast<float4 *>(a.part_o + part * D + c * 32);
+                    // four columns of all the slot's rows side by side: a warp writes 512 bytes at once
+                    float4 *dst = reinterpret_cast<float4 *>(a.part_o) + (static_cast<size_t>(r.slot) * (D / 4) + c * 8) * slot_rows + slot_row;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(u2f(o[4 * e]), u2f(o[4 * e + 1]), u2f(o[4 * e + 2]), u2f(o[4 * e + 3]));
+                        dst[e * slot_rows] = make_float4(u2f(o[4 * e]), u2f(o[4 * e + 1]), u2f(o[4 * e + 2]), u2f(o[4 * e + 3]));
                 } else if (write) {
                     uint4 *dst = reinterpret_cast<uint4 *>(out + c * 32);
 #pragma unroll
@@ -674,12 +731,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (write && r.slot >= 0 && (!one || x == 0)) *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(m, sum);
+            if (write && r.slot >= 0 && (!one || x == 0))
+                reinterpret_cast<float2 *>(a.part_ml)[static_cast<size_t>(r.slot) * slot_rows + slot_row] = make_float2(m, sum);
             mbar_arrive(&bars.run_empty[k % kRing]);
             tc_fence_before();
             __syncwarp();
-            // both streams are done with Q, the O accumulators, the ancestor sets and ex
-            join();
+            // both streams are done with each other's O and with ex
+            if (one) join();
         }
     }
 
@@ -700,56 +758,59 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
 
-// One row from n parts, by a warp: out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,
-// M the largest m_c, the parts added in order.  part(c) is the row's index in O and ml.
-template <int D, typename T, typename Part>
-__device__ __forceinline__ void merge_row(const float *po, const float *pml, int n, bool live, T *out, int lane, Part part) {
-    const float2 *ml = reinterpret_cast<const float2 *>(pml);
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, M the largest m_c, the
+// parts added in order, for one row and 4 C columns: part(c) gives where part c
+// has the row's (m, l), and column(c, e) its e-th four columns.
+template <int C, typename T, typename Part, typename Column>
+__device__ __forceinline__ void merge_row(int n, bool live, T *out, Part part, Column column) {
     float M = -INFINITY;
-    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[part(c)].x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+#pragma unroll 8
+    for (int c = 0; c < n; ++c) M = fmaxf(M, part(c).x);
     const float ref = M == -INFINITY ? 0.f : M;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[C];
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    const int col = D == 64 ? 4 * (lane % 16) : 4 * lane;
 #pragma unroll 4
     for (int c = 0; c < n; ++c) {
-        const size_t at = part(c);
-        const float2 x = ml[at];
-        const float4 o = *reinterpret_cast<const float4 *>(po + at * D + col);
+        const float2 x = part(c);
         const float w = ex2_approx(x.x - ref);
         sum = fmaf(w, x.y, sum);
-        // a part in which the row saw nothing holds zeros
-        acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
+#pragma unroll
+        for (int e = 0; e < C; ++e) {  // a part in which the row saw nothing holds zeros
+            const float4 o = column(c, e);
+            acc[e] = make_float4(fmaf(w, o.x, acc[e].x), fmaf(w, o.y, acc[e].y), fmaf(w, o.z, acc[e].z), fmaf(w, o.w, acc[e].w));
+        }
     }
     const float inv = live ? 1.f / sum : 0.f;
-    if (lane < D / 4)
-        store4(out + col, live ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv)
-                               : make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+    for (int e = 0; e < C; ++e)
+        store4(out + 4 * e, live ? make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
 // bf16: block (i, y) merges 32 rows of the unit that begins in CTA i of the main
-// kernel and ends in a later one: slot 2 i + 1, then slot 2 c of the CTAs after it.
+// kernel and ends in a later one: slot 2 i + 1, then slot 2 c of the CTAs after
+// it.  Lane = row, as the partial results lie; warp = D / 8 columns.
 template <int D>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const int slot_rows) {
     griddep_launch_dependents();
     griddep_wait();
-    const int i = blockIdx.x, lane = threadIdx.x % 32;
-    const int4 rec = reinterpret_cast<const int4 *>(a.merge)[2 * i];
+    const int i = blockIdx.x, rr = blockIdx.y * 32 + threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int4 rec = reinterpret_cast<const int4 *>(a.merge)[2 * i], rec2 = reinterpret_cast<const int4 *>(a.merge)[2 * i + 1];
     if (rec.x < 0) return;
-    const int4 rec2 = reinterpret_cast<const int4 *>(a.merge)[2 * i + 1];
     const int bk = rec.x, tile = rec.y, b = rec.z, last = rec.w, nd = rec2.x, past = rec2.y;
-    const int G = a.H / a.H_kv, rows = G * a.T;
-    for (int rr = blockIdx.y * 32 + threadIdx.x / 32; rr < blockIdx.y * 32 + 32; rr += 8) {
-        const int q = tile * kM + rr;
-        if (q >= rows || rr >= slot_rows) return;
-        const int h = (bk - b * a.H_kv) * G + q / a.T, t = q % a.T;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + b * a.o_bs + h * a.o_hs + t * a.o_ts;
-        merge_row<D>(a.part_o, a.part_ml, last - i + 1, t < nd && past + t >= 0, out, lane, [&](int c) {
-            return static_cast<size_t>(c == 0 ? 2 * i + 1 : 2 * (i + c)) * slot_rows + rr;
-        });
-    }
+    const int G = a.H / a.H_kv, q = tile * kM + rr;
+    if (q >= G * a.T) return;
+    const int h = (bk - b * a.H_kv) * G + q / a.T, t = q % a.T;
+    constexpr int C = D / 32;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + b * a.o_bs + h * a.o_hs + t * a.o_ts + warp * 4 * C;
+    auto slot = [&](int c) { return static_cast<size_t>(c == 0 ? 2 * i + 1 : 2 * (i + c)); };
+    merge_row<C>(last - i + 1, t < nd && past + t >= 0, out,
+                 [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[slot(c) * slot_rows + rr]; },
+                 [&](int c, int e) {
+                     return reinterpret_cast<const float4 *>(a.part_o)[(slot(c) * (D / 4) + warp * C + e) * slot_rows + rr];
+                 });
 }
 
 // fp32: one warp per row, n_split parts of `chunk` keys.
@@ -759,14 +820,15 @@ __global__ void __launch_bounds__(256) tree_merge_f32_kernel(const TreeArgs a) {
     griddep_wait();
     const int G = a.H / a.H_kv, rows = G * a.T, lane = threadIdx.x % 32;
     const long long R = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
-    if (R >= static_cast<long long>(a.B) * a.H_kv * rows) return;
+    if (R >= static_cast<long long>(a.B) * a.H_kv * rows || lane >= D / 4) return;
     const int bk = static_cast<int>(R / rows), r = static_cast<int>(R % rows), b = bk / a.H_kv, g = bk % a.H_kv;
     const int t = r % a.T;
     const Draft d = draft_of(a, b);
     const bool live = t < d.n && d.past + t >= 0;
-    float *out = static_cast<float *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts;
-    merge_row<D>(a.part_o, a.part_ml, live ? (d.L + a.chunk - 1) / a.chunk : 0, live, out, lane,
-                 [&](int c) { return static_cast<size_t>(R) * a.n_split + c; });
+    float *out = static_cast<float *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts + 4 * lane;
+    merge_row<1>(live ? (d.L + a.chunk - 1) / a.chunk : 0, live, out,
+                 [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[R * a.n_split + c]; },
+                 [&](int c, int) { return reinterpret_cast<const float4 *>(a.part_o)[(R * a.n_split + c) * (D / 4) + lane]; });
 }
 
 // No cache rows at all: zeros.
