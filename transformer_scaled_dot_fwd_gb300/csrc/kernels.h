@@ -96,7 +96,7 @@ struct TreeArgs {
 };
 // fp32: keys per split for these sizes.
 int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int n_sm);
-// bf16: CTAs for these sizes, and rows of a workspace slot.
+// bf16: CTAs for these sizes (-1: too large), and rows of a workspace slot.
 int tree_tc_grid(int B, int H, int H_kv, int T, int Skv, int n_sm);
 int tree_tc_slot_rows(int H, int H_kv, int T);
 // bf16 tcgen05 kernel and its merge; tk/tv view the caches as (D, Skv, B * H_kv) with 64 x 128 x 1 boxes.

@@ -64,6 +64,12 @@ constexpr float kHugeLog2 = 16777216.0f;  // 2^24
 #ifndef ATTN_TREE_MIN_TILES
 #define ATTN_TREE_MIN_TILES 2
 #endif
+// What a unit costs beside its tiles, in tiles: start, epilogue, merge.
+#ifndef ATTN_TREE_UNIT_COST
+#define ATTN_TREE_UNIT_COST 2
+#endif
+
+constexpr int kUnitCost = ATTN_TREE_UNIT_COST, kMinCost = ATTN_TREE_MIN_TILES;
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
@@ -126,6 +132,7 @@ static_assert(sizeof(Bars) <= 1024, "barrier block");
 // Every unit has at least one tile, so that the rows of empty sequences are
 // written (as zeros) like the others.
 __device__ __forceinline__ int tiles_of(const Draft &d) { return max(1, (d.L + kN - 1) / kN); }
+__device__ __forceinline__ int cost_of(const Draft &d) { return tiles_of(d) + kUnitCost; }
 
 __device__ __forceinline__ Run read_run(Bars &bars, int slot) {
     const volatile Run &s = bars.run[slot];
@@ -200,30 +207,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================================================================ walk and TMA loads
         regs_dec<kRegsOther>();
         const int per = a.H_kv * pairs;  // units of a sequence
-        long long total = 0;             // tiles of all units
+        int total = 0;                   // cost of all units (the host has checked that it fits)
         Draft mine{0, 0, 0};             // of sequence b0 + lane
         for (int b0 = lane; b0 < a.B; b0 += 32) {
             mine = draft_of(a, b0);
-            total += tiles_of(mine);
+            total += cost_of(mine);
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
         total *= per;
-        // CTA i of N takes tiles [total i / N, total (i + 1) / N)
-        const long long most = (total + ATTN_TREE_MIN_TILES - 1) / ATTN_TREE_MIN_TILES;
-        const int N = static_cast<int>(most < gridDim.x ? most : gridDim.x);
-        const bool idle = static_cast<int>(blockIdx.x) >= N;
-        const long long lo = idle ? 0 : total * blockIdx.x / N, hi = idle ? 0 : total * (blockIdx.x + 1LL) / N;
-        // sequence that holds tile lo, and the first tile of that sequence's units
-        int b = 0;
-        long long base = 0;
+        // CTA i of N takes [total i / N, total (i + 1) / N) of the units' costs laid end to
+        // end; a unit's tiles come first in its share, so a cut in the rest falls between units
+        const int most = (total + kMinCost - 1) / kMinCost;
+        const int N = min(most, static_cast<int>(gridDim.x)), I = blockIdx.x;
+        const bool idle = I >= N;
+        const int each = total / N, odd = total % N;
+        const int lo = idle ? 0 : each * I + odd * I / N, hi = idle ? 0 : each * (I + 1) + odd * (I + 1) / N;
+        // sequence that holds position lo, and the first position of its units
+        int b = 0, base = 0;
         for (int b0 = 0; !idle && b0 < a.B; b0 += 32) {
             if (a.B > 32) mine = draft_of(a, min(b0 + lane, a.B - 1));
-            const long long t = b0 + lane < a.B ? static_cast<long long>(tiles_of(mine)) * per : 0;
-            long long sum = t;
+            const int t = b0 + lane < a.B ? cost_of(mine) * per : 0;
+            int sum = t;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+                const int y = __shfl_up_sync(0xffffffffu, sum, d);
                 if (lane >= d) sum += y;
             }
             const unsigned past = __ballot_sync(0xffffffffu, base + sum > lo);
@@ -241,9 +249,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             int issued = 0, requests = 0, k = 0;
             bool ok = true;
             int4 rec = make_int4(-1, 0, 0, 0), rec2 = make_int4(0, 0, 0, 0);
-            long long pos = lo;
             int nt = tiles_of(d);
-            int u = static_cast<int>((lo - base) / nt), j = static_cast<int>((lo - base) % nt);
+            int u = (lo - base) / cost_of(d), j = (lo - base) % cost_of(d);
+            int pos = lo;  // of tile j of unit u
+            auto next_unit = [&] {
+                pos += cost_of(d) - j;
+                j = 0;
+                if (++u == per) {
+                    u = 0;
+                    if (++b < a.B) {
+                        d = draft_of(a, b);
+                        nt = tiles_of(d);
+                    }
+                }
+            };
+            if (j >= nt) next_unit();
             while (ok) {
                 const int slot = k % kRing;
                 if (k >= kRing && !(ok = mbar_wait(&bars.run_empty[slot], ((k / kRing) - 1) & 1, &bars.abort))) break;
@@ -253,12 +273,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.bk = b * a.H_kv + u / pairs;
                     r.tile = 2 * (u % pairs);
                     r.j0 = j;
-                    r.n = static_cast<int>(min(static_cast<long long>(nt - j), hi - pos));
+                    r.n = min(nt - j, hi - pos);
                     r.slot = r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
                     r.L = d.L, r.nd = d.n, r.past = d.past;
                     if (j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w
                         const long long last = pos + nt - 1;
-                        rec = make_int4(r.bk, r.tile, b, static_cast<int>(((last + 1) * N - 1) / total));
+                        rec = make_int4(r.bk, r.tile, b, static_cast<int>(((last + 1) * N - 1) / total));  // its CTA
                         rec2 = make_int4(d.n, d.past, 0, 0);
                     }
                 }
@@ -302,16 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         load(jj, 1);
                     }
                 }
-                pos += r.n;
                 ++k;
-                j = 0;
-                if (r.j0 + r.n == nt && ++u == per) {
-                    u = 0;
-                    if (++b < a.B) {
-                        d = draft_of(a, b);
-                        nt = tiles_of(d);
-                    }
-                }
+                if (r.j0 + r.n == nt)
+                    next_unit();
+                else
+                    pos = hi;
             }
             if (ok) {  // no more work for the guard
                 *static_cast<volatile int *>(&bars.req[requests % kGuardRing].stage) = kEnd;
@@ -471,23 +486,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return;
             if (edge_of(r) < r.n) build_ancestors<64>(a, r.b, Draft{r.L, r.nd, r.past}, anc[k & 1], tid, join);
             if (!ok || (k >= 1 && !(ok = mbar_wait_warp<64>(&bars.q_free, (k - 1) & 1, &bars.abort)))) return;
-            // rows as a TMA load would leave them (128-byte swizzle); rows without a token are zeros
+            // rows as a TMA load would leave them (128-byte swizzle); rows without a token are
+            // zeros.  kChunks threads share a row; a thread's rows are kStep apart, so its place
+            // in the swizzle pattern of 8 rows takes 8 / kStep values in turn.
             constexpr int kChunks = D / 8, kStep = 64 / kChunks;  // 16-byte chunks of a row; rows a pass
             const int n_rows = (Single || r.tile + 1 >= row_tiles ? 1 : 2) * kM;
-            const int ch = tid % kChunks;
+            const int ch = tid % kChunks, r0 = tid / kChunks;
+            const int q0 = r.tile * kM + r0;
+            int t = q0 % a.T, left = rows - q0;
             const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + r.b * a.q_bs +
-                                     static_cast<long long>(r.bk - r.b * a.H_kv) * G * a.q_hs + ch * 8;
-            int q = r.tile * kM + tid / kChunks, h = q / a.T, t = q - h * a.T;
-            const uint32_t base = smem_u32(smem) + (ch / 8) * L::kBlock;
-#pragma unroll 4
-            for (int rr = tid / kChunks; rr < n_rows; rr += kStep) {
-                const bool in = q < rows && t < r.nd;
-                const int rt = rr % kM;
-                cp_async16(base + (rr / kM) * L::kTile + rt * 128 + (((ch & 7) ^ (rt & 7)) << 4),
-                           in ? Q + h * a.q_hs + t * a.q_ts : static_cast<const __nv_bfloat16 *>(a.q), in ? 16u : 0u);
-                q += kStep;
-                t += kStep;
-                while (t >= a.T) t -= a.T, ++h;
+                                     static_cast<long long>((r.bk - r.b * a.H_kv) * G + q0 / a.T) * a.q_hs + t * a.q_ts + ch * 8;
+            const long long step = kStep * a.q_ts, wrap = a.q_hs - a.T * a.q_ts;
+            uint32_t dst = smem_u32(smem) + (ch / 8) * L::kBlock + r0 * 128;
+            for (int rr = 0; rr < n_rows; rr += 8) {
+                if (rr == kM) dst += L::kTile - L::kBlock;
+#pragma unroll
+                for (int e = 0; e < 8; e += kStep) {
+                    const bool in = left > 0 && t < r.nd;
+                    cp_async16(dst + (((ch & 7) ^ ((r0 + e) & 7)) << 4), in ? Q : static_cast<const __nv_bfloat16 *>(a.q),
+                               in ? 16u : 0u);
+                    dst += kStep * 128;
+                    left -= kStep;
+                    t += kStep;
+                    Q += step;
+                    while (t >= a.T) t -= a.T, Q += wrap;
+                }
             }
             cp_async_wait_all();
             fence_proxy_async_shared();
@@ -759,27 +782,38 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
 }
 
 // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, M the largest m_c, the
-// parts added in order, for one row and 4 C columns: part(c) gives where part c
-// has the row's (m, l), and column(c, e) its e-th four columns.
+// parts added in order, for one row and 4 C columns: part(c) is the row's (m, l) in
+// part c, column(c, e) its e-th four columns.
 template <int C, typename T, typename Part, typename Column>
 __device__ __forceinline__ void merge_row(int n, bool live, T *out, Part part, Column column) {
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int c = 0; c < n; ++c) M = fmaxf(M, part(c).x);
-    const float ref = M == -INFINITY ? 0.f : M;
     float4 acc[C];
 #pragma unroll
     for (int e = 0; e < C; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-        const float2 x = part(c);
-        const float w = ex2_approx(x.x - ref);
-        sum = fmaf(w, x.y, sum);
+    float sum = 0.f, M = -INFINITY;
+    // kAhead parts are loaded before the first is used: few rows, so latency counts
+    constexpr int kAhead = 4;
+    for (int c0 = 0; c0 < n; c0 += kAhead) {
+        float2 x[kAhead];
+        float4 o[kAhead][C];
 #pragma unroll
-        for (int e = 0; e < C; ++e) {  // a part in which the row saw nothing holds zeros
-            const float4 o = column(c, e);
-            acc[e] = make_float4(fmaf(w, o.x, acc[e].x), fmaf(w, o.y, acc[e].y), fmaf(w, o.z, acc[e].z), fmaf(w, o.w, acc[e].w));
+        for (int y = 0; y < kAhead; ++y) {
+            const int c = min(c0 + y, n - 1);
+            x[y] = part(c);
+#pragma unroll
+            for (int e = 0; e < C; ++e) o[y][e] = column(c, e);
+        }
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            if (c0 + y >= n) break;
+            // relative to the running max; a part in which the row saw nothing holds zeros
+            const float mn = fmaxf(M, x[y].x), ref = mn == -INFINITY ? 0.f : mn;
+            const float old = ex2_approx(M - ref), w = ex2_approx(x[y].x - ref);
+            M = mn;
+            sum = sum * old + w * x[y].y;
+#pragma unroll
+            for (int e = 0; e < C; ++e)
+                acc[e] = make_float4(fmaf(w, o[y][e].x, acc[e].x * old), fmaf(w, o[y][e].y, acc[e].y * old),
+                                     fmaf(w, o[y][e].z, acc[e].z * old), fmaf(w, o[y][e].w, acc[e].w * old));
         }
     }
     const float inv = live ? 1.f / sum : 0.f;
@@ -878,8 +912,9 @@ int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int n_sm) {
 int tree_tc_grid(int B, int H, int H_kv, int T, int Skv, int n_sm) {
     const int row_tiles = ((H / H_kv) * T + kM - 1) / kM;
     const long long tiles = Skv > kN ? (static_cast<long long>(Skv) + kN - 1) / kN : 1;
-    const long long total = static_cast<long long>(B) * H_kv * ((row_tiles + 1) / 2) * tiles;
-    const long long most = (total + ATTN_TREE_MIN_TILES - 1) / ATTN_TREE_MIN_TILES;
+    const long long total = static_cast<long long>(B) * H_kv * ((row_tiles + 1) / 2) * (tiles + kUnitCost);
+    if (total * 2 >= (1LL << 31)) return -1;  // the kernel counts in 32 bits
+    const long long most = (total + kMinCost - 1) / kMinCost;
     return static_cast<int>(most < n_sm ? most : n_sm);
 }
 
