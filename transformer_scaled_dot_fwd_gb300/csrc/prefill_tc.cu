@@ -57,6 +57,7 @@
 #include "kernels.h"
 #include "prefill_sched.cuh"
 #include "ptx.cuh"
+#include "serving.cuh"
 
 #include <atomic>
 #include <mutex>
@@ -194,9 +195,6 @@ __device__ __forceinline__ bool take_item(Bars &bars, int k, Item *it) {
 __device__ __forceinline__ void release_item(Bars &bars, int k) {
     mbar_arrive(&bars.item_empty[k % kItemRing]);
 }
-
-// Any bf16 of the pair w infinite or NaN (exponent bits all ones)?
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
 
 template <int D, typename Args>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -513,20 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (stage < 0) break;
                 if (!mbar_wait_warp(&bars.kv_full[stage], parity, &bars.abort)) break;
                 const uint32_t tile = smem_u32(ring + stage * L::kTileBytes);
-                bool bad = false;
-#pragma unroll 8
-                for (int c = tid; c < L::kTileBytes / 16; c += 64) {  // 8 chunks a row, 128 rows a block
-                    const uint4 v = ld_shared_v4(tile + c * 16);
-                    if ((c >> 3) % kBN >= rows) {
-                        st_shared_v4(tile + c * 16, 0u, 0u, 0u, 0u);
-                    } else {
-                        const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
-                        if (n0 | n1 | n2 | n3) {
-                            bad = true;
-                            st_shared_v4(tile + c * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
-                        }
-                    }
-                }
+                const bool bad = clean_v_tile<L::kSub, kBN, 64>(tile, rows, tid);
                 if (bad) *static_cast<volatile int *>(&guard.spoiled[item]) = 1;
                 fence_proxy_async_shared();
                 mbar_arrive(&guard.clean[slot]);
@@ -559,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lim = a.causal ? min(it.Lb, i + it.off + 1) : it.Lb;  // keys [0, lim) visible
             }
             float m_run = -INFINITY, l = 0.f;
+            bool huge = false;
 
             for (int j = 0; j < n; ++j) {
                 if (!(ok = mbar_wait_warp<32>(&bars.s_full[x], sp, &bars.abort))) break;
@@ -617,13 +603,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m_tile = mraw == -INFINITY ? -INFINITY : mraw * sl2;
                 const float m_new = fmaxf(m_run, m_tile);
                 const bool grow = m_new > m_run + kRescaleLog2;
-                if (__any_sync(0xffffffffu, grow)) {
+                float mul = sl2;
+                if (__any_sync(0xffffffffu, grow || (kPacked && huge))) {
                     const float factor = grow ? ex2_approx(m_run - m_new) : 1.f;
                     if (grow) {
                         l *= factor;
                         m_run = m_new;
                     }
-                    if (j > 0) {  // O holds earlier tiles: bring it to the new max
+                    if constexpr (kPacked) {
+                        // s * mul - m in one rounding leaves the rounding of m behind, 2^-24 of it: a
+                        // common factor of the row's weights, until it overflows them.  For huge
+                        // scores round the product first, so that the maximum's exponent is 0.
+                        // (In this branch, which such rows take every time: a branch of its own
+                        // cost 3 % of a long prompt.)
+                        huge = __any_sync(0xffffffffu, fabsf(m_run) > kHugeLog2 && m_run != -INFINITY);
+                        if (huge) {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c) s[c] = f2u(__fmul_rn(u2f(s[c]), sl2));
+                            mul = 1.f;
+                        }
+                    }
+                    if (j > 0 && (!kPacked || __any_sync(0xffffffffu, grow))) {  // O holds earlier tiles: bring it to the new max
     #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
@@ -637,17 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float negm = m_run == -INFINITY ? 0.f : -m_run;
-                float mul = sl2;
-                if constexpr (kPacked) {
-                    // s * mul - m in one rounding leaves the rounding of m behind, 2^-24 of it: a
-                    // common factor of the row's weights, until it overflows them.  For huge
-                    // scores round the product first, so that the maximum's exponent is 0.
-                    if (__any_sync(0xffffffffu, negm < -kHugeLog2 || negm > kHugeLog2)) {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c) s[c] = f2u(__fmul_rn(u2f(s[c]), sl2));
-                        mul = 1.f;
-                    }
-                }
                 const uint64_t sl2x2 = f2_pack(mul, mul), negmx2 = f2_pack(negm, negm);
                 uint64_t l4[4] = {0, 0, 0, 0};  // packed partial row sums
                 // p = 2^(s*scale*log2e - m), packed into bf16 pairs over the S

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace attn {
 
@@ -102,6 +103,49 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t *w, int s) {
     const int i = s / 32, r = s % 32;
     const uint32_t lo = w[i], hi = i < 3 ? w[i + 1] : 0u;
     return __funnelshift_r(lo, hi, r);
+}
+
+// Any bf16 of the pair w infinite or NaN (exponent bits all ones)?
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
+
+// Clean the V tile at shared address `tile` (kSub blocks of kRows rows of 128
+// bytes) for an MMA: rows from `inside` on become zeros, non-finite elements of
+// the others too.  Returns whether this thread met one.  `Threads` threads share
+// the tile.  An exponent of all ones carries into the sign bit when one is added
+// to it, so three operations test a pair of bf16, and eight 16-byte loads are in
+// flight before the first test.
+template <int kSub, int kRows, int Threads>
+__device__ __forceinline__ bool clean_v_tile(uint32_t tile, int inside, int tid) {
+    constexpr int kChunks = kSub * kRows * 8, kBatch = 8;
+    static_assert(kChunks % (Threads * kBatch) == 0, "whole batches");
+    bool bad = false;
+#pragma unroll 1
+    for (int c0 = tid; c0 < kChunks; c0 += Threads * kBatch) {
+        uint4 v[kBatch];
+        uint32_t acc = 0;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[i] = ld_shared_v4(tile + (c0 + i * Threads) * 16);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            acc |= ((v[i].x & 0x7f807f80u) + 0x00800080u) | ((v[i].y & 0x7f807f80u) + 0x00800080u) |
+                   ((v[i].z & 0x7f807f80u) + 0x00800080u) | ((v[i].w & 0x7f807f80u) + 0x00800080u);
+        if (!(acc & 0x80008000u) && inside >= kRows) continue;
+        // read again, one chunk at a time: nothing stays live for a rare case
+#pragma unroll 1
+        for (int c = c0; c < c0 + kBatch * Threads; c += Threads) {
+            const uint4 v = ld_shared_v4(tile + c * 16);
+            if ((c >> 3) % kRows >= inside) {
+                st_shared_v4(tile + c * 16, 0u, 0u, 0u, 0u);
+                continue;
+            }
+            const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
+            if (n0 | n1 | n2 | n3) {
+                bad = true;
+                st_shared_v4(tile + c * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
+            }
+        }
+    }
+    return bad;
 }
 
 }  // namespace attn

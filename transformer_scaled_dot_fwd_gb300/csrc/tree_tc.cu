@@ -73,7 +73,6 @@ constexpr int kUnitCost = ATTN_TREE_UNIT_COST, kMinCost = ATTN_TREE_MIN_TILES;
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
 
 // A run of K/V tiles [j0, j0 + n) of one unit.
 struct Run {
@@ -530,20 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (stage < 0) break;
             if (!mbar_wait_warp(&bars.kv_full[stage], parity, &bars.abort)) break;
             const uint32_t tile = smem_u32(ring + stage * L::kTile);
-            bool bad = false;
-#pragma unroll 8
-            for (int c = tid; c < L::kTile / 16; c += 64) {  // 8 chunks a row, 128 rows a block
-                const uint4 v = ld_shared_v4(tile + c * 16);
-                if ((c >> 3) % kN >= inside) {
-                    st_shared_v4(tile + c * 16, 0u, 0u, 0u, 0u);
-                } else {
-                    const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
-                    if (n0 | n1 | n2 | n3) {
-                        bad = true;
-                        st_shared_v4(tile + c * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
-                    }
-                }
-            }
+            const bool bad = clean_v_tile<L::kSub, kN, 64>(tile, inside, tid);
             if (bad) *static_cast<volatile int *>(&bars.spoiled[run]) = 1;
             fence_proxy_async_shared();
             mbar_arrive(&bars.guard_clean[edges % kGuardRing]);  // edge tiles are counted by themselves
@@ -586,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the ancestor sets (and Q) of this run
             if (!(ok = mbar_wait_warp<32>(&bars.q_full[k & 1], (k >> 1) & 1, &bars.abort))) break;
             float m_run = -INFINITY, l = 0.f;
+            bool huge = sl2 == 0.f;
             for (int i = 0; i < n; ++i) {
                 const int j = one ? 2 * i + x : i;
                 if (!(ok = mbar_wait_warp<32>(&bars.s_full[x], sp, &bars.abort))) break;
@@ -616,13 +603,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float raw = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
                 const float m_new = fmaxf(m_run, raw == -INFINITY ? -INFINITY : raw * sl2);
                 const bool grow = m_new > m_run + kRescaleLog2;
-                if (__any_sync(0xffffffffu, grow)) {
+                float mul = sl2;
+                if (__any_sync(0xffffffffu, grow || huge)) {
                     const float factor = grow ? ex2_approx(m_run - m_new) : 1.f;
                     if (grow) {
                         l *= factor;
                         m_run = m_new;
                     }
-                    if (i > 0) {  // this stream's earlier P V are complete: S was issued after them
+                    // huge scores: round the product before the difference (as in prefill_tc.cu); a
+                    // scale of 0: a hidden key's -inf must not become NaN
+                    huge = sl2 == 0.f || __any_sync(0xffffffffu, fabsf(m_run) > kHugeLog2 && m_run != -INFINITY);
+                    if (huge) {
+                        const int at = at0 + j * kN;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t see = !masked ? 0xffffffffu : live ? visible32(set, at + 32 * c) : 0u;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[32 * c + e] = see >> e & 1u ? f2u(__fmul_rn(u2f(s[32 * c + e]), sl2)) : f2u(-INFINITY);
+                        }
+                        mul = 1.f;
+                    }
+                    if (i > 0 && __any_sync(0xffffffffu, grow)) {  // this stream's earlier P V are complete: S was issued after them
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
@@ -636,20 +638,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float negm = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: every p below is zero
-                float mul = sl2;
-                // huge scores: round the product before the difference (as in prefill_tc.cu); a
-                // scale of 0: a hidden key's -inf must not become NaN
-                if (__any_sync(0xffffffffu, negm < -kHugeLog2 || negm > kHugeLog2) || sl2 == 0.f) {
-                    const int at = at0 + j * kN;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t see = !masked ? 0xffffffffu : live ? visible32(set, at + 32 * c) : 0u;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            s[32 * c + e] = see >> e & 1u ? f2u(__fmul_rn(u2f(s[32 * c + e]), sl2)) : f2u(-INFINITY);
-                    }
-                    mul = 1.f;
-                }
                 const uint64_t mul2 = f2_pack(mul, mul), negm2 = f2_pack(negm, negm);
                 uint64_t l4[4] = {0, 0, 0, 0};
 #pragma unroll
