@@ -700,7 +700,6 @@ ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *
         return fail(ATTN_EINVAL, "%s: q, k, v and out must be 16-byte aligned", who);
     if ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(lse)) & 3u)
         return fail(ATTN_EINVAL, "%s: cu_seqlens and lse must be 4-byte aligned", who);
-    if (H > 65535) return fail(ATTN_EINVAL, "%s: H must be <= 65535", who);
     const long long esz = dtype == ATTN_BF16 ? 2 : 4;
     const void *ptrs[4] = {q, k, v, out};
     const int heads[4] = {H, H_kv, H_kv, H};
@@ -748,6 +747,8 @@ ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *
     a.v_ts = rows[2].so / esz, a.v_hs = rows[2].si / esz, a.o_ts = rows[3].so / esz, a.o_hs = rows[3].si / esz;
     cudaError_t e;
     if (dtype == ATTN_F32) {
+        if (packed_f32_blocks(T, n_seq) * H > 0x7fffffffLL)
+            return fail(ATTN_EINVAL, "%s: %d tokens in %d sequences of %d heads are too many", who, T, n_seq, H);
         e = launch_packed_f32(a);
     } else {
         const int unit = packed_unit_rows(H, H_kv);

@@ -70,6 +70,7 @@ cudaError_t launch_packed_tc(const PackedArgs &a, long long plan_tiles, const CU
                              const CUtensorMap &tv);
 // fp32 packed prefill on the CUDA cores (no workspace).
 cudaError_t launch_packed_f32(const PackedArgs &a);
+long long packed_f32_blocks(long long T, long long n_seq);  // of one head
 
 // A tree of T drafted tokens per sequence against a KV cache (attn_decode_tree).
 // Row r of key/value head g is query head g * G + r / T, token r % T.

@@ -1,21 +1,25 @@
 // fp32 attention over tiles on the CUDA cores (FFMA only, no TF32): packed
 // sequences (attn_fwd_packed) and trees of drafted tokens (attn_decode_tree).
 //
-// 32 query rows against tiles of 64 keys, online softmax in log2 units.  128
-// threads hold the 32 x 64 scores as 4 x 4 each (rows 4 ty + i, keys tx + 16 j)
-// and the 32 x D output as 4 rows x D / 16 columns each: a K or V element read
-// from shared memory serves 4 rows, a Q or P element 4 keys or D / 16 columns, so
-// the FMA pipe, not shared memory, is the bound.  The sixteen threads that
-// share rows are half a warp: row sums are four shuffles, and P goes through
-// shared memory without a block barrier.  K rows are padded by 16 bytes so that
-// sixteen lanes read sixteen rows without conflicts.  The next tile's K is
-// copied in (cp.async) while P V runs, its V while the scores are computed.
+// 32 query rows against tiles of 64 keys, online softmax in log2 units.  A group
+// of 128 threads holds the 32 x 64 scores as 4 x 4 each (rows 4 ty + i, keys tx +
+// 16 j) and the 32 x D output as 4 rows x D / 16 columns each: a K or V element
+// read from shared memory serves 4 rows, a Q or P element 4 keys or D / 16 columns,
+// so the FMA pipe, not shared memory, is the bound.  FMAs go in pairs (two depths
+// of a score, two columns of the output).  The sixteen threads that share rows are
+// half a warp: row sums are four shuffles.  K rows are padded by 16 bytes so that
+// sixteen lanes read sixteen rows without conflicts.  The next tile's K is copied in
+// (cp.async) while P V runs, its V while the scores are computed.
 //
-// Packed rows see keys [lo, hi) of the token axis.  A block's 32 rows may
-// belong to several sequences: those are neighbours, so the block walks the
-// keys from its first row's lo to its last row's hi and every row takes its own part.
-// Tree rows see [0, hi) and the draft keys in their ancestor set.  A key that a
-// row does not see contributes nothing whatever its row of V holds.
+// Few rows and long keys leave one warp per scheduler waiting on shared memory
+// and shuffles, so a block has two groups that take alternate key tiles of the
+// same rows and join their output, max and sum at the end.
+//
+// Packed rows: a block's 32 rows lie in one sequence (a block that straddled two
+// would walk the keys of both), found by a search, not a table: sequence s
+// owns the blocks from cu[s] / 32 + s on, a few of which stay empty.  Tree rows
+// see [0, hi) and the draft keys in their ancestor set.  A key that a row does
+// not see contributes nothing whatever its row of V holds.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "serving.cuh"
@@ -28,17 +32,20 @@ namespace {
 
 constexpr int kRows = 32;
 constexpr int kKeys = 64;
-constexpr int kThreads = 128;
+constexpr int kGroup = 128;      // threads of a group
+constexpr int kThreads = 2 * kGroup;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct F32Smem {
     float q[kRows][D + 4];
-    float k[kKeys][D + 4];
-    float v[kKeys][D];
-    float p[kRows][kKeys + 4];
-    int lo[kRows], hi[kRows];
+    struct {
+        float k[kKeys][D + 4];
+        float v[kKeys][D];       // after the walk: group 1's output, [kRows][D]
+        float p[kRows][kKeys + 4];
+    } g[2];
+    float2 ml[kRows];            // group 1's max and sum
     Ancestors anc;
 };
 
@@ -49,63 +56,68 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Running state of a thread's four rows.
+// Running state of a thread's four rows: columns 64 c + 4 tx + e, in pairs.
 template <int D>
 struct Rows4 {
     float m[4], l[4];
-    float o[4][D / 16];  // columns 64 c + 4 tx + e
+    uint64_t o[4][D / 32];
 };
 
-// All tiles of keys [k0, k1): K row j at kbase + j * ks, V row j at vbase + j * vs.
+// This group's tiles of keys [k0, k1): K row j at kbase + j * ks, V row j at vbase + j * vs.
 // visible(i, key0) gives the bits of keys key0 + tx + 16 j, j < 4, of row 4 ty + i.
 template <int D, typename Visible>
-__device__ __forceinline__ void walk(F32Smem<D> &sm, const float *kbase, long long ks, const float *vbase, long long vs,
-                                     int k0, int k1, float sl2, Rows4<D> &st, Visible visible) {
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+__device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long long ks, const float *vbase,
+                                     long long vs, int k0, int k1, float sl2, Rows4<D> &st, Visible visible) {
+    const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, tx = tid % 16, ty = tid / 16;
+    auto &sm = smem.g[group];
+    const auto sync = [&] { named_bar_sync(1 + group, kGroup); };
     constexpr int C = D / 64;
     auto load = [&](float *dst, int stride, const float *base, long long gs, int key0) {
         const uint32_t to = smem_u32(dst);
-        for (int i = tid; i < kKeys * D / 4; i += kThreads) {
+#pragma unroll 8
+        for (int i = tid; i < kKeys * D / 4; i += kGroup) {
             const int row = i / (D / 4), c = i % (D / 4);
             const bool in = key0 + row < k1;
             cp_async16(to + (row * stride + 4 * c) * 4, base + (in ? key0 + row : k0) * gs + 4 * c, in ? 16u : 0u);
         }
         cp_async_commit();
     };
-    load(&sm.k[0][0], D + 4, kbase, ks, k0);
-    load(&sm.v[0][0], D, vbase, vs, k0);
-    for (int key0 = k0; key0 < k1; key0 += kKeys) {
-        const bool more = key0 + kKeys < k1;
+    const int first = k0 + group * kKeys;
+    if (first < k1) {
+        load(&sm.k[0][0], D + 4, kbase, ks, first);
+        load(&sm.v[0][0], D, vbase, vs, first);
+    }
+    for (int key0 = first; key0 < k1; key0 += 2 * kKeys) {
+        const bool more = key0 + 2 * kKeys < k1;
         cp_async_wait<1>();  // K of this tile (V may still be on its way)
-        __syncthreads();
-        float s[4][4] = {};
+        sync();
+        uint64_t s2[4][4] = {};  // sums over even and over odd depths
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
-            float4 qa[4], kb[4];
+            ulonglong2 qa[4], kb[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const float4 *>(&sm.q[4 * ty + i][d]);
+            for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const ulonglong2 *>(&smem.q[4 * ty + i][d]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kb[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][d]);
+            for (int j = 0; j < 4; ++j) kb[j] = *reinterpret_cast<const ulonglong2 *>(&sm.k[tx + 16 * j][d]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(qa[i].x, kb[j].x, s[i][j]);
-                    s[i][j] = fmaf(qa[i].y, kb[j].y, s[i][j]);
-                    s[i][j] = fmaf(qa[i].z, kb[j].z, s[i][j]);
-                    s[i][j] = fmaf(qa[i].w, kb[j].w, s[i][j]);
+                    s2[i][j] = ffma2(qa[i].x, kb[j].x, s2[i][j]);
+                    s2[i][j] = ffma2(qa[i].y, kb[j].y, s2[i][j]);
                 }
         }
-        uint32_t hidden = 0;  // some row of the thread misses some key of the tile
+        bool hidden = false;  // a row of the thread misses a key of the tile (those past k1 are zeros)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t see = visible(i, key0);
-            hidden |= ~see & 15u;
-            float mt = -INFINITY;
+            float s[4], mt = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] = __fmul_rn(s[i][j], sl2);  // rounded before the difference below: huge scores
-                if (see >> j & 1u) mt = fmaxf(mt, s[i][j]);
+                // rounded before the difference below: huge scores
+                s[j] = __fmul_rn(f2_lo(s2[i][j]) + f2_hi(s2[i][j]), sl2);
+                hidden = hidden || (!(see >> j & 1u) && key0 + tx + 16 * j < k1);
+                if (see >> j & 1u) mt = fmaxf(mt, s[j]);
             }
 #pragma unroll
             for (int x = 1; x < 16; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
@@ -116,22 +128,21 @@ __device__ __forceinline__ void walk(F32Smem<D> &sm, const float *kbase, long lo
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p = see >> j & 1u ? ex2_approx(s[i][j] - ref) : 0.f;
+                const float p = see >> j & 1u ? ex2_approx(s[j] - ref) : 0.f;
                 sum += p;
                 sm.p[4 * ty + i][tx + 16 * j] = p;
             }
+            st.l[i] = st.l[i] * corr + sum;  // this thread's keys; summed over the half warp at the end
+            const uint64_t corr2 = f2_pack(corr, corr);
 #pragma unroll
-            for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            st.l[i] = st.l[i] * corr + sum;
-#pragma unroll
-            for (int e = 0; e < D / 16; ++e) st.o[i][e] *= corr;
+            for (int e = 0; e < D / 32; ++e) st.o[i][e] = fmul2(st.o[i][e], corr2);
         }
         // every row of the warp sees every key: plain FMAs; otherwise a weight
         // of zero must not meet an infinite or NaN value
-        const bool edge = __any_sync(0xffffffffu, hidden != 0u);
+        const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
-        __syncthreads();     // all scores are done with K; P is visible
-        if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + kKeys);
+        sync();              // all scores are done with K; P is visible
+        if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + 2 * kKeys);
         auto mix = [&](auto guarded) {
 #pragma unroll 2
             for (int j = 0; j < kKeys; j += 4) {
@@ -142,15 +153,15 @@ __device__ __forceinline__ void walk(F32Smem<D> &sm, const float *kbase, long lo
                 for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        const float4 x = *reinterpret_cast<const float4 *>(&sm.v[j + jj][64 * c + 4 * tx]);
-                        const float xv[4] = {x.x, x.y, x.z, x.w};
+                        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sm.v[j + jj][64 * c + 4 * tx]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float p = jj == 0 ? p4[i].x : jj == 1 ? p4[i].y : jj == 2 ? p4[i].z : p4[i].w;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float y = fmaf(p, xv[e], st.o[i][4 * c + e]);
-                                st.o[i][4 * c + e] = decltype(guarded)::value && p == 0.f ? st.o[i][4 * c + e] : y;
+                            const uint64_t p2 = f2_pack(p, p);
+                            const uint64_t a = ffma2(p2, x.x, st.o[i][2 * c]), b = ffma2(p2, x.y, st.o[i][2 * c + 1]);
+                            if (!decltype(guarded)::value || p != 0.f) {
+                                st.o[i][2 * c] = a;
+                                st.o[i][2 * c + 1] = b;
                             }
                         }
                     }
@@ -160,10 +171,14 @@ __device__ __forceinline__ void walk(F32Smem<D> &sm, const float *kbase, long lo
             mix(std::true_type{});
         else
             mix(std::false_type{});
-        __syncthreads();  // V and P are free
-        if (more) load(&sm.v[0][0], D, vbase, vs, key0 + kKeys);
+        sync();  // V and P are free
+        if (more) load(&sm.v[0][0], D, vbase, vs, key0 + 2 * kKeys);
     }
     cp_async_wait<0>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 1; x < 16; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
 }
 
 template <int D>
@@ -173,74 +188,115 @@ __device__ __forceinline__ void reset(Rows4<D> &st) {
         st.m[i] = -INFINITY;
         st.l[i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) st.o[i][e] = 0.f;
+        for (int e = 0; e < D / 32; ++e) st.o[i][e] = 0;
     }
+}
+
+// Group 1's part into group 0's registers (the whole block calls it; group 1's
+// own state is left as it was).
+template <int D>
+__device__ __forceinline__ void join_groups(F32Smem<D> &sm, Rows4<D> &st) {
+    const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, tx = tid % 16, ty = tid / 16;
+    float *po = &sm.g[1].v[0][0];
+    if (group == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (tx == 0) sm.ml[4 * ty + i] = make_float2(st.m[i], st.l[i]);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<ulonglong2 *>(po + (4 * ty + i) * D + 64 * c + 4 * tx) =
+                    make_ulonglong2(st.o[i][2 * c], st.o[i][2 * c + 1]);
+        }
+    }
+    __syncthreads();
+    if (group == 1) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = sm.ml[4 * ty + i];
+        const float mn = fmaxf(st.m[i], y.x), ref = mn == -INFINITY ? 0.f : mn;
+        const float w0 = ex2_approx(st.m[i] - ref), w1 = ex2_approx(y.x - ref);
+        st.m[i] = mn;
+        st.l[i] = st.l[i] * w0 + y.y * w1;
+        const uint64_t a = f2_pack(w0, w0), b = f2_pack(w1, w1);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(po + (4 * ty + i) * D + 64 * c + 4 * tx);
+            st.o[i][2 * c] = ffma2(x.x, b, fmul2(st.o[i][2 * c], a));
+            st.o[i][2 * c + 1] = ffma2(x.y, b, fmul2(st.o[i][2 * c + 1], a));
+        }
+    }
+}
+
+// Row i's columns from 64 c + 4 tx, times f.
+template <int D>
+__device__ __forceinline__ float4 columns(const Rows4<D> &st, int i, int c, float f) {
+    return make_float4(f2_lo(st.o[i][2 * c]) * f, f2_hi(st.o[i][2 * c]) * f, f2_lo(st.o[i][2 * c + 1]) * f,
+                       f2_hi(st.o[i][2 * c + 1]) * f);
 }
 
 // ------------------------------------------------------------ packed sequences
 
+// Number of sequences whose first block, cu[s] / kRows + s, is <= w (32 probes a step).
+__device__ __forceinline__ int blocks_le(const int32_t *cu, int n, int w, int T, int lane) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, at < hi && min(max(cu[at], 0), T) / kRows + at <= w);
+        const int c = le == 0xffffffffu ? 32 : __ffs(~le) - 1;
+        if (c == 0) break;
+        hi = min(hi, lo + c * step);
+        lo = lo + (c - 1) * step + 1;
+    }
+    return lo;
+}
+
+// Block (h, w): head h, 32 rows of the sequence that owns block w.
 template <int D>
 __global__ void __launch_bounds__(kThreads) packed_f32_kernel(const PackedArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
     F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    const int h = blockIdx.y, g = h / (a.H / a.H_kv);
-    const int t0 = static_cast<int>(gridDim.x - 1 - blockIdx.x) * kRows;
-    for (int r = tid / 32; r < kRows; r += kThreads / 32) {
-        const int t = t0 + r;
-        const int s = min(count_le(a.cu_seqlens + 1, a.B, t, tid % 32), a.B - 1);
-        if (tid % 32 == 0) {
-            const int lo = min(max(a.cu_seqlens[s], 0), a.Sq), end = min(max(a.cu_seqlens[s + 1], lo), a.Sq);
-            const bool live = t >= lo && t < end;
-            sm.lo[r] = live ? lo : 0;
-            sm.hi[r] = live ? (a.causal ? t + 1 : end) : 0;
-        }
-    }
+    const int tid = threadIdx.x, tx = tid % 16, ty = tid % kGroup / 16;
+    const int h = blockIdx.x % a.H, w = blockIdx.x / a.H, g = h / (a.H / a.H_kv);
+    const int s = blocks_le(a.cu_seqlens, a.B, w, a.Sq, tid % 32) - 1;
+    if (s < 0) return;
+    const int c0 = min(max(a.cu_seqlens[s], 0), a.Sq), c1 = min(max(a.cu_seqlens[s + 1], c0), a.Sq);
+    const int t0 = c0 + (w - c0 / kRows - s) * kRows;  // first row
+    if (t0 >= c1) return;                              // one of the empty blocks
+    const int end = min(t0 + kRows, c1);
     const float *Q = static_cast<const float *>(a.q) + h * a.q_hs;
     for (int i = tid; i < kRows * D / 4; i += kThreads) {
         const int r = i / (D / 4), c = i % (D / 4);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + r < a.Sq) x = *reinterpret_cast<const float4 *>(Q + (t0 + r) * a.q_ts + 4 * c);
+        if (t0 + r < end) x = *reinterpret_cast<const float4 *>(Q + (t0 + r) * a.q_ts + 4 * c);
         *reinterpret_cast<float4 *>(&sm.q[r][4 * c]) = x;
     }
     __syncthreads();
-    int k0 = 0x7fffffff, k1 = 0;
-    for (int r = 0; r < kRows; ++r)
-        if (sm.hi[r] > 0) {
-            k0 = min(k0, sm.lo[r]);
-            k1 = max(k1, sm.hi[r]);
-        }
-    if (k1 == 0) return;  // no token of a sequence here
-    int lo[4], hi[4];
+    const int k1 = a.causal ? end : c1;
+    int hi[4];  // rows see keys [c0, hi)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo[i] = sm.lo[4 * ty + i];
-        hi[i] = sm.hi[4 * ty + i];
-    }
+    for (int i = 0; i < 4; ++i) hi[i] = a.causal ? min(t0 + 4 * ty + i + 1, k1) : k1;
     Rows4<D> st;
     reset(st);
     walk<D>(sm, static_cast<const float *>(a.k) + g * a.k_hs, a.k_ts, static_cast<const float *>(a.v) + g * a.v_hs,
-            a.v_ts, k0, k1, a.scale * kLog2e, st, [&](int i, int key0) {
+            a.v_ts, c0, k1, a.scale * kLog2e, st, [&](int i, int key0) {
                 uint32_t see = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = key0 + tx + 16 * j;
-                    see |= (key >= lo[i] && key < hi[i] ? 1u : 0u) << j;
-                }
+                for (int j = 0; j < 4; ++j) see |= (key0 + tx + 16 * j < hi[i] ? 1u : 0u) << j;
                 return see;
             });
+    join_groups(sm, st);
+    if (tid >= kGroup) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (hi[i] == 0) continue;
         const long long t = t0 + 4 * ty + i;
+        if (t >= end) break;
         const float inv = 1.f / st.l[i];
         float *O = static_cast<float *>(a.out) + t * a.o_ts + h * a.o_hs;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-            *reinterpret_cast<float4 *>(O + 64 * c + 4 * tx) = make_float4(
-                st.o[i][4 * c] * inv, st.o[i][4 * c + 1] * inv, st.o[i][4 * c + 2] * inv, st.o[i][4 * c + 3] * inv);
+        for (int c = 0; c < D / 64; ++c) *reinterpret_cast<float4 *>(O + 64 * c + 4 * tx) = columns(st, i, c, inv);
         if (a.lse && tx == 0) a.lse[t * a.H + h] = (st.m[i] + log2f(st.l[i])) * kLn2;
     }
 }
@@ -251,8 +307,8 @@ cudaError_t launch_packed_f32_t(const PackedArgs &a) {
     cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((a.Sq + kRows - 1) / kRows), static_cast<unsigned>(a.H));
-    return launch_pdl(packed_f32_kernel<D>, grid, dim3(kThreads), smem, a.stream, a);
+    const unsigned grid = static_cast<unsigned>(packed_f32_blocks(a.Sq, a.B) * a.H);
+    return launch_pdl(packed_f32_kernel<D>, dim3(grid), dim3(kThreads), smem, a.stream, a);
 }
 
 // ------------------------------------------------------------ trees of drafted tokens
@@ -264,14 +320,14 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
     F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    const int tid = threadIdx.x, tx = tid % 16, ty = tid % kGroup / 16;
     const int m = blockIdx.x % row_tiles, c = (blockIdx.x / row_tiles) % a.n_split;
     const int bk = blockIdx.x / row_tiles / a.n_split, b = bk / a.H_kv, g = bk % a.H_kv;
     const int G = a.H / a.H_kv, rows = G * a.T, r0 = m * kRows;
     const Draft d = draft_of(a, b);
     const int k0 = c * a.chunk, k1 = min(k0 + a.chunk, d.L);
     if (k0 >= k1 && a.n_split > 1) return;  // the merge never reads this split
-    build_ancestors<kThreads>(a, b, d, sm.anc, tid, [] { __syncthreads(); });
+    if (tid < kGroup) build_ancestors<kGroup>(a, b, d, sm.anc, tid, [] { named_bar_sync(1, kGroup); });
     for (int i = tid; i < kRows * D / 4; i += kThreads) {
         const int r = r0 + i / (D / 4), col = 4 * (i % (D / 4));
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -290,9 +346,9 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
     }
     Rows4<D> st;
     reset(st);
+    __syncthreads();
     const size_t head = static_cast<size_t>(bk) * a.Skv * D;
     if (k0 < k1) {
-        __syncthreads();
         walk<D>(sm, static_cast<const float *>(a.k) + head, D, static_cast<const float *>(a.v) + head, D, k0, k1,
                 a.scale * kLog2e, st, [&](int i, int key0) {
                     uint32_t see = 0;
@@ -302,6 +358,8 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
                     return live[i] ? see : 0u;
                 });
     }
+    join_groups(sm, st);
+    if (tid >= kGroup) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + 4 * ty + i;
@@ -317,9 +375,7 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
             if (tx == 0) *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(st.m[i], st.l[i]);
         }
 #pragma unroll
-        for (int cc = 0; cc < D / 64; ++cc)
-            *reinterpret_cast<float4 *>(O + 64 * cc + 4 * tx) =
-                make_float4(st.o[i][4 * cc] * f, st.o[i][4 * cc + 1] * f, st.o[i][4 * cc + 2] * f, st.o[i][4 * cc + 3] * f);
+        for (int cc = 0; cc < D / 64; ++cc) *reinterpret_cast<float4 *>(O + 64 * cc + 4 * tx) = columns(st, i, cc, f);
     }
 }
 
@@ -337,6 +393,8 @@ cudaError_t launch_tree_f32_t(const TreeArgs &a) {
 }
 
 }  // namespace
+
+long long packed_f32_blocks(long long T, long long n_seq) { return T / kRows + n_seq; }
 
 cudaError_t launch_packed_f32(const PackedArgs &a) {
     return a.D == 64 ? launch_packed_f32_t<64>(a) : launch_packed_f32_t<128>(a);
