@@ -14,6 +14,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 from typing import Optional
 
 ATTN_F32 = 0
@@ -353,9 +354,33 @@ def _elsewhere(device, stream):
 
 def _raw_stream(device):
     """cudaStream_t of the device's current stream."""
-    torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # spares building a Stream object
-    return get(device.index) if get is not None else torch.cuda.current_stream(device).cuda_stream
+    try:
+        return _torch()._C._cuda_getCurrentRawStream(device.index)  # spares building a Stream object
+    except AttributeError:
+        return _torch().cuda.current_stream(device).cuda_stream
+
+
+class _Workspace:
+    """``nbytes`` of device memory for one call on the current device's ``stream``,
+    from torch's caching allocator (its private pool during a graph capture): given
+    back when the call is enqueued, which is safe because the allocator reuses it
+    in stream order.  The raw calls cost 1 us where an empty tensor costs 4."""
+    __slots__ = ("ptr", "free")
+
+    def __init__(self, nbytes, stream):
+        c = _torch()._C
+        self.ptr = self.free = None
+        if nbytes > 0:
+            try:
+                self.ptr, self.free = c._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream), \
+                    c._cuda_cudaCachingAllocator_raw_delete
+            except AttributeError:
+                keep = _torch().empty(nbytes, dtype=_torch().uint8, device="cuda")
+                self.ptr, self.free = keep.data_ptr(), lambda _, keep=keep: None
+
+    def release(self):
+        if self.ptr is not None:
+            self.free(self.ptr)
 
 
 def _rows(name, t, T, D, dtype, device):
@@ -412,7 +437,8 @@ def _freqs_arg(freqs, D):
     return freqs.data_ptr(), 2 * freqs.shape[0]
 
 
-_LL6, _LL8, _LL10 = (ctypes.c_longlong * n for n in (6, 8, 10))
+# host int64 arrays of strides (a bytes object serves as the pointer)
+_LL6, _LL8, _LL10 = (struct.Struct(f"{n}q").pack for n in (6, 8, 10))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -460,12 +486,16 @@ def attn_fwd_packed(q, k, v, cu_seqlens, out=None, lse=None, scale: Optional[flo
     elif not (lse.dtype == torch.float32 and lse.shape == (T, H) and lse.is_contiguous() and lse.device == device):
         raise ValueError("lse must be a contiguous float32 (T, H) tensor on q's device")
     need = _packed_workspace(T, n_seq, H, H_kv, code)
-    ws = torch.empty(need, dtype=torch.uint8, device=device).data_ptr() if need > 0 else None
-    rc = lib().attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                               None if lse is None else lse.data_ptr(), T, H, H_kv, D,
-                               _LL8(sq[0], sq[1], kt, kh, vt, vh, ot, oh), cu, n_seq,
-                               1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, code, ws, need,
-                               _raw_stream(device))
+    stream = _raw_stream(device)
+    ws = _Workspace(need, stream)
+    try:
+        rc = lib().attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                   None if lse is None else lse.data_ptr(), T, H, H_kv, D,
+                                   _LL8(sq[0], sq[1], kt, kh, vt, vh, ot, oh), cu, n_seq,
+                                   1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, code, ws.ptr,
+                                   need, stream)
+    finally:
+        ws.release()
     if rc:
         _check(rc)
     return out if lse is None else (out, lse)
@@ -493,18 +523,21 @@ def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None,
     par = _ints("parents", parents, (T,) if one else (B, T), device)
     cl = _ints("cache_len", cache_len, (B,), device)
     dl = _ints("draft_len", draft_len, (B,), device)
-    torch = _torch()
     if out is None:
-        out = torch.empty_like(q)
+        out = _torch().empty_like(q)
     so = out.stride()
     if out.shape != q.shape or out.dtype != q.dtype or out.device != device or so[3] != 1:
         raise ValueError("out must match q's shape, dtype and device, with contiguous rows")
     need = _tree_workspace(B, H, H_kv, T, Skv, D, code, device.index) if B and 0 < T <= 128 else 0
-    ws = torch.empty(need, dtype=torch.uint8, device=device).data_ptr() if need > 0 else None
-    rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), out.data_ptr(), B, H, H_kv, T,
-                                Skv, D, _LL6(sq[0], sq[1], sq[2], so[0], so[1], so[2]), par, 0 if one else T, cl, dl,
-                                1.0 / math.sqrt(D) if scale is None else scale, code, ws, need if need > 0 else 0,
-                                _raw_stream(device))
+    stream = _raw_stream(device)
+    ws = _Workspace(need, stream)
+    try:
+        rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), out.data_ptr(), B, H, H_kv, T,
+                                    Skv, D, _LL6(sq[0], sq[1], sq[2], so[0], so[1], so[2]), par, 0 if one else T, cl,
+                                    dl, 1.0 / math.sqrt(D) if scale is None else scale, code, ws.ptr,
+                                    need if need > 0 else 0, stream)
+    finally:
+        ws.release()
     if rc:
         _check(rc)
     return out

@@ -185,7 +185,7 @@ cudaError_t launch_decode_tc(const DecodeArgs &a, const CUtensorMap &tq, const C
 
 // Rotary positions (attn_rope, attn_rope_append).  Rows are (token, head) with
 // element strides; kcache == nullptr: no append.
-constexpr int kRopeMaxTokens = 8;  // tokens a block takes at most
+constexpr int kRopeMaxTokens = 2;  // tokens a block takes at most
 struct RopeArgs {
     const void *q, *k, *v;      // (T, H | H_kv, D); v only with a cache
     void *q_out, *k_out;        // k_out may be nullptr with a cache
