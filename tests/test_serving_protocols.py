@@ -228,7 +228,7 @@ def tree_run(runs, stages, seed, mistake=None):
     """runs: (n tiles, first edge tile, one row tile?) per unit run of a CTA."""
     sc = Sched(seed)
     run_full, run_empty = [Bar() for _ in range(RING)], [Bar(3) for _ in range(RING)]
-    q_full, q_free = [Bar(2), Bar(2)], Bar()
+    q_full, q_free, q_first = [Bar(2), Bar(2)], Bar(), Bar(2)
     kv_full, kv_empty = [Bar() for _ in range(stages)], [Bar() for _ in range(stages)]
     s_full, p_ready, o_full = [Bar(), Bar()], [Bar(), Bar()], [Bar(), Bar()]
     g_full, g_clean = [Bar() for _ in range(TREE_REQS)], [Bar(2) for _ in range(TREE_REQS)]
@@ -263,7 +263,9 @@ def tree_run(runs, stages, seed, mistake=None):
             request((-2, 0, k))
             order = [(0, 0), (1, 0)] + [x for j in range(n) for x in ((j, 1), (j + 2, 0))] if one else [
                 x for j in range(n) for x in ((j, 0), (j, 1))]
-            for j, kv in order:
+            for i, (j, kv) in enumerate(order):
+                if i == 1 and k == 0:
+                    yield wait(q_first, 0)
                 if j >= n:
                     continue
                 s = issued % stages
@@ -291,10 +293,11 @@ def tree_run(runs, stages, seed, mistake=None):
                 if k >= 2:
                     yield wait(run_empty[(k - 2) % RING], (k - 2) // RING)
                 set_owner[k & 1] = k
-                if k >= 1 and mistake != "no_q_free":
-                    yield wait(q_free, k - 1)
-                staged[k] = staged.get(k, 0) + 1
-                q_owner[0] = k if staged[k] == 2 else None
+                if k >= 1:
+                    if mistake != "no_q_free":
+                        yield wait(q_free, k - 1)
+                    staged[k] = staged.get(k, 0) + 1
+                    q_owner[0] = k if staged[k] == 2 else None
                 q_full[k & 1].arrive()
             else:
                 yield wait_parity(kv_full[s], phase)
@@ -343,7 +346,7 @@ def tree_run(runs, stages, seed, mistake=None):
             run_empty[k % RING].arrive()
             if n < 0:
                 return
-            yield wait(q_full[k & 1], k >> 1)
+            yield wait(*((q_first, 0) if k == 0 else (q_full[k & 1], k >> 1)))
             left = [(2 * n if not one else n)]  # S MMAs of the run still to issue
             if one:
                 for x in range(min(2, n)):
@@ -398,6 +401,10 @@ def tree_run(runs, stages, seed, mistake=None):
             n, edge, one = r
             if n < 0:
                 return
+            if k == 0:
+                staged[0] = staged.get(0, 0) + 1
+                q_owner[0] = 0 if staged[0] == 2 else None
+                q_first.arrive()
             yield wait(q_full[k & 1], k >> 1)
             for _ in range((n - x + 1) // 2 if one else n):
                 yield wait(s_full[x], sp)

@@ -41,7 +41,7 @@ __device__ __forceinline__ Draft draft_of(const TreeArgs &a, int b) {
 // ancestors, as far as they have a cache row.  `Threads` threads call it
 // together, `sync` joins them.  The parent relation is closed by doubling: after
 // round i a set holds the 2^i nearest ancestors.
-struct Ancestors {
+struct alignas(16) Ancestors {
     uint32_t bits[kTreeMaxTokens][4];
     int jump[kTreeMaxTokens];
 };

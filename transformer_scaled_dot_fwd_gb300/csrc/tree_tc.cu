@@ -36,7 +36,7 @@
 // Roles (12 warps): warp 0 walks the CTA's run and loads K_j, V_j through a ring
 // of 128-row TMA tiles, warp 1 allocates TMEM and issues the MMAs, warps 2-3
 // stage the next unit's Q and ancestor sets while the streams finish the last
-// one, and guard, warps 4-7 and 8-11 are the streams (softmax, epilogue; thread =
+// one (the streams stage the first), and guard, warps 4-7 and 8-11 are the streams (softmax, epilogue; thread =
 // row = TMEM lane).
 #include "kernels.h"
 #include "ptx.cuh"
@@ -66,7 +66,7 @@ constexpr float kHugeLog2 = 16777216.0f;  // 2^24
 #endif
 // What a unit costs beside its tiles, in tiles: start, epilogue, merge.
 #ifndef ATTN_TREE_UNIT_COST
-#define ATTN_TREE_UNIT_COST 2
+#define ATTN_TREE_UNIT_COST 5
 #endif
 
 constexpr int kUnitCost = ATTN_TREE_UNIT_COST, kMinCost = ATTN_TREE_MIN_TILES;
@@ -113,12 +113,13 @@ struct Layout {
 
 struct Bars {
     uint64_t q_full[2];         // Q and ancestor sets of run k staged: [k & 1]
+    uint64_t q_first;           // Q of run 0 staged, by the streams
     uint64_t q_free;            // a run's last S MMA is complete
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2], p_ready[2], o_full[2];
     uint64_t run_full[kRing], run_empty[kRing];
     uint64_t guard_full[kGuardRing], guard_clean[kGuardRing];
-    uint64_t join, guard_join;  // both streams, both guard warps (barriers with a limit)
+    uint64_t join;              // both streams (a barrier with a limit)
     uint64_t mma_done;
     Run run[kRing];
     GuardReq req[kGuardRing];
@@ -147,6 +148,39 @@ __device__ __forceinline__ bool take_run(Bars &bars, int k, Run *r) {
 // part of, or that runs past the end.
 __device__ __forceinline__ int edge_of(const Run &r) { return min(r.n, max(0, max(0, r.past) / kN - r.j0)); }
 
+// Q rows of a run's row tiles into shared memory at `dst`, as a TMA load would
+// leave them (128-byte swizzle); rows without a token are zeros.  D / 8 threads
+// share a row; a thread's rows are kStep apart, so its place in the swizzle
+// pattern of 8 rows takes 8 / kStep values in turn (one, if kStep >= 8).
+template <int D, int Threads>
+__device__ __forceinline__ void stage_q(const TreeArgs &a, const Run &r, int tiles, uint32_t dst, int tid) {
+    constexpr int kBlock = 128 * 128, kTile = D / 64 * kBlock;
+    constexpr int kChunks = D / 8, kStep = Threads / kChunks;  // 16-byte chunks of a row; rows a pass
+    constexpr int kPass = kStep < 8 ? 8 : kStep;               // rows of the inner loop
+    const int G = a.H / a.H_kv, ch = tid % kChunks, r0 = tid / kChunks, q0 = r.tile * kM + r0;
+    int t = q0 % a.T, left = G * a.T - q0;
+    const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + r.b * a.q_bs +
+                             static_cast<long long>((r.bk - r.b * a.H_kv) * G + q0 / a.T) * a.q_hs + t * a.q_ts + ch * 8;
+    const long long step = kStep * a.q_ts, wrap = a.q_hs - a.T * a.q_ts;
+    dst += (ch / 8) * kBlock + r0 * 128;
+    for (int rr = 0; rr < tiles * kM; rr += kPass) {
+        if (rr == kM) dst += kTile - kBlock;
+#pragma unroll
+        for (int e = 0; e < kPass; e += kStep) {
+            const bool in = left > 0 && t < r.nd;
+            cp_async16(dst + (((ch & 7) ^ ((r0 + e) & 7)) << 4), in ? Q : static_cast<const __nv_bfloat16 *>(a.q),
+                       in ? 16u : 0u);
+            dst += kStep * 128;
+            left -= kStep;
+            t += kStep;
+            Q += step;
+            while (t >= a.T) t -= a.T, Q += wrap;
+        }
+    }
+    cp_async_wait_all();
+    fence_proxy_async_shared();
+}
+
 template <int D, bool Single>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const TreeArgs a, const int row_tiles, const __grid_constant__ CUtensorMap tk,
@@ -167,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
         for (int x = 0; x < 2; ++x) mbar_init(&bars.q_full[x], 64);
+        mbar_init(&bars.q_first, 256);
         mbar_init(&bars.q_free, 1);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars.kv_full[s], 1);
@@ -186,7 +221,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars.guard_clean[s], 64);
         }
         mbar_init(&bars.join, 256);
-        mbar_init(&bars.guard_join, 64);
         mbar_init(&bars.mma_done, 1);
         bars.abort = 0;
         fence_mbar_init();
@@ -308,8 +342,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kv && jj >= edge) request(s, (issued / kStages) & 1, r.L - (r.j0 + jj) * kN);
                     ++issued;
                 };
+                // at the start Q goes before all but the first K on the way from memory
+                auto q_before = [&] {
+                    if (k == 0 && ok) ok = mbar_wait(&bars.q_first, 0, &bars.abort);
+                };
                 if (Single || r.tile + 1 >= row_tiles) {  // one row tile: K0 K1 | V0 K2 | V1 K3 | ...
                     load(0, 0);
+                    q_before();
                     load(1, 0);
                     for (int jj = 0; jj < r.n && ok; ++jj) {
                         load(jj, 1);
@@ -318,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     for (int jj = 0; jj < r.n && ok; ++jj) {
                         load(jj, 0);
+                        if (jj == 0) q_before();
                         load(jj, 1);
                     }
                 }
@@ -383,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n < 0) break;
             const int edge = __shfl_sync(0xffffffffu, edge_of(r), 0);
             const bool one = Single || __shfl_sync(0xffffffffu, r.tile, 0) + 1 >= row_tiles;
-            if (!(ok = mbar_wait_warp(&bars.q_full[k & 1], (k >> 1) & 1, &bars.abort))) break;
+            if (!(ok = mbar_wait_warp(k == 0 ? &bars.q_first : &bars.q_full[k & 1], (k >> 1) & 1, &bars.abort))) break;
             int ks = 0, vs = 0;
             if (one) {
                 // stream x = tile & 1, both on Q buffer 0
@@ -471,48 +511,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kRegsOther>();
         const int tid = threadIdx.x - 64;
         bool ok = true;
-        uint32_t joins = 0;
-        auto join = [&] {  // both warps, or the abort flag
-            mbar_arrive(&bars.guard_join);
-            ok = mbar_wait_warp(&bars.guard_join, joins & 1, &bars.abort) && ok;
-            ++joins;
-        };
         // Run k, in ring slot `slot`.  Its set buffer was last read by run k - 2, its Q
         // buffers by the S MMAs of run k - 1.
         auto stage_run = [&](int k, int slot) {
             const Run r = read_run(bars, slot);
             if (k >= 2 && !(ok = mbar_wait_warp<64>(&bars.run_empty[(k - 2) % kRing], ((k - 2) / kRing) & 1, &bars.abort)))
                 return;
-            if (edge_of(r) < r.n) build_ancestors<64>(a, r.b, Draft{r.L, r.nd, r.past}, anc[k & 1], tid, join);
-            if (!ok || (k >= 1 && !(ok = mbar_wait_warp<64>(&bars.q_free, (k - 1) & 1, &bars.abort)))) return;
-            // rows as a TMA load would leave them (128-byte swizzle); rows without a token are
-            // zeros.  kChunks threads share a row; a thread's rows are kStep apart, so its place
-            // in the swizzle pattern of 8 rows takes 8 / kStep values in turn.
-            constexpr int kChunks = D / 8, kStep = 64 / kChunks;  // 16-byte chunks of a row; rows a pass
-            const int n_rows = (Single || r.tile + 1 >= row_tiles ? 1 : 2) * kM;
-            const int ch = tid % kChunks, r0 = tid / kChunks;
-            const int q0 = r.tile * kM + r0;
-            int t = q0 % a.T, left = rows - q0;
-            const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + r.b * a.q_bs +
-                                     static_cast<long long>((r.bk - r.b * a.H_kv) * G + q0 / a.T) * a.q_hs + t * a.q_ts + ch * 8;
-            const long long step = kStep * a.q_ts, wrap = a.q_hs - a.T * a.q_ts;
-            uint32_t dst = smem_u32(smem) + (ch / 8) * L::kBlock + r0 * 128;
-            for (int rr = 0; rr < n_rows; rr += 8) {
-                if (rr == kM) dst += L::kTile - L::kBlock;
-#pragma unroll
-                for (int e = 0; e < 8; e += kStep) {
-                    const bool in = left > 0 && t < r.nd;
-                    cp_async16(dst + (((ch & 7) ^ ((r0 + e) & 7)) << 4), in ? Q : static_cast<const __nv_bfloat16 *>(a.q),
-                               in ? 16u : 0u);
-                    dst += kStep * 128;
-                    left -= kStep;
-                    t += kStep;
-                    Q += step;
-                    while (t >= a.T) t -= a.T, Q += wrap;
-                }
+            // warp 2 alone closes the sets: a warp's barrier is cheaper than one of two warps
+            if (warp == 2 && edge_of(r) < r.n)
+                build_ancestors<32>(a, r.b, Draft{r.L, r.nd, r.past}, anc[k & 1], lane, [] { __syncwarp(); });
+            if (k >= 1) {
+                if (!(ok = mbar_wait_warp<64>(&bars.q_free, (k - 1) & 1, &bars.abort))) return;
+                stage_q<D, 64>(a, r, Single || r.tile + 1 >= row_tiles ? 1 : 2, smem_u32(smem), tid);
             }
-            cp_async_wait_all();
-            fence_proxy_async_shared();
             mbar_arrive(&bars.q_full[k & 1]);
         };
         for (int q = 0, k = 0, edges = 0; ok; ++q) {
@@ -568,6 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 set = anc[k & 1].bits[t];
                 n = one ? (r.n - x + 1) / 2 : r.n;
                 at0 = r.j0 * kN - r.past;
+                if (k == 0) {  // nothing else to do yet
+                    stage_q<D, 256>(a, r, one ? 1 : 2, smem_u32(smem), threadIdx.x - 128);
+                    mbar_arrive(&bars.q_first);
+                }
             }
             // the ancestor sets (and Q) of this run
             if (!(ok = mbar_wait_warp<32>(&bars.q_full[k & 1], (k >> 1) & 1, &bars.abort))) break;
