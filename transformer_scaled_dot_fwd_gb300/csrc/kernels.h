@@ -96,7 +96,7 @@ struct TreeArgs {
     int n_sm;
 };
 // fp32: keys per split for these sizes.
-int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int n_sm);
+int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int D, int n_sm);
 // bf16: CTAs for these sizes (-1: too large), and rows of a workspace slot.
 int tree_tc_grid(int B, int H, int H_kv, int T, int Skv, int n_sm);
 int tree_tc_slot_rows(int H, int H_kv, int T);

@@ -12,8 +12,12 @@
 // (cp.async) while P V runs, its V while the scores are computed.
 //
 // Few rows and long keys leave one warp per scheduler waiting on shared memory
-// and shuffles, so a block has two groups that take alternate key tiles of the
-// same rows and join their output, max and sum at the end.
+// and shuffles, so a block has several groups that take the key tiles of the same
+// rows in turn and join their output, max and sum at the end: as many as shared
+// memory holds, which also means one block an SM, so that a block left over goes
+// to the SM that is done first and not beside a long one (six sequences of 700 to 1
+// tokens, 4 heads of depth 64: one group 90 us, two groups and two blocks an SM
+// 47 us).
 //
 // Packed rows: a block's 32 rows lie in one sequence (a block that straddled two
 // would walk the keys of both), found by a search, not a table: sequence s
@@ -33,7 +37,10 @@ namespace {
 constexpr int kRows = 32;
 constexpr int kKeys = 64;
 constexpr int kGroup = 128;      // threads of a group
-constexpr int kThreads = 2 * kGroup;
+template <int D>
+constexpr int kGroups = D == 64 ? 4 : 2;
+template <int D>
+constexpr int kThreads = kGroups<D> * kGroup;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -42,10 +49,10 @@ struct F32Smem {
     float q[kRows][D + 4];
     struct {
         float k[kKeys][D + 4];
-        float v[kKeys][D];       // after the walk: group 1's output, [kRows][D]
+        float v[kKeys][D];       // after the walk: the group's output, [kRows][D]
         float p[kRows][kKeys + 4];
-    } g[2];
-    float2 ml[kRows];            // group 1's max and sum
+    } g[kGroups<D>];
+    float2 ml[kGroups<D>][kRows];  // each group's max and sum
     Ancestors anc;
 };
 
@@ -63,7 +70,8 @@ struct Rows4 {
     uint64_t o[4][D / 32];
 };
 
-// This group's tiles of keys [k0, k1): K row j at kbase + j * ks, V row j at vbase + j * vs.
+// This group's tiles of keys [k0, k1) (the whole block calls it, with the copies of
+// Q committed as one group): K row j at kbase + j * ks, V row j at vbase + j * vs.
 // visible(i, key0) gives the bits of keys key0 + tx + 16 j, j < 4, of row 4 ty + i.
 template <int D, typename Visible>
 __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long long ks, const float *vbase,
@@ -86,9 +94,14 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
     if (first < k1) {
         load(&sm.k[0][0], D + 4, kbase, ks, first);
         load(&sm.v[0][0], D, vbase, vs, first);
+        cp_async_wait<2>();  // Q, copied in before by all groups
+    } else {
+        cp_async_wait<0>();
     }
-    for (int key0 = first; key0 < k1; key0 += 2 * kKeys) {
-        const bool more = key0 + 2 * kKeys < k1;
+    __syncthreads();
+    constexpr int kStride = kGroups<D> * kKeys;
+    for (int key0 = first; key0 < k1; key0 += kStride) {
+        const bool more = key0 + kStride < k1;
         cp_async_wait<1>();  // K of this tile (V may still be on its way)
         sync();
         uint64_t s2[4][4] = {};  // sums over even and over odd depths
@@ -142,7 +155,7 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
         const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
         sync();              // all scores are done with K; P is visible
-        if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + 2 * kKeys);
+        if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + kStride);
         auto mix = [&](auto guarded) {
 #pragma unroll 2
             for (int j = 0; j < kKeys; j += 4) {
@@ -172,7 +185,7 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
         else
             mix(std::false_type{});
         sync();  // V and P are free
-        if (more) load(&sm.v[0][0], D, vbase, vs, key0 + 2 * kKeys);
+        if (more) load(&sm.v[0][0], D, vbase, vs, key0 + kStride);
     }
     cp_async_wait<0>();
 #pragma unroll
@@ -192,16 +205,16 @@ __device__ __forceinline__ void reset(Rows4<D> &st) {
     }
 }
 
-// Group 1's part into group 0's registers (the whole block calls it; group 1's
-// own state is left as it was).
+// The other groups' parts into group 0's registers, in order (the whole block
+// calls it; the others' own state is left as it was).
 template <int D>
 __device__ __forceinline__ void join_groups(F32Smem<D> &sm, Rows4<D> &st) {
     const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, tx = tid % 16, ty = tid / 16;
-    float *po = &sm.g[1].v[0][0];
-    if (group == 1) {
+    if (group > 0) {
+        float *po = &sm.g[group].v[0][0];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (tx == 0) sm.ml[4 * ty + i] = make_float2(st.m[i], st.l[i]);
+            if (tx == 0) sm.ml[group][4 * ty + i] = make_float2(st.m[i], st.l[i]);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
                 *reinterpret_cast<ulonglong2 *>(po + (4 * ty + i) * D + 64 * c + 4 * tx) =
@@ -209,20 +222,24 @@ __device__ __forceinline__ void join_groups(F32Smem<D> &sm, Rows4<D> &st) {
         }
     }
     __syncthreads();
-    if (group == 1) return;
+    if (group > 0) return;
+#pragma unroll 1
+    for (int y = 1; y < kGroups<D>; ++y) {
+        const float *po = &sm.g[y].v[0][0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 y = sm.ml[4 * ty + i];
-        const float mn = fmaxf(st.m[i], y.x), ref = mn == -INFINITY ? 0.f : mn;
-        const float w0 = ex2_approx(st.m[i] - ref), w1 = ex2_approx(y.x - ref);
-        st.m[i] = mn;
-        st.l[i] = st.l[i] * w0 + y.y * w1;
-        const uint64_t a = f2_pack(w0, w0), b = f2_pack(w1, w1);
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = sm.ml[y][4 * ty + i];
+            const float mn = fmaxf(st.m[i], x.x), ref = mn == -INFINITY ? 0.f : mn;
+            const float w0 = ex2_approx(st.m[i] - ref), w1 = ex2_approx(x.x - ref);
+            st.m[i] = mn;
+            st.l[i] = st.l[i] * w0 + x.y * w1;
+            const uint64_t a = f2_pack(w0, w0), b = f2_pack(w1, w1);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(po + (4 * ty + i) * D + 64 * c + 4 * tx);
-            st.o[i][2 * c] = ffma2(x.x, b, fmul2(st.o[i][2 * c], a));
-            st.o[i][2 * c + 1] = ffma2(x.y, b, fmul2(st.o[i][2 * c + 1], a));
+            for (int c = 0; c < D / 64; ++c) {
+                const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(po + (4 * ty + i) * D + 64 * c + 4 * tx);
+                st.o[i][2 * c] = ffma2(o.x, b, fmul2(st.o[i][2 * c], a));
+                st.o[i][2 * c + 1] = ffma2(o.y, b, fmul2(st.o[i][2 * c + 1], a));
+            }
         }
     }
 }
@@ -253,7 +270,7 @@ __device__ __forceinline__ int blocks_le(const int32_t *cu, int n, int w, int T,
 
 // Block (h, w): head h, 32 rows of the sequence that owns block w.
 template <int D>
-__global__ void __launch_bounds__(kThreads) packed_f32_kernel(const PackedArgs a) {
+__global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const PackedArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
@@ -267,13 +284,12 @@ __global__ void __launch_bounds__(kThreads) packed_f32_kernel(const PackedArgs a
     if (t0 >= c1) return;                              // one of the empty blocks
     const int end = min(t0 + kRows, c1);
     const float *Q = static_cast<const float *>(a.q) + h * a.q_hs;
-    for (int i = tid; i < kRows * D / 4; i += kThreads) {
+    for (int i = tid; i < kRows * D / 4; i += kThreads<D>) {
         const int r = i / (D / 4), c = i % (D / 4);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + r < end) x = *reinterpret_cast<const float4 *>(Q + (t0 + r) * a.q_ts + 4 * c);
-        *reinterpret_cast<float4 *>(&sm.q[r][4 * c]) = x;
+        const bool in = t0 + r < end;
+        cp_async16(smem_u32(&sm.q[r][4 * c]), Q + (in ? t0 + r : t0) * a.q_ts + 4 * c, in ? 16u : 0u);
     }
-    __syncthreads();
+    cp_async_commit();
     const int k1 = a.causal ? end : c1;
     int hi[4];  // rows see keys [c0, hi)
 #pragma unroll
@@ -308,14 +324,14 @@ cudaError_t launch_packed_f32_t(const PackedArgs &a) {
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(packed_f32_blocks(a.Sq, a.B) * a.H);
-    return launch_pdl(packed_f32_kernel<D>, dim3(grid), dim3(kThreads), smem, a.stream, a);
+    return launch_pdl(packed_f32_kernel<D>, dim3(grid), dim3(kThreads<D>), smem, a.stream, a);
 }
 
 // ------------------------------------------------------------ trees of drafted tokens
 
 // Block x: (sequence and key/value head, split of the cache, 32 rows).
 template <int D>
-__global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, const int row_tiles) {
+__global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs a, const int row_tiles) {
     griddep_launch_dependents();
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
@@ -327,15 +343,15 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
     const Draft d = draft_of(a, b);
     const int k0 = c * a.chunk, k1 = min(k0 + a.chunk, d.L);
     if (k0 >= k1 && a.n_split > 1) return;  // the merge never reads this split
-    if (tid < kGroup) build_ancestors<kGroup>(a, b, d, sm.anc, tid, [] { named_bar_sync(1, kGroup); });
-    for (int i = tid; i < kRows * D / 4; i += kThreads) {
+    for (int i = tid; i < kRows * D / 4; i += kThreads<D>) {
         const int r = r0 + i / (D / 4), col = 4 * (i % (D / 4));
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows && r % a.T < d.n)
-            x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + b * a.q_bs +
-                                                  (g * G + r / a.T) * a.q_hs + (r % a.T) * a.q_ts + col);
-        *reinterpret_cast<float4 *>(&sm.q[i / (D / 4)][col]) = x;
+        const bool in = r < rows && r % a.T < d.n;
+        const float *q = static_cast<const float *>(a.q);
+        if (in) q += b * a.q_bs + (g * G + r / a.T) * a.q_hs + (r % a.T) * a.q_ts + col;
+        cp_async16(smem_u32(&sm.q[i / (D / 4)][col]), q, in ? 16u : 0u);
     }
+    cp_async_commit();
+    if (tid < kGroup) build_ancestors<kGroup>(a, b, d, sm.anc, tid, [] { named_bar_sync(1, kGroup); });
     bool live[4];
     const uint32_t *w[4];
 #pragma unroll
@@ -346,7 +362,6 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
     }
     Rows4<D> st;
     reset(st);
-    __syncthreads();
     const size_t head = static_cast<size_t>(bk) * a.Skv * D;
     if (k0 < k1) {
         walk<D>(sm, static_cast<const float *>(a.k) + head, D, static_cast<const float *>(a.v) + head, D, k0, k1,
@@ -357,6 +372,8 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeArgs a, co
                         see |= (visible32(w[i], key0 + 16 * j + tx - d.past) & 1u) << j;
                     return live[i] ? see : 0u;
                 });
+    } else {
+        cp_async_wait<0>();
     }
     join_groups(sm, st);
     if (tid >= kGroup) return;
@@ -387,7 +404,7 @@ cudaError_t launch_tree_f32_t(const TreeArgs &a) {
     if (e != cudaSuccess) return e;
     const int row_tiles = ((a.H / a.H_kv) * a.T + kRows - 1) / kRows;
     const unsigned grid = static_cast<unsigned>(a.B * a.H_kv) * a.n_split * row_tiles;
-    e = launch_pdl(tree_f32_kernel<D>, dim3(grid), dim3(kThreads), smem, a.stream, a, row_tiles);
+    e = launch_pdl(tree_f32_kernel<D>, dim3(grid), dim3(kThreads<D>), smem, a.stream, a, row_tiles);
     if (e != cudaSuccess || a.n_split == 1) return e;
     return launch_tree_merge_f32(a);
 }
@@ -398,6 +415,20 @@ long long packed_f32_blocks(long long T, long long n_seq) { return T / kRows + n
 
 cudaError_t launch_packed_f32(const PackedArgs &a) {
     return a.D == 64 ? launch_packed_f32_t<64>(a) : launch_packed_f32_t<128>(a);
+}
+
+int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int D, int n_sm) {
+    // a few rounds of the blocks an SM holds, at least a tile for each group of a block
+    const int rows = (H / H_kv) * T;
+    const long long units = static_cast<long long>(B) * H_kv * ((rows + kRows - 1) / kRows);
+    const long long tiles = (static_cast<long long>(Skv) + kKeys - 1) / kKeys;
+    const long long want = 4LL * (n_sm > 0 ? n_sm : 1), least = 2;
+    long long per = (units * tiles + want - 1) / want;
+    per = (per + least - 1) / least * least;
+    per = per < least ? least : per;
+    per = per > tiles ? tiles : per;
+    per = per < 1 ? 1 : per;
+    return static_cast<int>(per * kKeys);
 }
 
 cudaError_t launch_tree_f32(const TreeArgs &a) {

@@ -899,19 +899,6 @@ cudaError_t launch_tree_t(const TreeArgs &a, int row_tiles, const CUtensorMap &t
 
 }  // namespace
 
-int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int n_sm) {
-    // several waves of the blocks an SM holds, at least two tiles of 64 keys each
-    const int rows = (H / H_kv) * T;
-    const long long units = static_cast<long long>(B) * H_kv * ((rows + 31) / 32);
-    const long long tiles = (static_cast<long long>(Skv) + 63) / 64;
-    const long long want = 6LL * 2 * (n_sm > 0 ? n_sm : 1);
-    long long per = (units * tiles + want - 1) / want;
-    per = per < 2 ? 2 : per;
-    per = per > tiles ? tiles : per;
-    per = per < 1 ? 1 : per;
-    return static_cast<int>(per * 64);
-}
-
 int tree_tc_grid(int B, int H, int H_kv, int T, int Skv, int n_sm) {
     const int row_tiles = ((H / H_kv) * T + kM - 1) / kM;
     const long long tiles = Skv > kN ? (static_cast<long long>(Skv) + kN - 1) / kN : 1;
