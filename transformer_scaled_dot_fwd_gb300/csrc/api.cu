@@ -41,8 +41,14 @@ bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Largest stride in elements and extent in bytes that the checks below take:
+// their sums and products then stay within 64 bits.
+constexpr long long kMaxStride = 1LL << 56;
+constexpr double kMaxExtent = 4.0e18;
+
 // A strided (n_outer, n_inner) set of rows of D elements: row (i, j) starts at
-// element i * so + j * si.  Strides of a dimension of one entry are ignored.
+// element i * so + j * si.  Strides of a dimension of one entry are ignored; one
+// out of range becomes -1, which rows_distinct refuses.
 struct Rows {
     const char *p;
     long long n_outer, n_inner, so, si;  // strides in bytes after make_rows
@@ -51,7 +57,9 @@ struct Rows {
 
 Rows make_rows(const void *p, long long n_outer, long long n_inner, long long so, long long si, long long D,
                long long esz) {
-    Rows r{static_cast<const char *>(p), n_outer, n_inner, so * esz, si * esz, D * esz};
+    so = so < 0 || so > kMaxStride ? -1 : so * esz;
+    si = si < 0 || si > kMaxStride ? -1 : si * esz;
+    Rows r{static_cast<const char *>(p), n_outer, n_inner, so, si, D * esz};
     if (n_inner == 1) r.si = r.row;
     if (n_outer == 1) r.so = r.si * n_inner > r.row ? r.si * n_inner : r.row;
     return r;
@@ -60,6 +68,9 @@ Rows make_rows(const void *p, long long n_outer, long long n_inner, long long so
 // No two rows share a byte: one dimension's rows fit inside the other's stride.
 bool rows_distinct(const Rows &r) {
     if (r.n_outer <= 0 || r.n_inner <= 0) return true;
+    if (r.so < 0 || r.si < 0 ||
+        static_cast<double>(r.n_outer) * static_cast<double>(r.so) + static_cast<double>(r.n_inner) * static_cast<double>(r.si) > kMaxExtent)
+        return false;
     return (r.si >= r.row && r.so >= (r.n_inner - 1) * r.si + r.row) ||
            (r.so >= r.row && r.si >= (r.n_outer - 1) * r.so + r.row);
 }
@@ -734,6 +745,10 @@ ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *
             (lse && overlaps(workspace, static_cast<size_t>(need), lse, static_cast<size_t>(T) * H * 4)))
             return fail(ATTN_EINVAL, "%s: workspace overlaps cu_seqlens or lse", who);
     }
+    const int unit = packed_unit_rows(H, H_kv);
+    const long long tiles = packed_plan_tiles(T, n_seq, unit);
+    if ((dtype == ATTN_F32 ? packed_f32_blocks(T, n_seq) * H : tiles * (unit == 128 ? H / 2 : H)) > 0x7fffffffLL)
+        return fail(ATTN_EINVAL, "%s: %d tokens in %d sequences of %d heads are too many", who, T, n_seq, H);
     int *status = nullptr;
     int rc = status_word(&status);
     if (rc) return rc;
@@ -747,14 +762,8 @@ ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *
     a.v_ts = rows[2].so / esz, a.v_hs = rows[2].si / esz, a.o_ts = rows[3].so / esz, a.o_hs = rows[3].si / esz;
     cudaError_t e;
     if (dtype == ATTN_F32) {
-        if (packed_f32_blocks(T, n_seq) * H > 0x7fffffffLL)
-            return fail(ATTN_EINVAL, "%s: %d tokens in %d sequences of %d heads are too many", who, T, n_seq, H);
         e = launch_packed_f32(a);
     } else {
-        const int unit = packed_unit_rows(H, H_kv);
-        const long long tiles = packed_plan_tiles(T, n_seq, unit);
-        if (tiles * (unit == 128 ? H / 2 : H) > 0x7fffffffLL)
-            return fail(ATTN_EINVAL, "%s: %lld tiles of %d heads are too many", who, tiles, H);
         CUtensorMap tq, tk, tv;
         if ((rc = make_map_packed(&tq, rows[0], D)) || (rc = make_map_packed(&tk, rows[1], D)) ||
             (rc = make_map_packed(&tv, rows[2], D)))
@@ -811,8 +820,14 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
         st[i][0] = B == 1 ? 0 : strides ? strides[3 * i] : static_cast<long long>(H) * T * D;
         st[i][1] = H == 1 ? 0 : strides ? strides[3 * i + 1] : static_cast<long long>(T) * D;
         st[i][2] = T == 1 ? 0 : strides ? strides[3 * i + 2] : D;
-        if (st[i][0] < 0 || st[i][1] < 0 || st[i][2] < 0)
-            return fail(ATTN_EINVAL, "%s: strides must not be negative", who);
+        double extent = 0;
+        const int count[3] = {B, H, T};
+        for (int x = 0; x < 3; ++x) {
+            if (st[i][x] < 0 || st[i][x] > kMaxStride)
+                return fail(ATTN_EINVAL, "%s: stride %lld is negative or too large", who, st[i][x]);
+            extent += static_cast<double>(count[x]) * static_cast<double>(st[i][x]) * static_cast<double>(esz);
+        }
+        if (extent > kMaxExtent) return fail(ATTN_EINVAL, "%s: the strides are too large", who);
         if (st[i][0] * esz % 16 || st[i][1] * esz % 16 || st[i][2] * esz % 16)
             return fail(ATTN_EINVAL, "%s: strides must be multiples of 16 bytes", who);
     }
