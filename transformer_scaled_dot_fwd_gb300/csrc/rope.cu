@@ -15,15 +15,17 @@
 //
 // The rows are read once and written once: bound by HBM for prompts, by the
 // launch and one round trip for a step of single tokens.  A block takes one or two
-// tokens with all their heads: the r / 2 angles of a token are computed once
-// into shared memory and serve every head of q and k.  Small blocks of 128
-// threads, many to an SM, hide one block's look-ups behind another's rows: 256
-// threads and 8 tokens a block took 74 us instead of 68 for 16385 tokens of
-// 32 + 8 heads into a cache, and several units in flight per thread, at the price
-// of fewer blocks, 100 us and more.  A thread then handles
-// units of VEC pairs: two 16-byte loads, 2 VEC elements turned in fp32 and
-// rounded once, two 16-byte stores.  Rows whose strides, addresses or rotary
-// depth do not allow 16-byte accesses take the same code with VEC = 1.
+// tokens with all their heads; the r / 2 angles of a token are computed once.  A
+// thread keeps one unit of VEC pairs of every few rows, its cosines and sines in
+// registers: two 16-byte loads, 2 VEC elements turned in fp32 and rounded once,
+// two 16-byte stores a row.  Rows whose strides, addresses or rotary depth do not
+// allow 16-byte accesses take the same code with VEC = 1.
+//
+// Small blocks, ten and more to an SM, hide one block's look-ups behind another's
+// rows.  16385 tokens of 32 + 8 heads of depth 128 into a cache (402 MB moved): 66
+// us, 6.1 TB/s; 256 threads and 8 tokens a block took 74 us, two rows in flight
+// per thread at 106 registers 109 us.  32768 tokens of 64 heads, half of each
+// turned (1.07 GB): 164 us, 6.5 TB/s.  A step of 64 tokens into a cache: 3.3 us.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "serving.cuh"
@@ -39,10 +41,62 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float x, float *y) { *y = x; }
 __device__ __forceinline__ void from_f32(float x, __nv_bfloat16 *y) { *y = __float2bfloat16_rn(x); }
 
+// VEC elements, as the 16 bytes (or the single element) they are moved in.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Vec {
+struct alignas(sizeof(T) * VEC > 16 ? 16 : sizeof(T) * VEC) Vec {
     T x[VEC];
 };
+template <>
+struct alignas(16) Vec<__nv_bfloat16, 8> {
+    uint32_t w[4];  // two elements each
+};
+
+// (a, b) -> (a c - b s, b c + a s), a and b the elements of x and of y.
+template <typename T, int VEC>
+__device__ __forceinline__ void turn_halves(Vec<T, VEC> &x, Vec<T, VEC> &y, const Vec<float, VEC> &c,
+                                            const Vec<float, VEC> &s) {
+#pragma unroll
+    for (int p = 0; p < VEC; ++p) {
+        const float a = to_f32(x.x[p]), b = to_f32(y.x[p]);
+        from_f32(a * c.x[p] - b * s.x[p], &x.x[p]);
+        from_f32(b * c.x[p] + a * s.x[p], &y.x[p]);
+    }
+}
+__device__ __forceinline__ void turn_halves(Vec<__nv_bfloat16, 8> &x, Vec<__nv_bfloat16, 8> &y, const Vec<float, 8> &c,
+                                            const Vec<float, 8> &s) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const float a0 = bf16lo_to_f32(x.w[p]), a1 = bf16hi_to_f32(x.w[p]);
+        const float b0 = bf16lo_to_f32(y.w[p]), b1 = bf16hi_to_f32(y.w[p]);
+        x.w[p] = pack_bf16x2(a0 * c.x[2 * p] - b0 * s.x[2 * p], a1 * c.x[2 * p + 1] - b1 * s.x[2 * p + 1]);
+        y.w[p] = pack_bf16x2(b0 * c.x[2 * p] + a0 * s.x[2 * p], b1 * c.x[2 * p + 1] + a1 * s.x[2 * p + 1]);
+    }
+}
+// The same for pairs that sit side by side in the 2 VEC elements of x and y.
+template <typename T, int VEC>
+__device__ __forceinline__ void turn_side_by_side(Vec<T, VEC> &x, Vec<T, VEC> &y, const Vec<float, VEC> &c,
+                                                  const Vec<float, VEC> &s) {
+    T z[2 * VEC];
+#pragma unroll
+    for (int p = 0; p < VEC; ++p) z[p] = x.x[p], z[VEC + p] = y.x[p];
+#pragma unroll
+    for (int p = 0; p < VEC; ++p) {
+        const float a = to_f32(z[2 * p]), b = to_f32(z[2 * p + 1]);
+        from_f32(a * c.x[p] - b * s.x[p], &z[2 * p]);
+        from_f32(b * c.x[p] + a * s.x[p], &z[2 * p + 1]);
+    }
+#pragma unroll
+    for (int p = 0; p < VEC; ++p) x.x[p] = z[p], y.x[p] = z[VEC + p];
+}
+__device__ __forceinline__ void turn_side_by_side(Vec<__nv_bfloat16, 8> &x, Vec<__nv_bfloat16, 8> &y,
+                                                  const Vec<float, 8> &c, const Vec<float, 8> &s) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        uint32_t &w = p < 4 ? x.w[p] : y.w[p - 4];
+        const float a = bf16lo_to_f32(w), b = bf16hi_to_f32(w);
+        w = pack_bf16x2(a * c.x[p] - b * s.x[p], b * c.x[p] + a * s.x[p]);
+    }
+}
 
 struct Token {
     long long cache_row;  // (b * H_kv) * Skv + row of head 0's cache row, or -1: not cached
@@ -51,9 +105,9 @@ struct Token {
 };
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 10)
     rope_kernel(const __grid_constant__ RopeArgs a, const int tokens, const int rows_per_block) {
-    __shared__ float2 turn[kRopeMaxTokens][64];
+    __shared__ __align__(16) float cosines[kRopeMaxTokens][64], sines[kRopeMaxTokens][64];
     __shared__ Token tok[kRopeMaxTokens];
     griddep_launch_dependents();
     griddep_wait();
@@ -96,7 +150,8 @@ __global__ void __launch_bounds__(kRopeThreads)
         const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(tok[k].position)) * a.turns[p];
         float s, c;
         sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &s, &c);
-        turn[k][p] = make_float2(c * a.mscale, s * a.sin_scale);
+        cosines[k][p] = c * a.mscale;
+        sines[k][p] = s * a.sin_scale;
     }
     __syncthreads();
 
@@ -105,70 +160,59 @@ __global__ void __launch_bounds__(kRopeThreads)
     const int ushift = 31 - __clz(units);  // a power of two
     const int r0 = blockIdx.y * rows_per_block;
     const int rows = min(rows_per_block, a.H + a.H_kv * (append ? 2 : 1) - r0);
-    const int turned_units = half / VEC;
-
-    for (int i = threadIdx.x; i < (nt * rows) << ushift; i += kRopeThreads) {
-        const int u = i & (units - 1);
-        const int k = (i >> ushift) / rows;
-        const int r = r0 + (i >> ushift) - k * rows;
-        if (!tok[k].live) continue;
+    // A thread keeps one unit of every step-th row, so the angles of a token stay in
+    // registers over its rows.
+    const int u = threadIdx.x & (units - 1), step = kRopeThreads >> ushift;
+    using V = Vec<T, VEC>;
+    for (int k = 0; k < nt; ++k) {
+        const Token token = tok[k];
+        if (!token.live) continue;
         const size_t t = static_cast<size_t>(t0 + k);
-        const T *src;
-        T *dst = nullptr, *cache = nullptr;
-        bool turned = u < turned_units;
-        if (r < a.H) {
-            src = static_cast<const T *>(a.q) + t * a.q_ts + r * a.q_hs;
-            dst = static_cast<T *>(a.q_out) + t * a.qo_ts + r * a.qo_hs;
-        } else {
-            const bool is_v = r >= a.H + a.H_kv;
-            const int g = r - a.H - (is_v ? a.H_kv : 0);
-            if (is_v) {
-                src = static_cast<const T *>(a.v) + t * a.v_ts + g * a.v_hs;
-                turned = false;
+        Vec<float, VEC> c, s;
+        if (u < half / VEC) {
+            c = *reinterpret_cast<const Vec<float, VEC> *>(&cosines[k][u * VEC]);
+            s = *reinterpret_cast<const Vec<float, VEC> *>(&sines[k][u * VEC]);
+        }
+        for (int r = r0 + (threadIdx.x >> ushift); r < r0 + rows; r += step) {
+            const T *src;
+            T *dst = nullptr, *cache = nullptr;
+            bool turned = u < half / VEC;
+            if (r < a.H) {
+                src = static_cast<const T *>(a.q) + t * a.q_ts + r * a.q_hs;
+                dst = static_cast<T *>(a.q_out) + t * a.qo_ts + r * a.qo_hs;
             } else {
-                src = static_cast<const T *>(a.k) + t * a.k_ts + g * a.k_hs;
-                if (a.k_out) dst = static_cast<T *>(a.k_out) + t * a.ko_ts + g * a.ko_hs;
-            }
-            if (append && tok[k].cache_row >= 0)
-                cache = static_cast<T *>(is_v ? a.vcache : a.kcache) +
-                        (tok[k].cache_row + static_cast<long long>(g) * a.Skv) * a.D;
-        }
-        if (!turned && dst == src) dst = nullptr;  // in place: nothing to copy
-        if (!dst && !cache) continue;
-        const int e0 = turned && !a.interleaved ? u * VEC : 2 * u * VEC;
-        const int e1 = turned && !a.interleaved ? half + u * VEC : e0 + VEC;
-        using V = Vec<T, VEC>;
-        V x = *reinterpret_cast<const V *>(src + e0), y = *reinterpret_cast<const V *>(src + e1);
-        if (turned) {
-            const float2 *cs = &turn[k][u * VEC];
-            if (a.interleaved) {
-                // element 2 VEC u + e of the unit: pairs sit side by side
-                V z[2] = {x, y};
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    T &pa = z[(2 * e) / VEC].x[(2 * e) % VEC], &pb = z[(2 * e + 1) / VEC].x[(2 * e + 1) % VEC];
-                    const float va = to_f32(pa), vb = to_f32(pb);
-                    from_f32(va * cs[e].x - vb * cs[e].y, &pa);
-                    from_f32(vb * cs[e].x + va * cs[e].y, &pb);
+                const bool is_v = r >= a.H + a.H_kv;
+                const int g = r - a.H - (is_v ? a.H_kv : 0);
+                if (is_v) {
+                    src = static_cast<const T *>(a.v) + t * a.v_ts + g * a.v_hs;
+                    turned = false;
+                } else {
+                    src = static_cast<const T *>(a.k) + t * a.k_ts + g * a.k_hs;
+                    if (a.k_out) dst = static_cast<T *>(a.k_out) + t * a.ko_ts + g * a.ko_hs;
                 }
-                x = z[0];
-                y = z[1];
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float va = to_f32(x.x[e]), vb = to_f32(y.x[e]);
-                    from_f32(va * cs[e].x - vb * cs[e].y, &x.x[e]);
-                    from_f32(vb * cs[e].x + va * cs[e].y, &y.x[e]);
-                }
+                if (append && token.cache_row >= 0)
+                    cache = static_cast<T *>(is_v ? a.vcache : a.kcache) +
+                            (token.cache_row + static_cast<long long>(g) * a.Skv) * a.D;
             }
-        }
-        if (dst) {
-            *reinterpret_cast<V *>(dst + e0) = x;
-            *reinterpret_cast<V *>(dst + e1) = y;
-        }
-        if (cache) {
-            *reinterpret_cast<V *>(cache + e0) = x;
-            *reinterpret_cast<V *>(cache + e1) = y;
+            if (!turned && dst == src) dst = nullptr;  // in place: nothing to copy
+            if (!dst && !cache) continue;
+            const int e0 = turned && !a.interleaved ? u * VEC : 2 * u * VEC;
+            const int e1 = turned && !a.interleaved ? half + u * VEC : e0 + VEC;
+            V x = *reinterpret_cast<const V *>(src + e0), y = *reinterpret_cast<const V *>(src + e1);
+            if (turned) {
+                if (a.interleaved)
+                    turn_side_by_side(x, y, c, s);
+                else
+                    turn_halves(x, y, c, s);
+            }
+            if (dst) {
+                *reinterpret_cast<V *>(dst + e0) = x;
+                *reinterpret_cast<V *>(dst + e1) = y;
+            }
+            if (cache) {
+                *reinterpret_cast<V *>(cache + e0) = x;
+                *reinterpret_cast<V *>(cache + e1) = y;
+            }
         }
     }
 }
