@@ -342,14 +342,15 @@ def attn_decode_splits(B: int, H: int, Skv: int, D: int) -> int:
 # allocator orders their reuse with it.
 
 def _elsewhere(device, stream):
-    """Context to re-enter a call in, or None when device and stream are current."""
+    """Context to re-enter a call in when device or stream are not current."""
     torch = _torch()
-    if stream is not None:
-        return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                 else torch.cuda.ExternalStream(int(stream), device=device))
-    if device.index != torch.cuda.current_device():
+    if stream is None:
         return torch.cuda.device(device)
-    return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream must be on q's device {device} (it is on {stream.device})")
+    return torch.cuda.stream(stream)
 
 
 def _raw_stream(device):
@@ -394,6 +395,16 @@ def _rows(name, t, T, D, dtype, device):
     if t.device != device:
         raise ValueError(f"{name} must be on q's device {device}")
     return shape[1], st[0], st[1]
+
+
+def _out_rows(name, t, T, heads, D, dtype, device):
+    """(tensor, token stride, head stride) of a (T, heads, D) output, made when not given."""
+    if t is None:
+        return _torch().empty((T, heads, D), dtype=dtype, device=device), heads * D, D
+    given, ts, hs = _rows(name, t, T, D, dtype, device)
+    if given != heads:
+        raise ValueError(f"{name} must be ({T}, {heads}, {D}) (got {tuple(t.shape)})")
+    return t, ts, hs
 
 
 def _first(q, ndim):
@@ -460,10 +471,10 @@ def attn_fwd_packed(q, k, v, cu_seqlens, out=None, lse=None, scale: Optional[flo
     ``return_lse`` (or an ``lse`` tensor) is given.  Rows outside every sequence
     are not written.  See include/attn.h.
     """
+    torch = _torch()
     (T, H, D), sq, code, device = _first(q, 3)
-    away = _elsewhere(device, stream)
-    if away is not None:
-        with away:
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
             return attn_fwd_packed(q, k, v, cu_seqlens, out, lse, scale, causal, return_lse)
     dtype = q.dtype
     H_kv, kt, kh = _rows("k", k, T, D, dtype, device)
@@ -474,12 +485,7 @@ def attn_fwd_packed(q, k, v, cu_seqlens, out=None, lse=None, scale: Optional[flo
         raise ValueError("cu_seqlens must be 1-D with at least one value")
     n_seq = cu_seqlens.shape[0] - 1
     cu = _ints("cu_seqlens", cu_seqlens, (n_seq + 1,), device)
-    torch = _torch()
-    if out is None:
-        out = torch.empty((T, H, D), dtype=dtype, device=device)
-    Ho, ot, oh = _rows("out", out, T, D, dtype, device)
-    if Ho != H:
-        raise ValueError("out must match q's shape")
+    out, ot, oh = _out_rows("out", out, T, H, D, dtype, device)
     if lse is None:
         if return_lse:
             lse = torch.empty((T, H), dtype=torch.float32, device=device)
@@ -511,10 +517,10 @@ def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None,
     committed cache, its ancestors and itself.  Returns ``out`` like q; rows
     without a token are zeros.  See include/attn.h.
     """
+    torch = _torch()
     (B, H, T, D), sq, code, device = _first(q, 4)
-    away = _elsewhere(device, stream)
-    if away is not None:
-        with away:
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
             return attn_decode_tree(q, kcache, vcache, parents, cache_len, draft_len, out, scale)
     Bc, H_kv, Skv = _caches(kcache, vcache, q.dtype, device, D)
     if Bc != B or H_kv < 1 or H % H_kv:
@@ -524,10 +530,12 @@ def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None,
     cl = _ints("cache_len", cache_len, (B,), device)
     dl = _ints("draft_len", draft_len, (B,), device)
     if out is None:
-        out = _torch().empty_like(q)
-    so = out.stride()
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != device or so[3] != 1:
-        raise ValueError("out must match q's shape, dtype and device, with contiguous rows")
+        out = torch.empty_like(q)
+        so = out.stride()
+    else:
+        so = out.stride()
+        if out.shape != q.shape or out.dtype != q.dtype or out.device != device or so[3] != 1:
+            raise ValueError("out must match q's shape, dtype and device, with contiguous rows")
     need = _tree_workspace(B, H, H_kv, T, Skv, D, code, device.index) if B and 0 < T <= 128 else 0
     stream = _raw_stream(device)
     ws = _Workspace(need, stream)
@@ -586,30 +594,23 @@ def attn_rope(q, k, positions, freqs, q_out=None, k_out=None, interleaved: bool 
     attn_rope_frequencies.  ``inverse`` turns back, which is also the gradient.
     Rows may be strided (slices of a fused projection).  See include/attn.h.
     """
+    torch = _torch()
     (T, H, D), sq, code, device = _first(q, 3)
-    away = _elsewhere(device, stream)
-    if away is not None:
-        with away:
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
             return attn_rope(q, k, positions, freqs, q_out, k_out, interleaved, inverse, mscale)
     dtype = q.dtype
     fr, rd = _freqs_arg(freqs, D)
     pos = _ints("positions", positions, (T,), device)
     if positions is None:
         raise ValueError("positions must be given")
-    torch = _torch()
-    if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=dtype, device=device)
-    Ho, ot, oh = _rows("q_out", q_out, T, D, dtype, device)
-    H_kv = kt = kh = kot = koh = Hko = 0
+    q_out, ot, oh = _out_rows("q_out", q_out, T, H, D, dtype, device)
+    H_kv = kt = kh = kot = koh = 0
     if k is not None:
         H_kv, kt, kh = _rows("k", k, T, D, dtype, device)
-        if k_out is None:
-            k_out = torch.empty((T, H_kv, D), dtype=dtype, device=device)
-        Hko, kot, koh = _rows("k_out", k_out, T, D, dtype, device)
+        k_out, kot, koh = _out_rows("k_out", k_out, T, H_kv, D, dtype, device)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if Ho != H or Hko != H_kv:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
     rc = lib().attn_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
                          None if k is None else k_out.data_ptr(), T, H, H_kv, D,
                          _LL8(sq[0], sq[1], kt, kh, ot, oh, kot, koh), pos, fr, rd, 1 if interleaved else 0,
@@ -628,10 +629,10 @@ def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=
     ``positions`` is given.  Returns ``q_out``, or ``(q_out, k_out)`` when a
     ``k_out`` (T, H_kv, D) is given for the turned keys.  See include/attn.h.
     """
+    torch = _torch()
     (T, H, D), sq, code, device = _first(q, 3)
-    away = _elsewhere(device, stream)
-    if away is not None:
-        with away:
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
             return attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens, cache_len, positions, q_out, k_out,
                                     interleaved, mscale)
     dtype = q.dtype
@@ -644,12 +645,10 @@ def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=
     cu = _ints("cu_seqlens", cu_seqlens, (B + 1,), device)
     cl = _ints("cache_len", cache_len, (B,), device)
     pos = _ints("positions", positions, (T,), device)
-    if q_out is None:
-        q_out = _torch().empty((T, H, D), dtype=dtype, device=device)
-    Ho, ot, oh = _rows("q_out", q_out, T, D, dtype, device)
-    Hko, kot, koh = (H_kv, 0, 0) if k_out is None else _rows("k_out", k_out, T, D, dtype, device)
-    if Ho != H or Hko != H_kv:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
+    q_out, ot, oh = _out_rows("q_out", q_out, T, H, D, dtype, device)
+    kot = koh = 0
+    if k_out is not None:
+        k_out, kot, koh = _out_rows("k_out", k_out, T, H_kv, D, dtype, device)
     rc = lib().attn_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
                                 None if k_out is None else k_out.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
                                 T, H, H_kv, D, _LL10(sq[0], sq[1], kt, kh, vt, vh, ot, oh, kot, koh), B, Skv, cu, cl,
