@@ -6,7 +6,10 @@ library's CUDA kernels.  PyTorch supplies device memory and streams.  There is
 no CPU path: when the library is missing, every call raises.
 
     attn_fwd(q, k, v, out=None, scale=None, causal=False, kv_len=None, stream=None)
+    attn_fwd_packed(q, k, v, cu_seqlens, scale=None, causal=False, return_lse=False, ...)
+    attn_rope(q, k, positions, freqs, ...), attn_rope_append(q, k, v, kcache, vcache, freqs, ...)
     attn_decode(q, kcache, vcache, out=None, kv_len=None, stream=None)
+    attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None, ...)
 """
 from __future__ import annotations
 

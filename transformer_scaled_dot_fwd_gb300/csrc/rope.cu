@@ -224,8 +224,8 @@ cudaError_t launch_rope_t(const RopeArgs &a) {
     // two tokens a block when that still leaves several rounds of blocks an SM;
     // with few tokens the rows of one are split
     int tokens = kRopeMaxTokens;
-    while (tokens > 1 && (a.T + tokens - 1) / tokens < 32 * sms) tokens /= 2;
-    const long long blocks = (a.T + tokens - 1) / tokens;
+    while (tokens > 1 && a.T / tokens < 32 * sms) tokens /= 2;
+    const long long blocks = (static_cast<long long>(a.T) + tokens - 1) / tokens;
     const int units = rows * (a.D / (2 * VEC));
     long long split = (2 * sms + blocks - 1) / blocks;
     const long long most = (units + kRopeThreads - 1) / kRopeThreads;
