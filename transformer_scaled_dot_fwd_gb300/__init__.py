@@ -338,11 +338,34 @@ def attn_decode_splits(B: int, H: int, Skv: int, D: int) -> int:
     return lib().attn_decode_splits(B, H, Skv, D)
 
 
-# The serving entry points below are called once per layer and token, so their
-# checks read each tensor's attributes once.  A call for another device or stream
+# The serving entry points below are called once per layer and token, so the usual
+# call, whose arguments are all in order and on the current device and stream, goes
+# through the compiled binding.  It answers None for any other, and the Python
+# below refuses that one with its reason or runs it.  A call for another device or stream
 # than the current one re-enters with that one current: outputs and
 # workspaces then belong to the stream the work runs on, and the caching
 # allocator orders their reuse with it.
+
+_native = None
+
+
+def _load_native():
+    """The compiled binding (csrc/binding.cpp), with the library's functions bound."""
+    global _native
+    import importlib.util
+    path = os.path.join(_HERE, f"_binding.torch{_torch().__version__}.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run `python -m transformer_scaled_dot_fwd_gb300.build`")
+    spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    handle = lib()
+    module.bind(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
+        "attn_fwd_packed", "attn_fwd_packed_workspace", "attn_rope", "attn_rope_append", "attn_decode_tree",
+        "attn_decode_tree_workspace")))
+    _native = module
+    return module
+
 
 def _elsewhere(device, stream):
     """Context to re-enter a call in when device or stream are not current."""
@@ -474,6 +497,10 @@ def attn_fwd_packed(q, k, v, cu_seqlens, out=None, lse=None, scale: Optional[flo
     ``return_lse`` (or an ``lse`` tensor) is given.  Rows outside every sequence
     are not written.  See include/attn.h.
     """
+    if stream is None:
+        done = (_native or _load_native()).packed(q, k, v, cu_seqlens, out, lse, scale, causal, return_lse)
+        if done is not None:
+            return done
     torch = _torch()
     (T, H, D), sq, code, device = _first(q, 3)
     if stream is not None or device.index != torch.cuda.current_device():
@@ -520,6 +547,10 @@ def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None,
     committed cache, its ancestors and itself.  Returns ``out`` like q; rows
     without a token are zeros.  See include/attn.h.
     """
+    if stream is None:
+        done = (_native or _load_native()).tree(q, kcache, vcache, parents, cache_len, draft_len, out, scale)
+        if done is not None:
+            return done
     torch = _torch()
     (B, H, T, D), sq, code, device = _first(q, 4)
     if stream is not None or device.index != torch.cuda.current_device():
@@ -597,6 +628,10 @@ def attn_rope(q, k, positions, freqs, q_out=None, k_out=None, interleaved: bool 
     attn_rope_frequencies.  ``inverse`` turns back, which is also the gradient.
     Rows may be strided (slices of a fused projection).  See include/attn.h.
     """
+    if stream is None:
+        done = (_native or _load_native()).rope(q, k, positions, freqs, q_out, k_out, interleaved, inverse, mscale)
+        if done is not None:
+            return done
     torch = _torch()
     (T, H, D), sq, code, device = _first(q, 3)
     if stream is not None or device.index != torch.cuda.current_device():
@@ -632,6 +667,11 @@ def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=
     ``positions`` is given.  Returns ``q_out``, or ``(q_out, k_out)`` when a
     ``k_out`` (T, H_kv, D) is given for the turned keys.  See include/attn.h.
     """
+    if stream is None:
+        done = (_native or _load_native()).rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens, cache_len, positions,
+                                                       q_out, k_out, interleaved, mscale)
+        if done is not None:
+            return done
     torch = _torch()
     (T, H, D), sq, code, device = _first(q, 3)
     if stream is not None or device.index != torch.cuda.current_device():

@@ -5,7 +5,9 @@
 Each .cu file compiles to an object in parallel; the objects link into
 ``transformer_scaled_dot_fwd_gb300/libattn.so`` with the CUDA runtime linked
 statically.  The driver API is reached through cudaGetDriverEntryPointByVersion,
-so no link against libcuda is needed.
+so no link against libcuda is needed.  csrc/binding.cpp, the Python binding of the
+serving entry points, compiles beside them with the host compiler against the
+installed torch, whose version its file name carries.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -33,6 +36,29 @@ def _nvcc():
     return exe
 
 
+def binding_path(version: str) -> str:
+    """The binding built for torch ``version``."""
+    return os.path.join(PKG, f"_binding.torch{version}.so")
+
+
+def _binding_command():
+    """(output, command) of the binding for the installed torch; None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    out = binding_path(torch.__version__)
+    return out, [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+                 "-isystem", os.path.join(root, "include"),
+                 "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                 "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+                 os.path.join(CSRC, "binding.cpp"), "-o", out + f".tmp{os.getpid()}",
+                 "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def _newest_input_mtime():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
@@ -41,8 +67,12 @@ def _newest_input_mtime():
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False) -> str:
-    """Compile every kernel file for sm_103a and link libattn.so; returns its path."""
-    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _newest_input_mtime():
+    """Compile every kernel file for sm_103a, link libattn.so and compile the binding;
+    returns the library's path."""
+    binding = _binding_command()
+    newest = _newest_input_mtime()
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= newest
+                         for p in [LIB_PATH] + ([binding[0]] if binding else [])):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -56,6 +86,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
         objs.append(obj)
         cmd = [nvcc] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    if binding:
+        procs.append(("binding.cpp", subprocess.Popen(binding[1], stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -73,6 +105,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIB_PATH)
+    if binding:
+        os.replace(binding[1][binding[1].index("-o") + 1], binding[0])
     return LIB_PATH
 
 
