@@ -327,3 +327,38 @@ def test_empty_calls_and_refusals(gpu):
         x = torch.zeros(8, 2, 96, dtype=BF16, device="cuda")
         attn.attn_fwd_packed(x, x.clone(), x.clone(), cu)
     assert e.value.code == attn.ATTN_EUNSUPPORTED
+
+
+# Few sequences: each CTA makes the plan; many, or many tiles: the plan kernel.  What
+# a row computes does not depend on where its tile stands in the plan.
+@pytest.mark.parametrize("H,H_kv", [(2, 1), (3, 3)])
+@pytest.mark.parametrize("lens", [[300, 1, 0, 128, 129, 700], [37] * 32, [257] * 31 + [1], [0] * 31 + [900]])
+@pytest.mark.parametrize("causal", [True, False])
+def test_both_plans_give_the_same_bits(gpu, lens, H, H_kv, causal):
+    q, k, v = tokens(sum(lens), H, H_kv, 64, 12, BF16)
+    few = attn.attn_fwd_packed(q, k, v, ints(offsets(lens)), causal=causal, return_lse=True)
+    many = attn.attn_fwd_packed(q, k, v, ints(offsets([0] * 20 + lens + [0] * 20)), causal=causal, return_lse=True)
+    attn.attn_device_status()
+    assert torch.equal(few[0], many[0]) and torch.equal(few[1], many[1])
+
+
+# T / 128 + n_seq = 384 is the last that fits the CTAs' own plan
+@pytest.mark.parametrize("T", [383 * 128 - 1, 383 * 128, 383 * 128 + 127, 384 * 128])
+def test_plans_at_the_most_tiles(gpu, T):
+    q, k, v = tokens(T, 2, 1, 64, 13, BF16)
+    lse = torch.full((T, 2), 5.0, device="cuda")
+    out, _ = attn.attn_fwd_packed(q, k, v, ints([0, T]), lse=lse, causal=True)
+    want, wl_ = attn.attn_fwd_packed(q, k, v, ints([0, T] + [T] * 40), causal=True, return_lse=True)
+    attn.attn_device_status()
+    assert torch.equal(out, want) and torch.equal(lse, wl_)
+
+
+@pytest.mark.parametrize("n", [16, 40])
+def test_overlapping_sequences_stay_inside(gpu, n):
+    # every other sequence holds all tokens: more tile units than the plan has places
+    T = 4000
+    q, k, v = tokens(T, 2, 1, 64, 14, BF16)
+    big = torch.full((T + 2, 2, 64), 5.0, dtype=BF16, device="cuda")
+    attn.attn_fwd_packed(q, k, v, ints([0, T] * n), out=big[1:T + 1], causal=True)
+    attn.attn_device_status()
+    assert torch.all(big[0] == 5) and torch.all(big[-1] == 5)

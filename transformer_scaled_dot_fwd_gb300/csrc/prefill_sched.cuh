@@ -181,10 +181,76 @@ inline bool plan_items(const FwdArgs &a, long long units, ItemPlan *plan, bool *
     return true;
 }
 
+// Packed sequences: head units in blocks as plan_items makes them, from the K/V
+// steps of one head unit's tiles, those of its longest item, and the units whose
+// keys and values fit the L2 share.
+template <typename I>
+__device__ __forceinline__ PackedPlan packed_blocks(int total, I steps, I longest, int heads, int c_l2, int grid) {
+    PackedPlan plan{total, heads, 0, total * heads};
+    const I c_tail = steps > 0 ? (static_cast<I>(kTailFactorX10) * longest * static_cast<I>(grid) + 10 * steps - 1) / (10 * steps)
+                               : static_cast<I>(heads);
+    if (kL2GroupBytes > 0 && c_l2 < heads && c_tail < static_cast<I>(heads)) {
+        const int n_front = (heads - static_cast<int>(c_tail)) / c_l2;
+        if (n_front > 0) {
+            plan.group = c_l2;
+            plan.front = n_front * c_l2;
+        }
+    }
+    return plan;
+}
+
+// K/V steps of one head unit's `n` tile units of a sequence: their count rises by
+// unit_rows / kBN a unit when causal.
+__device__ __forceinline__ int packed_steps(int len, int n, int unit_rows, int causal) {
+    return causal ? unit_rows / kBN * (n * (n + 1) / 2) : (len + kBN - 1) / kBN * n;
+}
+
+// Sequence s of a packed call, clamped into the tensor whatever cu_seqlens holds.
+__device__ __forceinline__ int packed_sequence(const PackedArgs &a, int s, int *start) {
+    const int c0 = min(max(a.cu_seqlens[s], 0), a.Sq), c1 = min(max(a.cu_seqlens[s + 1], c0), a.Sq);
+    *start = c0;
+    return c1 - c0;
+}
+
+// The plan of a small batch: at most 32 sequences and kSmallTiles tile units, in
+// the shared memory of each CTA.  One warp makes it, lane = sequence for the
+// look-ups and lane = unit index for the list: units of index u follow those above
+// it, the sequences in order.
+constexpr int kSmallTiles = 384;
+struct SmallPlan {
+    int2 seq[32];                 // first token, length
+    uint16_t tile[kSmallTiles];   // sequence | unit << 5
+};
+__device__ __forceinline__ PackedPlan make_small_plan(const PackedArgs &a, SmallPlan &sp, int unit_rows, int heads,
+                                                      int c_l2, int grid) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = static_cast<int>(threadIdx.x % 32);
+    int start = 0, len = 0;
+    if (lane < a.B) len = packed_sequence(a, lane, &start);
+    sp.seq[lane] = make_int2(start, len);
+    const int n = (len + unit_rows - 1) / unit_rows;
+    const int most = __reduce_max_sync(kAll, n);
+    for (int u0 = 0; u0 < most; u0 += 32) {
+        const int u = u0 + lane;
+        int at = 0;
+        for (int s = 0; s < a.B; ++s) at += max(__shfl_sync(kAll, n, s) - u - 1, 0);
+        for (int s = 0; s < a.B; ++s) {
+            if (__shfl_sync(kAll, n, s) <= u) continue;
+            if (at < kSmallTiles) sp.tile[at] = static_cast<uint16_t>(s | u << 5);
+            ++at;
+        }
+    }
+    const int total = min(__reduce_add_sync(kAll, n), kSmallTiles);
+    const int steps = __reduce_add_sync(kAll, packed_steps(len, n, unit_rows, a.causal));
+    const int longest = __reduce_max_sync(kAll, (len + kBN - 1) / kBN);
+    __syncwarp();
+    return packed_blocks(total, steps, longest, heads, c_l2, grid);
+}
+
 // Packed sequences: work item t of the plan.  The list holds the tile units of
 // one head unit, longest first; head units are the minor index, in the same
 // blocks as decode_item's.
-__device__ __forceinline__ Item decode_item(int t, const PackedArgs &a, const PackedPlan &plan) {
+__device__ __forceinline__ Item decode_item(int t, const PackedArgs &a, const PackedPlan &plan, const SmallPlan *sp) {
     Item it;
     const int G = a.H / a.H_kv;
     const bool hp = pairs_heads(a);
@@ -195,7 +261,14 @@ __device__ __forceinline__ Item decode_item(int t, const PackedArgs &a, const Pa
         cg = plan.group;
     }
     const int tt = t - base * plan.n_tiles;
-    const int4 e = a.plan[1 + tt / cg];
+    int4 e;
+    if (sp) {
+        const int tile = sp->tile[tt / cg];
+        const int2 seq = sp->seq[tile & 31];
+        e = make_int4(seq.x, seq.y, tile >> 5, 0);
+    } else {
+        e = a.plan[1 + tt / cg];
+    }
     const int u = base + tt % cg;
     it.start = e.x;
     it.Lb = e.y;

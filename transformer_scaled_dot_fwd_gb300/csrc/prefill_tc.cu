@@ -91,7 +91,8 @@ struct Layout {
     static constexpr int kBarOff = kStageOff + 8 * kStageBytes;
     static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // + barriers + alignment slack
     static constexpr int kGuardOff = kBarOff + 512;          // packed sequences only
-    static constexpr int kSmemBytesPacked = kGuardOff + 512 + 1024;
+    static constexpr int kPlanOff = kGuardOff + 512;
+    static constexpr int kSmemBytesPacked = kPlanOff + 1024 + 1024;
     // TMEM column of S_x (and of P_x, which aliases it) and of O_x
     static __device__ __forceinline__ uint32_t s_col(int x) { return static_cast<uint32_t>(x) * 128u; }
     static __device__ __forceinline__ uint32_t o_col(int x) { return 256u + static_cast<uint32_t>(x) * D; }
@@ -132,6 +133,7 @@ struct Guard {
     int spoiled[kItemRing];      // the item met a non-finite value in an edge tile
 };
 static_assert(sizeof(Guard) <= 512, "guard block");
+static_assert(sizeof(SmallPlan) <= 1024, "plan block");
 
 // Work counters, one slot per launch: [0] next item, [2] epoch of the launch
 // using the slot (0: free); [1] and [3] unused.  Every CTA's producer takes
@@ -199,6 +201,9 @@ __device__ __forceinline__ void release_item(Bars &bars, int k) {
     mbar_arrive(&bars.item_empty[k % kItemRing]);
 }
 
+// The four counts are decode_item's; for packed sequences they are the rows of a tile
+// unit, the head units whose keys and values fit the L2 share, the head units, and
+// whether each CTA makes the plan itself.
 template <int D, typename Args>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const Args a, const __grid_constant__ CUtensorMap tq,
@@ -268,14 +273,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ================================================================ TMA producer
         regs_dec<kRegsProducer>();
+        PackedPlan plan{};
+        const SmallPlan *small = nullptr;
+        if constexpr (kPacked) {
+            if (n_items > 0) {  // a small batch: no plan kernel ran
+                SmallPlan &sp = *reinterpret_cast<SmallPlan *>(smem + L::kPlanOff);
+                plan = make_small_plan(a, sp, n_major, /*heads=*/front, /*c_l2=*/group, static_cast<int>(gridDim.x));
+                small = &sp;
+            }
+        }
         if (lane == 0) {
             if (owner != 0u && owner != epoch) report_status(a.status, 0x12, kStatusSchedConflict);
             int total = n_items;
-            PackedPlan plan{};
-            if constexpr (kPacked) {  // the plan kernel counted the items
-                const int4 h = a.plan[0];
-                plan = PackedPlan{h.x, h.y, h.z, h.w};
-                total = h.w;
+            if constexpr (kPacked) {
+                if (!small) {  // the plan kernel counted the items
+                    const int4 h = a.plan[0];
+                    plan = PackedPlan{h.x, h.y, h.z, h.w};
+                }
+                total = plan.n_items;
             }
             int requests = 0;  // edge V tiles filed with the guard warps
             const unsigned int last_draw = static_cast<unsigned int>(total) + gridDim.x - 1u;
@@ -299,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Item it;
                 if (t < total) {
                     if constexpr (kPacked)
-                        it = decode_item(t, a, plan);
+                        it = decode_item(t, a, plan, small);
                     else
                         it = decode_item(t, a, n_major, group, front);
                 } else {
@@ -887,7 +902,8 @@ __device__ __forceinline__ int sum_above(int v, int *warp_sum) {
 // number of sequences and of units.  The order within one index is that of the
 // atomics; it decides where an item runs, not what it computes.
 __global__ void __launch_bounds__(kPlanThreads)
-    packed_plan_kernel(const PackedArgs a, int4 *out, const int cap, const int unit_rows, const int heads, const int grid) {
+    packed_plan_kernel(const PackedArgs a, int4 *out, const int cap, const int unit_rows, const int heads, const int c_l2,
+                       const int grid) {
     __shared__ int level[kPlanLevels];  // tiles of each index, then the next list position
     __shared__ int warp_sum[kPlanThreads / 32];
     __shared__ unsigned long long steps;
@@ -895,11 +911,6 @@ __global__ void __launch_bounds__(kPlanThreads)
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x;
-    auto sequence = [&](int s, int *start) {  // clamped into the tensor whatever cu_seqlens holds
-        const int c0 = min(max(a.cu_seqlens[s], 0), a.Sq), c1 = min(max(a.cu_seqlens[s + 1], c0), a.Sq);
-        *start = c0;
-        return c1 - c0;
-    };
     level[tid] = 0;
     if (tid == 0) {
         steps = 0;
@@ -911,9 +922,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     int most = 0;
     for (int s = tid; s < a.B; s += kPlanThreads) {
         int start;
-        const int len = sequence(s, &start), n = (len + unit_rows - 1) / unit_rows;
-        // K/V steps of the sequence's units: their count rises by unit_rows / kBN a unit when causal
-        const int kv = (len + kBN - 1) / kBN, per = unit_rows / kBN;
+        const int len = packed_sequence(a, s, &start), n = (len + unit_rows - 1) / unit_rows;
+        const int kv = (len + kBN - 1) / kBN, per = unit_rows / kBN;  // steps as packed_steps counts them
         mine += a.causal ? static_cast<unsigned long long>(per) * n * (n + 1) / 2 : static_cast<unsigned long long>(kv) * n;
         most = max(most, kv);
         if (n > 0) {
@@ -935,7 +945,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int warp = tid / 32, lane = tid % 32;
     for (int s = warp; s < a.B; s += kPlanThreads / 32) {
         int start;
-        const int len = sequence(s, &start), n = (len + unit_rows - 1) / unit_rows;
+        const int len = packed_sequence(a, s, &start), n = (len + unit_rows - 1) / unit_rows;
         for (int u = lane; u < n; u += 32) {
             const int at = atomicAdd(&level[min(u, kPlanLevels - 1)], 1);
             if (at < cap) out[1 + at] = make_int4(start, len, u, 0);
@@ -943,23 +953,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     if (tid == 0) {
         const int total = min(first + n_here, cap);  // thread 0 holds the last places
-        // blocks of head units as plan_items makes them, on the sequences' lengths
-        const long long kv_head_bytes = 2LL * a.Sq * a.D * 2;
-        const long long per_kv = unit_rows == kBM ? (a.H / a.H_kv) / 2 : a.H / a.H_kv;
-        long long c_l2 = kL2GroupBytes * per_kv / (kv_head_bytes > 0 ? kv_head_bytes : 1);
-        c_l2 = c_l2 > 1 ? c_l2 : 1;
-        const long long unit_steps = static_cast<long long>(steps);
-        const long long c_tail = unit_steps > 0
-            ? (kTailFactorX10 * longest * grid + 10 * unit_steps - 1) / (10 * unit_steps) : heads;
-        long long group = heads, front = 0;
-        if (kL2GroupBytes > 0 && c_l2 < heads && c_tail < heads) {
-            const long long n_front = (heads - c_tail) / c_l2;
-            if (n_front > 0) {
-                group = c_l2;
-                front = n_front * c_l2;
-            }
-        }
-        out[0] = make_int4(total, static_cast<int>(group), static_cast<int>(front), total * heads);
+        const PackedPlan plan = packed_blocks(total, static_cast<long long>(steps), static_cast<long long>(longest), heads,
+                                              c_l2, grid);
+        out[0] = make_int4(plan.n_tiles, plan.group, plan.front, plan.n_items);
     }
 }
 
@@ -979,11 +975,21 @@ cudaError_t launch_packed_t(const PackedArgs &a, long long plan_tiles, const CUt
     e = cudaFuncSetAttribute(prefill_tc_kernel<D, PackedArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kSmemBytesPacked);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a, const_cast<int4 *>(a.plan),
-                   static_cast<int>(plan_tiles), unit_rows, heads, static_cast<int>(grid));
-    if (e != cudaSuccess) return e;
+    // head units whose keys and values fit the L2 share (all tokens of a head)
+    const long long kv_head_bytes = 2LL * a.Sq * D * 2;
+    const long long per_kv = unit_rows == kBM ? (a.H / a.H_kv) / 2 : a.H / a.H_kv;
+    const long long fit = kL2GroupBytes * per_kv / kv_head_bytes;
+    const int c_l2 = static_cast<int>(fit < 1 ? 1 : fit < heads ? fit : heads);
+    // Few sequences and tiles: each CTA makes the plan itself in about a microsecond,
+    // where the plan kernel and its launch take 4.
+    const bool small = a.B <= 32 && plan_tiles <= kSmallTiles;
+    if (!small) {
+        e = launch_pdl(packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a, const_cast<int4 *>(a.plan),
+                       static_cast<int>(plan_tiles), unit_rows, heads, c_l2, static_cast<int>(grid));
+        if (e != cudaSuccess) return e;
+    }
     return launch_pdl(prefill_tc_kernel<D, PackedArgs>, dim3(grid), dim3(kThreads), L::kSmemBytesPacked, a.stream, a,
-                      tq, tk, tv, 0, 0, 0, 0, sched, epoch);
+                      tq, tk, tv, unit_rows, c_l2, heads, small ? 1 : 0, sched, epoch);
 }
 
 }  // namespace
