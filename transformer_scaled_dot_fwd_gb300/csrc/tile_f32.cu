@@ -12,14 +12,15 @@
 // (cp.async) while P V runs, its V while the scores are computed.
 //
 // Few rows and long keys leave one warp per scheduler waiting on shared memory
-// and shuffles, so a block has several groups that take the key tiles of the same
-// rows in turn and join their output, max and sum at the end: as many as shared
+// and shuffles, so a block has several groups that share the keys of the same rows
+// equally (in units of 16, so that 64 or 513 keys leave no group idle) and join their output, max and sum at the end: as many as shared
 // memory holds, which also means one block an SM, so that a block left over goes
 // to the SM that is done first and not beside a long one.
 //
 // Measured: six sequences of 700 to 1 tokens, 4 heads of depth 64, not causal (0.86
-// GFLOP): 43 us; with one group a block 90 us, two groups and two blocks an SM 47
-// us.  A tile takes 2 us of an SM, twice its FMAs' time.  8 rows a thread (half the
+// GFLOP): 40 us; with whole tiles in turn 43 us, one group a block 90 us, two groups
+// and two blocks an SM 47 us.  A tile takes 1.8 us of an SM, 1.6 times its FMAs'
+// time; 232 blocks on 152 SMs leave a second round to the long ones.  8 rows a thread (half the
 // loads, half the warps) came to 45 us, 8 rows a warp with the keys over its lanes
 // to 47 us.
 //
@@ -74,9 +75,10 @@ struct Rows4 {
     uint64_t o[4][D / 32];
 };
 
-// This group's tiles of keys [k0, k1) (the whole block calls it, with the copies of
-// Q committed as one group): K row j at kbase + j * ks, V row j at vbase + j * vs.
-// visible(i, key0) gives the bits of keys key0 + tx + 16 j, j < 4, of row 4 ty + i.
+// This group's part of keys [k0, k1), an equal share in units of 16 keys (the whole
+// block calls it, with the copies of Q committed as one group): K row j at
+// kbase + j * ks, V row j at vbase + j * vs.  visible(i, key0) gives the bits of
+// keys key0 + tx + 16 j, j < 4, of row 4 ty + i.
 template <int D, typename Visible>
 __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long long ks, const float *vbase,
                                      long long vs, int k0, int k1, float sl2, Rows4<D> &st, Visible visible) {
@@ -84,18 +86,22 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
     auto &sm = smem.g[group];
     const auto sync = [&] { named_bar_sync(1 + group, kGroup); };
     constexpr int C = D / 64;
+    const int per = (max(k1 - k0, 0) + 16 * kGroups<D> - 1) / (16 * kGroups<D>) * 16;
+    const int first = k0 + group * per, last = min(first + per, k1);  // no keys if last <= first
+    // the key units of 16 in the tile at key0; rows past the last key are zeros
+    auto units = [&](int key0) { return min((last - key0 + 15) / 16, kKeys / 16); };
     auto load = [&](float *dst, int stride, const float *base, long long gs, int key0) {
         const uint32_t to = smem_u32(dst);
+        const int n = units(key0) * (16 * D / 4);
 #pragma unroll 8
-        for (int i = tid; i < kKeys * D / 4; i += kGroup) {
+        for (int i = tid; i < n; i += kGroup) {
             const int row = i / (D / 4), c = i % (D / 4);
-            const bool in = key0 + row < k1;
+            const bool in = key0 + row < last;
             cp_async16(to + (row * stride + 4 * c) * 4, base + (in ? key0 + row : k0) * gs + 4 * c, in ? 16u : 0u);
         }
         cp_async_commit();
     };
-    const int first = k0 + group * kKeys;
-    if (first < k1) {
+    if (first < last) {
         load(&sm.k[0][0], D + 4, kbase, ks, first);
         load(&sm.v[0][0], D, vbase, vs, first);
         cp_async_wait<2>();  // Q, copied in before by all groups
@@ -103,66 +109,77 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
         cp_async_wait<0>();
     }
     __syncthreads();
-    constexpr int kStride = kGroups<D> * kKeys;
-    for (int key0 = first; key0 < k1; key0 += kStride) {
-        const bool more = key0 + kStride < k1;
+    for (int key0 = first; key0 < last; key0 += kKeys) {
+        const bool more = key0 + kKeys < last;
+        const int n_units = units(key0);
         cp_async_wait<1>();  // K of this tile (V may still be on its way)
         sync();
-        uint64_t s2[4][4] = {};  // sums over even and over odd depths
-#pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-            ulonglong2 qa[4], kb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const ulonglong2 *>(&smem.q[4 * ty + i][d]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) kb[j] = *reinterpret_cast<const ulonglong2 *>(&sm.k[tx + 16 * j][d]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s2[i][j] = ffma2(qa[i].x, kb[j].x, s2[i][j]);
-                    s2[i][j] = ffma2(qa[i].y, kb[j].y, s2[i][j]);
-                }
-        }
         bool hidden = false;  // a row of the thread misses a key of the tile (those past k1 are zeros)
+        auto score = [&](auto n) {
+            constexpr int N = decltype(n)::value;
+            uint64_t s2[4][N] = {};  // sums over even and over odd depths
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                ulonglong2 qa[4], kb[N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t see = visible(i, key0);
-            float s[4], mt = -INFINITY;
+                for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const ulonglong2 *>(&smem.q[4 * ty + i][d]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // rounded before the difference below: huge scores
-                s[j] = __fmul_rn(f2_lo(s2[i][j]) + f2_hi(s2[i][j]), sl2);
-                hidden = hidden || (!(see >> j & 1u) && key0 + tx + 16 * j < k1);
-                if (see >> j & 1u) mt = fmaxf(mt, s[j]);
+                for (int j = 0; j < N; ++j) kb[j] = *reinterpret_cast<const ulonglong2 *>(&sm.k[tx + 16 * j][d]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        s2[i][j] = ffma2(qa[i].x, kb[j].x, s2[i][j]);
+                        s2[i][j] = ffma2(qa[i].y, kb[j].y, s2[i][j]);
+                    }
             }
 #pragma unroll
-            for (int x = 1; x < 16; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-            const float mn = fmaxf(st.m[i], mt);
-            const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet (or nothing but -inf)
-            const float corr = ex2_approx(st.m[i] - ref);
-            st.m[i] = mn;
-            float sum = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t see = visible(i, key0);
+                float s[N], mt = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p = see >> j & 1u ? ex2_approx(s[j] - ref) : 0.f;
-                sum += p;
-                sm.p[4 * ty + i][tx + 16 * j] = p;
+                for (int j = 0; j < N; ++j) {
+                    // rounded before the difference below: huge scores
+                    s[j] = __fmul_rn(f2_lo(s2[i][j]) + f2_hi(s2[i][j]), sl2);
+                    hidden = hidden || (!(see >> j & 1u) && key0 + tx + 16 * j < k1);
+                    if (see >> j & 1u) mt = fmaxf(mt, s[j]);
+                }
+#pragma unroll
+                for (int x = 1; x < 16; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+                const float mn = fmaxf(st.m[i], mt);
+                const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet (or nothing but -inf)
+                const float corr = ex2_approx(st.m[i] - ref);
+                st.m[i] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float p = see >> j & 1u ? ex2_approx(s[j] - ref) : 0.f;
+                    sum += p;
+                    sm.p[4 * ty + i][tx + 16 * j] = p;
+                }
+                st.l[i] = st.l[i] * corr + sum;  // this thread's keys; summed over the half warp at the end
+                const uint64_t corr2 = f2_pack(corr, corr);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) st.o[i][e] = fmul2(st.o[i][e], corr2);
             }
-            st.l[i] = st.l[i] * corr + sum;  // this thread's keys; summed over the half warp at the end
-            const uint64_t corr2 = f2_pack(corr, corr);
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) st.o[i][e] = fmul2(st.o[i][e], corr2);
-        }
+        };
+        if (n_units == 4)
+            score(std::integral_constant<int, 4>{});
+        else if (n_units == 3)
+            score(std::integral_constant<int, 3>{});
+        else if (n_units == 2)
+            score(std::integral_constant<int, 2>{});
+        else
+            score(std::integral_constant<int, 1>{});
         // every row of the warp sees every key: plain FMAs; otherwise a weight
         // of zero must not meet an infinite or NaN value
         const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
         sync();              // all scores are done with K; P is visible
-        if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + kStride);
+        if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + kKeys);
         auto mix = [&](auto guarded) {
 #pragma unroll 2
-            for (int j = 0; j < kKeys; j += 4) {
+            for (int j = 0; j < 16 * n_units; j += 4) {
                 float4 p4[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(&sm.p[4 * ty + i][j]);
@@ -189,7 +206,7 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
         else
             mix(std::false_type{});
         sync();  // V and P are free
-        if (more) load(&sm.v[0][0], D, vbase, vs, key0 + kStride);
+        if (more) load(&sm.v[0][0], D, vbase, vs, key0 + kKeys);
     }
     cp_async_wait<0>();
 #pragma unroll
@@ -422,7 +439,8 @@ cudaError_t launch_packed_f32(const PackedArgs &a) {
 }
 
 int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int D, int n_sm) {
-    // a few rounds of the blocks an SM holds, at least a tile for each group of a block
+    // a few rounds of the blocks an SM holds, at least two tiles a block (four sequences
+    // of up to 1024 keys: 14 us with one or two tiles, 18 with four, 30 with eight)
     const int rows = (H / H_kv) * T;
     const long long units = static_cast<long long>(B) * H_kv * ((rows + kRows - 1) / kRows);
     const long long tiles = (static_cast<long long>(Skv) + kKeys - 1) / kKeys;
