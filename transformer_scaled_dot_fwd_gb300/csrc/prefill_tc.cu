@@ -201,6 +201,57 @@ __device__ __forceinline__ void release_item(Bars &bars, int k) {
     mbar_arrive(&bars.item_empty[k % kItemRing]);
 }
 
+// Packed sequences: the weights of a tile with scores of huge magnitude, p = 2^(s sl2 - m)
+// as bf16 pairs over the S columns, zeros from column t on; returns the row's sum.
+// s sl2 - m in one rounding leaves the rounding of m behind, 2^-24 of it: a common
+// factor of the row's weights, until it overflows them.  Here the product is rounded
+// first, as m was, so that the maximum's exponent is 0.  Not inlined: as a part of the
+// softmax loop it cost 1-4 % of a prompt that has no such score.
+__device__ __noinline__ float huge_weights(uint32_t t_s, int t, float sl2, float negm) {
+    float l = 0.f;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {  // P of 64 keys goes over S columns already read
+        uint32_t s[64], p[32];
+        tmem_ld32(t_s + h * 64, s);
+        tmem_ld32(t_s + h * 64 + 32, s + 32);
+        tmem_ld_wait();
+        reg_fence32(s);
+        reg_fence32(s + 32);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const int c = h * 64 + 2 * e;
+            const float p0 = c < t ? ex2_approx(__fmul_rn(u2f(s[2 * e]), sl2) + negm) : 0.f;
+            const float p1 = c + 1 < t ? ex2_approx(__fmul_rn(u2f(s[2 * e + 1]), sl2) + negm) : 0.f;
+            l += p0 + p1;
+            p[e] = pack_bf16x2(p0, p1);
+        }
+        tmem_st32(t_s + h * 32, p);
+    }
+    tmem_st_wait();
+    return l;
+}
+
+// Packed sequences: adds to a written row of the output the non-finite values of keys
+// [key, lim), which the guard took out of the edge tiles and this row does see: with
+// them the sum is not finite, whatever was rounded away.  After the stores and not
+// inlined, for the same reason (in the epilogue's own code it cost 4 us of 73).
+template <int D>
+__device__ __noinline__ void add_nonfinite(__nv_bfloat16 *out, const __nv_bfloat16 *v, long long v_ts, int key, int lim) {
+    uint32_t *o = reinterpret_cast<uint32_t *>(out);
+#pragma unroll 1
+    for (; key < lim; ++key) {
+        const uint32_t *vr = reinterpret_cast<const uint32_t *>(v + static_cast<size_t>(key) * v_ts);
+#pragma unroll 1
+        for (int e = 0; e < D / 2; ++e) {
+            const uint32_t w = vr[e], nf = nonfinite2(w);
+            if (!nf) continue;
+            const uint32_t y = o[e];
+            o[e] = pack_bf16x2(bf16lo_to_f32(y) + (nf & 0xffffu ? bf16lo_to_f32(w) : 0.f),
+                               bf16hi_to_f32(y) + (nf & 0xffff0000u ? bf16hi_to_f32(w) : 0.f));
+        }
+    }
+}
+
 // The four counts are decode_item's; for packed sequences they are the rows of a tile
 // unit, the head units whose keys and values fit the L2 share, the head units, and
 // whether each CTA makes the plan itself.
@@ -621,27 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m_tile = mraw == -INFINITY ? -INFINITY : mraw * sl2;
                 const float m_new = fmaxf(m_run, m_tile);
                 const bool grow = m_new > m_run + kRescaleLog2;
-                float mul = sl2;
-                if (__any_sync(0xffffffffu, grow || (kPacked && huge))) {
+                if (__any_sync(0xffffffffu, grow)) {
                     const float factor = grow ? ex2_approx(m_run - m_new) : 1.f;
                     if (grow) {
                         l *= factor;
                         m_run = m_new;
                     }
-                    if constexpr (kPacked) {
-                        // s * mul - m in one rounding leaves the rounding of m behind, 2^-24 of it: a
-                        // common factor of the row's weights, until it overflows them.  For huge
-                        // scores round the product first, so that the maximum's exponent is 0.
-                        // (In this branch, which such rows take every time: a branch of its own
-                        // cost 3 % of a long prompt.)
+                    if constexpr (kPacked)
                         huge = __any_sync(0xffffffffu, fabsf(m_run) > kHugeLog2 && m_run != -INFINITY);
-                        if (huge) {
-#pragma unroll
-                            for (int c = 0; c < 128; ++c) s[c] = f2u(__fmul_rn(u2f(s[c]), sl2));
-                            mul = 1.f;
-                        }
-                    }
-                    if (j > 0 && (!kPacked || __any_sync(0xffffffffu, grow))) {  // O holds earlier tiles: bring it to the new max
+                    if (j > 0) {  // O holds earlier tiles: bring it to the new max
     #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
@@ -655,7 +694,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float negm = m_run == -INFINITY ? 0.f : -m_run;
-                const uint64_t sl2x2 = f2_pack(mul, mul), negmx2 = f2_pack(negm, negm);
+                if (kPacked && huge) {
+                    l += huge_weights(t_s, t, sl2, negm);
+                    tc_fence_before();
+                    mbar_arrive(&bars.p_ready[x]);
+                    continue;
+                }
+                const uint64_t sl2x2 = f2_pack(sl2, sl2), negmx2 = f2_pack(negm, negm);
                 uint64_t l4[4] = {0, 0, 0, 0};  // packed partial row sums
                 // p = 2^(s*scale*log2e - m), packed into bf16 pairs over the S
                 // columns.  A hidden column holds -inf and 2^-inf is an exact
@@ -736,12 +781,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     zero_row ? -INFINITY : (m_run + log2f(l)) * 0.6931471805599453f;
             __nv_bfloat16 *obh = static_cast<__nv_bfloat16 *>(a.out);
             size_t o_row = D;
-            bool spoiled = false;
             if constexpr (kPacked) {
                 obh += static_cast<size_t>(it.start) * a.o_ts + static_cast<size_t>(head) * a.o_hs;
                 o_row = static_cast<size_t>(a.o_ts);
-                spoiled = *static_cast<volatile int *>(&guard.spoiled[k % kItemRing]) != 0 && i < n_rows && have_o;
-                release_item(bars, k);
             } else {
                 obh += static_cast<size_t>(head) * a.Sq * D;
             }
@@ -757,24 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait();
                     reg_fence32(o);
                     reg_fence32(o + 32);
-                }
-                if constexpr (kPacked) {
-                    if (spoiled) {  // add the non-finite values that this row does see
-                        const int lim = a.causal ? i + 1 : it.Lb;
-                        const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v) +
-                                                  static_cast<size_t>(it.bh_kv) * a.v_hs + c * 64;
-#pragma unroll 1
-                        for (int key = first_edge_tile(it, a.causal) * kBN; key < lim; ++key) {
-                            const uint32_t *vr = reinterpret_cast<const uint32_t *>(
-                                vp + static_cast<size_t>(it.start + key) * a.v_ts);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const uint32_t w = vr[e], nf = nonfinite2(w);
-                                if (nf & 0xffffu) o[2 * e] = f2u(u2f(o[2 * e]) + bf16lo_to_f32(w));
-                                if (nf & 0xffff0000u) o[2 * e + 1] = f2u(u2f(o[2 * e + 1]) + bf16hi_to_f32(w));
-                            }
-                        }
-                    }
                 }
                 __syncwarp();  // the previous pass has read the buffer back
 #pragma unroll
@@ -796,6 +820,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (row < n_rows)
                         *reinterpret_cast<uint4 *>(obh + static_cast<size_t>(row) * o_row + c * 64 + ch * 8) = v;
                 }
+            }
+            if constexpr (kPacked) {
+                if (*static_cast<volatile int *>(&guard.spoiled[k % kItemRing]) != 0) {
+                    __syncwarp();  // the warp has written its rows
+                    const Item at = read_item(bars, k);
+                    const int row = at.row_base + x * at.row_step + r;
+                    if (row < at.Lb && have_o)
+                        add_nonfinite<D>(
+                            static_cast<__nv_bfloat16 *>(a.out) + static_cast<size_t>(at.start + row) * a.o_ts +
+                                static_cast<size_t>(at.bh_base + x * at.bh_step) * a.o_hs,
+                            static_cast<const __nv_bfloat16 *>(a.v) + static_cast<size_t>(at.start) * a.v_ts +
+                                static_cast<size_t>(at.bh_kv) * a.v_hs,
+                            a.v_ts, first_edge_tile(at, a.causal) * kBN, a.causal ? row + 1 : at.Lb);
+                }
+                release_item(bars, k);
             }
         }
     }
