@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kPacked) {
             for (int s = 0; s < kGuardRing; ++s) {
                 mbar_init(&guard.full[s], 1);
-                mbar_init(&guard.clean[s], 64);
+                mbar_init(&guard.clean[s], 2);  // guard warps
             }
         }
         mbar_init(&bars.mma_done, 1);
@@ -582,8 +582,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tile = smem_u32(ring + stage * L::kTileBytes);
                 const bool bad = clean_v_tile<L::kSub, kBN, 64>(tile, rows, tid);
                 if (bad) *static_cast<volatile int *>(&guard.spoiled[item]) = 1;
-                fence_proxy_async_shared();
-                mbar_arrive(&guard.clean[slot]);
+                // what was written must be seen by the MMA; most tiles are left as they are
+                if (rows < kBN || __any_sync(0xffffffffu, bad)) fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&guard.clean[slot]);
             }
         }
     } else {
