@@ -5,6 +5,8 @@
 #include "kernels.h"
 #include "ptx.cuh"
 
+#include <type_traits>
+
 namespace attn {
 
 // Number of the n nondecreasing values v[0..n) that are <= t, found by the
@@ -119,32 +121,40 @@ __device__ __forceinline__ bool clean_v_tile(uint32_t tile, int inside, int tid)
     constexpr int kChunks = kSub * kRows * 8, kBatch = 8;
     static_assert(kChunks % (Threads * kBatch) == 0, "whole batches");
     bool bad = false;
+    auto pass = [&](auto partial) {
 #pragma unroll 1
-    for (int c0 = tid; c0 < kChunks; c0 += Threads * kBatch) {
-        uint4 v[kBatch];
-        uint32_t acc = 0;
+        for (int c0 = tid; c0 < kChunks; c0 += Threads * kBatch) {
+            uint4 v[kBatch];
+            uint32_t acc = 0;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) v[i] = ld_shared_v4(tile + (c0 + i * Threads) * 16);
+            for (int i = 0; i < kBatch; ++i) v[i] = ld_shared_v4(tile + (c0 + i * Threads) * 16);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            acc |= ((v[i].x & 0x7f807f80u) + 0x00800080u) | ((v[i].y & 0x7f807f80u) + 0x00800080u) |
-                   ((v[i].z & 0x7f807f80u) + 0x00800080u) | ((v[i].w & 0x7f807f80u) + 0x00800080u);
-        if (!(acc & 0x80008000u) && inside >= kRows) continue;
-        // read again, one chunk at a time: nothing stays live for a rare case
-#pragma unroll 1
-        for (int c = c0; c < c0 + kBatch * Threads; c += Threads) {
-            const uint4 v = ld_shared_v4(tile + c * 16);
-            if ((c >> 3) % kRows >= inside) {
-                st_shared_v4(tile + c * 16, 0u, 0u, 0u, 0u);
-                continue;
+            for (int i = 0; i < kBatch; ++i) {
+                if (decltype(partial)::value && ((c0 + i * Threads) >> 3) % kRows >= inside) {
+                    st_shared_v4(tile + (c0 + i * Threads) * 16, 0u, 0u, 0u, 0u);
+                    continue;
+                }
+                acc |= ((v[i].x & 0x7f807f80u) + 0x00800080u) | ((v[i].y & 0x7f807f80u) + 0x00800080u) |
+                       ((v[i].z & 0x7f807f80u) + 0x00800080u) | ((v[i].w & 0x7f807f80u) + 0x00800080u);
             }
-            const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
-            if (n0 | n1 | n2 | n3) {
-                bad = true;
-                st_shared_v4(tile + c * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
+            if (!(acc & 0x80008000u)) continue;
+            // read again, one chunk at a time: nothing stays live for a rare case
+#pragma unroll 1
+            for (int c = c0; c < c0 + kBatch * Threads; c += Threads) {
+                if (decltype(partial)::value && (c >> 3) % kRows >= inside) continue;
+                const uint4 v = ld_shared_v4(tile + c * 16);
+                const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
+                if (n0 | n1 | n2 | n3) {
+                    bad = true;
+                    st_shared_v4(tile + c * 16, v.x & ~n0, v.y & ~n1, v.z & ~n2, v.w & ~n3);
+                }
             }
         }
-    }
+    };
+    if (inside >= kRows)
+        pass(std::false_type{});
+    else
+        pass(std::true_type{});
     return bad;
 }
 

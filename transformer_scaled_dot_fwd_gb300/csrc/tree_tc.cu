@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < kGuardRing; ++s) {
             mbar_init(&bars.guard_full[s], 1);
-            mbar_init(&bars.guard_clean[s], 64);
+            mbar_init(&bars.guard_clean[s], 2);  // guard warps
         }
         mbar_init(&bars.join, 256);
         mbar_init(&bars.mma_done, 1);
@@ -553,8 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tile = smem_u32(ring + stage * L::kTile);
             const bool bad = clean_v_tile<L::kSub, kN, 64>(tile, inside, tid);
             if (bad) *static_cast<volatile int *>(&bars.spoiled[run]) = 1;
-            fence_proxy_async_shared();
-            mbar_arrive(&bars.guard_clean[edges % kGuardRing]);  // edge tiles are counted by themselves
+            if (inside < kN || __any_sync(0xffffffffu, bad)) fence_proxy_async_shared();  // written: the MMA must see it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.guard_clean[edges % kGuardRing]);  // edge tiles are counted by themselves
             ++edges;
         }
     } else {
