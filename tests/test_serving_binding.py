@@ -122,3 +122,52 @@ def test_other_calls_are_left_to_the_checked_path(native, name):
             entry(*args[:6], float("inf"), True, True)
         else:
             entry(*args[:7], float("inf"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("name", ["packed", "rope", "rope_append", "tree"])
+def test_the_checked_path_gives_the_same(native, name, dtype):
+    # integers for flags, a float of another type: valid, but not the usual call
+    class Float(float):
+        pass
+
+    entry, args = calls(dtype=dtype)[name]
+    i, other = {"packed": (7, 1), "rope": (6, 0), "rope_append": (11, 1), "tree": (7, Float(64 ** -0.5))}[name]
+    unusual = args[:i] + [other] + args[i + 1:]
+    assert getattr(native, name)(*unusual) is None
+    caches = args[3:5] if name == "rope_append" else []
+    got = [t.clone() for t in tensors(entry(*args)) + caches]
+    for t in caches:
+        t.zero_()
+    want = tensors(entry(*unusual)) + caches
+    if caches:  # rows that are not written were zeroed
+        for a, b in zip(got[-2:], caches):
+            a[b == 0] = 0
+    for a, b in zip(got, want):
+        assert a.shape == b.shape and a.dtype == b.dtype and torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_parameters_and_other_threads(native):
+    import threading
+    entry, args = calls()["rope"]
+    want = tensors(entry(*args))
+    args[1] = torch.nn.Parameter(args[1].clone(), requires_grad=True)
+    assert all(torch.equal(a, b) for a, b in zip(tensors(entry(*args)), want))
+    got = [[] for _ in range(4)]
+
+    def work(out):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                out[:] = tensors(entry(*args))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(g,)) for g in got]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))

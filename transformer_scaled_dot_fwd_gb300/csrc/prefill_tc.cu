@@ -45,18 +45,20 @@
 // KV tiles wholly above the causal diagonal or past kv_len are never loaded.
 //
 // Packed sequences (attn_fwd_packed) run the same kernel on token-major
-// (T, H, D) views: a plan kernel lists the query tiles of all sequences,
-// longest first, and an item's tiles start at its sequence's first token.  A
+// (T, H, D) views: a list holds the query tiles of all sequences, longest first
+// (each CTA makes a short one itself, a plan kernel a long one), and an item's tiles start at its sequence's first token.  A
 // K/V tile may then run into the next sequence, whose keys the row limits
 // hide; its values are hidden by P = 0, which would not hold against an
 // infinity or a NaN (0 * inf).  So warps 2-3, idle otherwise, look over
 // every V tile that some row sees only a part of before its MMA (the edge
 // tiles: on the diagonal, or past the sequence's end): rows past the end become
-// zeros, and non-finite elements become zeros that the epilogue adds back, to the
-// rows that see them only.  Measured (H 32, H_kv 8, D 128, causal): sequences of
-// 8192, 5001, 4097 and 1023 tokens 610 us (1480 TFLOP/s); 23 sequences of 2048 to 1
-// tokens 98 us, of it about 27 us the boundaries of nine items a CTA; 16 sequences
-// of 512 tokens 64 us against 53 us for the same as one dense batch.
+// zeros, and non-finite elements become zeros that are added back after the
+// epilogue, to the rows that see them only.  Measured (H 32, H_kv 8, D 128, causal):
+// sequences of 8192, 5001, 4097 and 1023 tokens 608-615 us (1460-1485 TFLOP/s); 23
+// sequences of 2048 to 1 tokens 93 us, of it about 27 us the boundaries of nine items
+// a CTA; 16 sequences of 512 tokens 58 us, as one dense batch 53 us (with H_kv 32, two
+// edge tiles an item, 71 and 61 us); 4 of 2048 tokens 112 and 110 us (120 and 114 us).
+// Without edge tiles the gap halves.
 #include "kernels.h"
 #include "prefill_sched.cuh"
 #include "ptx.cuh"

@@ -36,11 +36,10 @@
 // Measured (H 32, H_kv 8, D 128): 16 sequences of 2000-8192 rows, up to 24 drafts
 // (323 MB to read): 63 us, of it 49 us at 6.6 TB/s between the first and the last
 // tile, 4 us the merge.  64 sequences of 4096-8192 rows, 63 drafts (1.69 GB, 407
-// GFLOP): 316-333 us, 1220-1290 TFLOP/s, a pair of tiles in 1.7 us.  One sequence
-// of 1500 rows, 8 drafts: 14 us.  The first form, a CTA per 576-4608 keys of a
-// head with one stream, two to an SM, took 98, 526 and 14 us: its splits' partial
-// results were a third of the cache's bytes, and a single stream waits for its own
-// MMAs.
+// GFLOP): 314-329 us, 1240-1295 TFLOP/s, a pair of tiles in 1.7 us.  One sequence
+// of 1500 rows, 8 drafts: 13 us.  The first form, splits of a fixed number of keys
+// with a CTA and one stream each, two to an SM, took 98, 526 and 14 us: a single
+// stream waits for its own MMAs.
 //
 // Roles (12 warps): warp 0 walks the CTA's run and loads K_j, V_j through a ring
 // of 128-row TMA tiles, warp 1 allocates TMEM and issues the MMAs, warps 2-3
@@ -69,8 +68,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kHugeLog2 = 16777216.0f;  // 2^24
 // Fewest tiles a CTA takes: below it a run costs more to start and merge than to
-// compute (1, 2 and 4 tiles: 22, 18 and 18 us for one sequence of 1500 rows when
-// this was swept).
+// compute (1, 2, 3, 4 and 6 tiles: 16.7, 14.1, 14.0, 14.4 and 15.5 us for one
+// sequence of 1500 rows).
 #ifndef ATTN_TREE_MIN_TILES
 #define ATTN_TREE_MIN_TILES 2
 #endif
