@@ -1,28 +1,28 @@
 // fp32 attention over tiles on the CUDA cores (FFMA only, no TF32): packed
 // sequences (attn_fwd_packed) and trees of drafted tokens (attn_decode_tree).
 //
-// 32 query rows against tiles of 64 keys, online softmax in log2 units.  A group
-// of 128 threads holds the 32 x 64 scores as 4 x 4 each (rows 4 ty + i, keys tx +
-// 16 j) and the 32 x D output as 4 rows x D / 16 columns each: a K or V element
-// read from shared memory serves 4 rows, a Q or P element 4 keys or D / 16 columns,
-// so the FMA pipe, not shared memory, is the bound.  FMAs go in pairs (two depths
-// of a score, two columns of the output).  The sixteen threads that share rows are
-// half a warp: row sums are four shuffles.  K rows are padded by 16 bytes so that
-// sixteen lanes read sixteen rows without conflicts.  The next tile's K is copied in
-// (cp.async) while P V runs, its V while the scores are computed.
+// 32 query rows against tiles of 32 keys, online softmax in log2 units.  A warp
+// holds 16 rows x 32 keys of scores as 4 x 4 a thread (rows ty + 4 i, keys tx + 8 j)
+// and 16 x D of output as 4 rows x D / 8 columns a thread.  FMAs go in pairs (two
+// depths of a score, two columns of the output).  The eight lanes that share rows
+// differ in bits 1-3 of their number: then lanes 2 l and 2 l + 1 read the same K and V
+// elements, lanes l and l ^ 2 the same Q and P elements, and a 16-byte shared-memory
+// load takes two passes instead of four (passes of the whole kernel 5.6 to 3.4 million;
+// the FMA pipe is the bound).  K rows are padded by 16 bytes so that eight lanes read
+// eight rows without conflicts.  The next tile's K is copied in (cp.async) while P V
+// runs, its V while the scores are computed.
 //
 // Few rows and long keys leave one warp per scheduler waiting on shared memory
-// and shuffles, so a block has several groups that share the keys of the same rows
-// equally (in units of 16, so that 64 or 513 keys leave no group idle) and join their output, max and sum at the end: as many as shared
-// memory holds, which also means one block an SM, so that a block left over goes
-// to the SM that is done first and not beside a long one.
+// and shuffles, so a block has several workers, pairs of warps, that share the keys of
+// the same rows equally (in units of 8) and join their output, max and sum at the end:
+// as many as shared memory holds, which also means one block an SM, so that a block
+// left over goes to the SM that is done first and not beside a long one.
 //
 // Measured: six sequences of 700 to 1 tokens, 4 heads of depth 64, not causal (0.86
-// GFLOP): 40 us; with whole tiles in turn 43 us, one group a block 90 us, two groups
-// and two blocks an SM 47 us.  A tile takes 1.8 us of an SM, 1.6 times its FMAs'
-// time; 232 blocks on 152 SMs leave a second round to the long ones.  8 rows a thread (half the
-// loads, half the warps) came to 45 us, 8 rows a warp with the keys over its lanes
-// to 47 us.
+// GFLOP): 39 us; 232 blocks on 152 SMs leave a second round to some of the long ones.
+// Earlier forms, 128 threads a tile of 64 keys: one a block 90 us, two 47 us, four 43
+// us, with equal shares 40 us; 8 rows a thread 45 us.  Two blocks of four workers
+// an SM: 48 us.
 //
 // Packed rows: a block's 32 rows lie in one sequence (a block that straddled two
 // would walk the keys of both), found by a search, not a table: sequence s
@@ -39,13 +39,12 @@
 namespace attn {
 namespace {
 
-constexpr int kRows = 32;
-constexpr int kKeys = 64;
-constexpr int kGroup = 128;      // threads of a group
+constexpr int kRows = 32;        // of a block
+constexpr int kKeys = 32;        // of a tile
 template <int D>
-constexpr int kGroups = D == 64 ? 4 : 2;
+constexpr int kWorkers = D == 64 ? 8 : 4;  // pairs of warps
 template <int D>
-constexpr int kThreads = kGroups<D> * kGroup;
+constexpr int kThreads = kWorkers<D> * 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -54,12 +53,13 @@ struct F32Smem {
     float q[kRows][D + 4];
     struct {
         float k[kKeys][D + 4];
-        float v[kKeys][D];       // after the walk: the group's output, [kRows][D]
-        float p[kRows][kKeys + 4];
-    } g[kGroups<D>];
-    float2 ml[kGroups<D>][kRows];  // each group's max and sum
+        float v[kKeys][D];       // after the walk: the worker's output, [kRows][D]
+        float p[2][kRows / 2][kKeys + 8];
+    } w[kWorkers<D>];
+    float2 ml[kWorkers<D>][kRows];  // each worker's max and sum
     Ancestors anc;
 };
+static_assert(kRows == kKeys, "a worker's output takes its V tile's place");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -68,33 +68,38 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Running state of a thread's four rows: columns 64 c + 4 tx + e, in pairs.
+// Running state of a thread's four rows, row(i): columns 32 c + 4 tx + e, in pairs.
 template <int D>
 struct Rows4 {
     float m[4], l[4];
-    uint64_t o[4][D / 32];
+    uint64_t o[4][D / 16];
 };
+// Lane l is thread (tx, ty): bits 0 and 4 of l are ty, the others tx.
+__device__ __forceinline__ int tx_of() { return static_cast<int>(threadIdx.x / 2 % 8); }
+__device__ __forceinline__ int ty_of() { return static_cast<int>(threadIdx.x % 2 + threadIdx.x / 16 % 2 * 2); }
+__device__ __forceinline__ int row_of(int i) { return static_cast<int>(threadIdx.x / 32 % 2) * (kRows / 2) + ty_of() + 4 * i; }
 
-// This group's part of keys [k0, k1), an equal share in units of 16 keys (the whole
+// This worker's part of keys [k0, k1), an equal share in units of 8 keys (the whole
 // block calls it, with the copies of Q committed as one group): K row j at
 // kbase + j * ks, V row j at vbase + j * vs.  visible(i, key0) gives the bits of
-// keys key0 + tx + 16 j, j < 4, of row 4 ty + i.
+// keys key0 + tx + 8 j, j < 4, of row_of(i).
 template <int D, typename Visible>
 __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long long ks, const float *vbase,
                                      long long vs, int k0, int k1, float sl2, Rows4<D> &st, Visible visible) {
-    const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, tx = tid % 16, ty = tid / 16;
-    auto &sm = smem.g[group];
-    const auto sync = [&] { named_bar_sync(1 + group, kGroup); };
-    constexpr int C = D / 64;
-    const int per = (max(k1 - k0, 0) + 16 * kGroups<D> - 1) / (16 * kGroups<D>) * 16;
-    const int first = k0 + group * per, last = min(first + per, k1);  // no keys if last <= first
-    // the key units of 16 in the tile at key0; rows past the last key are zeros
-    auto units = [&](int key0) { return min((last - key0 + 15) / 16, kKeys / 16); };
+    const int worker = threadIdx.x / 64, tid = threadIdx.x % 64, half = tid / 32, tx = tx_of(), ty = ty_of();
+    auto &sm = smem.w[worker];
+    auto &sp = sm.p[half];
+    const auto sync = [&] { named_bar_sync(1 + worker, 64); };
+    constexpr int C = D / 32;
+    const int per = (max(k1 - k0, 0) + 8 * kWorkers<D> - 1) / (8 * kWorkers<D>) * 8;
+    const int first = k0 + worker * per, last = min(first + per, k1);  // no keys if last <= first
+    // the key units of 8 in the tile at key0; rows past the last key are zeros
+    auto units = [&](int key0) { return min((last - key0 + 7) / 8, kKeys / 8); };
     auto load = [&](float *dst, int stride, const float *base, long long gs, int key0) {
         const uint32_t to = smem_u32(dst);
-        const int n = units(key0) * (16 * D / 4);
+        const int n = units(key0) * (8 * D / 4);
 #pragma unroll 8
-        for (int i = tid; i < n; i += kGroup) {
+        for (int i = tid; i < n; i += 64) {
             const int row = i / (D / 4), c = i % (D / 4);
             const bool in = key0 + row < last;
             cp_async16(to + (row * stride + 4 * c) * 4, base + (in ? key0 + row : k0) * gs + 4 * c, in ? 16u : 0u);
@@ -104,7 +109,7 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
     if (first < last) {
         load(&sm.k[0][0], D + 4, kbase, ks, first);
         load(&sm.v[0][0], D, vbase, vs, first);
-        cp_async_wait<2>();  // Q, copied in before by all groups
+        cp_async_wait<2>();  // Q, copied in before by the whole block
     } else {
         cp_async_wait<0>();
     }
@@ -122,9 +127,9 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
             for (int d = 0; d < D; d += 4) {
                 ulonglong2 qa[4], kb[N];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const ulonglong2 *>(&smem.q[4 * ty + i][d]);
+                for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const ulonglong2 *>(&smem.q[row_of(i)][d]);
 #pragma unroll
-                for (int j = 0; j < N; ++j) kb[j] = *reinterpret_cast<const ulonglong2 *>(&sm.k[tx + 16 * j][d]);
+                for (int j = 0; j < N; ++j) kb[j] = *reinterpret_cast<const ulonglong2 *>(&sm.k[tx + 8 * j][d]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -141,11 +146,11 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
                 for (int j = 0; j < N; ++j) {
                     // rounded before the difference below: huge scores
                     s[j] = __fmul_rn(f2_lo(s2[i][j]) + f2_hi(s2[i][j]), sl2);
-                    hidden = hidden || (!(see >> j & 1u) && key0 + tx + 16 * j < k1);
+                    hidden = hidden || (!(see >> j & 1u) && key0 + tx + 8 * j < k1);
                     if (see >> j & 1u) mt = fmaxf(mt, s[j]);
                 }
 #pragma unroll
-                for (int x = 1; x < 16; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+                for (int x = 2; x < 16; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
                 const float mn = fmaxf(st.m[i], mt);
                 const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet (or nothing but -inf)
                 const float corr = ex2_approx(st.m[i] - ref);
@@ -155,12 +160,12 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
                 for (int j = 0; j < N; ++j) {
                     const float p = see >> j & 1u ? ex2_approx(s[j] - ref) : 0.f;
                     sum += p;
-                    sm.p[4 * ty + i][tx + 16 * j] = p;
+                    sp[ty + 4 * i][tx + 8 * j] = p;
                 }
-                st.l[i] = st.l[i] * corr + sum;  // this thread's keys; summed over the half warp at the end
+                st.l[i] = st.l[i] * corr + sum;  // this thread's keys; summed over the eight lanes at the end
                 const uint64_t corr2 = f2_pack(corr, corr);
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) st.o[i][e] = fmul2(st.o[i][e], corr2);
+                for (int e = 0; e < 2 * C; ++e) st.o[i][e] = fmul2(st.o[i][e], corr2);
             }
         };
         if (n_units == 4)
@@ -175,30 +180,35 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
         // of zero must not meet an infinite or NaN value
         const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
-        sync();              // all scores are done with K; P is visible
+        sync();              // both warps are done with K; V and P are visible
         if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + kKeys);
         auto mix = [&](auto guarded) {
-#pragma unroll 2
-            for (int j = 0; j < 16 * n_units; j += 4) {
+#pragma unroll 1
+            for (int j = 0; j < 8 * n_units; j += 4) {
                 float4 p4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(&sm.p[4 * ty + i][j]);
+                for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(&sp[ty + 4 * i][j]);
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj)
+                for (int jj = 0; jj < 4; ++jj) {
+                    uint64_t p2[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p = jj == 0 ? p4[i].x : jj == 1 ? p4[i].y : jj == 2 ? p4[i].z : p4[i].w;
+                        p2[i] = f2_pack(p, p);
+                    }
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sm.v[j + jj][64 * c + 4 * tx]);
+                        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sm.v[j + jj][32 * c + 4 * tx]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float p = jj == 0 ? p4[i].x : jj == 1 ? p4[i].y : jj == 2 ? p4[i].z : p4[i].w;
-                            const uint64_t p2 = f2_pack(p, p);
-                            const uint64_t a = ffma2(p2, x.x, st.o[i][2 * c]), b = ffma2(p2, x.y, st.o[i][2 * c + 1]);
-                            if (!decltype(guarded)::value || p != 0.f) {
+                            const uint64_t a = ffma2(p2[i], x.x, st.o[i][2 * c]), b = ffma2(p2[i], x.y, st.o[i][2 * c + 1]);
+                            if (!decltype(guarded)::value || f2_lo(p2[i]) != 0.f) {
                                 st.o[i][2 * c] = a;
                                 st.o[i][2 * c + 1] = b;
                             }
                         }
                     }
+                }
             }
         };
         if (edge)
@@ -212,7 +222,7 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int x = 1; x < 16; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
+        for (int x = 2; x < 16; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
 }
 
 template <int D>
@@ -222,54 +232,62 @@ __device__ __forceinline__ void reset(Rows4<D> &st) {
         st.m[i] = -INFINITY;
         st.l[i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) st.o[i][e] = 0;
+        for (int e = 0; e < D / 16; ++e) st.o[i][e] = 0;
     }
 }
 
-// The other groups' parts into group 0's registers, in order (the whole block
-// calls it; the others' own state is left as it was).
+// The workers' parts of one row, joined in order: thread t holds C float4 of row
+// t / kLanes, columns 4 (t % kLanes + kLanes c).
 template <int D>
-__device__ __forceinline__ void join_groups(F32Smem<D> &sm, Rows4<D> &st) {
-    const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, tx = tid % 16, ty = tid / 16;
-    if (group > 0) {
-        float *po = &sm.g[group].v[0][0];
+struct Joined {
+    static constexpr int kLanes = kThreads<D> / kRows, C = D / 4 / kLanes;
+    float m, l;
+    float4 o[C];
+    static __device__ __forceinline__ int row() { return static_cast<int>(threadIdx.x) / kLanes; }
+    static __device__ __forceinline__ int column(int c) { return 4 * (static_cast<int>(threadIdx.x) % kLanes + kLanes * c); }
+    __device__ __forceinline__ float4 times(int c, float f) const {
+        return make_float4(o[c].x * f, o[c].y * f, o[c].z * f, o[c].w * f);
+    }
+};
+
+// The whole block calls it.
+template <int D>
+__device__ __forceinline__ Joined<D> join_workers(F32Smem<D> &sm, const Rows4<D> &st) {
+    using J = Joined<D>;
+    const int worker = threadIdx.x / 64, tx = tx_of();
+    float *po = &sm.w[worker].v[0][0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (tx == 0) sm.ml[group][4 * ty + i] = make_float2(st.m[i], st.l[i]);
+    for (int i = 0; i < 4; ++i) {
+        if (tx == 0) sm.ml[worker][row_of(i)] = make_float2(st.m[i], st.l[i]);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-                *reinterpret_cast<ulonglong2 *>(po + (4 * ty + i) * D + 64 * c + 4 * tx) =
-                    make_ulonglong2(st.o[i][2 * c], st.o[i][2 * c + 1]);
-        }
+        for (int c = 0; c < D / 32; ++c)
+            *reinterpret_cast<ulonglong2 *>(po + row_of(i) * D + 32 * c + 4 * tx) =
+                make_ulonglong2(st.o[i][2 * c], st.o[i][2 * c + 1]);
     }
     __syncthreads();
-    if (group > 0) return;
-#pragma unroll 1
-    for (int y = 1; y < kGroups<D>; ++y) {
-        const float *po = &sm.g[y].v[0][0];
+    J r;
+    r.m = -INFINITY;
+    r.l = 0.f;
+    float2 ml[kWorkers<D>];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = sm.ml[y][4 * ty + i];
-            const float mn = fmaxf(st.m[i], x.x), ref = mn == -INFINITY ? 0.f : mn;
-            const float w0 = ex2_approx(st.m[i] - ref), w1 = ex2_approx(x.x - ref);
-            st.m[i] = mn;
-            st.l[i] = st.l[i] * w0 + x.y * w1;
-            const uint64_t a = f2_pack(w0, w0), b = f2_pack(w1, w1);
+    for (int y = 0; y < kWorkers<D>; ++y) {
+        ml[y] = sm.ml[y][J::row()];
+        r.m = fmaxf(r.m, ml[y].x);
+    }
+    const float ref = r.m == -INFINITY ? 0.f : r.m;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(po + (4 * ty + i) * D + 64 * c + 4 * tx);
-                st.o[i][2 * c] = ffma2(o.x, b, fmul2(st.o[i][2 * c], a));
-                st.o[i][2 * c + 1] = ffma2(o.y, b, fmul2(st.o[i][2 * c + 1], a));
-            }
+    for (int c = 0; c < J::C; ++c) r.o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int y = 0; y < kWorkers<D>; ++y) {
+        const float w = ex2_approx(ml[y].x - ref);
+        r.l = fmaf(w, ml[y].y, r.l);
+#pragma unroll
+        for (int c = 0; c < J::C; ++c) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.w[y].v[J::row()][J::column(c)]);
+            r.o[c] = make_float4(fmaf(w, x.x, r.o[c].x), fmaf(w, x.y, r.o[c].y), fmaf(w, x.z, r.o[c].z), fmaf(w, x.w, r.o[c].w));
         }
     }
-}
-
-// Row i's columns from 64 c + 4 tx, times f.
-template <int D>
-__device__ __forceinline__ float4 columns(const Rows4<D> &st, int i, int c, float f) {
-    return make_float4(f2_lo(st.o[i][2 * c]) * f, f2_hi(st.o[i][2 * c]) * f, f2_lo(st.o[i][2 * c + 1]) * f,
-                       f2_hi(st.o[i][2 * c + 1]) * f);
+    return r;
 }
 
 // ------------------------------------------------------------ packed sequences
@@ -296,7 +314,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const Packed
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
     F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid % kGroup / 16;
+    const int tid = threadIdx.x, tx = tx_of();
     const int h = blockIdx.x % a.H, w = blockIdx.x / a.H, g = h / (a.H / a.H_kv);
     const int s = blocks_le(a.cu_seqlens, a.B, w, a.Sq, tid % 32) - 1;
     if (s < 0) return;
@@ -314,28 +332,24 @@ __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const Packed
     const int k1 = a.causal ? end : c1;
     int hi[4];  // rows see keys [c0, hi)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) hi[i] = a.causal ? min(t0 + 4 * ty + i + 1, k1) : k1;
+    for (int i = 0; i < 4; ++i) hi[i] = a.causal ? min(t0 + row_of(i) + 1, k1) : k1;
     Rows4<D> st;
     reset(st);
     walk<D>(sm, static_cast<const float *>(a.k) + g * a.k_hs, a.k_ts, static_cast<const float *>(a.v) + g * a.v_hs,
             a.v_ts, c0, k1, a.scale * kLog2e, st, [&](int i, int key0) {
                 uint32_t see = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) see |= (key0 + tx + 16 * j < hi[i] ? 1u : 0u) << j;
+                for (int j = 0; j < 4; ++j) see |= (key0 + tx + 8 * j < hi[i] ? 1u : 0u) << j;
                 return see;
             });
-    join_groups(sm, st);
-    if (tid >= kGroup) return;
+    const Joined<D> x = join_workers(sm, st);
+    const long long t = t0 + x.row();
+    if (t >= end) return;
+    const float inv = 1.f / x.l;
+    float *O = static_cast<float *>(a.out) + t * a.o_ts + h * a.o_hs;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const long long t = t0 + 4 * ty + i;
-        if (t >= end) break;
-        const float inv = 1.f / st.l[i];
-        float *O = static_cast<float *>(a.out) + t * a.o_ts + h * a.o_hs;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) *reinterpret_cast<float4 *>(O + 64 * c + 4 * tx) = columns(st, i, c, inv);
-        if (a.lse && tx == 0) a.lse[t * a.H + h] = (st.m[i] + log2f(st.l[i])) * kLn2;
-    }
+    for (int c = 0; c < x.C; ++c) *reinterpret_cast<float4 *>(O + x.column(c)) = x.times(c, inv);
+    if (a.lse && x.column(0) == 0) a.lse[t * a.H + h] = (x.m + log2f(x.l)) * kLn2;
 }
 
 template <int D>
@@ -357,7 +371,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
     F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid % kGroup / 16;
+    const int tid = threadIdx.x, tx = tx_of();
     const int m = blockIdx.x % row_tiles, c = (blockIdx.x / row_tiles) % a.n_split;
     const int bk = blockIdx.x / row_tiles / a.n_split, b = bk / a.H_kv, g = bk % a.H_kv;
     const int G = a.H / a.H_kv, rows = G * a.T, r0 = m * kRows;
@@ -372,12 +386,12 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
         cp_async16(smem_u32(&sm.q[i / (D / 4)][col]), q, in ? 16u : 0u);
     }
     cp_async_commit();
-    if (tid < kGroup) build_ancestors<kGroup>(a, b, d, sm.anc, tid, [] { named_bar_sync(1, kGroup); });
+    if (tid < 128) build_ancestors<128>(a, b, d, sm.anc, tid, [] { named_bar_sync(1, 128); });
     bool live[4];
     const uint32_t *w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * ty + i, t = r % a.T;
+        const int r = r0 + row_of(i), t = r % a.T;
         live[i] = r < rows && t < d.n && d.past + t >= 0;
         w[i] = sm.anc.bits[t];
     }
@@ -390,31 +404,27 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
                     uint32_t see = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        see |= (visible32(w[i], key0 + 16 * j + tx - d.past) & 1u) << j;
+                        see |= (visible32(w[i], key0 + 8 * j + tx - d.past) & 1u) << j;
                     return live[i] ? see : 0u;
                 });
     } else {
         cp_async_wait<0>();
     }
-    join_groups(sm, st);
-    if (tid >= kGroup) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * ty + i;
-        if (r >= rows) continue;
-        float *O;
-        float f = 1.f;
-        if (a.n_split == 1) {
-            O = static_cast<float *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + (r % a.T) * a.o_ts;
-            f = live[i] ? 1.f / st.l[i] : 0.f;
-        } else {
-            const size_t part = (static_cast<size_t>(bk) * rows + r) * a.n_split + c;
-            O = a.part_o + part * D;
-            if (tx == 0) *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(st.m[i], st.l[i]);
-        }
-#pragma unroll
-        for (int cc = 0; cc < D / 64; ++cc) *reinterpret_cast<float4 *>(O + 64 * cc + 4 * tx) = columns(st, i, cc, f);
+    const Joined<D> x = join_workers(sm, st);
+    const int r = r0 + x.row(), t = r % a.T;
+    if (r >= rows) return;
+    float *O;
+    float f = 1.f;
+    if (a.n_split == 1) {
+        O = static_cast<float *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts;
+        f = t < d.n && d.past + t >= 0 ? 1.f / x.l : 0.f;
+    } else {
+        const size_t part = (static_cast<size_t>(bk) * rows + r) * a.n_split + c;
+        O = a.part_o + part * D;
+        if (x.column(0) == 0) *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(x.m, x.l);
     }
+#pragma unroll
+    for (int cc = 0; cc < x.C; ++cc) *reinterpret_cast<float4 *>(O + x.column(cc)) = x.times(cc, f);
 }
 
 template <int D>
@@ -439,12 +449,12 @@ cudaError_t launch_packed_f32(const PackedArgs &a) {
 }
 
 int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int D, int n_sm) {
-    // a few rounds of the blocks an SM holds, at least two tiles a block (four sequences
-    // of up to 1024 keys: 14 us with one or two tiles, 18 with four, 30 with eight)
+    // a few rounds of the blocks an SM holds, at least 128 keys a block (four sequences
+    // of up to 1024 keys: 14 us with 64 or 128 keys a block, 18 with 256, 30 with 512)
     const int rows = (H / H_kv) * T;
     const long long units = static_cast<long long>(B) * H_kv * ((rows + kRows - 1) / kRows);
     const long long tiles = (static_cast<long long>(Skv) + kKeys - 1) / kKeys;
-    const long long want = 4LL * (n_sm > 0 ? n_sm : 1), least = 2;
+    const long long want = 4LL * (n_sm > 0 ? n_sm : 1), least = 4;
     long long per = (units * tiles + want - 1) / want;
     per = (per + least - 1) / least * least;
     per = per < least ? least : per;
