@@ -362,3 +362,11 @@ def test_overlapping_sequences_stay_inside(gpu, n):
     attn.attn_fwd_packed(q, k, v, ints([0, T] * n), out=big[1:T + 1], causal=True)
     attn.attn_device_status()
     assert torch.all(big[0] == 5) and torch.all(big[-1] == 5)
+
+
+# fp32: few blocks are clusters of 2, 4 or 8 CTAs that share the keys
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[200], [300, 200], [600], [1100], [1025, 1]])
+@pytest.mark.parametrize("causal", [True, False])
+def test_fp32_clusters(gpu, lens, D, causal):
+    case(lens, 2, 1, D, causal, dtype=F32, seed=21)

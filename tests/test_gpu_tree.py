@@ -302,3 +302,18 @@ def test_empty_calls_and_refusals(gpu):
         with pytest.raises(attn.AttnError) as e:
             attn.attn_decode_tree(q, kc, vc, par, **kw)
         assert e.value.code == attn.ATTN_EINVAL
+
+
+# fp32: up to eight splits are a cluster (the sizes below give 1, 2, 4, 8 of them, some
+# past a sequence's end), more leave their parts in the workspace
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Skv", [100, 129, 256, 257, 400, 513, 1024, 1025, 3000])
+def test_fp32_splits(gpu, Skv, D):
+    lens = [Skv, max(Skv // 2, 5), 5, 0, Skv - 1]
+    T = 5
+    case(len(lens), 6, 2, T, Skv, D, dtype=F32, lens=lens, drafts=[T, T, T, 0, 3], seed=Skv)
+
+
+@pytest.mark.parametrize("G,T", [(1, 1), (1, 16), (1, 17), (2, 8), (4, 7), (1, 33)])
+def test_fp32_rows_of_one_warp(gpu, G, T):
+    case(2, 2 * G, 2, T, 300, 64, dtype=F32, lens=[300, 177], drafts=[T, max(T - 1, 1)], seed=T)

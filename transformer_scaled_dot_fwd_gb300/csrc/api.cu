@@ -779,9 +779,9 @@ ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int
         return ATTN_EINVAL;
     if (T == 0 || Skv == 0) return 0;
     if (dtype == ATTN_F32) {
-        const long long chunk = tree_chunk_f32(B, H, H_kv, T, Skv, D, num_sms());
-        const long long n_split = (Skv + chunk - 1) / chunk;
-        return n_split == 1 ? 0 : static_cast<long long>(B) * H * T * n_split * (D + 2) * 4;
+        const int chunk = tree_chunk_f32(B, H, H_kv, T, Skv, D, num_sms());
+        const long long n_split = tree_splits_f32(Skv, chunk);
+        return n_split <= kTreeClusterF32 ? 0 : static_cast<long long>(B) * H * T * n_split * (D + 2) * 4;
     }
     const long long grid = tree_tc_grid(B, H, H_kv, T, Skv, num_sms());
     if (grid < 0) return ATTN_EINVAL;
@@ -857,7 +857,7 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
     const long long rows = static_cast<long long>(B) * H * T;
     if (rows >= (1LL << 31) || bh_kv * Skv >= (1LL << 31)) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
     const int chunk = f32 && Skv > 0 ? tree_chunk_f32(B, H, H_kv, T, Skv, D, num_sms()) : 64;
-    const int n_split = !f32 ? tree_tc_grid(B, H, H_kv, T, Skv, num_sms()) : Skv > 0 ? (Skv + chunk - 1) / chunk : 1;
+    const int n_split = !f32 ? tree_tc_grid(B, H, H_kv, T, Skv, num_sms()) : Skv > 0 ? tree_splits_f32(Skv, chunk) : 1;
     if (n_split < 0) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
     if (f32 && bh_kv * n_split * (((H / H_kv) * static_cast<long long>(T) + 31) / 32) >= (1LL << 31))
         return fail(ATTN_EINVAL, "%s: the sizes are too large", who);

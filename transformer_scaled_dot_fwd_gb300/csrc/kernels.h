@@ -95,7 +95,13 @@ struct TreeArgs {
     cudaStream_t stream;
     int n_sm;
 };
-// fp32: keys per split for these sizes.
+// fp32: keys per split for these sizes.  Splits of up to kTreeClusterF32 (a power of two
+// of them) are the CTAs of a cluster and need no workspace.
+constexpr int kTreeClusterF32 = 8;
+inline int tree_splits_f32(int Skv, int chunk) {
+    const int n = (Skv + chunk - 1) / chunk;
+    return n <= 2 || n > kTreeClusterF32 ? n : n <= 4 ? 4 : 8;
+}
 int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int D, int n_sm);
 // bf16: CTAs for these sizes (-1: too large), and rows of a workspace slot.
 int tree_tc_grid(int B, int H, int H_kv, int T, int Skv, int n_sm);

@@ -57,6 +57,8 @@ struct F32Smem {
         float p[2][kRows / 2][kKeys + 8];
     } w[kWorkers<D>];
     float2 ml[kWorkers<D>][kRows];  // each worker's max and sum
+    float4 joined[kRows * D / 4];   // this CTA's part, read by the first CTA of its cluster
+    float2 joined_ml[kRows];
     Ancestors anc;
 };
 static_assert(kRows == kKeys, "a worker's output takes its V tile's place");
@@ -82,10 +84,11 @@ __device__ __forceinline__ int row_of(int i) { return static_cast<int>(threadIdx
 // This worker's part of keys [k0, k1), an equal share in units of 8 keys (the whole
 // block calls it, with the copies of Q committed as one group): K row j at
 // kbase + j * ks, V row j at vbase + j * vs.  visible(i, key0) gives the bits of
-// keys key0 + tx + 8 j, j < 4, of row_of(i).
+// keys key0 + tx + 8 j, j < 4, of row_of(i).  A warp none of whose rows is used
+// (`active` is false) only copies and keeps step.
 template <int D, typename Visible>
 __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long long ks, const float *vbase,
-                                     long long vs, int k0, int k1, float sl2, Rows4<D> &st, Visible visible) {
+                                     long long vs, int k0, int k1, float sl2, bool active, Rows4<D> &st, Visible visible) {
     const int worker = threadIdx.x / 64, tid = threadIdx.x % 64, half = tid / 32, tx = tx_of(), ty = ty_of();
     auto &sm = smem.w[worker];
     auto &sp = sm.p[half];
@@ -168,7 +171,8 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
                 for (int e = 0; e < 2 * C; ++e) st.o[i][e] = fmul2(st.o[i][e], corr2);
             }
         };
-        if (n_units == 4)
+        if (!active) {
+        } else if (n_units == 4)
             score(std::integral_constant<int, 4>{});
         else if (n_units == 3)
             score(std::integral_constant<int, 3>{});
@@ -211,7 +215,8 @@ __device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long 
                 }
             }
         };
-        if (edge)
+        if (!active) {
+        } else if (edge)
             mix(std::true_type{});
         else
             mix(std::false_type{});
@@ -290,6 +295,87 @@ __device__ __forceinline__ Joined<D> join_workers(F32Smem<D> &sm, const Rows4<D>
     return r;
 }
 
+// CTAs of a cluster share the keys of the same rows.
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+    unsigned n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(const void *p, unsigned rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// The cluster's parts into those of its first CTA, in order of the keys; returns
+// whether this CTA is the one that holds the result.  Every thread calls it.
+template <int D>
+__device__ __forceinline__ bool join_cluster(F32Smem<D> &sm, Joined<D> &x) {
+    using J = Joined<D>;
+    const unsigned n = cluster_size(), rank = cluster_rank();
+    if (n == 1) return true;
+    const int tid = threadIdx.x;
+    if (rank > 0) {
+#pragma unroll
+        for (int c = 0; c < J::C; ++c) sm.joined[c * kThreads<D> + tid] = x.o[c];
+        if (tid % J::kLanes == 0) sm.joined_ml[J::row()] = make_float2(x.m, x.l);
+    }
+    cluster_sync();
+    if (rank == 0) {
+#pragma unroll 1
+        for (unsigned y = 1; y < n; ++y) {
+            float m, l;
+            float4 o[J::C];
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(m), "=f"(l)
+                         : "r"(map_rank(&sm.joined_ml[J::row()], y)));
+#pragma unroll
+            for (int c = 0; c < J::C; ++c)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(o[c].x), "=f"(o[c].y), "=f"(o[c].z), "=f"(o[c].w)
+                             : "r"(map_rank(&sm.joined[c * kThreads<D> + tid], y)));
+            const float mn = fmaxf(x.m, m), ref = mn == -INFINITY ? 0.f : mn;
+            const float w0 = ex2_approx(x.m - ref), w1 = ex2_approx(m - ref);
+            x.m = mn;
+            x.l = fmaf(w1, l, x.l * w0);
+#pragma unroll
+            for (int c = 0; c < J::C; ++c)
+                x.o[c] = make_float4(fmaf(w1, o[c].x, x.o[c].x * w0), fmaf(w1, o[c].y, x.o[c].y * w0),
+                                     fmaf(w1, o[c].z, x.o[c].z * w0), fmaf(w1, o[c].w, x.o[c].w * w0));
+        }
+    }
+    cluster_sync();  // the parts have been read
+    return rank == 0;
+}
+
+// launch_pdl with clusters of `cluster` consecutive blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned cluster, unsigned grid, unsigned block, size_t smem,
+                            cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // ------------------------------------------------------------ packed sequences
 
 // Number of sequences whose first block, cu[s] / kRows + s, is <= w (32 probes a step).
@@ -307,7 +393,7 @@ __device__ __forceinline__ int blocks_le(const int32_t *cu, int n, int w, int T,
     return lo;
 }
 
-// Block (h, w): head h, 32 rows of the sequence that owns block w.
+// Cluster (h, w): head h, 32 rows of the sequence that owns w.
 template <int D>
 __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const PackedArgs a) {
     griddep_launch_dependents();
@@ -315,9 +401,10 @@ __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const Packed
     extern __shared__ __align__(16) uint8_t f32_smem[];
     F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
     const int tid = threadIdx.x, tx = tx_of();
-    const int h = blockIdx.x % a.H, w = blockIdx.x / a.H, g = h / (a.H / a.H_kv);
+    const unsigned n_cta = cluster_size(), x = blockIdx.x / n_cta;
+    const int h = x % a.H, w = x / a.H, g = h / (a.H / a.H_kv);
     const int s = blocks_le(a.cu_seqlens, a.B, w, a.Sq, tid % 32) - 1;
-    if (s < 0) return;
+    if (s < 0) return;  // as every CTA of the cluster
     const int c0 = min(max(a.cu_seqlens[s], 0), a.Sq), c1 = min(max(a.cu_seqlens[s + 1], c0), a.Sq);
     const int t0 = c0 + (w - c0 / kRows - s) * kRows;  // first row
     if (t0 >= c1) return;                              // one of the empty blocks
@@ -329,27 +416,31 @@ __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const Packed
         cp_async16(smem_u32(&sm.q[r][4 * c]), Q + (in ? t0 + r : t0) * a.q_ts + 4 * c, in ? 16u : 0u);
     }
     cp_async_commit();
-    const int k1 = a.causal ? end : c1;
+    const int limit = a.causal ? end : c1;
     int hi[4];  // rows see keys [c0, hi)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) hi[i] = a.causal ? min(t0 + row_of(i) + 1, k1) : k1;
+    for (int i = 0; i < 4; ++i) hi[i] = a.causal ? min(t0 + row_of(i) + 1, limit) : limit;
+    // this CTA's share of the keys, in units of 8
+    const int share = (limit - c0 + 8 * static_cast<int>(n_cta) - 1) / (8 * static_cast<int>(n_cta)) * 8;
+    const int k0 = min(c0 + static_cast<int>(cluster_rank()) * share, limit), k1 = min(k0 + share, limit);
     Rows4<D> st;
     reset(st);
     walk<D>(sm, static_cast<const float *>(a.k) + g * a.k_hs, a.k_ts, static_cast<const float *>(a.v) + g * a.v_hs,
-            a.v_ts, c0, k1, a.scale * kLog2e, st, [&](int i, int key0) {
+            a.v_ts, k0, k1, a.scale * kLog2e, t0 + tid / 32 % 2 * (kRows / 2) < end, st, [&](int i, int key0) {
                 uint32_t see = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) see |= (key0 + tx + 8 * j < hi[i] ? 1u : 0u) << j;
                 return see;
             });
-    const Joined<D> x = join_workers(sm, st);
-    const long long t = t0 + x.row();
+    Joined<D> y = join_workers(sm, st);
+    if (!join_cluster(sm, y)) return;
+    const long long t = t0 + y.row();
     if (t >= end) return;
-    const float inv = 1.f / x.l;
+    const float inv = 1.f / y.l;
     float *O = static_cast<float *>(a.out) + t * a.o_ts + h * a.o_hs;
 #pragma unroll
-    for (int c = 0; c < x.C; ++c) *reinterpret_cast<float4 *>(O + x.column(c)) = x.times(c, inv);
-    if (a.lse && x.column(0) == 0) a.lse[t * a.H + h] = (x.m + log2f(x.l)) * kLn2;
+    for (int c = 0; c < y.C; ++c) *reinterpret_cast<float4 *>(O + y.column(c)) = y.times(c, inv);
+    if (a.lse && y.column(0) == 0) a.lse[t * a.H + h] = (y.m + log2f(y.l)) * kLn2;
 }
 
 template <int D>
@@ -358,13 +449,21 @@ cudaError_t launch_packed_f32_t(const PackedArgs &a) {
     cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(packed_f32_blocks(a.Sq, a.B) * a.H);
-    return launch_pdl(packed_f32_kernel<D>, dim3(grid), dim3(kThreads<D>), smem, a.stream, a);
+    const long long blocks = packed_f32_blocks(a.Sq, a.B) * a.H, sms = a.n_sm > 0 ? a.n_sm : 1;
+    // Fewer blocks than SMs: clusters of CTAs share the keys, 64 and more each at the mean
+    // length (300 and 200 tokens, 4 heads: 14.6 us without, 10.5 with).  More blocks than
+    // that lose by it: 232 blocks as 464 CTAs 41.3 against 39.8 us, 260 as 520 134 against
+    // 123 us.
+    unsigned cluster = 1;
+    while (cluster < 8 && blocks * cluster <= sms && a.Sq / a.B >= 128 * static_cast<int>(cluster)) cluster *= 2;
+    return launch_clusters(packed_f32_kernel<D>, cluster, static_cast<unsigned>(blocks * cluster), kThreads<D>, smem, a.stream, a);
 }
 
 // ------------------------------------------------------------ trees of drafted tokens
 
-// Block x: (sequence and key/value head, split of the cache, 32 rows).
+// Block x: (sequence and key/value head, 32 rows, split of the cache).  Up to eight
+// splits are a cluster, whose first CTA writes the result; more leave their parts in
+// the workspace.
 template <int D>
 __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs a, const int row_tiles) {
     griddep_launch_dependents();
@@ -372,12 +471,13 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     extern __shared__ __align__(16) uint8_t f32_smem[];
     F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
     const int tid = threadIdx.x, tx = tx_of();
-    const int m = blockIdx.x % row_tiles, c = (blockIdx.x / row_tiles) % a.n_split;
-    const int bk = blockIdx.x / row_tiles / a.n_split, b = bk / a.H_kv, g = bk % a.H_kv;
+    const bool cluster = a.n_split <= kTreeClusterF32;  // of a.n_split CTAs
+    const int c = blockIdx.x % a.n_split, m = blockIdx.x / a.n_split % row_tiles;
+    const int bk = blockIdx.x / a.n_split / row_tiles, b = bk / a.H_kv, g = bk % a.H_kv;
     const int G = a.H / a.H_kv, rows = G * a.T, r0 = m * kRows;
     const Draft d = draft_of(a, b);
     const int k0 = c * a.chunk, k1 = min(k0 + a.chunk, d.L);
-    if (k0 >= k1 && a.n_split > 1) return;  // the merge never reads this split
+    if (k0 >= k1 && !cluster) return;  // the merge never reads this split
     for (int i = tid; i < kRows * D / 4; i += kThreads<D>) {
         const int r = r0 + i / (D / 4), col = 4 * (i % (D / 4));
         const bool in = r < rows && r % a.T < d.n;
@@ -400,7 +500,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     const size_t head = static_cast<size_t>(bk) * a.Skv * D;
     if (k0 < k1) {
         walk<D>(sm, static_cast<const float *>(a.k) + head, D, static_cast<const float *>(a.v) + head, D, k0, k1,
-                a.scale * kLog2e, st, [&](int i, int key0) {
+                a.scale * kLog2e, __any_sync(0xffffffffu, live[0] || live[1] || live[2] || live[3]), st, [&](int i, int key0) {
                     uint32_t see = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -410,12 +510,13 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     } else {
         cp_async_wait<0>();
     }
-    const Joined<D> x = join_workers(sm, st);
+    Joined<D> x = join_workers(sm, st);
+    if (cluster && !join_cluster(sm, x)) return;
     const int r = r0 + x.row(), t = r % a.T;
     if (r >= rows) return;
     float *O;
     float f = 1.f;
-    if (a.n_split == 1) {
+    if (cluster) {
         O = static_cast<float *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts;
         f = t < d.n && d.past + t >= 0 ? 1.f / x.l : 0.f;
     } else {
@@ -435,8 +536,10 @@ cudaError_t launch_tree_f32_t(const TreeArgs &a) {
     if (e != cudaSuccess) return e;
     const int row_tiles = ((a.H / a.H_kv) * a.T + kRows - 1) / kRows;
     const unsigned grid = static_cast<unsigned>(a.B * a.H_kv) * a.n_split * row_tiles;
-    e = launch_pdl(tree_f32_kernel<D>, dim3(grid), dim3(kThreads<D>), smem, a.stream, a, row_tiles);
-    if (e != cudaSuccess || a.n_split == 1) return e;
+    const bool cluster = a.n_split <= kTreeClusterF32;
+    e = launch_clusters(tree_f32_kernel<D>, cluster ? static_cast<unsigned>(a.n_split) : 1u, grid, kThreads<D>, smem,
+                        a.stream, a, row_tiles);
+    if (e != cudaSuccess || cluster) return e;
     return launch_tree_merge_f32(a);
 }
 
@@ -450,7 +553,8 @@ cudaError_t launch_packed_f32(const PackedArgs &a) {
 
 int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int D, int n_sm) {
     // a few rounds of the blocks an SM holds, at least 128 keys a block (four sequences
-    // of up to 1024 keys: 14 us with 64 or 128 keys a block, 18 with 256, 30 with 512)
+    // of up to 1024 keys, splits merged by a second kernel: 14 us with 64 or 128 keys a
+    // block, 18 with 256, 30 with 512; as a cluster of eight, 128 each: 12.4 us)
     const int rows = (H / H_kv) * T;
     const long long units = static_cast<long long>(B) * H_kv * ((rows + kRows - 1) / kRows);
     const long long tiles = (static_cast<long long>(Skv) + kKeys - 1) / kKeys;
