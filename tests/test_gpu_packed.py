@@ -370,3 +370,11 @@ def test_overlapping_sequences_stay_inside(gpu, n):
 @pytest.mark.parametrize("causal", [True, False])
 def test_fp32_clusters(gpu, lens, D, causal):
     case(lens, 2, 1, D, causal, dtype=F32, seed=21)
+
+
+# fp32: many short blocks take half the workers, two blocks an SM
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[50] * 90, [200, 1, 129] * 20])
+@pytest.mark.parametrize("causal", [True, False])
+def test_fp32_many_blocks(gpu, lens, D, causal):
+    case(lens, 4, 2, D, causal, dtype=F32, seed=22)

@@ -317,3 +317,12 @@ def test_fp32_splits(gpu, Skv, D):
 @pytest.mark.parametrize("G,T", [(1, 1), (1, 16), (1, 17), (2, 8), (4, 7), (1, 33)])
 def test_fp32_rows_of_one_warp(gpu, G, T):
     case(2, 2 * G, 2, T, 300, 64, dtype=F32, lens=[300, 177], drafts=[T, max(T - 1, 1)], seed=T)
+
+
+# more blocks than SMs: two blocks an SM, of half the workers; as clusters, alone, and
+# with the workspace
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H_kv,T,Skv", [(90, 2, 3, 70), (40, 2, 9, 500), (24, 1, 40, 900), (12, 2, 5, 3000)])
+def test_fp32_many_blocks(gpu, B, H_kv, T, Skv, D):
+    lens = [max(0, Skv - 37 * b % Skv) for b in range(B)]
+    case(B, 2 * H_kv, H_kv, T, Skv, D, lens, [min(T, n) for n in lens], dtype=F32, seed=B)

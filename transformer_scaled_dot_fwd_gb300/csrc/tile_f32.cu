@@ -16,13 +16,13 @@
 // and shuffles, so a block has several workers, pairs of warps, that share the keys of
 // the same rows equally (in units of 8) and join their output, max and sum at the end:
 // as many as shared memory holds, which also means one block an SM, so that a block
-// left over goes to the SM that is done first and not beside a long one.
+// left over goes to the SM that is done first and not beside a long one; or half as
+// many and two blocks an SM, where there are many blocks (the launches say when).
 //
 // Measured: six sequences of 700 to 1 tokens, 4 heads of depth 64, not causal (0.86
 // GFLOP): 39 us; 232 blocks on 152 SMs leave a second round to some of the long ones.
 // Earlier forms, 128 threads a tile of 64 keys: one a block 90 us, two 47 us, four 43
-// us, with equal shares 40 us; 8 rows a thread 45 us.  Two blocks of four workers
-// an SM: 48 us.
+// us, with equal shares 40 us; 8 rows a thread 45 us.
 //
 // Packed rows: a block's 32 rows lie in one sequence (a block that straddled two
 // would walk the keys of both), found by a search, not a table: sequence s
@@ -41,22 +41,24 @@ namespace {
 
 constexpr int kRows = 32;        // of a block
 constexpr int kKeys = 32;        // of a tile
+// W workers (pairs of warps) a block: kMany<D> fill an SM's shared memory, half of them
+// leave room for a second block.
 template <int D>
-constexpr int kWorkers = D == 64 ? 8 : 4;  // pairs of warps
-template <int D>
-constexpr int kThreads = kWorkers<D> * 64;
+constexpr int kMany = D == 64 ? 8 : 4;
+template <int W>
+constexpr int kThreads = W * 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D>
+template <int D, int W>
 struct F32Smem {
     float q[kRows][D + 4];
     struct {
         float k[kKeys][D + 4];
         float v[kKeys][D];       // after the walk: the worker's output, [kRows][D]
         float p[2][kRows / 2][kKeys + 8];
-    } w[kWorkers<D>];
-    float2 ml[kWorkers<D>][kRows];  // each worker's max and sum
+    } w[W];
+    float2 ml[W][kRows];  // each worker's max and sum
     float4 joined[kRows * D / 4];   // this CTA's part, read by the first CTA of its cluster
     float2 joined_ml[kRows];
     Ancestors anc;
@@ -86,15 +88,15 @@ __device__ __forceinline__ int row_of(int i) { return static_cast<int>(threadIdx
 // kbase + j * ks, V row j at vbase + j * vs.  visible(i, key0) gives the bits of
 // keys key0 + tx + 8 j, j < 4, of row_of(i).  A warp none of whose rows is used
 // (`active` is false) only copies and keeps step.
-template <int D, typename Visible>
-__device__ __forceinline__ void walk(F32Smem<D> &smem, const float *kbase, long long ks, const float *vbase,
+template <int D, int W, typename Visible>
+__device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, long long ks, const float *vbase,
                                      long long vs, int k0, int k1, float sl2, bool active, Rows4<D> &st, Visible visible) {
     const int worker = threadIdx.x / 64, tid = threadIdx.x % 64, half = tid / 32, tx = tx_of(), ty = ty_of();
     auto &sm = smem.w[worker];
     auto &sp = sm.p[half];
     const auto sync = [&] { named_bar_sync(1 + worker, 64); };
     constexpr int C = D / 32;
-    const int per = (max(k1 - k0, 0) + 8 * kWorkers<D> - 1) / (8 * kWorkers<D>) * 8;
+    const int per = (max(k1 - k0, 0) + 8 * W - 1) / (8 * W) * 8;
     const int first = k0 + worker * per, last = min(first + per, k1);  // no keys if last <= first
     // the key units of 8 in the tile at key0; rows past the last key are zeros
     auto units = [&](int key0) { return min((last - key0 + 7) / 8, kKeys / 8); };
@@ -243,9 +245,9 @@ __device__ __forceinline__ void reset(Rows4<D> &st) {
 
 // The workers' parts of one row, joined in order: thread t holds C float4 of row
 // t / kLanes, columns 4 (t % kLanes + kLanes c).
-template <int D>
+template <int D, int W>
 struct Joined {
-    static constexpr int kLanes = kThreads<D> / kRows, C = D / 4 / kLanes;
+    static constexpr int kLanes = kThreads<W> / kRows, C = D / 4 / kLanes;
     float m, l;
     float4 o[C];
     static __device__ __forceinline__ int row() { return static_cast<int>(threadIdx.x) / kLanes; }
@@ -256,9 +258,9 @@ struct Joined {
 };
 
 // The whole block calls it.
-template <int D>
-__device__ __forceinline__ Joined<D> join_workers(F32Smem<D> &sm, const Rows4<D> &st) {
-    using J = Joined<D>;
+template <int D, int W>
+__device__ __forceinline__ Joined<D, W> join_workers(F32Smem<D, W> &sm, const Rows4<D> &st) {
+    using J = Joined<D, W>;
     const int worker = threadIdx.x / 64, tx = tx_of();
     float *po = &sm.w[worker].v[0][0];
 #pragma unroll
@@ -273,9 +275,9 @@ __device__ __forceinline__ Joined<D> join_workers(F32Smem<D> &sm, const Rows4<D>
     J r;
     r.m = -INFINITY;
     r.l = 0.f;
-    float2 ml[kWorkers<D>];
+    float2 ml[W];
 #pragma unroll
-    for (int y = 0; y < kWorkers<D>; ++y) {
+    for (int y = 0; y < W; ++y) {
         ml[y] = sm.ml[y][J::row()];
         r.m = fmaxf(r.m, ml[y].x);
     }
@@ -283,7 +285,7 @@ __device__ __forceinline__ Joined<D> join_workers(F32Smem<D> &sm, const Rows4<D>
 #pragma unroll
     for (int c = 0; c < J::C; ++c) r.o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int y = 0; y < kWorkers<D>; ++y) {
+    for (int y = 0; y < W; ++y) {
         const float w = ex2_approx(ml[y].x - ref);
         r.l = fmaf(w, ml[y].y, r.l);
 #pragma unroll
@@ -317,15 +319,15 @@ __device__ __forceinline__ uint32_t map_rank(const void *p, unsigned rank) {
 
 // The cluster's parts into those of its first CTA, in order of the keys; returns
 // whether this CTA is the one that holds the result.  Every thread calls it.
-template <int D>
-__device__ __forceinline__ bool join_cluster(F32Smem<D> &sm, Joined<D> &x) {
-    using J = Joined<D>;
+template <int D, int W>
+__device__ __forceinline__ bool join_cluster(F32Smem<D, W> &sm, Joined<D, W> &x) {
+    using J = Joined<D, W>;
     const unsigned n = cluster_size(), rank = cluster_rank();
     if (n == 1) return true;
     const int tid = threadIdx.x;
     if (rank > 0) {
 #pragma unroll
-        for (int c = 0; c < J::C; ++c) sm.joined[c * kThreads<D> + tid] = x.o[c];
+        for (int c = 0; c < J::C; ++c) sm.joined[c * kThreads<W> + tid] = x.o[c];
         if (tid % J::kLanes == 0) sm.joined_ml[J::row()] = make_float2(x.m, x.l);
     }
     cluster_sync();
@@ -341,7 +343,7 @@ __device__ __forceinline__ bool join_cluster(F32Smem<D> &sm, Joined<D> &x) {
             for (int c = 0; c < J::C; ++c)
                 asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                              : "=f"(o[c].x), "=f"(o[c].y), "=f"(o[c].z), "=f"(o[c].w)
-                             : "r"(map_rank(&sm.joined[c * kThreads<D> + tid], y)));
+                             : "r"(map_rank(&sm.joined[c * kThreads<W> + tid], y)));
             const float mn = fmaxf(x.m, m), ref = mn == -INFINITY ? 0.f : mn;
             const float w0 = ex2_approx(x.m - ref), w1 = ex2_approx(m - ref);
             x.m = mn;
@@ -394,12 +396,12 @@ __device__ __forceinline__ int blocks_le(const int32_t *cu, int n, int w, int T,
 }
 
 // Cluster (h, w): head h, 32 rows of the sequence that owns w.
-template <int D>
-__global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const PackedArgs a) {
+template <int D, int W>
+__global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) packed_f32_kernel(const PackedArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
-    F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
+    F32Smem<D, W> &sm = *reinterpret_cast<F32Smem<D, W> *>(f32_smem);
     const int tid = threadIdx.x, tx = tx_of();
     const unsigned n_cta = cluster_size(), x = blockIdx.x / n_cta;
     const int h = x % a.H, w = x / a.H, g = h / (a.H / a.H_kv);
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const Packed
     if (t0 >= c1) return;                              // one of the empty blocks
     const int end = min(t0 + kRows, c1);
     const float *Q = static_cast<const float *>(a.q) + h * a.q_hs;
-    for (int i = tid; i < kRows * D / 4; i += kThreads<D>) {
+    for (int i = tid; i < kRows * D / 4; i += kThreads<W>) {
         const int r = i / (D / 4), c = i % (D / 4);
         const bool in = t0 + r < end;
         cp_async16(smem_u32(&sm.q[r][4 * c]), Q + (in ? t0 + r : t0) * a.q_ts + 4 * c, in ? 16u : 0u);
@@ -425,14 +427,14 @@ __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const Packed
     const int k0 = min(c0 + static_cast<int>(cluster_rank()) * share, limit), k1 = min(k0 + share, limit);
     Rows4<D> st;
     reset(st);
-    walk<D>(sm, static_cast<const float *>(a.k) + g * a.k_hs, a.k_ts, static_cast<const float *>(a.v) + g * a.v_hs,
+    walk<D, W>(sm, static_cast<const float *>(a.k) + g * a.k_hs, a.k_ts, static_cast<const float *>(a.v) + g * a.v_hs,
             a.v_ts, k0, k1, a.scale * kLog2e, t0 + tid / 32 % 2 * (kRows / 2) < end, st, [&](int i, int key0) {
                 uint32_t see = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) see |= (key0 + tx + 8 * j < hi[i] ? 1u : 0u) << j;
                 return see;
             });
-    Joined<D> y = join_workers(sm, st);
+    Joined<D, W> y = join_workers(sm, st);
     if (!join_cluster(sm, y)) return;
     const long long t = t0 + y.row();
     if (t >= end) return;
@@ -443,10 +445,10 @@ __global__ void __launch_bounds__(kThreads<D>, 1) packed_f32_kernel(const Packed
     if (a.lse && y.column(0) == 0) a.lse[t * a.H + h] = (y.m + log2f(y.l)) * kLn2;
 }
 
-template <int D>
-cudaError_t launch_packed_f32_t(const PackedArgs &a) {
-    const size_t smem = sizeof(F32Smem<D>);
-    cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int D, int W>
+cudaError_t launch_packed_f32_w(const PackedArgs &a) {
+    const size_t smem = sizeof(F32Smem<D, W>);
+    cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const long long blocks = packed_f32_blocks(a.Sq, a.B) * a.H, sms = a.n_sm > 0 ? a.n_sm : 1;
@@ -456,7 +458,19 @@ cudaError_t launch_packed_f32_t(const PackedArgs &a) {
     // 123 us.
     unsigned cluster = 1;
     while (cluster < 8 && blocks * cluster <= sms && a.Sq / a.B >= 128 * static_cast<int>(cluster)) cluster *= 2;
-    return launch_clusters(packed_f32_kernel<D>, cluster, static_cast<unsigned>(blocks * cluster), kThreads<D>, smem, a.stream, a);
+    return launch_clusters(packed_f32_kernel<D, W>, cluster, static_cast<unsigned>(blocks * cluster), kThreads<W>, smem, a.stream, a);
+}
+
+template <int D>
+cudaError_t launch_packed_f32_t(const PackedArgs &a) {
+    // Many short blocks: two of half the workers an SM hide each other's start and end (40
+    // sequences of 128 tokens, 4 heads 28 against 37 us; 20 of 400 97 against 111); few
+    // or long ones are spread more evenly by one (700 to 1 tokens 39 against 47 us, one
+    // of 2048 123 against 128).  Between them: as many blocks an SM as 128-key
+    // stretches in the mean sequence.
+    const long long blocks = packed_f32_blocks(a.Sq, a.B) * a.H, mean = a.Sq / a.B;
+    const bool small = blocks > a.n_sm && blocks * 128 >= mean * a.n_sm;
+    return small ? launch_packed_f32_w<D, kMany<D> / 2>(a) : launch_packed_f32_w<D, kMany<D>>(a);
 }
 
 // ------------------------------------------------------------ trees of drafted tokens
@@ -464,12 +478,12 @@ cudaError_t launch_packed_f32_t(const PackedArgs &a) {
 // Block x: (sequence and key/value head, 32 rows, split of the cache).  Up to eight
 // splits are a cluster, whose first CTA writes the result; more leave their parts in
 // the workspace.
-template <int D>
-__global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs a, const int row_tiles) {
+template <int D, int W>
+__global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) tree_f32_kernel(const TreeArgs a, const int row_tiles) {
     griddep_launch_dependents();
     griddep_wait();
     extern __shared__ __align__(16) uint8_t f32_smem[];
-    F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(f32_smem);
+    F32Smem<D, W> &sm = *reinterpret_cast<F32Smem<D, W> *>(f32_smem);
     const int tid = threadIdx.x, tx = tx_of();
     const bool cluster = a.n_split <= kTreeClusterF32;  // of a.n_split CTAs
     const int c = blockIdx.x % a.n_split, m = blockIdx.x / a.n_split % row_tiles;
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     const Draft d = draft_of(a, b);
     const int k0 = c * a.chunk, k1 = min(k0 + a.chunk, d.L);
     if (k0 >= k1 && !cluster) return;  // the merge never reads this split
-    for (int i = tid; i < kRows * D / 4; i += kThreads<D>) {
+    for (int i = tid; i < kRows * D / 4; i += kThreads<W>) {
         const int r = r0 + i / (D / 4), col = 4 * (i % (D / 4));
         const bool in = r < rows && r % a.T < d.n;
         const float *q = static_cast<const float *>(a.q);
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     reset(st);
     const size_t head = static_cast<size_t>(bk) * a.Skv * D;
     if (k0 < k1) {
-        walk<D>(sm, static_cast<const float *>(a.k) + head, D, static_cast<const float *>(a.v) + head, D, k0, k1,
+        walk<D, W>(sm, static_cast<const float *>(a.k) + head, D, static_cast<const float *>(a.v) + head, D, k0, k1,
                 a.scale * kLog2e, __any_sync(0xffffffffu, live[0] || live[1] || live[2] || live[3]), st, [&](int i, int key0) {
                     uint32_t see = 0;
 #pragma unroll
@@ -510,7 +524,7 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     } else {
         cp_async_wait<0>();
     }
-    Joined<D> x = join_workers(sm, st);
+    Joined<D, W> x = join_workers(sm, st);
     if (cluster && !join_cluster(sm, x)) return;
     const int r = r0 + x.row(), t = r % a.T;
     if (r >= rows) return;
@@ -528,19 +542,27 @@ __global__ void __launch_bounds__(kThreads<D>, 1) tree_f32_kernel(const TreeArgs
     for (int cc = 0; cc < x.C; ++cc) *reinterpret_cast<float4 *>(O + x.column(cc)) = x.times(cc, f);
 }
 
-template <int D>
-cudaError_t launch_tree_f32_t(const TreeArgs &a) {
-    const size_t smem = sizeof(F32Smem<D>);
-    cudaError_t e = cudaFuncSetAttribute(tree_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int D, int W>
+cudaError_t launch_tree_f32_w(const TreeArgs &a) {
+    const size_t smem = sizeof(F32Smem<D, W>);
+    cudaError_t e = cudaFuncSetAttribute(tree_f32_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int row_tiles = ((a.H / a.H_kv) * a.T + kRows - 1) / kRows;
     const unsigned grid = static_cast<unsigned>(a.B * a.H_kv) * a.n_split * row_tiles;
     const bool cluster = a.n_split <= kTreeClusterF32;
-    e = launch_clusters(tree_f32_kernel<D>, cluster ? static_cast<unsigned>(a.n_split) : 1u, grid, kThreads<D>, smem,
+    e = launch_clusters(tree_f32_kernel<D, W>, cluster ? static_cast<unsigned>(a.n_split) : 1u, grid, kThreads<W>, smem,
                         a.stream, a, row_tiles);
     if (e != cudaSuccess || cluster) return e;
     return launch_tree_merge_f32(a);
+}
+
+template <int D>
+cudaError_t launch_tree_f32_t(const TreeArgs &a) {
+    const long long blocks = static_cast<long long>(a.B) * a.H_kv * a.n_split * (((a.H / a.H_kv) * a.T + kRows - 1) / kRows);
+    // more blocks than SMs: two an SM (8 sequences of 1024 rows, 32 drafts, H 8, H_kv 2: 32
+    // against 54 us; 64 of 500 rows, 4 drafts, H 8, H_kv 8: 67 against 105)
+    return blocks > a.n_sm ? launch_tree_f32_w<D, kMany<D> / 2>(a) : launch_tree_f32_w<D, kMany<D>>(a);
 }
 
 }  // namespace
