@@ -171,3 +171,30 @@ def test_parameters_and_other_threads(native):
         t.join()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("name", ["packed", "rope", "rope_append", "tree"])
+def test_captured(native, name, dtype):
+    """The same call captured twice into one graph, after an eager one on another
+    stream, and replayed: the eager results (fp32: clusters of CTAs in a graph)."""
+    entry, args = calls(dtype=dtype)[name]
+    want = [t.clone() for t in tensors(entry(*args))]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        entry(*args)
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = tensors(entry(*args))
+        second = tensors(entry(*args))
+    for _ in range(3):
+        for t in first + second:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, first, second):
+            assert torch.equal(a, b) and torch.equal(a, c)
+    attn.attn_device_status()

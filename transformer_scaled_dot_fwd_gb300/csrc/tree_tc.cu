@@ -37,7 +37,7 @@
 // (323 MB to read): 63 us, of it 49 us at 6.6 TB/s between the first and the last
 // tile, 4 us the merge.  64 sequences of 4096-8192 rows, 63 drafts (1.69 GB, 407
 // GFLOP): 314-329 us, 1240-1295 TFLOP/s, a pair of tiles in 1.7 us.  One sequence
-// of 1500 rows, 8 drafts: 13 us.  The first form, splits of a fixed number of keys
+// of 1500 rows, 8 drafts: 12 us (12.8 a call).  The first form, splits of a fixed number of keys
 // with a CTA and one stream each, two to an SM, took 98, 526 and 14 us: a single
 // stream waits for its own MMAs.
 //
@@ -798,24 +798,18 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
 // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, M the largest m_c, the
 // parts added in order, for one row and 4 C columns: part(c) is the row's (m, l) in
 // part c, column(c, e) its e-th four columns.
-template <int C, typename T, typename Part, typename Column>
-__device__ __forceinline__ void merge_row(int n, bool live, T *out, Part part, Column column) {
+//
+// kAhead parts are loaded before the first is used: few rows, so latency counts.  Early:
+// x and o hold the first ones already.
+constexpr int kAhead = 4;
+template <int C, bool Early, typename T, typename Part, typename Column>
+__device__ __forceinline__ void merge_row(int n, bool live, T *out, Part part, Column column,
+                                          float2 (&x)[kAhead], float4 (&o)[kAhead][C]) {
     float4 acc[C];
 #pragma unroll
     for (int e = 0; e < C; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f, M = -INFINITY;
-    // kAhead parts are loaded before the first is used: few rows, so latency counts
-    constexpr int kAhead = 4;
-    for (int c0 = 0; c0 < n; c0 += kAhead) {
-        float2 x[kAhead];
-        float4 o[kAhead][C];
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-            const int c = min(c0 + y, n - 1);
-            x[y] = part(c);
-#pragma unroll
-            for (int e = 0; e < C; ++e) o[y][e] = column(c, e);
-        }
+    auto add = [&](int c0) {
 #pragma unroll
         for (int y = 0; y < kAhead; ++y) {
             if (c0 + y >= n) break;
@@ -829,6 +823,19 @@ __device__ __forceinline__ void merge_row(int n, bool live, T *out, Part part, C
                 acc[e] = make_float4(fmaf(w, o[y][e].x, acc[e].x * old), fmaf(w, o[y][e].y, acc[e].y * old),
                                      fmaf(w, o[y][e].z, acc[e].z * old), fmaf(w, o[y][e].w, acc[e].w * old));
         }
+    };
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int c = min(c0 + y, n - 1);
+            x[y] = part(c);
+#pragma unroll
+            for (int e = 0; e < C; ++e) o[y][e] = column(c, e);
+        }
+    };
+    for (int c0 = 0; c0 < n; c0 += kAhead) {
+        if (!Early || c0 > 0) load(c0);
+        add(c0);
     }
     const float inv = live ? 1.f / sum : 0.f;
 #pragma unroll
@@ -840,25 +847,37 @@ __device__ __forceinline__ void merge_row(int n, bool live, T *out, Part part, C
 // bf16: block (i, y) merges 32 rows of the unit that begins in CTA i of the main
 // kernel and ends in a later one: slot 2 i + 1, then slot 2 c of the CTAs after
 // it.  Lane = row, as the partial results lie; warp = D / 8 columns.
-template <int D>
+// Early: the first slots are loaded beside the look-up, parts or not (of 2 n_split).
+template <int D, bool Early>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const int slot_rows) {
     griddep_launch_dependents();
     griddep_wait();
     const int i = blockIdx.x, rr = blockIdx.y * 32 + threadIdx.x % 32, warp = threadIdx.x / 32;
+    constexpr int C = D / 32;
+    auto slot = [&](int c) { return static_cast<size_t>(c == 0 ? 2 * i + 1 : 2 * (i + c)); };
+    auto part = [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[slot(c) * slot_rows + rr]; };
+    auto column = [&](int c, int e) {
+        return reinterpret_cast<const float4 *>(a.part_o)[(slot(c) * (D / 4) + warp * C + e) * slot_rows + rr];
+    };
+    float2 x[kAhead];
+    float4 o[kAhead][C];
+    if (Early) {
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int c = min(y, a.n_split - 1 - i);
+            x[y] = part(c);
+#pragma unroll
+            for (int e = 0; e < C; ++e) o[y][e] = column(c, e);
+        }
+    }
     const int4 rec = reinterpret_cast<const int4 *>(a.merge)[2 * i], rec2 = reinterpret_cast<const int4 *>(a.merge)[2 * i + 1];
     if (rec.x < 0) return;
     const int bk = rec.x, tile = rec.y, b = rec.z, last = rec.w, nd = rec2.x, past = rec2.y;
     const int G = a.H / a.H_kv, q = tile * kM + rr;
     if (q >= G * a.T) return;
     const int h = (bk - b * a.H_kv) * G + q / a.T, t = q % a.T;
-    constexpr int C = D / 32;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + b * a.o_bs + h * a.o_hs + t * a.o_ts + warp * 4 * C;
-    auto slot = [&](int c) { return static_cast<size_t>(c == 0 ? 2 * i + 1 : 2 * (i + c)); };
-    merge_row<C>(last - i + 1, t < nd && past + t >= 0, out,
-                 [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[slot(c) * slot_rows + rr]; },
-                 [&](int c, int e) {
-                     return reinterpret_cast<const float4 *>(a.part_o)[(slot(c) * (D / 4) + warp * C + e) * slot_rows + rr];
-                 });
+    merge_row<C, Early>(last - i + 1, t < nd && past + t >= 0, out, part, column, x, o);
 }
 
 // fp32: one warp per row, n_split parts of `chunk` keys.
@@ -874,9 +893,12 @@ __global__ void __launch_bounds__(256) tree_merge_f32_kernel(const TreeArgs a) {
     const Draft d = draft_of(a, b);
     const bool live = t < d.n && d.past + t >= 0;
     float *out = static_cast<float *>(a.out) + b * a.o_bs + (g * G + r / a.T) * a.o_hs + t * a.o_ts + 4 * lane;
-    merge_row<1>(live ? (d.L + a.chunk - 1) / a.chunk : 0, live, out,
-                 [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[R * a.n_split + c]; },
-                 [&](int c, int) { return reinterpret_cast<const float4 *>(a.part_o)[(R * a.n_split + c) * (D / 4) + lane]; });
+    float2 x[kAhead];
+    float4 o[kAhead][1];
+    merge_row<1, false>(live ? (d.L + a.chunk - 1) / a.chunk : 0, live, out,
+                        [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[R * a.n_split + c]; },
+                        [&](int c, int) { return reinterpret_cast<const float4 *>(a.part_o)[(R * a.n_split + c) * (D / 4) + lane]; },
+                        x, o);
 }
 
 // No cache rows at all: zeros.
@@ -905,7 +927,12 @@ cudaError_t launch_tree_t(const TreeArgs &a, int row_tiles, const CUtensorMap &t
     const int slot_rows = L::kQTiles * kM;
     const int rows = (a.H / a.H_kv) * a.T;
     const unsigned y = static_cast<unsigned>(((rows < slot_rows ? rows : slot_rows) + 31) / 32);
-    return launch_pdl(tree_join_kernel<D>, dim3(grid - 1, y), dim3(256), 0, a.stream, a, slot_rows);
+    // Early where units have several CTAs each (one sequence of 1500 rows 13.7 -> 12.8
+    // us); where two share a unit now and then, loads for nothing and their registers
+    // cost more (16 sequences 63.5 -> 64.5 us).
+    const long long units = static_cast<long long>(a.B) * a.H_kv * ((row_tiles + L::kQTiles - 1) / L::kQTiles);
+    return launch_pdl(grid >= 3 * units ? tree_join_kernel<D, true> : tree_join_kernel<D, false>, dim3(grid - 1, y),
+                      dim3(256), 0, a.stream, a, slot_rows);
 }
 
 }  // namespace
