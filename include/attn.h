@@ -363,7 +363,9 @@ ATTN_API int attn_decode_splits(int B, int H, int Skv, int D);
  * magnitude count as infinite.  A row whose every score is -inf is a NaN.
  *
  * dtype, D, scale and errors as in attn_fwd; "Concurrency" there applies to the
- * bf16 form.  Results do not depend on how the sequences are packed or scheduled.
+ * bf16 form.  The same call gives the same bits every time.  bf16 rows do not
+ * depend on what else is packed with their sequence; an fp32 row's sums are split
+ * by the number of sequences and tokens, so it may differ in its last bits.
  */
 ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *out, float *lse, int T, int H, int H_kv,
                              int D, const long long *strides, const int32_t *cu_seqlens, int n_seq, float scale,
@@ -398,8 +400,8 @@ ATTN_API long long attn_fwd_packed_workspace(int T, int n_seq, int H, int H_kv, 
  *               aligned (may be NULL when that is 0); rules as in attn_fwd_packed
  *
  * The splits of a sequence are merged in order: a call gives the same bits
- * every time.  Scores beyond fp32's range as in attn_fwd_packed.  dtype, D, scale and errors as in attn_fwd; T > 128 returns
- * ATTN_EUNSUPPORTED.
+ * every time.  Scores beyond fp32's range as in attn_fwd_packed.  dtype, D, scale
+ * and errors as in attn_fwd; T > 128 returns ATTN_EUNSUPPORTED.
  */
 ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vcache, void *out, int B, int H, int H_kv,
                               int T, int Skv, int D, const long long *strides, const int32_t *parents,
