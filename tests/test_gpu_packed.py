@@ -378,3 +378,25 @@ def test_fp32_clusters(gpu, lens, D, causal):
 @pytest.mark.parametrize("causal", [True, False])
 def test_fp32_many_blocks(gpu, lens, D, causal):
     case(lens, 4, 2, D, causal, dtype=F32, seed=22)
+
+
+@pytest.mark.parametrize("H,H_kv", [(4, 2), (3, 3)])
+def test_bf16_rows_do_not_depend_on_the_batch(gpu, H, H_kv):
+    lens = [300, 1, 129, 0, 700, 64]
+    q, k, v = tokens(sum(lens), H, H_kv, 128, 23, BF16)
+    cu = offsets(lens)
+    out, lse = attn.attn_fwd_packed(q, k, v, ints(cu), causal=True, return_lse=True)
+    for a, b in zip(cu, cu[1:]):
+        if a < b:
+            alone = attn.attn_fwd_packed(q[a:b], k[a:b], v[a:b], ints([0, b - a]), causal=True, return_lse=True)
+            assert torch.equal(alone[0], out[a:b]) and torch.equal(alone[1], lse[a:b])
+    attn.attn_device_status()
+
+
+@pytest.mark.parametrize("lens", [[300, 200], [700, 513, 260, 129, 64, 1], [60] * 80])
+def test_fp32_repeated_calls_give_the_same_bits(gpu, lens):
+    q, k, v = tokens(sum(lens), 4, 4, 64, 24, F32)
+    first = attn.attn_fwd_packed(q, k, v, ints(offsets(lens)), return_lse=True)
+    for _ in range(5):
+        again = attn.attn_fwd_packed(q, k, v, ints(offsets(lens)), return_lse=True)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
