@@ -400,3 +400,30 @@ def test_fp32_repeated_calls_give_the_same_bits(gpu, lens):
     for _ in range(5):
         again = attn.attn_fwd_packed(q, k, v, ints(offsets(lens)), return_lse=True)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_seen_infinity_is_never_lost(gpu, dtype, causal, D):
+    """A key whose weight underflows (its score lies some 1400 below the others)
+    with an infinite or NaN value: the element is infinite or NaN in every row that
+    sees the key, whichever keys the row's neighbours see, and in no other."""
+    lens = [300, 45]
+    q, k, v = (x.contiguous() for x in tokens(345, 2, 1, D, 31, dtype))
+    q[..., 0] = 8.0
+    for row, col, x in ((17, 3, math.inf), (70, 20, -math.inf), (295, 41, math.nan), (305, 5, math.inf)):
+        k[row, 0, 0] = -180.0 * math.sqrt(D)
+        v[row, 0, col] = x
+    out = attn.attn_fwd_packed(q, k, v, ints([0, 300, 345]), causal=causal)
+    attn.attn_device_status()
+    for a, b in ((0, 300), (300, 345)):
+        i = torch.arange(b - a, device="cuda")
+        visible = i[:, None] >= i if causal else torch.ones(b - a, b - a, dtype=torch.bool, device="cuda")
+        hit = (visible.double() @ (~torch.isfinite(v[a:b, 0])).double()) > 0
+        for h in range(2):
+            assert torch.equal(~torch.isfinite(out[a:b, h]), hit)
+            o, _, A, size = ref.attend(q[a:b, h], k[a:b, 0], v[a:b, 0], visible, D ** -0.5)
+            tol, _ = ref.bounds(dtype, D, b - a, D ** -0.5, size, o, A)
+            got = torch.where(hit, torch.zeros_like(o), out[a:b, h].double())
+            ref.check(got, torch.where(hit, torch.zeros_like(o), o), tol)

@@ -326,3 +326,38 @@ def test_fp32_rows_of_one_warp(gpu, G, T):
 def test_fp32_many_blocks(gpu, B, H_kv, T, Skv, D):
     lens = [max(0, Skv - 37 * b % Skv) for b in range(B)]
     case(B, 2 * H_kv, H_kv, T, Skv, D, lens, [min(T, n) for n in lens], dtype=F32, seed=B)
+
+
+# a cache of one tile, several in one CTA or cluster, and one that many CTAs or splits share
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [5, 70])
+@pytest.mark.parametrize("B,Skv", [(1, 120), (3, 700), (1, 6000), (20, 1500)])
+@pytest.mark.parametrize("draft_low", [False, True])
+def test_a_seen_infinity_is_never_lost(gpu, dtype, B, Skv, T, draft_low):
+    """Keys whose weights underflow (their scores lie some 1400 below the others) with
+    infinite or NaN values: the element is infinite or NaN in every row that sees the
+    key, wherever the cache is cut, and in no other."""
+    H, H_kv, D = 4, 2, 64
+    q = wl.random_tensors((B, H, T, D), 60, dtype=dtype, count=1)[0]
+    kc, vc = wl.random_tensors((B, H_kv, Skv, D), 61, dtype=dtype, count=2)
+    q[..., 0] = 8.0
+    lens = [Skv - 3 * b for b in range(B)]
+    parents = [tree(T, "random", 62 + b) for b in range(B)]
+    for b in range(B):
+        for row, col, x in ((3, 1, math.inf), (lens[b] // 2, 20, -math.inf), (lens[b] - T, 41, math.inf),
+                            (lens[b] - T + 2, 50, math.nan), (lens[b] - 1, 7, -math.inf)):
+            kc[b, :, row, 0] = -180.0 * math.sqrt(D)
+            vc[b, :, row, col] = x
+        if draft_low:  # every drafted key: a part of the draft alone has a maximum far below the others'
+            kc[b, :, lens[b] - T:lens[b], 0] = -180.0 * math.sqrt(D)
+    out = attn.attn_decode_tree(q, kc, vc, ints(parents), cache_len=ints(lens))
+    attn.attn_device_status()
+    for b in range(B):
+        see = sight(parents[b], lens[b], T)
+        for h in range(H):
+            hit = (see.double() @ (~torch.isfinite(vc[b, h // 2, :lens[b]])).double()) > 0
+            assert torch.equal(~torch.isfinite(out[b, h]), hit), (b, h)
+            o, _, A, size = ref.attend(q[b, h], kc[b, h // 2, :lens[b]], vc[b, h // 2, :lens[b]], see, D ** -0.5)
+            tol, _ = ref.bounds(dtype, D, lens[b], D ** -0.5, size, o, A)
+            zero = torch.zeros_like(o)
+            ref.check(torch.where(hit, zero, out[b, h].double()), torch.where(hit, zero, o), tol)

@@ -163,7 +163,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float p = see >> j & 1u ? ex2_approx(s[j] - ref) : 0.f;
+                    const float p = see >> j & 1u ? ex2_approx(s[j] - ref) : -0.f;  // -0: not seen
                     sum += p;
                     sp[ty + 4 * i][tx + 8 * j] = p;
                 }
@@ -182,8 +182,9 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
             score(std::integral_constant<int, 2>{});
         else
             score(std::integral_constant<int, 1>{});
-        // every row of the warp sees every key: plain FMAs; otherwise a weight
-        // of zero must not meet an infinite or NaN value
+        // every row of the warp sees every key: plain FMAs; otherwise a key that the row
+        // does not see (weight -0) must not meet an infinite or NaN value, while a key it
+        // sees does, also where its weight has underflowed to +0
         const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
         sync();              // both warps are done with K; V and P are visible
@@ -208,7 +209,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint64_t a = ffma2(p2[i], x.x, st.o[i][2 * c]), b = ffma2(p2[i], x.y, st.o[i][2 * c + 1]);
-                            if (!decltype(guarded)::value || f2_lo(p2[i]) != 0.f) {
+                            if (!decltype(guarded)::value || __float_as_uint(f2_lo(p2[i])) != 0x80000000u) {
                                 st.o[i][2 * c] = a;
                                 st.o[i][2 * c + 1] = b;
                             }
