@@ -427,3 +427,21 @@ def test_a_seen_infinity_is_never_lost(gpu, dtype, causal, D):
             tol, _ = ref.bounds(dtype, D, b - a, D ** -0.5, size, o, A)
             got = torch.where(hit, torch.zeros_like(o), out[a:b, h].double())
             ref.check(got, torch.where(hit, torch.zeros_like(o), o), tol)
+
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_rows_of_infinitely_low_scores(gpu, dtype, n):
+    """A row whose every score is -inf is a NaN with a log-sum-exp of -inf; keys of
+    such scores beside an ordinary one have no weight."""
+    q, k, v = (x.contiguous() for x in tokens(2 * n, 2, 1, 64, 38, dtype))
+    q[..., 3] = 2.0
+    k[:n, 0, 3] = -math.inf
+    k[n:2 * n - 1, 0, 3] = -math.inf
+    out, lse = attn.attn_fwd_packed(q, k, v, ints([0, n, 2 * n]), return_lse=True)
+    attn.attn_device_status()
+    assert torch.isnan(out[:n]).all() and torch.all(lse[:n] == -math.inf)
+    assert torch.equal(out[n:], v[2 * n - 1:].expand(n, 2, 64))
+    s = (q[n:].double() @ k[-1, 0].double()) / 8
+    assert torch.all((lse[n:].double() - s).abs() <= 70 * 2.0 ** -23 * 16 + s.abs() * 2.0 ** -22)

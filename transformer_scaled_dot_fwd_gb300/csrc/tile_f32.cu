@@ -65,6 +65,12 @@ struct F32Smem {
 };
 static_assert(kRows == kKeys, "a worker's output takes its V tile's place");
 
+// The larger of two numbers, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
@@ -163,7 +169,11 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float p = see >> j & 1u ? ex2_approx(s[j] - ref) : -0.f;  // -0: not seen
+                    // A seen key's weight is never 0, however far it lies below the others: an
+                    // infinite or NaN value of it stays in the row (2^-149 of a finite one is
+                    // less than the 2^-126 that ex2 flushes).  Marking unseen keys instead, by
+                    // -0 or a mask in the product below, cost 1-5 %.
+                    const float p = see >> j & 1u ? max_nan(ex2_approx(s[j] - ref), 0x1p-149f) : 0.f;
                     sum += p;
                     sp[ty + 4 * i][tx + 8 * j] = p;
                 }
@@ -182,9 +192,8 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
             score(std::integral_constant<int, 2>{});
         else
             score(std::integral_constant<int, 1>{});
-        // every row of the warp sees every key: plain FMAs; otherwise a key that the row
-        // does not see (weight -0) must not meet an infinite or NaN value, while a key it
-        // sees does, also where its weight has underflowed to +0
+        // every row of the warp sees every key: plain FMAs; otherwise a weight of zero, that
+        // of a key the row does not see, must not meet an infinite or NaN value
         const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
         sync();              // both warps are done with K; V and P are visible
@@ -209,7 +218,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint64_t a = ffma2(p2[i], x.x, st.o[i][2 * c]), b = ffma2(p2[i], x.y, st.o[i][2 * c + 1]);
-                            if (!decltype(guarded)::value || __float_as_uint(f2_lo(p2[i])) != 0x80000000u) {
+                            if (!decltype(guarded)::value || f2_lo(p2[i]) != 0.f) {
                                 st.o[i][2 * c] = a;
                                 st.o[i][2 * c + 1] = b;
                             }
