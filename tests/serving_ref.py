@@ -46,3 +46,40 @@ def check(got, out, tol, what=""):
     err = (got.double() - out).abs()
     assert torch.isfinite(got.double()).all(), f"{what}: non-finite output"
     assert torch.all(err <= tol), f"{what}: worst excess {(err - tol).max():.3e}, worst error {err.max():.3e}"
+
+
+def huge_inputs(n_rows, n_keys, D, dtype, seed):
+    """q (n_rows, D) and k (n_keys, D) of one nonzero element each, whose scores are exact
+    in fp32, of both signs, 2^27 to 2^92 in magnitude and growing from tile to tile of 128
+    keys; two scores of a row are equal or differ by 2^-8 of them.  Every fourth row
+    is zero."""
+    g = torch.Generator().manual_seed(seed)
+
+    def pick(lo, hi, n):
+        return torch.randint(lo, hi, (n,), generator=g)
+
+    j = torch.arange(n_keys)
+    b = pick(128, 256, n_keys) * 2.0 ** (20 + (3 * (j // 128)).clamp(max=30) + pick(0, 3, n_keys)) * (2 * pick(0, 2, n_keys) - 1)
+    i = torch.arange(n_rows)
+    a = 2.0 ** torch.tensor([0.0, 10.0, 32.0, 0.0])[i % 4] * (2 * pick(0, 2, n_rows) - 1) * (i % 4 != 3)
+    q, k = torch.zeros(n_rows, D), torch.zeros(n_keys, D)
+    q[:, 0], k[:, 0] = a, b
+    return q.to(dtype).cuda(), k.to(dtype).cuda()
+
+
+def check_huge(got, lse, q, k, v, visible, dtype, what=""):
+    """Rows of huge_inputs (scale 1): the weights are 1 at the largest score (equal
+    scores share it) and underflow elsewhere, so the mean of those values comes out
+    of one product, one division and one rounding; a zero row is the mean of all it sees.
+    The log-sum-exp is the score through four products rounded to 24 bits."""
+    s = torch.where(visible, q.double() @ k.double().T, -math.inf)
+    top = (s == s.amax(-1, keepdim=True)) & visible
+    n = top.sum(-1, keepdim=True)
+    mean, size = top.double() @ v.double() / n, top.double() @ v.double().abs() / n
+    half = torch.finfo(dtype).eps / 2
+    tol = size * ((n + 8) * 2.0 ** -23) + (mean.abs() + size * 2.0 ** -12) * half + 1e-30
+    check(got, mean, tol, what)
+    if lse is not None:
+        want = s.amax(-1) + torch.log(n[:, 0].double())
+        err = (lse.double() - want).abs()
+        assert torch.all(err <= want.abs() * 2.0 ** -21 + 2.0 ** -18), f"{what} lse {err.max():.3e}"

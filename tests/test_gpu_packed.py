@@ -445,3 +445,64 @@ def test_rows_of_infinitely_low_scores(gpu, dtype, n):
     assert torch.equal(out[n:], v[2 * n - 1:].expand(n, 2, 64))
     s = (q[n:].double() @ k[-1, 0].double()) / 8
     assert torch.all((lse[n:].double() - s).abs() <= 70 * 2.0 ** -23 * 16 + s.abs() * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,H_kv,D", [(2, 1, 128), (2, 2, 64)])
+def test_huge_scores_stay_in_their_rows(gpu, dtype, causal, H, H_kv, D):
+    """Scores of huge or infinite magnitude in the next sequence, in tokens of no
+    sequence and in other rows of the same sequence: the rows that have no part in
+    them keep their bits, out and lse."""
+    lens, trail = [100, 75, 60], 40
+    T = sum(lens) + trail
+    cu = offsets(lens)
+    q, k, v = (x.contiguous() for x in tokens(T, H, H_kv, D, 32, dtype))
+    clean = attn.attn_fwd_packed(q, k, v, ints(cu), causal=causal, return_lse=True)
+    at = torch.arange(T, device="cuda")
+
+    def check(q, k, keep, what):
+        got = attn.attn_fwd_packed(q, k, v, ints(cu), causal=causal, return_lse=True)
+        attn.attn_device_status()
+        for a, b in zip(clean, got):
+            assert torch.equal(a[keep], b[keep]), what
+
+    q2 = q.clone()
+    q2[cu[1]:cu[2]] *= 1e9
+    q2[cu[3]:] *= -1e9
+    check(q2, k, (at < cu[1]) | ((at >= cu[2]) & (at < cu[3])), "the next sequence's q")
+    for x in (1e9, math.inf):
+        q2 = q.clone()
+        q2[20, :, 3] = x          # a row in the midst of a warp's
+        q2[cu[2] + 59] *= 1e12    # and the last of a sequence
+        check(q2, k, (at < cu[3]) & (at != 20) & (at != cu[2] + 59), "one row's q")
+    if causal:
+        for x in (1e9, math.inf, -math.inf):
+            k2 = k.clone()
+            k2[20, :, 3] = x
+            k2[cu[1] + 50, :, 0] = x
+            check(q, k2, (at < 20) | ((at >= cu[1]) & (at < cu[1] + 50)) | ((at >= cu[2]) & (at < cu[3])), "a later key")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,H_kv,D", [(2, 1, 128), (2, 2, 64)])
+def test_distinct_scores_of_huge_magnitude(gpu, dtype, causal, H, H_kv, D):
+    """Scores of 2^27 to 2^92 of both signs, growing over the tiles, beside rows of zeros."""
+    cu = offsets([700, 130, 33])
+    T = cu[-1]
+    v = wl.random_tensors((T, H_kv, D), 33, dtype=dtype, count=1)[0]
+    q, k = torch.zeros(T, H, D, dtype=dtype, device="cuda"), torch.zeros(T, H_kv, D, dtype=dtype, device="cuda")
+    for a, b in zip(cu, cu[1:]):
+        for h in range(H):
+            q[a:b, h] = ref.huge_inputs(b - a, b - a, D, dtype, 34 + h)[0]
+        for h in range(H_kv):
+            k[a:b, h] = ref.huge_inputs(b - a, b - a, D, dtype, 36 + h)[1]
+    out, lse = attn.attn_fwd_packed(q, k, v, ints(cu), causal=causal, return_lse=True, scale=1.0)
+    attn.attn_device_status()
+    for a, b in zip(cu, cu[1:]):
+        i = torch.arange(b - a, device="cuda")
+        visible = i[:, None] >= i if causal else torch.ones(b - a, b - a, dtype=torch.bool, device="cuda")
+        for h in range(H):
+            g = h * H_kv // H
+            ref.check_huge(out[a:b, h], lse[a:b, h], q[a:b, h], k[a:b, g], v[a:b, g], visible, dtype, f"{b - a} head {h}")

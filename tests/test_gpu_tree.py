@@ -361,3 +361,57 @@ def test_a_seen_infinity_is_never_lost(gpu, dtype, B, Skv, T, draft_low):
             tol, _ = ref.bounds(dtype, D, lens[b], D ** -0.5, size, o, A)
             zero = torch.zeros_like(o)
             ref.check(torch.where(hit, zero, out[b, h].double()), torch.where(hit, zero, o), tol)
+
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D,T", [(64, 30), (128, 70)])
+@pytest.mark.parametrize("Skv", [200, 4000])
+def test_huge_scores_stay_in_their_rows(gpu, dtype, D, T, Skv):
+    """Scores of huge or infinite magnitude of a drafted key or query: the rows that
+    have no part in them keep their bits."""
+    B, H, H_kv = 3, 4, 2
+    lens, drafts = [Skv - 1, 150, 64], [T, 21, min(T, 30)]
+    q = wl.random_tensors((B, H, T, D), 63, dtype=dtype, count=1)[0]
+    kc, vc = wl.random_tensors((B, H_kv, Skv, D), 64, dtype=dtype, count=2)
+    parents = [tree(T, "random", 65 + b) for b in range(B)]
+    call = lambda q, k: attn.attn_decode_tree(q, k, vc, ints(parents), cache_len=ints(lens), draft_len=ints(drafts))  # noqa: E731
+    clean = call(q, kc)
+    for x in (1e9, -1e9, math.inf, -math.inf):
+        k2, q2 = kc.clone(), q.clone()
+        for b in range(B):
+            k2[b, :, lens[b] - drafts[b] + 9, 3] = x
+            q2[b, :, 13, 3] = x
+        by_key, by_query = call(q, k2), call(q2, kc)
+        attn.attn_device_status()
+        for b in range(B):
+            n = drafts[b]
+            hidden = ~sight(parents[b], lens[b], n)[:, lens[b] - n + 9]
+            assert torch.equal(by_key[b, :, :n][:, hidden], clean[b, :, :n][:, hidden]), (x, b)
+            other = torch.arange(T, device="cuda") != 13
+            assert torch.equal(by_query[b][:, other], clean[b][:, other]), (x, b)
+
+
+# one tile, several tiles in a CTA, many CTAs or splits a unit; one and two row tiles
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D,T", [(64, 30), (128, 70)])
+@pytest.mark.parametrize("B,Skv", [(2, 120), (40, 500), (1, 6000)])
+def test_distinct_scores_of_huge_magnitude(gpu, dtype, D, T, B, Skv):
+    """Scores of 2^27 to 2^92 of both signs, growing over the tiles, beside rows of zeros."""
+    H, H_kv = 4, 2
+    vc = wl.random_tensors((B, H_kv, Skv, D), 66, dtype=dtype, count=1)[0]
+    q = torch.zeros(B, H, T, D, dtype=dtype, device="cuda")
+    kc = torch.zeros(B, H_kv, Skv, D, dtype=dtype, device="cuda")
+    for b in range(B):
+        for h in range(H):
+            q[b, h] = ref.huge_inputs(T, Skv, D, dtype, 67 + 8 * b + h)[0]
+        for g in range(H_kv):
+            kc[b, g] = ref.huge_inputs(T, Skv, D, dtype, 167 + 8 * b + g)[1]
+    lens = [Skv - 3 * b for b in range(B)]
+    parents = [tree(T, "random", 68 + b) for b in range(B)]
+    out = attn.attn_decode_tree(q, kc, vc, ints(parents), cache_len=ints(lens), scale=1.0)
+    attn.attn_device_status()
+    for b in range(B):
+        see = sight(parents[b], lens[b], T)
+        for h in range(H):
+            ref.check_huge(out[b, h], None, q[b, h], kc[b, h // 2, :lens[b]], vc[b, h // 2, :lens[b]], see, dtype, f"{b} {h}")

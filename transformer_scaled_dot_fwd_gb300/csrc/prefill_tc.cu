@@ -203,14 +203,21 @@ __device__ __forceinline__ void release_item(Bars &bars, int k) {
     mbar_arrive(&bars.item_empty[k % kItemRing]);
 }
 
-// Packed sequences: the weights of a tile with scores of huge magnitude, p = 2^(s sl2 - m)
-// as bf16 pairs over the S columns, zeros from column t on; returns the row's sum.
-// s sl2 - m in one rounding leaves the rounding of m behind, 2^-24 of it: a common
-// factor of the row's weights, until it overflows them.  Here the product is rounded
-// first, as m was, so that the maximum's exponent is 0.  Not inlined: as a part of the
+// Packed sequences: the weights of a tile where a row of the warp has scores of huge
+// magnitude, p = 2^(s sl2 - m) as bf16 pairs over the S columns, zeros from column t
+// on; returns the row's sum.  s sl2 - m in one rounding leaves the rounding of m
+// behind, 2^-24 of it: a common factor of the row's weights, until it overflows them.
+// In a huge row the product is rounded first, as m was, so that the maximum's exponent
+// is 0; the other rows of the warp take the arithmetic and the order of the usual path,
+// so that their bits do not depend on their neighbours.  Not inlined: as a part of the
 // softmax loop it cost 1-4 % of a prompt that has no such score.
 __device__ __noinline__ float huge_weights(uint32_t t_s, int t, float sl2, float negm) {
-    float l = 0.f;
+    // s in two factors, one of them 1: values, not a branch, as the lanes differ and the
+    // TMEM accesses below are the whole warp's
+    const bool huge = fabsf(negm) > kHugeLog2;
+    const float first = huge ? sl2 : 1.f, second = huge ? 1.f : sl2;
+    const uint64_t first2 = f2_pack(first, first), second2 = f2_pack(second, second), negm2 = f2_pack(negm, negm);
+    uint64_t l4[4] = {0, 0, 0, 0};
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {  // P of 64 keys goes over S columns already read
         uint32_t s[64], p[32];
@@ -222,15 +229,17 @@ __device__ __noinline__ float huge_weights(uint32_t t_s, int t, float sl2, float
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
             const int c = h * 64 + 2 * e;
-            const float p0 = c < t ? ex2_approx(__fmul_rn(u2f(s[2 * e]), sl2) + negm) : 0.f;
-            const float p1 = c + 1 < t ? ex2_approx(__fmul_rn(u2f(s[2 * e + 1]), sl2) + negm) : 0.f;
-            l += p0 + p1;
+            const uint64_t arg = ffma2(fmul2(f2_pack(u2f(s[2 * e]), u2f(s[2 * e + 1])), first2), second2, negm2);
+            const float p0 = c < t ? ex2_approx(f2_lo(arg)) : 0.f;
+            const float p1 = c + 1 < t ? ex2_approx(f2_hi(arg)) : 0.f;
+            l4[e % 4] = fadd2(l4[e % 4], f2_pack(p0, p1));
             p[e] = pack_bf16x2(p0, p1);
         }
         tmem_st32(t_s + h * 32, p);
     }
     tmem_st_wait();
-    return l;
+    const uint64_t l2 = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+    return f2_lo(l2) + f2_hi(l2);
 }
 
 // Packed sequences: adds to a written row of the output the non-finite values of keys
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lim = a.causal ? min(it.Lb, i + it.off + 1) : it.Lb;  // keys [0, lim) visible
             }
             float m_run = -INFINITY, l = 0.f;
-            bool huge = false;
+            bool huge = false;  // some row of the warp is: huge_weights chooses by row
 
             for (int j = 0; j < n; ++j) {
                 if (!(ok = mbar_wait_warp<32>(&bars.s_full[x], sp, &bars.abort))) break;

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the ancestor sets (and Q) of this run
             if (!(ok = mbar_wait_warp<32>(&bars.q_full[k & 1], (k >> 1) & 1, &bars.abort))) break;
             float m_run = -INFINITY, l = 0.f;
-            bool huge = sl2 == 0.f;
+            bool huge = sl2 == 0.f;  // some row of the warp is
             for (int i = 0; i < n; ++i) {
                 const int j = one ? 2 * i + x : i;
                 if (!(ok = mbar_wait_warp<32>(&bars.s_full[x], sp, &bars.abort))) break;
@@ -637,18 +637,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m_run = m_new;
                     }
                     // huge scores: round the product before the difference (as in prefill_tc.cu); a
-                    // scale of 0: a hidden key's -inf must not become NaN
-                    huge = sl2 == 0.f || __any_sync(0xffffffffu, fabsf(m_run) > kHugeLog2 && m_run != -INFINITY);
+                    // scale of 0: a hidden key's -inf must not become NaN.  A row without them
+                    // has its product there and here a factor of 1: another row's scores do not
+                    // change its bits.
+                    const bool mine = sl2 == 0.f || (fabsf(m_run) > kHugeLog2 && m_run != -INFINITY);
+                    huge = __any_sync(0xffffffffu, mine);
                     if (huge) {
                         const int at = at0 + j * kN;
+                        const float first = mine ? sl2 : 1.f;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const uint32_t see = !masked ? 0xffffffffu : live ? visible32(set, at + 32 * c) : 0u;
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                s[32 * c + e] = see >> e & 1u ? f2u(__fmul_rn(u2f(s[32 * c + e]), sl2)) : f2u(-INFINITY);
+                                s[32 * c + e] = see >> e & 1u ? f2u(__fmul_rn(u2f(s[32 * c + e]), first)) : f2u(-INFINITY);
                         }
-                        mul = 1.f;
+                        mul = mine ? 1.f : sl2;
                     }
                     if (i > 0 && __any_sync(0xffffffffu, grow)) {  // this stream's earlier P V are complete: S was issued after them
 #pragma unroll 1
