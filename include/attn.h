@@ -104,14 +104,16 @@ extern "C" {
  * nothing); D as above; B*H*max(Sq,Skv)*D must fit in 2^31 rows of D.
  *
  * Concurrency (bf16).  The kernel hands out its work through a counter in a
- * fixed table of the library (no allocation, no clearing launch).  Direct
- * calls take the table's first 64 counters in turn, so at most 64 bf16
- * prefill calls (attn_fwd, attn_fwd_gqa, attn_fwd_chunked, attn_fwd_host's
- * chunks) may be in flight on one device at once.  A call made while its
+ * fixed table of the library (no allocation, no clearing launch).  A direct
+ * call uses the counter of its stream, so bf16 prefill calls (attn_fwd,
+ * attn_fwd_gqa, attn_fwd_chunked, attn_fwd_packed, attn_fwd_host's chunks) of
+ * up to 256 streams may be in flight on one device at once, any number in each;
+ * a further stream takes the counter of the one that has been without a call for
+ * the longest time.  A call made while its
  * stream is being captured into a CUDA graph gets a counter of its own from
  * 1024 further ones, which every replay of that graph node uses; so one
- * graph must not be replayed on two streams at the same time, and at most
- * 1024 captured prefill calls should be alive.  A launch that finds its
+ * graph must not be replayed on two streams at the same time, nor two graphs
+ * that hold captured calls 1024 apart.  A launch that finds its
  * counter in use by another launch records that in the device status word:
  * attn_device_status() then returns ATTN_ECONFLICT, and the outputs of both
  * launches are undefined.  A conflict can leave the shared counter

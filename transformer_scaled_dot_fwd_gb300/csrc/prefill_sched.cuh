@@ -14,8 +14,9 @@ namespace attn {
 constexpr int kBM = 128;       // query rows per Q tile (one TMEM lane each)
 constexpr int kBN = 128;       // keys per K/V tile
 constexpr int kQTiles = 2;     // Q tiles per work item
-constexpr int kSchedSlots = 64;       // direct launches that may run at once with their own counter
+constexpr int kSchedSlots = 256;      // streams whose launches have a counter of their own
 constexpr int kGraphSlots = 1024;     // counters kept for launches captured into CUDA graphs
+constexpr unsigned int kTagBase = 1u << 21;  // tags of launches: kTagBase .. 2 kTagBase - 1
 // Bytes of keys and values per block of heads in the item order (see
 // decode_item); 0 puts all heads in one block.
 #ifndef ATTN_L2_GROUP_MB

@@ -63,6 +63,7 @@
 #include "prefill_sched.cuh"
 #include "ptx.cuh"
 #include "serving.cuh"
+#include "stream_slots.h"
 
 #include <atomic>
 #include <mutex>
@@ -137,23 +138,24 @@ struct Guard {
 static_assert(sizeof(Guard) <= 512, "guard block");
 static_assert(sizeof(SmallPlan) <= 1024, "plan block");
 
-// Work counters, one slot per launch: [0] next item, [2] epoch of the launch
-// using the slot (0: free); [1] and [3] unused.  Every CTA's producer takes
-// items until it draws one past the end, so a launch draws exactly n_items +
-// gridDim.x numbers: the CTA that draws the last one resets the slot (no CTA
-// of the launch touches it after that), and the next launch on the slot
-// starts from zero without a clearing step or any atomic at the end of the
-// kernel.  Each CTA claims the slot (writes its epoch) at its start, before
-// its first draw, which is a release operation; the last drawer fences before
-// it resets the epoch, so no claim can land after the reset.  Direct launches
-// take slots [0, kSchedSlots) in turn; a launch captured into a CUDA graph
-// gets its own slot from the kGraphSlots after them, so replays never share a
-// counter with direct launches.  A CTA that finds another launch's epoch in
-// its slot reports kStatusSchedConflict: the two launches' outputs are then
-// undefined.  A launch that gave up on a wait may stop drawing early and
-// leave its slot claimed; later launches on that slot then report the
+// Work counters.  The low word of a slot is the next item; the high word is the sum
+// of the tags of the CTAs that have drawn from it.  Every CTA's producer takes items
+// until it draws one past the end, so a launch draws exactly n_items + gridDim.x
+// numbers: the CTA that draws the last one resets the slot (no CTA of the launch
+// touches it after that), and the next launch on the slot starts from zero without
+// a clearing step or any atomic at the end of the kernel.  A CTA's first draw adds
+// the launch's tag with its one, so a number comes with the tags of the CTAs that drew
+// before: other than a multiple of the launch's own tag, and another launch uses the slot
+// (kStatusSchedConflict: the two launches' outputs are then undefined).  Tags are
+// 2^21 .. 2^22 - 1, by turn: up to 1024 of one sum to less than 2^32, and equal sums
+// of up to 152 each of two tags take tags that lie 13000 launches apart.
+// Direct launches take the slot of their stream (StreamSlots), whose order keeps
+// their draws apart (they come after griddep_wait); a launch captured into a CUDA
+// graph gets its own slot from the kGraphSlots after them, so replays never share a
+// counter with direct launches.  A launch that gave up on a wait may stop drawing
+// early and leave its slot claimed; later launches on that slot then report the
 // conflict until the counters are cleared from the host.
-__device__ unsigned int g_sched[kSchedSlots + kGraphSlots][4];
+__device__ unsigned long long g_sched[kSchedSlots + kGraphSlots];
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const Args a, const __grid_constant__ CUtensorMap tq,
                       const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const int n_major, const int group, const int front, const int n_items,
-                      unsigned int *sched, const unsigned int epoch) {
+                      unsigned long long *sched, const unsigned int tag) {
     using L = Layout<D>;
     constexpr bool kPacked = std::is_same<Args, PackedArgs>::value;
     extern __shared__ uint8_t smem_raw[];
@@ -283,12 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    unsigned int owner = 0u;
     if (threadIdx.x == 0) {
-        // claim the slot for this launch (the first CTA finds it free, the
-        // others this launch's epoch); the result is checked after the
-        // prologue, so the atomic's round trip overlaps it
-        owner = atomicExch(sched + 2, epoch);
         prefetch_tmap(&tq);
         prefetch_tmap(&tk);
         prefetch_tmap(&tv);
@@ -345,7 +342,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (lane == 0) {
-            if (owner != 0u && owner != epoch) report_status(a.status, 0x12, kStatusSchedConflict);
             int total = n_items;
             if constexpr (kPacked) {
                 if (!small) {  // the plan kernel counted the items
@@ -365,14 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (k >= kItemRing &&
                     !(ok = mbar_wait(&bars.item_empty[slot], ((k / kItemRing) - 1) & 1, &bars.abort)))
                     break;
-                // the first draw releases this CTA's claim of the slot
-                const unsigned int drawn = k == 0 ? atomic_add_release_gpu(sched, 1u) : atomicAdd(sched, 1u);
-                if (drawn == last_draw) {  // the launch's last draw: free the slot
-                    fence_acq_rel_gpu();
-                    atomicExch(sched, 0u);
-                    atomicExch(sched + 2, 0u);
-                }
-                const int t = static_cast<int>(drawn);
+                const unsigned long long draw = atomicAdd(sched, k == 0 ? (static_cast<unsigned long long>(tag) << 32) + 1u : 1ull);
+                const unsigned int drawn = static_cast<unsigned int>(draw);
+                if (drawn == last_draw) atomicExch(sched, 0ull);  // the launch's last draw: free the slot
+                const int t = drawn < static_cast<unsigned int>(total) ? static_cast<int>(drawn) : total;
                 Item it;
                 if (t < total) {
                     if constexpr (kPacked)
@@ -385,6 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 publish_item(bars, slot, it);
                 if constexpr (kPacked) *static_cast<volatile int *>(&guard.spoiled[slot]) = 0;
                 mbar_arrive(&bars.item_full[slot]);
+                if (k == 0) {
+                    const unsigned int tags = static_cast<unsigned int>(draw >> 32), n = tags / tag;
+                    if (n * tag != tags || n >= gridDim.x) report_status(a.status, 0x12, kStatusSchedConflict);
+                }
                 if (it.N < 0) break;
                 int kv_row = 0, edge = 0x7fffffff;
                 if constexpr (kPacked) {
@@ -867,15 +863,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_sched_mutex;
-unsigned int *g_sched_base[kMaxDevices];
-std::atomic<unsigned int> g_sched_turn{0}, g_graph_turn{0}, g_epoch{0};
+unsigned long long *g_sched_base[kMaxDevices];
+StreamSlots<kSchedSlots> g_stream_slots[kMaxDevices];
+std::atomic<unsigned int> g_graph_turn{0}, g_tag_turn{0};
 
-// Work counters for one launch: a slot of g_sched and a non-zero epoch.
-// Direct launches take the first kSchedSlots slots in turn, so launches
-// running at the same time on other streams count separately; a launch being
-// captured into a CUDA graph (which keeps its slot for every replay) takes
+// The work counter of one launch, a slot of g_sched, and its tag.  A direct launch
+// takes the slot of its stream, so no two that can run at the same time share one
+// while at most kSchedSlots streams of the device have launches in flight; a launch
+// being captured into a CUDA graph (which keeps its slot for every replay) takes
 // the next of the kGraphSlots reserved for captures.
-cudaError_t sched_slot(cudaStream_t stream, unsigned int **out, unsigned int *epoch) {
+cudaError_t sched_slot(cudaStream_t stream, unsigned long long **out, unsigned int *tag) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -883,26 +880,19 @@ cudaError_t sched_slot(cudaStream_t stream, unsigned int **out, unsigned int *ep
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     e = cudaStreamIsCapturing(stream, &cap);
     if (e != cudaSuccess) return e;
-    unsigned int *base;
-    {
-        std::lock_guard<std::mutex> lock(g_sched_mutex);
-        if (!g_sched_base[dev]) {
-            void *p = nullptr;
-            e = cudaGetSymbolAddress(&p, g_sched);
-            if (e != cudaSuccess) return e;
-            g_sched_base[dev] = static_cast<unsigned int *>(p);
-        }
-        base = g_sched_base[dev];
+    unsigned long long id = 0;
+    if (cap == cudaStreamCaptureStatusNone && (e = cudaStreamGetId(stream, &id)) != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_sched_mutex);
+    if (!g_sched_base[dev]) {
+        void *p = nullptr;
+        e = cudaGetSymbolAddress(&p, g_sched);
+        if (e != cudaSuccess) return e;
+        g_sched_base[dev] = static_cast<unsigned long long *>(p);
     }
-    const unsigned int slot = cap == cudaStreamCaptureStatusNone
-                                  ? g_sched_turn.fetch_add(1u) % kSchedSlots
-                                  : kSchedSlots + g_graph_turn.fetch_add(1u) % kGraphSlots;
-    *out = base + 4 * slot;
-    unsigned int ep;
-    do {
-        ep = g_epoch.fetch_add(1u) + 1u;
-    } while (ep == 0u);
-    *epoch = ep;
+    *out = g_sched_base[dev] + (cap == cudaStreamCaptureStatusNone
+                                    ? static_cast<unsigned int>(g_stream_slots[dev].of(id))
+                                    : kSchedSlots + g_graph_turn.fetch_add(1u) % kGraphSlots);
+    *tag = kTagBase + g_tag_turn.fetch_add(1u) % kTagBase;
     return cudaSuccess;
 }
 
@@ -914,8 +904,9 @@ cudaError_t launch_t(const FwdArgs &a, const CUtensorMap &tq, const CUtensorMap 
     bool too_many = false;
     const long long sms = a.n_sm > 0 ? a.n_sm : 1;
     if (!plan_items(a, sms, &plan, &too_many)) return too_many ? cudaErrorInvalidConfiguration : cudaSuccess;
-    unsigned int *sched = nullptr, epoch = 0;
-    cudaError_t e = sched_slot(a.stream, &sched, &epoch);
+    unsigned long long *sched = nullptr;
+    unsigned int tag = 0;
+    cudaError_t e = sched_slot(a.stream, &sched, &tag);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(plan.n_items < sms ? plan.n_items : sms);
     e = cudaFuncSetAttribute(prefill_tc_kernel<D, FwdArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
@@ -923,7 +914,7 @@ cudaError_t launch_t(const FwdArgs &a, const CUtensorMap &tq, const CUtensorMap 
     // programmatic dependent launch: back to back with the previous kernel,
     // the launch and the prologue overlap its end (griddep_wait in the kernel)
     return launch_pdl(prefill_tc_kernel<D, FwdArgs>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, tq, tk, tv,
-                      plan.n_major, plan.group, plan.front, plan.n_items, sched, epoch);
+                      plan.n_major, plan.group, plan.front, plan.n_items, sched, tag);
 }
 
 // ------------------------------------------------------------ packed sequences
@@ -1021,8 +1012,9 @@ cudaError_t launch_packed_t(const PackedArgs &a, long long plan_tiles, const CUt
     const long long most = plan_tiles * heads;
     if (most > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
-    unsigned int *sched = nullptr, epoch = 0;
-    cudaError_t e = sched_slot(a.stream, &sched, &epoch);
+    unsigned long long *sched = nullptr;
+    unsigned int tag = 0;
+    cudaError_t e = sched_slot(a.stream, &sched, &tag);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(prefill_tc_kernel<D, PackedArgs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kSmemBytesPacked);
@@ -1041,7 +1033,7 @@ cudaError_t launch_packed_t(const PackedArgs &a, long long plan_tiles, const CUt
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(prefill_tc_kernel<D, PackedArgs>, dim3(grid), dim3(kThreads), L::kSmemBytesPacked, a.stream, a,
-                      tq, tk, tv, unit_rows, c_l2, heads, small ? 1 : 0, sched, epoch);
+                      tq, tk, tv, unit_rows, c_l2, heads, small ? 1 : 0, sched, tag);
 }
 
 }  // namespace
