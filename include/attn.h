@@ -425,8 +425,9 @@ ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int
  * w_p = freqs[p]; inverse = 1 turns by -n w_p, which takes a turn back and is
  * also its gradient (grad_x = mscale R(-n) grad_out).  Scaled frequencies for
  * long contexts are a matter of freqs and mscale.  Angles are formed modulo
- * one turn in 64-bit fixed point, so far positions lose nothing; the
- * arithmetic is fp32, rounded once to the output type.
+ * one turn in 64-bit fixed point: for |w_p| < 2^40 they are off by less than 10^-9
+ * radians at any position.  The fraction of a turn is then rounded to 24 bits (10^-7
+ * radians); the arithmetic is fp32, rounded once to the output type.
  *
  *   q, q_out  (T, H, D) rows; k, k_out  (T, H_kv, D) rows, H_kv = 0 (and NULL)
  *             for q alone.  An output may be its own input (same pointer and

@@ -304,3 +304,23 @@ def test_gpu_refusals(gpu):
     kc = torch.zeros(3, 2, 8, 64, dtype=BF16, device="cuda")
     with pytest.raises(attn.AttnError):  # 4 tokens for 3 sequences without cu_seqlens
         attn.attn_rope_append(q, k, k.clone(), kc, kc.clone(), f)
+
+
+def test_far_positions_and_negative_frequencies(gpu):
+    """Positions to the ends of int32 and frequencies of both signs, angles from exact
+    integers (w as a ratio of integers, 2 pi to 40 digits): the usual tolerance."""
+    two_pi = 62831853071795864769252867665590057683943   # 1e40 times
+    q = rows(4, 3, 64, 30, F32)
+    positions = [2147483647, -2147483648, 2147480009, -1999999999]
+    for sign in (1, -1):
+        f = sign * attn.attn_rope_frequencies(64)
+        angle = torch.empty(4, 32, dtype=torch.float64)
+        for i, n in enumerate(positions):
+            for p, w in enumerate(f.tolist()):
+                top, bottom = w.as_integer_ratio()
+                left = (n * top * 10 ** 40) % (two_pi * bottom)   # what whole turns leave over
+                angle[i, p] = left / (bottom * 10 ** 40)
+        a, b = q.cpu().double()[..., :32], q.cpu().double()[..., 32:]
+        c, s = angle.cos()[:, None], angle.sin()[:, None]
+        size = torch.cat([a.abs() + b.abs()] * 2, -1)
+        check(attn.attn_rope(q, None, ints(positions), f), torch.cat((a * c - b * s, b * c + a * s), -1), size, what=f"{sign}")

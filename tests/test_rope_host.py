@@ -4,6 +4,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import os
+import random
+import shutil
+import subprocess
+from fractions import Fraction
 
 import pytest
 import torch
@@ -98,3 +103,40 @@ def test_frequencies():
                 dict(rotary_dim=8, scaling="wavelength", low=4.0, high=4.0)):
         with pytest.raises(ValueError):
             attn.attn_rope_frequencies(**bad)
+
+
+def _pi(digits=120):
+    """pi as a Fraction, by Machin's formula in integers."""
+    one = 10 ** (digits + 10)
+
+    def arctan_inverse(n):
+        total, term, k = 0, one // n, 0
+        while term:
+            total += (-1) ** k * (term // (2 * k + 1))
+            term, k = term // (n * n), k + 1
+        return total
+
+    return Fraction(4 * (4 * arctan_inverse(5) - arctan_inverse(239)), one)
+
+
+def test_turns_are_right_to_the_last_unit(tmp_path):
+    """Frequencies as 64-bit fractions of a turn (csrc/rope_turns.h, compiled here for
+    the CPU) against exact arithmetic: within one unit, both signs."""
+    gxx = shutil.which("g++")
+    if not gxx:
+        pytest.skip("no g++")
+    csrc = os.path.join(os.path.dirname(os.path.abspath(attn.__file__)), "csrc")
+    (tmp_path / "t.cpp").write_text('#include "rope_turns.h"\n'
+                                    'extern "C" unsigned long long turns(double w) { return attn::rope_turns(w); }\n')
+    subprocess.run([gxx, "-O2", "-shared", "-fPIC", "-I", csrc, str(tmp_path / "t.cpp"), "-o", str(tmp_path / "t.so")],
+                   check=True)
+    turns = ctypes.CDLL(str(tmp_path / "t.so")).turns
+    turns.argtypes, turns.restype = [ctypes.c_double], ctypes.c_ulonglong
+    two_pi = 2 * _pi()
+    r = random.Random(7)
+    ws = [0.0, -0.0, 1.0, 2 * math.pi, math.pi, 1e-320, 6.283185307179587, float(2 ** 40 - 1), 1.5e-9]
+    ws += [10000.0 ** (-p / 32) for p in range(32)] + [r.uniform(-1, 1) * 2.0 ** r.randint(-70, 40) for _ in range(2000)]
+    for w in ws:
+        for x in (w, -w):
+            off = (turns(x) - Fraction(x) / two_pi * 2 ** 64) % 2 ** 64
+            assert min(off, 2 ** 64 - off) <= 1, x

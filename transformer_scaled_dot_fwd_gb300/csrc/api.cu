@@ -3,6 +3,7 @@
 // point is documented in include/attn.h.
 #include "attn.h"
 #include "kernels.h"
+#include "rope_turns.h"
 #include "ptx.cuh"
 
 #include <cuda.h>
@@ -975,12 +976,7 @@ static int rope_impl(const char *who, RopeArgs a, const long long *strides, cons
     }
     a.q_ts = st[0][0], a.q_hs = st[0][1], a.k_ts = st[1][0], a.k_hs = st[1][1], a.v_ts = st[2][0], a.v_hs = st[2][1];
     a.qo_ts = st[3][0], a.qo_hs = st[3][1], a.ko_ts = st[4][0], a.ko_hs = st[4][1];
-    // frequencies as fractions of a turn per position, modulo 1 (positions are whole numbers)
-    for (int p = 0; p < a.rotary_dim / 2; ++p) {
-        double f = freqs[p] / 6.283185307179586476925286766559;
-        f -= floor(f);
-        a.turns[p] = f < 1.0 ? static_cast<uint64_t>(ldexp(f, 64)) : 0;
-    }
+    for (int p = 0; p < a.rotary_dim / 2; ++p) a.turns[p] = rope_turns(freqs[p]);
     a.sin_scale = inverse ? -a.mscale : a.mscale;
     a.n_sm = num_sms();
     a.stream = static_cast<cudaStream_t>(stream);

@@ -9,9 +9,10 @@
 //
 // Angles.  n w_p reaches 10^5 .. 10^9 radians for far positions, where a
 // 32-bit product has lost every digit of the angle.  w_p / 2 pi is held as a
-// 64-bit fixed-point fraction of a turn, so n times it modulo 2^64 is the exact
-// fraction of a turn left over (one 64-bit multiply, wrapping included, and
-// the right one for negative n too); its top 32 bits go to sincospif.
+// 64-bit fixed-point fraction of a turn, right to its last unit (rope_turns.h), so n
+// times it modulo 2^64 is the fraction of a turn left over, off by |n| units, 2^-33 of
+// a turn at most (one 64-bit multiply, wrapping included, and the right one for
+// negative n too); its top 32 bits go to sincospif as a float.
 //
 // The rows are read once and written once: bound by HBM for prompts, by the
 // launch and one round trip for a step of single tokens.  A block takes one or two
