@@ -468,7 +468,8 @@ ATTN_API int attn_rope(const void *q, const void *k, void *q_out, void *k_out, i
  *   q, q_out  (T, H, D) rows; k, v  (T, H_kv, D) rows, H_kv >= 1
  *   k_out     NULL, or (T, H_kv, D) rows: the turned keys once more, token by
  *             token (attn_fwd_packed reads them); may be k itself
- *   kcache, vcache  (B, H_kv, Skv, D), contiguous, written
+ *   kcache, vcache  (B, H_kv, Skv, D), contiguous, written (NULL allowed when
+ *             Skv = 0: every token is turned but not cached)
  *   strides   NULL or HOST int64[10]: q, k, v, q_out, k_out, as in attn_rope
  *   cu_seqlens  device int32[B + 1], nondecreasing, or NULL: T / B tokens per
  *             sequence (T a multiple of B)

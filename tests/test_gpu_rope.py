@@ -324,3 +324,19 @@ def test_far_positions_and_negative_frequencies(gpu):
         c, s = angle.cos()[:, None], angle.sin()[:, None]
         size = torch.cat([a.abs() + b.abs()] * 2, -1)
         check(attn.attn_rope(q, None, ints(positions), f), torch.cat((a * c - b * s, b * c + a * s), -1), size, what=f"{sign}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_append_to_a_cache_of_no_rows(gpu, dtype):
+    """Every token is turned, none cached, as attn_decode_tree takes such a cache."""
+    T, H, H_kv, D = 6, 4, 2, 64
+    q, k, v = rows(T, H, D, 37, dtype), rows(T, H_kv, D, 38, dtype), rows(T, H_kv, D, 39, dtype)
+    none = torch.empty((2, H_kv, 0, D), dtype=dtype, device="cuda")
+    f = attn.attn_rope_frequencies(D)
+    pos = ints([0, 3, 70000, -4, 9, 1])
+    qo, ko = attn.attn_rope_append(q, k, v, none, none.clone(), f, positions=pos, k_out=torch.empty_like(k))
+    for x, got in ((q, qo), (k, ko)):
+        check(got, *turned(x, pos, f))
+    qo = attn.attn_rope_append(q, k, v, none, none.clone(), f, cu_seqlens=ints([0, 4, 6]))
+    # token i of n goes to row i - n of no cache, which is its position
+    check(qo, *turned(q, torch.tensor([-4, -3, -2, -1, -2, -1]), f))

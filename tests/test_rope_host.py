@@ -140,3 +140,12 @@ def test_turns_are_right_to_the_last_unit(tmp_path):
         for x in (w, -w):
             off = (turns(x) - Fraction(x) / two_pi * 2 ** 64) % 2 ** 64
             assert min(off, 2 ** 64 - off) <= 1, x
+
+
+def test_a_cache_of_no_rows_needs_no_memory(attn_lib):
+    """NULL caches pass the check when Skv = 0 (and the call then fails on the overlap,
+    before any CUDA call), not otherwise."""
+    assert append(attn_lib, kc=None, vc=None, Skv=0, qo=V) == I and "overlaps" in attn.attn_last_error()
+    for kw in (dict(kc=None, vc=None), dict(kc=None), dict(vc=None), dict(kc=None, vc=None, Skv=1)):
+        assert append(attn_lib, qo=V, **kw) == I and "NULL" in attn.attn_last_error()
+    assert append(attn_lib, kc=None, vc=None, Skv=0, T=0) == attn.ATTN_OK

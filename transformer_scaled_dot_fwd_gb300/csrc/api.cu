@@ -905,7 +905,7 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
 static int rope_impl(const char *who, RopeArgs a, const long long *strides, const double *freqs, int inverse,
                      int dtype, void *stream) {
     g_last_error[0] = '\0';
-    const bool append = a.kcache || a.vcache;
+    const bool append = a.append != 0;
     if (a.T < 0 || a.H < 1 || a.H_kv < 0 || (append && (a.H_kv < 1 || a.B < 1 || a.Skv < 0)))
         return fail(ATTN_EINVAL, "%s: need T >= 0, H >= 1, H_kv >= %d%s", who, append ? 1 : 0,
                     append ? ", B >= 1, Skv >= 0" : "");
@@ -1006,9 +1006,8 @@ ATTN_API int attn_rope_append(const void *q, const void *k, const void *v, void 
                               const int32_t *cu_seqlens, const int32_t *cache_len, const int32_t *positions,
                               const double *freqs, int rotary_dim, int interleaved, float mscale, int dtype,
                               void *stream) {
-    g_last_error[0] = '\0';
-    if (!kcache || !vcache) return fail(ATTN_EINVAL, "attn_rope_append: kcache and vcache must not be NULL");
     RopeArgs a{};
+    a.append = 1;
     a.q = q, a.k = k, a.v = v, a.q_out = q_out, a.k_out = k_out, a.kcache = kcache, a.vcache = vcache;
     a.T = T, a.H = H, a.H_kv = H_kv, a.D = D, a.B = B, a.Skv = Skv;
     a.cu_seqlens = cu_seqlens, a.cache_len = cache_len, a.positions = positions;

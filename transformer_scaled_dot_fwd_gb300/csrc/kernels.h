@@ -190,17 +190,18 @@ cudaError_t launch_decode_tc(const DecodeArgs &a, const CUtensorMap &tq, const C
                              const CUtensorMap &tv);
 
 // Rotary positions (attn_rope, attn_rope_append).  Rows are (token, head) with
-// element strides; kcache == nullptr: no append.
+// element strides.
 constexpr int kRopeMaxTokens = 2;  // tokens a block takes at most
 struct RopeArgs {
-    const void *q, *k, *v;      // (T, H | H_kv, D); v only with a cache
-    void *q_out, *k_out;        // k_out may be nullptr with a cache
-    void *kcache, *vcache;      // (B, H_kv, Skv, D) or nullptr
+    const void *q, *k, *v;      // (T, H | H_kv, D); v only to append
+    void *q_out, *k_out;        // k_out may be nullptr to append
+    void *kcache, *vcache;      // (B, H_kv, Skv, D); nullptr without rows
     const int32_t *cu_seqlens;  // device int32[B + 1] or nullptr (T / B tokens each)
     const int32_t *cache_len;   // device int32[B] or nullptr (Skv)
     const int32_t *positions;   // device int32[T] or nullptr (the cache row)
     long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
     int T, H, H_kv, D, B, Skv;
+    int append;                 // 0: no cache (Skv = 0 is a cache of no rows)
     int rotary_dim, interleaved;
     float mscale, sin_scale;    // multipliers of cos and of sin (negative sin_scale: inverse)
     int n_sm;

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kRopeThreads, 10)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int t0 = blockIdx.x * tokens;
     const int nt = min(tokens, a.T - t0);
-    const bool append = a.kcache != nullptr;
+    const bool append = a.append != 0;
 
     for (int i = warp; i < nt; i += kRopeWarps) {
         const int t = t0 + i;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kRopeThreads, 10)
 
 template <typename T, int VEC>
 cudaError_t launch_rope_t(const RopeArgs &a) {
-    const int rows = a.H + a.H_kv * (a.kcache ? 2 : 1);
+    const int rows = a.H + a.H_kv * (a.append ? 2 : 1);
     const long long sms = a.n_sm > 0 ? a.n_sm : 1;
     // two tokens a block when that still leaves several rounds of blocks an SM;
     // with few tokens the rows of one are split
