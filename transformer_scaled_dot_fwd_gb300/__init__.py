@@ -349,17 +349,31 @@ def attn_decode_splits(B: int, H: int, Skv: int, D: int) -> int:
 _native = None
 
 
+class _NoBinding:
+    """Stands for a binding that is not there: leaves every call to the checked path."""
+
+    def _none(self, *args):
+        return None
+
+    packed = rope = rope_append = tree = _none
+
+
 def _load_native():
     """The compiled binding (csrc/binding.cpp), with the library's functions bound."""
     global _native
     import importlib.util
-    path = os.path.join(_HERE, f"_binding.torch{_torch().__version__}.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is not built; run `python -m transformer_scaled_dot_fwd_gb300.build`")
-    spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    import warnings
     handle = lib()
+    path = os.path.join(_HERE, f"_binding.torch{_torch().__version__}.so")
+    try:
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"no compiled binding for this torch ({e}): the serving entry points take their checked path, some "
+                      "10 us more a call; run `python -m transformer_scaled_dot_fwd_gb300.build`", RuntimeWarning)
+        _native = _NoBinding()
+        return _native
     module.bind(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
         "attn_fwd_packed", "attn_fwd_packed_workspace", "attn_rope", "attn_rope_append", "attn_decode_tree",
         "attn_decode_tree_workspace")))
