@@ -75,3 +75,14 @@ def test_calls_give_the_same_without_the_binding(gpu, request, name, dtype):
         got = tensors(entry(*args, **kw))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_a_depth_of_zero_is_the_library_s_to_refuse(gpu):
+    x = torch.zeros(4, 2, 0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    with pytest.raises(attn.AttnError, match="D must be positive"):
+        attn.attn_fwd_packed(x, x.clone(), x.clone(), cu)
+    c = torch.zeros(1, 2, 8, 0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(attn.AttnError, match="D must be positive"):
+        attn.attn_decode_tree(x.transpose(0, 1)[None], c, c.clone(), cu.new_zeros(4))

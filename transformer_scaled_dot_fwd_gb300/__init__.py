@@ -393,35 +393,20 @@ def _elsewhere(device, stream):
     return torch.cuda.stream(stream)
 
 
-def _raw_stream(device):
+def _current(device):
     """cudaStream_t of the device's current stream."""
-    try:
-        return _torch()._C._cuda_getCurrentRawStream(device.index)  # spares building a Stream object
-    except AttributeError:
-        return _torch().cuda.current_stream(device).cuda_stream
+    return _torch().cuda.current_stream(device).cuda_stream
 
 
-class _Workspace:
-    """``nbytes`` of device memory for one call on the current device's ``stream``,
-    from torch's caching allocator (its private pool during a graph capture): given
-    back when the call is enqueued, which is safe because the allocator reuses it
-    in stream order.  The raw calls cost 1 us where an empty tensor costs 4."""
-    __slots__ = ("ptr", "free")
+def _scale(scale, D):
+    """The default, 1 / sqrt(D), where none is given (a D of 0 is the library's to refuse)."""
+    return scale if scale is not None else 1.0 / math.sqrt(D) if D else 1.0
 
-    def __init__(self, nbytes, stream):
-        c = _torch()._C
-        self.ptr = self.free = None
-        if nbytes > 0:
-            try:
-                self.ptr, self.free = c._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream), \
-                    c._cuda_cudaCachingAllocator_raw_delete
-            except AttributeError:
-                keep = _torch().empty(nbytes, dtype=_torch().uint8, device="cuda")
-                self.ptr, self.free = keep.data_ptr(), lambda _, keep=keep: None
 
-    def release(self):
-        if self.ptr is not None:
-            self.free(self.ptr)
+def _workspace(nbytes, device):
+    """``nbytes`` of device memory for one call on the device's current stream, given
+    back with the last reference: the allocator reuses it in stream order."""
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if nbytes > 0 else None
 
 
 def _rows(name, t, T, D, dtype, device):
@@ -536,16 +521,11 @@ def attn_fwd_packed(q, k, v, cu_seqlens, out=None, lse=None, scale: Optional[flo
     elif not (lse.dtype == torch.float32 and lse.shape == (T, H) and lse.is_contiguous() and lse.device == device):
         raise ValueError("lse must be a contiguous float32 (T, H) tensor on q's device")
     need = _packed_workspace(T, n_seq, H, H_kv, code)
-    stream = _raw_stream(device)
-    ws = _Workspace(need, stream)
-    try:
-        rc = lib().attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                   None if lse is None else lse.data_ptr(), T, H, H_kv, D,
-                                   _LL8(sq[0], sq[1], kt, kh, vt, vh, ot, oh), cu, n_seq,
-                                   1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, code, ws.ptr,
-                                   need, stream)
-    finally:
-        ws.release()
+    ws = _workspace(need, device)
+    rc = lib().attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                               None if lse is None else lse.data_ptr(), T, H, H_kv, D,
+                               _LL8(sq[0], sq[1], kt, kh, vt, vh, ot, oh), cu, n_seq, _scale(scale, D),
+                               1 if causal else 0, code, _ptr(ws), need, _current(device))
     if rc:
         _check(rc)
     return out if lse is None else (out, lse)
@@ -585,15 +565,10 @@ def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None,
         if out.shape != q.shape or out.dtype != q.dtype or out.device != device or so[3] != 1:
             raise ValueError("out must match q's shape, dtype and device, with contiguous rows")
     need = _tree_workspace(B, H, H_kv, T, Skv, D, code, device.index) if B and 0 < T <= 128 else 0
-    stream = _raw_stream(device)
-    ws = _Workspace(need, stream)
-    try:
-        rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), out.data_ptr(), B, H, H_kv, T,
-                                    Skv, D, _LL6(sq[0], sq[1], sq[2], so[0], so[1], so[2]), par, 0 if one else T, cl,
-                                    dl, 1.0 / math.sqrt(D) if scale is None else scale, code, ws.ptr,
-                                    need if need > 0 else 0, stream)
-    finally:
-        ws.release()
+    ws = _workspace(need, device)
+    rc = lib().attn_decode_tree(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), out.data_ptr(), B, H, H_kv, T, Skv,
+                                D, _LL6(sq[0], sq[1], sq[2], so[0], so[1], so[2]), par, 0 if one else T, cl, dl,
+                                _scale(scale, D), code, _ptr(ws), need if need > 0 else 0, _current(device))
     if rc:
         _check(rc)
     return out
@@ -666,7 +641,7 @@ def attn_rope(q, k, positions, freqs, q_out=None, k_out=None, interleaved: bool 
     rc = lib().attn_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
                          None if k is None else k_out.data_ptr(), T, H, H_kv, D,
                          _LL8(sq[0], sq[1], kt, kh, ot, oh, kot, koh), pos, fr, rd, 1 if interleaved else 0,
-                         1 if inverse else 0, mscale, code, _raw_stream(device))
+                         1 if inverse else 0, mscale, code, _current(device))
     if rc:
         _check(rc)
     return q_out if k is None else (q_out, k_out)
@@ -709,7 +684,7 @@ def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=
     rc = lib().attn_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
                                 None if k_out is None else k_out.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
                                 T, H, H_kv, D, _LL10(sq[0], sq[1], kt, kh, vt, vh, ot, oh, kot, koh), B, Skv, cu, cl,
-                                pos, fr, rd, 1 if interleaved else 0, mscale, code, _raw_stream(device))
+                                pos, fr, rd, 1 if interleaved else 0, mscale, code, _current(device))
     if rc:
         _check(rc)
     return q_out if k_out is None else (q_out, k_out)
