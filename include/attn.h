@@ -33,7 +33,11 @@
  *           and writes nothing before that kernel has completed, so stream
  *           order holds as for an ordinary launch.
  * dtype.    ATTN_BF16: bfloat16 inputs and output, fp32 accumulation and
- *           softmax statistics, output rounded to nearest even.
+ *           softmax statistics, output rounded to nearest even.  On the tensor
+ *           cores (every bf16 prefill, attn_decode_tree, attn_decode_gqa with 4 to
+ *           128 query heads a cached head) the softmax weights are rounded to
+ *           bf16 before they multiply V, by at most 2^-8 of each; their sum is
+ *           that of the fp32 weights.
  *           ATTN_F32: float32 everywhere (no TF32).  Output dtype = input dtype.
  * Masking.  causal: key j is visible from query i iff j <= i + (Skv - Sq)
  *           (the last query is aligned with the last key; for Sq == Skv this
@@ -362,7 +366,9 @@ ATTN_API int attn_decode_splits(int B, int H, int Skv, int D);
  *             each, and a captured call keeps its address.
  *
  * Scores are held as base-2 exponents in fp32: scaled scores above 2.3e38 in
- * magnitude count as infinite.  A row whose every score is -inf is a NaN.
+ * magnitude count as infinite.  A row whose every score is -inf is a NaN.  An
+ * infinite or NaN element of V makes that element infinite or NaN in every row that
+ * sees its key; where the key's weight underflows, an infinity may become a NaN.
  *
  * dtype, D, scale and errors as in attn_fwd; "Concurrency" there applies to the
  * bf16 form.  The same call gives the same bits every time.  bf16 rows do not
@@ -402,7 +408,11 @@ ATTN_API long long attn_fwd_packed_workspace(int T, int n_seq, int H, int H_kv, 
  *               aligned (may be NULL when that is 0); rules as in attn_fwd_packed
  *
  * The splits of a sequence are merged in order: a call gives the same bits
- * every time.  Scores beyond fp32's range as in attn_fwd_packed.  dtype, D, scale
+ * every time.  bf16 cuts the work of all sequences into equal shares, so the last
+ * bits of a sequence's rows may depend on the other sequences' lengths; in fp32 they
+ * depend on the sizes alone.  Scores beyond fp32's range and infinite or NaN elements
+ * of V as in attn_fwd_packed (which of the two a row gets where a weight underflows may
+ * depend on the cuts as well).  dtype, D, scale
  * and errors as in attn_fwd; T > 128 returns ATTN_EUNSUPPORTED.
  */
 ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vcache, void *out, int B, int H, int H_kv,
