@@ -506,3 +506,32 @@ def test_distinct_scores_of_huge_magnitude(gpu, dtype, causal, H, H_kv, D):
         for h in range(H):
             g = h * H_kv // H
             ref.check_huge(out[a:b, h], lse[a:b, h], q[a:b, h], k[a:b, g], v[a:b, g], visible, dtype, f"{b - a} head {h}")
+
+
+def test_a_captured_plan_follows_the_lengths(gpu):
+    """40 sequences, planned by a kernel of its own in the call's workspace: two captured
+    calls keep theirs apart, and replays take new lengths."""
+    T, H, H_kv, D = 4000, 4, 2, 64
+    sets = []
+    for seed in (40, 41):
+        q, k, v = tokens(T, H, H_kv, D, seed, BF16)
+        sets.append((q, k, v, ints(offsets([100] * 40)), torch.empty((T, H, D), dtype=BF16, device="cuda")))
+    want = [attn.attn_fwd_packed(*x[:4], causal=True) for x in sets]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            attn.attn_fwd_packed(*sets[1][:4], out=sets[1][4], causal=True)
+        attn.attn_fwd_packed(*sets[0][:4], out=sets[0][4], causal=True)
+        torch.cuda.current_stream().wait_stream(side)
+    for lens in (None, [0, 999, 1] * 4 + [0] * 27 + [0], [1] * 20 + [199] * 19 + [4000 - 20 - 19 * 199]):
+        if lens is not None:
+            assert sum(lens) == T and len(lens) == 40
+            sets[0][3].copy_(ints(offsets(lens)))
+            sets[1][3].copy_(ints(offsets(lens[::-1])))
+            want = [attn.attn_fwd_packed(*x[:4], causal=True) for x in sets]
+        graph.replay()
+        torch.cuda.synchronize()
+        attn.attn_device_status()
+        assert torch.equal(sets[0][4], want[0]) and torch.equal(sets[1][4], want[1])

@@ -121,3 +121,15 @@ def test_binding_refuses_cpu_tensors(attn_lib):
         attn.attn_fwd_packed(x, x, x, torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         attn.attn_decode_tree(x[None], x[None], x[None], torch.zeros(2, dtype=torch.int32))
+
+
+def test_tree_keys_are_counted_in_32_bits(attn_lib):
+    """Caches whose last tile or split ends past 2^31 keys are refused on the host."""
+    w = attn_lib.attn_decode_tree_workspace
+    for dtype, most in ((BF, 0x7fffff00), (F32, 0x40000000)):
+        assert w(1, 1, 1, 8, most, 64, dtype) >= 0
+        for Skv in (most + 1, 0x7fffffff):
+            assert w(1, 1, 1, 8, Skv, 64, dtype) == I
+            assert tree(attn_lib, B=1, H=1, H_kv=1, Skv=Skv, o=ctypes.c_void_p(1 << 60), v=ctypes.c_void_p(1 << 59),
+                        ws=ctypes.c_void_p(1 << 58), nb=1 << 50, dtype=dtype) == I
+            assert "too large" in attn.attn_last_error()

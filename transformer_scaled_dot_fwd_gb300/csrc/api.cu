@@ -774,10 +774,15 @@ ATTN_API int attn_fwd_packed(const void *q, const void *k, const void *v, void *
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_fwd_packed launch");
 }
 
+// Most cache rows of a sequence: the kernels count keys in 32 bits to the end of a
+// 128-key tile (bf16), or of the last of eight splits, half of them past the end (fp32).
+static int tree_max_rows(int dtype) { return dtype == ATTN_BF16 ? 0x7fffff00 : 0x40000000; }
+
 ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int Skv, int D, int dtype) {
     if (B < 1 || H < 1 || H_kv < 1 || H % H_kv || T < 0 || T > kTreeMaxTokens || Skv < 0 || (D != 64 && D != 128) ||
         (dtype != ATTN_F32 && dtype != ATTN_BF16))
         return ATTN_EINVAL;
+    if (Skv > tree_max_rows(dtype)) return ATTN_EINVAL;
     if (T == 0 || Skv == 0) return 0;
     if (dtype == ATTN_F32) {
         const int chunk = tree_chunk_f32(B, H, H_kv, T, Skv, D, num_sms());
@@ -856,7 +861,7 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
         return fail(ATTN_EINVAL, "%s: out overlaps an input", who);
     const bool f32 = dtype == ATTN_F32;
     const long long rows = static_cast<long long>(B) * H * T;
-    if (rows >= (1LL << 31) || bh_kv * Skv >= (1LL << 31)) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    if (rows >= (1LL << 31) || bh_kv * Skv >= (1LL << 31) || Skv > tree_max_rows(dtype)) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
     const int chunk = f32 && Skv > 0 ? tree_chunk_f32(B, H, H_kv, T, Skv, D, num_sms()) : 64;
     const int n_split = !f32 ? tree_tc_grid(B, H, H_kv, T, Skv, num_sms()) : Skv > 0 ? tree_splits_f32(Skv, chunk) : 1;
     if (n_split < 0) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
