@@ -525,7 +525,7 @@ def test_a_captured_plan_follows_the_lengths(gpu):
             attn.attn_fwd_packed(*sets[1][:4], out=sets[1][4], causal=True)
         attn.attn_fwd_packed(*sets[0][:4], out=sets[0][4], causal=True)
         torch.cuda.current_stream().wait_stream(side)
-    for lens in (None, [0, 999, 1] * 4 + [0] * 27 + [0], [1] * 20 + [199] * 19 + [4000 - 20 - 19 * 199]):
+    for lens in (None, [0, 999, 1] * 4 + [0] * 28, [1] * 20 + [199] * 19 + [4000 - 20 - 19 * 199]):
         if lens is not None:
             assert sum(lens) == T and len(lens) == 40
             sets[0][3].copy_(ints(offsets(lens)))
