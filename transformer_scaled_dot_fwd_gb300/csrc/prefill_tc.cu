@@ -54,8 +54,8 @@
 // tiles: on the diagonal, or past the sequence's end): rows past the end become
 // zeros, and non-finite elements become zeros that are added back after the
 // epilogue, to the rows that see them only.  Measured (H 32, H_kv 8, D 128, causal):
-// sequences of 8192, 5001, 4097 and 1023 tokens 608-615 us (1460-1485 TFLOP/s); 23
-// sequences of 2048 to 1 tokens 93 us, of it about 27 us the boundaries of nine items
+// sequences of 8192, 5001, 4097 and 1023 tokens 608-625 us (1440-1480 TFLOP/s); 23
+// sequences of 2048 to 1 tokens 92 us, of it about 27 us the boundaries of nine items
 // a CTA; 16 sequences of 512 tokens 58 us, as one dense batch 53 us (with H_kv 32, two
 // edge tiles an item, 71 and 61 us); 4 of 2048 tokens 112 and 110 us (120 and 114 us).
 // Without edge tiles the gap halves.

@@ -26,7 +26,8 @@
 // rows.  16385 tokens of 32 + 8 heads of depth 128 into a cache (402 MB moved): 66
 // us, 6.1 TB/s; 256 threads and 8 tokens a block took 74 us, two rows in flight
 // per thread at 106 registers 109 us.  32768 tokens of 64 heads, half of each
-// turned (1.07 GB): 164 us, 6.5 TB/s.  A step of 64 tokens into a cache: 3.3 us.
+// turned (1.07 GB): 164 us, 6.5 TB/s.  A step of 64 tokens into a cache: 3.2 us.  With a
+// rotary depth of 36 (VEC = 1, single elements) the first takes 211 us, the second 505.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "serving.cuh"

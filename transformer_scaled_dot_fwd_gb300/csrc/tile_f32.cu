@@ -7,8 +7,8 @@
 // depths of a score, two columns of the output).  The eight lanes that share rows
 // differ in bits 1-3 of their number: then lanes 2 l and 2 l + 1 read the same K and V
 // elements, lanes l and l ^ 2 the same Q and P elements, and a 16-byte shared-memory
-// load takes two passes instead of four (passes of the whole kernel 5.6 to 3.4 million;
-// the FMA pipe is the bound).  K rows are padded by 16 bytes so that eight lanes read
+// load takes two passes instead of four (passes of the whole kernel 5.6 to 3.4 million).
+// K rows are padded by 16 bytes so that eight lanes read
 // eight rows without conflicts.  The next tile's K is copied in (cp.async) while P V
 // runs, its V while the scores are computed.
 //
@@ -20,7 +20,11 @@
 // many and two blocks an SM, where there are many blocks (the launches say when).
 //
 // Measured: six sequences of 700 to 1 tokens, 4 heads of depth 64, not causal (0.86
-// GFLOP): 39 us; 232 blocks on 152 SMs leave a second round to some of the long ones.
+// GFLOP, 11.6 us of FMAs): 39.5 us.  No pipe bounds it: 232 blocks on 152 SMs leave a
+// second round to some of the long ones (a third of the SMs' time idle), and while an SM
+// has work the FMA pipe (51 %), the issue slots (50 %) and shared memory (48 %) are each
+// half busy, 16 warps that wait on the FMA pipe in turn, on results and on the three
+// barriers of a tile.
 // Earlier forms, 128 threads a tile of 64 keys: one a block 90 us, two 47 us, four 43
 // us, with equal shares 40 us; 8 rows a thread 45 us.
 //

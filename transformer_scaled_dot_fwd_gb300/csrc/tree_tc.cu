@@ -36,7 +36,7 @@
 // Measured (H 32, H_kv 8, D 128): 16 sequences of 2000-8192 rows, up to 24 drafts
 // (323 MB to read): 63 us, of it 49 us at 6.6 TB/s between the first and the last
 // tile, 4 us the merge.  64 sequences of 4096-8192 rows, 63 drafts (1.69 GB, 407
-// GFLOP): 314-329 us, 1240-1295 TFLOP/s, a pair of tiles in 1.7 us.  One sequence
+// GFLOP): 314-348 us, 1170-1295 TFLOP/s by the power limit, a pair of tiles in 1.7 us.  One sequence
 // of 1500 rows, 8 drafts: 12 us (12.8 a call).  The first form, splits of a fixed number of keys
 // with a CTA and one stream each, two to an SM, took 98, 526 and 14 us: a single
 // stream waits for its own MMAs.
