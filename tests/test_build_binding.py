@@ -22,6 +22,8 @@ def test_the_library_is_linked_where_the_binding_does_not_compile(tmp_path, monk
         monkeypatch.setattr(build, name, value)
     fails = [sys.executable, "-c", "print('Python.h: No such file'); raise SystemExit(1)", "-o", out + ".tmp"]
     monkeypatch.setattr(build, "_binding_command", lambda: (out, fails))
+    with open(out, "w"):  # a binding of older sources must not stay beside the new library
+        os.utime(out, (1, 1))
     with pytest.warns(RuntimeWarning, match="(?s)could not compile csrc/binding.cpp.*Python.h: No such file"):
         assert build.build(quiet=True) == str(library)
     assert library.exists() and not os.path.exists(out)

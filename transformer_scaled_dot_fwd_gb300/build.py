@@ -90,6 +90,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
     if started and started.returncode == 0:
         os.replace(binding[1][binding[1].index("-o") + 1], binding[0])
     elif started:
+        if os.path.exists(binding[0]):
+            os.remove(binding[0])  # of older sources: its calls may not be the library's any more
         warnings.warn(f"{os.path.basename(binding[1][0])} could not compile csrc/binding.cpp; the serving entry points "
                       f"take their checked path in Python, some 10 us more a call:\n{text}", RuntimeWarning)
     return LIB_PATH
