@@ -423,6 +423,58 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
 ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int Skv, int D, int dtype);
 
 /*
+ * attn_fwd_paged -- attention of new tokens over a paged KV cache: chunks of prompts,
+ * single tokens, and both in one call.
+ *
+ * The cache is a pool of pages of page_size rows; sequence s holds L_s = cache_len[s]
+ * keys, key j in row j % page_size of page page_table[s][j / page_size].  Its last n_s
+ * keys are those of its new tokens (attn_rope_append_paged puts them there), which are
+ * tokens [cu_seqlens[s], cu_seqlens[s + 1]) of token-major (T, H, D) tensors.  Token i
+ * of them sits at position L_s - n_s + i and sees keys j <= L_s - n_s + i, as in
+ * attn_fwd_chunked; one whose position is negative sees none: its row is zero and its
+ * lse -inf.  Grouped heads as in attn_fwd_gqa.  Rows outside every sequence (before
+ * cu_seqlens[0], from cu_seqlens[n_seq] on) are left as they were in out and lse.  A key
+ * that a row does not see leaves no trace in it, whatever its page holds.  Sequences may
+ * share pages.
+ *
+ *   q, out      (T, H, D) rows; out must not overlap the inputs
+ *   kpages, vpages  (n_pages, H_kv, page_size, D) pages, or any strides of them: rows of
+ *               (n_pages, page_size, H_kv, D) pages, two halves of one tensor.  A
+ *               contiguous (B, H_kv, Skv, D) cache is one page a sequence.
+ *   page_size   a multiple of 8 (ATTN_EUNSUPPORTED otherwise); powers of two from 16 on
+ *               are the fast case
+ *   lse         NULL, or device float (T, H), written: the natural log-sum-exp of each
+ *               row's scaled scores
+ *   strides     NULL (contiguous), or HOST int64[10]: elements from token to token and
+ *               from head to head of q and of out, then from page to page, head to head
+ *               and row to row of kpages and of vpages; multiples of 16 bytes
+ *   page_table  device int32, max_pages entries a sequence, table_stride apart.  Only
+ *               entries that hold a visible key are read.  One outside [0, n_pages) counts
+ *               as a page of zeros, never as an access outside the pool.
+ *   cu_seqlens  device int32[n_seq + 1], nondecreasing, within [0, T], or NULL: T / n_seq
+ *               tokens each (one each when T = n_seq).  Other contents give undefined
+ *               rows of out and lse, never an access outside the tensors.
+ *   cache_len   device int32[n_seq], each clamped to [0, max_pages * page_size], or NULL
+ *               (every row of the table full)
+ *   workspace   device memory of attn_fwd_paged_workspace(...) bytes, 16-byte aligned (may
+ *               be NULL when that is 0); rules as in attn_fwd_packed
+ *
+ * The parts of a sequence are merged in order: a call gives the same bits every time.  The
+ * work of all sequences is cut into equal shares, so the last bits of a row may depend on
+ * the other sequences' lengths (bf16), or on the sizes of the call (fp32).  Scores beyond
+ * fp32's range and infinite or NaN elements of V as in attn_decode_tree.  dtype, D, scale
+ * and errors as in attn_fwd; no work counter is used, and no device memory is allocated.
+ */
+ATTN_API int attn_fwd_paged(const void *q, const void *kpages, const void *vpages, void *out, float *lse, int T, int H,
+                            int H_kv, int D, const long long *strides, int n_pages, int page_size, const int32_t *page_table,
+                            int max_pages, long long table_stride, const int32_t *cu_seqlens, const int32_t *cache_len,
+                            int n_seq, float scale, int dtype, void *workspace, long long workspace_bytes, void *stream);
+/* Bytes of workspace that call needs on the current device (may be 0); negative on bad
+ * sizes.  ragged: cu_seqlens is given. */
+ATTN_API long long attn_fwd_paged_workspace(int T, int n_seq, int H, int H_kv, int D, int max_pages, int page_size, int ragged,
+                                            int dtype);
+
+/*
  * attn_rope -- rotary positions: turns the pairs of each head row of q and k by
  * an angle proportional to the row's position, before attention or caching.
  *

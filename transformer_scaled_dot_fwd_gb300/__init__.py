@@ -50,6 +50,9 @@ SIGNATURES = {
     "attn_fwd_packed_workspace": (_ll, [_i, _i, _i, _i, _i]),
     "attn_decode_tree": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _f, _i, _vp, _ll, _vp]),
     "attn_decode_tree_workspace": (_ll, [_i, _i, _i, _i, _i, _i, _i]),
+    "attn_fwd_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _vp, _i, _ll, _vp, _vp, _i, _f, _i, _vp, _ll,
+                            _vp]),
+    "attn_fwd_paged_workspace": (_ll, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "attn_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp]),
     "attn_rope_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
                               _i, _i, _f, _i, _vp]),
@@ -355,7 +358,7 @@ class _NoBinding:
     def _none(self, *args):
         return None
 
-    packed = rope = rope_append = tree = _none
+    packed = rope = rope_append = tree = paged = _none
 
 
 def _load_native():
@@ -377,6 +380,8 @@ def _load_native():
     module.bind(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
         "attn_fwd_packed", "attn_fwd_packed_workspace", "attn_rope", "attn_rope_append", "attn_decode_tree",
         "attn_decode_tree_workspace")))
+    module.bind_paged(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
+        "attn_fwd_paged", "attn_fwd_paged_workspace")))
     _native = module
     return module
 
@@ -574,6 +579,81 @@ def attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None,
     return out
 
 
+def _pages(kpages, vpages, dtype, device, D, layered=False):
+    """(n_pages, H_kv, page_size, strides of both in order) of a pair of page pools."""
+    shape, n = kpages.shape, 5 if layered else 4
+    if len(shape) != n or vpages.shape != shape or shape[-1] != D:
+        raise ValueError(f"kpages and vpages must be ({'layers, ' if layered else ''}n_pages, H_kv, page_size, {D})")
+    if kpages.dtype != dtype or vpages.dtype != dtype:
+        raise TypeError("kpages and vpages must share one dtype" if layered else "q, kpages, vpages must share one dtype")
+    if kpages.device != device or vpages.device != device:
+        raise ValueError("the pages must be on one device" if layered else "the pages must be on q's device")
+    ks, vs = kpages.stride(), vpages.stride()
+    if ks[-1] != 1 or vs[-1] != 1:
+        raise ValueError("kpages and vpages must have contiguous rows of D elements")
+    return shape[-4], shape[-3], shape[-2], ks[:-1] + vs[:-1]
+
+
+def _table(page_table, device):
+    """(rows, max_pages, row stride, data_ptr) of a page table."""
+    if not (page_table.dtype == _torch().int32 and page_table.device == device and page_table.dim() == 2
+            and (page_table.stride(1) == 1 or page_table.shape[1] <= 1)):
+        raise ValueError("page_table must be an int32 tensor of shape (sequences, max_pages) with contiguous rows on the "
+                         "pages' device")
+    return page_table.shape[0], page_table.shape[1], page_table.stride(0), page_table.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace(T, n_seq, H, H_kv, D, max_pages, page_size, ragged, dtype, device):
+    return lib().attn_fwd_paged_workspace(T, n_seq, H, H_kv, D, max_pages, page_size, ragged, dtype)
+
+
+def attn_fwd_paged(q, kpages, vpages, page_table, cache_len=None, cu_seqlens=None, out=None, lse=None,
+                   scale: Optional[float] = None, return_lse: bool = False, stream=None):
+    """Attention of new tokens over a paged KV cache: q (T, H, D), pages (n_pages,
+    H_kv, page_size, D) (any strides, contiguous rows), ``page_table`` int32
+    (sequences, max_pages).  Sequence s has tokens [cu_seqlens[s], cu_seqlens[s + 1])
+    (T / sequences each without cu_seqlens, one each in a decode step), the last of
+    its cache_len[s] keys (default: all its table holds); each sees the keys up to its own.
+    Returns ``out`` (T, H, D), or ``(out, lse)`` with the (T, H) fp32 log-sum-exp
+    when ``return_lse`` (or an ``lse`` tensor) is given.  Rows outside every sequence
+    are not written.  See include/attn.h.
+    """
+    if stream is None:
+        done = (_native or _load_native()).paged(q, kpages, vpages, page_table, cache_len, cu_seqlens, out, lse, scale,
+                                                 return_lse)
+        if done is not None:
+            return done
+    torch = _torch()
+    (T, H, D), sq, code, device = _first(q, 3)
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
+            return attn_fwd_paged(q, kpages, vpages, page_table, cache_len, cu_seqlens, out, lse, scale, return_lse)
+    n_pages, H_kv, P, ps = _pages(kpages, vpages, q.dtype, device, D)
+    if H_kv < 1 or H % H_kv:
+        raise ValueError("kpages and vpages must be (n_pages, H_kv, page_size, D), with H_kv dividing H")
+    n_seq, M, ts, table = _table(page_table, device)
+    cu = _ints("cu_seqlens", cu_seqlens, (n_seq + 1,), device)
+    cl = _ints("cache_len", cache_len, (n_seq,), device)
+    if cu is None and (n_seq == 0 and T or n_seq and T % n_seq):
+        raise ValueError(f"without cu_seqlens q's {T} tokens must be a multiple of the {n_seq} sequences")
+    out, ot, oh = _out_rows("out", out, T, H, D, q.dtype, device)
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((T, H), dtype=torch.float32, device=device)
+    elif not (lse.dtype == torch.float32 and lse.shape == (T, H) and lse.is_contiguous() and lse.device == device):
+        raise ValueError("lse must be a contiguous float32 (T, H) tensor on q's device")
+    need = _paged_workspace(T, n_seq, H, H_kv, D, M, P, 0 if cu is None else 1, code, device.index)
+    ws = _workspace(need, device)
+    rc = lib().attn_fwd_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), out.data_ptr(),
+                              None if lse is None else lse.data_ptr(), T, H, H_kv, D,
+                              _LL10(sq[0], sq[1], ot, oh, *ps), n_pages, P, table, M, ts, cu, cl, n_seq,
+                              _scale(scale, D), code, _ptr(ws), need if need > 0 else 0, _current(device))
+    if rc:
+        _check(rc)
+    return out if lse is None else (out, lse)
+
+
 def attn_rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: Optional[str] = None,
                           factor: float = 1.0, original_len: int = 8192, low: float = 1.0, high: float = 4.0):
     """Rotary frequencies in radians per position, a CPU float64 tensor of
@@ -707,6 +787,7 @@ def attn_release() -> None:
 
 __all__ = [
     "attn_fwd", "attn_fwd_chunked", "attn_fwd_debug", "attn_fwd_host", "attn_decode", "attn_decode_noalloc", "attn_decode_splits", "attn_fwd_packed", "attn_decode_tree",
+    "attn_fwd_paged",
     "attn_rope",
     "attn_rope_append", "attn_rope_frequencies", "attn_device_status", "attn_release",
     "attn_last_error", "attn_selftest_wait_timeout", "lib", "AttnError", "SIGNATURES", "LIB_PATH",

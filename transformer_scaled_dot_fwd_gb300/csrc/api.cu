@@ -218,6 +218,111 @@ int make_map_packed(CUtensorMap *map, const Rows &r, int D) {
     return ATTN_OK;
 }
 
+// (D, heads, T) bf16 view of (T, heads, D) rows with byte strides; boxes of 64 x heads x
+// tokens with 128-byte swizzle: a token's heads are consecutive rows.
+int make_map_tokens(CUtensorMap *map, const Rows &r, int D, int heads, int tokens) {
+    EncodeTiledFn encode;
+    int rc = get_encode(&encode);
+    if (rc) return rc;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(r.n_inner),
+                                static_cast<cuuint64_t>(r.n_outer)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(r.si), static_cast<cuuint64_t>(r.so)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult e = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<char *>(r.p), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) return fail(ATTN_ECUDA, "cuTensorMapEncodeTiled (tokens) failed (%d)", static_cast<int>(e));
+    return ATTN_OK;
+}
+
+// ------------------------------------------------------------ paged caches
+
+// A pool of pages: (layers, n_pages, H_kv, P) rows of D elements, strides in bytes.
+struct Pool {
+    const char *p;
+    long long n[4], st[4], row;
+};
+
+// strides: elements from page to page, head to head and row to row (NULL: contiguous).
+// False when a stride is out of range.
+bool make_pool(Pool *o, const void *p, int layers, long long layer_stride, int n_pages, int H_kv, int P, int D, long long esz,
+               const long long *strides) {
+    const long long dense[4] = {1LL * n_pages * H_kv * P * D, 1LL * H_kv * P * D, 1LL * P * D, D};
+    const long long n[4] = {layers, n_pages, H_kv, P};
+    o->p = static_cast<const char *>(p);
+    o->row = D * esz;
+    double extent = static_cast<double>(o->row);
+    for (int i = 0; i < 4; ++i) {
+        const long long s = n[i] <= 1 ? dense[i] : !strides ? dense[i] : i == 0 ? layer_stride : strides[i - 1];
+        if (s < 0 || s > kMaxStride) return false;
+        o->n[i] = n[i];
+        o->st[i] = s * esz;
+        extent += static_cast<double>(n[i]) * static_cast<double>(o->st[i]);
+    }
+    return extent <= kMaxExtent;
+}
+bool pool_empty(const Pool &o) { return o.n[0] < 1 || o.n[1] < 1 || o.n[2] < 1 || o.n[3] < 1; }
+size_t pool_extent(const Pool &o) {
+    if (pool_empty(o)) return 0;
+    long long e = o.row;
+    for (int i = 0; i < 4; ++i) e += (o.n[i] - 1) * o.st[i];
+    return static_cast<size_t>(e);
+}
+// `dims` runs of rows nested in one another: sorted by stride, each one clears the extent of
+// the smaller ones.
+bool nested_distinct(long long *n, long long *st, int dims, long long row) {
+    long long extent = row;
+    for (int i = 0; i < dims; ++i) {
+        for (int y = i + 1; y < dims; ++y)
+            if (st[y] < st[i]) {
+                const long long t = st[i], c = n[i];
+                st[i] = st[y], n[i] = n[y], st[y] = t, n[y] = c;
+            }
+        if (n[i] <= 1) continue;
+        if (st[i] < extent) return false;
+        extent += (n[i] - 1) * st[i];
+    }
+    return true;
+}
+bool pool_distinct(const Pool &o) {
+    long long n[4], st[4];
+    for (int i = 0; i < 4; ++i) n[i] = o.n[i], st[i] = o.st[i];
+    return pool_empty(o) || nested_distinct(n, st, 4, o.row);
+}
+// May rows of two pools share a byte?  Known not to: extents apart, or two halves of one
+// tensor (the same strides, and the step from one to the other nested among them).
+bool pools_overlap(const Pool &a, const Pool &b) {
+    if (pool_empty(a) || pool_empty(b)) return false;
+    if (!overlaps(a.p, pool_extent(a), b.p, pool_extent(b))) return false;
+    long long n[5], st[5];
+    for (int i = 0; i < 4; ++i) {
+        if (a.st[i] != b.st[i] || a.n[i] != b.n[i]) return true;
+        n[i] = a.n[i], st[i] = a.st[i];
+    }
+    n[4] = 2, st[4] = a.p < b.p ? b.p - a.p : a.p - b.p;
+    return !nested_distinct(n, st, 5, a.row);
+}
+
+// (D, P, H_kv, n_pages) bf16 view of one layer; boxes of 64 x rows x 1 x 1 with 128-byte
+// swizzle, pages out of range read as zeros.
+int make_map_pages(CUtensorMap *map, const Pool &o, int rows) {
+    EncodeTiledFn encode;
+    int rc = get_encode(&encode);
+    if (rc) return rc;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(o.row / 2), static_cast<cuuint64_t>(o.n[3]),
+                                static_cast<cuuint64_t>(o.n[2]), static_cast<cuuint64_t>(o.n[1])};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(o.st[3]), static_cast<cuuint64_t>(o.st[2]),
+                                   static_cast<cuuint64_t>(o.st[1])};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult e = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<char *>(o.p), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) return fail(ATTN_ECUDA, "cuTensorMapEncodeTiled (pages) failed (%d)", static_cast<int>(e));
+    return ATTN_OK;
+}
+
 // ------------------------------------------------------------ decode workspace
 
 // The decode partials.  A buffer the workspace outgrows is kept on the
@@ -904,6 +1009,172 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
         e = Skv > 0 ? launch_tree_tc(a, tk, tv) : launch_tree_zero(a);
     }
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_decode_tree launch");
+}
+
+// What the sizes of a paged call decide: rows of a tile, CTAs, splits.  n_seq, T, H, H_kv,
+// D, P, max_len and `ragged` (sequences of different numbers of tokens) are given.
+// Returns the bytes of workspace, or a negative code with its reason.
+static long long paged_sizes(const char *who, PagedArgs &a, bool ragged, int dtype) {
+    const int G = a.H / a.H_kv;
+    a.n_sm = num_sms();
+    a.per_seq = ragged || a.n_seq < 1 ? 0 : a.T / a.n_seq;
+    const long long rows = static_cast<long long>(a.T) * a.H;
+    if (rows >= (1LL << 31) || a.max_len > tree_max_rows(dtype)) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    if (a.T == 0 || a.n_seq == 0) return 0;
+    if (dtype == ATTN_F32) {
+        static const int32_t some = 0;
+        PagedArgs b = a;
+        b.cu_seqlens = ragged ? &some : nullptr;
+        const long long blocks = paged_f32_blocks(b) * a.H_kv;
+        a.n_split = paged_f32_splits(b);
+        if (blocks * a.n_split >= (1LL << 31) || blocks * 4 >= (1LL << 31))
+            return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+        return a.n_split <= kTreeClusterF32 ? 0 : blocks * 32 * a.n_split * (a.D + 2) * 4;
+    }
+    a.groups = (G + 127) / 128;
+    a.heads = (G + a.groups - 1) / a.groups;
+    a.tokens = 128 / a.heads;
+    const int most = ragged ? a.T : a.per_seq;  // tokens of a sequence
+    a.box_tokens = most < a.tokens ? most : a.tokens;
+    a.single = most <= a.tokens;
+    a.slot_rows = a.single ? (a.box_tokens * a.heads + 31) / 32 * 32 : 256;
+    a.box = 128;
+    while (a.P % a.box) a.box /= 2;
+    const double axis = paged_tc_axis(a);
+    if (axis * 1024 > 4e18) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    a.grid = axis / 256 < a.n_sm ? static_cast<int>(axis / 256) + 1 : a.n_sm;
+    if (a.grid > 1023) a.grid = 1023;
+    return a.grid * 32LL + 2LL * a.grid * a.slot_rows * (a.D + 2) * 4;
+}
+
+static int paged_shape_ok(const char *who, int T, int n_seq, int H, int H_kv, int D, int max_pages, int P, int dtype) {
+    if (T < 0 || n_seq < 0 || H < 1 || max_pages < 0)
+        return fail(ATTN_EINVAL, "%s: need T >= 0, n_seq >= 0, H >= 1, max_pages >= 0", who);
+    if (H_kv < 1 || H % H_kv != 0)
+        return fail(ATTN_EINVAL, "%s: H_kv must divide H (got H = %d, H_kv = %d)", who, H, H_kv);
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return fail(ATTN_EINVAL, "%s: unknown dtype %d", who, dtype);
+    if (D <= 0) return fail(ATTN_EINVAL, "%s: D must be positive (got %d)", who, D);
+    if (D != 64 && D != 128) return fail(ATTN_EUNSUPPORTED, "%s: D = %d not supported (64 or 128)", who, D);
+    if (P < 1) return fail(ATTN_EINVAL, "%s: a page must have rows (got %d)", who, P);
+    if (P % 8) return fail(ATTN_EUNSUPPORTED, "%s: pages of %d rows not supported (a multiple of 8)", who, P);
+    if (static_cast<long long>(max_pages) * P > 0x7fffffffLL)
+        return fail(ATTN_EINVAL, "%s: %d pages of %d rows are too many for a sequence", who, max_pages, P);
+    return ATTN_OK;
+}
+
+ATTN_API long long attn_fwd_paged_workspace(int T, int n_seq, int H, int H_kv, int D, int max_pages, int page_size, int ragged,
+                                            int dtype) {
+    int rc = paged_shape_ok("attn_fwd_paged_workspace", T, n_seq, H, H_kv, D, max_pages, page_size, dtype);
+    if (rc) return rc;
+    if (!ragged && n_seq > 0 && T % n_seq) return ATTN_EINVAL;
+    PagedArgs a{};
+    a.T = T, a.n_seq = n_seq, a.H = H, a.H_kv = H_kv, a.D = D, a.P = page_size, a.max_len = max_pages * page_size;
+    return paged_sizes("attn_fwd_paged_workspace", a, ragged != 0, dtype);
+}
+
+ATTN_API int attn_fwd_paged(const void *q, const void *kpages, const void *vpages, void *out, float *lse, int T, int H,
+                            int H_kv, int D, const long long *strides, int n_pages, int page_size, const int32_t *page_table,
+                            int max_pages, long long table_stride, const int32_t *cu_seqlens, const int32_t *cache_len,
+                            int n_seq, float scale, int dtype, void *workspace, long long workspace_bytes, void *stream) {
+    g_last_error[0] = '\0';
+    const char *who = "attn_fwd_paged";
+    int rc = paged_shape_ok(who, T, n_seq, H, H_kv, D, max_pages, page_size, dtype);
+    if (rc) return rc;
+    if (n_pages < 0) return fail(ATTN_EINVAL, "%s: need n_pages >= 0 (got %d)", who, n_pages);
+    if (!(scale >= 0.f) || isinf(scale)) return fail(ATTN_EINVAL, "%s: scale must be finite and >= 0", who);
+    if (!cu_seqlens && n_seq > 0 && T % n_seq)
+        return fail(ATTN_EINVAL, "%s: without cu_seqlens T must be a multiple of n_seq (got %d, %d)", who, T, n_seq);
+    if (T == 0 || n_seq == 0) return ATTN_OK;
+    if (max_pages == 0) n_pages = 0;  // nothing is read
+    if (max_pages > 0 && n_pages == 0) return fail(ATTN_EINVAL, "%s: a table of pages needs n_pages >= 1", who);
+    if (!q || !out || (n_pages > 0 && (!kpages || !vpages || !page_table))) return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
+    if (!aligned16(q) || !aligned16(out) || (n_pages > 0 && (!aligned16(kpages) || !aligned16(vpages))))
+        return fail(ATTN_EINVAL, "%s: q, kpages, vpages and out must be 16-byte aligned", who);
+    if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(cu_seqlens) |
+         reinterpret_cast<uintptr_t>(cache_len) | reinterpret_cast<uintptr_t>(lse)) & 3u)
+        return fail(ATTN_EINVAL, "%s: page_table, cu_seqlens, cache_len and lse must be 4-byte aligned", who);
+    if (n_seq > 1 && (table_stride < 0 || table_stride > kMaxStride / n_seq))
+        return fail(ATTN_EINVAL, "%s: table_stride %lld is negative or too large", who, table_stride);
+    const long long esz = dtype == ATTN_BF16 ? 2 : 4;
+    const long long dense[4] = {static_cast<long long>(H) * D, D, static_cast<long long>(H) * D, D};
+    const long long *st = strides ? strides : dense;
+    const Rows rq = make_rows(q, T, H, st[0], st[1], D, esz), ro = make_rows(out, T, H, st[2], st[3], D, esz);
+    const Rows *rows[2] = {&rq, &ro};
+    for (int i = 0; i < 2; ++i) {
+        const char *name = i ? "out" : "q";
+        if (!rows_distinct(*rows[i]) || rows[i]->so >= (1LL << 40) || rows[i]->si >= (1LL << 40))
+            return fail(ATTN_EINVAL, "%s: the rows of %s overlap or lie too far apart", who, name);
+        if (rows[i]->so % 16 || rows[i]->si % 16)
+            return fail(ATTN_EINVAL, "%s: the strides of %s must be multiples of 16 bytes", who, name);
+    }
+    Pool pool[2];
+    for (int i = 0; i < 2; ++i) {
+        const char *name = i ? "vpages" : "kpages";
+        if (!make_pool(&pool[i], i ? vpages : kpages, 1, 0, n_pages, H_kv, page_size, D, esz, strides ? strides + 4 + 3 * i : nullptr))
+            return fail(ATTN_EINVAL, "%s: a stride of %s is negative or too large", who, name);
+        for (int x = 1; x < 4; ++x)
+            if (pool[i].st[x] % 16 || pool[i].st[x] >= (1LL << 40))
+                return fail(ATTN_EINVAL, "%s: the strides of %s must be multiples of 16 bytes, below 2^40", who, name);
+        if (overlaps(out, static_cast<size_t>((ro.n_outer - 1) * ro.so + (ro.n_inner - 1) * ro.si + ro.row), pool[i].p,
+                     pool_extent(pool[i])))
+            return fail(ATTN_EINVAL, "%s: out overlaps %s", who, name);
+    }
+    if (rows_overlap(ro, rq)) return fail(ATTN_EINVAL, "%s: out overlaps q", who);
+    const size_t table_bytes = n_pages > 0 ? static_cast<size_t>((n_seq - 1) * (n_seq > 1 ? table_stride : 0) + max_pages) * 4 : 0;
+    const Rows lr = make_rows(lse, T, 1, H, H, H, 4);
+    if (lse && (rows_overlap(lr, rq) || rows_overlap(lr, ro) ||
+                overlaps(lse, static_cast<size_t>(T) * H * 4, pool[0].p, pool_extent(pool[0])) ||
+                overlaps(lse, static_cast<size_t>(T) * H * 4, pool[1].p, pool_extent(pool[1])) ||
+                overlaps(lse, static_cast<size_t>(T) * H * 4, page_table, table_bytes)))
+        return fail(ATTN_EINVAL, "%s: lse overlaps another tensor", who);
+    PagedArgs a{};
+    a.T = T, a.n_seq = n_seq, a.H = H, a.H_kv = H_kv, a.D = D, a.P = page_size, a.n_pages = n_pages;
+    a.max_len = max_pages * page_size;
+    const long long need = paged_sizes(who, a, cu_seqlens != nullptr, dtype);
+    if (need < 0) return static_cast<int>(need);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need || !aligned16(workspace))
+            return fail(ATTN_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes (got %lld)", who, need,
+                        workspace ? workspace_bytes : 0LL);
+        const Rows wr = make_rows(workspace, 1, 1, need, need, need, 1);
+        const size_t nb = static_cast<size_t>(need);
+        if (rows_overlap(wr, rq) || rows_overlap(wr, ro) || (lse && rows_overlap(wr, lr)) ||
+            overlaps(workspace, nb, pool[0].p, pool_extent(pool[0])) || overlaps(workspace, nb, pool[1].p, pool_extent(pool[1])) ||
+            overlaps(workspace, nb, page_table, table_bytes) ||
+            (cu_seqlens && overlaps(workspace, nb, cu_seqlens, (static_cast<size_t>(n_seq) + 1) * 4)) ||
+            (cache_len && overlaps(workspace, nb, cache_len, static_cast<size_t>(n_seq) * 4)))
+            return fail(ATTN_EINVAL, "%s: workspace overlaps a tensor", who);
+    }
+    int *status = nullptr;
+    if ((rc = status_word(&status))) return rc;
+    a.q = q, a.k = kpages, a.v = vpages, a.out = out, a.lse = lse;
+    a.page_table = page_table, a.cu_seqlens = cu_seqlens, a.cache_len = cache_len;
+    a.table_stride = n_seq > 1 ? table_stride : 0;
+    a.q_ts = rq.so / esz, a.q_hs = rq.si / esz, a.o_ts = ro.so / esz, a.o_hs = ro.si / esz;
+    a.k_ps = pool[0].st[1] / esz, a.k_hs = pool[0].st[2] / esz, a.k_rs = pool[0].st[3] / esz;
+    a.v_ps = pool[1].st[1] / esz, a.v_hs = pool[1].st[2] / esz, a.v_rs = pool[1].st[3] / esz;
+    a.scale = scale, a.status = status, a.stream = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (dtype == ATTN_F32) {
+        if (need > 0) {
+            a.part_o = static_cast<float *>(workspace);
+            a.part_ml = a.part_o + need / 4 / (D + 2) * D;
+        }
+        e = launch_paged_f32(a);
+    } else {
+        const long long parts = 2LL * a.grid * a.slot_rows;
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = a.part_o + parts * D;
+        a.merge = reinterpret_cast<int *>(a.part_ml + parts * 2);
+        CUtensorMap tq, tk, tv;
+        if (n_pages == 0)  // no box is copied: any valid view
+            for (int i = 0; i < 2; ++i) make_pool(&pool[i], q, 1, 0, 1, 1, page_size, D, esz, nullptr);
+        if ((rc = make_map_tokens(&tq, rq, D, a.heads, a.box_tokens)) || (rc = make_map_pages(&tk, pool[0], a.box)) ||
+            (rc = make_map_pages(&tv, pool[1], a.box)))
+            return rc;
+        e = launch_paged_tc(a, tq, tk, tv);
+    }
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "attn_fwd_paged launch");
 }
 
 // Shared by attn_rope (no cache) and attn_rope_append.

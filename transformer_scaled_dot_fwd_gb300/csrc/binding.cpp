@@ -36,6 +36,8 @@ decltype(&attn_rope) f_rope;
 decltype(&attn_rope_append) f_rope_append;
 decltype(&attn_decode_tree) f_tree;
 decltype(&attn_decode_tree_workspace) f_tree_workspace;
+decltype(&attn_fwd_paged) f_paged;
+decltype(&attn_fwd_paged_workspace) f_paged_workspace;
 
 bool small(int64_t n) { return n >= 0 && n <= INT_MAX; }
 
@@ -82,6 +84,23 @@ struct Call {
         for (int64_t s : k->sizes())
             if (!small(s)) return false;
         return k->is_contiguous() && v->is_contiguous();
+    }
+
+    // A pair of (n_pages, H_kv, P, D) page pools with contiguous rows; their strides go to st.
+    bool pages(const at::Tensor* k, const at::Tensor* v, int64_t D, long long* st) const {
+        if (!shares(k) || !shares(v) || k->dim() != 4 || k->sizes() != v->sizes() || k->size(3) != D || k->stride(3) != 1 ||
+            v->stride(3) != 1)
+            return false;
+        for (int64_t s : k->sizes())
+            if (!small(s)) return false;
+        for (int i = 0; i < 3; ++i) st[i] = k->stride(i), st[3 + i] = v->stride(i);
+        return true;
+    }
+
+    // A (rows, entries) int32 table with contiguous rows.
+    bool table(const at::Tensor* t) const {
+        return t && t->scalar_type() == at::kInt && t->device() == device && t->dim() == 2 && t->stride(1) == 1 &&
+               small(t->size(0)) && small(t->size(1));
     }
 
     // An int32 tensor of the given shape, or None.
@@ -357,6 +376,57 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A given (T, H) log-sum-exp, one made here, or none.
+bool lse_of(PyObject* o, bool want, const Call& c, int64_t T, int64_t H, Out* lse) {
+    if (o != Py_None) {
+        lse->given = o;
+        lse->t = cuda_tensor(o);
+        return lse->t && lse->t->scalar_type() == at::kFloat && lse->t->sizes() == at::IntArrayRef({T, H}) &&
+               lse->t->is_contiguous() && lse->t->device() == c.device;
+    }
+    if (want) {
+        lse->made = c.make({T, H}, at::kFloat);
+        lse->t = &lse->made;
+    }
+    return true;
+}
+
+// paged(q, kpages, vpages, page_table, cache_len, cu_seqlens, out, lse, scale, return_lse)
+PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor *q, *kp, *vp, *table;
+    Call c;
+    long long st[10];
+    if (n != 10 || !(q = cuda_tensor(a[0])) || !c.of(q, 3) || !(kp = cuda_tensor(a[1])) || !(vp = cuda_tensor(a[2])) ||
+        !(table = cuda_tensor(a[3])))
+        Py_RETURN_NONE;
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
+    st[0] = q->stride(0), st[1] = q->stride(1);
+    if (!c.pages(kp, vp, D, st + 4) || !c.table(table)) Py_RETURN_NONE;
+    const int64_t n_pages = kp->size(0), H_kv = kp->size(1), P = kp->size(2), n_seq = table->size(0), M = table->size(1);
+    const int *cu, *cache_len;
+    float scale;
+    int want_lse;
+    if (H_kv < 1 || H % H_kv || D < 1 || !c.ints(a[4], {n_seq}, &cache_len) || !c.ints(a[5], {n_seq + 1}, &cu) ||
+        (!cu && (n_seq == 0 || T % n_seq)) || !number(a[8], 1.0 / std::sqrt(static_cast<double>(D)), &scale) ||
+        !flag(a[9], &want_lse))
+        Py_RETURN_NONE;
+    const long long need = f_paged_workspace(T, n_seq, H, H_kv, D, M, P, cu != nullptr, c.code);
+    if (need < 0) Py_RETURN_NONE;
+    Out lse, out;
+    if (!out.rows(a[6], c, T, H, D, st + 2) || !lse_of(a[7], want_lse, c, T, H, &lse)) Py_RETURN_NONE;
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.device.index());
+    Workspace ws(need, stream);
+    const int rc = unlocked([&] {
+        return f_paged(q->data_ptr(), kp->data_ptr(), vp->data_ptr(), out.ptr(), static_cast<float*>(lse.ptr()), T, H, H_kv, D,
+                       st, n_pages, P, static_cast<const int*>(table->data_ptr()), M, table->stride(0), cu, cache_len, n_seq,
+                       scale, c.code, ws.p, need, stream);
+    });
+    if (rc) Py_RETURN_NONE;
+    return lse.t ? pair(out.object(), lse.object()) : out.object();
+    END_HANDLE_TH_ERRORS
+}
+
 // bind(packed, packed_workspace, rope, rope_append, tree, tree_workspace): their addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* p[6];
@@ -378,6 +448,23 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// bind_paged(paged, paged_workspace)
+PyObject* bind_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    void* p[2];
+    if (n != 2) {
+        PyErr_SetString(PyExc_TypeError, "bind_paged takes two addresses");
+        return nullptr;
+    }
+    for (int i = 0; i < 2; ++i)
+        if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_paged: a null address");
+            return nullptr;
+        }
+    f_paged = reinterpret_cast<decltype(f_paged)>(p[0]);
+    f_paged_workspace = reinterpret_cast<decltype(f_paged_workspace)>(p[1]);
+    Py_RETURN_NONE;
+}
+
 template <class F>
 PyCFunction fast(F f) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -389,6 +476,8 @@ PyMethodDef kMethods[] = {
     {"rope", fast(rope), METH_FASTCALL, nullptr},
     {"rope_append", fast(rope_append), METH_FASTCALL, nullptr},
     {"tree", fast(tree), METH_FASTCALL, nullptr},
+    {"bind_paged", fast(bind_paged), METH_FASTCALL, nullptr},
+    {"paged", fast(paged), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -112,6 +112,47 @@ cudaError_t launch_tree_zero(const TreeArgs &a);  // bf16, Skv = 0
 cudaError_t launch_tree_f32(const TreeArgs &a);
 cudaError_t launch_tree_merge_f32(const TreeArgs &a);
 
+// New tokens over a paged KV cache (attn_fwd_paged).  Sequence s is tokens [cu_seqlens[s],
+// cu_seqlens[s + 1]) of q and out, the last of its cache_len[s] keys, which lie in pages
+// of P rows named by row s of the page table.
+struct PagedArgs {
+    const void *q;              // (T, H, D) rows, element strides below
+    const void *k, *v;          // pages: (n_pages, H_kv, P, D), element strides below
+    void *out;                  // (T, H, D) rows
+    float *lse;                 // (T, H) or nullptr
+    const int32_t *page_table;  // device, rows table_stride apart
+    const int32_t *cu_seqlens;  // device int32[n_seq + 1], or nullptr: per_seq tokens each
+    const int32_t *cache_len;   // device int32[n_seq], or nullptr (max_len)
+    long long q_ts, q_hs, o_ts, o_hs, k_ps, k_hs, k_rs, v_ps, v_hs, v_rs, table_stride;
+    int T, n_seq, per_seq, H, H_kv, D, P, n_pages;
+    int max_len;                // keys that a row of the page table holds
+    float scale;
+    // bf16: row tiles of `tokens` tokens by `heads` heads of one of `groups` groups of
+    // the query heads of a cached head; boxes of `box` rows of a page, box_tokens tokens of q
+    int heads, groups, tokens, box, box_tokens;
+    int single;                 // every unit has one row tile
+    int grid;                   // CTAs at most
+    int n_split;                // fp32: splits of the keys
+    // Partial results: O unnormalised [D] and (running max in log2 units, sum) of
+    // bf16: two slots per CTA of slot_rows rows, O as [slot][D / 4][row][4]
+    // fp32: row (((block of 32 rows) * H_kv + cached head) * 32 + r) * n_split + split
+    float *part_o, *part_ml;
+    int slot_rows;
+    int *merge;                 // bf16: 8 ints per CTA, the unit it shares with later CTAs
+    int *status;
+    cudaStream_t stream;
+    int n_sm;
+};
+// bf16 tcgen05 kernel and its merge; tq views q as (D, H, T) with 64 x heads x box_tokens
+// boxes, tk and tv the pages as (D, P, H_kv, n_pages) with 64 x box x 1 x 1 boxes.
+cudaError_t launch_paged_tc(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv);
+double paged_tc_axis(const PagedArgs &a);
+cudaError_t launch_paged_f32(const PagedArgs &a);
+// fp32: blocks of 32 rows of a cached head, and splits of the keys (1, 2, 4 or 8: CTAs of
+// a cluster; more: merged through the workspace).
+long long paged_f32_blocks(const PagedArgs &a);
+int paged_f32_splits(const PagedArgs &a);
+
 struct DecodeArgs {
     const void *q;          // (B, H, D) bf16 (fp32 for launch_decode_f32)
     const void *k, *v;      // (B, H_kv, Skv, D), same dtype

@@ -1,0 +1,883 @@
+// Attention of new tokens over a paged KV cache on the sm_103a tensor cores
+// (attn_fwd_paged, bf16).
+//
+// Sequence s holds L tokens in pages of P rows, named by its row of the page table;
+// the last n of them are new and have queries.  Token i of those sees the keys j <= L - n + i:
+//     out_i = softmax over visible j of (scale q_i . k_j) times v_j.
+// One form serves chunks of prompts, single tokens, and both in one call.
+//
+// Rows and units.  The G = H / H_kv query heads of a cached head and kTok = 128 / G
+// tokens are the rows of a 128-row tile, token by token (row r: token r / G, head
+// r % G), as one TMA box of (64 columns, G heads, kTok tokens) leaves them; groups of
+// more than 128 heads are cut.  A unit is a cached head of a sequence with two row tiles
+// (one, where the sequence has no more tokens).  It reads every key once for up to 256
+// rows; on the diagonal it wastes 2 kTok keys at most, as heads, not tokens, fill the tile.
+//
+// Work split.  All units lie end to end on an axis of keys: unit u of a sequence takes
+// max(L - n, 0) + 127 + (u + 1) 2 kTok keys and kUnitCost tiles for its start and end, so
+// that the place of a unit is a quadratic in u and no list is needed.  CTA i of N takes
+// the tiles that begin in the i-th equal part of the axis: no tail whatever the lengths
+// are, and at most two units a CTA are shared with neighbours.  Those leave unnormalised
+// O, running max and sum in fp32 in the CTA's slots of the workspace, for a merge in
+// the order of the keys; whole units are written out directly.
+//
+// Pages.  A 128-key tile is copied by boxes that lie in one page each (rows: the largest
+// power of two up to 128 that divides P), each lane of the loading warp with its own box
+// and its own entry of the table, fetched a tile ahead.  Boxes past the last visible key are not
+// copied; an entry that is no page reads as zeros (TMA's fill).
+//
+// Two softmax warpgroups (streams) keep two S and two O accumulators in TMEM busy.  A
+// unit with two row tiles gives each stream one of them, and both read the same K/V
+// tiles.  A unit with one gives the streams alternate K/V tiles; they join at its end:
+//     two tiles:  S0_0 S1_0 | PV0_j S0_{j+1} PV1_j S1_{j+1} | ...
+//     one tile:   S0_0 S1_1 | PV_j S_{j+2} (stream j & 1)   | ...
+//
+// A weight of zero does not hide an infinite or NaN value from the second product
+// (0 * inf), and a page's rows past the sequence's end hold whatever they were left with,
+// so two guard warps pass over the V of the tiles that some row sees a part of (edge
+// tiles): rows past the unit's last key become zeros, non-finite elements become zeros
+// which the epilogue adds back to the rows that see them.
+//
+// Roles (12 warps): warp 0 walks the CTA's run and loads Q, K_j, V_j, warp 1 allocates
+// TMEM and issues the MMAs, warps 2-3 guard, warps 4-7 and 8-11 are the streams (thread =
+// row = TMEM lane); a warp none of whose rows sees a key only keeps step.
+#include "kernels.h"
+#include "ptx.cuh"
+#include "serving.cuh"
+
+#include <climits>
+
+namespace attn {
+namespace {
+
+constexpr int kN = 128;          // keys per K/V tile
+constexpr int kM = 128;          // rows per tile
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsOther = 64;     // warps 0-3 after setmaxnreg
+constexpr uint32_t kRegsSoftmax = 216;  // warps 4-11: 128 * 64 + 256 * 216 <= 384 * 168
+constexpr int kTmemCols = 512;   // S0 0, S1 128, O0 256, O1 256 + D
+constexpr int kRing = 4;         // unit runs in flight between the roles
+constexpr int kRingReaders = 32 + 256;
+constexpr int kGuardRing = 16;   // an edge tile holds a K/V stage: fewer than 16 at once
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kHugeLog2 = 16777216.0f;  // 2^24
+#ifndef ATTN_PAGED_MIN_TILES
+#define ATTN_PAGED_MIN_TILES 2
+#endif
+#ifndef ATTN_PAGED_UNIT_COST
+#define ATTN_PAGED_UNIT_COST 5
+#endif
+constexpr int kUnitCost = ATTN_PAGED_UNIT_COST;  // what a unit costs beside its tiles, in tiles
+constexpr int kMinTiles = ATTN_PAGED_MIN_TILES;  // fewest tiles' worth of keys a CTA takes
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+
+// One sequence: first token, new tokens, keys.
+struct Seq {
+    int c0, n, L;
+};
+
+__device__ __forceinline__ Seq seq_of(const PagedArgs &a, int s) {
+    Seq q;
+    int c1;
+    if (a.cu_seqlens) {
+        q.c0 = min(max(a.cu_seqlens[s], 0), a.T);
+        c1 = min(max(a.cu_seqlens[s + 1], q.c0), a.T);
+    } else {
+        q.c0 = s * a.per_seq;
+        c1 = q.c0 + a.per_seq;
+    }
+    q.n = c1 - q.c0;
+    q.L = a.cache_len ? min(max(a.cache_len[s], 0), a.max_len) : a.max_len;
+    return q;
+}
+
+// The units of one cached head (and group of heads) of a sequence on the axis of keys:
+// unit u of nu takes keys [at(u), at(u + 1)).
+struct Units {
+    int nu, step;  // units, tokens of a unit
+    long long base;
+    __device__ __forceinline__ Units(const Seq &q, int tokens) {
+        nu = (q.n + tokens - 1) / tokens;
+        step = min(tokens, q.n);
+        base = max(q.L - q.n, 0) + kN - 1 + kUnitCost * kN;
+    }
+    __device__ __forceinline__ long long at(int u) const {
+        return u * base + static_cast<long long>(u) * (u + 1) / 2 * step;
+    }
+};
+
+// A run of K/V tiles [j0, j0 + n) of one unit.
+struct Run {
+    int seq, hs;    // sequence, cached head * groups of heads + group
+    int tok0, left; // first token of the unit in the sequence, tokens from there on
+    int j0, n;      // n < 0: no more work
+    int slot;       // workspace slot, -1: the whole unit, written out
+    int keys;       // keys that the unit's last row sees
+    int past;       // keys in front of the sequence's first new token (may be negative)
+    int c0;         // first token of the sequence
+};
+
+struct GuardReq {
+    int stage;   // K/V stage of an edge tile, kEnd: no more work
+    int parity;  // of the stage's kv_full
+    int rows;    // rows of the tile that the unit sees
+    int run;     // ring slot
+};
+constexpr int kEnd = -1;
+
+// Single: every unit has one row tile; its second Q buffer is one more K/V stage.
+template <int D, bool Single>
+struct Layout {
+    static constexpr int kSub = D / 64;
+    static constexpr int kBlock = 128 * 128;        // 128 rows x 128 bytes
+    static constexpr int kTile = kSub * kBlock;
+    static constexpr int kQTiles = Single ? 1 : 2;
+    static constexpr int kStages = D == 128 ? (Single ? 5 : 4) : 8;
+    static constexpr int kRingOff = kQTiles * kTile;
+    static constexpr int kExOff = kRingOff + kStages * kTile;
+    static constexpr int kBarOff = kExOff + 256 * 8;
+    static constexpr int kSmemBytes = kBarOff + 1024 + 1024;
+};
+
+struct Bars {
+    uint64_t q_full;            // Q of run k staged: phase k
+    uint64_t q_free;            // a run's last S MMA is complete
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t s_full[2], p_ready[2], o_full[2];
+    uint64_t run_full[kRing], run_empty[kRing];
+    uint64_t guard_full[kGuardRing], guard_clean[kGuardRing];
+    uint64_t join;              // both streams (a barrier with a limit)
+    uint64_t mma_done;
+    Run run[kRing];
+    GuardReq req[kGuardRing];
+    int spoiled[kRing];
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+__device__ __forceinline__ Run read_run(Bars &bars, int slot) {
+    const volatile Run &s = bars.run[slot];
+    return Run{s.seq, s.hs, s.tok0, s.left, s.j0, s.n, s.slot, s.keys, s.past, s.c0};
+}
+__device__ __forceinline__ bool take_run(Bars &bars, int k, Run *r) {
+    if (!mbar_wait_warp(&bars.run_full[k % kRing], (k / kRing) & 1, &bars.abort)) return false;
+    *r = read_run(bars, k % kRing);
+    return true;
+}
+
+// First edge tile of a run, relative to j0: a tile that some row sees only a part of.
+__device__ __forceinline__ int edge_of(const Run &r) { return min(r.n, max(0, max(0, r.past + r.tok0 + 1) / kN - r.j0)); }
+__device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kN - 1) / kN); }
+
+// Row r of row tile x of a run: its token in the sequence, its query head, whether it
+// exists, and the keys [0, lim) it sees.
+struct Row {
+    int token, head, lim;
+    bool valid;
+};
+__device__ __forceinline__ Row row_of(const PagedArgs &a, int hs, int tok0, int left, int past, int x, int r) {
+    const int t = r / a.heads, g = r - t * a.heads + (hs % a.groups) * a.heads, i = x * a.tokens + t, G = a.H / a.H_kv;
+    Row w;
+    w.valid = t < a.tokens && i < left && g < G;
+    w.token = tok0 + i;
+    w.head = hs / a.groups * G + g;
+    w.lim = w.valid ? max(0, past + w.token + 1) : 0;
+    return w;
+}
+
+template <int D, bool Single>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv) {
+    using L = Layout<D, Single>;
+    constexpr int kStages = L::kStages;
+    extern __shared__ __align__(1024) uint8_t dsmem[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = smem + L::kRingOff;
+    float2 *ex = reinterpret_cast<float2 *>(smem + L::kExOff);  // [stream][row] max, sum
+    Bars &bars = *reinterpret_cast<Bars *>(smem + L::kBarOff);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.q_free, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars.kv_full[s], 1);
+            mbar_init(&bars.kv_empty[s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bars.s_full[x], 1);
+            mbar_init(&bars.p_ready[x], kM);
+            mbar_init(&bars.o_full[x], 1);
+        }
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&bars.run_full[s], 1);
+            mbar_init(&bars.run_empty[s], kRingReaders);
+        }
+        for (int s = 0; s < kGuardRing; ++s) {
+            mbar_init(&bars.guard_full[s], 1);
+            mbar_init(&bars.guard_clean[s], 2);  // guard warps
+        }
+        mbar_init(&bars.join, 256);
+        mbar_init(&bars.mma_done, 1);
+        bars.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp == 0) {
+        // ================================================================ walk and TMA loads
+        regs_dec<kRegsOther>();
+        const int per = a.H_kv * a.groups;  // heads, or groups of them, of a sequence
+        const int tokens = (Single ? 1 : 2) * a.tokens;  // of a unit
+        auto cost_of = [&](const Seq &q) {
+            const Units u(q, tokens);
+            return u.at(u.nu) * per;
+        };
+        long long total = 0;  // keys on the axis (the host has checked that they fit)
+        Seq mine{0, 0, 0};    // sequence b0 + lane
+        for (int b0 = lane; b0 < a.n_seq; b0 += 32) {
+            mine = seq_of(a, b0);
+            total += cost_of(mine);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        const long long most = total / (kN * kMinTiles);
+        const int N = static_cast<int>(min(max(most, 1ll), static_cast<long long>(gridDim.x))), I = blockIdx.x;
+        const bool idle = I >= N || total == 0;
+        const long long lo = idle ? 0 : total * I / N, hi = idle ? 0 : total * (I + 1) / N;
+        // sequence that holds position lo, and the first position of its units
+        int b = 0;
+        long long base = 0;
+        for (int b0 = 0; !idle && b0 < a.n_seq; b0 += 32) {
+            if (a.n_seq > 32) mine = seq_of(a, min(b0 + lane, a.n_seq - 1));
+            const long long t = b0 + lane < a.n_seq ? cost_of(mine) : 0;
+            long long sum = t;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, base + sum > lo);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                b = b0 + f;
+                base += __shfl_sync(0xffffffffu, sum - t, f);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        Seq q{__shfl_sync(0xffffffffu, mine.c0, b % 32), __shfl_sync(0xffffffffu, mine.n, b % 32),
+              __shfl_sync(0xffffffffu, mine.L, b % 32)};
+        Units units(q, tokens);
+        int hs = 0, u = 0, j = 0;
+        long long pos = base;  // first key of unit u of hs
+        auto keys_of = [&](int unit) { return max(0, min(q.L, q.L - q.n + min((unit + 1) * tokens, q.n))); };
+        auto next_unit = [&] {
+            pos += units.at(u + 1) - units.at(u);
+            j = 0;
+            if (++u < units.nu) return;
+            u = 0;
+            if (++hs < per) return;
+            hs = 0;
+            while (++b < a.n_seq) {
+                q = seq_of(a, b);
+                if (q.n > 0) {
+                    units = Units(q, tokens);
+                    break;
+                }
+            }
+        };
+        if (!idle) {
+            const long long one = units.at(units.nu), rem = lo - base;
+            hs = static_cast<int>(rem / one);
+            pos += hs * one;
+            int top = units.nu;  // at(u) <= lo - pos < at(top)
+            while (top - u > 1) {
+                const int mid = (u + top) / 2;
+                if (units.at(mid) <= lo - pos)
+                    u = mid;
+                else
+                    top = mid;
+            }
+            pos += units.at(u);
+            const long long j_ll = (lo - pos + kN - 1) / kN;
+            if (j_ll >= tiles_of(keys_of(u)))
+                next_unit();
+            else
+                j = static_cast<int>(j_ll);
+        }
+        // this lane's box of a tile: rows [i box, (i + 1) box) of the columns from 64 c on
+        const int boxes = kN / a.box, i = lane % boxes, c = lane / boxes;
+        const bool carries = lane < boxes * L::kSub;
+        int issued = 0, requests = 0, k = 0, q_loads = 0;
+        bool ok = true;
+        int4 rec = make_int4(-1, 0, 0, 0), rec2 = make_int4(0, 0, 0, 0);
+        while (ok) {
+            const int slot = k % kRing;
+            if (k >= kRing && !(ok = mbar_wait_warp(&bars.run_empty[slot], ((k / kRing) - 1) & 1, &bars.abort))) break;
+            Run r{0, 0, 0, 0, 0, -1, 0, 0, 0, 0};
+            int nt = 0;
+            if (!idle && b < a.n_seq && pos + static_cast<long long>(j) * kN < hi) {
+                r.seq = b;
+                r.hs = hs;
+                r.tok0 = u * tokens;
+                r.left = q.n - r.tok0;
+                r.keys = keys_of(u);
+                r.past = q.L - q.n;
+                r.c0 = q.c0;
+                r.j0 = j;
+                nt = tiles_of(r.keys);
+                const long long room = (hi - pos + kN - 1) / kN - j;  // tiles that begin before hi
+                r.n = static_cast<int>(min(static_cast<long long>(nt - j), room));
+                r.slot = r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
+                if (j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w
+                    const long long last = pos + static_cast<long long>(nt - 1) * kN;
+                    rec = make_int4(b, hs, r.tok0, static_cast<int>(((last + 1) * N - 1) / total));
+                    rec2 = make_int4(r.left, r.past, r.c0, 0);
+                }
+            }
+            if (lane == 0) {
+                volatile Run &w = bars.run[slot];
+                w.seq = r.seq, w.hs = r.hs, w.tok0 = r.tok0, w.left = r.left, w.j0 = r.j0, w.n = r.n, w.slot = r.slot;
+                w.keys = r.keys, w.past = r.past, w.c0 = r.c0;
+                *static_cast<volatile int *>(&bars.spoiled[slot]) = 0;
+                mbar_arrive(&bars.run_full[slot]);
+            }
+            __syncwarp();
+            if (r.n < 0) break;
+            const int edge = edge_of(r), head = r.hs / a.groups;
+            const int32_t *table = a.page_table + static_cast<long long>(r.seq) * a.table_stride;
+            // this lane's page of tile jj
+            auto page_of = [&](int jj) {
+                const int row = (r.j0 + jj) * kN + i * a.box;
+                return jj < r.n && carries && row < r.keys ? table[row / a.P] : 0;
+            };
+            auto load = [&](int jj, int kv, int page) {
+                if (!ok || jj >= r.n) return;
+                const int s = issued % kStages;
+                if (issued >= kStages &&
+                    !(ok = mbar_wait_warp(&bars.kv_empty[s], ((issued / kStages) - 1) & 1, &bars.abort)))
+                    return;
+                const int key0 = (r.j0 + jj) * kN;
+                const int some = min(boxes, max(0, (r.keys - key0 + a.box - 1) / a.box));  // boxes with a visible key
+                if (lane == 0) {
+                    if (some > 0)
+                        mbar_arrive_expect_tx(&bars.kv_full[s], static_cast<uint32_t>(some * a.box * D * 2));
+                    else
+                        mbar_arrive(&bars.kv_full[s]);
+                }
+                __syncwarp();
+                if (carries && i < some)
+                    tma_load_4d(ring + s * L::kTile + c * L::kBlock + i * a.box * 128, kv ? &tv : &tk, &bars.kv_full[s],
+                                c * 64, (key0 + i * a.box) % a.P, head, page);
+                if (kv && jj >= edge && lane == 0) {
+                    volatile GuardReq &g = bars.req[requests % kGuardRing];
+                    g.stage = s, g.parity = (issued / kStages) & 1, g.rows = r.keys - key0, g.run = slot;
+                    mbar_arrive(&bars.guard_full[requests % kGuardRing]);
+                }
+                if (kv && jj >= edge) ++requests;
+                ++issued;
+            };
+            auto load_q = [&](int tiles) {  // once the last run's last S MMA has read the buffers
+                if (!ok || (k > 0 && !(ok = mbar_wait_warp(&bars.q_free, (k - 1) & 1, &bars.abort)))) return;
+                if (lane == 0) {
+                    const int h0 = head * (a.H / a.H_kv) + r.hs % a.groups * a.heads;
+                    mbar_arrive_expect_tx(&bars.q_full, static_cast<uint32_t>(tiles * a.box_tokens * a.heads * D * 2));
+                    for (int x = 0; x < tiles; ++x)
+#pragma unroll
+                        for (int cc = 0; cc < L::kSub; ++cc)
+                            tma_load_3d(smem + x * L::kTile + cc * L::kBlock, &tq, &bars.q_full, cc * 64, h0,
+                                        r.c0 + r.tok0 + x * a.tokens);
+                }
+                __syncwarp();
+                ++q_loads;
+            };
+            int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2), p3;  // of tiles jj, jj + 1, ...
+            if (Single || r.left <= a.tokens) {  // one row tile: K0 K1 | V0 K2 | V1 K3 | ...
+                if (k == 0) load_q(1);
+                load(0, 0, p0);
+                load(1, 0, p1);
+                if (k > 0) load_q(1);
+                for (int jj = 0; jj < r.n && ok; ++jj) {
+                    p3 = page_of(jj + 3);
+                    load(jj, 1, p0);
+                    load(jj + 2, 0, p2);
+                    p0 = p1, p1 = p2, p2 = p3;
+                }
+            } else {
+                if (k == 0) load_q(2);
+                load(0, 0, p0);
+                if (k > 0) load_q(2);
+                for (int jj = 0; jj < r.n && ok; ++jj) {
+                    p3 = page_of(jj + 3);
+                    load(jj, 1, p0);
+                    load(jj + 1, 0, p1);
+                    p0 = p1, p1 = p2, p2 = p3;
+                }
+            }
+            ++k;
+            j += r.n;
+            if (j == nt) next_unit();
+        }
+        if (lane == 0) {
+            if (ok) {  // no more work for the guard
+                *static_cast<volatile int *>(&bars.req[requests % kGuardRing].stage) = kEnd;
+                mbar_arrive(&bars.guard_full[requests % kGuardRing]);
+            }
+            int4 *out = reinterpret_cast<int4 *>(a.merge) + 2 * blockIdx.x;
+            out[0] = rec;
+            out[1] = rec2;
+            // never leave with copies still landing in shared memory
+            volatile int never = 0;
+            if (q_loads > 0) mbar_wait(&bars.q_full, (q_loads - 1) & 1, &never);
+            for (int x = max(0, issued - kStages); x < issued; ++x)
+                mbar_wait(&bars.kv_full[x % kStages], (x / kStages) & 1, &never);
+        }
+    } else if (warp == 1) {
+        // ================================================================ MMA issuer
+        regs_dec<kRegsOther>();
+        const uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0);
+        const uint32_t idesc_o = idesc_bf16_f32(kM, D, 1);
+        const uint64_t dq0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t dk0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+        const uint64_t dv0 = sdesc_sw128(smem_u32(ring), L::kBlock, 1024);
+        auto issue_s = [&](int x, int qbuf, int slot) {  // S_x = Q_qbuf K^T
+            const uint64_t da = desc_add(dq0, (qbuf * L::kTile) >> 4), db = desc_add(dk0, (slot * L::kTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk / 4) * L::kBlock + (kk % 4) * 32) >> 4;
+                mma_ss_warp(tmem + x * 128u, desc_add(da, off), desc_add(db, off), idesc_s, kk > 0);
+            }
+        };
+        auto issue_pv = [&](int x, int slot, bool acc) {  // O_x (+)= P_x V
+            const uint64_t db = desc_add(dv0, (slot * L::kTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kN / 16; ++kk)
+                mma_ts_warp(tmem + 256u + x * static_cast<uint32_t>(D), tmem + x * 128u + kk * 8,
+                            desc_add(db, (kk * 16 * 128) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
+        };
+        int consumed = 0, cleaned = 0;
+        uint32_t pr[2] = {0, 0};
+        bool ok = true;
+        auto next_stage = [&](int *slot) {  // wait for the next ring stage
+            *slot = consumed % kStages;
+            if (!(ok = mbar_wait_warp(&bars.kv_full[*slot], (consumed / kStages) & 1, &bars.abort))) return;
+            ++consumed;
+        };
+        auto guarded = [&](bool edge) {
+            if (!edge) return;
+            if ((ok = mbar_wait_warp(&bars.guard_clean[cleaned % kGuardRing], (cleaned / kGuardRing) & 1, &bars.abort)))
+                ++cleaned;
+        };
+        for (int k = 0; ok; ++k) {
+            Run r;
+            if (!(ok = take_run(bars, k, &r))) break;
+            mbar_arrive(&bars.run_empty[k % kRing]);
+            const int n = __shfl_sync(0xffffffffu, r.n, 0);
+            if (n < 0) break;
+            const int edge = __shfl_sync(0xffffffffu, edge_of(r), 0);
+            const bool one = Single || __shfl_sync(0xffffffffu, r.left, 0) <= a.tokens;
+            if (!(ok = mbar_wait_warp(&bars.q_full, k & 1, &bars.abort))) break;
+            int ks = 0, vs = 0;
+            if (one) {
+                // stream x = tile & 1, both on Q buffer 0
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x >= n) break;
+                    next_stage(&ks);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(x, 0, ks);
+                    tc_commit_warp(&bars.s_full[x]);
+                    tc_commit_warp(&bars.kv_empty[ks]);
+                    if (x + 1 == n) tc_commit_warp(&bars.q_free);
+                }
+                auto step = [&](int j, int x) {
+                    next_stage(&vs);
+                    if (ok) guarded(j >= edge);
+                    if (!ok || !(ok = mbar_wait_warp(&bars.p_ready[x], pr[x], &bars.abort))) return;
+                    pr[x] ^= 1;
+                    tc_fence_after();
+                    issue_pv(x, vs, j >= 2);
+                    if (j + 2 >= n) tc_commit_warp(&bars.o_full[x]);
+                    tc_commit_warp(&bars.kv_empty[vs]);
+                    if (j + 2 < n) {
+                        next_stage(&ks);
+                        if (!ok) return;
+                        tc_fence_after();
+                        issue_s(x, 0, ks);
+                        tc_commit_warp(&bars.s_full[x]);
+                        tc_commit_warp(&bars.kv_empty[ks]);
+                        if (j + 3 == n) tc_commit_warp(&bars.q_free);  // the last S of the run
+                    }
+                };
+                for (int j = 0; j < n && ok; j += 2) {
+                    step(j, 0);
+                    if (ok && j + 1 < n) step(j + 1, 1);
+                }
+            } else {
+                next_stage(&ks);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(0, 0, ks);
+                tc_commit_warp(&bars.s_full[0]);
+                issue_s(1, L::kQTiles - 1, ks);
+                tc_commit_warp(&bars.s_full[1]);
+                tc_commit_warp(&bars.kv_empty[ks]);
+                if (n == 1) tc_commit_warp(&bars.q_free);
+                for (int j = 0; j < n && ok; ++j) {
+                    next_stage(&vs);
+                    if (ok) guarded(j >= edge);
+                    if (!ok || !(ok = mbar_wait_warp(&bars.p_ready[0], pr[0], &bars.abort))) break;
+                    pr[0] ^= 1;
+                    tc_fence_after();
+                    issue_pv(0, vs, j > 0);
+                    const bool next = j + 1 < n;
+                    if (!next) tc_commit_warp(&bars.o_full[0]);
+                    if (next) {
+                        next_stage(&ks);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(0, 0, ks);
+                        tc_commit_warp(&bars.s_full[0]);
+                    }
+                    if (!(ok = mbar_wait_warp(&bars.p_ready[1], pr[1], &bars.abort))) break;
+                    pr[1] ^= 1;
+                    tc_fence_after();
+                    issue_pv(1, vs, j > 0);
+                    if (!next) tc_commit_warp(&bars.o_full[1]);
+                    tc_commit_warp(&bars.kv_empty[vs]);
+                    if (next) {
+                        issue_s(1, L::kQTiles - 1, ks);
+                        tc_commit_warp(&bars.s_full[1]);
+                        tc_commit_warp(&bars.kv_empty[ks]);
+                        if (j + 2 == n) tc_commit_warp(&bars.q_free);
+                    }
+                }
+            }
+        }
+        // every MMA must have finished before TMEM is released
+        tc_commit_warp(&bars.mma_done);
+        volatile int never = 0;
+        mbar_wait_warp(&bars.mma_done, 0, &never);
+    } else if (warp < 4) {
+        // ================================================================ guard of the edge V tiles
+        regs_dec<kRegsOther>();
+        const int tid = threadIdx.x - 64;
+        for (int q = 0;; ++q) {
+            const int slot = q % kGuardRing;
+            // a request comes after its load was issued, and its stage is not reused
+            // before guard_clean: kv_full cannot be a phase off
+            if (!mbar_wait_warp<64>(&bars.guard_full[slot], (q / kGuardRing) & 1, &bars.abort)) break;
+            const volatile GuardReq &rq = bars.req[slot];
+            const int stage = rq.stage, parity = rq.parity, inside = rq.rows, run = rq.run;
+            if (stage < 0) break;
+            if (!mbar_wait_warp(&bars.kv_full[stage], parity, &bars.abort)) break;
+            const uint32_t tile = smem_u32(ring + stage * L::kTile);
+            const bool bad = clean_v_tile<L::kSub, kN, 64>(tile, inside, tid);
+            if (bad) *static_cast<volatile int *>(&bars.spoiled[run]) = 1;
+            if (inside < kN || __any_sync(0xffffffffu, bad)) fence_proxy_async_shared();  // written: the MMA must see it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.guard_clean[slot]);
+        }
+    } else {
+        // ================================================================ softmax streams
+        regs_inc<kRegsSoftmax>();
+        const int x = (warp - 4) / 4;
+        const int quarter = warp % 4;  // TMEM lanes [32 * quarter, 32 * quarter + 32)
+        const int row = quarter * 32 + lane;
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t t_s = t_lane + x * 128u, t_o = t_lane + 256u + x * static_cast<uint32_t>(D);
+        const float sl2 = a.scale * kLog2e;
+        uint32_t sp = 0, o_uses[2] = {0, 0};
+        bool ok = true;
+        uint32_t joins = 0;
+        auto join = [&] {  // waits for all threads of both streams, or for the abort flag
+            mbar_arrive(&bars.join);
+            ok = mbar_wait_warp(&bars.join, joins & 1, &bars.abort) && ok;
+            ++joins;
+        };
+        for (int k = 0; ok; ++k) {
+            bool one;
+            int n, lim;  // tiles of this stream; this row sees columns [0, lim) from the run's first key on
+            {
+                Run r;
+                if (!(ok = take_run(bars, k, &r))) break;
+                if (r.n < 0) break;
+                one = Single || r.left <= a.tokens;
+                n = one ? (r.n - x + 1) / 2 : r.n;
+                lim = row_of(a, r.hs, r.tok0, r.left, r.past, one ? 0 : x, row).lim;
+                if (!__any_sync(0xffffffffu, lim > 0))
+                    lim = INT_MIN;  // the whole warp only keeps step
+                else
+                    lim -= r.j0 * kN;
+            }
+            float m_run = -INFINITY, l = 0.f;
+            bool huge = sl2 == 0.f;  // some row of the warp is
+            for (int i = 0; i < n; ++i) {
+                const int j = one ? 2 * i + x : i;
+                if (!(ok = mbar_wait_warp<32>(&bars.s_full[x], sp, &bars.abort))) break;
+                sp ^= 1;
+                if (lim == INT_MIN) {
+                    mbar_arrive(&bars.p_ready[x]);
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) reg_fence32(s + c * 32);
+                const int t = lim - j * kN;  // this row sees columns [0, t)
+                const bool masked = __any_sync(0xffffffffu, t < kN);
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < kN; ++e)
+                        if (e >= t) s[e] = f2u(-INFINITY);
+                }
+                float m8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m8[e] = fmaxf(u2f(s[2 * e]), u2f(s[2 * e + 1]));
+#pragma unroll
+                for (int c = 16; c < 128; c += 2) m8[(c / 2) % 8] = fmax3(m8[(c / 2) % 8], u2f(s[c]), u2f(s[c + 1]));
+                const float raw = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+                const float m_new = fmaxf(m_run, raw == -INFINITY ? -INFINITY : raw * sl2);
+                const bool grow = m_new > m_run + kRescaleLog2;
+                float mul = sl2;
+                if (__any_sync(0xffffffffu, grow || huge)) {
+                    const float factor = grow ? ex2_approx(m_run - m_new) : 1.f;
+                    if (grow) {
+                        l *= factor;
+                        m_run = m_new;
+                    }
+                    // huge scores: round the product before the difference (as in prefill_tc.cu); a
+                    // scale of 0: a hidden key's -inf must not become NaN.  A row without them
+                    // has its product there and here a factor of 1: another row's scores do not
+                    // change its bits.
+                    const bool mine = sl2 == 0.f || (fabsf(m_run) > kHugeLog2 && m_run != -INFINITY);
+                    huge = __any_sync(0xffffffffu, mine);
+                    if (huge) {
+                        const float first = mine ? sl2 : 1.f;
+#pragma unroll
+                        for (int e = 0; e < kN; ++e) s[e] = e < t ? f2u(__fmul_rn(u2f(s[e]), first)) : f2u(-INFINITY);
+                        mul = mine ? 1.f : sl2;
+                    }
+                    if (i > 0 && __any_sync(0xffffffffu, grow)) {  // this stream's earlier P V are complete: S was issued after them
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + c * 32, o);
+                            tmem_ld_wait();
+                            reg_fence32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = f2u(u2f(o[e]) * factor);
+                            tmem_st32(t_o + c * 32, o);
+                        }
+                    }
+                }
+                const float negm = m_run == -INFINITY ? 0.f : -m_run;  // nothing seen yet: every p below is zero
+                const uint64_t mul2 = f2_pack(mul, mul), negm2 = f2_pack(negm, negm);
+                uint64_t l4[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int c = 64 * h + 2 * e;
+                        const uint64_t arg = ffma2(f2_pack(u2f(s[c]), u2f(s[c + 1])), mul2, negm2);
+                        const float p0 = ex2_approx(f2_lo(arg)), p1 = ex2_approx(f2_hi(arg));
+                        l4[e % 4] = fadd2(l4[e % 4], f2_pack(p0, p1));
+                        // P is rounded to bf16, the operand type of the second product: each
+                        // weight is off by at most 2^-8 of itself; the sum keeps fp32
+                        p[e] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32(t_s + h * 32, p);
+                }
+                const uint64_t l2 = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+                l += f2_lo(l2) + f2_hi(l2);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bars.p_ready[x]);
+            }
+            // ---- epilogue (the run again, from its ring slot: nothing of it stays live above)
+            const Run r = read_run(bars, k % kRing);
+            const Row w = row_of(a, r.hs, r.tok0, r.left, r.past, one ? 0 : x, row);
+            const bool live = w.lim > 0;
+            const bool other = one && r.n > 1;  // the other stream has a part of the same rows
+            float wt = 1.f, wt_other = 0.f, m = m_run, sum = l;
+            if (one) {
+                ex[x * kM + row] = make_float2(m_run, l);
+                join();
+                const float2 y = ex[(x ^ 1) * kM + row];
+                m = fmaxf(m_run, y.x);
+                const float ref = m == -INFINITY ? 0.f : m;
+                wt = ex2_approx(m_run - ref);
+                wt_other = ex2_approx(y.x - ref);
+                sum = l * wt + y.y * wt_other;
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const bool used = one ? y < r.n : true;
+                if (used && (one || y == x) && ok) ok = mbar_wait_warp(&bars.o_full[y], o_uses[y] & 1, &bars.abort);
+                if (used) ++o_uses[y];
+            }
+            tc_fence_after();
+            const bool write = ok && w.valid;
+            const bool spoiled = *static_cast<volatile int *>(&bars.spoiled[k % kRing]) != 0 && live;
+            const float inv = 1.f / sum;
+            const int slot_row = (one ? 0 : x * kM) + row;
+            // a unit of one row tile: stream 0 writes the first half of the columns, stream 1 the second
+            const int c0 = one ? x * (D / 64) : 0, c1 = one ? c0 + D / 64 : D / 32;
+            const long long token = static_cast<long long>(r.c0) + w.token;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_ts + w.head * a.o_hs;
+            if (__any_sync(0xffffffffu, w.valid)) {
+#pragma unroll 1
+                for (int c = c0; c < c1; ++c) {
+                    __syncwarp();
+                    uint32_t o[32];  // TMEM of this CTA: loaded unconditionally, used only when valid
+                    tmem_ld32((one ? t_lane + 256u : t_o) + c * 32, o);
+                    tmem_ld_wait();
+                    reg_fence32(o);
+                    if (one) {
+                        const float wa = x ? wt_other : wt, wb = x ? wt : wt_other;  // of O0, of O1
+                        uint32_t o1[32];
+                        tmem_ld32(t_lane + 256u + D + c * 32, o1);
+                        tmem_ld_wait();
+                        reg_fence32(o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = f2u(other ? fmaf(wa, u2f(o[e]), wb * u2f(o1[e])) : wa * u2f(o[e]));
+                    }
+                    if (spoiled) {  // add the non-finite values of the edge tiles that this row sees
+                        const int end = min(w.lim, (r.j0 + r.n) * kN);
+                        const int32_t *table = a.page_table + static_cast<long long>(r.seq) * a.table_stride;
+#pragma unroll 1
+                        for (int key = (r.j0 + edge_of(r)) * kN; key < end; ++key) {
+                            const int page = table[key / a.P];
+                            if (page < 0 || page >= a.n_pages) continue;
+                            const uint32_t *vr = reinterpret_cast<const uint32_t *>(
+                                static_cast<const __nv_bfloat16 *>(a.v) + page * a.v_ps + (r.hs / a.groups) * a.v_hs +
+                                (key % a.P) * a.v_rs + c * 32);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const uint32_t v = vr[e], nf = nonfinite2(v);
+                                if (nf & 0xffffu) o[2 * e] = f2u(u2f(o[2 * e]) + bf16lo_to_f32(v));
+                                if (nf & 0xffff0000u) o[2 * e + 1] = f2u(u2f(o[2 * e + 1]) + bf16hi_to_f32(v));
+                            }
+                        }
+                    }
+                    if (write && r.slot >= 0) {
+                        // four columns of all the slot's rows side by side: a warp writes 512 bytes at once
+                        float4 *dst = reinterpret_cast<float4 *>(a.part_o) +
+                                      (static_cast<size_t>(r.slot) * (D / 4) + c * 8) * a.slot_rows + slot_row;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e * a.slot_rows] = make_float4(u2f(o[4 * e]), u2f(o[4 * e + 1]), u2f(o[4 * e + 2]), u2f(o[4 * e + 3]));
+                    } else if (write) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(out + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t pk[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                pk[y] = live ? pack_bf16x2(u2f(o[8 * e + 2 * y]) * inv, u2f(o[8 * e + 2 * y + 1]) * inv) : 0u;
+                            dst[e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        }
+                    }
+                }
+            }
+            if (write && (!one || x == 0)) {
+                if (r.slot >= 0)
+                    reinterpret_cast<float2 *>(a.part_ml)[static_cast<size_t>(r.slot) * a.slot_rows + slot_row] = make_float2(m, sum);
+                else if (a.lse)
+                    a.lse[token * a.H + w.head] = live ? (m + log2f(sum)) * kLn2 : -INFINITY;
+            }
+            mbar_arrive(&bars.run_empty[k % kRing]);
+            tc_fence_before();
+            __syncwarp();
+            // both streams are done with each other's O and with ex
+            if (one) join();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        __syncwarp();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    if (threadIdx.x == 0 && bars.abort) report_timeout(a.status, 0x45);
+}
+
+// Block (i, y) merges 32 rows of the unit that begins in CTA i of the main kernel and
+// ends in a later one: slot 2 i + 1, then slot 2 c of the CTAs after it.  Lane = row, as
+// the partial results lie; warp = D / 8 columns.
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int i = blockIdx.x, rr = blockIdx.y * 32 + threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int4 rec = reinterpret_cast<const int4 *>(a.merge)[2 * i], rec2 = reinterpret_cast<const int4 *>(a.merge)[2 * i + 1];
+    if (rec.x < 0) return;
+    const Row w = row_of(a, rec.y, rec.z, rec2.x, rec2.y, rr / kM, rr % kM);
+    if (!w.valid) return;
+    constexpr int C = D / 32;
+    auto slot = [&](int c) { return static_cast<size_t>(c == 0 ? 2 * i + 1 : 2 * (i + c)); };
+    auto part = [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[slot(c) * a.slot_rows + rr]; };
+    auto column = [&](int c, int e) {
+        return reinterpret_cast<const float4 *>(a.part_o)[(slot(c) * (D / 4) + warp * C + e) * a.slot_rows + rr];
+    };
+    float2 x[kAhead];
+    float4 o[kAhead][C];
+    const long long token = static_cast<long long>(rec2.z) + w.token;
+    const bool live = w.lim > 0;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_ts + w.head * a.o_hs + warp * 4 * C;
+    const float2 ml = merge_row<C, false>(rec.w - i + 1, live, out, part, column, x, o);
+    if (a.lse && warp == 0) a.lse[token * a.H + w.head] = live ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+}
+
+template <int D, bool Single>
+cudaError_t launch_paged_t(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv) {
+    using L = Layout<D, Single>;
+    cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, Single>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(a.grid);
+    e = launch_pdl(paged_tc_kernel<D, Single>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, tq, tk, tv);
+    if (e != cudaSuccess || grid == 1) return e;
+    return launch_pdl(paged_join_kernel<D>, dim3(grid - 1, static_cast<unsigned>(a.slot_rows / 32)), dim3(256), 0, a.stream, a);
+}
+
+}  // namespace
+
+// Keys on the axis of all units, at most; the rest of the split follows from them.
+double paged_tc_axis(const PagedArgs &a) {
+    const double units = static_cast<double>(a.n_seq) + static_cast<double>(a.T) / a.tokens;
+    return units * a.H_kv * a.groups * (static_cast<double>(a.max_len) + a.T + kN * (kUnitCost + 1));
+}
+
+cudaError_t launch_paged_tc(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv) {
+    if (a.D == 64) return a.single ? launch_paged_t<64, true>(a, tq, tk, tv) : launch_paged_t<64, false>(a, tq, tk, tv);
+    return a.single ? launch_paged_t<128, true>(a, tq, tk, tv) : launch_paged_t<128, false>(a, tq, tk, tv);
+}
+
+}  // namespace attn

@@ -1,5 +1,6 @@
 // fp32 attention over tiles on the CUDA cores (FFMA only, no TF32): packed
-// sequences (attn_fwd_packed) and trees of drafted tokens (attn_decode_tree).
+// sequences (attn_fwd_packed), trees of drafted tokens (attn_decode_tree) and new
+// tokens over a paged cache (attn_fwd_paged).
 //
 // 32 query rows against tiles of 32 keys, online softmax in log2 units.  A warp
 // holds 16 rows x 32 keys of scores as 4 x 4 a thread (rows ty + 4 i, keys tx + 8 j)
@@ -94,13 +95,13 @@ __device__ __forceinline__ int ty_of() { return static_cast<int>(threadIdx.x % 2
 __device__ __forceinline__ int row_of(int i) { return static_cast<int>(threadIdx.x / 32 % 2) * (kRows / 2) + ty_of() + 4 * i; }
 
 // This worker's part of keys [k0, k1), an equal share in units of 8 keys (the whole
-// block calls it, with the copies of Q committed as one group): K row j at
-// kbase + j * ks, V row j at vbase + j * vs.  visible(i, key0) gives the bits of
-// keys key0 + tx + 8 j, j < 4, of row_of(i).  A warp none of whose rows is used
+// block calls it, with the copies of Q committed as one group): K row j at kat(j, in),
+// V row j at vat(j, in), an address to be read where `in` stays true.  visible(i, key0)
+// gives the bits of keys key0 + tx + 8 j, j < 4, of row_of(i).  A warp none of whose rows is used
 // (`active` is false) only copies and keeps step.
-template <int D, int W, typename Visible>
-__device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, long long ks, const float *vbase,
-                                     long long vs, int k0, int k1, float sl2, bool active, Rows4<D> &st, Visible visible) {
+template <int D, int W, typename KAt, typename VAt, typename Visible>
+__device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int k0, int k1, float sl2, bool active,
+                                     Rows4<D> &st, Visible visible) {
     const int worker = threadIdx.x / 64, tid = threadIdx.x % 64, half = tid / 32, tx = tx_of(), ty = ty_of();
     auto &sm = smem.w[worker];
     auto &sp = sm.p[half];
@@ -110,20 +111,21 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
     const int first = k0 + worker * per, last = min(first + per, k1);  // no keys if last <= first
     // the key units of 8 in the tile at key0; rows past the last key are zeros
     auto units = [&](int key0) { return min((last - key0 + 7) / 8, kKeys / 8); };
-    auto load = [&](float *dst, int stride, const float *base, long long gs, int key0) {
+    auto load = [&](float *dst, int stride, auto at, int key0) {
         const uint32_t to = smem_u32(dst);
         const int n = units(key0) * (8 * D / 4);
 #pragma unroll 8
         for (int i = tid; i < n; i += 64) {
             const int row = i / (D / 4), c = i % (D / 4);
-            const bool in = key0 + row < last;
-            cp_async16(to + (row * stride + 4 * c) * 4, base + (in ? key0 + row : k0) * gs + 4 * c, in ? 16u : 0u);
+            bool in = key0 + row < last;
+            const float *src = at(key0 + row, in) + 4 * c;
+            cp_async16(to + (row * stride + 4 * c) * 4, src, in ? 16u : 0u);
         }
         cp_async_commit();
     };
     if (first < last) {
-        load(&sm.k[0][0], D + 4, kbase, ks, first);
-        load(&sm.v[0][0], D, vbase, vs, first);
+        load(&sm.k[0][0], D + 4, kat, first);
+        load(&sm.v[0][0], D, vat, first);
         cp_async_wait<2>();  // Q, copied in before by the whole block
     } else {
         cp_async_wait<0>();
@@ -201,7 +203,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
         const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
         sync();              // both warps are done with K; V and P are visible
-        if (more) load(&sm.k[0][0], D + 4, kbase, ks, key0 + kKeys);
+        if (more) load(&sm.k[0][0], D + 4, kat, key0 + kKeys);
         auto mix = [&](auto guarded) {
 #pragma unroll 1
             for (int j = 0; j < 8 * n_units; j += 4) {
@@ -237,13 +239,18 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, const float *kbase, lo
         else
             mix(std::false_type{});
         sync();  // V and P are free
-        if (more) load(&sm.v[0][0], D, vbase, vs, key0 + kKeys);
+        if (more) load(&sm.v[0][0], D, vat, key0 + kKeys);
     }
     cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int x = 2; x < 16; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
+}
+
+// Rows gs elements apart; k0 is one that may be read.
+__device__ __forceinline__ auto rows_at(const float *base, long long gs, int k0) {
+    return [=](int key, bool in) { return base + (in ? key : k0) * gs; };
 }
 
 template <int D>
@@ -441,8 +448,8 @@ __global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) packed_f32
     const int k0 = min(c0 + static_cast<int>(cluster_rank()) * share, limit), k1 = min(k0 + share, limit);
     Rows4<D> st;
     reset(st);
-    walk<D, W>(sm, static_cast<const float *>(a.k) + g * a.k_hs, a.k_ts, static_cast<const float *>(a.v) + g * a.v_hs,
-            a.v_ts, k0, k1, a.scale * kLog2e, t0 + tid / 32 % 2 * (kRows / 2) < end, st, [&](int i, int key0) {
+    walk<D, W>(sm, rows_at(static_cast<const float *>(a.k) + g * a.k_hs, a.k_ts, k0),
+            rows_at(static_cast<const float *>(a.v) + g * a.v_hs, a.v_ts, k0), k0, k1, a.scale * kLog2e, t0 + tid / 32 % 2 * (kRows / 2) < end, st, [&](int i, int key0) {
                 uint32_t see = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) see |= (key0 + tx + 8 * j < hi[i] ? 1u : 0u) << j;
@@ -527,8 +534,8 @@ __global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) tree_f32_k
     reset(st);
     const size_t head = static_cast<size_t>(bk) * a.Skv * D;
     if (k0 < k1) {
-        walk<D, W>(sm, static_cast<const float *>(a.k) + head, D, static_cast<const float *>(a.v) + head, D, k0, k1,
-                a.scale * kLog2e, __any_sync(0xffffffffu, live[0] || live[1] || live[2] || live[3]), st, [&](int i, int key0) {
+        walk<D, W>(sm, rows_at(static_cast<const float *>(a.k) + head, D, k0),
+                rows_at(static_cast<const float *>(a.v) + head, D, k0), k0, k1, a.scale * kLog2e, __any_sync(0xffffffffu, live[0] || live[1] || live[2] || live[3]), st, [&](int i, int key0) {
                     uint32_t see = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -579,6 +586,180 @@ cudaError_t launch_tree_f32_t(const TreeArgs &a) {
     return blocks > a.n_sm ? launch_tree_f32_w<D, kMany<D> / 2>(a) : launch_tree_f32_w<D, kMany<D>>(a);
 }
 
+// ------------------------------------------------------------ new tokens over a paged cache
+
+// The 32 rows of a block: rows [r0, r0 + 32) of a sequence's n G (token by token, row r is
+// token r / G, head r % G), and the keys [0, keys) that the last of them sees.
+struct PagedBlock {
+    int s, c0, n, past, r0, keys;
+};
+// Block w of any cached head; n = 0: an empty one.  The whole warp calls it.
+__device__ __forceinline__ PagedBlock paged_block(const PagedArgs &a, int w, int lane) {
+    const int G = a.H / a.H_kv;
+    PagedBlock p{0, 0, 0, 0, 0, 0};
+    if (a.cu_seqlens) {
+        // sequence s owns the blocks from cu[s] G / 32 + s on, a few of which stay empty
+        int lo = 0, hi = a.n_seq;
+        while (lo < hi) {
+            const int step = (hi - lo + 31) / 32;
+            const int at = lo + lane * step;
+            const unsigned le = __ballot_sync(0xffffffffu, at < hi && min(max(a.cu_seqlens[at], 0), a.T) * G / kRows + at <= w);
+            const int c = le == 0xffffffffu ? 32 : __ffs(~le) - 1;
+            if (c == 0) break;
+            hi = min(hi, lo + c * step);
+            lo = lo + (c - 1) * step + 1;
+        }
+        p.s = lo - 1;
+        if (p.s < 0) return p;
+        p.c0 = min(max(a.cu_seqlens[p.s], 0), a.T);
+        p.n = min(max(a.cu_seqlens[p.s + 1], p.c0), a.T) - p.c0;
+        p.r0 = (w - p.c0 * G / kRows - p.s) * kRows;
+    } else {
+        const int each = (a.per_seq * G + kRows - 1) / kRows;
+        p.s = w / each;
+        p.c0 = p.s * a.per_seq;
+        p.n = a.per_seq;
+        p.r0 = (w - p.s * each) * kRows;
+    }
+    if (p.r0 >= p.n * G) {
+        p.n = 0;
+        return p;
+    }
+    const int L = a.cache_len ? min(max(a.cache_len[p.s], 0), a.max_len) : a.max_len;
+    p.past = L - p.n;
+    p.keys = max(0, p.past + min(p.r0 + kRows - 1, p.n * G - 1) / G + 1);
+    return p;
+}
+// Keys of a split, in units of 8, at least 64.
+__device__ __forceinline__ int paged_share(int keys, int n_split) {
+    return max(64, ((keys + n_split - 1) / n_split + 7) / 8 * 8);
+}
+
+// Block x: (32 rows, cached head, split of the keys).  Up to eight splits are a cluster,
+// whose first CTA writes the result; more leave their parts in the workspace.
+template <int D, int W>
+__global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) paged_f32_kernel(const PagedArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    extern __shared__ __align__(16) uint8_t f32_smem[];
+    F32Smem<D, W> &sm = *reinterpret_cast<F32Smem<D, W> *>(f32_smem);
+    const int tid = threadIdx.x, tx = tx_of(), G = a.H / a.H_kv;
+    const bool cluster = a.n_split <= kTreeClusterF32;  // of a.n_split CTAs
+    const int c = blockIdx.x % a.n_split, g = blockIdx.x / a.n_split % a.H_kv, w = blockIdx.x / a.n_split / a.H_kv;
+    const PagedBlock p = paged_block(a, w, tid % 32);
+    if (p.n == 0) return;  // as every CTA of the cluster
+    const int rows = p.n * G, share = paged_share(p.keys, a.n_split);
+    const int k0 = static_cast<int>(min(static_cast<long long>(c) * share, static_cast<long long>(p.keys)));
+    const int k1 = min(k0 + share, p.keys);
+    if (k0 >= k1 && !cluster) return;  // the merge never reads this split
+    for (int i = tid; i < kRows * D / 4; i += kThreads<W>) {
+        const int r = p.r0 + i / (D / 4), col = 4 * (i % (D / 4));
+        const bool in = r < rows;
+        const float *q = static_cast<const float *>(a.q);
+        if (in) q += static_cast<long long>(p.c0 + r / G) * a.q_ts + (g * G + r % G) * a.q_hs + col;
+        cp_async16(smem_u32(&sm.q[i / (D / 4)][col]), q, in ? 16u : 0u);
+    }
+    cp_async_commit();
+    int lim[4];  // rows see keys [0, lim)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = p.r0 + row_of(i);
+        lim[i] = r < rows ? max(0, p.past + r / G + 1) : 0;
+    }
+    Rows4<D> st;
+    reset(st);
+    if (k0 < k1) {
+        const int32_t *table = a.page_table + p.s * a.table_stride;
+        auto pages_at = [&](const float *base, long long ps, long long rs) {
+            return [=](int key, bool &in) {
+                const int page = in ? table[key / a.P] : 0;
+                in = in && page >= 0 && page < a.n_pages;  // an entry that is no page reads as zeros
+                return base + (in ? page * ps + key % a.P * rs : 0ll);
+            };
+        };
+        walk<D, W>(sm, pages_at(static_cast<const float *>(a.k) + g * a.k_hs, a.k_ps, a.k_rs),
+                   pages_at(static_cast<const float *>(a.v) + g * a.v_hs, a.v_ps, a.v_rs), k0, k1, a.scale * kLog2e,
+                   __any_sync(0xffffffffu, lim[0] > k0 || lim[1] > k0 || lim[2] > k0 || lim[3] > k0), st, [&](int i, int key0) {
+                       uint32_t see = 0;
+#pragma unroll
+                       for (int j = 0; j < 4; ++j) see |= (key0 + tx + 8 * j < lim[i] ? 1u : 0u) << j;
+                       return see;
+                   });
+    } else {
+        cp_async_wait<0>();
+    }
+    Joined<D, W> x = join_workers(sm, st);
+    if (cluster && !join_cluster(sm, x)) return;
+    const int r = p.r0 + x.row();
+    if (r >= rows) return;
+    float *O;
+    float f = 1.f;
+    if (cluster) {
+        const long long token = p.c0 + r / G;
+        const int h = g * G + r % G;
+        const bool live = p.past + r / G >= 0;
+        O = static_cast<float *>(a.out) + token * a.o_ts + h * a.o_hs;
+        f = 1.f / x.l;
+        if (a.lse && x.column(0) == 0) a.lse[token * a.H + h] = live ? (x.m + log2f(x.l)) * kLn2 : -INFINITY;
+        if (!live) {
+#pragma unroll
+            for (int cc = 0; cc < x.C; ++cc) x.o[cc] = make_float4(0.f, 0.f, 0.f, 0.f);
+            f = 0.f;
+        }
+    } else {
+        const size_t part = ((static_cast<size_t>(w) * a.H_kv + g) * kRows + x.row()) * a.n_split + c;
+        O = a.part_o + part * D;
+        if (x.column(0) == 0) *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(x.m, x.l);
+    }
+#pragma unroll
+    for (int cc = 0; cc < x.C; ++cc) *reinterpret_cast<float4 *>(O + x.column(cc)) = x.times(cc, f);
+}
+
+// One warp per row of a block: the parts of its splits.
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_f32_kernel(const PagedArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int G = a.H / a.H_kv, lane = threadIdx.x % 32, rr = blockIdx.x % (kRows / 8) * 8 + threadIdx.x / 32;
+    const int g = blockIdx.x / (kRows / 8) % a.H_kv, w = blockIdx.x / (kRows / 8) / a.H_kv;
+    const PagedBlock p = paged_block(a, w, lane);
+    const int r = p.r0 + rr;
+    if (p.n == 0 || r >= p.n * G || lane >= D / 4) return;
+    const long long token = p.c0 + r / G;
+    const int h = g * G + r % G, share = paged_share(p.keys, a.n_split);
+    const bool live = p.past + r / G >= 0;
+    const size_t first = ((static_cast<size_t>(w) * a.H_kv + g) * kRows + rr) * a.n_split;
+    float2 x[kAhead];
+    float4 o[kAhead][1];
+    const float2 ml = merge_row<1, false>(live ? (p.keys + share - 1) / share : 0, live,
+                                          static_cast<float *>(a.out) + token * a.o_ts + h * a.o_hs + 4 * lane,
+                                          [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[first + c]; },
+                                          [&](int c, int) { return reinterpret_cast<const float4 *>(a.part_o)[(first + c) * (D / 4) + lane]; },
+                                          x, o);
+    if (a.lse && lane == 0) a.lse[token * a.H + h] = live ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+}
+
+template <int D, int W>
+cudaError_t launch_paged_f32_w(const PagedArgs &a, unsigned blocks) {
+    const size_t smem = sizeof(F32Smem<D, W>);
+    cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const bool cluster = a.n_split <= kTreeClusterF32;
+    e = launch_clusters(paged_f32_kernel<D, W>, cluster ? static_cast<unsigned>(a.n_split) : 1u, blocks * a.n_split,
+                        kThreads<W>, smem, a.stream, a);
+    if (e != cudaSuccess || cluster) return e;
+    return launch_pdl(paged_merge_f32_kernel<D>, dim3(blocks * (kRows / 8)), dim3(256), 0, a.stream, a);
+}
+
+template <int D>
+cudaError_t launch_paged_f32_t(const PagedArgs &a) {
+    const unsigned blocks = static_cast<unsigned>(paged_f32_blocks(a) * a.H_kv);
+    // more blocks than SMs: two an SM (as for trees)
+    return blocks * static_cast<long long>(a.n_split) > a.n_sm ? launch_paged_f32_w<D, kMany<D> / 2>(a, blocks)
+                                                               : launch_paged_f32_w<D, kMany<D>>(a, blocks);
+}
+
 }  // namespace
 
 long long packed_f32_blocks(long long T, long long n_seq) { return T / kRows + n_seq; }
@@ -605,6 +786,24 @@ int tree_chunk_f32(int B, int H, int H_kv, int T, int Skv, int D, int n_sm) {
 
 cudaError_t launch_tree_f32(const TreeArgs &a) {
     return a.D == 64 ? launch_tree_f32_t<64>(a) : launch_tree_f32_t<128>(a);
+}
+
+long long paged_f32_blocks(const PagedArgs &a) {
+    const long long G = a.H / a.H_kv;
+    return a.cu_seqlens ? a.T * G / kRows + a.n_seq : a.n_seq * ((a.per_seq * G + kRows - 1) / kRows);
+}
+
+int paged_f32_splits(const PagedArgs &a) {
+    // two blocks an SM, 128 keys at least a block where the table's rows are full
+    const long long blocks = paged_f32_blocks(a) * a.H_kv, want = 2LL * (a.n_sm > 0 ? a.n_sm : 1);
+    long long n = blocks > 0 ? want / blocks : 1;
+    const long long most = (static_cast<long long>(a.max_len) + 127) / 128;
+    n = n > most ? most : n;
+    return static_cast<int>(n >= 2 * kTreeClusterF32 ? n : n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1);
+}
+
+cudaError_t launch_paged_f32(const PagedArgs &a) {
+    return a.D == 64 ? launch_paged_f32_t<64>(a) : launch_paged_f32_t<128>(a);
 }
 
 }  // namespace attn

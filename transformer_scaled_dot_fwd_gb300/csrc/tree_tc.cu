@@ -794,60 +794,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------ merges of partial results
 
-__device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-}
-
-// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, M the largest m_c, the
-// parts added in order, for one row and 4 C columns: part(c) is the row's (m, l) in
-// part c, column(c, e) its e-th four columns.
-//
-// kAhead parts are loaded before the first is used: few rows, so latency counts.  Early:
-// x and o hold the first ones already.
-constexpr int kAhead = 4;
-template <int C, bool Early, typename T, typename Part, typename Column>
-__device__ __forceinline__ void merge_row(int n, bool live, T *out, Part part, Column column,
-                                          float2 (&x)[kAhead], float4 (&o)[kAhead][C]) {
-    float4 acc[C];
-#pragma unroll
-    for (int e = 0; e < C; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f, M = -INFINITY;
-    auto add = [&](int c0) {
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-            if (c0 + y >= n) break;
-            // relative to the running max; a part in which the row saw nothing holds zeros
-            const float mn = fmaxf(M, x[y].x), ref = mn == -INFINITY ? 0.f : mn;
-            const float old = ex2_approx(M - ref), w = ex2_approx(x[y].x - ref);
-            M = mn;
-            sum = sum * old + w * x[y].y;
-#pragma unroll
-            for (int e = 0; e < C; ++e)
-                acc[e] = make_float4(fmaf(w, o[y][e].x, acc[e].x * old), fmaf(w, o[y][e].y, acc[e].y * old),
-                                     fmaf(w, o[y][e].z, acc[e].z * old), fmaf(w, o[y][e].w, acc[e].w * old));
-        }
-    };
-    auto load = [&](int c0) {
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y) {
-            const int c = min(c0 + y, n - 1);
-            x[y] = part(c);
-#pragma unroll
-            for (int e = 0; e < C; ++e) o[y][e] = column(c, e);
-        }
-    };
-    for (int c0 = 0; c0 < n; c0 += kAhead) {
-        if (!Early || c0 > 0) load(c0);
-        add(c0);
-    }
-    const float inv = live ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int e = 0; e < C; ++e)
-        store4(out + 4 * e, live ? make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv)
-                                 : make_float4(0.f, 0.f, 0.f, 0.f));
-}
-
 // bf16: block (i, y) merges 32 rows of the unit that begins in CTA i of the main
 // kernel and ends in a later one: slot 2 i + 1, then slot 2 c of the CTAs after
 // it.  Lane = row, as the partial results lie; warp = D / 8 columns.
