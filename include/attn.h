@@ -547,6 +547,58 @@ ATTN_API int attn_rope_append(const void *q, const void *k, const void *v, void 
                               void *stream);
 
 /*
+ * attn_norm_rope -- RMS norm of each head row of q and k, and the rotary turn of the
+ * result, in one pass.
+ *
+ *     y = x / sqrt(mean over the row's D elements of x^2 + eps) * weight,
+ *
+ * then turned as attn_rope turns x.  The arithmetic is fp32 from the load to the one
+ * rounding at the store (the normed row is not rounded before its turn).  The squares are
+ * summed in fp32: a row of elements beyond 10^19 loses itself to their infinite sum, and
+ * with eps = 0 a row of zeros is NaN.
+ *
+ *   q_weight, k_weight  (D,) in the call's dtype, or NULL: that tensor is turned as it is
+ *   eps       finite, >= 0
+ *
+ * The rest as in attn_rope (outputs may be their inputs).  Fast are 16-byte aligned
+ * pointers and strides with interleaved pairs or a rotary_dim / 2 of whole 16 bytes.
+ */
+ATTN_API int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int T, int H, int H_kv, int D,
+                            const long long *strides, const int32_t *positions, const double *freqs, int rotary_dim,
+                            int interleaved, float mscale, const void *q_weight, const void *k_weight, float eps, int dtype,
+                            void *stream);
+
+/*
+ * attn_rope_append_paged -- new tokens into a paged KV cache: the norm (where weights are
+ * given) and turn of attn_norm_rope, the turned keys and the values written to their pages.
+ * It is the append that attn_fwd_paged expects.
+ *
+ * Sequence s's new tokens are [cu_seqlens[s], cu_seqlens[s + 1]), n_s of them, or T / n_seq
+ * each.  cache_len[s] = L_s counts them already, so token i of the sequence is key
+ * j = L_s - n_s + i, which is also its position unless `positions` says otherwise, and
+ * goes to row j % page_size of page page_table[s][j / page_size].  A token whose j is
+ * negative, or whose entry of the table is outside [0, n_pages), is turned but not cached.
+ * Tokens outside every sequence are neither read nor written anywhere; other rows of the
+ * pages stay as they were.  Two tokens of a call must not have the same row of a page.
+ *
+ *   q, q_out  (T, H, D) rows; k, v  (T, H_kv, D) rows, H_kv >= 1
+ *   k_out     NULL, or (T, H_kv, D) rows: the turned keys once more, token by token
+ *   kpages, vpages  (n_pages, H_kv, page_size, D) pages, written; any page_size >= 1
+ *   strides   NULL or HOST int64[16]: q, k, v, q_out, k_out as in attn_rope, then page, head
+ *             and row of kpages and of vpages
+ *   page_table, cu_seqlens, cache_len  as in attn_fwd_paged
+ *   positions device int32[T] or NULL
+ *
+ * The rest as in attn_norm_rope.
+ */
+ATTN_API int attn_rope_append_paged(const void *q, const void *k, const void *v, void *q_out, void *k_out, void *kpages,
+                                    void *vpages, int T, int H, int H_kv, int D, const long long *strides, int n_pages,
+                                    int page_size, const int32_t *page_table, int max_pages, long long table_stride,
+                                    const int32_t *cu_seqlens, const int32_t *cache_len, int n_seq, const int32_t *positions,
+                                    const double *freqs, int rotary_dim, int interleaved, float mscale, const void *q_weight,
+                                    const void *k_weight, float eps, int dtype, void *stream);
+
+/*
  * attn_device_status -- synchronise `stream`, then report and clear the
  * device-side status word.  Returns ATTN_OK, ATTN_ETIMEOUT when a kernel gave
  * up on a device-side wait (its output is then undefined), ATTN_ECONFLICT

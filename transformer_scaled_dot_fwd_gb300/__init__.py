@@ -56,6 +56,9 @@ SIGNATURES = {
     "attn_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp]),
     "attn_rope_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
                               _i, _i, _f, _i, _vp]),
+    "attn_norm_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _f, _vp, _vp, _f, _i, _vp]),
+    "attn_rope_append_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _vp, _i, _ll, _vp, _vp, _i,
+                                    _vp, _vp, _i, _i, _f, _vp, _vp, _f, _i, _vp]),
     "attn_device_status": (_i, [_vp]),
     "attn_last_error": (ctypes.c_char_p, []),
     "attn_release": (None, []),
@@ -358,7 +361,7 @@ class _NoBinding:
     def _none(self, *args):
         return None
 
-    packed = rope = rope_append = tree = paged = _none
+    packed = rope = rope_append = tree = paged = norm_rope = append_paged = _none
 
 
 def _load_native():
@@ -381,7 +384,7 @@ def _load_native():
         "attn_fwd_packed", "attn_fwd_packed_workspace", "attn_rope", "attn_rope_append", "attn_decode_tree",
         "attn_decode_tree_workspace")))
     module.bind_paged(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
-        "attn_fwd_paged", "attn_fwd_paged_workspace")))
+        "attn_fwd_paged", "attn_fwd_paged_workspace", "attn_norm_rope", "attn_rope_append_paged")))
     _native = module
     return module
 
@@ -479,7 +482,7 @@ def _freqs_arg(freqs, D):
 
 
 # host int64 arrays of strides (a bytes object serves as the pointer)
-_LL6, _LL8, _LL10 = (struct.Struct(f"{n}q").pack for n in (6, 8, 10))
+_LL6, _LL8, _LL10, _LL16 = (struct.Struct(f"{n}q").pack for n in (6, 8, 10, 16))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -770,6 +773,106 @@ def attn_rope_append(q, k, v, kcache, vcache, freqs, cu_seqlens=None, cache_len=
     return q_out if k_out is None else (q_out, k_out)
 
 
+def _weight(name, w, D, dtype, device):
+    """data_ptr of an optional (D,) weight."""
+    if w is None:
+        return None
+    if not (w.shape == (D,) and w.device == device and w.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous ({D},) tensor on q's device")
+    if w.dtype != dtype:
+        raise TypeError(f"{name} must share q's dtype {dtype}")
+    return w.data_ptr()
+
+
+def attn_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
+                   interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """RMS norm of each head row of q (T, H, D) and k (T, H_kv, D), times the (D,)
+    weights (a tensor without one is not normed), then attn_rope's turn of the result, in one
+    pass and with one rounding.  k may be None.  Returns ``(q_out, k_out)`` (``q_out``
+    alone without k); pass ``q_out=q`` to work in place.  See include/attn.h.
+    """
+    if stream is None:
+        done = (_native or _load_native()).norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, q_out, k_out,
+                                                     interleaved, mscale)
+        if done is not None:
+            return done
+    torch = _torch()
+    (T, H, D), sq, code, device = _first(q, 3)
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
+            return attn_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, q_out, k_out, interleaved, mscale)
+    dtype = q.dtype
+    fr, rd = _freqs_arg(freqs, D)
+    pos = _ints("positions", positions, (T,), device)
+    if positions is None:
+        raise ValueError("positions must be given")
+    wq, wk = _weight("q_weight", q_weight, D, dtype, device), _weight("k_weight", k_weight, D, dtype, device)
+    q_out, ot, oh = _out_rows("q_out", q_out, T, H, D, dtype, device)
+    H_kv = kt = kh = kot = koh = 0
+    if k is not None:
+        H_kv, kt, kh = _rows("k", k, T, D, dtype, device)
+        k_out, kot, koh = _out_rows("k_out", k_out, T, H_kv, D, dtype, device)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out or k_weight without k")
+    rc = lib().attn_norm_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                              None if k is None else k_out.data_ptr(), T, H, H_kv, D,
+                              _LL8(sq[0], sq[1], kt, kh, ot, oh, kot, koh), pos, fr, rd, 1 if interleaved else 0, mscale,
+                              wq, wk, eps, code, _current(device))
+    if rc:
+        _check(rc)
+    return q_out if k is None else (q_out, k_out)
+
+
+def attn_rope_append_paged(q, k, v, kpages, vpages, page_table, freqs, cache_len=None, cu_seqlens=None, positions=None,
+                           q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
+                           interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """attn_rope (or, with weights, attn_norm_rope) of new tokens, with the turned keys
+    and the values written to the pages (n_pages, H_kv, page_size, D) of a cache: token i of
+    sequence s (tokens [cu_seqlens[s], cu_seqlens[s + 1]), n of them; T / sequences
+    each without cu_seqlens) is key j = cache_len[s] - n + i, in row j % page_size of
+    page page_table[s, j // page_size]; j is also its position unless ``positions`` is given.
+    Returns ``q_out``, or ``(q_out, k_out)`` when a ``k_out`` (T, H_kv, D) is given
+    for the turned keys.  See include/attn.h.
+    """
+    if stream is None:
+        done = (_native or _load_native()).append_paged(q, k, v, kpages, vpages, page_table, freqs, cache_len, cu_seqlens,
+                                                        positions, q_weight, k_weight, eps, q_out, k_out, interleaved, mscale)
+        if done is not None:
+            return done
+    torch = _torch()
+    (T, H, D), sq, code, device = _first(q, 3)
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
+            return attn_rope_append_paged(q, k, v, kpages, vpages, page_table, freqs, cache_len, cu_seqlens, positions,
+                                          q_weight, k_weight, eps, q_out, k_out, interleaved, mscale)
+    dtype = q.dtype
+    H_kv, kt, kh = _rows("k", k, T, D, dtype, device)
+    Hv, vt, vh = _rows("v", v, T, D, dtype, device)
+    n_pages, Hp, P, ps = _pages(kpages, vpages, dtype, device, D)
+    if Hv != H_kv or Hp != H_kv:
+        raise ValueError("k and v must be (T, H_kv, D), kpages and vpages (n_pages, H_kv, page_size, D)")
+    n_seq, M, tst, table = _table(page_table, device)
+    fr, rd = _freqs_arg(freqs, D)
+    cu = _ints("cu_seqlens", cu_seqlens, (n_seq + 1,), device)
+    cl = _ints("cache_len", cache_len, (n_seq,), device)
+    pos = _ints("positions", positions, (T,), device)
+    if cu is None and n_seq == 0 and T:
+        raise ValueError(f"without cu_seqlens q's {T} tokens must be a multiple of the {n_seq} sequences")
+    wq, wk = _weight("q_weight", q_weight, D, dtype, device), _weight("k_weight", k_weight, D, dtype, device)
+    q_out, ot, oh = _out_rows("q_out", q_out, T, H, D, dtype, device)
+    kot = koh = 0
+    if k_out is not None:
+        k_out, kot, koh = _out_rows("k_out", k_out, T, H_kv, D, dtype, device)
+    rc = lib().attn_rope_append_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+                                      None if k_out is None else k_out.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
+                                      T, H, H_kv, D, _LL16(sq[0], sq[1], kt, kh, vt, vh, ot, oh, kot, koh, *ps), n_pages, P,
+                                      table, M, tst, cu, cl, n_seq, pos, fr, rd, 1 if interleaved else 0, mscale, wq, wk, eps,
+                                      code, _current(device))
+    if rc:
+        _check(rc)
+    return q_out if k_out is None else (q_out, k_out)
+
+
 def attn_device_status(stream=None) -> None:
     """Synchronise the stream and raise AttnError if a kernel reported a timed-out
     wait (ATTN_ETIMEOUT) or a shared prefill work counter (ATTN_ECONFLICT)."""
@@ -787,7 +890,7 @@ def attn_release() -> None:
 
 __all__ = [
     "attn_fwd", "attn_fwd_chunked", "attn_fwd_debug", "attn_fwd_host", "attn_decode", "attn_decode_noalloc", "attn_decode_splits", "attn_fwd_packed", "attn_decode_tree",
-    "attn_fwd_paged",
+    "attn_fwd_paged", "attn_norm_rope", "attn_rope_append_paged",
     "attn_rope",
     "attn_rope_append", "attn_rope_frequencies", "attn_device_status", "attn_release",
     "attn_last_error", "attn_selftest_wait_timeout", "lib", "AttnError", "SIGNATURES", "LIB_PATH",

@@ -1291,6 +1291,148 @@ ATTN_API int attn_rope_append(const void *q, const void *k, const void *v, void 
     return rope_impl("attn_rope_append", a, strides, freqs, 0, dtype, stream);
 }
 
+// Shared by attn_norm_rope (no cache) and attn_rope_append_paged.  strides: q, k, v,
+// q_out, k_out (token, head), kpages, vpages (page, head, row), or NULL.
+static int norm_rope_impl(const char *who, NormRopeArgs a, const long long *strides, const double *freqs, int max_pages,
+                          int dtype, void *stream) {
+    g_last_error[0] = '\0';
+    const bool append = a.append != 0;
+    if (a.T < 0 || a.H < 1 || a.H_kv < 0 || (append && (a.H_kv < 1 || a.n_seq < 0 || max_pages < 0 || a.n_pages < 0)))
+        return fail(ATTN_EINVAL, "%s: need T >= 0, H >= 1, H_kv >= %d%s", who, append ? 1 : 0,
+                    append ? ", n_seq >= 0, max_pages >= 0, n_pages >= 0" : "");
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return fail(ATTN_EINVAL, "%s: unknown dtype %d", who, dtype);
+    if (a.D <= 0) return fail(ATTN_EINVAL, "%s: D must be positive (got %d)", who, a.D);
+    if (a.D != 64 && a.D != 128) return fail(ATTN_EUNSUPPORTED, "%s: D = %d not supported (64 or 128)", who, a.D);
+    if (a.rotary_dim < 0 || a.rotary_dim > a.D || a.rotary_dim % 2)
+        return fail(ATTN_EINVAL, "%s: rotary_dim must be even, in [0, D] (got %d)", who, a.rotary_dim);
+    if (a.interleaved != 0 && a.interleaved != 1) return fail(ATTN_EINVAL, "%s: interleaved must be 0 or 1", who);
+    if (!(fabsf(a.mscale) <= 3.4e38f)) return fail(ATTN_EINVAL, "%s: mscale must be finite", who);
+    if (!(a.eps >= 0.f && a.eps <= 3.4e38f)) return fail(ATTN_EINVAL, "%s: eps must be finite and >= 0", who);
+    if (a.rotary_dim > 0 && !freqs) return fail(ATTN_EINVAL, "%s: freqs must not be NULL", who);
+    for (int p = 0; p < a.rotary_dim / 2; ++p)
+        if (!isfinite(freqs[p])) return fail(ATTN_EINVAL, "%s: freqs[%d] is not finite", who, p);
+    if (append && a.P < 1) return fail(ATTN_EINVAL, "%s: a page must have rows (got %d)", who, a.P);
+    if (append && static_cast<long long>(max_pages) * a.P > 0x7fffffffLL)
+        return fail(ATTN_EINVAL, "%s: %d pages of %d rows are too many for a sequence", who, max_pages, a.P);
+    if (a.T == 0 || (append && a.n_seq == 0)) return ATTN_OK;
+    if (append && max_pages == 0) a.n_pages = 0;  // every token is turned, none cached
+    a.max_len = append ? max_pages * a.P : 0;
+    if (append && max_pages > 0 && a.n_pages == 0) return fail(ATTN_EINVAL, "%s: a table of pages needs n_pages >= 1", who);
+    if (!a.q || !a.q_out || (a.H_kv > 0 && !a.k) || (!append && a.H_kv > 0 && !a.k_out) ||
+        (append && (!a.v || (a.n_pages > 0 && (!a.kpages || !a.vpages || !a.page_table)))))
+        return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
+    if (!append && !a.positions) return fail(ATTN_EINVAL, "%s: positions must not be NULL", who);
+    if (append && !a.cu_seqlens && a.T % a.n_seq)
+        return fail(ATTN_EINVAL, "%s: without cu_seqlens T must be a multiple of n_seq (got %d, %d)", who, a.T, a.n_seq);
+    const long long esz = dtype == ATTN_BF16 ? 2 : 4;
+    const uintptr_t amask = static_cast<uintptr_t>(esz - 1);
+    if ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+         reinterpret_cast<uintptr_t>(a.q_out) | reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.kpages) |
+         reinterpret_cast<uintptr_t>(a.vpages) | reinterpret_cast<uintptr_t>(a.q_weight) |
+         reinterpret_cast<uintptr_t>(a.k_weight)) & amask)
+        return fail(ATTN_EINVAL, "%s: tensors must be aligned to their element size", who);
+    if ((reinterpret_cast<uintptr_t>(a.cu_seqlens) | reinterpret_cast<uintptr_t>(a.cache_len) |
+         reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.page_table)) & 3u)
+        return fail(ATTN_EINVAL, "%s: cu_seqlens, cache_len, positions and page_table must be 4-byte aligned", who);
+    if (append && a.n_seq > 1 && (a.table_stride < 0 || a.table_stride > kMaxStride / a.n_seq))
+        return fail(ATTN_EINVAL, "%s: table_stride %lld is negative or too large", who, a.table_stride);
+    // views: q, k, v, q_out, k_out
+    const void *ptrs[5] = {a.q, a.H_kv ? a.k : nullptr, append ? a.v : nullptr, a.q_out, a.H_kv ? a.k_out : nullptr};
+    const int heads[5] = {a.H, a.H_kv, a.H_kv, a.H, a.H_kv};
+    const char *names[5] = {"q", "k", "v", "q_out", "k_out"};
+    const long long vec = 16 / esz;
+    Rows rows[5];
+    long long st[5][2];
+    // pairs side by side need whole units only, halves also whole units of pairs
+    bool wide = (a.interleaved || (a.rotary_dim / 2) % vec == 0) && aligned16(a.q_weight) && aligned16(a.k_weight);
+    for (int i = 0; i < 5; ++i) {
+        st[i][0] = strides ? strides[2 * i] : static_cast<long long>(heads[i]) * a.D;
+        st[i][1] = strides ? strides[2 * i + 1] : a.D;
+        rows[i] = make_rows(ptrs[i], a.T, heads[i], st[i][0], st[i][1], a.D, esz);
+        if (!ptrs[i]) continue;
+        if (!rows_distinct(rows[i]))
+            return fail(ATTN_EINVAL, "%s: the rows of %s overlap (strides %lld, %lld)", who, names[i], st[i][0], st[i][1]);
+        st[i][0] = rows[i].so / esz;
+        st[i][1] = rows[i].si / esz;
+        wide = wide && aligned16(ptrs[i]) && st[i][0] % vec == 0 && st[i][1] % vec == 0;
+    }
+    // an output may be its own input (in place); any other overlap is an error
+    for (int o = 3; o < 5; ++o) {
+        for (int i = 0; i < 5; ++i) {
+            if (i == o || (i < 3 && i == o - 3 && same_rows(rows[i], rows[o]))) continue;
+            if (rows_overlap(rows[o], rows[i])) return fail(ATTN_EINVAL, "%s: %s overlaps %s", who, names[o], names[i]);
+        }
+        for (const void *w : {a.q_weight, a.k_weight})
+            if (w && rows_overlap(rows[o], make_rows(w, 1, 1, a.D, a.D, a.D, esz)))
+                return fail(ATTN_EINVAL, "%s: %s overlaps a weight", who, names[o]);
+    }
+    if (append) {
+        Pool pool[2];
+        for (int i = 0; i < 2; ++i) {
+            const char *name = i ? "vpages" : "kpages";
+            if (!make_pool(&pool[i], i ? a.vpages : a.kpages, 1, 0, a.n_pages, a.H_kv, a.P, a.D, esz,
+                           strides ? strides + 10 + 3 * i : nullptr))
+                return fail(ATTN_EINVAL, "%s: a stride of %s is negative or too large", who, name);
+            if (!pool_distinct(pool[i])) return fail(ATTN_EINVAL, "%s: the rows of %s overlap", who, name);
+            const Rows pr = make_rows(pool[i].p, 1, 1, 1, 1, static_cast<long long>(pool_extent(pool[i])), 1);
+            for (int x = 0; x < 5; ++x)
+                if (!pool_empty(pool[i]) && rows_overlap(pr, rows[x]))
+                    return fail(ATTN_EINVAL, "%s: %s overlaps %s", who, names[x], name);
+            if (!pool_empty(pool[i]) &&
+                ((a.q_weight && overlaps(a.q_weight, static_cast<size_t>(a.D * esz), pool[i].p, pool_extent(pool[i]))) ||
+                 (a.k_weight && overlaps(a.k_weight, static_cast<size_t>(a.D * esz), pool[i].p, pool_extent(pool[i])))))
+                return fail(ATTN_EINVAL, "%s: a weight overlaps %s", who, name);
+            if (!pool_empty(pool[i]))
+                wide = wide && aligned16(pool[i].p) && pool[i].st[1] % 16 == 0 && pool[i].st[2] % 16 == 0 && pool[i].st[3] % 16 == 0;
+        }
+        if (pools_overlap(pool[0], pool[1])) return fail(ATTN_EINVAL, "%s: kpages overlaps vpages", who);
+        a.k_ps = pool[0].st[1] / esz, a.k_hs = pool[0].st[2] / esz, a.k_rs = pool[0].st[3] / esz;
+        a.v_ps = pool[1].st[1] / esz, a.v_hs = pool[1].st[2] / esz, a.v_rs = pool[1].st[3] / esz;
+        if (a.n_seq == 1) a.table_stride = 0;
+    }
+    a.q_ts = st[0][0], a.q_hs = st[0][1], a.k_ts = st[1][0], a.kt_hs = st[1][1], a.v_ts = st[2][0], a.vt_hs = st[2][1];
+    a.qo_ts = st[3][0], a.qo_hs = st[3][1], a.ko_ts = st[4][0], a.ko_hs = st[4][1];
+    for (int p = 0; p < a.rotary_dim / 2; ++p) a.turns[p] = rope_turns(freqs[p]);
+    a.n_sm = num_sms();
+    a.stream = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_norm_rope(a, dtype == ATTN_F32, wide);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, who);
+}
+
+ATTN_API int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_out, int T, int H, int H_kv, int D,
+                            const long long *strides, const int32_t *positions, const double *freqs, int rotary_dim,
+                            int interleaved, float mscale, const void *q_weight, const void *k_weight, float eps, int dtype,
+                            void *stream) {
+    NormRopeArgs a{};
+    a.q = q, a.k = k, a.q_out = q_out, a.k_out = k_out, a.q_weight = q_weight, a.k_weight = k_weight;
+    a.T = T, a.H = H, a.H_kv = H_kv, a.D = D, a.positions = positions;
+    a.rotary_dim = rotary_dim, a.interleaved = interleaved, a.mscale = mscale, a.eps = eps;
+    // strides holds q, k, q_out, k_out; norm_rope_impl takes v between them
+    long long st[16] = {};
+    if (strides) {
+        for (int i = 0; i < 4; ++i) st[i] = strides[i];
+        for (int i = 0; i < 4; ++i) st[6 + i] = strides[4 + i];
+    }
+    return norm_rope_impl("attn_norm_rope", a, strides ? st : nullptr, freqs, 0, dtype, stream);
+}
+
+ATTN_API int attn_rope_append_paged(const void *q, const void *k, const void *v, void *q_out, void *k_out, void *kpages,
+                                    void *vpages, int T, int H, int H_kv, int D, const long long *strides, int n_pages,
+                                    int page_size, const int32_t *page_table, int max_pages, long long table_stride,
+                                    const int32_t *cu_seqlens, const int32_t *cache_len, int n_seq, const int32_t *positions,
+                                    const double *freqs, int rotary_dim, int interleaved, float mscale, const void *q_weight,
+                                    const void *k_weight, float eps, int dtype, void *stream) {
+    NormRopeArgs a{};
+    a.append = 1;
+    a.q = q, a.k = k, a.v = v, a.q_out = q_out, a.k_out = k_out, a.kpages = kpages, a.vpages = vpages;
+    a.q_weight = q_weight, a.k_weight = k_weight;
+    a.T = T, a.H = H, a.H_kv = H_kv, a.D = D, a.n_pages = n_pages, a.P = page_size, a.n_seq = n_seq;
+    a.page_table = page_table, a.table_stride = table_stride;
+    a.cu_seqlens = cu_seqlens, a.cache_len = cache_len, a.positions = positions;
+    a.rotary_dim = rotary_dim, a.interleaved = interleaved, a.mscale = mscale, a.eps = eps;
+    return norm_rope_impl("attn_rope_append_paged", a, strides, freqs, max_pages, dtype, stream);
+}
+
 ATTN_API int attn_device_status(void *stream) {
     g_last_error[0] = '\0';
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));

@@ -1,5 +1,5 @@
 // Python's usual calls of the serving entry points (attn_fwd_packed, attn_rope,
-// attn_rope_append, attn_decode_tree), from tensors to the C ABI in one crossing:
+// attn_rope_append, attn_decode_tree and those of a paged cache), from tensors to the C ABI in one crossing:
 // outputs are made here and the workspace comes from torch's caching allocator.
 // The usual call is one whose arguments are all in order: plain strided tensors on
 // the current device.  For any other a function returns None, and the package's
@@ -38,6 +38,8 @@ decltype(&attn_decode_tree) f_tree;
 decltype(&attn_decode_tree_workspace) f_tree_workspace;
 decltype(&attn_fwd_paged) f_paged;
 decltype(&attn_fwd_paged_workspace) f_paged_workspace;
+decltype(&attn_norm_rope) f_norm_rope;
+decltype(&attn_rope_append_paged) f_append_paged;
 
 bool small(int64_t n) { return n >= 0 && n <= INT_MAX; }
 
@@ -101,6 +103,16 @@ struct Call {
     bool table(const at::Tensor* t) const {
         return t && t->scalar_type() == at::kInt && t->device() == device && t->dim() == 2 && t->stride(1) == 1 &&
                small(t->size(0)) && small(t->size(1));
+    }
+
+    // A (D,) weight in the call's dtype, or None.
+    bool weight(PyObject* o, int64_t D, const void** p) const {
+        *p = nullptr;
+        if (o == Py_None) return true;
+        const at::Tensor* t = cuda_tensor(o);
+        if (!shares(t) || t->dim() != 1 || t->size(0) != D || !t->is_contiguous()) return false;
+        *p = t->data_ptr();
+        return true;
     }
 
     // An int32 tensor of the given shape, or None.
@@ -427,6 +439,83 @@ PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, q_out, k_out, interleaved, mscale)
+PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor *q, *k = nullptr;
+    Call c;
+    long long st[8] = {};
+    if (n != 11 || !(q = cuda_tensor(a[0])) || !c.of(q, 3)) Py_RETURN_NONE;
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
+    st[0] = q->stride(0), st[1] = q->stride(1);
+    const int* pos;
+    const double* freqs;
+    const void *wq, *wk;
+    int rotary_dim, interleaved;
+    float eps, mscale;
+    if (a[2] == Py_None || !c.ints(a[2], {T}, &pos) || !frequencies(a[3], D, &freqs, &rotary_dim) ||
+        !c.weight(a[4], D, &wq) || !c.weight(a[5], D, &wk) || !number(a[6], kNone, &eps) || !flag(a[9], &interleaved) ||
+        !number(a[10], kNone, &mscale))
+        Py_RETURN_NONE;
+    int64_t H_kv = 0;
+    if (a[1] != Py_None) {
+        k = cuda_tensor(a[1]);
+        if (!c.rows(k, T, D, st + 2)) Py_RETURN_NONE;
+        H_kv = k->size(1);
+    } else if (a[8] != Py_None || a[5] != Py_None) {
+        Py_RETURN_NONE;
+    }
+    Out q_out, k_out;
+    if (!q_out.rows(a[7], c, T, H, D, st + 4) || (k && !k_out.rows(a[8], c, T, H_kv, D, st + 6))) Py_RETURN_NONE;
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.device.index());
+    const int rc = unlocked([&] {
+        return f_norm_rope(q->data_ptr(), k ? k->data_ptr() : nullptr, q_out.ptr(), k_out.ptr(), T, H, H_kv, D, st, pos, freqs,
+                           rotary_dim, interleaved, mscale, wq, wk, eps, c.code, stream);
+    });
+    if (rc) Py_RETURN_NONE;
+    return k ? pair(q_out.object(), k_out.object()) : q_out.object();
+    END_HANDLE_TH_ERRORS
+}
+
+// append_paged(q, k, v, kpages, vpages, page_table, freqs, cache_len, cu_seqlens, positions, q_weight, k_weight, eps,
+//              q_out, k_out, interleaved, mscale)
+PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor *q, *k, *v, *kp, *vp, *table;
+    Call c;
+    long long st[16] = {};
+    if (n != 17 || !(q = cuda_tensor(a[0])) || !c.of(q, 3) || !(k = cuda_tensor(a[1])) || !(v = cuda_tensor(a[2])) ||
+        !(kp = cuda_tensor(a[3])) || !(vp = cuda_tensor(a[4])) || !(table = cuda_tensor(a[5])))
+        Py_RETURN_NONE;
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
+    st[0] = q->stride(0), st[1] = q->stride(1);
+    if (!c.rows(k, T, D, st + 2) || !c.rows(v, T, D, st + 4) || !c.pages(kp, vp, D, st + 10) || !c.table(table)) Py_RETURN_NONE;
+    const int64_t H_kv = k->size(1), n_pages = kp->size(0), P = kp->size(2), n_seq = table->size(0), M = table->size(1);
+    const int *cu, *cache_len, *pos;
+    const double* freqs;
+    const void *wq, *wk;
+    int rotary_dim, interleaved;
+    float eps, mscale;
+    if (v->size(1) != H_kv || kp->size(1) != H_kv || n_seq == 0 || !frequencies(a[6], D, &freqs, &rotary_dim) ||
+        !c.ints(a[7], {n_seq}, &cache_len) || !c.ints(a[8], {n_seq + 1}, &cu) || !c.ints(a[9], {T}, &pos) ||
+        !c.weight(a[10], D, &wq) || !c.weight(a[11], D, &wk) || !number(a[12], kNone, &eps) || !flag(a[15], &interleaved) ||
+        !number(a[16], kNone, &mscale))
+        Py_RETURN_NONE;
+    Out q_out, k_out;
+    const bool turned = a[14] != Py_None;
+    if (!q_out.rows(a[13], c, T, H, D, st + 6) || (turned && !k_out.rows(a[14], c, T, H_kv, D, st + 8))) Py_RETURN_NONE;
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.device.index());
+    const int rc = unlocked([&] {
+        return f_append_paged(q->data_ptr(), k->data_ptr(), v->data_ptr(), q_out.ptr(), k_out.ptr(), kp->data_ptr(),
+                              vp->data_ptr(), T, H, H_kv, D, st, n_pages, P, static_cast<const int*>(table->data_ptr()), M,
+                              table->stride(0), cu, cache_len, n_seq, pos, freqs, rotary_dim, interleaved, mscale, wq, wk, eps,
+                              c.code, stream);
+    });
+    if (rc) Py_RETURN_NONE;
+    return turned ? pair(q_out.object(), k_out.object()) : q_out.object();
+    END_HANDLE_TH_ERRORS
+}
+
 // bind(packed, packed_workspace, rope, rope_append, tree, tree_workspace): their addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* p[6];
@@ -448,20 +537,22 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// bind_paged(paged, paged_workspace)
+// bind_paged(paged, paged_workspace, norm_rope, append_paged)
 PyObject* bind_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* p[2];
-    if (n != 2) {
-        PyErr_SetString(PyExc_TypeError, "bind_paged takes two addresses");
+    void* p[4];
+    if (n != 4) {
+        PyErr_SetString(PyExc_TypeError, "bind_paged takes four addresses");
         return nullptr;
     }
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
         if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_paged: a null address");
             return nullptr;
         }
     f_paged = reinterpret_cast<decltype(f_paged)>(p[0]);
     f_paged_workspace = reinterpret_cast<decltype(f_paged_workspace)>(p[1]);
+    f_norm_rope = reinterpret_cast<decltype(f_norm_rope)>(p[2]);
+    f_append_paged = reinterpret_cast<decltype(f_append_paged)>(p[3]);
     Py_RETURN_NONE;
 }
 
@@ -478,6 +569,8 @@ PyMethodDef kMethods[] = {
     {"tree", fast(tree), METH_FASTCALL, nullptr},
     {"bind_paged", fast(bind_paged), METH_FASTCALL, nullptr},
     {"paged", fast(paged), METH_FASTCALL, nullptr},
+    {"norm_rope", fast(norm_rope), METH_FASTCALL, nullptr},
+    {"append_paged", fast(append_paged), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

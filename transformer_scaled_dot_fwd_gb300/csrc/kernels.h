@@ -252,6 +252,30 @@ struct RopeArgs {
 // wide: every address, stride and rotary_dim / 2 allows 16-byte accesses
 cudaError_t launch_rope(const RopeArgs &a, bool f32, bool wide);
 
+// RMS norm of head rows, rotary positions, and their append to pages (attn_norm_rope,
+// attn_rope_append_paged).  Rows are (token, head) with element strides.
+struct NormRopeArgs {
+    const void *q, *k, *v;      // (T, H | H_kv, D); v only to append
+    void *q_out, *k_out;        // k_out may be nullptr to append
+    const void *q_weight, *k_weight;  // (D,) or nullptr: the tensor is turned as it is
+    void *kpages, *vpages;      // (n_pages, H_kv, P, D), element strides below
+    const int32_t *page_table;  // device, rows table_stride apart
+    const int32_t *cu_seqlens;  // device int32[n_seq + 1] or nullptr (T / n_seq tokens each)
+    const int32_t *cache_len;   // device int32[n_seq] or nullptr (max_len)
+    const int32_t *positions;   // device int32[T] or nullptr (the cache row)
+    long long q_ts, q_hs, k_ts, kt_hs, v_ts, vt_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+    long long k_ps, k_hs, k_rs, v_ps, v_hs, v_rs, table_stride;
+    int T, H, H_kv, D, n_seq, P, n_pages, max_len;
+    int append;                 // 0: no cache
+    int rotary_dim, interleaved;
+    float mscale, eps;
+    int n_sm;
+    cudaStream_t stream;
+    uint64_t turns[64];         // w_p / 2 pi as a fraction of 2^64
+};
+// wide: every address, stride and pair allows 16-byte accesses
+cudaError_t launch_norm_rope(const NormRopeArgs &a, bool f32, bool wide);
+
 // Size of the library-static decode scratch used by attn_decode_noalloc.
 constexpr size_t kDecodeNoAllocScratchBytes = 32u << 20;
 
