@@ -578,8 +578,8 @@ ATTN_API int attn_norm_rope(const void *q, const void *k, void *q_out, void *k_o
  * j = L_s - n_s + i, which is also its position unless `positions` says otherwise, and
  * goes to row j % page_size of page page_table[s][j / page_size].  A token whose j is
  * negative, or whose entry of the table is outside [0, n_pages), is turned but not cached.
- * Tokens outside every sequence are neither read nor written anywhere; other rows of the
- * pages stay as they were.  Two tokens of a call must not have the same row of a page.
+ * Nothing is written for tokens outside every sequence; other rows of the pages stay as
+ * they were.  Two tokens of a call must not have the same row of a page.
  *
  *   q, q_out  (T, H, D) rows; k, v  (T, H_kv, D) rows, H_kv >= 1
  *   k_out     NULL, or (T, H_kv, D) rows: the turned keys once more, token by token
@@ -597,6 +597,82 @@ ATTN_API int attn_rope_append_paged(const void *q, const void *k, const void *v,
                                     const int32_t *cu_seqlens, const int32_t *cache_len, int n_seq, const int32_t *positions,
                                     const double *freqs, int rotary_dim, int interleaved, float mscale, const void *q_weight,
                                     const void *k_weight, float eps, int dtype, void *stream);
+
+/*
+ * attn_pages_step -- the next table of pages: sequences grow, are cut back, fork, end and
+ * begin, without the host.
+ *
+ * Row b of the new table goes on from row parents[b] of the old one (several rows may have
+ * one parent: they fork; a parent outside [0, n_seq) starts an empty sequence; a row that
+ * nobody goes on from has ended).  It is to hold new_len[b] tokens, of which it keeps the
+ * first keep = min(cache_len[parents[b]], new_len[b]) of its parent's:
+ *   - The keep / page_size full pages are shared with whoever else holds them.
+ *   - A partly filled page, to whose rows behind `keep` the sequence will append, has one
+ *     holder: the lowest row that keeps it so, unless some row keeps it full or it is
+ *     pinned.  Every other row gets a new page and asks for a copy of its rows.
+ *   - Entries up to ceil(new_len[b] / page_size) that are missing, or are no pages, become
+ *     new pages; entries from there on are -1.
+ * New pages are those that no row of the new table keeps and that are not pinned, the
+ * lowest first, given out in the order of rows and of entries.  A page that ends with its
+ * sequence can be given out in the same call.  Where they run out, entries are -1 (tokens
+ * there are not cached, their keys read as zeros) and free_pages is negative; a later call
+ * asks for them again.
+ *
+ *   page_table  device int32 (n_seq, max_pages), rows table_stride apart
+ *   cache_len   device int32[n_seq], each clamped to [0, max_pages * page_size], or NULL
+ *               (every row full)
+ *   parents     device int32[n_out], or NULL: row b goes on from row b (n_out = n_seq)
+ *   new_len     device int32[n_out], clamped like cache_len, or NULL: the parent's length
+ *   pinned      device int32[n_pages] or NULL: pages with a value other than 0 are held
+ *               outside the table too (a cache of prefixes): never given out, never written
+ *   table_out   (n_out, max_pages), rows out_stride apart, written; len_out (n_out): the
+ *               clamped new_len; copies (n_out, 3): page copied from, page copied to and
+ *               rows, or -1, -1, 0 where the row needs none (for attn_pages_copy, before
+ *               anything is appended); free_pages (1): free pages left, or minus those
+ *               missing.  Outputs must not overlap inputs.
+ *   workspace   device memory of attn_pages_workspace(n_out, n_pages) bytes, 16-byte
+ *               aligned; rules as in attn_fwd_packed
+ *
+ * The same call gives the same table every time.
+ */
+ATTN_API int attn_pages_step(const int32_t *page_table, const int32_t *cache_len, int n_seq, int max_pages, long long table_stride,
+                             int n_pages, int page_size, const int32_t *parents, const int32_t *new_len,
+                             const int32_t *pinned, int n_out, int32_t *table_out, long long out_stride, int32_t *len_out,
+                             int32_t *copies, int32_t *free_pages, void *workspace, long long workspace_bytes,
+                             void *stream);
+/* Bytes of workspace of attn_pages_step and attn_pages_compact (n_out = n_seq there). */
+ATTN_API long long attn_pages_workspace(int n_out, int n_pages);
+
+/*
+ * attn_pages_compact -- moves the pages held together at the front of the pool.
+ *
+ * With n pages held (by the rows up to cache_len, or pinned), the k-th lowest page from n
+ * on that a row holds and that is not pinned becomes the k-th lowest free page below n, in
+ * every row that holds it.  table_out names the new places (-1 behind a row's pages and for
+ * entries that are no pages); copies ((n_pages + 1) / 2, 3) lists page copied from, page
+ * copied to and page_size, then -1, -1, 0; free_pages (1) is n_pages - n.  Arguments
+ * as in attn_pages_step.
+ */
+ATTN_API int attn_pages_compact(const int32_t *page_table, const int32_t *cache_len, int n_seq, int max_pages,
+                                long long table_stride, int n_pages, int page_size, const int32_t *pinned, int32_t *table_out,
+                                long long out_stride, int32_t *copies, int32_t *free_pages, void *workspace,
+                                long long workspace_bytes, void *stream);
+
+/*
+ * attn_pages_copy -- copies of pages, keys and values of all layers: for each (from, to,
+ * rows) of `copies` the first `rows` rows of page `to` become those of page `from`.
+ *
+ *   kpages, vpages  (layers, n_pages, H_kv, page_size, D) pages, any strides; not
+ *             overlapping each other
+ *   strides   NULL (contiguous), or HOST int64[8]: layer, page, head and row of kpages and
+ *             of vpages in elements.  16-byte aligned pointers and strides are the fast case.
+ *   copies    device int32 (n_copies, 3).  Pairs with a page outside [0, n_pages) are
+ *             passed over, rows are clamped to [0, page_size].  A page that one pair writes
+ *             must not be read or written by another (the lists of attn_pages_step and
+ *             attn_pages_compact are such).
+ */
+ATTN_API int attn_pages_copy(void *kpages, void *vpages, int layers, int n_pages, int H_kv, int page_size, int D,
+                             const long long *strides, const int32_t *copies, int n_copies, int dtype, void *stream);
 
 /*
  * attn_device_status -- synchronise `stream`, then report and clear the

@@ -8,6 +8,8 @@ no CPU path: when the library is missing, every call raises.
     attn_fwd(q, k, v, out=None, scale=None, causal=False, kv_len=None, stream=None)
     attn_fwd_packed(q, k, v, cu_seqlens, scale=None, causal=False, return_lse=False, ...)
     attn_rope(q, k, positions, freqs, ...), attn_rope_append(q, k, v, kcache, vcache, freqs, ...)
+    attn_fwd_paged(q, kpages, vpages, page_table, cache_len, ...), attn_rope_append_paged(...), attn_norm_rope(...)
+    attn_pages_step(page_table, cache_len, n_pages, page_size, ...), attn_pages_compact(...), attn_pages_copy(...)
     attn_decode(q, kcache, vcache, out=None, kv_len=None, stream=None)
     attn_decode_tree(q, kcache, vcache, parents, cache_len=None, draft_len=None, ...)
 """
@@ -59,6 +61,10 @@ SIGNATURES = {
     "attn_norm_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _f, _vp, _vp, _f, _i, _vp]),
     "attn_rope_append_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _vp, _i, _ll, _vp, _vp, _i,
                                     _vp, _vp, _i, _i, _f, _vp, _vp, _f, _i, _vp]),
+    "attn_pages_step": (_i, [_vp, _vp, _i, _i, _ll, _i, _i, _vp, _vp, _vp, _i, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _vp]),
+    "attn_pages_compact": (_i, [_vp, _vp, _i, _i, _ll, _i, _i, _vp, _vp, _ll, _vp, _vp, _vp, _ll, _vp]),
+    "attn_pages_copy": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _i, _vp]),
+    "attn_pages_workspace": (_ll, [_i, _i]),
     "attn_device_status": (_i, [_vp]),
     "attn_last_error": (ctypes.c_char_p, []),
     "attn_release": (None, []),
@@ -362,6 +368,7 @@ class _NoBinding:
         return None
 
     packed = rope = rope_append = tree = paged = norm_rope = append_paged = _none
+    pages_step = pages_compact = pages_copy = _none
 
 
 def _load_native():
@@ -384,7 +391,8 @@ def _load_native():
         "attn_fwd_packed", "attn_fwd_packed_workspace", "attn_rope", "attn_rope_append", "attn_decode_tree",
         "attn_decode_tree_workspace")))
     module.bind_paged(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in (
-        "attn_fwd_paged", "attn_fwd_paged_workspace", "attn_norm_rope", "attn_rope_append_paged")))
+        "attn_fwd_paged", "attn_fwd_paged_workspace", "attn_norm_rope", "attn_rope_append_paged",
+        "attn_pages_step", "attn_pages_compact", "attn_pages_copy", "attn_pages_workspace")))
     _native = module
     return module
 
@@ -873,6 +881,121 @@ def attn_rope_append_paged(q, k, v, kpages, vpages, page_table, freqs, cache_len
     return q_out if k_out is None else (q_out, k_out)
 
 
+def _given(out, shapes, device):
+    """``out``, int32 tensors of the given shapes, or new ones."""
+    torch = _torch()
+    if out is None:
+        return [torch.empty(s, dtype=torch.int32, device=device) for s in shapes]
+    out = list(out)
+    if len(out) != len(shapes):
+        raise ValueError(f"out must hold {len(shapes)} tensors")
+    for t, s in zip(out, shapes):
+        if not (t.dtype == torch.int32 and t.device == device and t.shape == s and t.is_contiguous()):
+            raise ValueError(f"out must hold contiguous int32 tensors of shapes {', '.join(str(tuple(s)) for s in shapes)} on "
+                             "page_table's device")
+    return out
+
+
+def attn_pages_step(page_table, cache_len, n_pages: int, page_size: int, parents=None, new_len=None, pinned=None, out=None,
+                    stream=None):
+    """The next table of pages.  Row b goes on from row ``parents[b]`` of ``page_table``
+    int32 (sequences, max_pages) (itself by default; an index that is no row starts an
+    empty sequence) and is to hold ``new_len[b]`` tokens (by default its parent's
+    ``cache_len``): pages beyond are dropped, missing ones are taken from those that no row
+    holds and that are not ``pinned`` int32 (n_pages,).  Full pages are shared, a partly
+    filled one has one holder and is copied for the others.  Returns ``(table, lengths,
+    copies, free)``: new tensors, or the four of ``out``; ``copies`` (rows, 3) is for
+    attn_pages_copy, ``free`` (1,) counts the free pages left (negative: missing).
+    See include/attn.h.
+    """
+    if stream is None:
+        done = (_native or _load_native()).pages_step(page_table, cache_len, n_pages, page_size, parents, new_len, pinned, out)
+        if done is not None:
+            return done
+    torch = _torch()
+    device = page_table.device
+    if not page_table.is_cuda:
+        raise ValueError("page_table must be a CUDA tensor")
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
+            return attn_pages_step(page_table, cache_len, n_pages, page_size, parents, new_len, pinned, out)
+    n_seq, M, ts, table = _table(page_table, device)
+    n_out = n_seq if parents is None else parents.shape[0]
+    cl = _ints("cache_len", cache_len, (n_seq,), device)
+    par = _ints("parents", parents, (n_out,), device)
+    new = _ints("new_len", new_len, (n_out,), device)
+    pin = _ints("pinned", pinned, (n_pages,), device)
+    r = _given(out, [(n_out, M), (n_out,), (n_out, 3), (1,)], device)
+    need = lib().attn_pages_workspace(n_out, n_pages)
+    ws = _workspace(need, device)
+    rc = lib().attn_pages_step(table, cl, n_seq, M, ts, n_pages, page_size, par, new, pin, n_out, r[0].data_ptr(), M,
+                               r[1].data_ptr(), r[2].data_ptr(), r[3].data_ptr(), _ptr(ws), max(need, 0), _current(device))
+    if rc:
+        _check(rc)
+    return tuple(r)
+
+
+def attn_pages_compact(page_table, cache_len, n_pages: int, page_size: int, pinned=None, out=None, stream=None):
+    """Moves the pages that the rows of ``page_table`` hold together at the front of the
+    pool (``pinned`` ones stay where they are).  Returns ``(table, copies, free)``: new
+    tensors, or the three of ``out``; ``copies`` ((n_pages + 1) // 2, 3) is for
+    attn_pages_copy, ``free`` (1,) counts the free pages.  See include/attn.h.
+    """
+    if stream is None:
+        done = (_native or _load_native()).pages_compact(page_table, cache_len, n_pages, page_size, pinned, out)
+        if done is not None:
+            return done
+    torch = _torch()
+    device = page_table.device
+    if not page_table.is_cuda:
+        raise ValueError("page_table must be a CUDA tensor")
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
+            return attn_pages_compact(page_table, cache_len, n_pages, page_size, pinned, out)
+    n_seq, M, ts, table = _table(page_table, device)
+    cl = _ints("cache_len", cache_len, (n_seq,), device)
+    pin = _ints("pinned", pinned, (n_pages,), device)
+    r = _given(out, [(n_seq, M), ((n_pages + 1) // 2, 3), (1,)], device)
+    need = lib().attn_pages_workspace(n_seq, n_pages)
+    ws = _workspace(need, device)
+    rc = lib().attn_pages_compact(table, cl, n_seq, M, ts, n_pages, page_size, pin, r[0].data_ptr(), M, r[1].data_ptr(),
+                                  r[2].data_ptr(), _ptr(ws), max(need, 0), _current(device))
+    if rc:
+        _check(rc)
+    return tuple(r)
+
+
+def attn_pages_copy(kpages, vpages, copies, stream=None) -> None:
+    """Copies pages within both pools, (n_pages, H_kv, page_size, D) or (layers, n_pages,
+    H_kv, page_size, D) of any strides: for each (from, to, rows) of ``copies`` int32 (n, 3)
+    the first ``rows`` rows of page ``to`` become those of page ``from``; pairs with an index
+    that is no page are passed over.  See include/attn.h.
+    """
+    if stream is None and (_native or _load_native()).pages_copy(kpages, vpages, copies):
+        return
+    torch = _torch()
+    device = kpages.device
+    if not kpages.is_cuda:
+        raise ValueError("kpages must be a CUDA tensor")
+    if stream is not None or device.index != torch.cuda.current_device():
+        with _elsewhere(device, stream):
+            return attn_pages_copy(kpages, vpages, copies)
+    code = _dtype_code(kpages)
+    layered = kpages.dim() == 5
+    D = kpages.shape[-1]
+    n_pages, H_kv, P, st = _pages(kpages, vpages, kpages.dtype, device, D, layered)
+    layers = kpages.shape[0] if layered else 1
+    if not layered:
+        st = (0, *st[:3], 0, *st[3:])
+    if not (copies.dtype == torch.int32 and copies.device == device and copies.dim() == 2 and copies.shape[1] == 3
+            and copies.is_contiguous()):
+        raise ValueError("copies must be a contiguous int32 tensor of shape (n, 3) on the pages' device")
+    rc = lib().attn_pages_copy(kpages.data_ptr(), vpages.data_ptr(), layers, n_pages, H_kv, P, D, _LL8(*st),
+                               copies.data_ptr(), copies.shape[0], code, _current(device))
+    if rc:
+        _check(rc)
+
+
 def attn_device_status(stream=None) -> None:
     """Synchronise the stream and raise AttnError if a kernel reported a timed-out
     wait (ATTN_ETIMEOUT) or a shared prefill work counter (ATTN_ECONFLICT)."""
@@ -891,6 +1014,7 @@ def attn_release() -> None:
 __all__ = [
     "attn_fwd", "attn_fwd_chunked", "attn_fwd_debug", "attn_fwd_host", "attn_decode", "attn_decode_noalloc", "attn_decode_splits", "attn_fwd_packed", "attn_decode_tree",
     "attn_fwd_paged", "attn_norm_rope", "attn_rope_append_paged",
+    "attn_pages_step", "attn_pages_compact", "attn_pages_copy",
     "attn_rope",
     "attn_rope_append", "attn_rope_frequencies", "attn_device_status", "attn_release",
     "attn_last_error", "attn_selftest_wait_timeout", "lib", "AttnError", "SIGNATURES", "LIB_PATH",

@@ -1433,6 +1433,151 @@ ATTN_API int attn_rope_append_paged(const void *q, const void *k, const void *v,
     return norm_rope_impl("attn_rope_append_paged", a, strides, freqs, max_pages, dtype, stream);
 }
 
+// ------------------------------------------------------------ the table of pages
+
+static long long pages_workspace(int n_out, int n_pages) {
+    // held, pins; first or move; need, stays; the list with its count in front
+    const long long words = (static_cast<long long>(n_pages) + 31) / 32;
+    return (2 * words + n_pages + 2LL * n_out + n_pages + 1) * 4;
+}
+
+ATTN_API long long attn_pages_workspace(int n_out, int n_pages) {
+    return n_out < 0 || n_pages < 0 ? ATTN_EINVAL : pages_workspace(n_out, n_pages);
+}
+
+// Shared by attn_pages_step and attn_pages_compact.
+static int pages_impl(const char *who, PagesArgs a, bool step, void *workspace, long long workspace_bytes, void *stream) {
+    g_last_error[0] = '\0';
+    if (a.n_seq < 0 || a.n_out < 0 || a.max_pages < 0 || a.n_pages < 0)
+        return fail(ATTN_EINVAL, "%s: the numbers of sequences and pages must not be negative", who);
+    if (a.P < 1) return fail(ATTN_EINVAL, "%s: a page must have rows (got %d)", who, a.P);
+    if (static_cast<long long>(a.max_pages) * a.P > 0x7fffffffLL)
+        return fail(ATTN_EINVAL, "%s: %d pages of %d rows are too many for a sequence", who, a.max_pages, a.P);
+    if (!a.parents && a.n_out != a.n_seq)
+        return fail(ATTN_EINVAL, "%s: without parents there are as many rows as before (got %d, %d)", who, a.n_out, a.n_seq);
+    // ranks and counts are kept in 32 bits
+    if (static_cast<long long>(a.n_out) * a.max_pages >= (1LL << 30) || a.n_pages >= 1 << 30)
+        return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    const bool entries = a.n_seq > 0 && a.max_pages > 0, out_entries = a.n_out > 0 && a.max_pages > 0;
+    if (!a.free_pages || (entries && !a.table) || (out_entries && !a.table_out) || (step && a.n_out > 0 && !a.len_out) ||
+        (a.n_copies > 0 && !a.copies))
+        return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
+    if (a.n_seq > 1 && (a.table_stride < 0 || a.table_stride > kMaxStride / a.n_seq))
+        return fail(ATTN_EINVAL, "%s: table_stride %lld is negative or too large", who, a.table_stride);
+    if (a.n_out > 1 && (a.out_stride < a.max_pages || a.out_stride > kMaxStride / a.n_out))
+        return fail(ATTN_EINVAL, "%s: out_stride %lld is below max_pages or too large", who, a.out_stride);
+    if (a.n_seq <= 1) a.table_stride = 0;
+    if (a.n_out <= 1) a.out_stride = 0;
+    const long long need = pages_workspace(a.n_out, a.n_pages);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace))
+        return fail(ATTN_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes (got %lld)", who, need,
+                    workspace ? workspace_bytes : 0LL);
+    const struct {
+        const void *p;
+        long long n;
+        const char *name;
+    } t[] = {
+        {a.table_out, out_entries ? (a.n_out - 1) * a.out_stride + a.max_pages : 0, "the new table"},
+        {a.len_out, a.n_out, "the new lengths"},
+        {a.copies, 3LL * a.n_copies, "copies"},
+        {a.free_pages, 1, "free_pages"},
+        {workspace, need / 4, "workspace"},
+        {a.table, entries ? (a.n_seq - 1) * a.table_stride + a.max_pages : 0, "page_table"},
+        {a.cache_len, a.n_seq, "cache_len"},
+        {a.parents, a.n_out, "parents"},
+        {a.new_len, a.n_out, "new_len"},
+        {a.pinned, a.n_pages, "pinned"},
+    };
+    for (int i = 0; i < 10; ++i) {
+        if (!t[i].p) continue;
+        if (reinterpret_cast<uintptr_t>(t[i].p) & 3u) return fail(ATTN_EINVAL, "%s: %s must be 4-byte aligned", who, t[i].name);
+        for (int j = 0; j < i && j < 5; ++j)
+            if (t[j].p && overlaps(t[i].p, static_cast<size_t>(t[i].n) * 4, t[j].p, static_cast<size_t>(t[j].n) * 4))
+                return fail(ATTN_EINVAL, "%s: %s overlaps %s", who, t[j].name, t[i].name);
+    }
+    a.words = (a.n_pages + 31) / 32;
+    a.held = static_cast<unsigned *>(workspace);
+    a.pins = a.held + a.words;
+    int32_t *rest = reinterpret_cast<int32_t *>(a.pins + a.words);
+    if (step)
+        a.first = rest;
+    else
+        a.move = rest;
+    a.need = rest + a.n_pages;
+    a.stays = a.need + a.n_out;
+    a.list = a.stays + a.n_out + 1;
+    a.stream = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = step ? launch_pages_step(a) : launch_pages_compact(a);
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, who);
+}
+
+ATTN_API int attn_pages_step(const int32_t *page_table, const int32_t *cache_len, int n_seq, int max_pages, long long table_stride,
+                             int n_pages, int page_size, const int32_t *parents, const int32_t *new_len,
+                             const int32_t *pinned, int n_out, int32_t *table_out, long long out_stride, int32_t *len_out,
+                             int32_t *copies, int32_t *free_pages, void *workspace, long long workspace_bytes,
+                             void *stream) {
+    PagesArgs a{};
+    a.table = page_table, a.cache_len = cache_len, a.parents = parents, a.new_len = new_len, a.pinned = pinned;
+    a.table_out = table_out, a.len_out = len_out, a.copies = copies, a.free_pages = free_pages;
+    a.table_stride = table_stride, a.out_stride = out_stride;
+    a.n_seq = n_seq, a.n_out = n_out, a.max_pages = max_pages, a.P = page_size, a.n_pages = n_pages, a.n_copies = n_out;
+    return pages_impl("attn_pages_step", a, true, workspace, workspace_bytes, stream);
+}
+
+ATTN_API int attn_pages_compact(const int32_t *page_table, const int32_t *cache_len, int n_seq, int max_pages,
+                                long long table_stride, int n_pages, int page_size, const int32_t *pinned, int32_t *table_out,
+                                long long out_stride, int32_t *copies, int32_t *free_pages, void *workspace,
+                                long long workspace_bytes, void *stream) {
+    PagesArgs a{};
+    a.table = page_table, a.cache_len = cache_len, a.pinned = pinned;
+    a.table_out = table_out, a.copies = copies, a.free_pages = free_pages;
+    a.table_stride = table_stride, a.out_stride = out_stride;
+    a.n_seq = a.n_out = n_seq, a.max_pages = max_pages, a.P = page_size, a.n_pages = n_pages, a.n_copies = (n_pages + 1) / 2;
+    return pages_impl("attn_pages_compact", a, false, workspace, workspace_bytes, stream);
+}
+
+ATTN_API int attn_pages_copy(void *kpages, void *vpages, int layers, int n_pages, int H_kv, int page_size, int D,
+                             const long long *strides, const int32_t *copies, int n_copies, int dtype, void *stream) {
+    g_last_error[0] = '\0';
+    const char *who = "attn_pages_copy";
+    if (layers < 0 || n_pages < 0 || H_kv < 1 || n_copies < 0)
+        return fail(ATTN_EINVAL, "%s: need layers >= 0, n_pages >= 0, H_kv >= 1, n_copies >= 0", who);
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return fail(ATTN_EINVAL, "%s: unknown dtype %d", who, dtype);
+    if (D <= 0) return fail(ATTN_EINVAL, "%s: D must be positive (got %d)", who, D);
+    if (D != 64 && D != 128) return fail(ATTN_EUNSUPPORTED, "%s: D = %d not supported (64 or 128)", who, D);
+    if (page_size < 1) return fail(ATTN_EINVAL, "%s: a page must have rows (got %d)", who, page_size);
+    if (static_cast<long long>(H_kv) * page_size >= (1LL << 30) || layers >= 1 << 30)
+        return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    if (layers == 0 || n_pages == 0 || n_copies == 0) return ATTN_OK;
+    if (!kpages || !vpages || !copies) return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
+    const long long esz = dtype == ATTN_BF16 ? 2 : 4;
+    if ((reinterpret_cast<uintptr_t>(kpages) | reinterpret_cast<uintptr_t>(vpages)) & static_cast<uintptr_t>(esz - 1))
+        return fail(ATTN_EINVAL, "%s: tensors must be aligned to their element size", who);
+    if (reinterpret_cast<uintptr_t>(copies) & 3u) return fail(ATTN_EINVAL, "%s: copies must be 4-byte aligned", who);
+    Pool pool[2];
+    bool wide = true;
+    for (int i = 0; i < 2; ++i) {
+        const char *name = i ? "vpages" : "kpages";
+        if (!make_pool(&pool[i], i ? vpages : kpages, layers, strides ? strides[4 * i] : 0, n_pages, H_kv, page_size, D, esz,
+                       strides ? strides + 4 * i + 1 : nullptr))
+            return fail(ATTN_EINVAL, "%s: a stride of %s is negative or too large", who, name);
+        if (!pool_distinct(pool[i])) return fail(ATTN_EINVAL, "%s: the rows of %s overlap", who, name);
+        if (overlaps(copies, static_cast<size_t>(n_copies) * 12, pool[i].p, pool_extent(pool[i])))
+            return fail(ATTN_EINVAL, "%s: copies overlaps %s", who, name);
+        wide = wide && aligned16(pool[i].p);
+        for (int x = 0; x < 4; ++x) wide = wide && pool[i].st[x] % 16 == 0;
+    }
+    if (pools_overlap(pool[0], pool[1])) return fail(ATTN_EINVAL, "%s: kpages overlaps vpages", who);
+    PagesCopyArgs a{};
+    a.k = {const_cast<char *>(pool[0].p), pool[0].st[0], pool[0].st[1], pool[0].st[2], pool[0].st[3]};
+    a.v = {const_cast<char *>(pool[1].p), pool[1].st[0], pool[1].st[1], pool[1].st[2], pool[1].st[3]};
+    a.copies = copies, a.n_copies = n_copies, a.layers = layers, a.n_pages = n_pages, a.H_kv = H_kv, a.P = page_size;
+    a.row_bytes = static_cast<int>(D * esz);
+    a.stream = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_pages_copy(a, wide, static_cast<int>(esz));
+    return e == cudaSuccess ? ATTN_OK : cuda_fail(e, who);
+}
+
 ATTN_API int attn_device_status(void *stream) {
     g_last_error[0] = '\0';
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));

@@ -40,6 +40,10 @@ decltype(&attn_fwd_paged) f_paged;
 decltype(&attn_fwd_paged_workspace) f_paged_workspace;
 decltype(&attn_norm_rope) f_norm_rope;
 decltype(&attn_rope_append_paged) f_append_paged;
+decltype(&attn_pages_step) f_pages_step;
+decltype(&attn_pages_compact) f_pages_compact;
+decltype(&attn_pages_copy) f_pages_copy;
+decltype(&attn_pages_workspace) f_pages_workspace;
 
 bool small(int64_t n) { return n >= 0 && n <= INT_MAX; }
 
@@ -516,6 +520,115 @@ PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A Python int that fits 32 bits.
+bool whole(PyObject* o, int64_t* x) {
+    if (!PyLong_CheckExact(o)) return false;
+    int overflow = 0;
+    *x = PyLong_AsLongLongAndOverflow(o, &overflow);
+    return !overflow && small(*x);
+}
+
+// int32 outputs, made here: the usual call gives none.
+template <size_t N>
+PyObject* tuple_of(at::Tensor (&t)[N]) {
+    PyObject* r = PyTuple_New(N);
+    for (size_t i = 0; r && i < N; ++i) {
+        PyObject* o = THPVariable_Wrap(std::move(t[i]));
+        if (!o) Py_CLEAR(r);
+        else PyTuple_SET_ITEM(r, i, o);
+    }
+    return r;
+}
+
+// A table on the current device, as the first argument of a call about pages.
+bool first_table(PyObject* o, const at::Tensor** t, Call* c) {
+    *t = cuda_tensor(o);
+    if (!*t) return false;
+    c->device = (*t)->device();
+    return c->device.index() == c10::cuda::current_device() && c->table(*t);
+}
+
+// pages_step(page_table, cache_len, n_pages, page_size, parents, new_len, pinned, out)
+PyObject* pages_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor* table;
+    Call c;
+    int64_t n_pages, P;
+    if (n != 8 || a[7] != Py_None || !first_table(a[0], &table, &c) || !whole(a[2], &n_pages) || !whole(a[3], &P)) Py_RETURN_NONE;
+    const int64_t n_seq = table->size(0), M = table->size(1);
+    int64_t n_out = n_seq;
+    if (a[4] != Py_None) {
+        const at::Tensor* p = cuda_tensor(a[4]);
+        if (!p || p->dim() != 1 || !small(p->size(0))) Py_RETURN_NONE;
+        n_out = p->size(0);
+    }
+    const int *cache_len, *parents, *new_len, *pinned;
+    if (!c.ints(a[1], {n_seq}, &cache_len) || !c.ints(a[4], {n_out}, &parents) || !c.ints(a[5], {n_out}, &new_len) ||
+        !c.ints(a[6], {n_pages}, &pinned))
+        Py_RETURN_NONE;
+    at::Tensor r[4] = {c.make({n_out, M}, at::kInt), c.make({n_out}, at::kInt), c.make({n_out, 3}, at::kInt), c.make({1}, at::kInt)};
+    const long long need = f_pages_workspace(n_out, n_pages);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.device.index());
+    Workspace ws(need, stream);
+    int* o[4];
+    for (int i = 0; i < 4; ++i) o[i] = static_cast<int*>(r[i].data_ptr());
+    const int rc = unlocked([&] {
+        return f_pages_step(static_cast<const int*>(table->data_ptr()), cache_len, n_seq, M, table->stride(0), n_pages, P,
+                            parents, new_len, pinned, n_out, o[0], M, o[1], o[2], o[3], ws.p, need, stream);
+    });
+    if (rc) Py_RETURN_NONE;
+    return tuple_of(r);
+    END_HANDLE_TH_ERRORS
+}
+
+// pages_compact(page_table, cache_len, n_pages, page_size, pinned, out)
+PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor* table;
+    Call c;
+    int64_t n_pages, P;
+    if (n != 6 || a[5] != Py_None || !first_table(a[0], &table, &c) || !whole(a[2], &n_pages) || !whole(a[3], &P)) Py_RETURN_NONE;
+    const int64_t n_seq = table->size(0), M = table->size(1);
+    const int *cache_len, *pinned;
+    if (!c.ints(a[1], {n_seq}, &cache_len) || !c.ints(a[4], {n_pages}, &pinned)) Py_RETURN_NONE;
+    at::Tensor r[3] = {c.make({n_seq, M}, at::kInt), c.make({(n_pages + 1) / 2, 3}, at::kInt), c.make({1}, at::kInt)};
+    const long long need = f_pages_workspace(n_seq, n_pages);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.device.index());
+    Workspace ws(need, stream);
+    int* o[3];
+    for (int i = 0; i < 3; ++i) o[i] = static_cast<int*>(r[i].data_ptr());
+    const int rc = unlocked([&] {
+        return f_pages_compact(static_cast<const int*>(table->data_ptr()), cache_len, n_seq, M, table->stride(0), n_pages, P,
+                               pinned, o[0], M, o[1], o[2], ws.p, need, stream);
+    });
+    if (rc) Py_RETURN_NONE;
+    return tuple_of(r);
+    END_HANDLE_TH_ERRORS
+}
+
+// pages_copy(kpages, vpages, copies): True when done
+PyObject* pages_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor *k, *v, *copies;
+    Call c;
+    if (n != 3 || !(k = cuda_tensor(a[0])) || !(v = cuda_tensor(a[1])) || !(copies = cuda_tensor(a[2])) ||
+        (k->dim() != 4 && k->dim() != 5) || !c.of(k, k->dim()) || !c.shares(v) || v->sizes() != k->sizes() ||
+        v->stride(-1) != 1 || copies->scalar_type() != at::kInt || copies->device() != c.device || copies->dim() != 2 ||
+        copies->size(1) != 3 || !copies->is_contiguous() || !small(copies->size(0)))
+        Py_RETURN_NONE;
+    const int l = k->dim() == 5;
+    long long st[8] = {};
+    for (int i = 1 - l; i < 4; ++i) st[i] = k->stride(i - 1 + l), st[4 + i] = v->stride(i - 1 + l);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(c.device.index());
+    const int rc = unlocked([&] {
+        return f_pages_copy(k->data_ptr(), v->data_ptr(), l ? k->size(0) : 1, k->size(l), k->size(l + 1), k->size(l + 2),
+                            k->size(l + 3), st, static_cast<const int*>(copies->data_ptr()), copies->size(0), c.code, stream);
+    });
+    if (rc) Py_RETURN_NONE;
+    Py_RETURN_TRUE;
+    END_HANDLE_TH_ERRORS
+}
+
 // bind(packed, packed_workspace, rope, rope_append, tree, tree_workspace): their addresses
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* p[6];
@@ -537,14 +650,14 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// bind_paged(paged, paged_workspace, norm_rope, append_paged)
+// bind_paged(paged, paged_workspace, norm_rope, append_paged, pages_step, pages_compact, pages_copy, pages_workspace)
 PyObject* bind_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* p[4];
-    if (n != 4) {
-        PyErr_SetString(PyExc_TypeError, "bind_paged takes four addresses");
+    void* p[8];
+    if (n != 8) {
+        PyErr_SetString(PyExc_TypeError, "bind_paged takes eight addresses");
         return nullptr;
     }
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
         if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_paged: a null address");
             return nullptr;
@@ -553,6 +666,10 @@ PyObject* bind_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     f_paged_workspace = reinterpret_cast<decltype(f_paged_workspace)>(p[1]);
     f_norm_rope = reinterpret_cast<decltype(f_norm_rope)>(p[2]);
     f_append_paged = reinterpret_cast<decltype(f_append_paged)>(p[3]);
+    f_pages_step = reinterpret_cast<decltype(f_pages_step)>(p[4]);
+    f_pages_compact = reinterpret_cast<decltype(f_pages_compact)>(p[5]);
+    f_pages_copy = reinterpret_cast<decltype(f_pages_copy)>(p[6]);
+    f_pages_workspace = reinterpret_cast<decltype(f_pages_workspace)>(p[7]);
     Py_RETURN_NONE;
 }
 
@@ -571,6 +688,9 @@ PyMethodDef kMethods[] = {
     {"paged", fast(paged), METH_FASTCALL, nullptr},
     {"norm_rope", fast(norm_rope), METH_FASTCALL, nullptr},
     {"append_paged", fast(append_paged), METH_FASTCALL, nullptr},
+    {"pages_step", fast(pages_step), METH_FASTCALL, nullptr},
+    {"pages_compact", fast(pages_compact), METH_FASTCALL, nullptr},
+    {"pages_copy", fast(pages_copy), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -276,6 +276,44 @@ struct NormRopeArgs {
 // wide: every address, stride and pair allows 16-byte accesses
 cudaError_t launch_norm_rope(const NormRopeArgs &a, bool f32, bool wide);
 
+// The table of pages (attn_pages_step, attn_pages_compact).
+struct PagesArgs {
+    const int32_t *table;       // (n_seq, max_pages), rows table_stride apart
+    const int32_t *cache_len;   // (n_seq) or nullptr (rows full)
+    const int32_t *parents;     // (n_out) or nullptr (row b goes on from row b)
+    const int32_t *new_len;     // (n_out) or nullptr (the parent's length)
+    const int32_t *pinned;      // (n_pages), not 0: held elsewhere too; or nullptr
+    int32_t *table_out;         // (n_out, max_pages), rows out_stride apart
+    int32_t *len_out;           // (n_out); step only
+    int32_t *copies;            // (n_copies, 3): from, to, rows
+    int32_t *free_pages;        // (1)
+    long long table_stride, out_stride;
+    int n_seq, n_out, max_pages, P, n_pages, n_copies;
+    // workspace
+    int words;                  // of 32 pages
+    unsigned *held, *pins;      // bits
+    int32_t *first;             // step: (n_pages), the lowest row that holds a page partly filled
+    int32_t *need, *stays;      // step: (n_out)
+    int32_t *list;              // pages to be given out (list[-1]: their number, or that of the pages held)
+    int32_t *move;              // compact: (n_pages), a moved page's place in the list
+    cudaStream_t stream;
+};
+cudaError_t launch_pages_step(const PagesArgs &a);
+cudaError_t launch_pages_compact(const PagesArgs &a);
+
+// Copies of pages (attn_pages_copy).  Strides in bytes.
+struct PagesCopyArgs {
+    struct Side {
+        char *p;
+        long long layer, page, head, row;
+    } k, v;
+    const int32_t *copies;      // (n_copies, 3)
+    int n_copies, layers, n_pages, H_kv, P, row_bytes, unit_shift;
+    cudaStream_t stream;
+};
+// wide: every address and stride allows 16-byte accesses
+cudaError_t launch_pages_copy(PagesCopyArgs a, bool wide, int esz);
+
 // Size of the library-static decode scratch used by attn_decode_noalloc.
 constexpr size_t kDecodeNoAllocScratchBytes = 32u << 20;
 
