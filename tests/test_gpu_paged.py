@@ -31,10 +31,15 @@ class Paged:
         counts = [-(-L // P) for L, _ in seqs]
         self.n_pages = n_pages = sum(counts) + 3
         self.M = max(counts, default=0) + 2
-        shape = {"heads": (n_pages, H_kv, P, D), "rows": (n_pages, P, H_kv, D), "halves": (n_pages, 2, H_kv, P, D)}[layout]
+        shape = {"heads": (n_pages, H_kv, P, D), "rows": (n_pages, P, H_kv, D), "halves": (n_pages, 2, H_kv, P, D),
+                 "apart": (n_pages, H_kv * P * D + 64), "by head": (H_kv, n_pages, P, D)}[layout]
         pools = [torch.full(shape, junk, dtype=dtype, device="cuda") for _ in range(1 if layout == "halves" else 2)]
         if layout == "heads":
             self.kp, self.vp = pools
+        elif layout == "apart":  # the heads of all pages are not evenly spaced
+            self.kp, self.vp = (x[:, :H_kv * P * D].view(n_pages, H_kv, P, D) for x in pools)
+        elif layout == "by head":
+            self.kp, self.vp = (x.transpose(0, 1) for x in pools)
         elif layout == "rows":
             self.kp, self.vp = (x.transpose(1, 2) for x in pools)
         else:
@@ -140,10 +145,11 @@ def test_long_sequences_are_split(gpu, dtype, L, n):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("layout", ["rows", "halves"])
-def test_strides_of_pages(gpu, layout, dtype):
-    x = Paged(SEQS, 8, 4, 64, 16, dtype, seed=9, layout=layout)
-    y = Paged(SEQS, 8, 4, 64, 16, dtype, seed=9)
+@pytest.mark.parametrize("layout", ["rows", "halves", "apart", "by head"])
+@pytest.mark.parametrize("P,D", [(16, 64), (16, 128), (256, 128)])
+def test_strides_of_pages(gpu, P, D, layout, dtype):
+    x = Paged(SEQS, 8, 4, D, P, dtype, seed=9, layout=layout)
+    y = Paged(SEQS, 8, 4, D, P, dtype, seed=9)
     a, la = x.call(return_lse=True)
     b, lb = y.call(return_lse=True)
     attn.attn_device_status()

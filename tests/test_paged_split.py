@@ -4,7 +4,7 @@ import random
 
 import pytest
 
-KN, UNIT_COST, MIN_TILES = 128, 5, 2
+KN, UNIT_COST, MIN_TILES, WEIGHT_TWO, LEAST_TWO = 128, 5, 2, 6, 2
 
 
 def cdiv(a, b):
@@ -12,14 +12,20 @@ def cdiv(a, b):
 
 
 class Units:
-    def __init__(self, n, L, tokens):
+    """The axis counts quarters of a key; a sequence of more tokens than one row tile holds has units of two."""
+
+    def __init__(self, n, L, tokens, one_tile):
         self.n, self.L, self.tokens = n, L, tokens
         self.nu = cdiv(n, tokens)
         self.step = min(tokens, n)
-        self.base = max(L - n, 0) + KN - 1 + UNIT_COST * KN
+        self.two = n > one_tile
+        self.weight = WEIGHT_TWO if self.two else 4
+        self.tile = self.weight * KN
+        self.least = LEAST_TWO if self.two else 1
+        self.base = self.weight * (max(L - n, 0) + KN - 1) + UNIT_COST * KN * 4
 
     def at(self, u):
-        return u * self.base + u * (u + 1) // 2 * self.step
+        return u * self.base + u * (u + 1) // 2 * self.step * self.weight
 
     def keys(self, u):
         return max(0, min(self.L, self.L - self.n + min((u + 1) * self.tokens, self.n)))
@@ -27,12 +33,18 @@ class Units:
     def tiles(self, u):
         return max(1, cdiv(self.keys(u), KN))
 
+    def cut(self, x, nt):
+        if x >= nt * self.tile:
+            return nt
+        j = 0 if x <= 0 else cdiv(x, self.tile)
+        return 0 if j < self.least else nt if j > nt - self.least else j
 
-def runs_of(seqs, per, tokens, grid, cta):
+
+def runs_of(seqs, per, tokens, one_tile, grid, cta):
     """The (sequence, head, unit, first tile, tiles) of one CTA, walked as its loading warp does."""
-    cost = [Units(n, L, tokens).at(cdiv(n, tokens)) * per if n else 0 for n, L in seqs]
+    cost = [Units(n, L, tokens, one_tile).at(cdiv(n, tokens)) * per if n else 0 for n, L in seqs]
     total = sum(cost)
-    N = max(1, min(total // (KN * MIN_TILES), grid))
+    N = max(1, min(total // (4 * KN * MIN_TILES), grid))
     if cta >= N or total == 0:
         return [], None, N, total
     lo, hi = total * cta // N, total * (cta + 1) // N
@@ -40,7 +52,7 @@ def runs_of(seqs, per, tokens, grid, cta):
     while base + cost[b] <= lo:
         base += cost[b]
         b += 1
-    units = Units(*seqs[b], tokens)
+    units = Units(*seqs[b], tokens, one_tile)
     one = units.at(units.nu)
     hs, pos = divmod(lo - base, one)
     pos = base + hs * one
@@ -65,24 +77,23 @@ def runs_of(seqs, per, tokens, grid, cta):
                 while b < len(seqs) and seqs[b][0] == 0:
                     b += 1
                 if b < len(seqs):
-                    units = Units(*seqs[b], tokens)
+                    units = Units(*seqs[b], tokens, one_tile)
         state[:] = [b, hs, u, 0, pos, units]
 
-    j = cdiv(lo - pos, KN)
-    if j >= units.tiles(u):
+    state[3] = units.cut(lo - pos, units.tiles(u))
+    if state[3] == units.tiles(u):
         advance()
-    else:
-        state[3] = j
     runs, rec = [], None
-    while state[0] < len(seqs) and state[4] + state[3] * KN < hi:
+    while state[0] < len(seqs) and state[4] < hi:
         b, hs, u, j, pos, units = state
         nt = units.tiles(u)
-        n = min(nt - j, cdiv(hi - pos, KN) - j)
-        assert n > 0
+        n = units.cut(hi - pos, nt) - j
+        if n <= 0:
+            break
         runs.append((b, hs, u, j, n))
         if j == 0 and n < nt:
             assert rec is None
-            rec = (b, hs, u, ((pos + (nt - 1) * KN + 1) * N - 1) // total)
+            rec = (b, hs, u, ((pos + (nt - units.least) * units.tile + 1) * N - 1) // total)
         if j + n == nt:
             advance()
         else:
@@ -94,7 +105,8 @@ def runs_of(seqs, per, tokens, grid, cta):
 @pytest.mark.parametrize("seed", range(60))
 def test_every_tile_once_and_every_part_found(seed):
     r = random.Random(seed)
-    tokens = r.choice((1, 2, 16, 25, 32, 50, 64, 128, 256))
+    one_tile = r.choice((1, 2, 16, 25, 32, 64, 128))
+    tokens = one_tile * r.choice((1, 2))
     per = r.choice((1, 2, 8))
     seqs = []
     for _ in range(r.choice((1, 2, 5, 40))):
@@ -104,19 +116,19 @@ def test_every_tile_once_and_every_part_found(seed):
     grid = r.choice((1, 3, 152))
     taken, recs, parts = set(), {}, {}
     for cta in range(grid):
-        runs, rec, N, _ = runs_of(seqs, per, tokens, grid, cta)
+        runs, rec, N, _ = runs_of(seqs, per, tokens, one_tile, grid, cta)
         for b, hs, u, j, n in runs:
             for t in range(j, j + n):
                 assert (b, hs, u, t) not in taken
                 taken.add((b, hs, u, t))
-            whole = n == Units(*seqs[b], tokens).tiles(u)
+            whole = n == Units(*seqs[b], tokens, one_tile).tiles(u)
             if not whole:
                 # slot 2 cta + 1 for the beginning, 2 cta for what goes on: one each a CTA
                 assert parts.setdefault((cta, j == 0), (b, hs, u)) == (b, hs, u)
         if rec:
             recs[cta] = rec
     want = {(b, hs, u, t) for b, (n, L) in enumerate(seqs) if n for hs in range(per)
-            for u in range(cdiv(n, tokens)) for t in range(Units(n, L, tokens).tiles(u))}
+            for u in range(cdiv(n, tokens)) for t in range(Units(n, L, tokens, one_tile).tiles(u))}
     assert taken == want
     cut = {v for v in parts.values()}
     assert {rec[:3] for rec in recs.values()} == cut
@@ -131,12 +143,13 @@ def test_axis_holds_every_unit():
     """A unit's share holds its tiles, and the host's bound on the axis holds all of them."""
     r = random.Random(5)
     for _ in range(3000):
-        tokens = r.choice((1, 16, 25, 64, 256))
+        one_tile = r.choice((1, 16, 25, 64, 128))
+        tokens = 2 * one_tile
         n, L = r.randint(1, 2000), r.randint(0, 5000)
-        u = Units(n, L, tokens)
+        u = Units(n, L, tokens, one_tile)
         for i in range(u.nu):
-            assert u.tiles(i) * KN <= u.at(i + 1) - u.at(i)
-        assert u.at(u.nu) <= (1 + n / (tokens / 2)) * (L + n + KN * (UNIT_COST + 1))
+            assert u.tiles(i) * u.tile <= u.at(i + 1) - u.at(i)
+        assert u.at(u.nu) <= (1 + n / one_tile) * (WEIGHT_TWO * (L + n + KN) + 4 * KN * UNIT_COST)
 
 
 @pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 7, 8, 16, 33, 64, 100, 128, 129, 200, 300])

@@ -304,22 +304,55 @@ bool pools_overlap(const Pool &a, const Pool &b) {
     return !nested_distinct(n, st, 5, a.row);
 }
 
-// (D, P, H_kv, n_pages) bf16 view of one layer; boxes of 64 x rows x 1 x 1 with 128-byte
-// swizzle, pages out of range read as zeros.
-int make_map_pages(CUtensorMap *map, const Pool &o, int rows) {
+// Are the heads of all pages evenly spaced?  Then head h of page p is entry p * pstep +
+// h * hstep of a list of `n` heads `stride` bytes apart.
+struct Heads {
+    long long n, stride, pstep, hstep;
+};
+bool even_heads(const Pool &o, Heads *e) {
+    const long long page = o.st[1], head = o.st[2];
+    if (o.n[2] == 1)
+        *e = {o.n[1], page, 1, 0};
+    else if (o.n[1] == 1)
+        *e = {o.n[2], head, 0, 1};
+    else if (head > 0 && page % head == 0)
+        *e = {0, head, page / head, 1};
+    else if (page > 0 && head % page == 0)
+        *e = {0, page, 1, head / page};
+    else
+        return false;
+    if (e->n == 0) e->n = (o.n[1] - 1) * e->pstep + (o.n[2] - 1) * e->hstep + 1;
+    return e->n <= 0x7fffffff;
+}
+
+// bf16 view of one layer of pages with 128-byte swizzle, for boxes of `rows` rows and all
+// columns: (64, 8, D / 64, P / 8, heads), so that a box arrives as groups of 8 rows, in each
+// the 64-column blocks.  Without even heads (e = NULL) (D, P, H_kv, n_pages) with boxes of
+// one such block.  Pages out of range read as zeros.
+int make_map_pages(CUtensorMap *map, const Pool &o, const Heads *e, int rows) {
     EncodeTiledFn encode;
     int rc = get_encode(&encode);
     if (rc) return rc;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(o.row / 2), static_cast<cuuint64_t>(o.n[3]),
-                                static_cast<cuuint64_t>(o.n[2]), static_cast<cuuint64_t>(o.n[1])};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(o.st[3]), static_cast<cuuint64_t>(o.st[2]),
-                                   static_cast<cuuint64_t>(o.st[1])};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult e = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<char *>(o.p), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (e != CUDA_SUCCESS) return fail(ATTN_ECUDA, "cuTensorMapEncodeTiled (pages) failed (%d)", static_cast<int>(e));
+    const cuuint64_t D = static_cast<cuuint64_t>(o.row / 2), P = static_cast<cuuint64_t>(o.n[3]);
+    const cuuint64_t row = static_cast<cuuint64_t>(o.st[3]);
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r;
+    if (e) {
+        const cuuint64_t dims[5] = {64, 8, D / 64, P / 8, static_cast<cuuint64_t>(e->n)};
+        const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(e->stride)};
+        const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(rows / 8), 1};
+        r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<char *>(o.p), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {
+        const cuuint64_t dims[4] = {D, P, static_cast<cuuint64_t>(o.n[2]), static_cast<cuuint64_t>(o.n[1])};
+        const cuuint64_t strides[3] = {row, static_cast<cuuint64_t>(o.st[2]), static_cast<cuuint64_t>(o.st[1])};
+        const cuuint32_t box[4] = {64, 8, 1, 1};
+        r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<char *>(o.p), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    if (r != CUDA_SUCCESS) return fail(ATTN_ECUDA, "cuTensorMapEncodeTiled (pages) failed (%d)", static_cast<int>(r));
     return ATTN_OK;
 }
 
@@ -1042,7 +1075,7 @@ static long long paged_sizes(const char *who, PagedArgs &a, bool ragged, int dty
     while (a.P % a.box) a.box /= 2;
     const double axis = paged_tc_axis(a);
     if (axis * 1024 > 4e18) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
-    a.grid = axis / 256 < a.n_sm ? static_cast<int>(axis / 256) + 1 : a.n_sm;
+    a.grid = axis / 1024 < a.n_sm ? static_cast<int>(axis / 1024) + 1 : a.n_sm;
     if (a.grid > 1023) a.grid = 1023;
     return a.grid * 32LL + 2LL * a.grid * a.slot_rows * (a.D + 2) * 4;
 }
@@ -1169,8 +1202,14 @@ ATTN_API int attn_fwd_paged(const void *q, const void *kpages, const void *vpage
         CUtensorMap tq, tk, tv;
         if (n_pages == 0)  // no box is copied: any valid view
             for (int i = 0; i < 2; ++i) make_pool(&pool[i], q, 1, 0, 1, 1, page_size, D, esz, nullptr);
-        if ((rc = make_map_tokens(&tq, rq, D, a.heads, a.box_tokens)) || (rc = make_map_pages(&tk, pool[0], a.box)) ||
-            (rc = make_map_pages(&tv, pool[1], a.box)))
+        Heads heads[2] = {};
+        a.halves = !even_heads(pool[0], &heads[0]) || !even_heads(pool[1], &heads[1]);
+        if (a.halves) a.box = 8;
+        a.k_pstep = static_cast<int>(heads[0].pstep), a.k_hstep = static_cast<int>(heads[0].hstep);
+        a.v_pstep = static_cast<int>(heads[1].pstep), a.v_hstep = static_cast<int>(heads[1].hstep);
+        if ((rc = make_map_tokens(&tq, rq, D, a.heads, a.box_tokens)) ||
+            (rc = make_map_pages(&tk, pool[0], a.halves ? nullptr : &heads[0], a.box)) ||
+            (rc = make_map_pages(&tv, pool[1], a.halves ? nullptr : &heads[1], a.box)))
             return rc;
         e = launch_paged_tc(a, tq, tk, tv);
     }

@@ -130,6 +130,8 @@ struct PagedArgs {
     // bf16: row tiles of `tokens` tokens by `heads` heads of one of `groups` groups of
     // the query heads of a cached head; boxes of `box` rows of a page, box_tokens tokens of q
     int heads, groups, tokens, box, box_tokens;
+    // the pages' views: head h of page p is entry p pstep + h hstep; halves: boxes of 64 columns
+    int halves, k_pstep, k_hstep, v_pstep, v_hstep;
     int single;                 // every unit has one row tile
     int grid;                   // CTAs at most
     int n_split;                // fp32: splits of the keys
@@ -144,7 +146,8 @@ struct PagedArgs {
     int n_sm;
 };
 // bf16 tcgen05 kernel and its merge; tq views q as (D, H, T) with 64 x heads x box_tokens
-// boxes, tk and tv the pages as (D, P, H_kv, n_pages) with 64 x box x 1 x 1 boxes.
+// boxes, tk and tv the pages as (64, 8, D / 64, P / 8, heads of pages) with 64 x 8 x D / 64 x
+// box / 8 x 1 boxes (halves: as (D, P, H_kv, n_pages) with 64 x 8 x 1 x 1 boxes).
 cudaError_t launch_paged_tc(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv);
 double paged_tc_axis(const PagedArgs &a);
 cudaError_t launch_paged_f32(const PagedArgs &a);

@@ -24,7 +24,12 @@
 // Pages.  A 128-key tile is copied by boxes that lie in one page each (rows: the largest
 // power of two up to 128 that divides P), each lane of the loading warp with its own box
 // and its own entry of the table, fetched a tile ahead.  Boxes past the last visible key are not
-// copied; an entry that is no page reads as zeros (TMA's fill).
+// copied; an entry that is no page reads as zeros (TMA's fill).  What a small box costs is
+// its instruction (some 25 ns each, one after the other), so one box brings all D columns: in
+// shared memory a tile is groups of 8 rows, in each the 64-column blocks of 8 x 128 bytes
+// one behind the other, which a view of (64 columns, 8 rows, D / 64 blocks, groups of
+// rows, heads of pages) writes and the strides of the MMA's descriptors take.  Where
+// the heads of all pages are not evenly spaced, boxes are the blocks themselves.
 //
 // Two softmax warpgroups (streams) keep two S and two O accumulators in TMEM busy.  A
 // unit with two row tiles gives each stream one of them, and both read the same K/V
@@ -53,8 +58,8 @@ namespace {
 constexpr int kN = 128;          // keys per K/V tile
 constexpr int kM = 128;          // rows per tile
 constexpr int kThreads = 384;
-constexpr uint32_t kRegsOther = 64;     // warps 0-3 after setmaxnreg
-constexpr uint32_t kRegsSoftmax = 216;  // warps 4-11: 128 * 64 + 256 * 216 <= 384 * 168
+constexpr uint32_t kRegsOther = 80;     // warps 0-3 after setmaxnreg
+constexpr uint32_t kRegsSoftmax = 208;  // warps 4-11: 128 * 80 + 256 * 208 <= 384 * 168
 constexpr int kTmemCols = 512;   // S0 0, S1 128, O0 256, O1 256 + D
 constexpr int kRing = 4;         // unit runs in flight between the roles
 constexpr int kRingReaders = 32 + 256;
@@ -69,11 +74,21 @@ constexpr float kHugeLog2 = 16777216.0f;  // 2^24
 #ifndef ATTN_PAGED_UNIT_COST
 #define ATTN_PAGED_UNIT_COST 5
 #endif
+#ifndef ATTN_PAGED_WEIGHT
+#define ATTN_PAGED_WEIGHT 6
+#endif
+#ifndef ATTN_PAGED_LEAST
+#define ATTN_PAGED_LEAST 2
+#endif
 constexpr int kUnitCost = ATTN_PAGED_UNIT_COST;  // what a unit costs beside its tiles, in tiles
 constexpr int kMinTiles = ATTN_PAGED_MIN_TILES;  // fewest tiles' worth of keys a CTA takes
+constexpr int kWeightTwo = ATTN_PAGED_WEIGHT;    // quarters of a tile's cost, where a unit has two row tiles
+constexpr int kLeastTwo = ATTN_PAGED_LEAST;      // fewest tiles of such a unit that a cut leaves on either side
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+
+__device__ __forceinline__ bool is_page(const PagedArgs &a, int page) { return page >= 0 && page < a.n_pages; }
 
 // One sequence: first token, new tokens, keys.
 struct Seq {
@@ -95,18 +110,37 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs &a, int s) {
     return q;
 }
 
-// The units of one cached head (and group of heads) of a sequence on the axis of keys:
-// unit u of nu takes keys [at(u), at(u + 1)).
+// a / b, in 32 bits where they do (a 64-bit division is a call of some 100 instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
+
+// The units of one cached head (and group of heads) of a sequence on the axis: unit u of nu
+// takes [at(u), at(u + 1)), its tile j begins at at(u) + j tile.
 struct Units {
-    int nu, step;  // units, tokens of a unit
+    int nu, step;   // units, tokens of a unit
+    int weight;     // quarters a key
+    int tile;       // quarters a K/V tile
+    int least;      // tiles of a unit that a cut leaves on either side
     long long base;
-    __device__ __forceinline__ Units(const Seq &q, int tokens) {
+    __device__ __forceinline__ Units(const Seq &q, int tokens, int one_tile) {
         nu = (q.n + tokens - 1) / tokens;
         step = min(tokens, q.n);
-        base = max(q.L - q.n, 0) + kN - 1 + kUnitCost * kN;
+        const bool two = q.n > one_tile;
+        weight = two ? kWeightTwo : 4;
+        tile = weight * kN;
+        least = two ? kLeastTwo : 1;
+        base = static_cast<long long>(weight) * (max(q.L - q.n, 0) + kN - 1) + kUnitCost * kN * 4;
     }
     __device__ __forceinline__ long long at(int u) const {
-        return u * base + static_cast<long long>(u) * (u + 1) / 2 * step;
+        return u * base + static_cast<long long>(u) * (u + 1) / 2 * (step * weight);
+    }
+    // The first of a unit's nt tiles that lies behind a cut at x, counted from the unit's begin.
+    __device__ __forceinline__ int cut(long long x, int nt) const {
+        if (x >= static_cast<long long>(nt) * tile) return nt;
+        const int j = x <= 0 ? 0 : static_cast<int>(quotient(x + tile - 1, tile));
+        return j < least ? 0 : j > nt - least ? nt : j;
     }
 };
 
@@ -128,6 +162,7 @@ struct GuardReq {
     int run;     // ring slot
 };
 constexpr int kEnd = -1;
+constexpr int kNoBox = INT_MIN, kBadPage = -1;  // a box that is not copied; an entry that is no page (or one from n_pages on)
 
 // Single: every unit has one row tile; its second Q buffer is one more K/V stage.
 template <int D, bool Single>
@@ -139,7 +174,8 @@ struct Layout {
     static constexpr int kStages = D == 128 ? (Single ? 5 : 4) : 8;
     static constexpr int kRingOff = kQTiles * kTile;
     static constexpr int kExOff = kRingOff + kStages * kTile;
-    static constexpr int kBarOff = kExOff + 256 * 8;
+    static constexpr int kStageOff = kExOff + 256 * 8;   // per softmax warp: 32 rows x 64 bytes of output
+    static constexpr int kBarOff = kStageOff + 8 * 2048;
     static constexpr int kSmemBytes = kBarOff + 1024 + 1024;
 };
 
@@ -248,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int per = a.H_kv * a.groups;  // heads, or groups of them, of a sequence
         const int tokens = (Single ? 1 : 2) * a.tokens;  // of a unit
         auto cost_of = [&](const Seq &q) {
-            const Units u(q, tokens);
+            const Units u(q, tokens, a.tokens);
             return u.at(u.nu) * per;
         };
-        long long total = 0;  // keys on the axis (the host has checked that they fit)
+        long long total = 0;  // length of the axis (the host has checked that it fits)
         Seq mine{0, 0, 0};    // sequence b0 + lane
         for (int b0 = lane; b0 < a.n_seq; b0 += 32) {
             mine = seq_of(a, b0);
@@ -259,10 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        const long long most = total / (kN * kMinTiles);
+        // CTA i of N takes what begins in [total i / N, total (i + 1) / N)
+        const long long most = total / (4 * kN * kMinTiles);
         const int N = static_cast<int>(min(max(most, 1ll), static_cast<long long>(gridDim.x))), I = blockIdx.x;
         const bool idle = I >= N || total == 0;
-        const long long lo = idle ? 0 : total * I / N, hi = idle ? 0 : total * (I + 1) / N;
+        const long long each = quotient(total, N);
+        const int odd = static_cast<int>(total - each * N);
+        const long long lo = idle ? 0 : each * I + odd * I / N, hi = idle ? 0 : each * (I + 1) + odd * (I + 1) / N;
         // sequence that holds position lo, and the first position of its units
         int b = 0;
         long long base = 0;
@@ -286,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Seq q{__shfl_sync(0xffffffffu, mine.c0, b % 32), __shfl_sync(0xffffffffu, mine.n, b % 32),
               __shfl_sync(0xffffffffu, mine.L, b % 32)};
-        Units units(q, tokens);
+        Units units(q, tokens, a.tokens);
         int hs = 0, u = 0, j = 0;
-        long long pos = base;  // first key of unit u of hs
+        long long pos = base;  // of unit u of hs
         auto keys_of = [&](int unit) { return max(0, min(q.L, q.L - q.n + min((unit + 1) * tokens, q.n))); };
         auto next_unit = [&] {
             pos += units.at(u + 1) - units.at(u);
@@ -300,14 +339,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (++b < a.n_seq) {
                 q = seq_of(a, b);
                 if (q.n > 0) {
-                    units = Units(q, tokens);
+                    units = Units(q, tokens, a.tokens);
                     break;
                 }
             }
         };
         if (!idle) {
-            const long long one = units.at(units.nu), rem = lo - base;
-            hs = static_cast<int>(rem / one);
+            const long long one = units.at(units.nu);
+            hs = static_cast<int>(quotient(lo - base, one));
             pos += hs * one;
             int top = units.nu;  // at(u) <= lo - pos < at(top)
             while (top - u > 1) {
@@ -318,16 +357,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     top = mid;
             }
             pos += units.at(u);
-            const long long j_ll = (lo - pos + kN - 1) / kN;
-            if (j_ll >= tiles_of(keys_of(u)))
-                next_unit();
-            else
-                j = static_cast<int>(j_ll);
+            const int nt = tiles_of(keys_of(u));
+            j = units.cut(lo - pos, nt);
+            if (j == nt) next_unit();
         }
-        // this lane's box of a tile: rows [i box, (i + 1) box) of the columns from 64 c on
+        // this lane's box of a tile: rows [i box, (i + 1) box), of the columns from 64 c on
+        // where a box does not hold them all
         const int boxes = kN / a.box, i = lane % boxes, c = lane / boxes;
-        const bool carries = lane < boxes * L::kSub;
-        int issued = 0, requests = 0, k = 0, q_loads = 0;
+        const bool carries = lane < boxes * (a.halves ? L::kSub : 1);
+        const uint32_t box_at = static_cast<uint32_t>(i * a.box * (D * 2) + c * 1024);
+        const int page_inc = kN / a.P, row_inc = kN % a.P;  // from tile to tile
+        int issued = 0, stage = 0, requests = 0, k = 0, q_loads = 0;
+        uint32_t stage_phase = 1;  // of kv_empty: the first round of the ring waits for nothing
         bool ok = true;
         int4 rec = make_int4(-1, 0, 0, 0), rec2 = make_int4(0, 0, 0, 0);
         while (ok) {
@@ -335,23 +376,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k >= kRing && !(ok = mbar_wait_warp(&bars.run_empty[slot], ((k / kRing) - 1) & 1, &bars.abort))) break;
             Run r{0, 0, 0, 0, 0, -1, 0, 0, 0, 0};
             int nt = 0;
-            if (!idle && b < a.n_seq && pos + static_cast<long long>(j) * kN < hi) {
-                r.seq = b;
-                r.hs = hs;
-                r.tok0 = u * tokens;
-                r.left = q.n - r.tok0;
-                r.keys = keys_of(u);
-                r.past = q.L - q.n;
-                r.c0 = q.c0;
-                r.j0 = j;
-                nt = tiles_of(r.keys);
-                const long long room = (hi - pos + kN - 1) / kN - j;  // tiles that begin before hi
-                r.n = static_cast<int>(min(static_cast<long long>(nt - j), room));
-                r.slot = r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
-                if (j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w
-                    const long long last = pos + static_cast<long long>(nt - 1) * kN;
-                    rec = make_int4(b, hs, r.tok0, static_cast<int>(((last + 1) * N - 1) / total));
-                    rec2 = make_int4(r.left, r.past, r.c0, 0);
+            if (!idle && b < a.n_seq && pos < hi) {
+                const int keys = keys_of(u);
+                nt = tiles_of(keys);
+                const int end = units.cut(hi - pos, nt);
+                if (end > j) {
+                    r.seq = b;
+                    r.hs = hs;
+                    r.tok0 = u * tokens;
+                    r.left = q.n - r.tok0;
+                    r.keys = keys;
+                    r.past = q.L - q.n;
+                    r.c0 = q.c0;
+                    r.j0 = j;
+                    r.n = end - j;
+                    r.slot = r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
+                    if (j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w,
+                                               // the last whose begin leaves enough of it
+                        const long long last = pos + static_cast<long long>(nt - units.least) * units.tile;
+                        rec = make_int4(b, hs, r.tok0, static_cast<int>(quotient((last + 1) * N - 1, total)));
+                        rec2 = make_int4(r.left, r.past, r.c0, 0);
+                    }
                 }
             }
             if (lane == 0) {
@@ -364,37 +409,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (r.n < 0) break;
             const int edge = edge_of(r), head = r.hs / a.groups;
-            const int32_t *table = a.page_table + static_cast<long long>(r.seq) * a.table_stride;
-            // this lane's page of tile jj
-            auto page_of = [&](int jj) {
-                const int row = (r.j0 + jj) * kN + i * a.box;
-                return jj < r.n && carries && row < r.keys ? table[row / a.P] : 0;
+            // This lane's box of the next tile to be looked up: its key, its entry of the table and its row
+            // in that page.  A box past the last visible key is not copied: kNoBox.
+            const int k_head = head * a.k_hstep, v_head = head * a.v_hstep;
+            int next_key = r.j0 * kN + i * a.box, next_row = next_key % a.P;
+            const int32_t *next_entry = a.page_table + static_cast<long long>(r.seq) * a.table_stride + next_key / a.P;
+            const int last_key = min(r.keys, (r.j0 + r.n) * kN);
+            struct Box {
+                int page, row;
             };
-            auto load = [&](int jj, int kv, int page) {
+            auto look_up = [&] {
+                Box x{kNoBox, next_row};
+                if (carries && next_key < last_key) x.page = max(*next_entry, kBadPage);
+                next_key += kN;
+                next_entry += page_inc;
+                next_row += row_inc;
+                if (next_row >= a.P) next_row -= a.P, ++next_entry;
+                return x;
+            };
+            auto load = [&](int jj, int kv, const Box &x) {
                 if (!ok || jj >= r.n) return;
-                const int s = issued % kStages;
-                if (issued >= kStages &&
-                    !(ok = mbar_wait_warp(&bars.kv_empty[s], ((issued / kStages) - 1) & 1, &bars.abort)))
+                if (!__all_sync(0xffffffffu, mbar_try_wait(&bars.kv_empty[stage], stage_phase)) &&
+                    !(ok = mbar_wait_warp(&bars.kv_empty[stage], stage_phase, &bars.abort)))
                     return;
-                const int key0 = (r.j0 + jj) * kN;
-                const int some = min(boxes, max(0, (r.keys - key0 + a.box - 1) / a.box));  // boxes with a visible key
+                uint64_t *full = &bars.kv_full[stage];
+                const int inside = r.keys - (r.j0 + jj) * kN;
                 if (lane == 0) {
-                    if (some > 0)
-                        mbar_arrive_expect_tx(&bars.kv_full[s], static_cast<uint32_t>(some * a.box * D * 2));
+                    if (inside >= kN)
+                        mbar_arrive_expect_tx(full, kN * D * 2);
+                    else if (inside > 0)
+                        mbar_arrive_expect_tx(full, static_cast<uint32_t>((inside + a.box - 1) / a.box * a.box * D * 2));
                     else
-                        mbar_arrive(&bars.kv_full[s]);
+                        mbar_arrive(full);
                 }
-                __syncwarp();
-                if (carries && i < some)
-                    tma_load_4d(ring + s * L::kTile + c * L::kBlock + i * a.box * 128, kv ? &tv : &tk, &bars.kv_full[s],
-                                c * 64, (key0 + i * a.box) % a.P, head, page);
-                if (kv && jj >= edge && lane == 0) {
-                    volatile GuardReq &g = bars.req[requests % kGuardRing];
-                    g.stage = s, g.parity = (issued / kStages) & 1, g.rows = r.keys - key0, g.run = slot;
-                    mbar_arrive(&bars.guard_full[requests % kGuardRing]);
+                if (x.page != kNoBox) {
+                    uint8_t *dst = ring + stage * L::kTile + box_at;
+                    if (a.halves)
+                        tma_load_4d(dst, kv ? &tv : &tk, full, c * 64, x.row, head, x.page);
+                    else {
+                        const unsigned at = kv ? x.page * static_cast<unsigned>(a.v_pstep) + v_head : x.page * static_cast<unsigned>(a.k_pstep) + k_head;
+                        tma_load_5d(dst, kv ? &tv : &tk, full, 0, 0, 0, x.row / 8, is_page(a, x.page) ? static_cast<int>(at) : -1);
+                    }
                 }
-                if (kv && jj >= edge) ++requests;
+                if (kv && jj >= edge) {
+                    if (lane == 0) {
+                        volatile GuardReq &g = bars.req[requests % kGuardRing];
+                        g.stage = stage, g.parity = stage_phase ^ 1, g.rows = inside, g.run = slot;
+                        mbar_arrive(&bars.guard_full[requests % kGuardRing]);
+                    }
+                    ++requests;
+                }
                 ++issued;
+                if (++stage == kStages) stage = 0, stage_phase ^= 1;
             };
             auto load_q = [&](int tiles) {  // once the last run's last S MMA has read the buffers
                 if (!ok || (k > 0 && !(ok = mbar_wait_warp(&bars.q_free, (k - 1) & 1, &bars.abort)))) return;
@@ -410,27 +476,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 ++q_loads;
             };
-            int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2), p3;  // of tiles jj, jj + 1, ...
+            Box b0 = look_up(), b1 = look_up(), b2 = look_up();  // of tiles jj, jj + 1, jj + 2
             if (Single || r.left <= a.tokens) {  // one row tile: K0 K1 | V0 K2 | V1 K3 | ...
                 if (k == 0) load_q(1);
-                load(0, 0, p0);
-                load(1, 0, p1);
+                load(0, 0, b0);
+                load(1, 0, b1);
                 if (k > 0) load_q(1);
                 for (int jj = 0; jj < r.n && ok; ++jj) {
-                    p3 = page_of(jj + 3);
-                    load(jj, 1, p0);
-                    load(jj + 2, 0, p2);
-                    p0 = p1, p1 = p2, p2 = p3;
+                    const Box b3 = look_up();
+                    load(jj, 1, b0);
+                    load(jj + 2, 0, b2);
+                    b0 = b1, b1 = b2, b2 = b3;
                 }
             } else {
                 if (k == 0) load_q(2);
-                load(0, 0, p0);
+                load(0, 0, b0);
                 if (k > 0) load_q(2);
                 for (int jj = 0; jj < r.n && ok; ++jj) {
-                    p3 = page_of(jj + 3);
-                    load(jj, 1, p0);
-                    load(jj + 1, 0, p1);
-                    p0 = p1, p1 = p2, p2 = p3;
+                    const Box b3 = look_up();
+                    load(jj, 1, b0);
+                    load(jj + 1, 0, b1);
+                    b0 = b1, b1 = b2, b2 = b3;
                 }
             }
             ++k;
@@ -457,14 +523,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0);
         const uint32_t idesc_o = idesc_bf16_f32(kM, D, 1);
         const uint64_t dq0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-        const uint64_t dk0 = sdesc_sw128(smem_u32(ring), 16, 1024);
-        const uint64_t dv0 = sdesc_sw128(smem_u32(ring), L::kBlock, 1024);
+        const uint64_t dk0 = sdesc_sw128(smem_u32(ring), 16, L::kSub * 1024);
+        const uint64_t dv0 = sdesc_sw128(smem_u32(ring), 1024, L::kSub * 1024);
         auto issue_s = [&](int x, int qbuf, int slot) {  // S_x = Q_qbuf K^T
             const uint64_t da = desc_add(dq0, (qbuf * L::kTile) >> 4), db = desc_add(dk0, (slot * L::kTile) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk / 4) * L::kBlock + (kk % 4) * 32) >> 4;
-                mma_ss_warp(tmem + x * 128u, desc_add(da, off), desc_add(db, off), idesc_s, kk > 0);
+                const uint32_t q_off = ((kk / 4) * L::kBlock + (kk % 4) * 32) >> 4, k_off = ((kk / 4) * 1024 + (kk % 4) * 32) >> 4;
+                mma_ss_warp(tmem + x * 128u, desc_add(da, q_off), desc_add(db, k_off), idesc_s, kk > 0);
             }
         };
         auto issue_pv = [&](int x, int slot, bool acc) {  // O_x (+)= P_x V
@@ -472,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kN / 16; ++kk)
                 mma_ts_warp(tmem + 256u + x * static_cast<uint32_t>(D), tmem + x * 128u + kk * 8,
-                            desc_add(db, (kk * 16 * 128) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
+                            desc_add(db, (kk * 16 * D * 2) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
         };
         int consumed = 0, cleaned = 0;
         uint32_t pr[2] = {0, 0};
@@ -592,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (stage < 0) break;
             if (!mbar_wait_warp(&bars.kv_full[stage], parity, &bars.abort)) break;
             const uint32_t tile = smem_u32(ring + stage * L::kTile);
-            const bool bad = clean_v_tile<L::kSub, kN, 64>(tile, inside, tid);
+            const bool bad = clean_v_tile<L::kSub, kN, 64, true>(tile, inside, tid);
             if (bad) *static_cast<volatile int *>(&bars.spoiled[run]) = 1;
             if (inside < kN || __any_sync(0xffffffffu, bad)) fence_proxy_async_shared();  // written: the MMA must see it
             __syncwarp();
@@ -748,8 +814,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a unit of one row tile: stream 0 writes the first half of the columns, stream 1 the second
             const int c0 = one ? x * (D / 64) : 0, c1 = one ? c0 + D / 64 : D / 32;
             const long long token = static_cast<long long>(r.c0) + w.token;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_ts + w.head * a.o_hs;
             if (__any_sync(0xffffffffu, w.valid)) {
+                // rows that the lanes store: 8 y + lane / 4, 16 bytes each
+                const uint32_t stage = smem_u32(smem + L::kStageOff + (warp - 4) * 2048);
+                const unsigned long long out = write && r.slot < 0
+                    ? reinterpret_cast<unsigned long long>(static_cast<__nv_bfloat16 *>(a.out) + token * a.o_ts + w.head * a.o_hs) : 0ull;
+                unsigned long long to[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) to[y] = __shfl_sync(0xffffffffu, out, 8 * y + lane / 4);
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
                     __syncwarp();
@@ -773,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int key = (r.j0 + edge_of(r)) * kN; key < end; ++key) {
                             const int page = table[key / a.P];
-                            if (page < 0 || page >= a.n_pages) continue;
+                            if (!is_page(a, page)) continue;
                             const uint32_t *vr = reinterpret_cast<const uint32_t *>(
                                 static_cast<const __nv_bfloat16 *>(a.v) + page * a.v_ps + (r.hs / a.groups) * a.v_hs +
                                 (key % a.P) * a.v_rs + c * 32);
@@ -792,16 +864,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             dst[e * a.slot_rows] = make_float4(u2f(o[4 * e]), u2f(o[4 * e + 1]), u2f(o[4 * e + 2]), u2f(o[4 * e + 3]));
-                    } else if (write) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(out + c * 32);
+                    }
+                    if (r.slot < 0) {
+                        // through the warp's buffer, so that a store writes 64 bytes of each of 8 rows
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t pk[4];
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
                                 pk[y] = live ? pack_bf16x2(u2f(o[8 * e + 2 * y]) * inv, u2f(o[8 * e + 2 * y + 1]) * inv) : 0u;
-                            dst[e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            st_shared_v4(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), pk[0], pk[1], pk[2], pk[3]);
                         }
+                        __syncwarp();
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int rr = 8 * y + lane / 4, q4 = lane % 4;
+                            const uint4 v = ld_shared_v4(stage + rr * 64 + ((q4 ^ ((rr >> 1) & 3)) << 4));
+                            if (to[y]) *reinterpret_cast<uint4 *>(to[y] + c * 64 + q4 * 16) = v;
+                        }
+                        __syncwarp();
                     }
                 }
             }
@@ -832,15 +913,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Block (i, y) merges 32 rows of the unit that begins in CTA i of the main kernel and
 // ends in a later one: slot 2 i + 1, then slot 2 c of the CTAs after it.  Lane = row, as
 // the partial results lie; warp = D / 8 columns.
-template <int D>
+// Early: the first slots are loaded beside the look-up, parts or not.
+template <int D, bool Early>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     const int i = blockIdx.x, rr = blockIdx.y * 32 + threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int4 rec = reinterpret_cast<const int4 *>(a.merge)[2 * i], rec2 = reinterpret_cast<const int4 *>(a.merge)[2 * i + 1];
-    if (rec.x < 0) return;
-    const Row w = row_of(a, rec.y, rec.z, rec2.x, rec2.y, rr / kM, rr % kM);
-    if (!w.valid) return;
     constexpr int C = D / 32;
     auto slot = [&](int c) { return static_cast<size_t>(c == 0 ? 2 * i + 1 : 2 * (i + c)); };
     auto part = [&](int c) { return reinterpret_cast<const float2 *>(a.part_ml)[slot(c) * a.slot_rows + rr]; };
@@ -849,10 +927,23 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
     };
     float2 x[kAhead];
     float4 o[kAhead][C];
+    if (Early) {
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int c = min(y, a.grid - 1 - i);
+            x[y] = part(c);
+#pragma unroll
+            for (int e = 0; e < C; ++e) o[y][e] = column(c, e);
+        }
+    }
+    const int4 rec = reinterpret_cast<const int4 *>(a.merge)[2 * i], rec2 = reinterpret_cast<const int4 *>(a.merge)[2 * i + 1];
+    if (rec.x < 0) return;
+    const Row w = row_of(a, rec.y, rec.z, rec2.x, rec2.y, rr / kM, rr % kM);
+    if (!w.valid) return;
     const long long token = static_cast<long long>(rec2.z) + w.token;
     const bool live = w.lim > 0;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_ts + w.head * a.o_hs + warp * 4 * C;
-    const float2 ml = merge_row<C, false>(rec.w - i + 1, live, out, part, column, x, o);
+    const float2 ml = merge_row<C, Early>(rec.w - i + 1, live, out, part, column, x, o);
     if (a.lse && warp == 0) a.lse[token * a.H + w.head] = live ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
 }
 
@@ -864,15 +955,18 @@ cudaError_t launch_paged_t(const PagedArgs &a, const CUtensorMap &tq, const CUte
     const unsigned grid = static_cast<unsigned>(a.grid);
     e = launch_pdl(paged_tc_kernel<D, Single>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, tq, tk, tv);
     if (e != cudaSuccess || grid == 1) return e;
-    return launch_pdl(paged_join_kernel<D>, dim3(grid - 1, static_cast<unsigned>(a.slot_rows / 32)), dim3(256), 0, a.stream, a);
+    // Early where units have several CTAs each, as in tree_tc.cu
+    const long long units = static_cast<long long>(a.n_seq) * a.H_kv * a.groups;
+    return launch_pdl(Single && grid >= 3 * units ? paged_join_kernel<D, true> : paged_join_kernel<D, false>,
+                      dim3(grid - 1, static_cast<unsigned>(a.slot_rows / 32)), dim3(256), 0, a.stream, a);
 }
 
 }  // namespace
 
-// Keys on the axis of all units, at most; the rest of the split follows from them.
+// Length of the axis of all units, at most.
 double paged_tc_axis(const PagedArgs &a) {
     const double units = static_cast<double>(a.n_seq) + static_cast<double>(a.T) / a.tokens;
-    return units * a.H_kv * a.groups * (static_cast<double>(a.max_len) + a.T + kN * (kUnitCost + 1));
+    return units * a.H_kv * a.groups * (kWeightTwo * (static_cast<double>(a.max_len) + a.T + kN) + 4 * kN * kUnitCost);
 }
 
 cudaError_t launch_paged_tc(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv) {

@@ -111,16 +111,18 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t *w, int s) {
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
 
 // Clean the V tile at shared address `tile` (kSub blocks of kRows rows of 128
-// bytes) for an MMA: rows from `inside` on become zeros, non-finite elements of
+// bytes; kGroups: kRows / 8 groups of kSub blocks of 8 rows) for an MMA: rows from `inside` on become zeros, non-finite elements of
 // the others too.  Returns whether this thread met one.  `Threads` threads share
 // the tile.  An exponent of all ones carries into the sign bit when one is added
 // to it, so three operations test a pair of bf16, and eight 16-byte loads are in
 // flight before the first test.
-template <int kSub, int kRows, int Threads>
+template <int kSub, int kRows, int Threads, bool kGroups = false>
 __device__ __forceinline__ bool clean_v_tile(uint32_t tile, int inside, int tid) {
     constexpr int kChunks = kSub * kRows * 8, kBatch = 8;
     static_assert(kChunks % (Threads * kBatch) == 0, "whole batches");
     bool bad = false;
+    // row of 16-byte chunk c
+    auto row_of = [](int c) { return kGroups ? (c / (kSub * 64)) * 8 + (c >> 3) % 8 : (c >> 3) % kRows; };
     auto pass = [&](auto partial) {
 #pragma unroll 1
         for (int c0 = tid; c0 < kChunks; c0 += Threads * kBatch) {
@@ -130,7 +132,7 @@ __device__ __forceinline__ bool clean_v_tile(uint32_t tile, int inside, int tid)
             for (int i = 0; i < kBatch; ++i) v[i] = ld_shared_v4(tile + (c0 + i * Threads) * 16);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (decltype(partial)::value && ((c0 + i * Threads) >> 3) % kRows >= inside) {
+                if (decltype(partial)::value && row_of(c0 + i * Threads) >= inside) {
                     st_shared_v4(tile + (c0 + i * Threads) * 16, 0u, 0u, 0u, 0u);
                     continue;
                 }
@@ -141,7 +143,7 @@ __device__ __forceinline__ bool clean_v_tile(uint32_t tile, int inside, int tid)
             // read again, one chunk at a time: nothing stays live for a rare case
 #pragma unroll 1
             for (int c = c0; c < c0 + kBatch * Threads; c += Threads) {
-                if (decltype(partial)::value && (c >> 3) % kRows >= inside) continue;
+                if (decltype(partial)::value && row_of(c) >= inside) continue;
                 const uint4 v = ld_shared_v4(tile + c * 16);
                 const uint32_t n0 = nonfinite2(v.x), n1 = nonfinite2(v.y), n2 = nonfinite2(v.z), n3 = nonfinite2(v.w);
                 if (n0 | n1 | n2 | n3) {
