@@ -1475,9 +1475,9 @@ ATTN_API int attn_rope_append_paged(const void *q, const void *k, const void *v,
 // ------------------------------------------------------------ the table of pages
 
 static long long pages_workspace(int n_out, int n_pages) {
-    // held, pins; first or move; need, stays; the list with its count in front
+    // held, pins; first or move; need, stays, lost; the list with its count in front
     const long long words = (static_cast<long long>(n_pages) + 31) / 32;
-    return (2 * words + n_pages + 2LL * n_out + n_pages + 1) * 4;
+    return (2 * words + n_pages + 3LL * n_out + n_pages + 1) * 4;
 }
 
 ATTN_API long long attn_pages_workspace(int n_out, int n_pages) {
@@ -1544,7 +1544,8 @@ static int pages_impl(const char *who, PagesArgs a, bool step, void *workspace, 
         a.move = rest;
     a.need = rest + a.n_pages;
     a.stays = a.need + a.n_out;
-    a.list = a.stays + a.n_out + 1;
+    a.lost = a.stays + a.n_out;
+    a.list = a.lost + a.n_out + 1;
     a.stream = static_cast<cudaStream_t>(stream);
     const cudaError_t e = step ? launch_pages_step(a) : launch_pages_compact(a);
     return e == cudaSuccess ? ATTN_OK : cuda_fail(e, who);

@@ -296,7 +296,7 @@ struct PagesArgs {
     int words;                  // of 32 pages
     unsigned *held, *pins;      // bits
     int32_t *first;             // step: (n_pages), the lowest row that holds a page partly filled
-    int32_t *need, *stays;      // step: (n_out)
+    int32_t *need, *stays, *lost;  // step: (n_out)
     int32_t *list;              // pages to be given out (list[-1]: their number, or that of the pages held)
     int32_t *move;              // compact: (n_pages), a moved page's place in the list
     cudaStream_t stream;

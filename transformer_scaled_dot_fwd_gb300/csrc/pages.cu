@@ -4,14 +4,13 @@
 // parents[b], cut back or grown to new_len[b] tokens.  No counts of holders are kept from
 // call to call: which pages are held is read off the table, as a set of bits.
 //   1. bits = pinned pages; `first` = nobody                     (pages_clear_kernel)
-//   2. a warp a row: full pages that stay set their bits (a row that shares a page reads
-//      the bit first); a partly filled page takes the lowest row that holds it as such
-//                                                                (pages_mark_kernel)
+//   2. a block a row: full pages that stay set their bits; a partly filled page takes the
+//      lowest row that holds it as such                          (pages_mark_kernel)
 //   3. one block: which rows keep their partly filled page (its first, unless the bit says
 //      that another row holds it full or it is pinned), how many new pages each row wants,
 //      the prefix sums of both the wants and the free pages of each word of bits, and
 //      the list of the lowest free pages, as many as are wanted   (pages_plan_kernel)
-//   4. a warp a row: writes it, and the copy it needs             (pages_write_kernel)
+//   4. a block a row: writes it, and the copy it needs            (pages_write_kernel)
 // Minima, unions and prefix sums do not depend on the order of the threads, so a call gives
 // the same table every time.
 //
@@ -24,6 +23,8 @@
 #include "kernels.h"
 #include "ptx.cuh"
 
+#include <climits>
+
 namespace attn {
 namespace {
 
@@ -32,9 +33,11 @@ constexpr int kNobody = 0x7fffffff;
 
 __device__ __forceinline__ bool is_page(const PagesArgs &a, int page) { return page >= 0 && page < a.n_pages; }
 
+// The kernels behind this one start once all its blocks have passed their wait: what came
+// before the call is complete then, and they read the call's inputs before their own wait.
 __global__ void __launch_bounds__(256) pages_clear_kernel(const PagesArgs a) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int lane = threadIdx.x % 32;
     for (int w = (blockIdx.x * 256 + threadIdx.x) / 32; w < a.words; w += gridDim.x * 8) {
         const int page = w * 32 + lane;
@@ -68,35 +71,58 @@ __device__ __forceinline__ Kept kept_of(const PagesArgs &a, int b) {
     return k;
 }
 
-__global__ void __launch_bounds__(256) pages_mark_kernel(const PagesArgs a) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int b = (blockIdx.x * 256 + threadIdx.x) / 32, lane = threadIdx.x % 32;
-    if (b >= a.n_out) return;
-    const Kept k = kept_of(a, b);
-    const int whole = a.first ? k.full : k.full + (k.part != 0);  // compaction: every page alike
-    int lost = 0;  // entries that are no pages: asked for anew
-    for (int i0 = 0; i0 < whole; i0 += 128) {
-        int page[4];
+constexpr int kRowThreads = 128;
+
+// A row's first entries, kEarly of each thread, on their way while the kernel waits.
+constexpr int kEarly = 4;
+struct Early {
+    int page[kEarly];
+    __device__ __forceinline__ Early(const int32_t *row, int n) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) page[y] = i0 + 32 * y + lane < whole ? k.old[i0 + 32 * y + lane] : -1;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            if (i0 + 32 * y + lane >= whole) continue;
-            if (!is_page(a, page[y])) {
-                ++lost;
-                continue;
-            }
-            const unsigned bit = 1u << (page[y] % 32);
-            if (!(*const_cast<volatile unsigned *>(&a.held[page[y] / 32]) & bit)) atomicOr(&a.held[page[y] / 32], bit);
+        for (int y = 0; y < kEarly; ++y) {
+            const int i = static_cast<int>(threadIdx.x) + y * kRowThreads;
+            page[y] = i < n ? row[i] : -1;
         }
     }
-    if (!a.first) return;
+    // take(i, page) for entries [0, n) of the row
+    template <typename Take>
+    __device__ __forceinline__ void each(const int32_t *row, int n, Take take) const {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) lost += __shfl_xor_sync(0xffffffffu, lost, d);
-    if (lane == 0) {
-        a.need[b] = lost;
-        if (k.part && is_page(a, k.old[k.full])) atomicMin(&a.first[k.old[k.full]], b);
+        for (int y = 0; y < kEarly; ++y) {
+            const int i = static_cast<int>(threadIdx.x) + y * kRowThreads;
+            if (i < n) take(i, page[y]);
+        }
+#pragma unroll 4
+        for (int i = static_cast<int>(threadIdx.x) + kEarly * kRowThreads; i < n; i += kRowThreads) take(i, row[i]);
+    }
+};
+
+// One block a row.
+__global__ void __launch_bounds__(kRowThreads) pages_mark_kernel(const PagesArgs a) {
+    griddep_launch_dependents();
+    const int b = blockIdx.x, tid = threadIdx.x;
+    const Kept k = kept_of(a, b);
+    const int whole = a.first ? k.full : k.full + (k.part != 0);  // compaction: every page alike
+    const Early early(k.old, whole);
+    const int last = k.part ? k.old[k.full] : -1;
+    griddep_wait();
+    int lost = 0;  // entries that are no pages: asked for anew
+    early.each(k.old, whole, [&](int, int page) {
+        if (is_page(a, page))
+            atomicOr(&a.held[page / 32], 1u << (page % 32));
+        else
+            ++lost;
+    });
+    if (!a.first) return;
+    if (tid == 0 && is_page(a, last)) atomicMin(&a.first[last], b);
+    __shared__ int sums[kRowThreads / 32];
+    lost = __reduce_add_sync(0xffffffffu, lost);
+    if (tid % 32 == 0) sums[tid / 32] = lost;
+    __syncthreads();
+    if (tid == 0) {
+        int all = 0;
+        for (int w = 0; w < kRowThreads / 32; ++w) all += sums[w];
+        a.lost[b] = all;
     }
 }
 
@@ -130,27 +156,53 @@ __device__ __forceinline__ unsigned pages_of_word(const PagesArgs &a, int w) {  
     return n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
+// Calls take(page, k) for the k-th set bit, counted on from `from`, of the words that the
+// threads hold (w0 + thread), a lane a bit: neighbours write side by side.  Returns how many
+// there are.  k from `most` on is left out.  The whole block calls it.
+template <typename Take>
+__device__ __forceinline__ int each_bit(int w0, unsigned bits, int from, int most, Take take) {
+    __shared__ int2 words[kPlanThreads];
+    int all;
+    const int at = from + block_prefix(__popc(bits), &all);
+    words[threadIdx.x] = make_int2(static_cast<int>(bits), at);
+    __syncthreads();
+    const int lane = threadIdx.x % 32;
+    for (int w = threadIdx.x / 32; w < kPlanThreads; w += kPlanThreads / 32) {
+        const int2 x = words[w];
+        const unsigned set = static_cast<unsigned>(x.x);
+        if (!set || x.y >= most) continue;
+        const int k = x.y + __popc(set & ((1u << lane) - 1u));
+        if ((set >> lane & 1u) && k < most) take((w0 + w) * 32 + lane, k);
+    }
+    __syncthreads();
+    return all;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PagesArgs a) {
     griddep_launch_dependents();
-    griddep_wait();
     const int tid = threadIdx.x;
     // rows: who keeps its partly filled page, and the wants
     int wants = 0;
-    for (int b0 = 0; b0 < a.n_out; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 == 0 || b0 < a.n_out; b0 += kPlanThreads) {
         const int b = b0 + tid;
-        int want = 0;
+        int want = 0, page = -1;
+        Kept k{};
         if (b < a.n_out) {
-            const Kept k = kept_of(a, b);
+            k = kept_of(a, b);
+            if (k.part) page = k.old[k.full];
+        }
+        if (b0 == 0) griddep_wait();
+        if (b < a.n_out) {
+            const int lost = a.lost[b];
             int stays = 0;
             if (k.part) {
-                const int page = k.old[k.full];
                 // a row whose page this is sets the bit below: no other row is its first
                 if (is_page(a, page) && a.first[page] == b && !(*const_cast<volatile unsigned *>(&a.held[page / 32]) >> (page % 32) & 1u)) {
                     stays = 1;
                     atomicOr(&a.held[page / 32], 1u << (page % 32));
                 }
             }
-            want = a.need[b] + k.pages - k.full - stays;
+            want = lost + k.pages - k.full - stays;
             a.stays[b] = stays;
         }
         int all;
@@ -158,19 +210,12 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PagesArg
         if (b < a.n_out) a.need[b] = at;  // the row's first new page in the list
         wants += all;
     }
-    __threadfence_block();
-    __syncthreads();
+    __syncthreads();  // the bits set above
     int free_pages = 0;
     for (int w0 = 0; w0 < a.words; w0 += kPlanThreads) {
         const int w = w0 + tid;
-        unsigned bits = w < a.words ? ~*const_cast<volatile unsigned *>(&a.held[w]) & pages_of_word(a, w) : 0u;
-        int all;
-        int at = free_pages + block_prefix(__popc(bits), &all);
-        for (; bits && at < wants; ++at) {
-            a.list[at] = w * 32 + __ffs(bits) - 1;
-            bits &= bits - 1;
-        }
-        free_pages += all;
+        const unsigned bits = w < a.words ? ~*const_cast<volatile unsigned *>(&a.held[w]) & pages_of_word(a, w) : 0u;
+        free_pages += each_bit(w0, bits, free_pages, wants, [&](int page, int k) { a.list[k] = page; });
     }
     if (tid == 0) {
         a.list[-1] = free_pages;
@@ -178,41 +223,47 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PagesArg
     }
 }
 
-__global__ void __launch_bounds__(256) pages_write_kernel(const PagesArgs a) {
+// One block a row.
+__global__ void __launch_bounds__(kRowThreads) pages_write_kernel(const PagesArgs a) {
     griddep_launch_dependents();
-    griddep_wait();
-    const int b = (blockIdx.x * 256 + threadIdx.x) / 32, lane = threadIdx.x % 32;
-    if (b >= a.n_out) return;
+    const int b = blockIdx.x, tid = threadIdx.x;
     const Kept k = kept_of(a, b);
-    const int stays = a.stays[b], n_free = a.list[-1];
-    int nth = a.need[b];  // in the list of free pages
+    const Early early(k.old, k.full + (k.part != 0));
+    const int from = k.part ? k.old[k.full] : -1;
+    griddep_wait();
+    const int stays = a.stays[b], n_free = a.list[-1], first = a.need[b], lost = a.lost[b];
+    const int kept = k.full + stays;
     int32_t *out = a.table_out + b * a.out_stride;
-    int to = -1;  // the copy of the partly filled page
-    for (int i0 = 0; i0 < a.max_pages; i0 += 32) {
-        const int i = i0 + lane;
-        int page = -1;
-        if (i < k.full + stays) page = k.old[i];
-        const bool wanted = i < k.pages && (i >= k.full + stays || !is_page(a, page));
-        const unsigned all = __ballot_sync(0xffffffffu, wanted);
-        const int at = nth + __popc(all & ((1u << lane) - 1u));
-        if (wanted) page = at < n_free ? a.list[at] : -1;
-        nth += __popc(all);
-        if (i < a.max_pages) out[i] = page;
-        if (i == k.full) to = page;
+    auto given = [&](int nth) { return nth < n_free ? a.list[nth] : -1; };
+    // new pages: entries that are no pages come first, then those behind the kept ones
+    if (lost == 0) early.each(k.old, kept, [&](int i, int page) { out[i] = page; });
+#pragma unroll 4
+    for (int i = kept + tid; i < a.max_pages; i += kRowThreads) out[i] = i < k.pages ? given(first + lost + i - kept) : -1;
+    if (lost > 0 && tid < 32) {  // rare: one warp counts its way through them
+        int nth = first;
+        for (int i0 = 0; i0 < kept; i0 += 32) {
+            const int i = i0 + tid;
+            int page = i < kept ? k.old[i] : 0;
+            const bool wanted = i < kept && !is_page(a, page);
+            const unsigned all = __ballot_sync(0xffffffffu, wanted);
+            if (wanted) page = given(nth + __popc(all & ((1u << tid) - 1u)));
+            nth += __popc(all);
+            if (i < kept) out[i] = page;
+        }
     }
-    to = __shfl_sync(0xffffffffu, to, k.full % 32);
-    if (lane == 0) {
+    if (tid == kRowThreads - 1) {
         a.len_out[b] = k.len;
-        const int from = k.part ? k.old[k.full] : -1;
-        const bool copied = k.part && !stays && is_page(a, from) && to >= 0;
+        // a page not kept is the first entry behind those that are
+        const int to = k.part && !stays ? given(first + lost) : -1;
+        const bool copied = is_page(a, from) && to >= 0;
         a.copies[3 * b] = copied ? from : -1;
         a.copies[3 * b + 1] = copied ? to : -1;
         a.copies[3 * b + 2] = copied ? k.part : 0;
     }
 }
 
-// Compaction: n pages are held or pinned; lists the free ones below n, then the movable ones
-// from n on with the places they go to.
+// Compaction: n pages are held or pinned; the movable ones from n on go to the free ones
+// below n.
 __global__ void __launch_bounds__(kPlanThreads) pages_moves_kernel(const PagesArgs a) {
     griddep_launch_dependents();
     griddep_wait();
@@ -222,36 +273,25 @@ __global__ void __launch_bounds__(kPlanThreads) pages_moves_kernel(const PagesAr
     int all;
     block_prefix(n, &all);
     n = all;
+    auto below = [&](int w) { return n - w * 32 >= 32 ? 0xffffffffu : n > w * 32 ? (1u << (n - w * 32)) - 1u : 0u; };  // pages < n
     int holes = 0, moves = 0;
-    for (int w0 = 0; w0 < a.words; w0 += kPlanThreads) {
+    for (int w0 = 0; w0 * 32 < n; w0 += kPlanThreads) {
         const int w = w0 + tid;
-        unsigned free_bits = 0, moved = 0;
-        if (w < a.words) {
-            const unsigned held = a.held[w];
-            const unsigned below = n - w * 32 >= 32 ? 0xffffffffu : n > w * 32 ? (1u << (n - w * 32)) - 1u : 0u;  // pages < n
-            free_bits = ~held & below;
-            moved = held & ~below & ~a.pins[w];
-        }
-        int at = holes + block_prefix(__popc(free_bits), &all);
-        holes += all;
-        for (; free_bits; ++at, free_bits &= free_bits - 1) a.list[at] = w * 32 + __ffs(free_bits) - 1;
-        at = moves + block_prefix(__popc(moved), &all);
-        moves += all;
-        for (; moved; ++at, moved &= moved - 1) {
-            const int page = w * 32 + __ffs(moved) - 1;
-            a.move[page] = at;
-            a.copies[3 * at] = page;
-            a.copies[3 * at + 2] = a.P;
-        }
+        holes += each_bit(w0, w < a.words ? ~a.held[w] & below(w) : 0u, holes, INT_MAX, [&](int page, int k) { a.list[k] = page; });
     }
-    __syncthreads();
-    for (int i = tid; i < a.n_copies; i += kPlanThreads) {
-        if (i < moves) {
-            a.copies[3 * i + 1] = a.list[i];
-        } else {
-            a.copies[3 * i] = a.copies[3 * i + 1] = -1;
-            a.copies[3 * i + 2] = 0;
-        }
+    for (int w0 = n / 32 / kPlanThreads * kPlanThreads; w0 < a.words; w0 += kPlanThreads) {
+        const int w = w0 + tid;
+        moves += each_bit(w0, w < a.words ? a.held[w] & ~below(w) & ~a.pins[w] : 0u, moves, INT_MAX, [&](int page, int k) {
+            const int to = a.list[k];
+            a.move[page] = to;
+            a.copies[3 * k] = page;
+            a.copies[3 * k + 1] = to;
+            a.copies[3 * k + 2] = a.P;
+        });
+    }
+    for (int i = moves + tid; i < a.n_copies; i += kPlanThreads) {
+        a.copies[3 * i] = a.copies[3 * i + 1] = -1;
+        a.copies[3 * i + 2] = 0;
     }
     if (tid == 0) {
         a.list[-1] = n;
@@ -259,22 +299,25 @@ __global__ void __launch_bounds__(kPlanThreads) pages_moves_kernel(const PagesAr
     }
 }
 
-__global__ void __launch_bounds__(256) pages_rename_kernel(const PagesArgs a) {
+// One block a row.
+__global__ void __launch_bounds__(kRowThreads) pages_rename_kernel(const PagesArgs a) {
     griddep_launch_dependents();
-    griddep_wait();
-    const int b = (blockIdx.x * 256 + threadIdx.x) / 32, lane = threadIdx.x % 32;
-    if (b >= a.n_out) return;
+    const int b = blockIdx.x;
     const Kept k = kept_of(a, b);
+    const Early early(k.old, k.pages);
+    griddep_wait();
     const int n = a.list[-1];
-    for (int i = lane; i < a.max_pages; i += 32) {
-        int page = -1;
-        if (i < k.pages && is_page(a, page = k.old[i])) {
-            if (page >= n && !(a.pins[page / 32] >> (page % 32) & 1u)) page = a.list[a.move[page]];
+    int32_t *out = a.table_out + b * a.out_stride;
+    early.each(k.old, k.pages, [&](int i, int page) {
+        if (is_page(a, page)) {
+            const int to = a.move[page];  // of a page that moves
+            if (page >= n && !(a.pins[page / 32] >> (page % 32) & 1u)) page = to;
         } else {
             page = -1;
         }
-        a.table_out[b * a.out_stride + i] = page;
-    }
+        out[i] = page;
+    });
+    for (int i = k.pages + static_cast<int>(threadIdx.x); i < a.max_pages; i += kRowThreads) out[i] = -1;
 }
 
 // ------------------------------------------------------------ copies
@@ -282,10 +325,10 @@ __global__ void __launch_bounds__(256) pages_rename_kernel(const PagesArgs a) {
 // Block (c, y): pair c of the list, y = layer * 2 + (0: keys, 1: values).  Vec is what a
 // thread moves at once; a row is 2^unit_shift of them, 256 at most.
 template <typename Vec>
-__global__ void __launch_bounds__(256) pages_copy_kernel(const PagesCopyArgs a) {
+__global__ void __launch_bounds__(256, 5) pages_copy_kernel(const PagesCopyArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 4;
     const int src = a.copies[3 * blockIdx.x], dst = a.copies[3 * blockIdx.x + 1];
     const int rows = min(max(a.copies[3 * blockIdx.x + 2], 0), a.P);
     if (src < 0 || src >= a.n_pages || dst < 0 || dst >= a.n_pages || src == dst) return;
@@ -318,23 +361,21 @@ cudaError_t launch_clear(const PagesArgs &a) {
     return launch_pdl(pages_clear_kernel, dim3(static_cast<unsigned>(blocks > 0 ? blocks : 1)), dim3(256), 0, a.stream, a);
 }
 
-dim3 warps_for(long long rows) { return dim3(static_cast<unsigned>((rows + 7) / 8)); }
-
 }  // namespace
 
 cudaError_t launch_pages_step(const PagesArgs &a) {
     cudaError_t e = launch_clear(a);
-    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_mark_kernel, warps_for(a.n_out), dim3(256), 0, a.stream, a);
+    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_mark_kernel, dim3(static_cast<unsigned>(a.n_out)), dim3(kRowThreads), 0, a.stream, a);
     if (e == cudaSuccess) e = launch_pdl(pages_plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a);
-    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_write_kernel, warps_for(a.n_out), dim3(256), 0, a.stream, a);
+    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_write_kernel, dim3(static_cast<unsigned>(a.n_out)), dim3(kRowThreads), 0, a.stream, a);
     return e;
 }
 
 cudaError_t launch_pages_compact(const PagesArgs &a) {
     cudaError_t e = launch_clear(a);
-    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_mark_kernel, warps_for(a.n_out), dim3(256), 0, a.stream, a);
+    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_mark_kernel, dim3(static_cast<unsigned>(a.n_out)), dim3(kRowThreads), 0, a.stream, a);
     if (e == cudaSuccess) e = launch_pdl(pages_moves_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a);
-    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_rename_kernel, warps_for(a.n_out), dim3(256), 0, a.stream, a);
+    if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_rename_kernel, dim3(static_cast<unsigned>(a.n_out)), dim3(kRowThreads), 0, a.stream, a);
     return e;
 }
 
