@@ -1049,6 +1049,10 @@ ATTN_API int attn_decode_tree(const void *q, const void *kcache, const void *vca
 // Returns the bytes of workspace, or a negative code with its reason.
 static long long paged_sizes(const char *who, PagedArgs &a, bool ragged, int dtype) {
     const int G = a.H / a.H_kv;
+    // key / P as the upper half of key * ceil(2^32 / P): right while key times what was rounded up
+    // stays below 2^32
+    const unsigned long long magic = ((1ULL << 32) + a.P - 1) / a.P, over = magic * a.P - (1ULL << 32);
+    a.page_magic = over * static_cast<unsigned long long>(a.max_len) < (1ULL << 32) ? static_cast<unsigned>(magic) : 0u;
     a.n_sm = num_sms();
     a.per_seq = ragged || a.n_seq < 1 ? 0 : a.T / a.n_seq;
     const long long rows = static_cast<long long>(a.T) * a.H;

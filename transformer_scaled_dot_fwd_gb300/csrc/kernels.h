@@ -126,6 +126,7 @@ struct PagedArgs {
     long long q_ts, q_hs, o_ts, o_hs, k_ps, k_hs, k_rs, v_ps, v_hs, v_rs, table_stride;
     int T, n_seq, per_seq, H, H_kv, D, P, n_pages;
     int max_len;                // keys that a row of the page table holds
+    unsigned page_magic;        // ceil(2^32 / P) where that divides every key exactly, or 0
     float scale;
     // bf16: row tiles of `tokens` tokens by `heads` heads of one of `groups` groups of
     // the query heads of a cached head; boxes of `box` rows of a page, box_tokens tokens of q

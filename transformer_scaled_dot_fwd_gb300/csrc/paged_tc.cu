@@ -412,8 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // This lane's box of the next tile to be looked up: its key, its entry of the table and its row
             // in that page.  A box past the last visible key is not copied: kNoBox.
             const int k_head = head * a.k_hstep, v_head = head * a.v_hstep;
-            int next_key = r.j0 * kN + i * a.box, next_row = next_key % a.P;
-            const int32_t *next_entry = a.page_table + static_cast<long long>(r.seq) * a.table_stride + next_key / a.P;
+            int next_key = r.j0 * kN + i * a.box, next_row = page_of_key(a, next_key);
+            const int32_t *next_entry = a.page_table + static_cast<long long>(r.seq) * a.table_stride + next_row;
+            next_row = next_key - next_row * a.P;
             const int last_key = min(r.keys, (r.j0 + r.n) * kN);
             struct Box {
                 int page, row;
@@ -844,11 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int32_t *table = a.page_table + static_cast<long long>(r.seq) * a.table_stride;
 #pragma unroll 1
                         for (int key = (r.j0 + edge_of(r)) * kN; key < end; ++key) {
-                            const int page = table[key / a.P];
+                            const int entry = page_of_key(a, key), page = table[entry];
                             if (!is_page(a, page)) continue;
                             const uint32_t *vr = reinterpret_cast<const uint32_t *>(
                                 static_cast<const __nv_bfloat16 *>(a.v) + page * a.v_ps + (r.hs / a.groups) * a.v_hs +
-                                (key % a.P) * a.v_rs + c * 32);
+                                (key - entry * a.P) * a.v_rs + c * 32);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const uint32_t v = vr[e], nf = nonfinite2(v);

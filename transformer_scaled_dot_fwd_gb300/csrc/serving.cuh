@@ -25,6 +25,11 @@ __device__ __forceinline__ int count_le(const int32_t *v, int n, int t, int lane
     return lo;
 }
 
+// Entry of the page table that holds a key (a division is some 40 instructions).
+__device__ __forceinline__ int page_of_key(const PagedArgs &a, int key) {
+    return a.page_magic ? static_cast<int>(__umulhi(static_cast<unsigned>(key), a.page_magic)) : key / a.P;
+}
+
 // What the draft of one sequence looks like: L cache rows, the last n of them
 // drafted, so draft token j's key sits at row past + j (none when negative).
 struct Draft {
