@@ -28,6 +28,26 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// launch_pdl with clusters of `cluster` consecutive blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned cluster, unsigned grid, unsigned block, size_t smem,
+                            cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 struct FwdArgs {
     const void *q, *k, *v;  // (B, H, Sq|Skv, D), device
     void *out;              // (B, H, Sq, D), device
@@ -134,6 +154,7 @@ struct PagedArgs {
     // the pages' views: head h of page p is entry p pstep + h hstep; halves: boxes of 64 columns
     int halves, k_pstep, k_hstep, v_pstep, v_hstep;
     int single;                 // every unit has one row tile
+    int cluster;                // every unit is a cluster of kPagedCluster CTAs; no workspace
     int grid;                   // CTAs at most
     int n_split;                // fp32: splits of the keys
     // Partial results: O unnormalised [D] and (running max in log2 units, sum) of
@@ -151,6 +172,7 @@ struct PagedArgs {
 // box / 8 x 1 boxes (halves: as (D, P, H_kv, n_pages) with 64 x 8 x 1 x 1 boxes).
 cudaError_t launch_paged_tc(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv);
 double paged_tc_axis(const PagedArgs &a);
+constexpr int kPagedCluster = 8;
 cudaError_t launch_paged_f32(const PagedArgs &a);
 // fp32: blocks of 32 rows of a cached head, and splits of the keys (1, 2, 4 or 8: CTAs of
 // a cluster; more: merged through the workspace).

@@ -21,6 +21,10 @@
 // O, running max and sum in fp32 in the CTA's slots of the workspace, for a merge in
 // the order of the keys; whole units are written out directly.
 //
+// Few units of one row tile (one user, or a few) are clusters of eight CTAs instead, with an
+// eighth of the unit's tiles each, whose parts meet in distributed shared memory: no axis, no
+// workspace, no second kernel.
+//
 // Pages.  A 128-key tile is copied by boxes that lie in one page each (rows: the largest
 // power of two up to 128 that divides P), each lane of the loading warp with its own box
 // and its own entry of the table, fetched a tile ahead.  Boxes past the last visible key are not
@@ -89,6 +93,16 @@ __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
 
 __device__ __forceinline__ bool is_page(const PagedArgs &a, int page) { return page >= 0 && page < a.n_pages; }
+
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ long long prefix(long long v, int lane) {
+#pragma unroll 1
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += y;
+    }
+    return v;
+}
 
 // One sequence: first token, new tokens, keys.
 struct Seq {
@@ -226,11 +240,39 @@ __device__ __forceinline__ Row row_of(const PagedArgs &a, int hs, int tok0, int 
     return w;
 }
 
-template <int D, bool Single>
+// A cluster's CTA leaves its part of its rows in its K/V ring: O, D + 4 floats a row, then max
+// and sum.
+template <int D>
+__device__ __forceinline__ float2 *cluster_ml(uint8_t *ring) {
+    return reinterpret_cast<float2 *>(ring + kM * (D + 4) * 4);
+}
+
+// Adds to columns [c, c + 32) of a row the non-finite values that the guard took out of the
+// run's edge tiles, of the keys that the row sees.
+__device__ __forceinline__ void add_nonfinite(const PagedArgs &a, const Run &r, int lim, int c, uint32_t (&o)[32]) {
+    const int end = min(lim, (r.j0 + r.n) * kN);
+    const int32_t *table = a.page_table + static_cast<long long>(r.seq) * a.table_stride;
+#pragma unroll 1
+    for (int key = (r.j0 + edge_of(r)) * kN; key < end; ++key) {
+        const int entry = page_of_key(a, key), page = table[entry];
+        if (!is_page(a, page)) continue;
+        const uint32_t *vr = reinterpret_cast<const uint32_t *>(
+            static_cast<const __nv_bfloat16 *>(a.v) + page * a.v_ps + (r.hs / a.groups) * a.v_hs + (key - entry * a.P) * a.v_rs + c);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t v = vr[e], nf = nonfinite2(v);
+            if (nf & 0xffffu) o[2 * e] = f2u(u2f(o[2 * e]) + bf16lo_to_f32(v));
+            if (nf & 0xffff0000u) o[2 * e + 1] = f2u(u2f(o[2 * e + 1]) + bf16hi_to_f32(v));
+        }
+    }
+}
+
+template <int D, bool Single, bool Cluster>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv) {
     using L = Layout<D, Single>;
+    static_assert(!Cluster || Single, "a cluster has one row tile");
     constexpr int kStages = L::kStages;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
@@ -287,44 +329,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Units u(q, tokens, a.tokens);
             return u.at(u.nu) * per;
         };
-        long long total = 0;  // length of the axis (the host has checked that it fits)
-        Seq mine{0, 0, 0};    // sequence b0 + lane
-        for (int b0 = lane; b0 < a.n_seq; b0 += 32) {
-            mine = seq_of(a, b0);
-            total += cost_of(mine);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        // CTA i of N takes what begins in [total i / N, total (i + 1) / N)
-        const long long most = total / (4 * kN * kMinTiles);
-        const int N = static_cast<int>(min(max(most, 1ll), static_cast<long long>(gridDim.x))), I = blockIdx.x;
-        const bool idle = I >= N || total == 0;
-        const long long each = quotient(total, N);
-        const int odd = static_cast<int>(total - each * N);
-        const long long lo = idle ? 0 : each * I + odd * I / N, hi = idle ? 0 : each * (I + 1) + odd * (I + 1) / N;
-        // sequence that holds position lo, and the first position of its units
-        int b = 0;
-        long long base = 0;
-        for (int b0 = 0; !idle && b0 < a.n_seq; b0 += 32) {
-            if (a.n_seq > 32) mine = seq_of(a, min(b0 + lane, a.n_seq - 1));
-            const long long t = b0 + lane < a.n_seq ? cost_of(mine) : 0;
-            long long sum = t;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += y;
+        // A cluster's CTAs share the tiles of its one unit; else CTA I of N takes what begins in
+        // [total I / N, total (I + 1) / N) of the axis (whose length the host has checked).
+        long long total = 0, lo = 0, hi = 0, base = 0;  // base: first position of sequence b's units
+        int N = 1, b = 0;
+        bool idle = false;
+        Seq q{0, 0, 0};
+        if (Cluster) {
+            b = static_cast<int>(blockIdx.x) / (kPagedCluster * per);
+            q = seq_of(a, b);
+            idle = q.n == 0;
+            hi = LLONG_MAX;
+        } else {
+            Seq mine{0, 0, 0};  // sequence b0 + lane
+            long long t = 0, sum = 0;
+            for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+                mine = seq_of(a, min(b0 + lane, a.n_seq - 1));
+                t = b0 + lane < a.n_seq ? cost_of(mine) : 0;
+                total += t;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, base + sum > lo);
-            if (past) {
-                const int f = __ffs(past) - 1;
-                b = b0 + f;
-                base += __shfl_sync(0xffffffffu, sum - t, f);
-                break;
+            if (a.n_seq <= 32) {
+                sum = prefix(t, lane);
+                total = __shfl_sync(0xffffffffu, sum, 31);
+            } else {
+#pragma unroll 1
+                for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
             }
-            base += __shfl_sync(0xffffffffu, sum, 31);
+            const long long most = total / (4 * kN * kMinTiles);
+            N = static_cast<int>(min(max(most, 1ll), static_cast<long long>(gridDim.x)));
+            const int I = blockIdx.x;
+            idle = I >= N || total == 0;
+            const long long each = quotient(total, N);
+            const int odd = static_cast<int>(total - each * N);
+            if (!idle) lo = each * I + odd * I / N, hi = each * (I + 1) + odd * (I + 1) / N;
+            for (int b0 = 0; !idle && b0 < a.n_seq; b0 += 32) {  // the sequence that holds position lo
+                if (a.n_seq > 32) {
+                    mine = seq_of(a, min(b0 + lane, a.n_seq - 1));
+                    t = b0 + lane < a.n_seq ? cost_of(mine) : 0;
+                    sum = prefix(t, lane);
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, base + sum > lo);
+                if (past) {
+                    const int f = __ffs(past) - 1;
+                    b = b0 + f;
+                    base += __shfl_sync(0xffffffffu, sum - t, f);
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, sum, 31);
+            }
+            q = Seq{__shfl_sync(0xffffffffu, mine.c0, b % 32), __shfl_sync(0xffffffffu, mine.n, b % 32),
+                    __shfl_sync(0xffffffffu, mine.L, b % 32)};
         }
-        Seq q{__shfl_sync(0xffffffffu, mine.c0, b % 32), __shfl_sync(0xffffffffu, mine.n, b % 32),
-              __shfl_sync(0xffffffffu, mine.L, b % 32)};
         Units units(q, tokens, a.tokens);
         int hs = 0, u = 0, j = 0;
         long long pos = base;  // of unit u of hs
@@ -344,7 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         };
-        if (!idle) {
+        if (Cluster) {
+            hs = static_cast<int>(blockIdx.x) / kPagedCluster % per;
+            j = tiles_of(keys_of(0)) * static_cast<int>(cluster_rank()) / kPagedCluster;
+        } else if (!idle) {
             const long long one = units.at(units.nu);
             hs = static_cast<int>(quotient(lo - base, one));
             pos += hs * one;
@@ -376,11 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k >= kRing && !(ok = mbar_wait_warp(&bars.run_empty[slot], ((k / kRing) - 1) & 1, &bars.abort))) break;
             Run r{0, 0, 0, 0, 0, -1, 0, 0, 0, 0};
             int nt = 0;
-            if (!idle && b < a.n_seq && pos < hi) {
+            if (!idle && b < a.n_seq && pos < hi) {  // r.n = 0: a CTA of a cluster without a tile
                 const int keys = keys_of(u);
                 nt = tiles_of(keys);
-                const int end = units.cut(hi - pos, nt);
-                if (end > j) {
+                const int end = Cluster ? nt * static_cast<int>(cluster_rank() + 1) / kPagedCluster : units.cut(hi - pos, nt);
+                if (Cluster || end > j) {
                     r.seq = b;
                     r.hs = hs;
                     r.tok0 = u * tokens;
@@ -390,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.c0 = q.c0;
                     r.j0 = j;
                     r.n = end - j;
-                    r.slot = r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
-                    if (j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w,
+                    r.slot = Cluster || r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
+                    if (!Cluster && j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w,
                                                // the last whose begin leaves enough of it
                         const long long last = pos + static_cast<long long>(nt - units.least) * units.tile;
                         rec = make_int4(b, hs, r.tok0, static_cast<int>(quotient((last + 1) * N - 1, total)));
@@ -464,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++stage == kStages) stage = 0, stage_phase ^= 1;
             };
             auto load_q = [&](int tiles) {  // once the last run's last S MMA has read the buffers
+                if (r.n == 0) return;
                 if (!ok || (k > 0 && !(ok = mbar_wait_warp(&bars.q_free, (k - 1) & 1, &bars.abort)))) return;
                 if (lane == 0) {
                     const int h0 = head * (a.H / a.H_kv) + r.hs % a.groups * a.heads;
@@ -501,6 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ++k;
+            if (Cluster) {
+                b = a.n_seq;
+                continue;
+            }
             j += r.n;
             if (j == nt) next_unit();
         }
@@ -509,15 +572,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *static_cast<volatile int *>(&bars.req[requests % kGuardRing].stage) = kEnd;
                 mbar_arrive(&bars.guard_full[requests % kGuardRing]);
             }
-            int4 *out = reinterpret_cast<int4 *>(a.merge) + 2 * blockIdx.x;
-            out[0] = rec;
-            out[1] = rec2;
+            if (!Cluster) {
+                int4 *out = reinterpret_cast<int4 *>(a.merge) + 2 * blockIdx.x;
+                out[0] = rec;
+                out[1] = rec2;
+            }
             // never leave with copies still landing in shared memory
             volatile int never = 0;
             if (q_loads > 0) mbar_wait(&bars.q_full, (q_loads - 1) & 1, &never);
             for (int x = max(0, issued - kStages); x < issued; ++x)
                 mbar_wait(&bars.kv_full[x % kStages], (x / kStages) & 1, &never);
         }
+        __syncwarp();
+        if (Cluster) cluster_sync(), cluster_sync();
     } else if (warp == 1) {
         // ================================================================ MMA issuer
         regs_dec<kRegsOther>();
@@ -560,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&bars.run_empty[k % kRing]);
             const int n = __shfl_sync(0xffffffffu, r.n, 0);
             if (n < 0) break;
+            if (Cluster && n == 0) continue;
             const int edge = __shfl_sync(0xffffffffu, edge_of(r), 0);
             const bool one = Single || __shfl_sync(0xffffffffu, r.left, 0) <= a.tokens;
             if (!(ok = mbar_wait_warp(&bars.q_full, k & 1, &bars.abort))) break;
@@ -645,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit_warp(&bars.mma_done);
         volatile int never = 0;
         mbar_wait_warp(&bars.mma_done, 0, &never);
+        if (Cluster) cluster_sync(), cluster_sync();
     } else if (warp < 4) {
         // ================================================================ guard of the edge V tiles
         regs_dec<kRegsOther>();
@@ -665,6 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.guard_clean[slot]);
         }
+        __syncwarp();
+        if (Cluster) cluster_sync(), cluster_sync();
     } else {
         // ================================================================ softmax streams
         regs_inc<kRegsSoftmax>();
@@ -808,6 +879,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (used) ++o_uses[y];
             }
             tc_fence_after();
+            if (Cluster) {
+                // this CTA's part of its rows, for the cluster: the ring is free, every MMA on it is complete
+                float *part = reinterpret_cast<float *>(ring) + row * (D + 4);
+                if (__any_sync(0xffffffffu, w.valid)) {
+#pragma unroll 1
+                    for (int c = x * (D / 64); c < (x + 1) * (D / 64); ++c) {
+                        uint32_t o[32], o1[32];
+                        tmem_ld32(t_lane + 256u + c * 32, o);
+                        tmem_ld32(t_lane + 256u + D + c * 32, o1);
+                        tmem_ld_wait();
+                        reg_fence32(o);
+                        reg_fence32(o1);
+                        const float wa = x ? wt_other : wt, wb = x ? wt : wt_other;  // of O0, of O1
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = r.n == 0 || !live ? 0u : f2u(other ? fmaf(wa, u2f(o[e]), wb * u2f(o1[e])) : wa * u2f(o[e]));
+                        if (*static_cast<volatile int *>(&bars.spoiled[k % kRing]) != 0 && live)
+                            add_nonfinite(a, r, w.lim, c * 32, o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4 *>(part + c * 32 + 4 * e) =
+                                make_float4(u2f(o[4 * e]), u2f(o[4 * e + 1]), u2f(o[4 * e + 2]), u2f(o[4 * e + 3]));
+                    }
+                }
+                if (x == 0) cluster_ml<D>(ring)[row] = make_float2(m, sum);  // both streams hold the same
+                mbar_arrive(&bars.run_empty[k % kRing]);
+                tc_fence_before();
+                continue;
+            }
             const bool write = ok && w.valid;
             const bool spoiled = *static_cast<volatile int *>(&bars.spoiled[k % kRing]) != 0 && live;
             const float inv = 1.f / sum;
@@ -840,24 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e)
                             o[e] = f2u(other ? fmaf(wa, u2f(o[e]), wb * u2f(o1[e])) : wa * u2f(o[e]));
                     }
-                    if (spoiled) {  // add the non-finite values of the edge tiles that this row sees
-                        const int end = min(w.lim, (r.j0 + r.n) * kN);
-                        const int32_t *table = a.page_table + static_cast<long long>(r.seq) * a.table_stride;
-#pragma unroll 1
-                        for (int key = (r.j0 + edge_of(r)) * kN; key < end; ++key) {
-                            const int entry = page_of_key(a, key), page = table[entry];
-                            if (!is_page(a, page)) continue;
-                            const uint32_t *vr = reinterpret_cast<const uint32_t *>(
-                                static_cast<const __nv_bfloat16 *>(a.v) + page * a.v_ps + (r.hs / a.groups) * a.v_hs +
-                                (key - entry * a.P) * a.v_rs + c * 32);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const uint32_t v = vr[e], nf = nonfinite2(v);
-                                if (nf & 0xffffu) o[2 * e] = f2u(u2f(o[2 * e]) + bf16lo_to_f32(v));
-                                if (nf & 0xffff0000u) o[2 * e + 1] = f2u(u2f(o[2 * e + 1]) + bf16hi_to_f32(v));
-                            }
-                        }
-                    }
+                    if (spoiled) add_nonfinite(a, r, w.lim, c * 32, o);
                     if (write && r.slot >= 0) {
                         // four columns of all the slot's rows side by side: a warp writes 512 bytes at once
                         float4 *dst = reinterpret_cast<float4 *>(a.part_o) +
@@ -898,6 +981,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             // both streams are done with each other's O and with ex
             if (one) join();
+        }
+        if (Cluster) {
+            // each CTA joins its share of the columns, the parts in the order of the keys
+            __syncwarp();
+            cluster_sync();
+            constexpr int kQuads = D / kPagedCluster / 4;  // of a CTA's columns
+            const Run r = read_run(bars, 0);
+            const unsigned rank = cluster_rank();
+#pragma unroll 1
+            for (int i = static_cast<int>(threadIdx.x) - 128; i < kM * kQuads; i += 256) {
+                const int rr = i / kQuads, c = static_cast<int>(rank) * (D / kPagedCluster) + i % kQuads * 4;
+                const Row w = row_of(a, r.hs, r.tok0, r.left, r.past, 0, rr);
+                if (!w.valid) continue;
+                float2 ml[kPagedCluster];
+                float4 o[kPagedCluster];
+                float M = -INFINITY, sum = 0.f;
+                const float *part = reinterpret_cast<const float *>(ring) + rr * (D + 4) + c;
+#pragma unroll
+                for (unsigned y = 0; y < kPagedCluster; ++y) {
+                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                                 : "=f"(ml[y].x), "=f"(ml[y].y) : "r"(map_rank(cluster_ml<D>(ring) + rr, y)));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(o[y].x), "=f"(o[y].y), "=f"(o[y].z), "=f"(o[y].w) : "r"(map_rank(part, y)));
+                }
+#pragma unroll
+                for (int y = 0; y < kPagedCluster; ++y) M = fmaxf(M, ml[y].x);
+                const float ref = M == -INFINITY ? 0.f : M;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < kPagedCluster; ++y) {
+                    const float f = ex2_approx(ml[y].x - ref);
+                    sum = fmaf(f, ml[y].y, sum);
+                    acc = make_float4(fmaf(f, o[y].x, acc.x), fmaf(f, o[y].y, acc.y), fmaf(f, o[y].z, acc.z), fmaf(f, o[y].w, acc.w));
+                }
+                const bool live = w.lim > 0;
+                const float inv = 1.f / sum;
+                const long long token = static_cast<long long>(r.c0) + w.token;
+                store4(static_cast<__nv_bfloat16 *>(a.out) + token * a.o_ts + w.head * a.o_hs + c,
+                       live ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+                if (a.lse && c == 0) a.lse[token * a.H + w.head] = live ? (M + log2f(sum)) * kLn2 : -INFINITY;
+            }
+            __syncwarp();
+            cluster_sync();  // the parts have been read
         }
     }
 
@@ -948,18 +1074,25 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedArgs a) {
     if (a.lse && warp == 0) a.lse[token * a.H + w.head] = live ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool Single>
+template <int D, bool Single, bool Cluster>
 cudaError_t launch_paged_t(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv) {
     using L = Layout<D, Single>;
-    cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, Single>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    const auto kernel = paged_tc_kernel<D, Single, Cluster>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(a.grid);
-    e = launch_pdl(paged_tc_kernel<D, Single>, dim3(grid), dim3(kThreads), L::kSmemBytes, a.stream, a, tq, tk, tv);
-    if (e != cudaSuccess || grid == 1) return e;
+    e = launch_clusters(kernel, Cluster ? kPagedCluster : 1u, grid, kThreads, L::kSmemBytes, a.stream, a, tq, tk, tv);
+    if (Cluster || e != cudaSuccess || grid == 1) return e;
     // Early where units have several CTAs each, as in tree_tc.cu
     const long long units = static_cast<long long>(a.n_seq) * a.H_kv * a.groups;
     return launch_pdl(Single && grid >= 3 * units ? paged_join_kernel<D, true> : paged_join_kernel<D, false>,
                       dim3(grid - 1, static_cast<unsigned>(a.slot_rows / 32)), dim3(256), 0, a.stream, a);
+}
+
+template <int D>
+cudaError_t launch_paged_d(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv) {
+    return a.cluster ? launch_paged_t<D, true, true>(a, tq, tk, tv)
+           : a.single ? launch_paged_t<D, true, false>(a, tq, tk, tv) : launch_paged_t<D, false, false>(a, tq, tk, tv);
 }
 
 }  // namespace
@@ -971,8 +1104,7 @@ double paged_tc_axis(const PagedArgs &a) {
 }
 
 cudaError_t launch_paged_tc(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv) {
-    if (a.D == 64) return a.single ? launch_paged_t<64, true>(a, tq, tk, tv) : launch_paged_t<64, false>(a, tq, tk, tv);
-    return a.single ? launch_paged_t<128, true>(a, tq, tk, tv) : launch_paged_t<128, false>(a, tq, tk, tv);
+    return a.D == 64 ? launch_paged_d<64>(a, tq, tk, tv) : launch_paged_d<128>(a, tq, tk, tv);
 }
 
 }  // namespace attn
