@@ -54,7 +54,9 @@ def compare(got, want):
 
 
 @pytest.mark.parametrize("seed", range(40))
-def test_step(gpu, seed):
+@pytest.mark.parametrize("spare", [0, 262200])
+def test_step(gpu, seed, spare):
+    """spare: free pages behind those that matter, for a pool that takes a launch a step."""
     r = random.Random(seed)
     B, M, P = r.choice((1, 2, 9, 40)), r.choice((1, 2, 5, 31, 33, 70)), r.choice((1, 8, 16, 37))
     n_pages = r.choice((1, 31, 32, 33, 100, B * M, 2 * B * M + 5))
@@ -66,25 +68,34 @@ def test_step(gpu, seed):
         base = [lens[p] if 0 <= p < B else 0 for p in (parents or range(B))]
         new_len = [L + 1 for L in base]
     pinned = None if r.random() < 0.5 else [int(r.random() < 0.1) * r.choice((1, -1, 5)) for _ in range(n_pages)]
+    if spare:  # entries that were no pages may be now
+        pinned = pinned and pinned + [0] * spare
+        n_pages += spare
     got = run_step(table, lens, n_pages, P, M, parents, new_len, pinned)
     compare(got, ref.step(table, lens, n_pages, P, parents, new_len, pinned))
 
 
 @pytest.mark.parametrize("seed", range(20))
-def test_compact(gpu, seed):
+@pytest.mark.parametrize("spare", [0, 262200])
+def test_compact(gpu, seed, spare):
     r = random.Random(100 + seed)
     B, M, P = r.choice((1, 2, 9, 40)), r.choice((1, 2, 5, 33)), r.choice((1, 8, 16))
     n_pages = r.choice((1, 31, 32, 33, 100, 3 * B * M))
     table, lens = state(r, B, M, P, n_pages)
     pinned = None if r.random() < 0.5 else [int(r.random() < 0.2) for _ in range(n_pages)]
+    if spare:
+        table = [[p + spare // 2 if p < n_pages and r.random() < 0.3 else p for p in row] for row in table]
+        pinned = pinned and pinned + [0] * spare
+        n_pages += spare
     got = attn.attn_pages_compact(ints(table, (B, M)), ints(lens), n_pages, P, pinned=None if pinned is None else ints(pinned))
     compare(got, ref.compact(table, lens, n_pages, P, pinned))
 
 
-def test_a_large_pool(gpu):
-    """More words of bits and more rows than the planning block has threads."""
+@pytest.mark.parametrize("n_pages,B", [(100003, 1500), (262144, 2048), (262145, 300), (90000, 2049)])
+def test_a_large_pool(gpu, n_pages, B):
+    """More words of bits and more rows than a block has threads; the largest of the one-launch form and beyond."""
     r = random.Random(7)
-    n_pages, B, M, P = 100003, 1500, 40, 16
+    M, P = 40, 16
     table, lens = state(r, B, M, P, n_pages, share=0.2, bad=0.0)
     parents = [r.randrange(B) for _ in range(B)]
     new_len = [min(M * P, lens[p] + r.randint(0, 40)) for p in parents]

@@ -156,14 +156,12 @@ __device__ __forceinline__ unsigned pages_of_word(const PagesArgs &a, int w) {  
     return n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// Calls take(page, k) for the k-th set bit, counted on from `from`, of the words that the
-// threads hold (w0 + thread), a lane a bit: neighbours write side by side.  Returns how many
-// there are.  k from `most` on is left out.  The whole block calls it.
+// Calls take(page, k) for the k-th set bit of the words that the threads hold (w0 + thread,
+// its first bit the at-th), a lane a bit: neighbours write side by side.  k from `most` on is
+// left out.  The whole block calls it.
 template <typename Take>
-__device__ __forceinline__ int each_bit(int w0, unsigned bits, int from, int most, Take take) {
+__device__ __forceinline__ void each_bit(int w0, unsigned bits, int at, int most, Take take) {
     __shared__ int2 words[kPlanThreads];
-    int all;
-    const int at = from + block_prefix(__popc(bits), &all);
     words[threadIdx.x] = make_int2(static_cast<int>(bits), at);
     __syncthreads();
     const int lane = threadIdx.x % 32;
@@ -175,7 +173,6 @@ __device__ __forceinline__ int each_bit(int w0, unsigned bits, int from, int mos
         if ((set >> lane & 1u) && k < most) take((w0 + w) * 32 + lane, k);
     }
     __syncthreads();
-    return all;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PagesArgs a) {
@@ -215,7 +212,10 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PagesArg
     for (int w0 = 0; w0 < a.words; w0 += kPlanThreads) {
         const int w = w0 + tid;
         const unsigned bits = w < a.words ? ~*const_cast<volatile unsigned *>(&a.held[w]) & pages_of_word(a, w) : 0u;
-        free_pages += each_bit(w0, bits, free_pages, wants, [&](int page, int k) { a.list[k] = page; });
+        int all;
+        const int at = free_pages + block_prefix(__popc(bits), &all);
+        each_bit(w0, bits, at, wants, [&](int page, int k) { a.list[k] = page; });
+        free_pages += all;
     }
     if (tid == 0) {
         a.list[-1] = free_pages;
@@ -277,17 +277,23 @@ __global__ void __launch_bounds__(kPlanThreads) pages_moves_kernel(const PagesAr
     int holes = 0, moves = 0;
     for (int w0 = 0; w0 * 32 < n; w0 += kPlanThreads) {
         const int w = w0 + tid;
-        holes += each_bit(w0, w < a.words ? ~a.held[w] & below(w) : 0u, holes, INT_MAX, [&](int page, int k) { a.list[k] = page; });
+        const unsigned bits = w < a.words ? ~a.held[w] & below(w) : 0u;
+        const int at = holes + block_prefix(__popc(bits), &all);
+        each_bit(w0, bits, at, INT_MAX, [&](int page, int k) { a.list[k] = page; });
+        holes += all;
     }
     for (int w0 = n / 32 / kPlanThreads * kPlanThreads; w0 < a.words; w0 += kPlanThreads) {
         const int w = w0 + tid;
-        moves += each_bit(w0, w < a.words ? a.held[w] & ~below(w) & ~a.pins[w] : 0u, moves, INT_MAX, [&](int page, int k) {
+        const unsigned bits = w < a.words ? a.held[w] & ~below(w) & ~a.pins[w] : 0u;
+        const int at = moves + block_prefix(__popc(bits), &all);
+        each_bit(w0, bits, at, INT_MAX, [&](int page, int k) {
             const int to = a.list[k];
             a.move[page] = to;
             a.copies[3 * k] = page;
             a.copies[3 * k + 1] = to;
             a.copies[3 * k + 2] = a.P;
         });
+        moves += all;
     }
     for (int i = moves + tid; i < a.n_copies; i += kPlanThreads) {
         a.copies[3 * i] = a.copies[3 * i + 1] = -1;
@@ -318,6 +324,231 @@ __global__ void __launch_bounds__(kRowThreads) pages_rename_kernel(const PagesAr
         out[i] = page;
     });
     for (int i = k.pages + static_cast<int>(threadIdx.x); i < a.max_pages; i += kRowThreads) out[i] = -1;
+}
+
+// ------------------------------------------------------------ both in one launch
+
+// Pools of up to kOneMaxPages and tables of up to kOneMaxRows: one cluster of eight CTAs goes
+// through the same steps, with the bits in shared memory.  A CTA marks the pages of every
+// eighth row in bits of its own, then owns an eighth of the words, of all CTAs together.
+constexpr int kOne = 8;
+constexpr int kOneMaxPages = 1 << 18, kOneMaxRows = 2048;
+constexpr int kOneWords = kOneMaxPages / 32;
+struct OneSmem {
+    unsigned marks[kOneWords];                // of this CTA's rows
+    unsigned held[kOneWords / kOne], pins[kOneWords / kOne];  // this CTA's words
+    int last[kOneMaxRows];                    // a row's partly filled page or -1 (every CTA has them all)
+    int want[kOneMaxRows];                    // new pages a row wants, then its first in the list
+    Kept kept[kOneMaxRows / kOne];            // of this CTA's rows
+    int lost[kOneMaxRows / kOne], stays[kOneMaxRows / kOne];
+    int count[kOne];                          // pages held, of each CTA's words
+    int2 totals[kOne];                        // pages to be given out, pages to be moved
+};
+static_assert(kOneWords / kOne == kPlanThreads, "a thread a word");
+
+__device__ __forceinline__ void store_remote(const void *p, unsigned rank, int v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(map_rank(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned load_remote(const void *p, unsigned rank) {
+    unsigned v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(map_rank(p, rank)) : "memory");
+    return v;
+}
+
+template <bool Step>
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_one_kernel(const PagesArgs a) {
+    extern __shared__ __align__(16) uint8_t one_smem[];
+    OneSmem &sm = *reinterpret_cast<OneSmem *>(one_smem);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const unsigned rank = cluster_rank();
+    const int each = (a.words + kOne - 1) / kOne;          // words of a CTA
+    const int w = static_cast<int>(rank) * each + tid;     // this thread's word
+    const bool mine = tid < each && w < a.words;
+    constexpr int kStride = kOne * (kPlanThreads / 32);    // rows of a pass
+    const int row0 = static_cast<int>(rank) + kOne * warp;
+    for (int i = tid; i < a.words; i += kPlanThreads) sm.marks[i] = 0;
+    cluster_sync();  // every CTA runs: its shared memory may be written
+    griddep_launch_dependents();
+    griddep_wait();
+    // ---- marks of this CTA's rows
+    for (int b = row0; b < a.n_out; b += kStride) {
+        const Kept k = kept_of(a, b);
+        const int whole = Step ? k.full : k.full + (k.part != 0);
+        int lost = 0;
+#pragma unroll 16
+        for (int i = lane; i < whole; i += 32) {
+            const int page = k.old[i];
+            if (is_page(a, page))
+                atomicOr(&sm.marks[page / 32], 1u << (page % 32));
+            else
+                ++lost;
+        }
+        if (Step) {
+            lost = __reduce_add_sync(0xffffffffu, lost);
+            int last = k.part ? k.old[k.full] : -1;
+            if (!is_page(a, last)) last = -1;
+            if (lane < kOne) store_remote(&sm.last[b], static_cast<unsigned>(lane), last);
+            if (lane == 0) sm.lost[b / kOne] = lost;
+        }
+        if (lane == 0) sm.kept[b / kOne] = k;
+    }
+    // ---- pinned pages of this CTA's words, a lane a page
+    if (a.pinned) {
+        for (int i = warp; i < each; i += kPlanThreads / 32) {
+            const int page = (static_cast<int>(rank) * each + i) * 32 + lane;
+            const unsigned bits = __ballot_sync(0xffffffffu, page < a.n_pages && a.pinned[page] != 0);
+            if (lane == 0) sm.pins[i] = bits;
+        }
+    } else if (tid < each) {
+        sm.pins[tid] = 0;
+    }
+    cluster_sync();
+    // ---- this CTA's words, of all rows
+    if (mine) {
+        unsigned bits = sm.pins[tid];
+#pragma unroll
+        for (unsigned y = 0; y < kOne; ++y) bits |= load_remote(&sm.marks[w], y);
+        sm.held[tid] = bits;
+    }
+    if (!Step) {
+        int all;
+        block_prefix(mine ? __popc(sm.held[tid]) : 0, &all);
+        if (tid < kOne) store_remote(&sm.count[rank], static_cast<unsigned>(tid), all);
+    }
+    cluster_sync();
+    int n = 0;  // compaction: pages held
+    if (Step) {
+        // ---- which rows keep their partly filled page, and what each wants
+        for (int b = row0; b < a.n_out; b += kStride) {
+            const Kept k = sm.kept[b / kOne];
+            const int page = sm.last[b];
+            int stays = 0;
+            if (page >= 0) {
+                bool first = true;
+                for (int y = lane; y < b; y += 32) first = first && sm.last[y] != page;
+                const unsigned owner = static_cast<unsigned>(page / 32 / each);
+                unsigned *at = &sm.held[page / 32 % each];
+                // a row whose page this is sets the bit: no other row is its first
+                stays = __all_sync(0xffffffffu, first) && !(load_remote(at, owner) >> (page % 32) & 1u);
+                stays = __shfl_sync(0xffffffffu, stays, 0);
+                if (stays && lane == 0)
+                    asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(map_rank(at, owner)),
+                                 "r"(1u << (page % 32)) : "memory");
+            }
+            const int lost = sm.lost[b / kOne];
+            if (lane < kOne) store_remote(&sm.want[b], static_cast<unsigned>(lane), lost + k.pages - k.full - stays);
+            if (lane == 0) sm.stays[b / kOne] = stays;
+        }
+        cluster_sync();
+    } else {
+        for (int y = 0; y < kOne; ++y) n += sm.count[y];
+    }
+    // ---- places in the list: of the rows' wants, and of the free pages of each word
+    int wants = Step ? 0 : INT_MAX;
+    if (Step)
+        for (int b0 = 0; b0 < a.n_out; b0 += kPlanThreads) {
+            const int b = b0 + tid;
+            int all;
+            const int at = wants + block_prefix(b < a.n_out ? sm.want[b] : 0, &all);
+            if (b < a.n_out) sm.want[b] = at;
+            wants += all;
+        }
+    const unsigned below = n - w * 32 >= 32 ? 0xffffffffu : n > w * 32 ? (1u << (n - w * 32)) - 1u : 0u;  // pages < n
+    const unsigned free_bits = !mine ? 0u : ~sm.held[tid] & (Step ? pages_of_word(a, w) : below);
+    const unsigned moved = Step || !mine ? 0u : sm.held[tid] & ~below & ~sm.pins[tid];
+    int2 all = make_int2(0, 0);
+    const int free_at = block_prefix(__popc(free_bits), &all.x);
+    const int moved_at = Step ? 0 : block_prefix(__popc(moved), &all.y);
+    if (tid < kOne) {
+        store_remote(&sm.totals[rank].x, static_cast<unsigned>(tid), all.x);
+        if (!Step) store_remote(&sm.totals[rank].y, static_cast<unsigned>(tid), all.y);
+    }
+    cluster_sync();
+    int2 from = make_int2(0, 0), sum = make_int2(0, 0);
+    for (int y = 0; y < kOne; ++y) {
+        if (y == static_cast<int>(rank)) from = sum;
+        sum.x += sm.totals[y].x;
+        if (!Step) sum.y += sm.totals[y].y;
+    }
+    const int w0 = static_cast<int>(rank) * each;
+    each_bit(w0, free_bits, from.x + free_at, wants, [&](int page, int k) { a.list[k] = page; });
+    if (!Step) {
+        each_bit(w0, moved, from.y + moved_at, INT_MAX, [&](int page, int k) {
+            a.move[page] = k;
+            a.copies[3 * k] = page;
+            a.copies[3 * k + 2] = a.P;
+        });
+        if (a.pinned) each_bit(w0, !mine ? 0u : sm.held[tid] & ~below & sm.pins[tid], 0, INT_MAX, [&](int page, int) { a.move[page] = -1; });
+    }
+    __threadfence();
+    cluster_sync();
+    // ---- the new rows
+    if (rank == 0 && tid == 0) *a.free_pages = Step ? sum.x - wants : a.n_pages - n;
+    for (int b = row0; b < a.n_out; b += kStride) {
+        const Kept k = sm.kept[b / kOne];
+        int32_t *out = a.table_out + b * a.out_stride;
+        if (!Step) {
+#pragma unroll 4
+            for (int i = lane; i < a.max_pages; i += 32) {
+                int page = i < k.pages ? k.old[i] : -1;
+                if (!is_page(a, page)) page = -1;
+                if (page >= n) {
+                    const int to = __ldcg(&a.move[page]);
+                    if (to >= 0) page = __ldcg(&a.list[to]);
+                }
+                out[i] = page;
+            }
+            continue;
+        }
+        const int stays = sm.stays[b / kOne], lost = sm.lost[b / kOne], first = sm.want[b], kept = k.full + stays;
+        auto given = [&](int nth) { return nth < sum.x ? __ldcg(&a.list[nth]) : -1; };
+        if (lost == 0) {
+#pragma unroll 16
+            for (int i = lane; i < a.max_pages; i += 32)
+                out[i] = i < kept ? k.old[i] : i < k.pages ? given(first + i - kept) : -1;
+        } else {  // rare: entries that are no pages get new ones first
+            int nth = first;
+            for (int i0 = 0; i0 < a.max_pages; i0 += 32) {
+                const int i = i0 + lane;
+                int page = i < kept ? k.old[i] : -1;
+                const bool wanted = i < k.pages && !is_page(a, page);
+                const unsigned some = __ballot_sync(0xffffffffu, wanted);
+                page = wanted ? given(nth + __popc(some & ((1u << lane) - 1u))) : i < kept ? page : -1;
+                nth += __popc(some);
+                if (i < a.max_pages) out[i] = page;
+            }
+        }
+        if (lane == 0) {
+            a.len_out[b] = k.len;
+            const int source = sm.last[b], to = k.part && !stays ? given(first + lost) : -1;
+            const bool copied = source >= 0 && to >= 0;
+            a.copies[3 * b] = copied ? source : -1;
+            a.copies[3 * b + 1] = copied ? to : -1;
+            a.copies[3 * b + 2] = copied ? k.part : 0;
+        }
+    }
+    if (!Step)
+        for (int i = static_cast<int>(rank) * kPlanThreads + tid; i < a.n_copies; i += kOne * kPlanThreads) {
+            if (i < sum.y) {
+                a.copies[3 * i + 1] = __ldcg(&a.list[i]);
+            } else {
+                a.copies[3 * i] = a.copies[3 * i + 1] = -1;
+                a.copies[3 * i + 2] = 0;
+            }
+        }
+}
+
+template <bool Step>
+cudaError_t launch_one(const PagesArgs &a) {
+    cudaError_t e = cudaFuncSetAttribute(pages_one_kernel<Step>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(OneSmem));
+    if (e != cudaSuccess) return e;
+    return launch_clusters(pages_one_kernel<Step>, kOne, kOne, kPlanThreads, sizeof(OneSmem), a.stream, a);
+}
+bool fits_one(const PagesArgs &a) {
+#ifdef PAGES_NO_ONE
+    return false;
+#endif
+    return a.n_pages <= kOneMaxPages && a.n_out <= kOneMaxRows;
 }
 
 // ------------------------------------------------------------ copies
@@ -364,6 +595,7 @@ cudaError_t launch_clear(const PagesArgs &a) {
 }  // namespace
 
 cudaError_t launch_pages_step(const PagesArgs &a) {
+    if (fits_one(a)) return launch_one<true>(a);
     cudaError_t e = launch_clear(a);
     if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_mark_kernel, dim3(static_cast<unsigned>(a.n_out)), dim3(kRowThreads), 0, a.stream, a);
     if (e == cudaSuccess) e = launch_pdl(pages_plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a);
@@ -372,6 +604,7 @@ cudaError_t launch_pages_step(const PagesArgs &a) {
 }
 
 cudaError_t launch_pages_compact(const PagesArgs &a) {
+    if (fits_one(a)) return launch_one<false>(a);
     cudaError_t e = launch_clear(a);
     if (e == cudaSuccess && a.n_out > 0) e = launch_pdl(pages_mark_kernel, dim3(static_cast<unsigned>(a.n_out)), dim3(kRowThreads), 0, a.stream, a);
     if (e == cudaSuccess) e = launch_pdl(pages_moves_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a);
