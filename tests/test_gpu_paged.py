@@ -267,6 +267,54 @@ def test_nonfinite_values_go_to_the_rows_that_see_them(gpu, value, dtype):
     assert bool(out[:first, 2:, 7].isfinite().all()) and not bool(out[first:150, 2:, 7].isfinite().any())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,H_kv,B", [(4, 2, 1), (4, 2, 40), (24, 1, 1), (24, 1, 40), (96, 2, 1), (96, 2, 30)])
+def test_nonfinite_values_and_single_tokens(gpu, H, H_kv, B, dtype):
+    """Few and many sequences, few rows a tile and many: the values reach every head of their group,
+    and none of those past the end, of the other group or of a neighbour."""
+    lens = [700, 129, 257, 64, 1, 300]
+    x = Paged([(lens[b % 6], 1) for b in range(B)], H, H_kv, 64, 16, dtype, seed=14, even=True)
+    clean = x.call()
+    G = H // H_kv
+    for b, j, value in ((0, 699, math.inf), (0, 3, -math.inf), (B - 1, 0, math.nan)):
+        x.vp[int(x.table[b, j // 16]), H_kv - 1, j % 16, 9 + b % 2] = value
+    out = x.call()
+    attn.attn_device_status()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, H - G:, 9] = True
+    hit[B - 1, H - G:, 9 + (B - 1) % 2] = True
+    assert torch.equal(out[~hit], clean[~hit]) and not bool(out[hit].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,G", [(1, 4), (1, 40), (50, 4)])
+def test_huge_scores_of_single_tokens(gpu, B, G, dtype):
+    L, D = 400, 64
+    x = Paged([(L, 1)] * B, G, 1, D, 16, dtype, seed=15, even=True)
+    q, k = ref.huge_inputs(B * G, L, D, dtype, 3)
+    for b in range(B):
+        pages = x.table[b, :L // 16].long()
+        x.kp[pages, 0] = k.view(-1, 16, D)
+        x.vp[pages, 0] = x.v[b][:, 0].view(-1, 16, D)
+    x.q = q.view(B, G, D)
+    out, lse = x.call(scale=1.0, return_lse=True)
+    attn.attn_device_status()
+    see = torch.ones(G, L, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        ref.check_huge(out[b], lse[b], x.q[b], k, x.v[b][:, 0], see, dtype)
+
+
+@pytest.mark.parametrize("H,H_kv", [(8, 2), (32, 1), (33, 1), (20, 2), (64, 1)])
+@pytest.mark.parametrize("n", [1, 2, 3, 7, 8, 9, 33])
+def test_a_few_rows(gpu, n, H, H_kv):
+    """Numbers of rows around those that share a tile's columns among four warps, one sequence and many, chunks beside them."""
+    for seqs in ([(1500, n)], [(n, n)], [(n - 1, n)], [(200 + 7 * i, n) for i in range(20)], [(300, n), (900, 100), (17, 1), (260, n)]):
+        x = Paged(seqs, H, H_kv, 128 if H < 33 else 64, 16, seed=n + H)
+        out, lse = x.call(return_lse=True)
+        attn.attn_device_status()
+        x.check(out, lse, heads=(0, H // H_kv - 1, H - 1), what=f"n {n} H {H}/{H_kv} {seqs[:2]}")
+
+
 def _into_pages(x, b, k, v):
     for j in range(k.shape[0]):
         page = int(x.table[b, j // x.P])

@@ -1056,7 +1056,9 @@ static long long paged_sizes(const char *who, PagedArgs &a, bool ragged, int dty
     a.n_sm = num_sms();
     a.per_seq = ragged || a.n_seq < 1 ? 0 : a.T / a.n_seq;
     const long long rows = static_cast<long long>(a.T) * a.H;
-    if (rows >= (1LL << 31) || a.max_len > tree_max_rows(dtype)) return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
+    // keys are counted in 32 bits some tiles past the last one (bf16), or to the end of the last split
+    if (rows >= (1LL << 31) || a.max_len > (dtype == ATTN_BF16 ? 0x7fff0000 : 0x40000000))
+        return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
     if (a.T == 0 || a.n_seq == 0) return 0;
     if (dtype == ATTN_F32) {
         static const int32_t some = 0;

@@ -55,6 +55,7 @@
 #include "serving.cuh"
 
 #include <climits>
+#include <type_traits>
 
 namespace attn {
 namespace {
@@ -176,7 +177,7 @@ struct GuardReq {
     int run;     // ring slot
 };
 constexpr int kEnd = -1;
-constexpr int kNoBox = INT_MIN, kBadPage = -1;  // a box that is not copied; an entry that is no page (or one from n_pages on)
+constexpr int kNoBox = INT_MIN, kBadPage = -1;  // a box that is not copied; out of range in every view of the pages
 
 // Single: every unit has one row tile; its second Q buffer is one more K/V stage.
 template <int D, bool Single>
@@ -423,12 +424,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // where a box does not hold them all
         const int boxes = kN / a.box, i = lane % boxes, c = lane / boxes;
         const bool carries = lane < boxes * (a.halves ? L::kSub : 1);
-        const uint32_t box_at = static_cast<uint32_t>(i * a.box * (D * 2) + c * 1024);
+        const uint32_t box_bytes = static_cast<uint32_t>(a.box * D * 2), box_at = i * box_bytes + c * 1024;
         const int page_inc = kN / a.P, row_inc = kN % a.P;  // from tile to tile
         int issued = 0, stage = 0, requests = 0, k = 0, q_loads = 0;
         uint32_t stage_phase = 1;  // of kv_empty: the first round of the ring waits for nothing
         bool ok = true;
-        int4 rec = make_int4(-1, 0, 0, 0), rec2 = make_int4(0, 0, 0, 0);
+        int4 *record = reinterpret_cast<int4 *>(a.merge) + 2 * blockIdx.x;  // of the unit shared with later CTAs
+        if (!Cluster && lane == 0) record[0] = make_int4(-1, 0, 0, 0);
         while (ok) {
             const int slot = k % kRing;
             if (k >= kRing && !(ok = mbar_wait_warp(&bars.run_empty[slot], ((k / kRing) - 1) & 1, &bars.abort))) break;
@@ -449,11 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.j0 = j;
                     r.n = end - j;
                     r.slot = Cluster || r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
-                    if (!Cluster && j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to rec.w,
+                    if (!Cluster && j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to the record's,
                                                // the last whose begin leaves enough of it
                         const long long last = pos + static_cast<long long>(nt - units.least) * units.tile;
-                        rec = make_int4(b, hs, r.tok0, static_cast<int>(quotient((last + 1) * N - 1, total)));
-                        rec2 = make_int4(r.left, r.past, r.c0, 0);
+                        if (lane == 0) {
+                            record[0] = make_int4(b, hs, r.tok0, static_cast<int>(quotient((last + 1) * N - 1, total)));
+                            record[1] = make_int4(r.left, r.past, r.c0, 0);
+                        }
                     }
                 }
             }
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (r.n < 0) break;
             const int edge = edge_of(r), head = r.hs / a.groups;
             // This lane's box of the next tile to be looked up: its key, its entry of the table and its row
-            // in that page.  A box past the last visible key is not copied: kNoBox.
+            // in that page.
             const int k_head = head * a.k_hstep, v_head = head * a.v_hstep;
             int next_key = r.j0 * kN + i * a.box, next_row = page_of_key(a, next_key);
             const int32_t *next_entry = a.page_table + static_cast<long long>(r.seq) * a.table_stride + next_row;
@@ -486,8 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (next_row >= a.P) next_row -= a.P, ++next_entry;
                 return x;
             };
-            auto load = [&](int jj, int kv, const Box &x) {
-                if (!ok || jj >= r.n) return;
+            auto load = [&](int jj, auto v, const Box &x) {  // K or V of tile jj into the next stage
+                constexpr bool kv = decltype(v)::value;
+                if (!ok) return;
                 if (!__all_sync(0xffffffffu, mbar_try_wait(&bars.kv_empty[stage], stage_phase)) &&
                     !(ok = mbar_wait_warp(&bars.kv_empty[stage], stage_phase, &bars.abort)))
                     return;
@@ -501,14 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else
                         mbar_arrive(full);
                 }
-                if (x.page != kNoBox) {
-                    uint8_t *dst = ring + stage * L::kTile + box_at;
-                    if (a.halves)
-                        tma_load_4d(dst, kv ? &tv : &tk, full, c * 64, x.row, head, x.page);
-                    else {
-                        const unsigned at = kv ? x.page * static_cast<unsigned>(a.v_pstep) + v_head : x.page * static_cast<unsigned>(a.k_pstep) + k_head;
-                        tma_load_5d(dst, kv ? &tv : &tk, full, 0, 0, 0, x.row / 8, is_page(a, x.page) ? static_cast<int>(at) : -1);
-                    }
+                uint8_t *dst = ring + stage * L::kTile;
+                const CUtensorMap *map = kv ? &tv : &tk;
+                if (a.halves) {
+                    if (x.page != kNoBox) tma_load_4d(dst + box_at, map, full, c * 64, x.row, head, x.page);
+                } else {
+                    const unsigned at = kv ? x.page * static_cast<unsigned>(a.v_pstep) + v_head : x.page * static_cast<unsigned>(a.k_pstep) + k_head;
+                    const int entry = is_page(a, x.page) ? static_cast<int>(at) : kBadPage, row = x.row / 8;
+                    if (x.page != kNoBox) tma_load_5d(dst + box_at, map, full, row, entry);
                 }
                 if (kv && jj >= edge) {
                     if (lane == 0) {
@@ -536,28 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 ++q_loads;
             };
-            Box b0 = look_up(), b1 = look_up(), b2 = look_up();  // of tiles jj, jj + 1, jj + 2
-            if (Single || r.left <= a.tokens) {  // one row tile: K0 K1 | V0 K2 | V1 K3 | ...
-                if (k == 0) load_q(1);
-                load(0, 0, b0);
-                load(1, 0, b1);
-                if (k > 0) load_q(1);
-                for (int jj = 0; jj < r.n && ok; ++jj) {
-                    const Box b3 = look_up();
-                    load(jj, 1, b0);
-                    load(jj + 2, 0, b2);
-                    b0 = b1, b1 = b2, b2 = b3;
-                }
-            } else {
-                if (k == 0) load_q(2);
-                load(0, 0, b0);
-                if (k > 0) load_q(2);
-                for (int jj = 0; jj < r.n && ok; ++jj) {
-                    const Box b3 = look_up();
-                    load(jj, 1, b0);
-                    load(jj + 1, 0, b1);
-                    b0 = b1, b1 = b2, b2 = b3;
-                }
+            const bool one = Single || r.left <= a.tokens;
+            const int lead = one ? 2 : 1;  // tiles that K is ahead: K0 K1 | V0 K2 | V1 K3 or K0 | V0 K1 | V1 K2
+            // boxes of tiles jj + lead - 2 to jj + lead + 1
+            Box v2{kBadPage, 0}, v1 = v2, now = look_up(), next = look_up();
+            if (k == 0) load_q(one ? 1 : 2);  // before the first K; later behind it
+            for (int jj = -lead; jj < r.n && ok; ++jj) {
+                if (jj == 0 && k > 0) load_q(one ? 1 : 2);
+                if (jj >= 0) load(jj, std::true_type{}, one ? v2 : v1);
+                if (jj + lead < r.n) load(jj + lead, std::false_type{}, now);
+                v2 = v1, v1 = now, now = next, next = look_up();
             }
             ++k;
             if (Cluster) {
@@ -571,11 +564,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) {  // no more work for the guard
                 *static_cast<volatile int *>(&bars.req[requests % kGuardRing].stage) = kEnd;
                 mbar_arrive(&bars.guard_full[requests % kGuardRing]);
-            }
-            if (!Cluster) {
-                int4 *out = reinterpret_cast<int4 *>(a.merge) + 2 * blockIdx.x;
-                out[0] = rec;
-                out[1] = rec2;
             }
             // never leave with copies still landing in shared memory
             volatile int never = 0;
