@@ -49,7 +49,7 @@ PAGES = (2 * 16 * 128, 16 * 128, 128) * 2
     (dict(ws=None), I), (dict(nb=16), I), (dict(ws=off(A[8], 8)), I), (dict(ws=A[3]), I), (dict(ws=A[1]), I), (dict(ws=A[5]), I),
     (dict(ws=A[6]), I), (dict(ws=A[7]), I), (dict(T=1 << 28, H=16, nb=1 << 60, k=ctypes.c_void_p(1 << 60), v=ctypes.c_void_p(3 << 59),
                                               o=ctypes.c_void_p(1 << 61)), I),
-    (dict(dtype=F32, M=1 << 27, nb=1 << 60), I), (dict(P=1 << 16, M=0x7fff, ts=0x7fff, nb=1 << 60), I),
+    (dict(dtype=F32, M=1 << 27, nb=1 << 60), I), (dict(P=24, M=0x7fffffff // 24, nb=1 << 60), I),
 ])
 def test_paged_rejects_bad_arguments(attn_lib, kw, code):
     assert paged(attn_lib, **kw) == code
