@@ -3,6 +3,7 @@
 // point is documented in include/attn.h.
 #include "attn.h"
 #include "kernels.h"
+#include "paged.h"
 #include "rope_turns.h"
 #include "ptx.cuh"
 

@@ -22,6 +22,7 @@
 // a warp a row.  Interleaved pairs need no multiple of VEC: the unit in which the turned
 // ones end chooses pair by pair.
 #include "kernels.h"
+#include "paged.h"
 #include "ptx.cuh"
 #include "serving.cuh"
 

@@ -50,7 +50,8 @@
 // Roles (12 warps): warp 0 walks the CTA's run and loads Q, K_j, V_j, warp 1 allocates
 // TMEM and issues the MMAs, warps 2-3 guard, warps 4-7 and 8-11 are the streams (thread =
 // row = TMEM lane); a warp none of whose rows sees a key only keeps step.
-#include "kernels.h"
+#include "clusters.cuh"
+#include "paged.h"
 #include "ptx.cuh"
 #include "serving.cuh"
 
@@ -73,25 +74,31 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kHugeLog2 = 16777216.0f;  // 2^24
-#ifndef ATTN_PAGED_MIN_TILES
-#define ATTN_PAGED_MIN_TILES 2
-#endif
-#ifndef ATTN_PAGED_UNIT_COST
-#define ATTN_PAGED_UNIT_COST 5
-#endif
-#ifndef ATTN_PAGED_WEIGHT
-#define ATTN_PAGED_WEIGHT 6
-#endif
-#ifndef ATTN_PAGED_LEAST
-#define ATTN_PAGED_LEAST 2
-#endif
-constexpr int kUnitCost = ATTN_PAGED_UNIT_COST;  // what a unit costs beside its tiles, in tiles
-constexpr int kMinTiles = ATTN_PAGED_MIN_TILES;  // fewest tiles' worth of keys a CTA takes
-constexpr int kWeightTwo = ATTN_PAGED_WEIGHT;    // quarters of a tile's cost, where a unit has two row tiles
-constexpr int kLeastTwo = ATTN_PAGED_LEAST;      // fewest tiles of such a unit that a cut leaves on either side
+constexpr int kUnitCost = 5;  // what a unit costs beside its tiles, in tiles
+constexpr int kMinTiles = 2;  // fewest tiles' worth of keys a CTA takes
+constexpr int kWeightTwo = 6;    // quarters of a tile's cost, where a unit has two row tiles
+constexpr int kLeastTwo = 2;      // fewest tiles of such a unit that a cut leaves on either side
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// 5-D: the first three coordinates 0.
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c3), "r"(c4)
+        : "memory");
+}
 
 __device__ __forceinline__ bool is_page(const PagedArgs &a, int page) { return page >= 0 && page < a.n_pages; }
 

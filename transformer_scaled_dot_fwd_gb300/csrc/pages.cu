@@ -20,7 +20,9 @@
 // Both move a few hundred KB; what bounds them is the chain of four launches (programmatic
 // ones, about 2 us each).  attn_pages_copy moves whole rows of pages, 16 bytes a thread and
 // eight in flight, bound by HBM.
+#include "clusters.cuh"
 #include "kernels.h"
+#include "paged.h"
 #include "ptx.cuh"
 
 #include <climits>
@@ -545,9 +547,6 @@ cudaError_t launch_one(const PagesArgs &a) {
     return launch_clusters(pages_one_kernel<Step>, kOne, kOne, kPlanThreads, sizeof(OneSmem), a.stream, a);
 }
 bool fits_one(const PagesArgs &a) {
-#ifdef PAGES_NO_ONE
-    return false;
-#endif
     return a.n_pages <= kOneMaxPages && a.n_out <= kOneMaxRows;
 }
 

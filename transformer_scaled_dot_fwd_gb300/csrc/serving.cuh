@@ -25,11 +25,6 @@ __device__ __forceinline__ int count_le(const int32_t *v, int n, int t, int lane
     return lo;
 }
 
-// Entry of the page table that holds a key (a division is some 40 instructions).
-__device__ __forceinline__ int page_of_key(const PagedArgs &a, int key) {
-    return a.page_magic ? static_cast<int>(__umulhi(static_cast<unsigned>(key), a.page_magic)) : key / a.P;
-}
-
 // What the draft of one sequence looks like: L cache rows, the last n of them
 // drafted, so draft token j's key sits at row past + j (none when negative).
 struct Draft {
@@ -116,8 +111,8 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t *w, int s) {
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
 
 // Clean the V tile at shared address `tile` (kSub blocks of kRows rows of 128
-// bytes; kGroups: kRows / 8 groups of kSub blocks of 8 rows) for an MMA: rows from `inside` on become zeros, non-finite elements of
-// the others too.  Returns whether this thread met one.  `Threads` threads share
+// bytes; kGroups: kRows / 8 groups of kSub blocks of 8 rows) for an MMA: rows from
+// `inside` on become zeros, non-finite elements of the others too.  Returns whether this thread met one.  `Threads` threads share
 // the tile.  An exponent of all ones carries into the sign bit when one is added
 // to it, so three operations test a pair of bf16, and eight 16-byte loads are in
 // flight before the first test.

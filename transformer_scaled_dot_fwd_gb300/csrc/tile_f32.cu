@@ -34,7 +34,9 @@
 // owns the blocks from cu[s] / 32 + s on, a few of which stay empty.  Tree rows
 // see [0, hi) and the draft keys in their ancestor set.  A key that a row does
 // not see contributes nothing whatever its row of V holds.
+#include "clusters.cuh"
 #include "kernels.h"
+#include "paged.h"
 #include "ptx.cuh"
 #include "serving.cuh"
 
