@@ -3,23 +3,31 @@
 // attn_pages_step makes the next table from the last one: row b goes on from row
 // parents[b], cut back or grown to new_len[b] tokens.  No counts of holders are kept from
 // call to call: which pages are held is read off the table, as a set of bits.
-//   1. bits = pinned pages; `first` = nobody                     (pages_clear_kernel)
-//   2. a block a row: full pages that stay set their bits; a partly filled page takes the
-//      lowest row that holds it as such                          (pages_mark_kernel)
-//   3. one block: which rows keep their partly filled page (its first, unless the bit says
-//      that another row holds it full or it is pinned), how many new pages each row wants,
-//      the prefix sums of both the wants and the free pages of each word of bits, and
-//      the list of the lowest free pages, as many as are wanted   (pages_plan_kernel)
-//   4. a block a row: writes it, and the copy it needs            (pages_write_kernel)
+//   1. bits = pinned pages
+//   2. full pages that stay set their bits; a partly filled page goes to the lowest row
+//      that holds it as such
+//   3. which rows keep their partly filled page (its first, unless the bit says that
+//      another row holds it full or it is pinned), how many new pages each row wants, the
+//      prefix sums of both the wants and the free pages of each word of bits, and the list
+//      of the lowest free pages, as many as are wanted
+//   4. each row is written, and the copy it needs
 // Minima, unions and prefix sums do not depend on the order of the threads, so a call gives
 // the same table every time.
 //
 // attn_pages_compact sets the bits of all pages held (n of them) in the same way; the k-th
 // lowest held page from n on moves to the k-th lowest free one below n.
 //
-// Both move a few hundred KB; what bounds them is the chain of four launches (programmatic
-// ones, about 2 us each).  attn_pages_copy moves whole rows of pages, 16 bytes a thread and
-// eight in flight, bound by HBM.
+// Both move a few hundred KB; what bounds them is the chain of dependent steps.  Pools of up
+// to 262144 pages, whose bits fit in shared memory, take one launch of a cluster of eight
+// CTAs with four barriers (pages_one_kernel): 256 sequences of up to 7000 tokens in pages
+// of 16 rows 8.7 us (10 us with a lane's entries of the table read one after the other, 13
+// also with a pass over all words for the list, 13.4 as four launches; sixteen CTAs
+// change nothing: the chain is the same).  Larger ones take four launches with the bits in
+// the workspace: clear, mark (a block a row), plan or moves (one block), write or rename (a
+// block a row).
+//
+// attn_pages_copy moves whole rows of pages, 16 bytes a thread and four in flight, bound by
+// HBM: 120 MB read and 120 MB written in 37 us, 6.5 TB/s.
 #include "clusters.cuh"
 #include "kernels.h"
 #include "paged.h"
@@ -130,27 +138,27 @@ __global__ void __launch_bounds__(kRowThreads) pages_mark_kernel(const PagesArgs
 
 // Sum of the values of the threads before this one, and of all of them.  The whole block
 // calls it.
-__device__ __forceinline__ int block_prefix(int v, int *total) {
-    __shared__ int sums[kPlanThreads / 32];
+__device__ __forceinline__ int block_prefix(unsigned v, int *total) {
+    __shared__ unsigned sums[kPlanThreads / 32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int s = v;
+    unsigned s = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, d);
+        const unsigned y = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += y;
     }
     if (lane == 31) sums[warp] = s;
     __syncthreads();
-    int w = sums[lane];
+    unsigned w = sums[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, d);
+        const unsigned y = __shfl_up_sync(0xffffffffu, w, d);
         if (lane >= d) w += y;
     }
     *total = __shfl_sync(0xffffffffu, w, 31);
-    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
+    const unsigned before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
     __syncthreads();
-    return s - v + (warp ? before : 0);
+    return static_cast<int>(s - v + (warp ? before : 0u));
 }
 
 __device__ __forceinline__ unsigned pages_of_word(const PagesArgs &a, int w) {  // bits that stand for a page
@@ -158,19 +166,19 @@ __device__ __forceinline__ unsigned pages_of_word(const PagesArgs &a, int w) {  
     return n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// Calls take(page, k) for the k-th set bit of the words that the threads hold (w0 + thread,
-// its first bit the at-th), a lane a bit: neighbours write side by side.  k from `most` on is
-// left out.  The whole block calls it.
+// Calls take(page, k) for the k-th set bit of the words that the first `n` threads hold (w0 +
+// thread, its first bit the at-th, in order), a lane a bit: neighbours write side by side.  k
+// from `most` on is left out.  The whole block calls it.
 template <typename Take>
-__device__ __forceinline__ void each_bit(int w0, unsigned bits, int at, int most, Take take) {
+__device__ __forceinline__ void each_bit(int w0, int n, unsigned bits, int at, int most, Take take) {
     __shared__ int2 words[kPlanThreads];
     words[threadIdx.x] = make_int2(static_cast<int>(bits), at);
     __syncthreads();
     const int lane = threadIdx.x % 32;
-    for (int w = threadIdx.x / 32; w < kPlanThreads; w += kPlanThreads / 32) {
+    for (int w = threadIdx.x / 32; w < min(n, kPlanThreads); w += kPlanThreads / 32) {
         const int2 x = words[w];
         const unsigned set = static_cast<unsigned>(x.x);
-        if (!set || x.y >= most) continue;
+        if (x.y >= most) break;
         const int k = x.y + __popc(set & ((1u << lane) - 1u));
         if ((set >> lane & 1u) && k < most) take((w0 + w) * 32 + lane, k);
     }
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(const PagesArg
         const unsigned bits = w < a.words ? ~*const_cast<volatile unsigned *>(&a.held[w]) & pages_of_word(a, w) : 0u;
         int all;
         const int at = free_pages + block_prefix(__popc(bits), &all);
-        each_bit(w0, bits, at, wants, [&](int page, int k) { a.list[k] = page; });
+        each_bit(w0, a.words - w0, bits, at, wants, [&](int page, int k) { a.list[k] = page; });
         free_pages += all;
     }
     if (tid == 0) {
@@ -281,14 +289,14 @@ __global__ void __launch_bounds__(kPlanThreads) pages_moves_kernel(const PagesAr
         const int w = w0 + tid;
         const unsigned bits = w < a.words ? ~a.held[w] & below(w) : 0u;
         const int at = holes + block_prefix(__popc(bits), &all);
-        each_bit(w0, bits, at, INT_MAX, [&](int page, int k) { a.list[k] = page; });
+        each_bit(w0, a.words - w0, bits, at, INT_MAX, [&](int page, int k) { a.list[k] = page; });
         holes += all;
     }
     for (int w0 = n / 32 / kPlanThreads * kPlanThreads; w0 < a.words; w0 += kPlanThreads) {
         const int w = w0 + tid;
         const unsigned bits = w < a.words ? a.held[w] & ~below(w) & ~a.pins[w] : 0u;
         const int at = moves + block_prefix(__popc(bits), &all);
-        each_bit(w0, bits, at, INT_MAX, [&](int page, int k) {
+        each_bit(w0, a.words - w0, bits, at, INT_MAX, [&](int page, int k) {
             const int to = a.list[k];
             a.move[page] = to;
             a.copies[3 * k] = page;
@@ -339,12 +347,14 @@ constexpr int kOneWords = kOneMaxPages / 32;
 struct OneSmem {
     unsigned marks[kOneWords];                // of this CTA's rows
     unsigned held[kOneWords / kOne], pins[kOneWords / kOne];  // this CTA's words
+    unsigned used[kOneWords / kOne];          // step: held, or some row's partly filled page
     int last[kOneMaxRows];                    // a row's partly filled page or -1 (every CTA has them all)
     int want[kOneMaxRows];                    // new pages a row wants, then its first in the list
     Kept kept[kOneMaxRows / kOne];            // of this CTA's rows
     int lost[kOneMaxRows / kOne], stays[kOneMaxRows / kOne];
-    int count[kOne];                          // pages held, of each CTA's words
-    int2 totals[kOne];                        // pages to be given out, pages to be moved
+    unsigned total[kOne];                     // step: free pages of each CTA's words; compaction: pages held
+                                              // and, 16 bits up, those that may move
+    int most;                                 // step: new pages that the rows want at most
 };
 static_assert(kOneWords / kOne == kPlanThreads, "a thread a word");
 
@@ -363,12 +373,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_one_kernel(const PagesA
     OneSmem &sm = *reinterpret_cast<OneSmem *>(one_smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const unsigned rank = cluster_rank();
-    const int each = (a.words + kOne - 1) / kOne;          // words of a CTA
+    const int each = max(1, (a.words + kOne - 1) / kOne);  // words of a CTA
     const int w = static_cast<int>(rank) * each + tid;     // this thread's word
     const bool mine = tid < each && w < a.words;
     constexpr int kStride = kOne * (kPlanThreads / 32);    // rows of a pass
+    constexpr int kBatch = 16;                             // entries on their way to a lane
     const int row0 = static_cast<int>(rank) + kOne * warp;
     for (int i = tid; i < a.words; i += kPlanThreads) sm.marks[i] = 0;
+    if (tid == 0) sm.most = 0;
     cluster_sync();  // every CTA runs: its shared memory may be written
     griddep_launch_dependents();
     griddep_wait();
@@ -376,20 +388,32 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_one_kernel(const PagesA
     for (int b = row0; b < a.n_out; b += kStride) {
         const Kept k = kept_of(a, b);
         const int whole = Step ? k.full : k.full + (k.part != 0);
-        int lost = 0;
-#pragma unroll 16
-        for (int i = lane; i < whole; i += 32) {
-            const int page = k.old[i];
-            if (is_page(a, page))
-                atomicOr(&sm.marks[page / 32], 1u << (page % 32));
-            else
-                ++lost;
+        int32_t *out = a.table_out + b * a.out_stride;
+        int lost = 0, last = Step && k.part ? k.old[k.full] : -1;
+        for (int i0 = lane; i0 < whole; i0 += 32 * kBatch) {
+            int page[kBatch];
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) page[y] = i0 + 32 * y < whole ? k.old[i0 + 32 * y] : -1;
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+                if (i0 + 32 * y >= whole) break;
+                if (is_page(a, page[y]))
+                    atomicOr(&sm.marks[page[y] / 32], 1u << (page[y] % 32));
+                else
+                    ++lost;
+                if (Step) out[i0 + 32 * y] = page[y];  // those that are no pages get others below
+            }
         }
         if (Step) {
+#pragma unroll 4
+            for (int i = k.pages + lane; i < a.max_pages; i += 32) out[i] = -1;
             lost = __reduce_add_sync(0xffffffffu, lost);
-            int last = k.part ? k.old[k.full] : -1;
             if (!is_page(a, last)) last = -1;
-            if (lane < kOne) store_remote(&sm.last[b], static_cast<unsigned>(lane), last);
+            if (lane < kOne) {
+                store_remote(&sm.last[b], static_cast<unsigned>(lane), last);
+                asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(map_rank(&sm.most, static_cast<unsigned>(lane))),
+                             "r"(lost + k.pages - k.full) : "memory");
+            }
             if (lane == 0) sm.lost[b / kOne] = lost;
         }
         if (lane == 0) sm.kept[b / kOne] = k;
@@ -406,118 +430,132 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_one_kernel(const PagesA
     }
     cluster_sync();
     // ---- this CTA's words, of all rows
+    const int w0 = static_cast<int>(rank) * each;
+    unsigned held = 0, pins = 0;
     if (mine) {
-        unsigned bits = sm.pins[tid];
+        held = pins = sm.pins[tid];
 #pragma unroll
-        for (unsigned y = 0; y < kOne; ++y) bits |= load_remote(&sm.marks[w], y);
-        sm.held[tid] = bits;
+        for (unsigned y = 0; y < kOne; ++y) held |= load_remote(&sm.marks[w], y);
+        sm.held[tid] = held;
     }
-    if (!Step) {
-        int all;
-        block_prefix(mine ? __popc(sm.held[tid]) : 0, &all);
-        if (tid < kOne) store_remote(&sm.count[rank], static_cast<unsigned>(tid), all);
-    }
-    cluster_sync();
-    int n = 0;  // compaction: pages held
+    int wants = 0, given_out = 0;  // step: new pages wanted, and there to be given out
+    int n = 0, moves = 0;          // compaction: pages held, pages that move
     if (Step) {
+        // A partly filled page of any row is not free, whoever keeps it: full, pinned or this.
+        if (mine) sm.used[tid] = held;
+        __syncthreads();
+        for (int b = tid; b < a.n_out; b += kPlanThreads) {
+            const int page = sm.last[b], at = page / 32 - w0;
+            if (page >= 0 && at >= 0 && at < each) atomicOr(&sm.used[at], 1u << (page % 32));
+        }
+        __syncthreads();
+        const unsigned free_bits = mine ? ~sm.used[tid] & pages_of_word(a, w) : 0u;
+        int all;
+        int at = block_prefix(__popc(free_bits), &all);
+        if (tid < kOne) store_remote(&sm.total[rank], static_cast<unsigned>(tid), all);
+        cluster_sync();
         // ---- which rows keep their partly filled page, and what each wants
         for (int b = row0; b < a.n_out; b += kStride) {
             const Kept k = sm.kept[b / kOne];
             const int page = sm.last[b];
             int stays = 0;
             if (page >= 0) {
+                const unsigned bits = load_remote(&sm.held[page / 32 % each], static_cast<unsigned>(page / 32 / each));
                 bool first = true;
                 for (int y = lane; y < b; y += 32) first = first && sm.last[y] != page;
-                const unsigned owner = static_cast<unsigned>(page / 32 / each);
-                unsigned *at = &sm.held[page / 32 % each];
-                // a row whose page this is sets the bit: no other row is its first
-                stays = __all_sync(0xffffffffu, first) && !(load_remote(at, owner) >> (page % 32) & 1u);
-                stays = __shfl_sync(0xffffffffu, stays, 0);
-                if (stays && lane == 0)
-                    asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(map_rank(at, owner)),
-                                 "r"(1u << (page % 32)) : "memory");
+                stays = __all_sync(0xffffffffu, first) && !(bits >> (page % 32) & 1u);
             }
             const int lost = sm.lost[b / kOne];
             if (lane < kOne) store_remote(&sm.want[b], static_cast<unsigned>(lane), lost + k.pages - k.full - stays);
             if (lane == 0) sm.stays[b / kOne] = stays;
         }
+        // ---- the list of free pages, as far as they may be wanted
+        for (int y = 0; y < kOne; ++y) {
+            if (y == static_cast<int>(rank)) at += given_out;
+            given_out += static_cast<int>(sm.total[y]);
+        }
+        each_bit(w0, each, free_bits, at, sm.most, [&](int page, int k) { a.list[k] = page; });
+        __threadfence();
         cluster_sync();
-    } else {
-        for (int y = 0; y < kOne; ++y) n += sm.count[y];
-    }
-    // ---- places in the list: of the rows' wants, and of the free pages of each word
-    int wants = Step ? 0 : INT_MAX;
-    if (Step)
+        // ---- the places of the rows' wants in it
         for (int b0 = 0; b0 < a.n_out; b0 += kPlanThreads) {
             const int b = b0 + tid;
-            int all;
-            const int at = wants + block_prefix(b < a.n_out ? sm.want[b] : 0, &all);
-            if (b < a.n_out) sm.want[b] = at;
+            const int first = wants + block_prefix(b < a.n_out ? sm.want[b] : 0, &all);
+            if (b < a.n_out) sm.want[b] = first;
             wants += all;
         }
-    const unsigned below = n - w * 32 >= 32 ? 0xffffffffu : n > w * 32 ? (1u << (n - w * 32)) - 1u : 0u;  // pages < n
-    const unsigned free_bits = !mine ? 0u : ~sm.held[tid] & (Step ? pages_of_word(a, w) : below);
-    const unsigned moved = Step || !mine ? 0u : sm.held[tid] & ~below & ~sm.pins[tid];
-    int2 all = make_int2(0, 0);
-    const int free_at = block_prefix(__popc(free_bits), &all.x);
-    const int moved_at = Step ? 0 : block_prefix(__popc(moved), &all.y);
-    if (tid < kOne) {
-        store_remote(&sm.totals[rank].x, static_cast<unsigned>(tid), all.x);
-        if (!Step) store_remote(&sm.totals[rank].y, static_cast<unsigned>(tid), all.y);
-    }
-    cluster_sync();
-    int2 from = make_int2(0, 0), sum = make_int2(0, 0);
-    for (int y = 0; y < kOne; ++y) {
-        if (y == static_cast<int>(rank)) from = sum;
-        sum.x += sm.totals[y].x;
-        if (!Step) sum.y += sm.totals[y].y;
-    }
-    const int w0 = static_cast<int>(rank) * each;
-    each_bit(w0, free_bits, from.x + free_at, wants, [&](int page, int k) { a.list[k] = page; });
-    if (!Step) {
-        each_bit(w0, moved, from.y + moved_at, INT_MAX, [&](int page, int k) {
+        __syncthreads();
+    } else {
+        int all;
+        const unsigned movable = held & ~pins;
+        const unsigned before = block_prefix(__popc(held) | static_cast<unsigned>(__popc(movable)) << 16, &all);  // at most 2^15 each
+        if (tid < kOne) store_remote(&sm.total[rank], static_cast<unsigned>(tid), all);
+        cluster_sync();
+        // held pages before this word, those of them that may move, and of the latter those below page n
+        int held_at = static_cast<int>(before & 0xffffu), movable_at = static_cast<int>(before >> 16), below_n = 0;
+        for (int y = 0; y < kOne; ++y) {
+            if (y == static_cast<int>(rank)) held_at += n, movable_at += moves;
+            n += static_cast<int>(sm.total[y] & 0xffffu);
+            moves += static_cast<int>(sm.total[y] >> 16);
+        }
+        const int owner = n / 32 / each;  // of page n
+        for (int y = 0; y < owner && y < kOne; ++y) below_n += static_cast<int>(sm.total[y] >> 16);
+        auto below = [&](int x) { return n - x * 32 >= 32 ? 0xffffffffu : n > x * 32 ? (1u << (n - x * 32)) - 1u : 0u; };  // pages < n
+        const int word = owner * each + tid;
+        int part = 0;
+        if (tid < each && word * 32 < n) {
+            const unsigned there = static_cast<unsigned>(owner);
+            part = __popc(load_remote(&sm.held[tid], there) & ~load_remote(&sm.pins[tid], there) & below(word));
+        }
+        block_prefix(part, &all);
+        below_n += all;
+        moves -= below_n;
+        // the free pages before a word are those that are not held
+        each_bit(w0, each, mine ? ~held & below(w) : 0u, w * 32 - held_at, INT_MAX, [&](int page, int k) { a.list[k] = page; });
+        each_bit(w0, each, movable & ~below(w), movable_at + __popc(movable & below(w)) - below_n, INT_MAX, [&](int page, int k) {
             a.move[page] = k;
             a.copies[3 * k] = page;
             a.copies[3 * k + 2] = a.P;
         });
-        if (a.pinned) each_bit(w0, !mine ? 0u : sm.held[tid] & ~below & sm.pins[tid], 0, INT_MAX, [&](int page, int) { a.move[page] = -1; });
+        if (a.pinned) each_bit(w0, each, held & ~below(w) & pins, 0, INT_MAX, [&](int page, int) { a.move[page] = -1; });
+        __threadfence();
+        cluster_sync();
     }
-    __threadfence();
-    cluster_sync();
     // ---- the new rows
-    if (rank == 0 && tid == 0) *a.free_pages = Step ? sum.x - wants : a.n_pages - n;
+    if (rank == 0 && tid == 0) *a.free_pages = Step ? given_out - wants : a.n_pages - n;
     for (int b = row0; b < a.n_out; b += kStride) {
         const Kept k = sm.kept[b / kOne];
         int32_t *out = a.table_out + b * a.out_stride;
         if (!Step) {
-#pragma unroll 4
-            for (int i = lane; i < a.max_pages; i += 32) {
-                int page = i < k.pages ? k.old[i] : -1;
-                if (!is_page(a, page)) page = -1;
-                if (page >= n) {
-                    const int to = __ldcg(&a.move[page]);
-                    if (to >= 0) page = __ldcg(&a.list[to]);
+            for (int i0 = lane; i0 < a.max_pages; i0 += 32 * kBatch) {
+                int page[kBatch];
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y) page[y] = i0 + 32 * y < k.pages ? k.old[i0 + 32 * y] : -1;
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y) {
+                    if (!is_page(a, page[y])) page[y] = -1;
+                    const int to = page[y] >= n ? __ldcg(&a.move[page[y]]) : -1;
+                    if (to >= 0) page[y] = __ldcg(&a.list[to]);
                 }
-                out[i] = page;
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y)
+                    if (i0 + 32 * y < a.max_pages) out[i0 + 32 * y] = page[y];
             }
             continue;
         }
         const int stays = sm.stays[b / kOne], lost = sm.lost[b / kOne], first = sm.want[b], kept = k.full + stays;
-        auto given = [&](int nth) { return nth < sum.x ? __ldcg(&a.list[nth]) : -1; };
-        if (lost == 0) {
-#pragma unroll 16
-            for (int i = lane; i < a.max_pages; i += 32)
-                out[i] = i < kept ? k.old[i] : i < k.pages ? given(first + i - kept) : -1;
-        } else {  // rare: entries that are no pages get new ones first
+        auto given = [&](int nth) { return nth < given_out ? __ldcg(&a.list[nth]) : -1; };
+        if (stays && lane == 0) out[k.full] = sm.last[b];
+#pragma unroll 4
+        for (int i = kept + lane; i < k.pages; i += 32) out[i] = given(first + lost + i - kept);
+        if (lost > 0) {  // rare: entries that are no pages get the first of the new ones
             int nth = first;
-            for (int i0 = 0; i0 < a.max_pages; i0 += 32) {
+            for (int i0 = 0; i0 < k.full; i0 += 32) {
                 const int i = i0 + lane;
-                int page = i < kept ? k.old[i] : -1;
-                const bool wanted = i < k.pages && !is_page(a, page);
+                const bool wanted = i < k.full && !is_page(a, k.old[i]);
                 const unsigned some = __ballot_sync(0xffffffffu, wanted);
-                page = wanted ? given(nth + __popc(some & ((1u << lane) - 1u))) : i < kept ? page : -1;
+                if (wanted) out[i] = given(nth + __popc(some & ((1u << lane) - 1u)));
                 nth += __popc(some);
-                if (i < a.max_pages) out[i] = page;
             }
         }
         if (lane == 0) {
@@ -531,7 +569,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_one_kernel(const PagesA
     }
     if (!Step)
         for (int i = static_cast<int>(rank) * kPlanThreads + tid; i < a.n_copies; i += kOne * kPlanThreads) {
-            if (i < sum.y) {
+            if (i < moves) {
                 a.copies[3 * i + 1] = __ldcg(&a.list[i]);
             } else {
                 a.copies[3 * i] = a.copies[3 * i + 1] = -1;
