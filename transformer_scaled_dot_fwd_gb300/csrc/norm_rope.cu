@@ -14,9 +14,15 @@
 // or three round trips would otherwise stand in front of every block's rows; angles and
 // weights are read again with each row, from shared memory and L1.
 //
+// The arithmetic of a row is most of the issue slots (some 200 instructions for 4 rows
+// of a warp), so it goes two elements at a time (f32x2), each value with the roundings that
+// rope.cu's turn has, and the layouts of the pairs are two kernels.
+//
 // Measured: 16385 tokens of 32 + 8 heads of depth 128 into pages of 64 rows (402 MB moved)
-// 74 us, 5.4 TB/s (without the load ahead 82-89 us; one token a block 80 us); a step of 64
-// tokens 4.9 us a call.
+// 68.5 us, 5.9 TB/s; a step of 64 tokens 4.9 us a call, 3.5 of them in the kernel.  Eight
+// blocks an SM 70.6 us, ten 72.5 (registers spill); element by element 74; both layouts in
+// one kernel 2 us more; two or three rows ahead 78-89 us (fewer blocks an SM); without
+// the load ahead 82-89 us.  One token a block 80 us, three to eight as two.
 //
 // Rows whose addresses, strides or pairs do not allow 16-byte accesses take VEC = 1, with
 // a warp a row.  Interleaved pairs need no multiple of VEC: the unit in which the turned
@@ -31,6 +37,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kResident = 9;  // blocks an SM: 56 registers a thread
 constexpr int kTokens = 2;  // a block takes at most
 
 // VEC elements, as the 16 bytes (or the single element) they are moved in.
@@ -73,8 +80,8 @@ struct Token {
     int cached;            // the token has a page
 };
 
-template <typename T, int VEC, int D>
-__global__ void __launch_bounds__(kThreads, 8)
+template <typename T, int VEC, int D, bool Interleaved>
+__global__ void __launch_bounds__(kThreads, kResident)
     norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const int tokens, const int rows_per_block) {
     constexpr int kUnits = D / (2 * VEC);                // of a row
     constexpr int kLanes = kUnits < 32 ? kUnits : 32;    // that share a row
@@ -89,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 8)
     const int t0 = blockIdx.x * tokens;
     const int nt = min(tokens, a.T - t0);
     const bool append = a.append != 0;
+    const bool interleaved = VEC > 1 ? Interleaved : a.interleaved != 0;
     const int half = a.rotary_dim / 2;
     const int u0 = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
     const int r0 = blockIdx.y * rows_per_block;
@@ -105,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 8)
     };
     auto columns = [&](int r, int y, int *e0, int *e1) {
         const int u = u0 + y * kLanes;
-        const bool split = r < a.H + a.H_kv && !a.interleaved && u * VEC < half;  // the pairs' second halves lie apart
+        const bool split = r < a.H + a.H_kv && !interleaved && u * VEC < half;  // the pairs' second halves lie apart
         *e0 = split ? u * VEC : 2 * u * VEC;
         *e1 = split ? half + u * VEC : 2 * u * VEC + VEC;
     };
@@ -211,21 +219,29 @@ __global__ void __launch_bounds__(kThreads, 8)
                 x_hi[y].unpack(x[y] + VEC);
             }
             if (w) {
-                float ss = 0.f;
+                uint64_t sq = 0;
 #pragma unroll
                 for (int y = 0; y < kEach; ++y)
 #pragma unroll
-                    for (int p = 0; p < 2 * VEC; ++p) ss = fmaf(x[y][p], x[y][p], ss);
+                    for (int p = 0; p < 2 * VEC; p += 2) {
+                        const uint64_t v = f2_pack(x[y][p], x[y][p + 1]);
+                        sq = ffma2(v, v, sq);
+                    }
+                float ss = f2_lo(sq) + f2_hi(sq);
 #pragma unroll
                 for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(mask, ss, d);
                 const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+                const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
                 for (int y = 0; y < kEach; ++y) {
                     float ww[2 * VEC];
                     reinterpret_cast<const U *>(w + e0[y])->unpack(ww);
                     reinterpret_cast<const U *>(w + e1[y])->unpack(ww + VEC);
 #pragma unroll
-                    for (int p = 0; p < 2 * VEC; ++p) x[y][p] = x[y][p] * inv * ww[p];
+                    for (int p = 0; p < 2 * VEC; p += 2) {
+                        const uint64_t v = fmul2(fmul2(f2_pack(x[y][p], x[y][p + 1]), inv2), f2_pack(ww[p], ww[p + 1]));
+                        x[y][p] = f2_lo(v), x[y][p + 1] = f2_hi(v);
+                    }
                 }
             }
 #pragma unroll
@@ -239,12 +255,20 @@ __global__ void __launch_bounds__(kThreads, 8)
                         // past the last pair nothing is multiplied: 0 times an infinity is none
                         if (first + p < half) f = f2, g = g2;
                     };
-                    if (a.interleaved) {
+                    if (interleaved) {
 #pragma unroll
                         for (int p = 0; p < VEC; ++p) turn(p, x[y][2 * p], x[y][2 * p + 1]);
-                    } else {
+                    } else if (VEC == 1) {
+                        turn(0, x[y][0], x[y][VEC]);
+                    } else {  // whole units of pairs, two at a time
 #pragma unroll
-                        for (int p = 0; p < VEC; ++p) turn(p, x[y][p], x[y][VEC + p]);
+                        for (int p = 0; p < VEC; p += 2) {
+                            const uint64_t c = f2_pack(cs[p], cs[p + 1]), s = f2_pack(sn[p], sn[p + 1]);
+                            const uint64_t f = f2_pack(x[y][p], x[y][p + 1]), g = f2_pack(x[y][VEC + p], x[y][VEC + p + 1]);
+                            const uint64_t f2 = ffma2(f, c, fmul2(fmul2(g, f2_pack(-1.f, -1.f)), s)), g2 = ffma2(f, s, fmul2(g, c));
+                            x[y][p] = f2_lo(f2), x[y][p + 1] = f2_hi(f2);
+                            x[y][VEC + p] = f2_lo(g2), x[y][VEC + p + 1] = f2_hi(g2);
+                        }
                     }
                 }
                 x_lo[y].pack(x[y]);
@@ -265,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 8)
     }
 }
 
-template <typename T, int VEC, int D>
+template <typename T, int VEC, int D, bool Interleaved>
 cudaError_t launch_t(const NormRopeArgs &a) {
     const int rows = a.H + a.H_kv * (a.append ? 2 : 1);
     const long long sms = a.n_sm > 0 ? a.n_sm : 1;
@@ -280,17 +304,20 @@ cudaError_t launch_t(const NormRopeArgs &a) {
     split = split > most ? most : split;
     const int per = static_cast<int>((rows + split - 1) / split);
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((rows + per - 1) / per));
-    return launch_pdl(norm_rope_kernel<T, VEC, D>, grid, dim3(kThreads), 0, a.stream, a, tokens, per);
+    return launch_pdl(norm_rope_kernel<T, VEC, D, Interleaved>, grid, dim3(kThreads), 0, a.stream, a, tokens, per);
 }
 
 }  // namespace
 
+template <typename T, int VEC, int D>
+static cudaError_t launch_d(const NormRopeArgs &a, bool wide) {
+    if (!wide) return launch_t<T, 1, D, false>(a);
+    return a.interleaved ? launch_t<T, VEC, D, true>(a) : launch_t<T, VEC, D, false>(a);
+}
+
 cudaError_t launch_norm_rope(const NormRopeArgs &a, bool f32, bool wide) {
-    if (a.D == 64)
-        return f32 ? (wide ? launch_t<float, 4, 64>(a) : launch_t<float, 1, 64>(a))
-                   : (wide ? launch_t<__nv_bfloat16, 8, 64>(a) : launch_t<__nv_bfloat16, 1, 64>(a));
-    return f32 ? (wide ? launch_t<float, 4, 128>(a) : launch_t<float, 1, 128>(a))
-               : (wide ? launch_t<__nv_bfloat16, 8, 128>(a) : launch_t<__nv_bfloat16, 1, 128>(a));
+    if (a.D == 64) return f32 ? launch_d<float, 4, 64>(a, wide) : launch_d<__nv_bfloat16, 8, 64>(a, wide);
+    return f32 ? launch_d<float, 4, 128>(a, wide) : launch_d<__nv_bfloat16, 8, 128>(a, wide);
 }
 
 }  // namespace attn
