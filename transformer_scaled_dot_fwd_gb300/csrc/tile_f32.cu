@@ -29,6 +29,11 @@
 // Earlier forms, 128 threads a tile of 64 keys: one a block 90 us, two 47 us, four 43
 // us, with equal shares 40 us; 8 rows a thread 45 us.
 //
+// Single tokens over pages leave most of the 32 rows empty: with up to four, only the
+// first row of a thread is computed (64 tokens over 2000 keys, H 8 / 2, D 64: 39 against
+// 76 us), and a split of the keys may be as short as a unit for each worker (six
+// sequences of up to 1024 keys and two chunks: 11.0 us, with 64 keys at least and all rows 14.7).
+//
 // Packed rows: a block's 32 rows lie in one sequence (a block that straddled two
 // would walk the keys of both), found by a search, not a table: sequence s
 // owns the blocks from cu[s] / 32 + s on, a few of which stay empty.  Tree rows
@@ -100,10 +105,11 @@ __device__ __forceinline__ int row_of(int i) { return static_cast<int>(threadIdx
 // block calls it, with the copies of Q committed as one group): K row j at kat(j, in),
 // V row j at vat(j, in), an address to be read where `in` stays true.  visible(i, key0)
 // gives the bits of keys key0 + tx + 8 j, j < 4, of row_of(i).  A warp none of whose rows is used
-// (`active` is false) only copies and keeps step.
-template <int D, int W, typename KAt, typename VAt, typename Visible>
+// (`active` is false) only copies and keeps step.  Few: where `few` is set only the first of
+// a thread's rows is used (a block of up to four rows).
+template <int D, int W, bool Few = false, typename KAt, typename VAt, typename Visible>
 __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int k0, int k1, float sl2, bool active,
-                                     Rows4<D> &st, Visible visible) {
+                                     Rows4<D> &st, Visible visible, bool few = false) {
     const int worker = threadIdx.x / 64, tid = threadIdx.x % 64, half = tid / 32, tx = tx_of(), ty = ty_of();
     auto &sm = smem.w[worker];
     auto &sp = sm.p[half];
@@ -139,18 +145,18 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
         cp_async_wait<1>();  // K of this tile (V may still be on its way)
         sync();
         bool hidden = false;  // a row of the thread misses a key of the tile (those past k1 are zeros)
-        auto score = [&](auto n) {
-            constexpr int N = decltype(n)::value;
-            uint64_t s2[4][N] = {};  // sums over even and over odd depths
+        auto score = [&](auto n, auto rows) {
+            constexpr int N = decltype(n)::value, R = decltype(rows)::value;
+            uint64_t s2[R][N] = {};  // sums over even and over odd depths
 #pragma unroll 4
             for (int d = 0; d < D; d += 4) {
-                ulonglong2 qa[4], kb[N];
+                ulonglong2 qa[R], kb[N];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const ulonglong2 *>(&smem.q[row_of(i)][d]);
+                for (int i = 0; i < R; ++i) qa[i] = *reinterpret_cast<const ulonglong2 *>(&smem.q[row_of(i)][d]);
 #pragma unroll
                 for (int j = 0; j < N; ++j) kb[j] = *reinterpret_cast<const ulonglong2 *>(&sm.k[tx + 8 * j][d]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         s2[i][j] = ffma2(qa[i].x, kb[j].x, s2[i][j]);
@@ -158,7 +164,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
                     }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
                 const uint32_t see = visible(i, key0);
                 float s[N], mt = -INFINITY;
 #pragma unroll
@@ -191,32 +197,39 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
                 for (int e = 0; e < 2 * C; ++e) st.o[i][e] = fmul2(st.o[i][e], corr2);
             }
         };
+        auto score_units = [&](auto rows) {
+            if (n_units == 4)
+                score(std::integral_constant<int, 4>{}, rows);
+            else if (n_units == 3)
+                score(std::integral_constant<int, 3>{}, rows);
+            else if (n_units == 2)
+                score(std::integral_constant<int, 2>{}, rows);
+            else
+                score(std::integral_constant<int, 1>{}, rows);
+        };
         if (!active) {
-        } else if (n_units == 4)
-            score(std::integral_constant<int, 4>{});
-        else if (n_units == 3)
-            score(std::integral_constant<int, 3>{});
-        else if (n_units == 2)
-            score(std::integral_constant<int, 2>{});
+        } else if (Few && few)
+            score_units(std::integral_constant<int, 1>{});
         else
-            score(std::integral_constant<int, 1>{});
+            score_units(std::integral_constant<int, 4>{});
         // every row of the warp sees every key: plain FMAs; otherwise a weight of zero, that
         // of a key the row does not see, must not meet an infinite or NaN value
         const bool edge = __any_sync(0xffffffffu, hidden);
         cp_async_wait<0>();  // V of this tile
         sync();              // both warps are done with K; V and P are visible
         if (more) load(&sm.k[0][0], D + 4, kat, key0 + kKeys);
-        auto mix = [&](auto guarded) {
+        auto mix = [&](auto guarded, auto rows) {
+            constexpr int R = decltype(rows)::value;
 #pragma unroll 1
             for (int j = 0; j < 8 * n_units; j += 4) {
-                float4 p4[4];
+                float4 p4[R];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(&sp[ty + 4 * i][j]);
+                for (int i = 0; i < R; ++i) p4[i] = *reinterpret_cast<const float4 *>(&sp[ty + 4 * i][j]);
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
-                    uint64_t p2[4];
+                    uint64_t p2[R];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < R; ++i) {
                         const float p = jj == 0 ? p4[i].x : jj == 1 ? p4[i].y : jj == 2 ? p4[i].z : p4[i].w;
                         p2[i] = f2_pack(p, p);
                     }
@@ -224,7 +237,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
                     for (int c = 0; c < C; ++c) {
                         const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sm.v[j + jj][32 * c + 4 * tx]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < R; ++i) {
                             const uint64_t a = ffma2(p2[i], x.x, st.o[i][2 * c]), b = ffma2(p2[i], x.y, st.o[i][2 * c + 1]);
                             if (!decltype(guarded)::value || f2_lo(p2[i]) != 0.f) {
                                 st.o[i][2 * c] = a;
@@ -236,10 +249,12 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
             }
         };
         if (!active) {
-        } else if (edge)
-            mix(std::true_type{});
+        } else if (Few && few)
+            mix(std::true_type{}, std::integral_constant<int, 1>{});
+        else if (edge)
+            mix(std::true_type{}, std::integral_constant<int, 4>{});
         else
-            mix(std::false_type{});
+            mix(std::false_type{}, std::integral_constant<int, 4>{});
         sync();  // V and P are free
         if (more) load(&sm.v[0][0], D, vat, key0 + kKeys);
     }
@@ -592,9 +607,10 @@ __device__ __forceinline__ PagedBlock paged_block(const PagedArgs &a, int w, int
     p.keys = max(0, p.past + min(p.r0 + kRows - 1, p.n * G - 1) / G + 1);
     return p;
 }
-// Keys of a split, in units of 8, at least 64.
+// Keys of a split, in units of 8, at least 8 for each of the block's workers.
+template <int W>
 __device__ __forceinline__ int paged_share(int keys, int n_split) {
-    return max(64, ((keys + n_split - 1) / n_split + 7) / 8 * 8);
+    return max(8 * W, ((keys + n_split - 1) / n_split + 7) / 8 * 8);
 }
 
 // Block x: (32 rows, cached head, split of the keys).  Up to eight splits are a cluster,
@@ -610,7 +626,7 @@ __global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) paged_f32_
     const int c = blockIdx.x % a.n_split, g = blockIdx.x / a.n_split % a.H_kv, w = blockIdx.x / a.n_split / a.H_kv;
     const PagedBlock p = paged_block(a, w, tid % 32);
     if (p.n == 0) return;  // as every CTA of the cluster
-    const int rows = p.n * G, share = paged_share(p.keys, a.n_split);
+    const int rows = p.n * G, share = paged_share<W>(p.keys, a.n_split);
     const int k0 = static_cast<int>(min(static_cast<long long>(c) * share, static_cast<long long>(p.keys)));
     const int k1 = min(k0 + share, p.keys);
     if (k0 >= k1 && !cluster) return;  // the merge never reads this split
@@ -639,14 +655,14 @@ __global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) paged_f32_
                 return base + (in ? page * ps + (key - entry * a.P) * rs : 0ll);
             };
         };
-        walk<D, W>(sm, pages_at(static_cast<const float *>(a.k) + g * a.k_hs, a.k_ps, a.k_rs),
+        walk<D, W, true>(sm, pages_at(static_cast<const float *>(a.k) + g * a.k_hs, a.k_ps, a.k_rs),
                    pages_at(static_cast<const float *>(a.v) + g * a.v_hs, a.v_ps, a.v_rs), k0, k1, a.scale * kLog2e,
                    __any_sync(0xffffffffu, lim[0] > k0 || lim[1] > k0 || lim[2] > k0 || lim[3] > k0), st, [&](int i, int key0) {
                        uint32_t see = 0;
 #pragma unroll
                        for (int j = 0; j < 4; ++j) see |= (key0 + tx + 8 * j < lim[i] ? 1u : 0u) << j;
                        return see;
-                   });
+                   }, rows - p.r0 <= 4);
     } else {
         cp_async_wait<0>();
     }
@@ -678,7 +694,7 @@ __global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) paged_f32_
 }
 
 // One warp per row of a block: the parts of its splits.
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(256) paged_merge_f32_kernel(const PagedArgs a) {
     griddep_launch_dependents();
     griddep_wait();
@@ -688,7 +704,7 @@ __global__ void __launch_bounds__(256) paged_merge_f32_kernel(const PagedArgs a)
     const int r = p.r0 + rr;
     if (p.n == 0 || r >= p.n * G || lane >= D / 4) return;
     const long long token = p.c0 + r / G;
-    const int h = g * G + r % G, share = paged_share(p.keys, a.n_split);
+    const int h = g * G + r % G, share = paged_share<W>(p.keys, a.n_split);
     const bool live = p.past + r / G >= 0;
     const size_t first = ((static_cast<size_t>(w) * a.H_kv + g) * kRows + rr) * a.n_split;
     float2 x[kAhead];
@@ -711,15 +727,18 @@ cudaError_t launch_paged_f32_w(const PagedArgs &a, unsigned blocks) {
     e = launch_clusters(paged_f32_kernel<D, W>, cluster ? static_cast<unsigned>(a.n_split) : 1u, blocks * a.n_split,
                         kThreads<W>, smem, a.stream, a);
     if (e != cudaSuccess || cluster) return e;
-    return launch_pdl(paged_merge_f32_kernel<D>, dim3(blocks * (kRows / 8)), dim3(256), 0, a.stream, a);
+    return launch_pdl(paged_merge_f32_kernel<D, W>, dim3(blocks * (kRows / 8)), dim3(256), 0, a.stream, a);
 }
 
 template <int D>
 cudaError_t launch_paged_f32_t(const PagedArgs &a) {
     const unsigned blocks = static_cast<unsigned>(paged_f32_blocks(a) * a.H_kv);
-    // more blocks than SMs: two an SM (as for trees)
-    return blocks * static_cast<long long>(a.n_split) > a.n_sm ? launch_paged_f32_w<D, kMany<D> / 2>(a, blocks)
-                                                               : launch_paged_f32_w<D, kMany<D>>(a, blocks);
+    // More blocks than SMs: two an SM (as for trees).  Clusters of eight cannot take every
+    // SM: of 16 with one block an SM one waits (eight sequences of 1000 keys, H 8 / 2: 16.5
+    // against 10.5 us with two).
+    const long long sms = a.n_split == 8 ? a.n_sm * 2 / 3 : a.n_sm;
+    return blocks * static_cast<long long>(a.n_split) > sms ? launch_paged_f32_w<D, kMany<D> / 2>(a, blocks)
+                                                            : launch_paged_f32_w<D, kMany<D>>(a, blocks);
 }
 
 }  // namespace
@@ -756,8 +775,9 @@ long long paged_f32_blocks(const PagedArgs &a) {
 }
 
 int paged_f32_splits(const PagedArgs &a) {
-    // two blocks an SM, 128 keys at least a block where the table's rows are full (1 and 4 an SM:
-    // 17.1 and 14.9 against 14.4 us for eight sequences, 101 and 81 against 74 for 64 of 2000 keys)
+    // Two blocks an SM (1 and 4: 43.3 and 44.1 against 39.1 us for 64 single tokens over 2000 keys, H 8 / 2,
+    // D 64), 128 keys at least a block where the table's rows are full (64 and 256: 19.3 and
+    // 16.9 against 11.7 us for four over 500 keys, H 32 / 8, D 128).
     const long long blocks = paged_f32_blocks(a) * a.H_kv, want = 2LL * (a.n_sm > 0 ? a.n_sm : 1);
     long long n = blocks > 0 ? want / blocks : 1;
     const long long most = (static_cast<long long>(a.max_len) + 127) / 128;
