@@ -53,6 +53,7 @@ cudaError_t launch_paged_f32(const PagedArgs &a);
 long long paged_f32_blocks(const PagedArgs &a);
 int paged_f32_splits(const PagedArgs &a);
 
+__device__ __forceinline__ bool is_page(const PagedArgs &a, int page) { return page >= 0 && page < a.n_pages; }
 // Entry of the page table that holds a key (a division is some 40 instructions).
 __device__ __forceinline__ int page_of_key(const PagedArgs &a, int key) {
     return a.page_magic ? static_cast<int>(__umulhi(static_cast<unsigned>(key), a.page_magic)) : key / a.P;

@@ -100,8 +100,6 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
-__device__ __forceinline__ bool is_page(const PagedArgs &a, int page) { return page >= 0 && page < a.n_pages; }
-
 // Inclusive prefix sum over the warp.
 __device__ __forceinline__ long long prefix(long long v, int lane) {
 #pragma unroll 1

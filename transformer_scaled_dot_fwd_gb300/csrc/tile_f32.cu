@@ -31,8 +31,10 @@
 //
 // Single tokens over pages leave most of the 32 rows empty: with up to four, only the
 // first row of a thread is computed (64 tokens over 2000 keys, H 8 / 2, D 64: 39 against
-// 76 us), and a split of the keys may be as short as a unit for each worker (six
-// sequences of up to 1024 keys and two chunks: 11.0 us, with 64 keys at least and all rows 14.7).
+// 76 us), a split of the keys may be as short as a unit for each worker (six
+// sequences of up to 1024 keys and two chunks: 11.0 us, with 64 keys at least and all rows
+// 14.7), and the entries of the table are looked up once a unit, not once a copy (34 and 10.7
+// us; 64 tokens over 2000 keys, H 8 / 8, D 128, 1.05 GB: 220 us, 4.8 TB/s, against 310).
 //
 // Packed rows: a block's 32 rows lie in one sequence (a block that straddled two
 // would walk the keys of both), found by a search, not a table: sequence s
@@ -103,11 +105,12 @@ __device__ __forceinline__ int row_of(int i) { return static_cast<int>(threadIdx
 
 // This worker's part of keys [k0, k1), an equal share in units of 8 keys (the whole
 // block calls it, with the copies of Q committed as one group): K row j at kat(j, in),
-// V row j at vat(j, in), an address to be read where `in` stays true.  visible(i, key0)
+// V row j at vat(j, in), an address to be read where `in` is true.  visible(i, key0)
 // gives the bits of keys key0 + tx + 8 j, j < 4, of row_of(i).  A warp none of whose rows is used
-// (`active` is false) only copies and keeps step.  Few: where `few` is set only the first of
-// a thread's rows is used (a block of up to four rows).
-template <int D, int W, bool Few = false, typename KAt, typename VAt, typename Visible>
+// (`active` is false) only copies and keeps step.
+// Paged: k0 is a multiple of 8, kat and vat give a unit's first row, its stride and whether it may
+// be read; where `few` is set only the first of a thread's rows is used (a block of up to four).
+template <int D, int W, bool Paged = false, typename KAt, typename VAt, typename Visible>
 __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int k0, int k1, float sl2, bool active,
                                      Rows4<D> &st, Visible visible, bool few = false) {
     const int worker = threadIdx.x / 64, tid = threadIdx.x % 64, half = tid / 32, tx = tx_of(), ty = ty_of();
@@ -121,13 +124,27 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
     auto units = [&](int key0) { return min((last - key0 + 7) / 8, kKeys / 8); };
     auto load = [&](float *dst, int stride, auto at, int key0) {
         const uint32_t to = smem_u32(dst);
-        const int n = units(key0) * (8 * D / 4);
+        if constexpr (Paged) {  // a unit lies in one page: looked up once
+            const int n = units(key0);
+#pragma unroll
+            for (int u = 0; u < kKeys / 8; ++u) {
+                if (u >= n) break;
+                const auto page = at(key0 + 8 * u);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int row = i * (256 / D) + tid / (D / 4), c = tid % (D / 4);
+                    const bool in = page.in && key0 + 8 * u + row < last;
+                    cp_async16(to + ((8 * u + row) * stride + 4 * c) * 4, page.row + (in ? row * page.stride : 0) + 4 * c, in ? 16u : 0u);
+                }
+            }
+        } else {
+            const int n = units(key0) * (8 * D / 4);
 #pragma unroll 8
-        for (int i = tid; i < n; i += 64) {
-            const int row = i / (D / 4), c = i % (D / 4);
-            bool in = key0 + row < last;
-            const float *src = at(key0 + row, in) + 4 * c;
-            cp_async16(to + (row * stride + 4 * c) * 4, src, in ? 16u : 0u);
+            for (int i = tid; i < n; i += 64) {
+                const int row = i / (D / 4), c = i % (D / 4);
+                const bool in = key0 + row < last;
+                cp_async16(to + (row * stride + 4 * c) * 4, at(key0 + row, in) + 4 * c, in ? 16u : 0u);
+            }
         }
         cp_async_commit();
     };
@@ -208,7 +225,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
                 score(std::integral_constant<int, 1>{}, rows);
         };
         if (!active) {
-        } else if (Few && few)
+        } else if (Paged && few)
             score_units(std::integral_constant<int, 1>{});
         else
             score_units(std::integral_constant<int, 4>{});
@@ -249,7 +266,7 @@ __device__ __forceinline__ void walk(F32Smem<D, W> &smem, KAt kat, VAt vat, int 
             }
         };
         if (!active) {
-        } else if (Few && few)
+        } else if (Paged && few)
             mix(std::true_type{}, std::integral_constant<int, 1>{});
         else if (edge)
             mix(std::true_type{}, std::integral_constant<int, 4>{});
@@ -648,11 +665,16 @@ __global__ void __launch_bounds__(kThreads<W>, W == kMany<D> ? 1 : 2) paged_f32_
     reset(st);
     if (k0 < k1) {
         const int32_t *table = a.page_table + p.s * a.table_stride;
+        struct Unit {
+            const float *row;
+            long long stride;
+            bool in;
+        };
         auto pages_at = [&](const float *base, long long ps, long long rs) {
-            return [=](int key, bool &in) {
-                const int entry = page_of_key(a, key), page = in ? table[entry] : 0;
-                in = in && page >= 0 && page < a.n_pages;  // an entry that is no page reads as zeros
-                return base + (in ? page * ps + (key - entry * a.P) * rs : 0ll);
+            return [=](int key) {
+                const int entry = page_of_key(a, key), page = table[entry];
+                const bool in = is_page(a, page);  // an entry that is no page reads as zeros
+                return Unit{base + (in ? page * ps + (key - entry * a.P) * rs : 0ll), rs, in};
             };
         };
         walk<D, W, true>(sm, pages_at(static_cast<const float *>(a.k) + g * a.k_hs, a.k_ps, a.k_rs),
