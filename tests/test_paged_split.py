@@ -4,7 +4,7 @@ import random
 
 import pytest
 
-KN, UNIT_COST, MIN_TILES, WEIGHT_TWO, LEAST_TWO = 128, 5, 2, 6, 2
+KN, UNIT_COST, MIN_TILES, WEIGHT_TWO = 128, 5, 2, 6
 
 
 def cdiv(a, b):
@@ -21,7 +21,6 @@ class Units:
         self.two = n > one_tile
         self.weight = WEIGHT_TWO if self.two else 4
         self.tile = self.weight * KN
-        self.least = LEAST_TWO if self.two else 1
         self.base = self.weight * (max(L - n, 0) + KN - 1) + UNIT_COST * KN * 4
 
     def at(self, u):
@@ -36,8 +35,7 @@ class Units:
     def cut(self, x, nt):
         if x >= nt * self.tile:
             return nt
-        j = 0 if x <= 0 else cdiv(x, self.tile)
-        return 0 if j < self.least else nt if j > nt - self.least else j
+        return 0 if x <= 0 else cdiv(x, self.tile)
 
 
 def runs_of(seqs, per, tokens, one_tile, grid, cta):
@@ -93,7 +91,7 @@ def runs_of(seqs, per, tokens, one_tile, grid, cta):
         runs.append((b, hs, u, j, n))
         if j == 0 and n < nt:
             assert rec is None
-            rec = (b, hs, u, ((pos + (nt - units.least) * units.tile + 1) * N - 1) // total)
+            rec = (b, hs, u, ((pos + (nt - 1) * units.tile + 1) * N - 1) // total)
         if j + n == nt:
             advance()
         else:

@@ -47,6 +47,19 @@
 // tiles): rows past the unit's last key become zeros, non-finite elements become zeros
 // which the epilogue adds back to the rows that see them.
 //
+// Measured (H 32 / 8, D 128):
+//   64 sequences of up to 8192 keys in pages of 64, one token each, 1.29 GB     196 us, 6.6 TB/s
+//   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                  104 us, 5.4 TB/s
+//   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     160 us
+//   4096 tokens, the last of 32768, 2.1 PFLOP     1.19 ms, 1740 TFLOP/s (1.4 ms at the power limit)
+//   one sequence of 1501 keys                                                   9.7 us
+// The first is bound by HBM (a plain copy runs at 6.8 TB/s); the second and third by what a
+// unit costs beside its tiles, some 3 us that the ring of loads covers in part; the fourth
+// by the chain S, softmax, P V; the last by latency.  Loads of one 64-column block each took 209,
+// 154 and 210 us in the first three, a loading loop for each form of unit 177 us in the third.
+// Few rows spread over all lanes (a row's columns over the warps) halved the softmax of a tile,
+// but the end of a unit took 1 us more: 194, 188 and 10.3 us in the first, third and last.
+//
 // Roles (12 warps): warp 0 walks the CTA's run and loads Q, K_j, V_j, warp 1 allocates
 // TMEM and issues the MMAs, warps 2-3 guard, warps 4-7 and 8-11 are the streams (thread =
 // row = TMEM lane); a warp none of whose rows sees a key only keeps step.
@@ -64,8 +77,10 @@ namespace {
 constexpr int kN = 128;          // keys per K/V tile
 constexpr int kM = 128;          // rows per tile
 constexpr int kThreads = 384;
-constexpr uint32_t kRegsOther = 80;     // warps 0-3 after setmaxnreg
-constexpr uint32_t kRegsSoftmax = 208;  // warps 4-11: 128 * 80 + 256 * 208 <= 384 * 168
+// Registers after setmaxnreg: 128 * 80 + 256 * 208 <= 384 * 168.  The loading warp spills below
+// 80, the softmax below 208 (96 and 200: 177 us for the third case above).
+constexpr uint32_t kRegsOther = 80;     // warps 0-3
+constexpr uint32_t kRegsSoftmax = 208;  // warps 4-11
 constexpr int kTmemCols = 512;   // S0 0, S1 128, O0 256, O1 256 + D
 constexpr int kRing = 4;         // unit runs in flight between the roles
 constexpr int kRingReaders = 32 + 256;
@@ -74,10 +89,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kHugeLog2 = 16777216.0f;  // 2^24
-constexpr int kUnitCost = 5;  // what a unit costs beside its tiles, in tiles
-constexpr int kMinTiles = 2;  // fewest tiles' worth of keys a CTA takes
-constexpr int kWeightTwo = 6;    // quarters of a tile's cost, where a unit has two row tiles
-constexpr int kLeastTwo = 2;      // fewest tiles of such a unit that a cut leaves on either side
+// The axis, with what other values cost: 64 decoding sequences, 16 with all heads cached, 60
+// and four chunks (the first three cases above) take 200, 104 and 161 us.
+constexpr int kUnitCost = 5;   // what a unit costs beside its tiles, in tiles (3: 202, 103, 164; 8: 200, 110, 164 us)
+constexpr int kMinTiles = 2;   // fewest tiles' worth of keys a CTA takes (1: 163, 3: 165 us for the chunks)
+constexpr int kWeightTwo = 6;  // quarters of a tile's cost, where a unit has two row tiles (4: 191, 5: 169, 7: 166 us)
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
@@ -142,7 +158,6 @@ struct Units {
     int nu, step;   // units, tokens of a unit
     int weight;     // quarters a key
     int tile;       // quarters a K/V tile
-    int least;      // tiles of a unit that a cut leaves on either side
     long long base;
     __device__ __forceinline__ Units(const Seq &q, int tokens, int one_tile) {
         nu = (q.n + tokens - 1) / tokens;
@@ -150,7 +165,6 @@ struct Units {
         const bool two = q.n > one_tile;
         weight = two ? kWeightTwo : 4;
         tile = weight * kN;
-        least = two ? kLeastTwo : 1;
         base = static_cast<long long>(weight) * (max(q.L - q.n, 0) + kN - 1) + kUnitCost * kN * 4;
     }
     __device__ __forceinline__ long long at(int u) const {
@@ -159,8 +173,7 @@ struct Units {
     // The first of a unit's nt tiles that lies behind a cut at x, counted from the unit's begin.
     __device__ __forceinline__ int cut(long long x, int nt) const {
         if (x >= static_cast<long long>(nt) * tile) return nt;
-        const int j = x <= 0 ? 0 : static_cast<int>(quotient(x + tile - 1, tile));
-        return j < least ? 0 : j > nt - least ? nt : j;
+        return x <= 0 ? 0 : static_cast<int>(quotient(x + tile - 1, tile));
     }
 };
 
@@ -457,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.n = end - j;
                     r.slot = Cluster || r.n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (j == 0 ? 1 : 0);
                     if (!Cluster && j == 0 && r.n < nt) {  // the unit begins here and goes on in CTAs up to the record's,
-                                               // the last whose begin leaves enough of it
-                        const long long last = pos + static_cast<long long>(nt - units.least) * units.tile;
+                                                           // the last that begins at or before its last tile
+                        const long long last = pos + static_cast<long long>(nt - 1) * units.tile;
                         if (lane == 0) {
                             record[0] = make_int4(b, hs, r.tok0, static_cast<int>(quotient((last + 1) * N - 1, total)));
                             record[1] = make_int4(r.left, r.past, r.c0, 0);
