@@ -195,7 +195,8 @@ struct GuardReq {
     int run;     // ring slot
 };
 constexpr int kEnd = -1;
-constexpr int kNoBox = INT_MIN, kBadPage = -1;  // a box that is not copied; out of range in every view of the pages
+constexpr int kNoBox = -1;    // the row of a box that is not copied
+constexpr int kBadPage = -1;  // out of range in every view of the pages
 
 // Single: every unit has one row tile; its second Q buffer is one more K/V stage.
 template <int D, bool Single>
@@ -332,6 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&bars.tmem_base, kTmemCols);
         tmem_relinquish();
     }
+    // rows that no load of Q writes have scores of 0: their lanes never take a rare path
+    for (int i = threadIdx.x; i < L::kQTiles * L::kTile / 16; i += kThreads) st_shared_v4(smem_u32(smem) + i * 16, 0u, 0u, 0u, 0u);
+    fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -497,11 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             next_row = next_key - next_row * a.P;
             const int last_key = min(r.keys, (r.j0 + r.n) * kN);
             struct Box {
-                int page, row;
+                int page, row;  // page: as it stands in the table, untouched until its tile is loaded (two tiles later)
             };
             auto look_up = [&] {
-                Box x{kNoBox, next_row};
-                if (carries && next_key < last_key) x.page = max(*next_entry, kBadPage);
+                Box x{kBadPage, kNoBox};
+                if (carries && next_key < last_key) x.page = *next_entry, x.row = next_row;
                 next_key += kN;
                 next_entry += page_inc;
                 next_row += row_inc;
@@ -526,12 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint8_t *dst = ring + stage * L::kTile;
                 const CUtensorMap *map = kv ? &tv : &tk;
-                if (a.halves) {
-                    if (x.page != kNoBox) tma_load_4d(dst + box_at, map, full, c * 64, x.row, head, x.page);
-                } else {
-                    const unsigned at = kv ? x.page * static_cast<unsigned>(a.v_pstep) + v_head : x.page * static_cast<unsigned>(a.k_pstep) + k_head;
-                    const int entry = is_page(a, x.page) ? static_cast<int>(at) : kBadPage, row = x.row / 8;
-                    if (x.page != kNoBox) tma_load_5d(dst + box_at, map, full, row, entry);
+                if (x.row != kNoBox) {
+                    if (a.halves) {
+                        tma_load_4d(dst + box_at, map, full, c * 64, x.row, head, is_page(a, x.page) ? x.page : kBadPage);
+                    } else {
+                        const int at = kv ? x.page * a.v_pstep + v_head : x.page * a.k_pstep + k_head;
+                        tma_load_5d(dst + box_at, map, full, x.row / 8, is_page(a, x.page) ? at : kBadPage);
+                    }
                 }
                 if (kv && jj >= edge) {
                     if (lane == 0) {
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool one = Single || r.left <= a.tokens;
             const int lead = one ? 2 : 1;  // tiles that K is ahead: K0 K1 | V0 K2 | V1 K3 or K0 | V0 K1 | V1 K2
             // boxes of tiles jj + lead - 2 to jj + lead + 1
-            Box v2{kBadPage, 0}, v1 = v2, now = look_up(), next = look_up();
+            Box v2{kBadPage, kNoBox}, v1 = v2, now = look_up(), next = look_up();
             if (k == 0) load_q(one ? 1 : 2);  // before the first K; later behind it
             for (int jj = -lead; jj < r.n && ok; ++jj) {
                 if (jj == 0 && k > 0) load_q(one ? 1 : 2);
@@ -768,11 +773,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (r.n < 0) break;
                 one = Single || r.left <= a.tokens;
                 n = one ? (r.n - x + 1) / 2 : r.n;
-                lim = row_of(a, r.hs, r.tok0, r.left, r.past, one ? 0 : x, row).lim;
-                if (!__any_sync(0xffffffffu, lim > 0))
-                    lim = INT_MIN;  // the whole warp only keeps step
-                else
-                    lim -= r.j0 * kN;
+                const Row w = row_of(a, r.hs, r.tok0, r.left, r.past, one ? 0 : x, row);
+                const int most = __reduce_max_sync(0xffffffffu, w.lim);
+                // a lane without a row hides no keys, so that only the edge tiles are masked
+                lim = (w.valid ? w.lim : most) - r.j0 * kN;
+                if (most <= 0) lim = INT_MIN;  // the whole warp only keeps step
             }
             float m_run = -INFINITY, l = 0.f;
             bool huge = sl2 == 0.f;  // some row of the warp is
@@ -793,10 +798,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 4; ++c) reg_fence32(s + c * 32);
                 const int t = lim - j * kN;  // this row sees columns [0, t)
                 const bool masked = __any_sync(0xffffffffu, t < kN);
-                if (masked) {
+                if (masked) {  // 32 columns at a time: bits of those that the row sees
 #pragma unroll
-                    for (int e = 0; e < kN; ++e)
-                        if (e >= t) s[e] = f2u(-INFINITY);
+                    for (int c = 0; c < 4; ++c) {
+                        const int left = t - 32 * c;
+                        const uint32_t see = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see >> e & 1u)) s[32 * c + e] = f2u(-INFINITY);
+                    }
                 }
                 float m8[8];
 #pragma unroll
