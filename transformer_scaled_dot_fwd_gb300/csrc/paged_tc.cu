@@ -49,19 +49,22 @@
 //
 // Measured (H 32 / 8, D 128):
 //   64 sequences of up to 8192 keys in pages of 64, one token each, 1.29 GB     196 us, 6.6 TB/s
-//   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                  104 us, 5.4 TB/s
-//   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     160 us
+//   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                  100 us, 5.6 TB/s
+//   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     151 us
 //   4096 tokens, the last of 32768, 2.1 PFLOP     1.19 ms, 1740 TFLOP/s (1.4 ms at the power limit)
 //   one sequence of 1501 keys                                                   9.7 us
-// The first is bound by HBM (a plain copy runs at 6.8 TB/s); the second and third by what a
-// unit costs beside its tiles, some 3 us that the ring of loads covers in part; the fourth
-// by the chain S, softmax, P V; the last by latency.  Loads of one 64-column block each took 209,
+// The first is bound by HBM (a plain copy runs at 6.8 TB/s).  The second by the loading warp: a
+// tile of eight boxes takes it 1300 cycles (175 and 58 a box in the copies, the rest in waiting,
+// announcing and looking up), at which all SMs just draw 7.2 TB/s.  The third by both that (1200
+// cycles at four boxes) and the units' ends, where loads in flight drain; the fourth
+// by the chain S, softmax, P V; the last by latency.  Masking every tile, for the sake
+// of the lanes without a row, took 104, 160 us in the second and third.  Loads of one 64-column block each took 209,
 // 154 and 210 us in the first three, a loading loop for each form of unit 177 us in the third.
 // Few rows spread over all lanes (a row's columns over the warps) halved the softmax of a tile,
 // but the end of a unit took 1 us more: 194, 188 and 10.3 us in the first, third and last.
 //
-// Roles (12 warps): warp 0 walks the CTA's run and loads Q, K_j, V_j, warp 1 allocates
-// TMEM and issues the MMAs, warps 2-3 guard, warps 4-7 and 8-11 are the streams (thread =
+// Roles (12 warps): warp 3 walks the CTA's run and loads Q, K_j, V_j, warp 2 allocates
+// TMEM and issues the MMAs, warps 0-1 guard, warps 4-7 and 8-11 are the streams (thread =
 // row = TMEM lane); a warp none of whose rows sees a key only keeps step.
 #include "clusters.cuh"
 #include "paged.h"
@@ -77,6 +80,10 @@ namespace {
 constexpr int kN = 128;          // keys per K/V tile
 constexpr int kM = 128;          // rows per tile
 constexpr int kThreads = 384;
+// Warps w, w + 4 and w + 8 share a scheduler.  A few rows keep only warps 4 and 8 busy, so the
+// warps on which they wait lie elsewhere (loads by warp 0, MMAs by warp 1: one user 10.1 against
+// 9.7 us, all heads 101 against 100).
+constexpr int kLoadWarp = 3, kMmaWarp = 2;
 // Registers after setmaxnreg: 128 * 80 + 256 * 208 <= 384 * 168.  The loading warp spills below
 // 80, the softmax below 208 (96 and 200: 177 us for the third case above).
 constexpr uint32_t kRegsOther = 80;     // warps 0-3
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bars.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&bars.tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     griddep_wait();
 
-    if (warp == 0) {
+    if (warp == kLoadWarp) {
         // ================================================================ walk and TMA loads
         regs_dec<kRegsOther>();
         const int per = a.H_kv * a.groups;  // heads, or groups of them, of a sequence
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (Cluster) cluster_sync(), cluster_sync();
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
         // ================================================================ MMA issuer
         regs_dec<kRegsOther>();
         const uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0);
@@ -728,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 4) {
         // ================================================================ guard of the edge V tiles
         regs_dec<kRegsOther>();
-        const int tid = threadIdx.x - 64;
+        const int tid = threadIdx.x;
         for (int q = 0;; ++q) {
             const int slot = q % kGuardRing;
             // a request comes after its load was issued, and its stage is not reused
@@ -1045,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         __syncwarp();
         tmem_dealloc(tmem, kTmemCols);
