@@ -34,8 +34,8 @@
  *           order holds as for an ordinary launch.
  * dtype.    ATTN_BF16: bfloat16 inputs and output, fp32 accumulation and
  *           softmax statistics, output rounded to nearest even.  On the tensor
- *           cores (every bf16 prefill, attn_decode_tree, attn_decode_gqa with 4 to
- *           128 query heads a cached head) the softmax weights are rounded to
+ *           cores (every bf16 prefill, attn_decode_tree, attn_fwd_paged, attn_decode_gqa
+ *           with 4 to 128 query heads a cached head) the softmax weights are rounded to
  *           bf16 before they multiply V, by at most 2^-8 of each; their sum is
  *           that of the fp32 weights.
  *           ATTN_F32: float32 everywhere (no TF32).  Output dtype = input dtype.
@@ -459,9 +459,9 @@ ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int
  *   workspace   device memory of attn_fwd_paged_workspace(...) bytes, 16-byte aligned (may
  *               be NULL when that is 0); rules as in attn_fwd_packed
  *
- * The parts of a sequence are merged in order: a call gives the same bits every time.  The
- * work of all sequences is cut into equal shares, so the last bits of a row may depend on
- * the other sequences' lengths (bf16), or on the sizes of the call (fp32).  Scores beyond
+ * The parts of a sequence are merged in order: a call gives the same bits every time.  How
+ * the keys are shared out follows from the sizes of the call and, in bf16, from the lengths of
+ * all sequences, so the last bits of a row may depend on those.  Scores beyond
  * fp32's range and infinite or NaN elements of V as in attn_decode_tree.  dtype, D, scale
  * and errors as in attn_fwd; no work counter is used, and no device memory is allocated.
  */

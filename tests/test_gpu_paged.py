@@ -115,6 +115,20 @@ def test_single_tokens(gpu, lens, H, H_kv, dtype, D):
         x.check(out, lse, heads=(0, H - 1), what=f"{n} a sequence")
 
 
+@pytest.mark.parametrize("H_kv", [1, 2, 8])
+@pytest.mark.parametrize("B", [1, 2, 3, 4, 9, 16, 19, 37, 75])
+@pytest.mark.parametrize("longest", [60, 700, 2100])
+def test_a_few_sequences(gpu, longest, B, H_kv):
+    """One to a few hundred units: clusters of eight, four, two and one CTAs, and none."""
+    lens = [longest] + [(37 * b * b) % (longest + 1) for b in range(1, B)]
+    for n, D in ((1, 128), (2, 64)):
+        x = Paged([(L, n) for L in lens], 2 * H_kv, H_kv, D, 16, BF16, seed=B + longest, even=True)
+        out, lse = x.call(return_lse=True)
+        attn.attn_device_status()
+        x.check(out, lse, heads=(0, 2 * H_kv - 1), what=f"{B} sequences of {n}")
+        assert torch.equal(x.call(), out)
+
+
 @pytest.mark.parametrize("H,H_kv", [(33, 1), (128, 1), (130, 1), (200, 1), (260, 2), (600, 2)])
 def test_large_groups(gpu, H, H_kv):
     for dtype in (BF16, F32):

@@ -1080,14 +1080,23 @@ static long long paged_sizes(const char *who, PagedArgs &a, bool ragged, int dty
     a.slot_rows = a.single ? (a.box_tokens * a.heads + 31) / 32 * 32 : 256;
     a.box = 128;
     while (a.P % a.box) a.box /= 2;
-    // Few units: each a cluster, which joins its parts over distributed shared memory (one user's
-    // 1500 keys 9.3 us against 13.8, 8000 15.9 against 19.0).  Beyond 32768 keys the equal shares
-    // of all SMs win (50000: 46.8 against 65.0 us).  Not all SMs can be taken by clusters: of 16
-    // one waits for the others (17.6 us), of 15 none (9.9); two thirds of the SMs are left to them.
+    // Few units: each a cluster of eight, four, two or one CTAs, as many as the SMs hold (of
+    // four and eight not on all of them: 16 of eight take 17.6 us, as one waits, 15 take 9.9).
+    // Against the equal shares of all SMs, with H 32 / 8 and D 128: one sequence of 1000 keys
+    // 9.0 against 12.7 us, two 10.1 and 13.6, four 12.5 and 14.7, 9 13.6 and 20.4, 16 18.3 and
+    // 23.4.  Long ones lose: 42.9 and 35.3 for one of 32000, 24.3 and 20.6 for two of 8000, 24.7 and
+    // 19.9 for four of 4000.  So up to 6 tiles more for the longest sequence than an equal share is,
+    // where that fills its row of the table and the others are half as long.
     const long long units = static_cast<long long>(a.n_seq) * a.H_kv * a.groups;
-    a.cluster = a.single && 3 * units * kPagedCluster <= 2LL * a.n_sm && a.max_len <= 32768;
+    a.cluster = 0;
+    for (int c = a.single ? kPagedCluster : 0; c > 0 && a.cluster == 0; c /= 2)
+        if (3 * units * c <= (c < 4 ? 3LL : 2LL) * a.n_sm) a.cluster = c;
     if (a.cluster) {
-        a.grid = static_cast<int>(units) * kPagedCluster;
+        const double shared = units * (a.n_seq + 1.0) / (2.0 * a.n_seq) / a.n_sm;  // of a tile of every unit, an SM's
+        if (a.max_len / 128.0 * (1.0 / a.cluster - shared) > 6.0) a.cluster = 0;
+    }
+    if (a.cluster) {
+        a.grid = static_cast<int>(units) * a.cluster;
         return 0;
     }
     const double axis = paged_tc_axis(a);

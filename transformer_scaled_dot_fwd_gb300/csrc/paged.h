@@ -28,7 +28,7 @@ struct PagedArgs {
     // the pages' views: head h of page p is entry p pstep + h hstep; halves: boxes of 64 columns
     int halves, k_pstep, k_hstep, v_pstep, v_hstep;
     int single;                 // every unit has one row tile
-    int cluster;                // every unit is a cluster of kPagedCluster CTAs; no workspace
+    int cluster;                // > 0: every unit is a cluster of so many CTAs; no workspace
     int grid;                   // CTAs at most
     int n_split;                // fp32: splits of the keys
     // Partial results: O unnormalised [D] and (running max in log2 units, sum) of
@@ -46,7 +46,7 @@ struct PagedArgs {
 // box / 8 x 1 boxes (halves: as (D, P, H_kv, n_pages) with 64 x 8 x 1 x 1 boxes).
 cudaError_t launch_paged_tc(const PagedArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv);
 double paged_tc_axis(const PagedArgs &a);
-constexpr int kPagedCluster = 8;
+constexpr int kPagedCluster = 8;  // CTAs of a cluster at most
 cudaError_t launch_paged_f32(const PagedArgs &a);
 // fp32: blocks of 32 rows of a cached head, and splits of the keys (1, 2, 4 or 8: CTAs of
 // a cluster; more: merged through the workspace).

@@ -21,8 +21,8 @@
 // O, running max and sum in fp32 in the CTA's slots of the workspace, for a merge in
 // the order of the keys; whole units are written out directly.
 //
-// Few units of one row tile (one user, or a few) are clusters of eight CTAs instead, with an
-// eighth of the unit's tiles each, whose parts meet in distributed shared memory: no axis, no
+// Few units of one row tile (up to an SM each) are clusters of one to eight CTAs instead, with
+// equal parts of the unit's tiles, which meet in distributed shared memory: no axis, no
 // workspace, no second kernel.
 //
 // Pages.  A 128-key tile is copied by boxes that lie in one page each (rows: the largest
@@ -96,11 +96,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kHugeLog2 = 16777216.0f;  // 2^24
-// The axis, with what other values cost: 64 decoding sequences, 16 with all heads cached, 60
-// and four chunks (the first three cases above) take 200, 104 and 161 us.
-constexpr int kUnitCost = 5;   // what a unit costs beside its tiles, in tiles (3: 202, 103, 164; 8: 200, 110, 164 us)
-constexpr int kMinTiles = 2;   // fewest tiles' worth of keys a CTA takes (1: 163, 3: 165 us for the chunks)
-constexpr int kWeightTwo = 6;  // quarters of a tile's cost, where a unit has two row tiles (4: 191, 5: 169, 7: 166 us)
+// The axis, with what other values cost in the first three cases above.
+constexpr int kUnitCost = 5;   // what a unit costs beside its tiles, in tiles (4: 199, 100, 152; 7: 197, 103, 152 us)
+constexpr int kMinTiles = 2;   // fewest tiles' worth of keys a CTA takes (4: 128 tokens over 500 keys 18.9 against 17.9 us)
+constexpr int kWeightTwo = 6;  // quarters of a tile's cost, where a unit has two row tiles (7: 157 us in the third; 4 and 5: worse by
+                               // 30 and 8 us in an earlier form)
+static_assert(4 * kMinTiles >= kWeightTwo, "a tile begins in every share: the merge reads all CTAs from a unit's first to its last");
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool idle = false;
         Seq q{0, 0, 0};
         if (Cluster) {
-            b = static_cast<int>(blockIdx.x) / (kPagedCluster * per);
+            b = static_cast<int>(blockIdx.x) / (a.cluster * per);
             q = seq_of(a, b);
             idle = q.n == 0;
             hi = LLONG_MAX;
@@ -430,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         if (Cluster) {
-            hs = static_cast<int>(blockIdx.x) / kPagedCluster % per;
-            j = tiles_of(keys_of(0)) * static_cast<int>(cluster_rank()) / kPagedCluster;
+            hs = static_cast<int>(blockIdx.x) / a.cluster % per;
+            j = tiles_of(keys_of(0)) * static_cast<int>(cluster_rank()) / a.cluster;
         } else if (!idle) {
             const long long one = units.at(units.nu);
             hs = static_cast<int>(quotient(lo - base, one));
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!idle && b < a.n_seq && pos < hi) {  // r.n = 0: a CTA of a cluster without a tile
                 const int keys = keys_of(u);
                 nt = tiles_of(keys);
-                const int end = Cluster ? nt * static_cast<int>(cluster_rank() + 1) / kPagedCluster : units.cut(hi - pos, nt);
+                const int end = Cluster ? nt * static_cast<int>(cluster_rank() + 1) / a.cluster : units.cut(hi - pos, nt);
                 if (Cluster || end > j) {
                     r.seq = b;
                     r.hs = hs;
@@ -1009,12 +1010,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // each CTA joins its share of the columns, the parts in the order of the keys
             __syncwarp();
             cluster_sync();
-            constexpr int kQuads = D / kPagedCluster / 4;  // of a CTA's columns
+            const int n_cta = a.cluster, quads = D / 4 / n_cta;  // of a CTA's columns
             const Run r = read_run(bars, 0);
             const unsigned rank = cluster_rank();
 #pragma unroll 1
-            for (int i = static_cast<int>(threadIdx.x) - 128; i < kM * kQuads; i += 256) {
-                const int rr = i / kQuads, c = static_cast<int>(rank) * (D / kPagedCluster) + i % kQuads * 4;
+            for (int i = static_cast<int>(threadIdx.x) - 128; i < kM * quads; i += 256) {
+                const int rr = i / quads, c = (static_cast<int>(rank) * quads + i % quads) * 4;
                 const Row w = row_of(a, r.hs, r.tok0, r.left, r.past, 0, rr);
                 if (!w.valid) continue;
                 float2 ml[kPagedCluster];
@@ -1023,6 +1024,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float *part = reinterpret_cast<const float *>(ring) + rr * (D + 4) + c;
 #pragma unroll
                 for (unsigned y = 0; y < kPagedCluster; ++y) {
+                    ml[y] = make_float2(-INFINITY, 0.f), o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (static_cast<int>(y) >= n_cta) continue;
                     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
                                  : "=f"(ml[y].x), "=f"(ml[y].y) : "r"(map_rank(cluster_ml<D>(ring) + rr, y)));
                     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -1104,7 +1107,7 @@ cudaError_t launch_paged_t(const PagedArgs &a, const CUtensorMap &tq, const CUte
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(a.grid);
-    e = launch_clusters(kernel, Cluster ? kPagedCluster : 1u, grid, kThreads, L::kSmemBytes, a.stream, a, tq, tk, tv);
+    e = launch_clusters(kernel, Cluster ? static_cast<unsigned>(a.cluster) : 1u, grid, kThreads, L::kSmemBytes, a.stream, a, tq, tk, tv);
     if (Cluster || e != cudaSuccess || grid == 1) return e;
     // Early where units have several CTAs each, as in tree_tc.cu
     const long long units = static_cast<long long>(a.n_seq) * a.H_kv * a.groups;
