@@ -1097,6 +1097,7 @@ static long long paged_sizes(const char *who, PagedArgs &a, bool ragged, int dty
     }
     if (a.cluster) {
         a.grid = static_cast<int>(units) * a.cluster;
+        a.cluster_shift = a.cluster == 8 ? 3 : a.cluster == 4 ? 2 : a.cluster == 2 ? 1 : 0;
         return 0;
     }
     const double axis = paged_tc_axis(a);

@@ -28,7 +28,8 @@ struct PagedArgs {
     // the pages' views: head h of page p is entry p pstep + h hstep; halves: boxes of 64 columns
     int halves, k_pstep, k_hstep, v_pstep, v_hstep;
     int single;                 // every unit has one row tile
-    int cluster;                // > 0: every unit is a cluster of so many CTAs; no workspace
+    int cluster;                // > 0: every unit is a cluster of so many CTAs, 1 << cluster_shift; no workspace
+    int cluster_shift;
     int grid;                   // CTAs at most
     int n_split;                // fp32: splits of the keys
     // Partial results: O unnormalised [D] and (running max in log2 units, sum) of

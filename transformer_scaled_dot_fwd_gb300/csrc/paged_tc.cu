@@ -49,10 +49,10 @@
 //
 // Measured (H 32 / 8, D 128):
 //   64 sequences of up to 8192 keys in pages of 64, one token each, 1.29 GB     196 us, 6.6 TB/s
-//   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                  100 us, 5.6 TB/s
+//   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                  99 us, 5.7 TB/s
 //   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     151 us
 //   4096 tokens, the last of 32768, 2.1 PFLOP     1.19 ms, 1740 TFLOP/s (1.4 ms at the power limit)
-//   one sequence of 1501 keys                                                   9.7 us
+//   one sequence of 1501 keys                                                   9.5 us
 // The first is bound by HBM (a plain copy runs at 6.8 TB/s).  The second by the loading warp: a
 // tile of eight boxes takes it 1300 cycles (175 and 58 a box in the copies, the rest in waiting,
 // announcing and looking up), at which all SMs just draw 7.2 TB/s.  The third by both that (1200
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool idle = false;
         Seq q{0, 0, 0};
         if (Cluster) {
-            b = static_cast<int>(blockIdx.x) / (a.cluster * per);
+            b = static_cast<int>(blockIdx.x >> a.cluster_shift) / per;
             q = seq_of(a, b);
             idle = q.n == 0;
             hi = LLONG_MAX;
@@ -431,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         if (Cluster) {
-            hs = static_cast<int>(blockIdx.x) / a.cluster % per;
-            j = tiles_of(keys_of(0)) * static_cast<int>(cluster_rank()) / a.cluster;
+            hs = static_cast<int>(blockIdx.x >> a.cluster_shift) - b * per;
+            j = tiles_of(keys_of(0)) * static_cast<int>(cluster_rank()) >> a.cluster_shift;
         } else if (!idle) {
             const long long one = units.at(units.nu);
             hs = static_cast<int>(quotient(lo - base, one));
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!idle && b < a.n_seq && pos < hi) {  // r.n = 0: a CTA of a cluster without a tile
                 const int keys = keys_of(u);
                 nt = tiles_of(keys);
-                const int end = Cluster ? nt * static_cast<int>(cluster_rank() + 1) / a.cluster : units.cut(hi - pos, nt);
+                const int end = Cluster ? nt * static_cast<int>(cluster_rank() + 1) >> a.cluster_shift : units.cut(hi - pos, nt);
                 if (Cluster || end > j) {
                     r.seq = b;
                     r.hs = hs;
@@ -491,15 +491,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (lane == 0) {
-                volatile Run &w = bars.run[slot];
-                w.seq = r.seq, w.hs = r.hs, w.tok0 = r.tok0, w.left = r.left, w.j0 = r.j0, w.n = r.n, w.slot = r.slot;
-                w.keys = r.keys, w.past = r.past, w.c0 = r.c0;
-                *static_cast<volatile int *>(&bars.spoiled[slot]) = 0;
-                mbar_arrive(&bars.run_full[slot]);
+            auto publish = [&] {
+                if (lane == 0) {
+                    volatile Run &w = bars.run[slot];
+                    w.seq = r.seq, w.hs = r.hs, w.tok0 = r.tok0, w.left = r.left, w.j0 = r.j0, w.n = r.n, w.slot = r.slot;
+                    w.keys = r.keys, w.past = r.past, w.c0 = r.c0;
+                    *static_cast<volatile int *>(&bars.spoiled[slot]) = 0;
+                    mbar_arrive(&bars.run_full[slot]);
+                }
+                __syncwarp();
+            };
+            if (r.n < 0) {
+                publish();
+                break;
             }
-            __syncwarp();
-            if (r.n < 0) break;
             const int edge = edge_of(r), head = r.hs / a.groups;
             // This lane's box of the next tile to be looked up: its key, its entry of the table and its row
             // in that page.
@@ -576,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lead = one ? 2 : 1;  // tiles that K is ahead: K0 K1 | V0 K2 | V1 K3 or K0 | V0 K1 | V1 K2
             // boxes of tiles jj + lead - 2 to jj + lead + 1
             Box v2{kBadPage, kNoBox}, v1 = v2, now = look_up(), next = look_up();
+            publish();
             if (k == 0) load_q(one ? 1 : 2);  // before the first K; later behind it
             for (int jj = -lead; jj < r.n && ok; ++jj) {
                 if (jj == 0 && k > 0) load_q(one ? 1 : 2);
@@ -907,8 +913,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // this CTA's part of its rows, for the cluster: the ring is free, every MMA on it is complete
                 float *part = reinterpret_cast<float *>(ring) + row * (D + 4);
                 if (__any_sync(0xffffffffu, w.valid)) {
-#pragma unroll 1
-                    for (int c = x * (D / 64); c < (x + 1) * (D / 64); ++c) {
+#pragma unroll
+                    for (int c = x * (D / 64), y = 0; y < D / 64; ++c, ++y) {
                         uint32_t o[32], o1[32];
                         tmem_ld32(t_lane + 256u + c * 32, o);
                         tmem_ld32(t_lane + 256u + D + c * 32, o1);
@@ -1010,12 +1016,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // each CTA joins its share of the columns, the parts in the order of the keys
             __syncwarp();
             cluster_sync();
-            const int n_cta = a.cluster, quads = D / 4 / n_cta;  // of a CTA's columns
+            const int n_cta = 1 << a.cluster_shift, quads = D / 4 >> a.cluster_shift;  // of a CTA's columns
             const Run r = read_run(bars, 0);
             const unsigned rank = cluster_rank();
 #pragma unroll 1
-            for (int i = static_cast<int>(threadIdx.x) - 128; i < kM * quads; i += 256) {
-                const int rr = i / quads, c = (static_cast<int>(rank) * quads + i % quads) * 4;
+            for (int i = static_cast<int>(threadIdx.x) - 128; i < (a.box_tokens * a.heads * (D / 4)) >> a.cluster_shift; i += 256) {
+                const int rr = (i << a.cluster_shift) / (D / 4), c = (static_cast<int>(rank) * quads + (i & (quads - 1))) * 4;
                 const Row w = row_of(a, r.hs, r.tok0, r.left, r.past, 0, rr);
                 if (!w.valid) continue;
                 float2 ml[kPagedCluster];
