@@ -349,6 +349,25 @@ def test_huge_scores(gpu, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("value", [math.inf, math.nan, 1e30])
+@pytest.mark.parametrize("seqs", [[(300, 20), (500, 40), (700, 1), (64, 64), (1000, 3)], [(900, 1), (900, 1), (100, 1), (20, 1), (5, 1)]])
+def test_tokens_of_other_sequences_leave_no_trace(gpu, seqs, value, dtype):
+    """A tile's rows behind its sequence's last token are other sequences' tokens, or nothing."""
+    x = Paged(seqs, 8, 2, 128, 16, dtype, seed=11)
+    out, lse = x.call(return_lse=True)
+    for b in range(len(seqs)):
+        rows = slice(x.ends[b], x.ends[b + 1])
+        kept, x.q = x.q, x.q.clone()
+        x.q[rows] = value
+        got, got_lse = x.call(return_lse=True)
+        x.q = kept
+        others = torch.ones(x.T, dtype=torch.bool, device="cuda")
+        others[rows] = False
+        assert torch.equal(got[others], out[others]) and torch.equal(got_lse[others], lse[others])
+    attn.attn_device_status()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_scale_of_zero_is_the_mean(gpu, dtype):
     x = Paged([(300, 45), (1, 1), (131, 1)], 4, 2, 64, 16, dtype, seed=16)
     out, lse = x.call(scale=0.0, return_lse=True)

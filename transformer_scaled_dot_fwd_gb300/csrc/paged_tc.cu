@@ -50,18 +50,20 @@
 // Measured (H 32 / 8, D 128):
 //   64 sequences of up to 8192 keys in pages of 64, one token each, 1.29 GB     196 us, 6.6 TB/s
 //   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                  99 us, 5.7 TB/s
-//   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     151 us
-//   4096 tokens, the last of 32768, 2.1 PFLOP     1.19 ms, 1740 TFLOP/s (1.4 ms at the power limit)
-//   one sequence of 1501 keys                                                   9.5 us
+//   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     148 us
+//   4096 tokens, the last of 32768, 2.06 TFLOP    1.19 ms, 1730 TFLOP/s (1.4 ms at the power limit)
+//   one sequence of 1501 keys                                                   9.0 us
 // The first is bound by HBM (a plain copy runs at 6.8 TB/s).  The second by the loading warp: a
-// tile of eight boxes takes it 1300 cycles (175 and 58 a box in the copies, the rest in waiting,
-// announcing and looking up), at which all SMs just draw 7.2 TB/s.  The third by both that (1200
-// cycles at four boxes) and the units' ends, where loads in flight drain; the fourth
-// by the chain S, softmax, P V; the last by latency.  Masking every tile, for the sake
-// of the lanes without a row, took 104, 160 us in the second and third.  Loads of one 64-column block each took 209,
-// 154 and 210 us in the first three, a loading loop for each form of unit 177 us in the third.
-// Few rows spread over all lanes (a row's columns over the warps) halved the softmax of a tile,
-// but the end of a unit took 1 us more: 194, 188 and 10.3 us in the first, third and last.
+// tile of eight boxes takes it some 1250 cycles (175 and 58 a box in the copies, the rest in
+// waiting, announcing and looking up), at which all SMs just draw 7.2 TB/s.  The third by both
+// that (four boxes) and the units' ends, where loads in flight drain; the fourth by the chain S,
+// softmax, P V; the last by latency.
+// Other forms, in the first, second, third and last: loads of one 64-column block each 209, 154,
+// 210 and 16.8 us; a loading loop for each form of unit 177 us in the third; every tile
+// masked, for the sake of lanes without a row, 199, 104, 161 us; what a load needs computed behind
+// its wait 152 us in the third, 9.5 in the last; few rows spread over all lanes (a row's columns
+// over the warps), which halves the softmax of a tile but adds 1 us to the end of a unit, 3 us
+// less, 11 us more and 1 us more in the first, third and last.
 //
 // Roles (12 warps): warp 3 walks the CTA's run and loads Q, K_j, V_j, warp 2 allocates
 // TMEM and issues the MMAs, warps 0-1 guard, warps 4-7 and 8-11 are the streams (thread =
@@ -528,28 +530,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto load = [&](int jj, auto v, const Box &x) {  // K or V of tile jj into the next stage
                 constexpr bool kv = decltype(v)::value;
                 if (!ok) return;
+                // before the wait: what does not depend on it
+                const int inside = r.keys - (r.j0 + jj) * kN;
+                const uint32_t bytes = inside >= kN ? kN * D * 2u : inside > 0 ? ((inside + a.box - 1) & -a.box) * (D * 2u) : 0u;
+                const unsigned at = static_cast<unsigned>(x.page) * (kv ? a.v_pstep : a.k_pstep) + (kv ? v_head : k_head);
+                const int entry = is_page(a, x.page) ? a.halves ? x.page : static_cast<int>(at) : kBadPage;
                 if (!__all_sync(0xffffffffu, mbar_try_wait(&bars.kv_empty[stage], stage_phase)) &&
                     !(ok = mbar_wait_warp(&bars.kv_empty[stage], stage_phase, &bars.abort)))
                     return;
                 uint64_t *full = &bars.kv_full[stage];
-                const int inside = r.keys - (r.j0 + jj) * kN;
-                if (lane == 0) {
-                    if (inside >= kN)
-                        mbar_arrive_expect_tx(full, kN * D * 2);
-                    else if (inside > 0)
-                        mbar_arrive_expect_tx(full, static_cast<uint32_t>((inside + a.box - 1) / a.box * a.box * D * 2));
-                    else
-                        mbar_arrive(full);
-                }
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 uint8_t *dst = ring + stage * L::kTile;
                 const CUtensorMap *map = kv ? &tv : &tk;
                 if (x.row != kNoBox) {
-                    if (a.halves) {
-                        tma_load_4d(dst + box_at, map, full, c * 64, x.row, head, is_page(a, x.page) ? x.page : kBadPage);
-                    } else {
-                        const int at = kv ? x.page * a.v_pstep + v_head : x.page * a.k_pstep + k_head;
-                        tma_load_5d(dst + box_at, map, full, x.row / 8, is_page(a, x.page) ? at : kBadPage);
-                    }
+                    if (a.halves)
+                        tma_load_4d(dst + box_at, map, full, c * 64, x.row, head, entry);
+                    else
+                        tma_load_5d(dst + box_at, map, full, x.row / 8, entry);
                 }
                 if (kv && jj >= edge) {
                     if (lane == 0) {
