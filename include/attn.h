@@ -633,7 +633,8 @@ ATTN_API int attn_rope_append_paged(const void *q, const void *k, const void *v,
  *   workspace   device memory of attn_pages_workspace(n_out, n_pages) bytes, 16-byte
  *               aligned; rules as in attn_fwd_packed
  *
- * The same call gives the same table every time.
+ * n_out is at most 2^29, n_out max_pages and n_pages are below 2^30.  The same call gives the
+ * same table every time.
  */
 ATTN_API int attn_pages_step(const int32_t *page_table, const int32_t *cache_len, int n_seq, int max_pages, long long table_stride,
                              int n_pages, int page_size, const int32_t *parents, const int32_t *new_len,
@@ -666,7 +667,7 @@ ATTN_API int attn_pages_compact(const int32_t *page_table, const int32_t *cache_
  *             overlapping each other
  *   strides   NULL (contiguous), or HOST int64[8]: layer, page, head and row of kpages and
  *             of vpages in elements.  16-byte aligned pointers and strides are the fast case.
- *   copies    device int32 (n_copies, 3).  Pairs with a page outside [0, n_pages) are
+ *   copies    device int32 (n_copies, 3), at most 2^29.  Pairs with a page outside [0, n_pages) are
  *             passed over, rows are clamped to [0, page_size].  A page that one pair writes
  *             must not be read or written by another (the lists of attn_pages_step and
  *             attn_pages_compact are such).

@@ -1513,6 +1513,10 @@ ATTN_API long long attn_pages_workspace(int n_out, int n_pages) {
     return n_out < 0 || n_pages < 0 ? ATTN_EINVAL : pages_workspace(n_out, n_pages);
 }
 
+// Rows of a new table and pairs of a list of copies: the kernels count three entries of each in
+// 32 bits.
+constexpr int kMaxCopies = 1 << 29;
+
 // Shared by attn_pages_step and attn_pages_compact.
 static int pages_impl(const char *who, PagesArgs a, bool step, void *workspace, long long workspace_bytes, void *stream) {
     g_last_error[0] = '\0';
@@ -1523,8 +1527,8 @@ static int pages_impl(const char *who, PagesArgs a, bool step, void *workspace, 
         return fail(ATTN_EINVAL, "%s: %d pages of %d rows are too many for a sequence", who, a.max_pages, a.P);
     if (!a.parents && a.n_out != a.n_seq)
         return fail(ATTN_EINVAL, "%s: without parents there are as many rows as before (got %d, %d)", who, a.n_out, a.n_seq);
-    // ranks and counts are kept in 32 bits
-    if (static_cast<long long>(a.n_out) * a.max_pages >= (1LL << 30) || a.n_pages >= 1 << 30)
+    // ranks, counts and places in the lists are kept in 32 bits; few entries a row do not bound the rows
+    if (static_cast<long long>(a.n_out) * a.max_pages >= (1LL << 30) || a.n_pages >= 1 << 30 || a.n_out > kMaxCopies)
         return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
     const bool entries = a.n_seq > 0 && a.max_pages > 0, out_entries = a.n_out > 0 && a.max_pages > 0;
     if (!a.free_pages || (entries && !a.table) || (out_entries && !a.table_out) || (step && a.n_out > 0 && !a.len_out) ||
@@ -1615,7 +1619,7 @@ ATTN_API int attn_pages_copy(void *kpages, void *vpages, int layers, int n_pages
     if (D <= 0) return fail(ATTN_EINVAL, "%s: D must be positive (got %d)", who, D);
     if (D != 64 && D != 128) return fail(ATTN_EUNSUPPORTED, "%s: D = %d not supported (64 or 128)", who, D);
     if (page_size < 1) return fail(ATTN_EINVAL, "%s: a page must have rows (got %d)", who, page_size);
-    if (static_cast<long long>(H_kv) * page_size >= (1LL << 30) || layers >= 1 << 30)
+    if (static_cast<long long>(H_kv) * page_size >= (1LL << 30) || layers >= 1 << 30 || n_copies > kMaxCopies)
         return fail(ATTN_EINVAL, "%s: the sizes are too large", who);
     if (layers == 0 || n_pages == 0 || n_copies == 0) return ATTN_OK;
     if (!kpages || !vpages || !copies) return fail(ATTN_EINVAL, "%s: a tensor is NULL", who);
