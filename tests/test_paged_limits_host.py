@@ -8,7 +8,7 @@ import ctypes
 import pytest
 
 import transformer_scaled_dot_fwd_gb300 as attn
-from test_paged_host import A, I, compact, copy, step
+from test_paged_host import A, BF, F32, I, append, compact, copy, norm, off, paged, step
 
 MOST = 1 << 29  # rows of a new table, pairs of a list: three entries of each are counted in 32 bits
 
@@ -34,3 +34,46 @@ def test_the_largest_compaction_has_a_list_that_can_be_copied(attn_lib):
     assert ((1 << 30) - 1 + 1) // 2 == MOST
     # accepted as far as its size goes: the next check refuses what it overlaps
     assert copy(attn_lib, n=MOST, c=A[0]) == I and "copies overlaps kpages" in attn.attn_last_error()
+
+
+# the arrays that say where a call's rows lie: T 100, n_seq 3, a table of 3 x 20 entries
+INDEX = {"page_table": (A[5], 3 * 20 * 4), "cu_seqlens": (A[6], 4 * 4), "cache_len": (A[7], 3 * 4)}
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("out", ["o", "lse"])
+@pytest.mark.parametrize("name", INDEX)
+def test_attention_refuses_outputs_over_its_index_arrays(attn_lib, name, out, dtype):
+    """Other blocks, and the merge that follows, still read them."""
+    p, n = INDEX[name]
+    size = 100 * 4 * (128 * (2 if dtype == BF else 4) if out == "o" else 4)
+    arg = {"page_table": "table", "cu_seqlens": "cu", "cache_len": "cl"}[name]
+    base = off(p, 1 << 20)
+    for at in (0, size - 4):  # the array's first bytes, its last ones at the output's front
+        assert paged(attn_lib, dtype=dtype, **{out: base, arg: off(base, at)}) == I
+        assert attn.attn_last_error().endswith(f"overlaps {name}"), attn.attn_last_error()
+    assert paged(attn_lib, dtype=dtype, **{out: off(base, (n - 1) // 16 * 16), arg: base}) == I
+    assert attn.attn_last_error().endswith(f"overlaps {name}")
+    # side by side: the call goes on to refuse something else
+    assert paged(attn_lib, ws=None, **{out: base, arg: off(base, 100 * 4 * 128 * 2)}) == I and "workspace" in attn.attn_last_error()
+
+
+APPEND_INDEX = {"page_table": ("table", 3 * 20 * 4), "cu_seqlens": ("cu", 16), "cache_len": ("cl", 12), "positions": ("pos", 64 * 4)}
+
+
+@pytest.mark.parametrize("out", ["qo", "ko", "kp", "vp"])
+@pytest.mark.parametrize("name", APPEND_INDEX)
+def test_appends_refuse_outputs_over_their_index_arrays(attn_lib, name, out):
+    arg, n = APPEND_INDEX[name]
+    size = {"qo": 64 * 4 * 128, "ko": 64 * 2 * 128, "kp": 100 * 2 * 16 * 128, "vp": 100 * 2 * 16 * 128}[out] * 2
+    base = off(A[12], 1 << 20)
+    for at in (0, 256, size - 4):
+        assert append(attn_lib, **{out: base, arg: off(base, at)}) == I
+        assert attn.attn_last_error().endswith(f"overlaps {name}"), attn.attn_last_error()
+    assert append(attn_lib, **{out: off(base, n - 4), arg: base}) == I and attn.attn_last_error().endswith(f"overlaps {name}")
+
+
+@pytest.mark.parametrize("out", ["qo", "ko"])
+def test_norm_refuses_outputs_over_its_positions(attn_lib, out):
+    base = off(A[12], 1 << 20)
+    assert norm(attn_lib, **{out: base, "pos": off(base, 64)}) == I and attn.attn_last_error().endswith("overlaps positions")

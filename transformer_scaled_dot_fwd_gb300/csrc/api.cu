@@ -305,6 +305,24 @@ bool pools_overlap(const Pool &a, const Pool &b) {
     return !nested_distinct(n, st, 5, a.row);
 }
 
+// The int32 arrays that say where a call's rows lie (NULL: not given, or nothing of it is read).
+// Other blocks, and kernels that follow, still read them when the first rows are written.
+struct Index {
+    const int32_t *p;
+    long long n;
+    const char *name;
+};
+Index table_index(const int32_t *page_table, int n_pages, int n_seq, int max_pages, long long table_stride) {
+    return {n_pages > 0 ? page_table : nullptr, (n_seq - 1) * (n_seq > 1 ? table_stride : 0) + max_pages, "page_table"};
+}
+// The name of the first that `rows` may share a byte with, or NULL.
+template <int N>
+const char *index_under(const Rows &rows, const Index (&index)[N]) {
+    for (const Index &x : index)
+        if (rows_overlap(rows, make_rows(x.p, 1, 1, x.n, x.n, x.n, 4))) return x.name;
+    return nullptr;
+}
+
 // Are the heads of all pages evenly spaced?  Then head h of page p is entry p * pstep +
 // h * hstep of a list of `n` heads `stride` bytes apart.
 struct Heads {
@@ -1180,13 +1198,15 @@ ATTN_API int attn_fwd_paged(const void *q, const void *kpages, const void *vpage
             return fail(ATTN_EINVAL, "%s: out overlaps %s", who, name);
     }
     if (rows_overlap(ro, rq)) return fail(ATTN_EINVAL, "%s: out overlaps q", who);
-    const size_t table_bytes = n_pages > 0 ? static_cast<size_t>((n_seq - 1) * (n_seq > 1 ? table_stride : 0) + max_pages) * 4 : 0;
+    const Index index[3] = {table_index(page_table, n_pages, n_seq, max_pages, table_stride),
+                            {cu_seqlens, n_seq + 1LL, "cu_seqlens"}, {cache_len, n_seq, "cache_len"}};
     const Rows lr = make_rows(lse, T, 1, H, H, H, 4);
     if (lse && (rows_overlap(lr, rq) || rows_overlap(lr, ro) ||
                 overlaps(lse, static_cast<size_t>(T) * H * 4, pool[0].p, pool_extent(pool[0])) ||
-                overlaps(lse, static_cast<size_t>(T) * H * 4, pool[1].p, pool_extent(pool[1])) ||
-                overlaps(lse, static_cast<size_t>(T) * H * 4, page_table, table_bytes)))
+                overlaps(lse, static_cast<size_t>(T) * H * 4, pool[1].p, pool_extent(pool[1]))))
         return fail(ATTN_EINVAL, "%s: lse overlaps another tensor", who);
+    if (const char *name = index_under(ro, index)) return fail(ATTN_EINVAL, "%s: out overlaps %s", who, name);
+    if (const char *name = index_under(lr, index)) return fail(ATTN_EINVAL, "%s: lse overlaps %s", who, name);
     PagedArgs a{};
     a.T = T, a.n_seq = n_seq, a.H = H, a.H_kv = H_kv, a.D = D, a.P = page_size, a.n_pages = n_pages;
     a.max_len = max_pages * page_size;
@@ -1200,9 +1220,7 @@ ATTN_API int attn_fwd_paged(const void *q, const void *kpages, const void *vpage
         const size_t nb = static_cast<size_t>(need);
         if (rows_overlap(wr, rq) || rows_overlap(wr, ro) || (lse && rows_overlap(wr, lr)) ||
             overlaps(workspace, nb, pool[0].p, pool_extent(pool[0])) || overlaps(workspace, nb, pool[1].p, pool_extent(pool[1])) ||
-            overlaps(workspace, nb, page_table, table_bytes) ||
-            (cu_seqlens && overlaps(workspace, nb, cu_seqlens, (static_cast<size_t>(n_seq) + 1) * 4)) ||
-            (cache_len && overlaps(workspace, nb, cache_len, static_cast<size_t>(n_seq) * 4)))
+            index_under(wr, index))
             return fail(ATTN_EINVAL, "%s: workspace overlaps a tensor", who);
     }
     int *status = nullptr;
@@ -1434,6 +1452,12 @@ static int norm_rope_impl(const char *who, NormRopeArgs a, const long long *stri
             if (w && rows_overlap(rows[o], make_rows(w, 1, 1, a.D, a.D, a.D, esz)))
                 return fail(ATTN_EINVAL, "%s: %s overlaps a weight", who, names[o]);
     }
+    const Index index[4] = {{a.positions, a.T, "positions"},
+                            table_index(append ? a.page_table : nullptr, a.n_pages, a.n_seq, max_pages, a.table_stride),
+                            {append ? a.cu_seqlens : nullptr, a.n_seq + 1LL, "cu_seqlens"},
+                            {append ? a.cache_len : nullptr, a.n_seq, "cache_len"}};
+    for (int o = 3; o < 5; ++o)
+        if (const char *name = index_under(rows[o], index)) return fail(ATTN_EINVAL, "%s: %s overlaps %s", who, names[o], name);
     if (append) {
         Pool pool[2];
         for (int i = 0; i < 2; ++i) {
@@ -1446,6 +1470,8 @@ static int norm_rope_impl(const char *who, NormRopeArgs a, const long long *stri
             for (int x = 0; x < 5; ++x)
                 if (!pool_empty(pool[i]) && rows_overlap(pr, rows[x]))
                     return fail(ATTN_EINVAL, "%s: %s overlaps %s", who, names[x], name);
+            if (const char *under = pool_empty(pool[i]) ? nullptr : index_under(pr, index))
+                return fail(ATTN_EINVAL, "%s: %s overlaps %s", who, name, under);
             if (!pool_empty(pool[i]) &&
                 ((a.q_weight && overlaps(a.q_weight, static_cast<size_t>(a.D * esz), pool[i].p, pool_extent(pool[i]))) ||
                  (a.k_weight && overlaps(a.k_weight, static_cast<size_t>(a.D * esz), pool[i].p, pool_extent(pool[i])))))
