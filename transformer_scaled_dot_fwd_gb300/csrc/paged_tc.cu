@@ -103,6 +103,9 @@ constexpr int kUnitCost = 5;   // what a unit costs beside its tiles, in tiles (
 constexpr int kMinTiles = 2;   // fewest tiles' worth of keys a CTA takes (4: 128 tokens over 500 keys 18.9 against 17.9 us)
 constexpr int kWeightTwo = 6;  // quarters of a tile's cost, where a unit has two row tiles (7: 157 us in the third; 4 and 5: worse by
                                // 30 and 8 us in an earlier form)
+// The longest axis: the host accepts no call whose axis could be longer.  Offsets that are none (decreasing: sequences
+// overlap) can make it longer all the same; it is no work then, before a place on it times the number of CTAs wraps.
+constexpr long long kMaxAxis = 1ll << 52;
 static_assert(4 * kMinTiles >= kWeightTwo, "a tile begins in every share: the merge reads all CTAs from a unit's first to its last");
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
                 mine = seq_of(a, min(b0 + lane, a.n_seq - 1));
                 t = b0 + lane < a.n_seq ? cost_of(mine) : 0;
-                total += t;
+                total = min(total + t, kMaxAxis + 1);
             }
             if (a.n_seq <= 32) {
                 sum = prefix(t, lane);
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long most = total / (4 * kN * kMinTiles);
             N = static_cast<int>(min(max(most, 1ll), static_cast<long long>(gridDim.x)));
             const int I = blockIdx.x;
-            idle = I >= N || total == 0;
+            idle = I >= N || total == 0 || total > kMaxAxis;
             const long long each = quotient(total, N);
             const int odd = static_cast<int>(total - each * N);
             if (!idle) lo = each * I + odd * I / N, hi = each * (I + 1) + odd * (I + 1) / N;
