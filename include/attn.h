@@ -618,9 +618,10 @@ ATTN_API int attn_rope_append_paged(const void *q, const void *k, const void *v,
  * there are not cached, their keys read as zeros; a fork's copy is not asked for) and
  * free_pages is negative.  A later call gives such an entry a page, but not the tokens that
  * were to be in it: its rows are whatever they were.  So a negative free_pages is an answer
- * to act on before anything is copied or appended: nothing has moved yet, and a call
- * from the old table with fewer or shorter rows has all their tokens; or a call from the new
- * one cuts each row back to its entries in front of the first -1.
+ * to act on before anything is appended.  Until the copies are made nothing has moved, and
+ * a call from the old table with fewer or shorter rows has all their tokens.  Or the copies
+ * are made, and a call from the new table cuts each row back to its entries in front of
+ * the first -1.
  *
  *   page_table  device int32 (n_seq, max_pages), rows table_stride apart
  *   cache_len   device int32[n_seq], each clamped to [0, max_pages * page_size], or NULL

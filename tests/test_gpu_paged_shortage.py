@@ -47,13 +47,19 @@ def test_the_old_table_still_stands(gpu, spare):
     # again from the old table, with a beam less: nothing was lost
     good = attn.attn_pages_step(t, L, n_pages, P, parents=ints([0, 0]), new_len=ints([7, 7]), pinned=pin)
     assert good[3].item() == 0
-    attn.attn_pages_copy(kp, vp, good[2])
+    x, y = kp.clone(), vp.clone()
+    attn.attn_pages_copy(x, y, good[2])
     for b in range(2):
-        for x, want in zip((kp, vp), before):
-            assert torch.equal(rows_of(x, good[0][b].tolist(), 6), want)
-    # or from the short table, with that beam cut back to the pages it has
+        for pool, want in zip((x, y), before):
+            assert torch.equal(rows_of(pool, good[0][b].tolist(), 6), want)
+    # or on from the short table, its copies made, with that beam cut back to the pages it has
     cut = attn.attn_pages_step(short[0], short[1], n_pages, P, parents=ints([0, 1, 2]), new_len=ints([7, 7, 4]), pinned=pin)
     assert cut[3].item() == 0 and cut[0][2].tolist() == [0, -1, -1, -1] and cut[1].tolist() == [7, 7, 4]
+    attn.attn_pages_copy(kp, vp, short[2])
+    attn.attn_pages_copy(kp, vp, cut[2])
+    for b, n in enumerate((6, 6, 4)):
+        for pool, want in zip((kp, vp), before):
+            assert torch.equal(rows_of(pool, cut[0][b].tolist(), n), want[:n])
 
 
 @pytest.mark.parametrize("spare", [0, 262200])

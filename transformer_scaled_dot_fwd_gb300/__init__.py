@@ -906,7 +906,7 @@ def attn_pages_step(page_table, cache_len, n_pages: int, page_size: int, parents
     filled one has one holder and is copied for the others.  Returns ``(table, lengths,
     copies, free)``: new tensors, or the four of ``out``; ``copies`` (rows, 3) is for
     attn_pages_copy, ``free`` (1,) counts the free pages left (negative: missing; then
-    call again from the old table with fewer or shorter rows, before copying or
+    call again from the old table with fewer or shorter rows, before copying and
     appending, as a page given later comes without the tokens it was to hold).
     See include/attn.h.
     """
