@@ -461,9 +461,11 @@ ATTN_API long long attn_decode_tree_workspace(int B, int H, int H_kv, int T, int
  *
  * The parts of a sequence are merged in order: a call gives the same bits every time.  How
  * the keys are shared out follows from the sizes of the call and, in bf16, from the lengths of
- * all sequences, so the last bits of a row may depend on those.  Scores beyond
- * fp32's range and infinite or NaN elements of V as in attn_decode_tree.  dtype, D, scale
- * and errors as in attn_fwd; no work counter is used, and no device memory is allocated.
+ * all sequences, so the last bits of a row may depend on those.  One of the sizes is the
+ * table's width: a few short sequences in a table for many more tokens take some 5 us longer
+ * than in one that fits them.  Scores beyond fp32's range and infinite or NaN elements of V as
+ * in attn_decode_tree.  dtype, D, scale and errors as in attn_fwd; no work counter is used, and
+ * no device memory is allocated.
  */
 ATTN_API int attn_fwd_paged(const void *q, const void *kpages, const void *vpages, void *out, float *lse, int T, int H,
                             int H_kv, int D, const long long *strides, int n_pages, int page_size, const int32_t *page_table,
@@ -675,7 +677,8 @@ ATTN_API int attn_pages_compact(const int32_t *page_table, const int32_t *cache_
  *   copies    device int32 (n_copies, 3), at most 2^29.  Pairs with a page outside [0, n_pages) are
  *             passed over, rows are clamped to [0, page_size].  A page that one pair writes
  *             must not be read or written by another (the lists of attn_pages_step and
- *             attn_pages_compact are such).
+ *             attn_pages_compact are such).  A pair passed over costs some 2 ns a layer: of a
+ *             compaction's list, whose pairs come first, the first so many may be given.
  */
 ATTN_API int attn_pages_copy(void *kpages, void *vpages, int layers, int n_pages, int H_kv, int page_size, int D,
                              const long long *strides, const int32_t *copies, int n_copies, int dtype, void *stream);

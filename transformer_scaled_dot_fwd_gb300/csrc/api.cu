@@ -1101,10 +1101,12 @@ static long long paged_sizes(const char *who, PagedArgs &a, bool ragged, int dty
     // Few units: each a cluster of eight, four, two or one CTAs, as many as the SMs hold (of
     // four and eight not on all of them: 16 of eight take 17.6 us, as one waits, 15 take 9.9).
     // Against the equal shares of all SMs, with H 32 / 8 and D 128: one sequence of 1000 keys
-    // 9.0 against 12.7 us, two 10.1 and 13.6, four 12.5 and 14.7, 9 13.6 and 20.4, 16 18.3 and
-    // 23.4.  Long ones lose: 42.9 and 35.3 for one of 32000, 24.3 and 20.6 for two of 8000, 24.7 and
-    // 19.9 for four of 4000.  So up to 6 tiles more for the longest sequence than an equal share is,
-    // where that fills its row of the table and the others are half as long.
+    // 8.6 against 13.4 us, two 9.6 and 14.2, four 11.6 and 14.9, 9 12.4 and 20.0, 16 15.0 and
+    // 23.3.  Long ones lose: 42.9 and 36.0 for one of 32000, 24.3 and 20.7 for two of 8000, 24.7 and
+    // 19.5 for four of 4000.  So up to 6 tiles more for the longest sequence than an equal share is,
+    // where that fills its row of the table and the others are half as long.  The lengths themselves
+    // are on the device: short sequences in a wide table take the equal shares (one of 1501
+    // keys 9.1 us where the table has up to some 10600 tokens, 13.7 in a wider one).
     const long long units = static_cast<long long>(a.n_seq) * a.H_kv * a.groups;
     a.cluster = 0;
     for (int c = a.single ? kPagedCluster : 0; c > 0 && a.cluster == 0; c /= 2)

@@ -49,21 +49,22 @@
 //
 // Measured (H 32 / 8, D 128):
 //   64 sequences of up to 8192 keys in pages of 64, one token each, 1.29 GB     196 us, 6.6 TB/s
-//   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                  99 us, 5.7 TB/s
-//   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     148 us
+//   16 of up to 4096, all 32 heads cached, pages of 16, 0.56 GB                 100 us, 5.6 TB/s
+//   60 of up to 6000 and chunks of 512, 512, 300 and 77 tokens, pages of 32     150 us
 //   4096 tokens, the last of 32768, 2.06 TFLOP    1.19 ms, 1730 TFLOP/s (1.4 ms at the power limit)
-//   one sequence of 1501 keys                                                   9.0 us
+//   one sequence of 1501 keys (table of up to 10600 tokens; 13.7 in a wider one)  9.1 us
+//   256 of 100 to 1000 keys, pages of 16, 0.59 GB                               179 us, 3.3 TB/s
 // The first is bound by HBM (a plain copy runs at 6.8 TB/s).  The second by the loading warp: a
 // tile of eight boxes takes it some 1250 cycles (175 and 58 a box in the copies, the rest in
 // waiting, announcing and looking up), at which all SMs just draw 7.2 TB/s.  The third by both
 // that (four boxes) and the units' ends, where loads in flight drain; the fourth by the chain S,
-// softmax, P V; the last by latency.
-// Other forms, in the first, second, third and last: loads of one 64-column block each 209, 154,
+// softmax, P V; the fifth by latency; the last by the units' ends (four tiles a unit).
+// Other forms, in the first, second, third and fifth: loads of one 64-column block each 209, 154,
 // 210 and 16.8 us; a loading loop for each form of unit 177 us in the third; every tile
 // masked, for the sake of lanes without a row, 199, 104, 161 us; what a load needs computed behind
-// its wait 152 us in the third, 9.5 in the last; few rows spread over all lanes (a row's columns
+// its wait 3 us more in the third, 9.5 us in the fifth; few rows spread over all lanes (a row's columns
 // over the warps), which halves the softmax of a tile but adds 1 us to the end of a unit, 3 us
-// less, 11 us more and 1 us more in the first, third and last.
+// less, 11 us more and 1 us more in the first, third and fifth.
 //
 // Roles (12 warps): warp 3 walks the CTA's run and loads Q, K_j, V_j, warp 2 allocates
 // TMEM and issues the MMAs, warps 0-1 guard, warps 4-7 and 8-11 are the streams (thread =

@@ -20,14 +20,22 @@
 // Both move a few hundred KB; what bounds them is the chain of dependent steps.  Pools of up
 // to 262144 pages, whose bits fit in shared memory, take one launch of a cluster of eight
 // CTAs with four barriers (pages_one_kernel): 256 sequences of up to 7000 tokens in pages
-// of 16 rows 8.7 us (10 us with a lane's entries of the table read one after the other, 13
+// of 16 rows 8.9 us (10 us with a lane's entries of the table read one after the other, 13
 // also with a pass over all words for the list, 13.4 as four launches; sixteen CTAs
 // change nothing: the chain is the same).  Larger ones take four launches with the bits in
 // the workspace: clear, mark (a block a row), plan or moves (one block), write or rename (a
-// block a row).
+// block a row).  The limits (with 2048 rows) are what shared memory holds, not where the forms
+// cross: rows of 512 entries in pools of 262145 and 1048576 pages take the four launches 14.5 and
+// 33 us a step, 130 and 565 a compaction (its one block walks all words), and of wide tables eight
+// CTAs write less than all SMs do (8192 entries a row, a tenth of them in use and nine tenths;
+// step, compaction):
+//   256 rows, one launch 26, 55 and 36, 61 us; four launches 18, 121 and 68, 150 us
+//   2048 rows, one launch 165, 190 and 240, 373 us; four launches 73, 143 and 261, 328 us
 //
 // attn_pages_copy moves whole rows of pages, 16 bytes a thread and four in flight, bound by
-// HBM: 120 MB read and 120 MB written in 37 us, 6.5 TB/s.
+// HBM: 120 MB read and 120 MB written in 37 us, 6.5 TB/s.  A pair that is none costs its blocks, two
+// a layer: some 1 ns each (5 pages of a pool of 100000, whose list has 50000 pairs, 101 us in
+// one layer, 3.2 ms in 32).
 #include "clusters.cuh"
 #include "kernels.h"
 #include "paged.h"
